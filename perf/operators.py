@@ -400,7 +400,7 @@ def _plain_append(s):
     src = full[:, None] + back  # [M, 64] packed rows of each block; those before the call are in the tail
     held = src < start[seq[full]][:, None]
     keep = (at >= 0) & ((at < S) | (at >= end[seq] - R))
-    keep = keep.nonzero()[:, 0]
+    keep = keep.nonzero()[:, 0] if stream.numel() else keep.nonzero()[:0, 0]
     slot = torch.where(at[keep] < S, at[keep], S + (at[keep] - S) % R)
     s["pos"][seq[keep], slot] = at[keep].int()
     for name in ("k", "v"):
