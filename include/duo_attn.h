@@ -154,7 +154,7 @@ duo_status duo_attn_prefill_select(duo_handle* handle, const duo_kv_cache* cache
                                    const void* v, int32_t T, void* o, int32_t kind_mask, void* stream);
 
 /* Bytes of device workspace the decode entry points (duo_attn_decode, _paged, _varlen,
- * duo_dca_decode, duo_attn_decode_kv4) need for a cache of n tokens; the size covers
+ * duo_dca_decode, duo_attn_decode_kv4, duo_attn_decode_kv8) need for a cache of n tokens; the size covers
  * the largest grid any of them launches, so one workspace serves them all. */
 size_t duo_decode_workspace_size(const duo_handle* handle, int64_t n);
 
@@ -316,6 +316,149 @@ duo_status duo_kv_append_kv4_paged(duo_handle* handle, duo_kv_cache* cache, cons
 duo_status duo_attn_decode_kv4_paged(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
                                      const duo_kv4_cache* kv4, const void* q, void* o, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/* 8-bit KV caches: the retrieval heads' rows as 8-bit codes, with one fp32 scale for each
+ * block of DUO_KV8_BLOCK = 64 tokens of one head (K and V apart). Half the bytes of the
+ * bf16 caches at decode, and a milder rounding than the 4-bit ones. Streaming heads keep
+ * their bf16 sink + ring caches (cache->k_sr, v_sr, pos), whose size does not grow.
+ *
+ * Tokens 64 j ... 64 j + 63 of a head form block j. When the block is full its rows are
+ * rounded, once, from their bf16 values x:
+ *     DUO_KV8_INT8:  scale = fp32(amax / 127),  code = clamp(rint(fp32(x / scale)), -127, 127)
+ *     DUO_KV8_E4M3:  scale = fp32(amax / 448),  code = e4m3(fp32(x / scale)), saturating
+ * amax = the largest |x| of the block's 64 x D values, every step rounded to nearest even;
+ * value = code * scale. A block of zeros has scale 0 and codes 0; a block with an infinity
+ * or a NaN has scale NaN and codes 0 (its head's outputs are then NaN, never silently wrong).
+ * The rows of the block that is not full yet stay in bf16, in the tail: row t of the open
+ * block at row t % 64 of the (sequence, head)'s tail. So T appends of one token leave the
+ * same cache as one append of T, and recent tokens are exact.
+ *
+ * Layout (device memory, caller-owned, 16-byte aligned), cap64 = max_seq_len rounded up to
+ * a multiple of 64:
+ *   k_codes, v_codes  8-bit [B, n_ret, cap64, D]     row t = token t
+ *   k_scale, v_scale  fp32  [B, n_ret, cap64 / 64]
+ *   k_tail, v_tail    bf16  [B, n_ret, 64, D]
+ * With a duo_paged descriptor (the _paged, _ragged and _varlen entry points;
+ * paged->stream_table must be NULL) the codes and scales are pools:
+ *   k_codes, v_codes  8-bit [num_blocks, block_size, D]     (rows addressed as in duo_paged)
+ *   k_scale, v_scale  fp32  [num_blocks, block_size / 64]
+ * cache->n and cache->pos keep their meaning; cache->k_full and v_full are not used. Every
+ * pointer may be NULL when the handle has no retrieval head. The rows of the codes (B n_ret
+ * cap64, or num_blocks block_size) must stay below 2^31. */
+#define DUO_KV8_BLOCK 64
+#define DUO_KV8_INT8 0
+#define DUO_KV8_E4M3 1
+
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+  void* k_tail;
+  void* v_tail;
+  int32_t code_type; /* DUO_KV8_INT8 or DUO_KV8_E4M3 */
+} duo_kv8_cache;
+
+/* duo_kv_append into these caches: T new tokens at positions n ... n+T-1 (k_new, v_new:
+ * bf16 [B, T, Hkv, D]). Full blocks are written as codes, the open block's rows to the
+ * tail; everything else of the arrays is left as it was. Capacity and errors as
+ * duo_kv_append / duo_kv_append_paged. */
+duo_status duo_kv_append_kv8(duo_handle* handle, duo_kv_cache* cache, const duo_kv8_cache* kv8, const void* k_new,
+                             const void* v_new, int32_t T, void* stream);
+duo_status duo_kv_append_kv8_paged(duo_handle* handle, duo_kv_cache* cache, const duo_paged* paged,
+                                   const duo_kv8_cache* kv8, const void* k_new, const void* v_new, int32_t T,
+                                   void* stream);
+
+/* Where the tokens of a packed batch go (device memory; duo_block_tables_update writes it):
+ *   cu_new    int32 [B + 1]             tokens cu_new[b] ... cu_new[b + 1] - 1 are sequence b's
+ *   token_seq int32 [num_tokens]        the sequence of each token, -1 for padding
+ *   token_pos int32 [num_tokens]        its position in the sequence, -1: not stored
+ *   slots     int64 [num_tokens, n_ret] its row in the pool for each retrieval head (block id
+ *                                       times block_size plus the row in the block), -1: none
+ * Tokens of one sequence follow each other at consecutive positions, and a sequence has its
+ * tokens in one piece. */
+typedef struct {
+  int32_t* cu_new;
+  int32_t* token_seq;
+  int32_t* token_pos;
+  int64_t* slots;
+} duo_slot_map;
+
+/* Append of a packed batch, each sequence with its own length and number of new tokens:
+ * k_new, v_new: bf16 [num_tokens, Hkv, D], 0 <= num_tokens. The positions and rows come from
+ * `map` alone (cache->n is neither read nor changed, no table is read), so a step captured
+ * in a CUDA graph replays with other lengths. Tokens at position -1 are skipped and nothing
+ * of their sequence changes. A slot or sequence out of range is not dereferenced: its rows
+ * are skipped and duo_device_error() reports DUO_ERR_INVALID_ARG. */
+duo_status duo_kv_append_kv8_ragged(duo_handle* handle, duo_kv_cache* cache, const duo_paged* paged,
+                                    const duo_kv8_cache* kv8, const duo_slot_map* map, int32_t num_tokens,
+                                    const void* k_new, const void* v_new, void* stream);
+
+/* One decode step over 8-bit caches, as duo_attn_decode (same q, o, workspace and order of
+ * calls): scores and outputs are accumulated in fp32 from the codes (fp16 tensor-core
+ * operands, exact for both code types; q scaled to fp16 by a power of two of its own per
+ * head, so any finite bf16 q is taken) and the tail and ring rows (bf16 operands); p is
+ * rounded to fp16 over codes and to bf16 over bf16 rows. Workspace as for duo_attn_decode.
+ * duo_attn_decode_kv8_varlen reads the lengths on the device (seq_lens int32 [B], clamped
+ * to [0, max_len], the new token included; a sequence of length 0 gets zeros) and splits the
+ * work by them; `paged` may be NULL (contiguous caches). */
+duo_status duo_attn_decode_kv8(duo_handle* handle, const duo_kv_cache* cache, const duo_kv8_cache* kv8, const void* q,
+                               void* o, void* workspace, size_t workspace_bytes, void* stream);
+duo_status duo_attn_decode_kv8_paged(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
+                                     const duo_kv8_cache* kv8, const void* q, void* o, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
+                                      const duo_kv8_cache* kv8, const int32_t* seq_lens, int64_t max_len,
+                                      const void* q, void* o, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Block tables kept on the device. A pool of num_blocks blocks of block_size tokens serves
+ * B sequences with `planes` tables each (planes = n_ret: one per retrieval head).
+ *   block_table int32 [B, planes, max_blocks]  entry j of a plane: the block of its tokens
+ *                                              block_size j ...; entries past the length are
+ *                                              not read
+ *   free_list   int32 [num_blocks]             ids of the free blocks: the first *free_count
+ *   free_count  int32 [1]
+ *   seq_lens    int32 [B]                      tokens each sequence holds
+ * all device memory. B planes max_blocks and block_size max_blocks must stay below 2^31. */
+typedef struct {
+  int32_t* block_table;
+  int32_t* free_list;
+  int32_t* free_count;
+  int32_t* seq_lens;
+  int32_t batch;
+  int32_t planes;
+  int32_t block_size; /* >= 1; a multiple of 128 for the attention entry points */
+  int32_t max_blocks;
+  int64_t num_blocks;
+} duo_block_pool;
+
+/* Brings tables, free list and lengths up to date for a step in which sequence b takes
+ * new_lens[b] >= 0 more tokens, or has finished (new_lens[b] = -1), and writes the slot map
+ * of the packed new tokens (arrays of max_tokens tokens). All on the device, so the call can
+ * be captured in a CUDA graph and replayed. In this order:
+ *   1. Finished sequences, by index: the blocks of their planes (plane by plane, first block
+ *      first) go onto the end of the free list; their length becomes 0. Their table entries
+ *      are left as they are.
+ *   2. The others, by index: a sequence that needs new blocks gets them if the free list
+ *      holds enough for it and all sequences before it; otherwise neither it nor any later
+ *      one that needs blocks gets any. Blocks are taken from the end of the free list, for
+ *      plane 0 first. A sequence is also turned down if it would pass max_blocks or if its
+ *      tokens pass max_tokens. A sequence that was turned down keeps its length, its tokens
+ *      get position and slots -1, and duo_device_error() reports DUO_ERR_CAPACITY.
+ * cu_new[b] is the sum of max(new_lens, 0) of the sequences before b, served or not (up to
+ * 2^31 - 1). Tokens past cu_new[B] are padding: sequence, position and slots -1.
+ * seq_lens_out [B] and free_count_out [1] receive the new lengths and count; they may be
+ * pool->seq_lens and pool->free_count. If they are not, the call leaves both inputs as they
+ * were, and the same call again gives the same result.
+ * A length below 0 or past the tables, new_lens below -1, a free count outside [0,
+ * num_blocks] (clamped) or a block id outside [0, num_blocks) (dropped from the free list,
+ * slots -1) is reported by duo_device_error() as DUO_ERR_INVALID_ARG; that sequence is
+ * turned down. workspace: duo_block_tables_workspace_size(batch) bytes of device memory, 16-byte
+ * aligned; nothing in it survives the call, and calls sharing it must be ordered. */
+size_t duo_block_tables_workspace_size(int32_t batch);
+duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* new_lens, int32_t max_tokens,
+                                   int32_t* seq_lens_out, int32_t* free_count_out, const duo_slot_map* map,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Dual Chunk Attention (vLLM pull request "[Model] Implement DualChunkAttention for
  * Qwen2 Models"): the sequence is cut into chunks of chunk_len positions from the start

@@ -315,6 +315,200 @@ class DuoKv4PagedLayer(DuoKv4Layer):
         return out
 
 
+class DuoKv8Layer(DuoLayer):
+    """A layer whose retrieval heads' caches hold 8-bit codes (``code``: "int8" or "e4m3") with
+    one fp32 scale per block of 64 tokens of a head (layout and rounding in include/duo_attn.h):
+    k_codes/v_codes [B, n_ret, cap64, D], k_scale/v_scale fp32 [B, n_ret, cap64 / 64] and the
+    open block's rows in bf16, k_tail/v_tail [B, n_ret, 64, D]. Streaming heads keep their bf16
+    sink + ring caches."""
+
+    def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, max_seq_len,
+                 is_retrieval, code="int8", device="cuda"):
+        super().__init__(batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, 1, is_retrieval,
+                         device=device)
+        self.cap = max_seq_len
+        self._set_capacity(max_seq_len)
+        cap64 = -(-max_seq_len // _lib.DUO_KV8_BLOCK) * _lib.DUO_KV8_BLOCK if self.n_ret else 0
+        self._codes(code, (batch, self.n_ret, cap64), (batch, self.n_ret, cap64 // _lib.DUO_KV8_BLOCK))
+        self.reset()
+
+    def _set_capacity(self, max_seq_len):
+        """The handle's capacity is max_seq_len: create it again with that value."""
+        import torch
+        duo_destroy(self.handle)
+        self.handle = None
+        with torch.cuda.device(self.device):
+            self.handle = duo_create(self.B, self.Hq, self.Hkv, self.D, self.S, self.R, max_seq_len,
+                                     self.is_retrieval)
+
+    def _codes(self, code, rows, blocks):
+        import torch
+        if code not in ("int8", "e4m3"):
+            raise ValueError(f'code: "int8" or "e4m3", got {code!r}')
+        self.code = code
+        dtype = torch.int8 if code == "int8" else torch.float8_e4m3fn
+        dev = dict(device=self.device)
+        self.k_codes = torch.zeros(rows + (self.D,), dtype=torch.uint8, **dev).view(dtype)
+        self.v_codes = torch.zeros(rows + (self.D,), dtype=torch.uint8, **dev).view(dtype)
+        self.k_scale = torch.zeros(blocks, dtype=torch.float32, **dev)
+        self.v_scale = torch.zeros(blocks, dtype=torch.float32, **dev)
+        self.k_tail = torch.zeros((self.B, self.n_ret, _lib.DUO_KV8_BLOCK, self.D), dtype=torch.bfloat16, **dev)
+        self.v_tail = torch.zeros_like(self.k_tail)
+        ptr = lambda t: t.data_ptr() if t.numel() else None
+        self.kv8 = _lib.duo_kv8_cache(ptr(self.k_codes), ptr(self.v_codes), ptr(self.k_scale), ptr(self.v_scale),
+                                      ptr(self.k_tail), ptr(self.v_tail),
+                                      _lib.DUO_KV8_INT8 if code == "int8" else _lib.DUO_KV8_E4M3)
+        self.paged = None
+
+    def append(self, k_new, v_new, stream=None) -> None:
+        T = k_new.shape[1]
+        _on(self.device, "k_new", k_new, (self.B, T, self.Hkv, self.D))
+        _on(self.device, "v_new", v_new, (self.B, T, self.Hkv, self.D))
+        if self.paged is None:
+            _lib.duo_kv_append_kv8(self.handle, self.cache, self.kv8, k_new, v_new, T, stream)
+        else:
+            _lib.duo_kv_append_kv8_paged(self.handle, self.cache, self.paged, self.kv8, k_new, v_new, T, stream)
+
+    def decode(self, q, out=None, stream=None):
+        out = self._out(q, (self.B, self.Hq, self.D), out)
+        if self.paged is None:
+            _lib.duo_attn_decode_kv8(self.handle, self.cache, self.kv8, q, out, self.workspace, stream)
+        else:
+            _lib.duo_attn_decode_kv8_paged(self.handle, self.cache, self.paged, self.kv8, q, out, self.workspace,
+                                           stream)
+        return out
+
+    def decode_varlen(self, q, seq_lens, max_len, out=None, stream=None):
+        """Decode where sequence b holds seq_lens[b] tokens, the new one included (device int32
+        [B], <= max_len); a sequence of length 0 gets zeros."""
+        out = self._out(q, (self.B, self.Hq, self.D), out)
+        _check_lens(seq_lens, self.B)
+        _lib.duo_attn_decode_kv8_varlen(self.handle, self.cache, self.paged, self.kv8, seq_lens, max_len, q, out,
+                                        self.workspace, stream)
+        return out
+
+    def _out(self, q, shape, out):
+        import torch
+        _on(self.device, "q", q, shape)
+        if out is None:
+            return torch.empty_like(q)
+        _on(self.device, "o", out, shape)
+        return out
+
+    def append_varlen(self, *args, **kwargs):
+        raise NotImplementedError("8-bit caches: append_ragged (a paged layer) takes lengths from the device")
+
+    def prefill(self, *args, **kwargs):
+        raise NotImplementedError("prefill against 8-bit caches is not provided")
+
+    def dca_prefill(self, *args, **kwargs):
+        raise NotImplementedError("Dual Chunk Attention over 8-bit caches is not provided")
+
+    dca_decode = dca_prefill
+
+
+class DuoKv8PagedLayer(DuoKv8Layer):
+    """8-bit caches whose codes and scales live in a pool of blocks shared by every sequence
+    and head: k_codes/v_codes [num_blocks, block_size, D], k_scale/v_scale [num_blocks,
+    block_size / 64], row t of retrieval head r of sequence b at row t % block_size of block
+    block_table[b, r, t // block_size] (device int32 [B, n_ret, max_blocks]; block_size a
+    multiple of 128). ``append_ragged`` and ``decode_varlen`` take every length from the device
+    (see DuoBlockPool)."""
+
+    def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, block_size,
+                 max_blocks, num_blocks, block_table, is_retrieval, code="int8", device="cuda"):
+        import torch
+        super().__init__(batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, 1, is_retrieval,
+                         code=code, device=device)
+        if block_table is not None:
+            if (block_table.dtype != torch.int32 or not block_table.is_cuda or not block_table.is_contiguous()
+                    or tuple(block_table.shape) != (batch, self.n_ret, max_blocks)):
+                raise ValueError(f"block_table: need a contiguous CUDA int32 tensor of shape "
+                                 f"{(batch, self.n_ret, max_blocks)}")
+        blocks = num_blocks if self.n_ret else 0
+        self._codes(code, (blocks, block_size), (blocks, block_size // _lib.DUO_KV8_BLOCK))
+        self.block_size = block_size
+        self.block_table = block_table
+        self.paged = _lib.duo_paged(block_table.data_ptr() if block_table is not None else None, block_size,
+                                    max_blocks, num_blocks, None)
+
+    def append_ragged(self, k_new, v_new, slot_map, stream=None) -> None:
+        """A packed batch of tokens [num_tokens, Hkv, D], each at its own place (a DuoSlotMap)."""
+        N = k_new.shape[0]
+        _on(self.device, "k_new", k_new, (N, self.Hkv, self.D))
+        _on(self.device, "v_new", v_new, (N, self.Hkv, self.D))
+        if slot_map.batch != self.B or slot_map.num_tokens != N or (self.n_ret and slot_map.planes != self.n_ret):
+            raise ValueError(f"slot_map: of {slot_map.batch} sequences, {slot_map.num_tokens} tokens and "
+                             f"{slot_map.planes} planes; need {self.B}, {N} and {self.n_ret}")
+        _lib.duo_kv_append_kv8_ragged(self.handle, self.cache, self.paged, self.kv8, slot_map.c, N, k_new, v_new,
+                                      stream)
+
+
+class DuoSlotMap:
+    """Where the tokens of a packed batch go: cu_new int32 [B + 1], token_seq and token_pos int32
+    [num_tokens], slots int64 [num_tokens, planes], all on the device (include/duo_attn.h)."""
+
+    def __init__(self, cu_new, token_seq, token_pos, slots):
+        import torch
+        N = token_seq.shape[0]
+        for name, t, dtype, dims in (("cu_new", cu_new, torch.int32, 1), ("token_seq", token_seq, torch.int32, 1),
+                                     ("token_pos", token_pos, torch.int32, 1), ("slots", slots, torch.int64, 2)):
+            if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
+                raise ValueError(f"{name}: need a contiguous CUDA {dtype} tensor of {dims} dimension(s)")
+        if token_pos.shape[0] != N or slots.shape[0] != N:
+            raise ValueError("token_seq, token_pos and slots: different numbers of tokens")
+        self.cu_new, self.token_seq, self.token_pos, self.slots = cu_new, token_seq, token_pos, slots
+        self.batch, self.num_tokens, self.planes = cu_new.shape[0] - 1, N, slots.shape[1]
+        self.c = _lib.duo_slot_map(cu_new.data_ptr(), token_seq.data_ptr(), token_pos.data_ptr(), slots.data_ptr())
+
+
+class DuoBlockPool:
+    """Block tables, free list and lengths of a batch kept on the device, and the slot map of
+    its packed steps of up to max_tokens tokens. block_table int32 [B, planes, max_blocks],
+    free_list int32 [num_blocks] (at first every block, taken from the end), free_count int32
+    [1], seq_lens int32 [B]. ``planes`` is a layer's number of retrieval heads."""
+
+    def __init__(self, batch, planes, block_size, max_blocks, num_blocks, max_tokens, device="cuda"):
+        import torch
+        self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.block_table = torch.full((batch, planes, max_blocks), -1, **i32)
+        self.free_list = torch.arange(num_blocks, **i32)
+        self.free_count = torch.full((1,), num_blocks, **i32)
+        self.seq_lens = torch.zeros(batch, **i32)
+        self.max_tokens = max_tokens
+        self.slot_map = DuoSlotMap(torch.zeros(batch + 1, **i32), torch.full((max_tokens,), -1, **i32),
+                                   torch.full((max_tokens,), -1, **i32),
+                                   torch.full((max_tokens, planes), -1, dtype=torch.int64, device=self.device))
+        self.workspace = torch.empty(_lib.duo_block_tables_workspace_size(batch), dtype=torch.uint8,
+                                     device=self.device)
+        self.c = _lib.duo_block_pool(self.block_table.data_ptr(), self.free_list.data_ptr(),
+                                     self.free_count.data_ptr(), self.seq_lens.data_ptr(), batch, planes, block_size,
+                                     max_blocks, num_blocks)
+
+    def update(self, new_lens, seq_lens_out=None, free_count_out=None, stream=None):
+        """Sequence b takes new_lens[b] more tokens (-1: it has finished; device int32 [B]).
+        Updates tables, free list and lengths (into the *_out tensors if given) and returns
+        the slot map of the packed tokens, whose arrays the next update overwrites."""
+        B = self.seq_lens.shape[0]
+        lens = self.seq_lens if seq_lens_out is None else seq_lens_out
+        count = self.free_count if free_count_out is None else free_count_out
+        for name, t, n in (("new_lens", new_lens, B), ("seq_lens_out", lens, B), ("free_count_out", count, 1)):
+            if str(t.dtype) != "torch.int32" or t.device != self.seq_lens.device or not t.is_contiguous() \
+                    or t.numel() != n:
+                raise ValueError(f"{name}: need a contiguous int32 tensor of {n} element(s) on {self.seq_lens.device}")
+        _lib.duo_block_tables_update(self.c, new_lens, self.max_tokens, lens, count, self.slot_map.c, self.workspace,
+                                     stream)
+        return self.slot_map
+
+
+def _on(device, name, t, shape):
+    """_lib._bf16, and on the layer's own device."""
+    _lib._bf16(t, shape, name)
+    if device.index is not None and t.device.index != device.index:
+        raise ValueError(f"{name}: on {t.device}, the layer is on {device}")
+
+
 def _check_mscale(mscale, shape):
     import torch
     if mscale is None:

@@ -26,6 +26,10 @@ DUO_ERR_WORKSPACE = 6
 DUO_STREAMING = 0
 DUO_RETRIEVAL = 1
 
+DUO_KV8_BLOCK = 64  # tokens that share a scale in an 8-bit cache
+DUO_KV8_INT8 = 0
+DUO_KV8_E4M3 = 1
+
 # exported names of include/duo_attn.h (checked against the library by the tests)
 EXPORTS = (
     "duo_classify_heads", "duo_create", "duo_destroy", "duo_set_head_mask", "duo_cache_reset", "duo_kv_append",
@@ -33,7 +37,9 @@ EXPORTS = (
     "duo_attn_decode_static", "duo_kv_append_paged", "duo_attn_prefill_paged", "duo_attn_decode_paged",
     "duo_paged_stream_dead_blocks", "duo_dca_prefill", "duo_dca_decode", "duo_kv_append_kv4",
     "duo_attn_decode_kv4", "duo_kv_append_kv4_paged", "duo_attn_decode_kv4_paged", "duo_attn_prefill_kv4",
-    "duo_kv_append_varlen", "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait",
+    "duo_kv_append_kv8", "duo_kv_append_kv8_paged", "duo_kv_append_kv8_ragged", "duo_attn_decode_kv8",
+    "duo_attn_decode_kv8_paged", "duo_attn_decode_kv8_varlen", "duo_block_tables_workspace_size",
+    "duo_block_tables_update", "duo_kv_append_varlen", "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait",
     "duo_last_error", "duo_status_string",
 )
 
@@ -58,6 +64,21 @@ class duo_paged(ctypes.Structure):
 class duo_kv4_cache(ctypes.Structure):
     _fields_ = [(name, c_void_p) for name in ("k_codes", "v_codes", "k_sz", "v_sz", "ks_codes", "vs_codes", "ks_sz",
                                               "vs_sz")]
+
+
+class duo_kv8_cache(ctypes.Structure):
+    _fields_ = [(name, c_void_p) for name in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail")] + \
+        [("code_type", c_int32)]
+
+
+class duo_slot_map(ctypes.Structure):
+    _fields_ = [(name, c_void_p) for name in ("cu_new", "token_seq", "token_pos", "slots")]
+
+
+class duo_block_pool(ctypes.Structure):
+    _fields_ = [(name, c_void_p) for name in ("block_table", "free_list", "free_count", "seq_lens")] + \
+        [("batch", c_int32), ("planes", c_int32), ("block_size", c_int32), ("max_blocks", c_int32),
+         ("num_blocks", c_int64)]
 
 
 class duo_kv_cache(ctypes.Structure):
@@ -115,6 +136,24 @@ def library() -> ctypes.CDLL:
                                       c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
         "duo_dca_decode": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_void_p, c_void_p, c_void_p,
                                      c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "duo_kv_append_kv8": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_kv8_cache), c_void_p, c_void_p,
+                                        c_int32, c_void_p]),
+        "duo_kv_append_kv8_paged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
+                                              POINTER(duo_kv8_cache), c_void_p, c_void_p, c_int32, c_void_p]),
+        "duo_kv_append_kv8_ragged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
+                                               POINTER(duo_kv8_cache), POINTER(duo_slot_map), c_int32, c_void_p,
+                                               c_void_p, c_void_p]),
+        "duo_attn_decode_kv8": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_kv8_cache), c_void_p,
+                                          c_void_p, c_void_p, c_size_t, c_void_p]),
+        "duo_attn_decode_kv8_paged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
+                                                POINTER(duo_kv8_cache), c_void_p, c_void_p, c_void_p, c_size_t,
+                                                c_void_p]),
+        "duo_attn_decode_kv8_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
+                                                 POINTER(duo_kv8_cache), c_void_p, c_int64, c_void_p, c_void_p,
+                                                 c_void_p, c_size_t, c_void_p]),
+        "duo_block_tables_workspace_size": (c_size_t, [c_int32]),
+        "duo_block_tables_update": (c_int32, [POINTER(duo_block_pool), c_void_p, c_int32, c_void_p, c_void_p,
+                                              POINTER(duo_slot_map), c_void_p, c_size_t, c_void_p]),
         "duo_kv_append_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_void_p, c_void_p,
                                            c_void_p]),
         "duo_attn_decode_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_int64, c_void_p, c_void_p,
@@ -272,6 +311,64 @@ def duo_attn_decode_kv4_paged(handle, cache: "duo_kv_cache", paged: "duo_paged",
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(library().duo_attn_decode_kv4_paged(handle, ctypes.byref(cache), ctypes.byref(paged), ctypes.byref(kv4),
                                                _ptr(q), _ptr(o), _ptr(workspace), nbytes, _stream_ptr(stream)))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def duo_kv_append_kv8(handle, cache: "duo_kv_cache", kv8: "duo_kv8_cache", k_new, v_new, T: int,
+                      stream=None) -> None:
+    _check(library().duo_kv_append_kv8(handle, _ref(cache), _ref(kv8), _ptr(k_new), _ptr(v_new), T,
+                                       _stream_ptr(stream)))
+
+
+def duo_kv_append_kv8_paged(handle, cache: "duo_kv_cache", paged: "duo_paged", kv8: "duo_kv8_cache", k_new, v_new,
+                            T: int, stream=None) -> None:
+    _check(library().duo_kv_append_kv8_paged(handle, _ref(cache), _ref(paged), _ref(kv8), _ptr(k_new), _ptr(v_new), T,
+                                             _stream_ptr(stream)))
+
+
+def duo_kv_append_kv8_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", kv8: "duo_kv8_cache",
+                             slot_map: "duo_slot_map", num_tokens: int, k_new, v_new, stream=None) -> None:
+    """A packed batch: each token at the position and pool rows its slot map entries name."""
+    _check(library().duo_kv_append_kv8_ragged(handle, _ref(cache), _ref(paged), _ref(kv8), _ref(slot_map), num_tokens,
+                                              _ptr(k_new), _ptr(v_new), _stream_ptr(stream)))
+
+
+def duo_attn_decode_kv8(handle, cache: "duo_kv_cache", kv8: "duo_kv8_cache", q, o, workspace, stream=None) -> None:
+    _check(library().duo_attn_decode_kv8(handle, _ref(cache), _ref(kv8), _ptr(q), _ptr(o), _ptr(workspace),
+                                         _nbytes(workspace), _stream_ptr(stream)))
+
+
+def duo_attn_decode_kv8_paged(handle, cache: "duo_kv_cache", paged: "duo_paged", kv8: "duo_kv8_cache", q, o,
+                              workspace, stream=None) -> None:
+    _check(library().duo_attn_decode_kv8_paged(handle, _ref(cache), _ref(paged), _ref(kv8), _ptr(q), _ptr(o),
+                                               _ptr(workspace), _nbytes(workspace), _stream_ptr(stream)))
+
+
+def duo_attn_decode_kv8_varlen(handle, cache: "duo_kv_cache", paged, kv8: "duo_kv8_cache", seq_lens, max_len: int,
+                               q, o, workspace, stream=None) -> None:
+    """Decode with lengths read on the device; paged: a duo_paged, or None (contiguous)."""
+    _check(library().duo_attn_decode_kv8_varlen(handle, _ref(cache), _ref(paged), _ref(kv8), _ptr(seq_lens), max_len,
+                                                _ptr(q), _ptr(o), _ptr(workspace), _nbytes(workspace),
+                                                _stream_ptr(stream)))
+
+
+def duo_block_tables_workspace_size(batch: int) -> int:
+    return int(library().duo_block_tables_workspace_size(batch))
+
+
+def duo_block_tables_update(pool: "duo_block_pool", new_lens, max_tokens: int, seq_lens_out, free_count_out,
+                            slot_map: "duo_slot_map", workspace, stream=None) -> None:
+    """Block tables, free list, lengths and slot map of a step, from its new lengths (on the device)."""
+    _check(library().duo_block_tables_update(_ref(pool), _ptr(new_lens), max_tokens, _ptr(seq_lens_out),
+                                             _ptr(free_count_out), _ref(slot_map), _ptr(workspace),
+                                             _nbytes(workspace), _stream_ptr(stream)))
 
 
 def duo_dca_prefill(handle, cache, q, q_succ, q_inter, k, v, mscale, T: int, chunk_len: int, o,

@@ -1,0 +1,308 @@
+// duo_block_tables_update: block tables, slot maps, free list and lengths of a serving
+// step, from the requests' lengths, on the device.
+//
+// With s = block_size, L_b the length and new_b the new tokens of sequence b, it holds
+// ceil(L_b / s) blocks a plane and needs planes (ceil((L_b + new_b) / s) - ceil(L_b / s))
+// more. Three prefix sums over the sequences decide everything: the new tokens (cu_new),
+// the blocks needed (first come, first served: a sequence is served iff it needs none or
+// the sum up to it fits) and the blocks given back. The k-th new block is entry
+// avail - 1 - k of the free list, so every table entry and slot follows from the sums
+// without an atomic and the result does not depend on the order of threads.
+//
+// Latency-bound: a few KB of lengths in, 8 + 8 planes bytes a token out. One CTA of 1024
+// threads does the sums (each thread one sequence, warp shuffles, a carry between rounds
+// of 1024). A small step (kFuseWork outputs) is finished by the same CTA in the same
+// launch; larger ones by a second grid, launched as the first one's programmatic
+// dependent, in which each thread finds its sequence by bisecting the sums.
+#include "duo_device.cuh"
+
+namespace duo {
+namespace {
+
+__device__ unsigned int g_tables_err;
+
+constexpr int kScanThreads = 1024;
+// outputs (table entries and slots) up to which the scanning CTA writes them itself
+constexpr int64_t kFuseWork = 8192;
+
+// Scratch, int32: [0] free blocks after the returns, [1] blocks handed out, [2] tokens in
+// the packed batch (at most max_tokens), then per sequence the old length (-1: turned down
+// or finished), and the prefix sums of needed and returned blocks, B + 1 entries each.
+struct Scratch {
+  int32_t* head;
+  int32_t* old_len;
+  int32_t* need_base;
+  int32_t* rel_base;
+};
+__device__ __forceinline__ Scratch scratch_of(const BlockTablesParams& p) {
+  Scratch s;
+  s.head = p.scratch;
+  s.old_len = p.scratch + 4;
+  s.need_base = s.old_len + p.B;
+  s.rel_base = s.need_base + p.B + 1;
+  return s;
+}
+
+__device__ __forceinline__ int blocks_of(int64_t len, int bs) { return (int)((len + bs - 1) / bs); }
+
+// Largest i in [0, n) with base[i] <= v (base non-decreasing, base[0] = 0 <= v).
+__device__ __forceinline__ int bisect(const int32_t* base, int n, int v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (base[mid] <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Inclusive sums of three values over the CTA's threads (tok saturates in 64 bits only).
+struct Sums {
+  int64_t tok;
+  int32_t need, rel;
+};
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, v.tok, o);
+    const int32_t a = __shfl_up_sync(0xffffffffu, v.need, o);
+    const int32_t r = __shfl_up_sync(0xffffffffu, v.rel, o);
+    if (lane >= o) v.tok += t, v.need += a, v.rel += r;
+  }
+  __syncthreads();  // the last round's readers are done with warp_sums
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    Sums w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, w.tok, o);
+      const int32_t a = __shfl_up_sync(0xffffffffu, w.need, o);
+      const int32_t r = __shfl_up_sync(0xffffffffu, w.rel, o);
+      if (lane >= o) w.tok += t, w.need += a, w.rel += r;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    const Sums w = warp_sums[warp - 1];
+    v.tok += w.tok, v.need += w.need, v.rel += w.rel;
+  }
+  return v;
+}
+
+// Writes the new blocks' table entries and the tokens' maps (items = tokens x planes), both
+// shared out among `step` threads, of which this is number `first`.
+__device__ void fill(const BlockTablesParams& p, const Scratch& s, int64_t first, int64_t step) {
+  const int avail = s.head[0], handed = s.head[1], tokens = s.head[2];
+  for (int64_t e = first; e < handed; e += step) {
+    const int b = bisect(s.need_base, p.B, (int)e);
+    const int have = blocks_of(s.old_len[b], p.bs);
+    const int per = (s.need_base[b + 1] - s.need_base[b]) / p.planes;
+    const int k = (int)e - s.need_base[b];
+    const int id = p.free_list[avail - 1 - (int)e];
+    if (id < 0 || id >= p.num_blocks) atomicOr(&g_tables_err, kErrBadBlock);
+    p.table[((int64_t)b * p.planes + k / per) * p.max_blocks + have + k % per] = id;
+  }
+  const int64_t items = (int64_t)p.max_tokens * p.planes;
+  for (int64_t it = first; it < items; it += step) {
+    const int i = (int)(it / p.planes);
+    const int pl = (int)(it - (int64_t)i * p.planes);
+    int seq = -1, pos = -1;
+    int64_t slot = -1;
+    if (i < tokens) {
+      seq = bisect(p.cu_new, p.B, i);
+      const int old = s.old_len[seq];
+      if (old >= 0) {
+        pos = old + (i - p.cu_new[seq]);
+        const int have = blocks_of(old, p.bs);
+        const int j = pos / p.bs;
+        int id;
+        if (j < have) {
+          id = p.table[((int64_t)seq * p.planes + pl) * p.max_blocks + j];
+        } else {
+          const int nb = s.need_base[seq];
+          const int per = (s.need_base[seq + 1] - nb) / p.planes;
+          id = p.free_list[avail - 1 - (nb + pl * per + (j - have))];
+        }
+        if (id < 0 || id >= p.num_blocks)
+          atomicOr(&g_tables_err, kErrBadBlock);
+        else
+          slot = (int64_t)id * p.bs + (pos - j * p.bs);
+      }
+    }
+    if (pl == 0) {
+      p.token_seq[i] = seq;
+      p.token_pos[i] = pos;
+    }
+    p.slots[it] = slot;
+  }
+}
+
+__global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const BlockTablesParams p, int fuse) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ Sums warp_sums[32];
+  __shared__ int s_handed;
+  const Scratch s = scratch_of(p);
+  const int tid = threadIdx.x;
+  const int64_t cap = (int64_t)p.max_blocks * p.bs;
+  uint32_t err = 0;
+
+  // the sums: tokens, blocks needed, blocks given back
+  int64_t c_tok = 0;
+  int32_t c_need = 0, c_rel = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+    const int b = b0 + tid;
+    Sums v{0, 0, 0};
+    int len = 0, nw = 0, kind = 2;  // 0 takes tokens, 1 finished, 2 turned down
+    if (b < p.B) {
+      len = p.seq_lens[b];
+      nw = p.new_lens[b];
+      if (len < 0 || len > cap || nw < -1)
+        err |= kErrBadLength;
+      else if (nw == -1)
+        kind = 1;
+      else if (len + (int64_t)nw > cap)
+        err |= kErrPoolFull;
+      else
+        kind = 0;
+      v.tok = nw > 0 ? nw : 0;
+      if (kind == 0) v.need = p.planes * (blocks_of(len + (int64_t)nw, p.bs) - blocks_of(len, p.bs));
+      if (kind == 1) v.rel = p.planes * blocks_of(len, p.bs);
+    }
+    // a sequence whose tokens pass the packed batch is turned down before it asks for blocks
+    Sums t = block_scan(Sums{v.tok, 0, 0}, warp_sums);
+    const int64_t tok_end = c_tok + t.tok, tok_begin = tok_end - v.tok;
+    if (kind == 0 && nw > 0 && tok_end > p.max_tokens) {
+      kind = 2;
+      v.need = 0;
+      err |= kErrPoolFull;
+    }
+    const Sums u = block_scan(Sums{v.tok, v.need, v.rel}, warp_sums);
+    if (b < p.B) {
+      p.cu_new[b] = (int)(tok_begin < 0x7fffffff ? tok_begin : 0x7fffffff);
+      s.need_base[b] = c_need + u.need - v.need;
+      s.rel_base[b] = c_rel + u.rel - v.rel;
+      s.old_len[b] = kind == 0 ? len : (kind == 1 ? -2 - len : -1);
+    }
+    const Sums last = warp_sums[31];
+    c_tok += last.tok;
+    c_need += last.need;
+    c_rel += last.rel;
+  }
+  if (tid == 0) {
+    p.cu_new[p.B] = (int)(c_tok < 0x7fffffff ? c_tok : 0x7fffffff);
+    s.need_base[p.B] = c_need;
+    s.rel_base[p.B] = c_rel;
+    s_handed = 0;
+  }
+  int count = *p.free_count;
+  if (count < 0 || count > p.num_blocks) {
+    err |= kErrBadLength;
+    count = count < 0 ? 0 : (int)p.num_blocks;
+  }
+  __syncthreads();
+
+  // returned blocks, in order, dropping ids that are none
+  int avail = count;
+  for (int e0 = 0; e0 < c_rel; e0 += kScanThreads) {
+    const int e = e0 + tid;
+    int id = -1;
+    if (e < c_rel) {
+      const int b = bisect(s.rel_base, p.B, e);
+      const int have = blocks_of(-2 - s.old_len[b], p.bs);
+      const int k = e - s.rel_base[b];
+      id = p.table[((int64_t)b * p.planes + k / have) * p.max_blocks + k % have];
+      if (id < 0 || id >= p.num_blocks) {
+        err |= kErrBadBlock;
+        id = -1;
+      }
+    }
+    const Sums u = block_scan(Sums{0, id >= 0, 0}, warp_sums);
+    const int64_t at = (int64_t)avail + u.need - 1;
+    if (id >= 0 && at < p.num_blocks) p.free_list[at] = id;
+    const int64_t next = (int64_t)avail + warp_sums[31].need;
+    if (next > p.num_blocks) err |= kErrBadBlock;  // more blocks than the pool has: one came back twice
+    avail = (int)(next < p.num_blocks ? next : p.num_blocks);
+  }
+
+  // who is served
+  for (int b = tid; b < p.B; b += kScanThreads) {
+    const int old = s.old_len[b];
+    const int end = s.need_base[b + 1];
+    const bool asks = end > s.need_base[b];
+    int len = p.seq_lens[b];
+    if (old >= 0) {
+      if (!asks || end <= avail) {
+        len = old + p.new_lens[b];
+        if (asks) atomicMax(&s_handed, end);
+      } else {
+        s.old_len[b] = -1;
+        err |= kErrPoolFull;
+      }
+    } else if (old <= -2) {
+      len = 0;
+    }
+    p.seq_lens_out[b] = len;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    s.head[0] = avail;
+    s.head[1] = s_handed;
+    s.head[2] = (int)(c_tok < p.max_tokens ? c_tok : p.max_tokens);
+    *p.free_count_out = avail - s_handed;
+  }
+  if (err) atomicOr(&g_tables_err, err);
+  if (fuse) {
+    __syncthreads();
+    fill(p, s, tid, kScanThreads);
+  }
+}
+
+__global__ void __launch_bounds__(256) block_tables_fill_kernel(const BlockTablesParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  fill(p, scratch_of(p), (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+}  // namespace
+
+size_t block_tables_scratch_bytes(int B) { return ((size_t)4 + 3 * (size_t)B + 2) * 4; }
+
+cudaError_t launch_block_tables(const BlockTablesParams& p, int num_sms, cudaStream_t stream) {
+  // table entries of the new blocks: at most one partly filled block a plane and sequence
+  // beside the full ones
+  const int64_t work = (int64_t)p.max_tokens * p.planes + (int64_t)p.B * p.planes;
+  const bool fuse = work <= kFuseWork;
+  block_tables_scan_kernel<<<1, kScanThreads, 0, stream>>>(p, fuse ? 1 : 0);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || fuse) return e;
+  int64_t blocks = (work + 255) / 256;
+  if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_tables_fill_kernel, p);
+}
+
+cudaError_t block_tables_read_clear_error(uint32_t* code) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_tables_err, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *code = v;
+  if (v) {
+    v = 0;
+    e = cudaMemcpyToSymbol(g_tables_err, &v, sizeof(v));
+  }
+  return e;
+}
+
+}  // namespace duo

@@ -747,6 +747,270 @@ duo_status duo_dca_decode(duo_handle* h, const duo_kv_cache* c, const void* q, c
   return decode_impl(h, c, nullptr, q, o, workspace, workspace_bytes, stream, &dca);
 }
 
+// ---------------------------------------------------------------------- 8-bit caches
+static int64_t pitch64(int64_t rows) { return (rows + kKv8Block - 1) / kKv8Block * kKv8Block; }
+
+// Rows of the codes in all (a plane pitch of cap64, or the pool); -1 if a row index would pass 2^31.
+static int64_t kv8_rows(const duo_handle* h, const PagedLayout& pg) {
+  const int64_t rows = pg.table ? pg.num_blocks * pg.block_size : (int64_t)h->sh.B * h->sh.n_ret * pitch64(h->sh.cap);
+  return rows <= 0x7fffffffLL ? rows : -1;
+}
+
+static duo_status check_kv8(const duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, const duo_kv8_cache* kv,
+                            PagedLayout* pg) {
+  if (!c) return fail(DUO_ERR_INVALID_ARG, "cache is NULL");
+  if (!kv) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
+  if (kv->code_type != DUO_KV8_INT8 && kv->code_type != DUO_KV8_E4M3)
+    return fail(DUO_ERR_INVALID_ARG, "code_type = %d is neither DUO_KV8_INT8 nor DUO_KV8_E4M3", kv->code_type);
+  if (pgd && pgd->stream_table)
+    return fail(DUO_ERR_UNSUPPORTED, "8-bit caches keep streaming heads in their ring caches");
+  *pg = PagedLayout{nullptr, 0, 0, 0, nullptr};
+  duo_status st;
+  if (h->sh.n_ret > 0) {
+    if ((st = check_paged(h, pgd, pg)) != DUO_OK) return st;
+    const void* a[] = {kv->k_codes, kv->v_codes, kv->k_scale, kv->v_scale, kv->k_tail, kv->v_tail};
+    for (const void* x : a)
+      if (!x || !aligned16(x)) return fail(DUO_ERR_INVALID_ARG, "8-bit cache arrays NULL or not 16-byte aligned");
+    if (kv8_rows(h, *pg) < 0) return fail(DUO_ERR_UNSUPPORTED, "the codes have 2^31 rows or more");
+  }
+  return check_cache(h, c, false, true);
+}
+
+static duo_status append_kv8_impl(duo_handle* h, duo_kv_cache* c, const duo_paged* pgd, const duo_kv8_cache* kv,
+                                  const duo_slot_map* map, const void* k_new, const void* v_new, int32_t T,
+                                  void* stream) {
+  duo_status st = check_handle(h);
+  if (st != DUO_OK) return st;
+  PagedLayout pg;
+  if ((st = check_kv8(h, c, pgd, kv, &pg)) != DUO_OK) return st;
+  const Shape& sh = h->sh;
+  int64_t tokens;
+  if (map) {
+    if (T < 0) return fail(DUO_ERR_INVALID_ARG, "num_tokens = %d < 0", T);
+    if (T == 0) return ok();
+    if (!map->cu_new || !map->token_seq || !map->token_pos || (sh.n_ret > 0 && !map->slots))
+      return fail(DUO_ERR_INVALID_ARG, "slot map: NULL array");
+    if ((reinterpret_cast<uintptr_t>(map->cu_new) | reinterpret_cast<uintptr_t>(map->token_seq) |
+         reinterpret_cast<uintptr_t>(map->token_pos)) & 3u || reinterpret_cast<uintptr_t>(map->slots) & 7u)
+      return fail(DUO_ERR_INVALID_ARG, "slot map: misaligned array");
+    tokens = T;
+  } else {
+    if (T < 1) return fail(DUO_ERR_INVALID_ARG, "T = %d < 1", T);
+    if (c->n + T > 0x7fffffffLL) return fail(DUO_ERR_CAPACITY, "positions would reach 2^31");
+    if (sh.n_ret > 0 && (st = check_capacity(h, pg, c->n + T, DUO_ERR_CAPACITY)) != DUO_OK) return st;
+    tokens = (int64_t)sh.B * T;
+    if (tokens > 0x7fffffffLL - 64) return fail(DUO_ERR_UNSUPPORTED, "B x T reaches 2^31");
+  }
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
+    return fail(DUO_ERR_INVALID_ARG, "k_new / v_new NULL or not 16-byte aligned");
+  Kv8AppendParams p;
+  memset(&p, 0, sizeof(p));
+  p.k_new = static_cast<const uint16_t*>(k_new);
+  p.v_new = static_cast<const uint16_t*>(v_new);
+  p.k_codes = static_cast<uint8_t*>(kv->k_codes);
+  p.v_codes = static_cast<uint8_t*>(kv->v_codes);
+  p.k_scale = kv->k_scale;
+  p.v_scale = kv->v_scale;
+  p.k_tail = static_cast<uint16_t*>(kv->k_tail);
+  p.v_tail = static_cast<uint16_t*>(kv->v_tail);
+  p.k_sr = static_cast<uint16_t*>(c->k_sr);
+  p.v_sr = static_cast<uint16_t*>(c->v_sr);
+  p.pos = c->pos;
+  p.n = c->n;
+  p.T = T;
+  p.tokens = (int)tokens;
+  // Tokens per CTA and plane: a block's 64 when there are enough for several CTAs per SM,
+  // down to one token (64 sequences of one token on a CTA would take them in turn).
+  const int64_t per = tokens * (2 * sh.n_ret + (sh.n_str > 0)) / ((int64_t)h->num_sms * 8);
+  p.chunk = 1;
+  while (p.chunk < kKv8Block && p.chunk * 2 <= per) p.chunk *= 2;
+  p.code_type = kv->code_type;
+  p.cap64 = pitch64(sh.cap);
+  p.rows = sh.n_ret > 0 ? kv8_rows(h, pg) : 0;
+  p.sh = sh;
+  p.heads = h->heads;
+  p.pg = pg;
+  if (map) {
+    p.cu_new = map->cu_new;
+    p.token_seq = map->token_seq;
+    p.token_pos = map->token_pos;
+    p.slots = map->slots;
+  }
+  cudaError_t ce = launch_append_kv8(p, (cudaStream_t)stream);
+  if (ce != cudaSuccess) return cuda_fail(ce, "append launch (8-bit)");
+  if (!map) c->n += T;
+  return ok();
+}
+
+duo_status duo_kv_append_kv8(duo_handle* h, duo_kv_cache* c, const duo_kv8_cache* kv8, const void* k_new,
+                             const void* v_new, int32_t T, void* stream) {
+  return append_kv8_impl(h, c, nullptr, kv8, nullptr, k_new, v_new, T, stream);
+}
+
+duo_status duo_kv_append_kv8_paged(duo_handle* h, duo_kv_cache* c, const duo_paged* paged, const duo_kv8_cache* kv8,
+                                   const void* k_new, const void* v_new, int32_t T, void* stream) {
+  if (!paged) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
+  return append_kv8_impl(h, c, paged, kv8, nullptr, k_new, v_new, T, stream);
+}
+
+duo_status duo_kv_append_kv8_ragged(duo_handle* h, duo_kv_cache* c, const duo_paged* paged, const duo_kv8_cache* kv8,
+                                    const duo_slot_map* map, int32_t num_tokens, const void* k_new, const void* v_new,
+                                    void* stream) {
+  if (!paged) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
+  if (!map) return fail(DUO_ERR_INVALID_ARG, "map is NULL");
+  return append_kv8_impl(h, c, paged, kv8, map, k_new, v_new, num_tokens, stream);
+}
+
+// 2-D map over codes [rows, D]: boxes of 32 rows, the swizzle of the row's width.
+static duo_status encode_codes(const duo_handle* h, CUtensorMap* map, const void* base, int64_t rows, int D) {
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)(kKv8TK / 8)};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DUO_ERR_CUDA, "cuTensorMapEncodeTiled (codes) failed: %d", (int)r);
+  return DUO_OK;
+}
+
+static duo_status decode_kv8_impl(duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, const duo_kv8_cache* kv,
+                                  const int32_t* seq_lens, int64_t n, const void* q, void* o, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  duo_status st = check_handle(h);
+  if (st != DUO_OK) return st;
+  PagedLayout pg;
+  if ((st = check_kv8(h, c, pgd, kv, &pg)) != DUO_OK) return st;
+  if (!seq_lens) n = c->n;
+  if (n < 1)
+    return seq_lens ? fail(DUO_ERR_INVALID_ARG, "max_len = %lld < 1", (long long)n)
+                    : fail(DUO_ERR_INVALID_ARG, "decode needs the query token appended first (cache->n >= 1)");
+  if (n > 0x7fffffffLL) return fail(DUO_ERR_INVALID_ARG, "max_len reaches 2^31");
+  const Shape& sh = h->sh;
+  if (sh.n_ret > 0 && (st = check_capacity(h, pg, n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
+  if (reinterpret_cast<uintptr_t>(seq_lens) & 3u) return fail(DUO_ERR_INVALID_ARG, "seq_lens not 4-byte aligned");
+  if (!q || !o || !aligned16(q) || !aligned16(o))
+    return fail(DUO_ERR_INVALID_ARG, "q / o NULL or not 16-byte aligned");
+  const size_t need = decode_workspace_bytes(sh, h->num_sms);
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(DUO_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  if (!workspace || ws_bytes < need)
+    return fail(DUO_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
+  Kv8DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  if (sh.n_ret > 0) {
+    const int64_t rows = kv8_rows(h, pg);
+    if ((st = encode_codes(h, &p.tm_k, kv->k_codes, rows, sh.D)) != DUO_OK) return st;
+    if ((st = encode_codes(h, &p.tm_v, kv->v_codes, rows, sh.D)) != DUO_OK) return st;
+  }
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = static_cast<uint16_t*>(o);
+  p.k_scale = kv->k_scale;
+  p.v_scale = kv->v_scale;
+  p.k_tail = static_cast<const uint16_t*>(kv->k_tail);
+  p.v_tail = static_cast<const uint16_t*>(kv->v_tail);
+  p.k_sr = static_cast<const uint16_t*>(c->k_sr);
+  p.v_sr = static_cast<const uint16_t*>(c->v_sr);
+  p.pos = c->pos;
+  p.seq_lens = seq_lens;
+  p.n = n;
+  p.U_r = sh.B * sh.n_ret;
+  p.U_s = sh.B * sh.n_str;
+  p.code_type = kv->code_type;
+  p.cap64 = pitch64(sh.cap);
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)sh.D));
+  p.partials = static_cast<float*>(workspace);
+  p.sh = sh;
+  p.heads = h->heads;
+  p.pg = pg;
+  plan_decode_kv8(&p, h->num_sms);
+  cudaError_t ce = launch_decode_kv8(p, (cudaStream_t)stream);
+  if (ce != cudaSuccess) return cuda_fail(ce, "decode launch (8-bit)");
+  return ok();
+}
+
+duo_status duo_attn_decode_kv8(duo_handle* h, const duo_kv_cache* c, const duo_kv8_cache* kv8, const void* q, void* o,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_kv8_impl(h, c, nullptr, kv8, nullptr, 0, q, o, workspace, workspace_bytes, stream);
+}
+
+duo_status duo_attn_decode_kv8_paged(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged,
+                                     const duo_kv8_cache* kv8, const void* q, void* o, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!paged) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
+  return decode_kv8_impl(h, c, paged, kv8, nullptr, 0, q, o, workspace, workspace_bytes, stream);
+}
+
+duo_status duo_attn_decode_kv8_varlen(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged,
+                                      const duo_kv8_cache* kv8, const int32_t* seq_lens, int64_t max_len,
+                                      const void* q, void* o, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!seq_lens) return fail(DUO_ERR_INVALID_ARG, "seq_lens is NULL");
+  return decode_kv8_impl(h, c, paged, kv8, seq_lens, max_len, q, o, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------- block tables
+size_t duo_block_tables_workspace_size(int32_t batch) {
+  return batch < 1 ? 0 : (block_tables_scratch_bytes(batch) + 15) / 16 * 16;
+}
+
+duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* new_lens, int32_t max_tokens,
+                                   int32_t* seq_lens_out, int32_t* free_count_out, const duo_slot_map* map,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!pool || !map) return fail(DUO_ERR_INVALID_ARG, "pool / map is NULL");
+  const duo_block_pool& q = *pool;
+  if (q.batch < 1 || q.batch > 65535) return fail(DUO_ERR_INVALID_ARG, "batch = %d outside [1, 65535]", q.batch);
+  if (q.planes < 1 || q.planes > kMaxHeads)
+    return fail(DUO_ERR_INVALID_ARG, "planes = %d outside [1, %d]", q.planes, kMaxHeads);
+  if (q.block_size < 1 || q.max_blocks < 1) return fail(DUO_ERR_INVALID_ARG, "block_size / max_blocks < 1");
+  if (q.num_blocks < 1 || q.num_blocks > 0x7fffffffLL) return fail(DUO_ERR_INVALID_ARG, "num_blocks out of range");
+  if (max_tokens < 0) return fail(DUO_ERR_INVALID_ARG, "max_tokens = %d < 0", max_tokens);
+  if ((int64_t)q.block_size * q.max_blocks >= 0x7fffffffLL)
+    return fail(DUO_ERR_UNSUPPORTED, "block_size x max_blocks >= 2^31 - 1");
+  if ((int64_t)q.batch * q.planes * q.max_blocks > 0x7fffffffLL)
+    return fail(DUO_ERR_UNSUPPORTED, "batch x planes x max_blocks >= 2^31");
+  const void* a[] = {q.block_table, q.free_list, q.free_count, q.seq_lens, new_lens, seq_lens_out, free_count_out,
+                     map->cu_new};
+  for (const void* x : a)
+    if (!x || (reinterpret_cast<uintptr_t>(x) & 3u))
+      return fail(DUO_ERR_INVALID_ARG, "block tables: array NULL or not 4-byte aligned");
+  if (max_tokens > 0) {
+    if (!map->token_seq || !map->token_pos || !map->slots ||
+        ((reinterpret_cast<uintptr_t>(map->token_seq) | reinterpret_cast<uintptr_t>(map->token_pos)) & 3u) ||
+        (reinterpret_cast<uintptr_t>(map->slots) & 7u))
+      return fail(DUO_ERR_INVALID_ARG, "slot map: array NULL or misaligned");
+  }
+  if (workspace && !aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+  const size_t need = duo_block_tables_workspace_size(q.batch);
+  if (!workspace || workspace_bytes < need)
+    return fail(DUO_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  BlockTablesParams p;
+  p.table = q.block_table;
+  p.free_list = q.free_list;
+  p.free_count = q.free_count;
+  p.seq_lens = q.seq_lens;
+  p.new_lens = new_lens;
+  p.seq_lens_out = seq_lens_out;
+  p.free_count_out = free_count_out;
+  p.cu_new = map->cu_new;
+  p.token_seq = map->token_seq;
+  p.token_pos = map->token_pos;
+  p.slots = map->slots;
+  p.scratch = static_cast<int32_t*>(workspace);
+  p.B = q.batch;
+  p.planes = q.planes;
+  p.bs = q.block_size;
+  p.max_blocks = q.max_blocks;
+  p.max_tokens = max_tokens;
+  p.num_blocks = q.num_blocks;
+  e = launch_block_tables(p, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "block tables launch");
+  return ok();
+}
+
 duo_status duo_kv_append_varlen(duo_handle* h, duo_kv_cache* c, int32_t* seq_lens, const void* k_new,
                                 const void* v_new, void* stream) {
   duo_status st = check_handle(h);
@@ -811,15 +1075,25 @@ duo_status duo_device_error(uint32_t* code) {
   if (!code) return fail(DUO_ERR_INVALID_ARG, "code is NULL");
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  uint32_t a = 0, b = 0, t = 0, ap = 0;
+  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, bt = 0;
   if ((e = prefill_read_clear_error(&a)) != cudaSuccess) return cuda_fail(e, "read prefill error word");
   if ((e = decode_read_clear_error(&b)) != cudaSuccess) return cuda_fail(e, "read decode error word");
   if ((e = selftest_read_clear_error(&t)) != cudaSuccess) return cuda_fail(e, "read self-test error word");
   if ((e = append_read_clear_error(&ap)) != cudaSuccess) return cuda_fail(e, "read append error word");
-  *code = a | b | t | ap;
-  if ((*code & kErrBadBlock) && !(*code & ~(kErrBadBlock | kErrAppendCapacity)))
+  if ((e = decode_kv8_read_clear_error(&d8)) != cudaSuccess) return cuda_fail(e, "read 8-bit decode error word");
+  if ((e = append_kv8_read_clear_error(&a8)) != cudaSuccess) return cuda_fail(e, "read 8-bit append error word");
+  if ((e = block_tables_read_clear_error(&bt)) != cudaSuccess) return cuda_fail(e, "read block tables error word");
+  b |= d8;
+  ap |= a8;
+  *code = a | b | t | ap | bt;
+  constexpr uint32_t kFull = kErrAppendCapacity | kErrPoolFull, kBad = kErrBadBlock | kErrBadLength;
+  if ((*code & kErrBadLength) && !(*code & ~(kFull | kBad)))
+    return fail(DUO_ERR_INVALID_ARG, "block tables: a length or count is out of range (code 0x%x)", *code);
+  if ((*code & kErrBadBlock) && !(*code & ~(kFull | kBad)))
     return fail(DUO_ERR_INVALID_ARG, "a block table held an id outside [0, num_blocks) (code 0x%x)", *code);
-  if (ap && !(a | b | t))
+  if (bt && !(a | b | t | ap))
+    return fail(DUO_ERR_CAPACITY, "block tables: a sequence was turned down (code 0x%x)", *code);
+  if ((ap | bt) && !(a | b | t))
     return fail(DUO_ERR_CAPACITY, "a device-side append found a full retrieval cache (code 0x%x)", *code);
   if (*code) return fail(DUO_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (code 0x%x)", *code);
   return ok();

@@ -24,6 +24,8 @@ enum : uint32_t {
   kErrSelftest = 1u << 16,
   kErrAppendCapacity = 1u << 20,
   kErrBadBlock = 1u << 21,
+  kErrPoolFull = 1u << 22,   // block tables: a sequence was turned down
+  kErrBadLength = 1u << 23,  // block tables: a length or count that cannot be
 };
 
 struct Shape {
@@ -214,6 +216,95 @@ struct PrefillParams {
   int kv4;
 };
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);
+
+// ------------------------------------------------------------------ 8-bit caches
+constexpr int kKv8Block = 64;  // rows that share a scale
+constexpr int kKv8Int8 = 0, kKv8E4m3 = 1;
+
+struct Kv8AppendParams {
+  const uint16_t* k_new;  // bf16 [tokens, Hkv, D]; uniform: tokens = B x T
+  const uint16_t* v_new;
+  uint8_t* k_codes;  // [planes, cap64, D] or the pool [num_blocks, block_size, D]
+  uint8_t* v_codes;
+  float* k_scale;  // one per 64 rows of the codes
+  float* v_scale;
+  uint16_t* k_tail;  // bf16 [B, n_ret, 64, D]
+  uint16_t* v_tail;
+  uint16_t* k_sr;
+  uint16_t* v_sr;
+  int32_t* pos;
+  int64_t n;  // uniform: tokens before the call
+  int T;      // uniform: new tokens per sequence
+  int tokens;
+  int chunk;  // tokens per CTA and plane, a power of two up to 64
+  int code_type;
+  int64_t cap64;   // row pitch of a contiguous plane
+  int64_t rows;    // rows of the codes in all
+  Shape sh;
+  HeadTable heads;
+  PagedLayout pg;
+  // packed batches (token_seq != nullptr)
+  const int32_t* cu_new;
+  const int32_t* token_seq;
+  const int32_t* token_pos;
+  const int64_t* slots;
+};
+cudaError_t launch_append_kv8(const Kv8AppendParams& p, cudaStream_t stream);
+cudaError_t append_kv8_read_clear_error(uint32_t* code);
+
+constexpr int kKv8TK = 256;       // keys of a decode tile over codes (32 per warp)
+constexpr int kKv8TKBf16 = 128;   // keys of a tile over bf16 rows (ring or tail; 16 per warp)
+
+struct Kv8DecodeParams {
+  CUtensorMap tm_k;  // 2-D over the codes [rows, D], box 32 x D, swizzled by the row width
+  CUtensorMap tm_v;
+  const uint16_t* q;  // bf16 [B, Hq, D]
+  uint16_t* o;
+  const float* k_scale;
+  const float* v_scale;
+  const uint16_t* k_tail;
+  const uint16_t* v_tail;
+  const uint16_t* k_sr;
+  const uint16_t* v_sr;
+  const int32_t* pos;
+  const int32_t* seq_lens;  // or nullptr: every sequence holds n tokens
+  int64_t n;                // uniform length, or the planned maximum
+  int U_r, U_s;             // units (one per (sequence, KV head)) of each kind
+  int C;                    // CTAs
+  int whole;                // 1: CTA c takes unit c, no unit is split
+  int code_type;
+  int64_t cap64;
+  float scale_log2;  // log2(e) / sqrt(D)
+  float* partials;   // [U_r + U_s + C][g][D + 4]: first parts by unit, then one continuation per CTA
+  Shape sh;
+  HeadTable heads;
+  PagedLayout pg;
+};
+// Chooses C and whole from the other fields.
+void plan_decode_kv8(Kv8DecodeParams* p, int num_sms);
+cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, cudaStream_t stream);
+cudaError_t decode_kv8_read_clear_error(uint32_t* code);
+
+// ------------------------------------------------------------------ block tables
+struct BlockTablesParams {
+  int32_t* table;  // [B, planes, max_blocks]
+  int32_t* free_list;
+  const int32_t* free_count;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* seq_lens_out;
+  int32_t* free_count_out;
+  int32_t* cu_new;
+  int32_t* token_seq;
+  int32_t* token_pos;
+  int64_t* slots;
+  int32_t* scratch;
+  int B, planes, bs, max_blocks, max_tokens;
+  int64_t num_blocks;
+};
+size_t block_tables_scratch_bytes(int B);
+cudaError_t launch_block_tables(const BlockTablesParams& p, int num_sms, cudaStream_t stream);
+cudaError_t block_tables_read_clear_error(uint32_t* code);
 
 // Error words of the kernel translation units (synchronous read-and-clear).
 cudaError_t prefill_read_clear_error(uint32_t* code);
