@@ -411,6 +411,15 @@ duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* ca
                                       const duo_kv8_cache* kv8, const int32_t* seq_lens, int64_t max_len,
                                       const void* q, void* o, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Prefill of T new tokens against 8-bit caches, as duo_attn_prefill: cache rows are
+ * code * scale in fp32 rounded to bf16 (tail and ring rows are bf16 already), the T new
+ * tokens' k and v the bf16 inputs. Append the chunk afterwards. */
+duo_status duo_attn_prefill_kv8(duo_handle* handle, const duo_kv_cache* cache, const duo_kv8_cache* kv8,
+                                const void* q, const void* k, const void* v, int32_t T, void* o, void* stream);
+duo_status duo_attn_prefill_kv8_paged(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
+                                      const duo_kv8_cache* kv8, const void* q, const void* k, const void* v,
+                                      int32_t T, void* o, void* stream);
+
 /* Block tables kept on the device. A pool of num_blocks blocks of block_size tokens serves
  * B sequences with `planes` tables each (planes = n_ret: one per retrieval head).
  *   block_table int32 [B, planes, max_blocks]  entry j of a plane: the block of its tokens

@@ -398,8 +398,19 @@ class DuoKv8Layer(DuoLayer):
     def append_varlen(self, *args, **kwargs):
         raise NotImplementedError("8-bit caches: append_ragged (a paged layer) takes lengths from the device")
 
-    def prefill(self, *args, **kwargs):
-        raise NotImplementedError("prefill against 8-bit caches is not provided")
+    def prefill(self, q, k, v, out=None, kind_mask=3, stream=None):
+        """A chunk of T new tokens against the 8-bit caches (dequantized in the kernel)."""
+        if kind_mask != 3:
+            raise NotImplementedError("8-bit caches: prefill takes the heads of both kinds")
+        T = q.shape[1]
+        out = self._out(q, (self.B, T, self.Hq, self.D), out)
+        _on(self.device, "k", k, (self.B, T, self.Hkv, self.D))
+        _on(self.device, "v", v, (self.B, T, self.Hkv, self.D))
+        if self.paged is None:
+            _lib.duo_attn_prefill_kv8(self.handle, self.cache, self.kv8, q, k, v, T, out, stream)
+        else:
+            _lib.duo_attn_prefill_kv8_paged(self.handle, self.cache, self.paged, self.kv8, q, k, v, T, out, stream)
+        return out
 
     def dca_prefill(self, *args, **kwargs):
         raise NotImplementedError("Dual Chunk Attention over 8-bit caches is not provided")

@@ -38,7 +38,8 @@ EXPORTS = (
     "duo_paged_stream_dead_blocks", "duo_dca_prefill", "duo_dca_decode", "duo_kv_append_kv4",
     "duo_attn_decode_kv4", "duo_kv_append_kv4_paged", "duo_attn_decode_kv4_paged", "duo_attn_prefill_kv4",
     "duo_kv_append_kv8", "duo_kv_append_kv8_paged", "duo_kv_append_kv8_ragged", "duo_attn_decode_kv8",
-    "duo_attn_decode_kv8_paged", "duo_attn_decode_kv8_varlen", "duo_block_tables_workspace_size",
+    "duo_attn_decode_kv8_paged", "duo_attn_decode_kv8_varlen", "duo_attn_prefill_kv8",
+    "duo_attn_prefill_kv8_paged", "duo_block_tables_workspace_size",
     "duo_block_tables_update", "duo_kv_append_varlen", "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait",
     "duo_last_error", "duo_status_string",
 )
@@ -151,6 +152,11 @@ def library() -> ctypes.CDLL:
         "duo_attn_decode_kv8_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
                                                  POINTER(duo_kv8_cache), c_void_p, c_int64, c_void_p, c_void_p,
                                                  c_void_p, c_size_t, c_void_p]),
+        "duo_attn_prefill_kv8": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_kv8_cache), c_void_p,
+                                           c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
+        "duo_attn_prefill_kv8_paged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
+                                                 POINTER(duo_kv8_cache), c_void_p, c_void_p, c_void_p, c_int32,
+                                                 c_void_p, c_void_p]),
         "duo_block_tables_workspace_size": (c_size_t, [c_int32]),
         "duo_block_tables_update": (c_int32, [POINTER(duo_block_pool), c_void_p, c_int32, c_void_p, c_void_p,
                                               POINTER(duo_slot_map), c_void_p, c_size_t, c_void_p]),
@@ -357,6 +363,18 @@ def duo_attn_decode_kv8_varlen(handle, cache: "duo_kv_cache", paged, kv8: "duo_k
     _check(library().duo_attn_decode_kv8_varlen(handle, _ref(cache), _ref(paged), _ref(kv8), _ptr(seq_lens), max_len,
                                                 _ptr(q), _ptr(o), _ptr(workspace), _nbytes(workspace),
                                                 _stream_ptr(stream)))
+
+
+def duo_attn_prefill_kv8(handle, cache: "duo_kv_cache", kv8: "duo_kv8_cache", q, k, v, T: int, o,
+                         stream=None) -> None:
+    _check(library().duo_attn_prefill_kv8(handle, _ref(cache), _ref(kv8), _ptr(q), _ptr(k), _ptr(v), T, _ptr(o),
+                                          _stream_ptr(stream)))
+
+
+def duo_attn_prefill_kv8_paged(handle, cache: "duo_kv_cache", paged: "duo_paged", kv8: "duo_kv8_cache", q, k, v,
+                               T: int, o, stream=None) -> None:
+    _check(library().duo_attn_prefill_kv8_paged(handle, _ref(cache), _ref(paged), _ref(kv8), _ptr(q), _ptr(k), _ptr(v),
+                                                T, _ptr(o), _stream_ptr(stream)))
 
 
 def duo_block_tables_workspace_size(batch: int) -> int:

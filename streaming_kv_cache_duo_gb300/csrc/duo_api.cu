@@ -388,17 +388,48 @@ duo_status duo_kv_append_paged(duo_handle* h, duo_kv_cache* c, const duo_paged* 
   return append_impl(h, c, paged, k_new, v_new, T, stream);
 }
 
+// ---------------------------------------------------------------------- 8-bit caches
+static int64_t pitch64(int64_t rows) { return (rows + kKv8Block - 1) / kKv8Block * kKv8Block; }
+
+// Rows of the codes in all (a plane pitch of cap64, or the pool); -1 if a row index would pass 2^31.
+static int64_t kv8_rows(const duo_handle* h, const PagedLayout& pg) {
+  const int64_t rows = pg.table ? pg.num_blocks * pg.block_size : (int64_t)h->sh.B * h->sh.n_ret * pitch64(h->sh.cap);
+  return rows <= 0x7fffffffLL ? rows : -1;
+}
+
+static duo_status check_kv8(const duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, const duo_kv8_cache* kv,
+                            PagedLayout* pg) {
+  if (!c) return fail(DUO_ERR_INVALID_ARG, "cache is NULL");
+  if (!kv) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
+  if (kv->code_type != DUO_KV8_INT8 && kv->code_type != DUO_KV8_E4M3)
+    return fail(DUO_ERR_INVALID_ARG, "code_type = %d is neither DUO_KV8_INT8 nor DUO_KV8_E4M3", kv->code_type);
+  if (pgd && pgd->stream_table)
+    return fail(DUO_ERR_UNSUPPORTED, "8-bit caches keep streaming heads in their ring caches");
+  *pg = PagedLayout{nullptr, 0, 0, 0, nullptr};
+  duo_status st;
+  if (h->sh.n_ret > 0) {
+    if ((st = check_paged(h, pgd, pg)) != DUO_OK) return st;
+    const void* a[] = {kv->k_codes, kv->v_codes, kv->k_scale, kv->v_scale, kv->k_tail, kv->v_tail};
+    for (const void* x : a)
+      if (!x || !aligned16(x)) return fail(DUO_ERR_INVALID_ARG, "8-bit cache arrays NULL or not 16-byte aligned");
+    if (kv8_rows(h, *pg) < 0) return fail(DUO_ERR_UNSUPPORTED, "the codes have 2^31 rows or more");
+  }
+  return check_cache(h, c, false, true);
+}
+
 static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, const void* q,
                                const void* k, const void* v, int32_t T, void* o, int32_t kind_mask, void* stream,
-                               const duo_kv4_cache* kv4 = nullptr) {
+                               const duo_kv4_cache* kv4 = nullptr, const duo_kv8_cache* kv8 = nullptr) {
   duo_status st = check_handle(h);
   if (st != DUO_OK) return st;
   if (!c) return fail(DUO_ERR_INVALID_ARG, "cache is NULL");
   const Shape& sh = h->sh;
   const bool use_cache = c->n > 0;
   PagedLayout pg;
-  if ((st = check_paged(h, pgd, &pg)) != DUO_OK) return st;
-  if (kv4) {
+  if (!kv8 && (st = check_paged(h, pgd, &pg)) != DUO_OK) return st;
+  if (kv8) {
+    if ((st = check_kv8(h, c, pgd, kv8, &pg)) != DUO_OK) return st;
+  } else if (kv4) {
     if ((st = check_kv4(h, c, kv4)) != DUO_OK) return st;
   } else if ((st = check_cache(h, c, use_cache, use_cache && !pg.stream_table)) != DUO_OK) {
     return st;
@@ -430,6 +461,17 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
     p.cap16 = pitch16(sh.cap);
     p.sr16 = (int)pitch16(SR);
     p.kv4 = 1;
+  } else if (kv8) {  // likewise, but for the bf16 rings (below)
+    if (sh.n_ret > 0 && (st = check_capacity(h, pg, c->n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
+    p.k8 = static_cast<const uint8_t*>(kv8->k_codes);
+    p.v8 = static_cast<const uint8_t*>(kv8->v_codes);
+    p.k8_scale = kv8->k_scale;
+    p.v8_scale = kv8->v_scale;
+    p.k8_tail = static_cast<const uint16_t*>(kv8->k_tail);
+    p.v8_tail = static_cast<const uint16_t*>(kv8->v_tail);
+    p.cap64 = pitch64(sh.cap);
+    p.code_type = kv8->code_type;
+    p.kv8 = 1;
   } else if (use_cache && (sh.n_ret > 0 || pg.stream_table)) {
     if ((st = check_capacity(h, pg, c->n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
     if (!is_paged(pg)) {
@@ -747,35 +789,6 @@ duo_status duo_dca_decode(duo_handle* h, const duo_kv_cache* c, const void* q, c
   return decode_impl(h, c, nullptr, q, o, workspace, workspace_bytes, stream, &dca);
 }
 
-// ---------------------------------------------------------------------- 8-bit caches
-static int64_t pitch64(int64_t rows) { return (rows + kKv8Block - 1) / kKv8Block * kKv8Block; }
-
-// Rows of the codes in all (a plane pitch of cap64, or the pool); -1 if a row index would pass 2^31.
-static int64_t kv8_rows(const duo_handle* h, const PagedLayout& pg) {
-  const int64_t rows = pg.table ? pg.num_blocks * pg.block_size : (int64_t)h->sh.B * h->sh.n_ret * pitch64(h->sh.cap);
-  return rows <= 0x7fffffffLL ? rows : -1;
-}
-
-static duo_status check_kv8(const duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, const duo_kv8_cache* kv,
-                            PagedLayout* pg) {
-  if (!c) return fail(DUO_ERR_INVALID_ARG, "cache is NULL");
-  if (!kv) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
-  if (kv->code_type != DUO_KV8_INT8 && kv->code_type != DUO_KV8_E4M3)
-    return fail(DUO_ERR_INVALID_ARG, "code_type = %d is neither DUO_KV8_INT8 nor DUO_KV8_E4M3", kv->code_type);
-  if (pgd && pgd->stream_table)
-    return fail(DUO_ERR_UNSUPPORTED, "8-bit caches keep streaming heads in their ring caches");
-  *pg = PagedLayout{nullptr, 0, 0, 0, nullptr};
-  duo_status st;
-  if (h->sh.n_ret > 0) {
-    if ((st = check_paged(h, pgd, pg)) != DUO_OK) return st;
-    const void* a[] = {kv->k_codes, kv->v_codes, kv->k_scale, kv->v_scale, kv->k_tail, kv->v_tail};
-    for (const void* x : a)
-      if (!x || !aligned16(x)) return fail(DUO_ERR_INVALID_ARG, "8-bit cache arrays NULL or not 16-byte aligned");
-    if (kv8_rows(h, *pg) < 0) return fail(DUO_ERR_UNSUPPORTED, "the codes have 2^31 rows or more");
-  }
-  return check_cache(h, c, false, true);
-}
-
 static duo_status append_kv8_impl(duo_handle* h, duo_kv_cache* c, const duo_paged* pgd, const duo_kv8_cache* kv,
                                   const duo_slot_map* map, const void* k_new, const void* v_new, int32_t T,
                                   void* stream) {
@@ -859,6 +872,20 @@ duo_status duo_kv_append_kv8_ragged(duo_handle* h, duo_kv_cache* c, const duo_pa
   if (!paged) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
   if (!map) return fail(DUO_ERR_INVALID_ARG, "map is NULL");
   return append_kv8_impl(h, c, paged, kv8, map, k_new, v_new, num_tokens, stream);
+}
+
+duo_status duo_attn_prefill_kv8(duo_handle* h, const duo_kv_cache* c, const duo_kv8_cache* kv8, const void* q,
+                                const void* k, const void* v, int32_t T, void* o, void* stream) {
+  if (!kv8) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
+  return prefill_impl(h, c, nullptr, q, k, v, T, o, 3, stream, nullptr, kv8);
+}
+
+duo_status duo_attn_prefill_kv8_paged(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged,
+                                      const duo_kv8_cache* kv8, const void* q, const void* k, const void* v,
+                                      int32_t T, void* o, void* stream) {
+  if (!paged) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
+  if (!kv8) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
+  return prefill_impl(h, c, paged, q, k, v, T, o, 3, stream, nullptr, kv8);
 }
 
 // 2-D map over codes [rows, D]: boxes of 32 rows, the swizzle of the row's width.

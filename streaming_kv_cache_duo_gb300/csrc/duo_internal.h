@@ -214,6 +214,17 @@ struct PrefillParams {
   int64_t cap16;
   int sr16;
   int kv4;
+  // 8-bit caches (kv8 != 0): the retrieval heads' cache tiles are dequantized the same way,
+  // their last rows copied from the bf16 tail; laid out as in Kv8DecodeParams
+  const uint8_t* k8;
+  const uint8_t* v8;
+  const float* k8_scale;
+  const float* v8_scale;
+  const uint16_t* k8_tail;
+  const uint16_t* v8_tail;
+  int64_t cap64;
+  int kv8;
+  int code_type;
 };
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);
 

@@ -1,0 +1,159 @@
+"""Prefill of a chunk against 8-bit caches: every head of sampled rows against attention in 64 bits
+over the cache's rows (code * scale rounded to bf16, as documented; the open block's as they were)
+and the chunk's own keys, within the bound of kv8_util.attend."""
+
+import numpy as np
+import pytest
+import torch
+
+from kv8_util import BLOCK, Batch, attend, check, f64, scattered_table
+
+pytestmark = pytest.mark.gpu
+
+
+def _layer(c, cap, page=0, seed=1):
+    from streaming_kv_cache_duo_gb300 import DuoKv8Layer, DuoKv8PagedLayer
+    if page:
+        mb = -(-cap // page)
+        table, nb = scattered_table(np.random.default_rng(seed), c.B, len(c.ret), mb)
+        return DuoKv8PagedLayer(c.B, c.Hq, c.Hkv, c.D, c.S, c.R, page, mb, nb, table, c.kinds, code=c.code)
+    return DuoKv8Layer(c.B, c.Hq, c.Hkv, c.D, c.S, c.R, cap, c.kinds, code=c.code)
+
+
+def _bf16(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16).double().numpy()
+
+
+def _check_chunk(c, n, T, out, rows=None):
+    got = f64(out)
+    for b in range(c.B):
+        for h in range(c.Hkv):
+            keep = {}
+            for name, x in (("k", c.k), ("v", c.v)):
+                _, cached, full = c.heads_rows(b, h, n, x)
+                cached = np.concatenate([_bf16(np.float32(cached[:full])), cached[full:]]) if c.kinds[h] else cached
+                keep[name] = np.concatenate([cached, x[b, n:n + T, h]])
+            at = np.arange(n + T)
+            for t in rows if rows is not None else range(T):
+                i = n + t
+                see = at <= i
+                if not c.kinds[h]:
+                    see &= (at < c.S) | (i - at < c.R)
+                for j in range(h * c.g, (h + 1) * c.g):
+                    ref, tol = attend(c.q[b, i, j], keep["k"][see], keep["v"][see])
+                    check(got[b, t, j], ref, tol, f"sequence {b} row {t} head {j}")
+
+
+def _run(c, layer, n, T):
+    from streaming_kv_cache_duo_gb300 import duo_device_error
+    pick = lambda x: x[:, n:n + T].contiguous().cuda()
+    out = layer.prefill(pick(c.qt), pick(c.kt), pick(c.vt))
+    torch.cuda.synchronize()
+    assert duo_device_error() == 0
+    return out
+
+
+def _fill(c, layer, n):
+    if n:
+        layer.append(c.kt[:, :n].contiguous().cuda(), c.vt[:, :n].contiguous().cuda())
+        for name in ("k", "v"):  # nothing past the tokens may be used
+            getattr(layer, name + "_tail")[:, :, n % BLOCK:] = float("nan")
+            if layer.paged is None:
+                getattr(layer, name + "_scale")[:, :, n // BLOCK:] = float("nan")
+
+
+CASES = [
+    # B, Hq, Hkv, D, S, R, kinds, n, T, page
+    (1, 2, 2, 128, 4, 32, [1, 0], 0, 5, 0),
+    (1, 2, 2, 128, 4, 32, [1, 0], 1, 1, 0),
+    (2, 4, 2, 64, 4, 32, [1, 0], 63, 130, 0),
+    (1, 4, 1, 128, 4, 32, [1], 64, 3, 0),
+    (1, 4, 2, 128, 64, 256, [0, 1], 65, 300, 128),
+    (1, 8, 1, 64, 4, 32, [1], 191, 40, 256),
+    (2, 4, 2, 128, 0, 5, [1, 1], 128, 257, 0),
+    (1, 4, 2, 128, 3, 100, [1, 0], 1000, 70, 384),
+    (1, 2, 2, 64, 4, 32, [0, 0], 500, 33, 0),
+    (1, 2, 1, 128, 4, 32, [1], 2500, 9, 128),
+]
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("case", CASES, ids=[f"case{i}" for i in range(len(CASES))])
+def test_chunks_match(case, code):
+    B, Hq, Hkv, D, S, R, kinds, n, T, page = case
+    c = Batch(50, [n + T] * B, Hq, Hkv, D, S, R, kinds, code)
+    layer = _layer(c, n + T, page)
+    _fill(c, layer, n)
+    out = _run(c, layer, n, T)
+    _check_chunk(c, n, T, out, None if T <= 40 else sorted({0, 1, T // 2, T - 2, T - 1, min(T - 1, 127), min(T - 1, 128)}))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_a_chunked_prompt_then_decode(code):
+    """Chunks of odd sizes, each prefilled then appended, and a decode over what they leave."""
+    B, Hq, Hkv, D = 1, 8, 2, 128
+    chunks = [200, 1, 319, 64, 77]
+    c = Batch(51, [sum(chunks) + 1], Hq, Hkv, D, 4, 64, [1, 0], code)
+    layer = _layer(c, sum(chunks) + 1, 128)
+    n = 0
+    for T in chunks:
+        out = _run(c, layer, n, T)
+        _check_chunk(c, n, T, out, sorted({0, T // 3, T - 1}))
+        layer.append(c.kt[:, n:n + T].contiguous().cuda(), c.vt[:, n:n + T].contiguous().cuda())
+        n += T
+    layer.append(c.kt[:, n:].contiguous().cuda(), c.vt[:, n:].contiguous().cuda())
+    ref, tol = c.decode(0, n + 1)
+    check(f64(layer.decode(c.query([n + 1])))[0], ref, tol)
+
+
+def test_equals_the_bf16_prefill_over_the_dequantized_rows():
+    from streaming_kv_cache_duo_gb300 import DuoLayer
+    n, T = 777, 400
+    c = Batch(52, [n + T], 8, 2, 128, 64, 256, [1, 0], "int8")
+    layer = _layer(c, n + T)
+    _fill(c, layer, n)
+    plain = DuoLayer(1, 8, 2, 128, 64, 256, n + T, [1, 0])
+    kt, vt = c.kt.clone(), c.vt.clone()
+    for x, name in ((kt, "k"), (vt, "v")):
+        rows = c.heads_rows(0, 0, n, getattr(c, name))[1]
+        x[0, :n, 0] = torch.from_numpy(rows.astype(np.float32)).to(torch.bfloat16)
+    plain.append(kt[:, :n].contiguous().cuda(), vt[:, :n].contiguous().cuda())
+    pick = lambda x: x[:, n:n + T].contiguous().cuda()
+    want = plain.prefill(pick(c.qt), pick(c.kt), pick(c.vt))
+    assert torch.equal(_run(c, layer, n, T), want)
+
+
+def test_bad_pages_read_as_nothing_and_are_reported():
+    from streaming_kv_cache_duo_gb300 import duo_device_error
+    n, T = 400, 50
+    c = Batch(53, [n + T], 4, 2, 64, 4, 32, [1, 0], "e4m3")
+    layer = _layer(c, n + T, 128)
+    _fill(c, layer, n)
+    good = layer.block_table.clone()
+    pick = lambda x: x[:, n:n + T].contiguous().cuda()
+    for bad in (-1, layer.k_codes.shape[0], -(1 << 31)):
+        layer.block_table.copy_(good)
+        layer.block_table[0, 0, 1] = bad
+        out = layer.prefill(pick(c.qt), pick(c.kt), pick(c.vt))
+        torch.cuda.synchronize()
+        assert duo_device_error() != 0
+        assert torch.isfinite(out).all()
+
+
+def test_refusals():
+    from streaming_kv_cache_duo_gb300 import DuoError, _lib
+    c = Batch(54, [100], 4, 2, 64, 4, 32, [1, 0], "int8")
+    layer = _layer(c, 100)
+    q, k, v = (x[:, :10].contiguous().cuda() for x in (c.qt, c.kt, c.vt))
+    with pytest.raises(NotImplementedError):
+        layer.prefill(q, k, v, kind_mask=2)
+    for bad in ((q.float(), k, v), (q, k[:, :9].contiguous(), v), (q, k, v.cpu())):
+        with pytest.raises(ValueError):
+            layer.prefill(*bad)
+    call = lambda kv8, T=10, qq=q: _lib.duo_attn_prefill_kv8(layer.handle, layer.cache, kv8, qq, k, v, T, q)
+    for args in ((None,), (layer.kv8, 0), (layer.kv8, -1), (layer.kv8, 10, None)):
+        with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
+            call(*args)
+    layer.cache.n = 101
+    with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
+        call(layer.kv8)
