@@ -1,18 +1,19 @@
 // duo_attn_decode_kv8: one query token per sequence over 8-bit caches (codes with one scale
 // per 64 rows of a head, the open block in a bf16 tail) and the streaming heads' bf16 rings.
 //
-// A unit is one (sequence, KV head). Its keys are cut into tiles that take a CTA about the
-// same time: 256 keys of codes (64 KB at D = 128), or up to 128 bf16 rows of a ring or a
-// tail. All tiles of all units, laid end to end in unit order, are shared out evenly over
-// one CTA per SM: CTA c takes [c W / C, (c + 1) W / C). With lengths on the device every
-// CTA sums the units' tiles itself, so a batch of ragged lengths is as balanced as a
-// uniform one and nothing is planned on the host but the launch shape.
+// A unit is one (sequence, KV head). Its keys are cut into tiles of 64 KB (at D = 128): 256
+// keys of codes, or 128 bf16 rows of a ring or a tail. All tiles of all units, laid end to end
+// in unit order with one tile's worth of room before each unit for what a unit costs apart from
+// its keys (q, the merge of the warps), are shared out evenly over one CTA per SM: CTA c takes
+// those that start in [c W / C, (c + 1) W / C). With lengths on the device every CTA sums the
+// units' tiles itself, so a batch of ragged lengths is as balanced as a uniform one and
+// nothing is planned on the host but the launch shape.
 //
-// Codes: eight warps, each with its own 32 keys of a tile and its own ring of three stages
-// (K and V, 8 KB together at D = 128) filled by TMA through a swizzled map, so that both
-// fragment reads below are free of bank conflicts while the rows in HBM stay plain
-// row-major. The two scales of a slice come along by 4-byte asynchronous copies on the same
-// barrier. A warp refills its own stage; no warp waits for another.
+// Eight warps, each with its own slice of every tile (32 keys of codes or 16 bf16 rows) and
+// its own ring of three stages (K and V, 8 KB together at D = 128) that it refills itself; no
+// warp waits for another. Codes come by TMA through a swizzled map, so that both fragment
+// reads below are free of bank conflicts while the rows in HBM stay plain row-major, their two
+// scales by 4-byte asynchronous copies on the same barrier; bf16 rows by plain bulk copies.
 //
 // Per slice, on warp-level tensor-core products (a decode has one to eight query heads per
 // KV head: 8 columns, far too few rows to fill a 128-row tcgen05 tile, and the time is
@@ -26,8 +27,7 @@
 // as fp16 after a scaling by a power of two of its own (exact), p as fp16 with 7 bits of
 // headroom taken from above (p <= 2^15, flushed below 2^-31 of the maximum).
 //
-// bf16 rows (at most 63 of a tail, S + R of a ring): fragments straight from global memory,
-// 16 keys a warp, bf16 products. Only these need masks.
+// bf16 rows (at most 63 of a tail, S + R of a ring) take bf16 products. Only these need masks.
 //
 // Merge: as the bf16 decode. The warps of a CTA merge in shared memory; a unit split over
 // CTAs leaves (o, max, sum) parts for a second kernel, launched as a programmatic dependent.
@@ -180,49 +180,65 @@ __device__ __forceinline__ Unit unit_of(const Kv8DecodeParams& p, int u) {
   return x;
 }
 
-// This CTA's share of the tiles: [t0, t1) of W, shared by C CTAs, starting in unit u whose
-// first tile is ub.
+// Rows of a unit that are bf16: a streaming unit's ring slots, or the tail of the open block.
+__device__ __forceinline__ int bf16_rows(const Kv8DecodeParams& p, const Unit& x) {
+  const int SR = p.sh.S + p.sh.R;
+  return x.streaming ? (int)(x.n < SR ? x.n : SR) : (int)(x.n % kKv8Block);
+}
+
+// Places on the line of all tiles: a unit whose first tile is at ub takes tiles + 1 places, tile
+// lt >= 1 is at ub + lt + 1. Tiles of a unit of T tiles that lie before place ub + y:
+__device__ __forceinline__ int64_t tiles_before(int64_t y, int64_t T) {
+  const int64_t t = y > 1 ? y - 1 : y;
+  return t <= 0 ? 0 : (t < T ? t : T);
+}
+
+// This CTA's share of the line, places [x0, x1) of W, shared by C CTAs (each gets at least two
+// places, so none inside a unit's span is left without a tile of it), starting in unit u at ub.
 struct Share {
-  int64_t W, t0, t1, ub;
+  int64_t W, x0, x1, ub;
   int C, u;
 };
-__device__ __forceinline__ int cta_of(const Share& s, int64_t t) { return (int)(((t + 1) * s.C - 1) / s.W); }
+__device__ __forceinline__ int cta_of(const Share& s, int64_t x) { return (int)(((x + 1) * s.C - 1) / s.W); }
+__device__ __forceinline__ void cut(Share& s, int ctas) {
+  const int c = blockIdx.x;
+  s.C = (int)(ctas < s.W / 2 ? ctas : s.W / 2);
+  s.x0 = c < s.C ? c * s.W / s.C : s.W;
+  s.x1 = c < s.C ? (c + 1) * s.W / s.C : s.W;
+}
 
 __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   Share s;
-  const int c = blockIdx.x;
   const int SR = p.sh.S + p.sh.R;
   if (p.whole) {
-    s.W = s.t0 = s.t1 = s.ub = 0;
+    s.W = s.x0 = s.x1 = s.ub = 0;
     s.C = p.C;
-    s.u = c;
+    s.u = blockIdx.x;
     return s;
   }
   if (!p.seq_lens) {
-    const int64_t tr = tiles_ret(p.n), ts = tiles_str(p.n, SR), Wr = tr * p.U_r;
+    const int64_t tr = tiles_ret(p.n) + 1, ts = tiles_str(p.n, SR) + 1, Wr = tr * p.U_r;
     s.W = Wr + ts * p.U_s;
-    s.C = (int)(p.C < s.W ? p.C : s.W);
-    s.t0 = c < s.C ? c * s.W / s.C : s.W;
-    s.t1 = c < s.C ? (c + 1) * s.W / s.C : s.W;
-    if (s.t0 < Wr) {
-      s.u = (int)(s.t0 / tr);
+    cut(s, p.C);
+    if (s.x0 < Wr) {
+      s.u = (int)(s.x0 / tr);
       s.ub = s.u * tr;
     } else {
-      s.u = p.U_r + (int)((s.t0 - Wr) / ts);
+      s.u = p.U_r + (int)((s.x0 - Wr) / ts);
       s.ub = Wr + (s.u - p.U_r) * ts;
     }
     return s;
   }
-  // lengths on the device: thread t sums the tiles of sequences [t per, (t + 1) per), then
-  // the thread whose sums hold t0 finds the unit
+  // lengths on the device: thread t sums the places of sequences [t per, (t + 1) per), then
+  // the thread whose sums hold x0 finds the unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.sh.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.sh.B), b1 = min(b0 + per, p.sh.B);
   int64_t r = 0, q = 0;
   for (int b = b0; b < b1; ++b) {
     const int64_t n = seq_len(p, b);
-    r += p.sh.n_ret * tiles_ret(n);
-    q += p.sh.n_str * tiles_str(n, SR);
+    r += p.sh.n_ret * (tiles_ret(n) + 1);
+    q += p.sh.n_str * (tiles_str(n, SR) + 1);
   }
   const int64_t r_own = r, q_own = q;
 #pragma unroll
@@ -243,19 +259,17 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
     Wq += scratch[kWarps + w];
   }
   s.W = Wr + Wq;
-  s.C = (int)(p.C < s.W ? p.C : s.W);
-  s.t0 = c < s.C ? c * s.W / s.C : s.W;
-  s.t1 = c < s.C ? (c + 1) * s.W / s.C : s.W;
-  const bool in_r = s.t0 < Wr && s.t0 >= r - r_own && s.t0 < r;
-  const bool in_q = s.t0 >= Wr && s.t0 - Wr >= q - q_own && s.t0 - Wr < q;
+  cut(s, p.C);
+  const bool in_r = s.x0 < Wr && s.x0 >= r - r_own && s.x0 < r;
+  const bool in_q = s.x0 >= Wr && s.x0 - Wr >= q - q_own && s.x0 - Wr < q;
   if (in_r || in_q) {
     const int heads = in_r ? p.sh.n_ret : p.sh.n_str;
     int64_t base = in_r ? r - r_own : Wr + q - q_own;
     for (int b = b0; b < b1; ++b) {
       const int64_t n = seq_len(p, b);
-      const int64_t T = in_r ? tiles_ret(n) : tiles_str(n, SR);
-      if (s.t0 < base + heads * T) {
-        const int64_t k = (s.t0 - base) / T;
+      const int64_t T = (in_r ? tiles_ret(n) : tiles_str(n, SR)) + 1;
+      if (s.x0 < base + heads * T) {
+        const int64_t k = (s.x0 - base) / T;
         scratch[2 * kWarps] = (in_r ? 0 : p.U_r) + (int64_t)b * heads + k;
         scratch[2 * kWarps + 1] = base + k * T;
         break;
@@ -264,70 +278,75 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
     }
   }
   __syncthreads();
-  s.u = (int)scratch[2 * kWarps];
-  s.ub = scratch[2 * kWarps + 1];
+  // (a CTA without a share starts past the end)
+  s.u = s.x0 < s.x1 ? (int)scratch[2 * kWarps] : p.U_r + p.U_s;
+  s.ub = s.x0 < s.x1 ? scratch[2 * kWarps + 1] : s.W;
   return s;
 }
 
-// The slices of codes this warp takes, in order, over the CTA's share: one tile further each
-// time, across units.
+// The slices this warp takes, in order, over the CTA's share: one tile further each time, across
+// units.
 struct Cursor {
   Unit x;
-  int64_t ub, t, t1;
-  int row;    // first row of the slice in its unit
-  bool live;
-  int blk;    // paged: the id of the page the slice lies in
+  int64_t ub, x0, x1;
+  int64_t lt, lt1;  // next tile of the unit, and the end of the share's tiles in it
+  int row, rows;    // first row of the slice in its codes (32 rows), or in its bf16 rows (1 to 16)
+  bool live, codes;
+  int blk;  // paged codes: the id of the page the slice lies in
   int warp;
 
   __device__ __forceinline__ void init(const Kv8DecodeParams& p, const Share& s, int w) {
     warp = w;
-    live = true;
-    if (p.whole) {
-      x = unit_of(p, s.u);
-      ub = t = 0;
-      t1 = x.tiles;
-    } else {
-      t = s.t0;
-      t1 = s.t1;
-      ub = s.ub;
-      if (t >= t1) {
-        live = false;
-        return;
-      }
-      x = unit_of(p, s.u);
-    }
+    live = p.whole || s.x0 < s.x1;
+    if (!live) return;
+    x = unit_of(p, s.u);
+    x0 = s.x0;
+    x1 = s.x1;
+    ub = s.ub;
+    lt = p.whole ? 0 : tiles_before(x0 - ub, x.tiles);
+    lt1 = p.whole ? x.tiles : tiles_before(x1 - ub, x.tiles);
     settle(p);
   }
-  // from tile t on, the first with a slice for this warp
+  // from tile lt on, the first with a slice for this warp
   __device__ __forceinline__ void settle(const Kv8DecodeParams& p) {
     for (;;) {
-      if (t >= t1) {
+      if (lt < lt1) {
+        const int64_t tc = x.streaming ? 0 : tiles_codes(x.n);
+        if (lt < tc) {
+          const int64_t r = lt * kKv8TK + warp * kRows;
+          if (r < x.n / kKv8Block * kKv8Block) {
+            row = (int)r;
+            codes = true;
+            if (p.pg.table)
+              blk = __ldg(p.pg.table + ((int64_t)x.b * p.sh.n_ret + x.idx) * p.pg.max_blocks +
+                          (uint32_t)row / (uint32_t)p.pg.block_size);
+            return;
+          }
+          lt = tc;  // none in the last, partial tile of codes: on to the tail
+          continue;
+        }
+        const int r = (int)(lt - tc) * kKv8TKBf16 + warp * 16;
+        const int have = bf16_rows(p, x);
+        if (r < have) {
+          row = r;
+          rows = min(16, have - r);
+          codes = false;
+          return;
+        }
+      }
+      // nothing (more) for this warp in the unit
+      ub += x.tiles + 1;
+      if (p.whole || ub >= x1) {
         live = false;
         return;
       }
-      if (t >= ub + x.tiles) {
-        ub += x.tiles;
-        x = unit_of(p, x.u + 1);
-        continue;
-      }
-      if (x.streaming) {  // the streaming units come last
-        live = false;
-        return;
-      }
-      const int64_t r = (t - ub) * kKv8TK + warp * kRows;
-      if (r < x.n / kKv8Block * kKv8Block) {
-        row = (int)r;
-        if (p.pg.table)
-          blk = __ldg(p.pg.table + ((int64_t)x.b * p.sh.n_ret + x.idx) * p.pg.max_blocks +
-                      (uint32_t)row / (uint32_t)p.pg.block_size);
-        return;
-      }
-      // no slice in this tile: on to the next unit's
-      t = ub + x.tiles;
+      x = unit_of(p, x.u + 1);
+      lt = 0;
+      lt1 = tiles_before(x1 - ub, x.tiles);
     }
   }
   __device__ __forceinline__ void advance(const Kv8DecodeParams& p) {
-    ++t;
+    ++lt;
     settle(p);
   }
 };
@@ -337,6 +356,16 @@ template <int D, int G>
 __device__ __forceinline__ bool issue(const Kv8DecodeParams& p, const Cursor& cur, uint8_t* stage, float* scales,
                                       uint64_t* bar, uint64_t pol) {
   using C = Cfg<D, G>;
+  if (!cur.codes) {
+    const int64_t first = cur.x.streaming ? ((int64_t)cur.x.b * p.sh.n_str + cur.x.idx) * (p.sh.S + p.sh.R) + cur.row
+                                          : ((int64_t)cur.x.b * p.sh.n_ret + cur.x.idx) * kKv8Block + cur.row;
+    const uint32_t bytes = (uint32_t)cur.rows * D * 2;
+    mbar_arrive_expect_tx(bar, 2 * bytes);
+    bulk_g2s(stage, (cur.x.streaming ? p.k_sr : p.k_tail) + first * D, bytes, bar);
+    bulk_g2s(stage + C::SLICE, (cur.x.streaming ? p.v_sr : p.v_tail) + first * D, bytes, bar);
+    mbar_arrive(bar);
+    return true;
+  }
   int64_t row;
   if (p.pg.table) {
     if (cur.blk < 0 || cur.blk >= p.pg.num_blocks) {
@@ -485,36 +514,31 @@ struct State {
       for (int k = 0; k < 4; ++k) o[i][k] = fmaf(acc[i][k], vs, o[i][k]);
   }
 
-  // Up to 16 bf16 rows straight from global memory. rows: how many exist; vis: bit k set
-  // where value k's key is visible (keys gid and gid + 8, heads 2 tig and + 1).
-  __device__ __forceinline__ void rows16(const uint16_t* kr, const uint16_t* vr, int rows, uint32_t vis,
+  // A slice of up to 16 bf16 rows. vis: bit k set where value k's key is visible (keys gid and
+  // gid + 8, heads 2 tig and + 1); what lies in the other rows is not used.
+  __device__ __forceinline__ void rows16(const uint8_t* sk, const uint8_t* sv, uint32_t vis,
                                          const uint32_t (&qa)[D / 16][2], float qf, int gid, int tig) {
     float sc[2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k) sc[c][k] = 0.f;
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    uint4 ka[D / 32], kb[D / 32];
-    uint32_t w[4][MT];
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
-      ka[u] = gid < rows ? *reinterpret_cast<const uint4*>(kr + gid * D + (tig + 4 * u) * 8) : none;
-      kb[u] = gid + 8 < rows ? *reinterpret_cast<const uint4*>(kr + (gid + 8) * D + (tig + 4 * u) * 8) : none;
+      const uint4 ka = *reinterpret_cast<const uint4*>(sk + gid * D * 2 + (tig + 4 * u) * 16);
+      const uint4 kb = *reinterpret_cast<const uint4*>(sk + (gid + 8) * D * 2 + (tig + 4 * u) * 16);
+      mma<false>(sc[0], ka.x, kb.x, ka.y, kb.y, qa[2 * u][0], qa[2 * u][1]);
+      mma<false>(sc[1], ka.z, kb.z, ka.w, kb.w, qa[2 * u + 1][0], qa[2 * u + 1][1]);
     }
+    uint32_t w[4][MT];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = 2 * tig + (k & 1) + 8 * (k >> 1);
 #pragma unroll
       for (int c = 0; c < MT / 4; ++c) {
-        const uint4 v = row < rows ? *reinterpret_cast<const uint4*>(vr + row * D + DT * gid + 8 * c) : none;
+        const uint4 v = *reinterpret_cast<const uint4*>(sv + row * D * 2 + DT * 2 * gid + 16 * c);
         w[k][4 * c] = v.x, w[k][4 * c + 1] = v.y, w[k][4 * c + 2] = v.z, w[k][4 * c + 3] = v.w;
       }
-    }
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      mma<false>(sc[0], ka[u].x, kb[u].x, ka[u].y, kb[u].y, qa[2 * u][0], qa[2 * u][1]);
-      mma<false>(sc[1], ka[u].z, kb[u].z, ka[u].w, kb[u].w, qa[2 * u + 1][0], qa[2 * u + 1][1]);
     }
     float x[4];
 #pragma unroll
@@ -646,43 +670,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   const int SR = p.sh.S + p.sh.R;
   bool ok = true;  // of this warp: a wait that ran out stops its copies, not the CTA's barriers
   State<D, G> st;
-  uint32_t qb[D / 16][2];
-  int64_t t = sh.t0, t1 = sh.t1, ub = sh.ub;
-  int u = sh.u;
-  for (bool first = true;; first = false) {
-    if (!first) {
-      if (p.whole || t >= t1) break;
-      ++u;
-    } else if (!p.whole && t >= t1) {
-      break;
-    }
+  int64_t ub = sh.ub;
+  // next slice: refills the stage of the one before, and waits for its own
+  auto next = [&]() {
+    if (cur.live && ok) refill();
+    const int s = (int)(used % kStages);
+    if (ok) ok = mbar_wait(&bars[s], (used / kStages) & 1u, err, kErrDecodeConsumer);
+    if (ok) ++landed;
+    ++used;
+    return s;
+  };
+  for (int u = sh.u; p.whole ? u == sh.u : ub < sh.x1; ++u) {
     const Unit x = unit_of(p, u);
-    if (p.whole) {
-      ub = t = 0;
-      t1 = x.tiles;
+    const int64_t lt0 = p.whole ? 0 : tiles_before(sh.x0 - ub, x.tiles);
+    const int64_t lt1 = p.whole ? x.tiles : tiles_before(sh.x1 - ub, x.tiles);
+    if (lt0 >= lt1) {  // (the share starts behind its last tile)
+      ub += x.tiles + 1;
+      continue;
     }
-    const int64_t lt0 = t - ub;
-    const int64_t lt1 = (t1 < ub + x.tiles ? t1 : ub + x.tiles) - ub;
     st.reset();
     const uint16_t* qh = gid < G ? p.q + ((int64_t)x.b * p.sh.Hq + (int64_t)x.kvh * G + gid) * D : nullptr;
     const int64_t tc = x.streaming ? 0 : tiles_codes(x.n);
     if (lt0 < tc) {
+      uint32_t qb[D / 16][2];
       const float f = load_q16<D>(qh, qb, tig) * p.scale_log2;
       const float f0 = __shfl_sync(0xffffffffu, f, 8 * tig), f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
       const int64_t full = x.n / kKv8Block * kKv8Block;
       for (int64_t lt = lt0; lt < lt1 && lt < tc; ++lt) {
         if (lt * kKv8TK + warp * kRows >= full) break;
-        if (cur.live && ok) refill();
-        const int s = (int)(used % kStages);
-        if (ok) ok = mbar_wait(&bars[s], (used / kStages) & 1u, err, kErrDecodeConsumer);
-        if (ok) ++landed;
+        const int s = next();
         const bool skip = !ok || ((__shfl_sync(0xffffffffu, bad, 0) >> s) & 1u);
         if (!skip) {
           const uint8_t* sk = ring + s * C::STAGE;
           const float ks = scales[2 * s], vs = scales[2 * s + 1];
           st.template codes<CODE>(sk, sk + C::SLICE, qb, f0 * ks, f1 * ks, vs, gid, tig);
         }
-        ++used;
         __syncwarp();
       }
     }
@@ -690,27 +712,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     if (tb < lt1) {
       uint32_t qa[D / 16][2];
       load_qbf16<D>(qh, qa, tig);
-      const int64_t plane = x.streaming ? (int64_t)x.b * p.sh.n_str + x.idx : (int64_t)x.b * p.sh.n_ret + x.idx;
-      const int pitch = x.streaming ? SR : kKv8Block;
-      const int have = x.streaming ? (int)(x.n < SR ? x.n : SR) : (int)(x.n % kKv8Block);
-      const uint16_t* kr = (x.streaming ? p.k_sr : p.k_tail) + plane * pitch * D;
-      const uint16_t* vr = (x.streaming ? p.v_sr : p.v_tail) + plane * pitch * D;
+      const int have = bf16_rows(p, x);
       for (int64_t lt = tb; lt < lt1; ++lt) {
         const int r0 = (int)(lt - tc) * kKv8TKBf16 + warp * 16;
-        const int rows = have - r0 < 16 ? have - r0 : 16;
-        if (rows <= 0) break;
-        uint32_t vis = 0;
+        if (r0 >= have) break;
+        int64_t at[2];  // positions of keys gid and gid + 8
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int key = gid + 8 * k;
-          bool v = key < rows;
-          if (v && x.streaming) {
-            const int64_t jp = __ldg(p.pos + (int64_t)x.b * SR + r0 + key);
-            v = jp >= 0 && jp < x.n && (jp < p.sh.S || x.n - 1 - jp < p.sh.R);
-          }
+          at[k] = r0 + key >= have ? -1 : (x.streaming ? __ldg(p.pos + (int64_t)x.b * SR + r0 + key) : 0);
+        }
+        const int s = next();
+        uint32_t vis = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool v = at[k] >= 0 && (!x.streaming || (at[k] < x.n && (at[k] < p.sh.S || x.n - 1 - at[k] < p.sh.R)));
           vis |= (v ? 3u : 0u) << (2 * k);
         }
-        st.rows16(kr + (int64_t)r0 * D, vr + (int64_t)r0 * D, rows, vis, qa, p.scale_log2, gid, tig);
+        const uint8_t* sk = ring + s * C::STAGE;
+        if (ok) st.rows16(sk, sk + C::SLICE, vis, qa, p.scale_log2, gid, tig);
+        __syncwarp();
       }
     }
 
@@ -720,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     int c_first = 0, n_parts = 1;
     if (!p.whole) {
       c_first = cta_of(sh, ub);
-      n_parts = cta_of(sh, ub + x.tiles - 1) - c_first + 1;
+      n_parts = cta_of(sh, x.tiles > 1 ? ub + x.tiles : ub) - c_first + 1;
     }
     float* part = p.partials + (int64_t)(lt0 == 0 ? u : U + (int)blockIdx.x) * G * C::PS;
     for (int e = tid; e < G * D; e += kThreads) {
@@ -748,8 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
       }
     }
     __syncthreads();  // the buffer is the next unit's
-    t = ub + lt1;
-    ub += x.tiles;
+    ub += x.tiles + 1;
   }
   // copies still in flight (after a wait that ran out) land before the CTA ends
   if (lane == 0)
@@ -862,7 +882,7 @@ void plan_decode_kv8(Kv8DecodeParams* p, int num_sms) {
   const int64_t tr = p->U_r ? tiles_ret(p->n) : 0, ts = p->U_s ? tiles_str(p->n, SR) : 0;
   const int64_t U = (int64_t)p->U_r + p->U_s;
   p->whole = U <= num_sms && tr <= kShortTiles && ts <= kShortTiles;
-  const int64_t W = tr * p->U_r + ts * p->U_s;
+  const int64_t W = tr * p->U_r + ts * p->U_s;  // (a CTA's share is at least one tile)
   p->C = (int)(p->whole ? U : (W < num_sms ? W : num_sms));
 }
 
