@@ -44,10 +44,10 @@ namespace {
 
 __device__ unsigned int g_decode_kv8_err;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = kKv8Warps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kKv8TK / kWarps;  // keys of a slice: 32
-constexpr int kStages = 3;
+constexpr int kRows = kKv8Rows;  // keys of a slice of codes
+constexpr int kStages = kKv8Stages;
 // units of at most this many tiles are not split (their merge would cost more)
 constexpr int kShortTiles = 4;
 // p is kept times 2^kPShift: fp16 then holds it down to 2^-(24 + kPShift) of the row maximum,
@@ -59,11 +59,12 @@ struct Cfg {
   static constexpr int SLICE = kRows * D;  // bytes of a warp's K (or V) codes
   static constexpr int STAGE = 2 * SLICE;
   static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int RED = kWarps * G * (D + 2);
+  static constexpr int HR = G < 4 ? G : 4;  // heads merged at a time
+  static constexpr int RED = kWarps * HR * (D + 2);
   static constexpr int PS = D + 4;  // floats per head of a part
   static constexpr int OFF_RED = RING;
   static constexpr int OFF_BAR = OFF_RED + RED * 4;
-  static constexpr int OFF_SCALE = OFF_BAR + kWarps * kStages * 8;
+  static constexpr int OFF_SCALE = OFF_BAR + kWarps * kStages * 16;
   static constexpr size_t SMEM = (size_t)OFF_SCALE + kWarps * kStages * 8 + 1024;  // + alignment
 };
 
@@ -79,6 +80,9 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
 // 4 bytes to shared memory, counted by the barrier's arrival below
 __device__ __forceinline__ void copy4_async(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 // one (already expected) arrival once this thread's earlier cp.async copies have landed
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
@@ -98,6 +102,30 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four 8x8 matrices of 16-bit values (rows of 16 bytes, lane l naming row l % 8 of matrix l / 8):
+// lane (gid, tig) gets the four bytes at 4 tig of row gid of each. Transposed: the values of
+// rows 2 tig and 2 tig + 1 in column gid.
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared::cta.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4_trans(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// Two 16x16 matrices of bytes, transposed (lane l names row l % 16 of matrix l / 16): of each, the
+// bytes of rows 4 tig ... 4 tig + 3 in column gid, and in column gid + 8.
+__device__ __forceinline__ void ldm2_trans8(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared::cta.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
 // 8x8 transpose of 16-bit values in fragment layout
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t m) {
   uint32_t d;
@@ -110,21 +138,29 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The codes in bytes 0, 1 and 2, 3 of w as two fp16 pairs, exactly.
+// Four codes as two fp16 pairs, exactly. Which bytes make a pair is up to the code: e4m3's
+// conversion takes neighbours (0, 1) and (2, 3); int8 takes (0, 2) and (1, 3), each pair one
+// masked xor (a byte with its sign bit flipped under the exponent of 1024 reads as 1152 + code)
+// after a shift for the second. byte_of: the byte in place i of pair j.
 template <int CODE>
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__host__ __device__ constexpr int byte_of(int j, int i) {
+  return CODE == kKv8E4m3 ? 2 * j + i : j + 2 * i;
+}
+template <int CODE>
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t& p0, uint32_t& p1) {
   if constexpr (CODE == kKv8E4m3) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
+        : "=r"(p0), "=r"(p1)
         : "r"(w));
   } else {
-    const uint32_t u = w ^ 0x80808080u;  // code + 128
     const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));  // 1152
-    const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+    uint32_t l, h;
+    asm("lop3.b32 %0, %1, 0x00FF00FF, 0x64806480, 0x6A;" : "=r"(l) : "r"(w));  // (w & mask) ^ magic
+    asm("lop3.b32 %0, %1, 0x00FF00FF, 0x64806480, 0x6A;" : "=r"(h) : "r"(w >> 8));
     const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
     const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
-    lo = *reinterpret_cast<const uint32_t*>(&a);
-    hi = *reinterpret_cast<const uint32_t*>(&b);
+    p0 = *reinterpret_cast<const uint32_t*>(&a);
+    p1 = *reinterpret_cast<const uint32_t*>(&b);
   }
 }
 
@@ -135,62 +171,76 @@ __device__ __forceinline__ int chunk_at(int row, int c) {
   return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ int64_t seq_len(const Kv8DecodeParams& p, int b) {
-  if (!p.seq_lens) return p.n;
-  const int64_t v = __ldg(p.seq_lens + b);
-  return v < 0 ? 0 : (v > p.n ? p.n : v);
+// The same for a bf16 slice, as its copies place it (rows of 2 D bytes).
+template <int D>
+__device__ __forceinline__ int chunk16_at(int row, int c) {
+  return row * D * 2 + ((c ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ int seq_len(const Kv8DecodeParams& p, int b) {
+  if (!p.seq_lens) return (int)p.n;
+  const int v = __ldg(p.seq_lens + b);
+  return v < 0 ? 0 : (v > p.n ? (int)p.n : v);
 }
 
 // Tiles of a retrieval / streaming unit of a sequence of n tokens (at least one, so that
 // every unit's output is written).
-__host__ __device__ __forceinline__ int64_t tiles_codes(int64_t n) { return (n / kKv8Block + 3) / 4; }
-__host__ __device__ __forceinline__ int64_t tiles_ret(int64_t n) {
-  const int64_t t = tiles_codes(n) + (n % kKv8Block > 0);
+__host__ __device__ __forceinline__ int code_rows_of(int n) { return n & ~(kKv8Block - 1); }
+__host__ __device__ __forceinline__ int tiles_codes(int n) {
+  return (int)(((uint32_t)code_rows_of(n) + kKv8TK - 1) / kKv8TK);
+}
+__host__ __device__ __forceinline__ int tiles_ret(int n) {
+  const int t = tiles_codes(n) + ((n & (kKv8Block - 1)) > 0);
   return t > 0 ? t : 1;
 }
-__host__ __device__ __forceinline__ int64_t tiles_str(int64_t n, int SR) {
-  const int64_t rows = n < SR ? n : SR;
-  return rows > 0 ? (rows + kKv8TKBf16 - 1) / kKv8TKBf16 : 1;
+__host__ __device__ __forceinline__ int tiles_str(int n, int SR) {
+  const int rows = n < SR ? n : SR;
+  return rows > 0 ? (int)(((uint32_t)rows + kKv8TKBf16 - 1) / kKv8TKBf16) : 1;
 }
 
 struct Unit {
-  int u, b, kvh, idx;  // idx: its index among the heads of its kind
+  int u, b, idx;  // idx: its index among the heads of its kind
+  int n;          // tokens of the sequence
+  int tiles, tc;  // tiles, and those of codes among them
   bool streaming;
-  int64_t n;      // tokens of the sequence
-  int64_t tiles;
 };
 __device__ __forceinline__ Unit unit_of(const Kv8DecodeParams& p, int u) {
   Unit x;
   x.u = u;
   x.streaming = u >= p.U_r;
-  if (!x.streaming) {
-    x.b = u / p.sh.n_ret;
-    x.idx = u - x.b * p.sh.n_ret;
-    x.kvh = p.heads.ret_head[x.idx];
-    x.n = seq_len(p, x.b);
-    x.tiles = tiles_ret(x.n);
-  } else {
-    const int us = u - p.U_r;
-    x.b = us / p.sh.n_str;
-    x.idx = us - x.b * p.sh.n_str;
-    x.kvh = p.heads.str_head[x.idx];
-    x.n = seq_len(p, x.b);
-    x.tiles = tiles_str(x.n, p.sh.S + p.sh.R);
-  }
+  const uint32_t k = x.streaming ? u - p.U_r : u, heads = x.streaming ? p.sh.n_str : p.sh.n_ret;
+  x.b = (int)(k / heads);
+  x.idx = (int)(k - x.b * heads);
+  x.n = seq_len(p, x.b);
+  x.tiles = x.streaming ? tiles_str(x.n, p.sh.S + p.sh.R) : tiles_ret(x.n);
+  x.tc = x.streaming ? 0 : tiles_codes(x.n);
   return x;
 }
-
+// Its query heads' first row in q and o.
+template <int G>
+__device__ __forceinline__ int64_t head_row(const Kv8DecodeParams& p, const Unit& x) {
+  const int kvh = x.streaming ? p.heads.str_head[x.idx] : p.heads.ret_head[x.idx];
+  return (int64_t)x.b * p.sh.Hq + kvh * G;
+}
 // Rows of a unit that are bf16: a streaming unit's ring slots, or the tail of the open block.
 __device__ __forceinline__ int bf16_rows(const Kv8DecodeParams& p, const Unit& x) {
   const int SR = p.sh.S + p.sh.R;
-  return x.streaming ? (int)(x.n < SR ? x.n : SR) : (int)(x.n % kKv8Block);
+  return x.streaming ? (x.n < SR ? x.n : SR) : x.n & (kKv8Block - 1);
 }
 
 // Places on the line of all tiles: a unit whose first tile is at ub takes tiles + 1 places, tile
 // lt >= 1 is at ub + lt + 1. Tiles of a unit of T tiles that lie before place ub + y:
-__device__ __forceinline__ int64_t tiles_before(int64_t y, int64_t T) {
+__device__ __forceinline__ int tiles_before(int64_t y, int T) {
   const int64_t t = y > 1 ? y - 1 : y;
-  return t <= 0 ? 0 : (t < T ? t : T);
+  return t <= 0 ? 0 : (t < T ? (int)t : T);
+}
+
+// a b / c for a, b, c >= 0; in 32 bits where it fits (64-bit divisions on a CTA's way in and
+// out cost a microsecond).
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  const int64_t ab = a * b;
+  if (((ab | c) >> 32) == 0) return (int64_t)((uint32_t)ab / (uint32_t)c);
+  return ab / c;
 }
 
 // This CTA's share of the line, places [x0, x1) of W, shared by C CTAs (each gets at least two
@@ -199,17 +249,19 @@ struct Share {
   int64_t W, x0, x1, ub;
   int C, u;
 };
-__device__ __forceinline__ int cta_of(const Share& s, int64_t x) { return (int)(((x + 1) * s.C - 1) / s.W); }
+__device__ __forceinline__ int cta_of(const Share& s, int64_t x) {
+  const int64_t a = (x + 1) * s.C - 1;
+  return (int)mul_div(a, 1, s.W);
+}
 __device__ __forceinline__ void cut(Share& s, int ctas) {
   const int c = blockIdx.x;
   s.C = (int)(ctas < s.W / 2 ? ctas : s.W / 2);
-  s.x0 = c < s.C ? c * s.W / s.C : s.W;
-  s.x1 = c < s.C ? (c + 1) * s.W / s.C : s.W;
+  s.x0 = c < s.C ? mul_div(c, s.W, s.C) : s.W;
+  s.x1 = c < s.C ? mul_div(c + 1, s.W, s.C) : s.W;
 }
 
 __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   Share s;
-  const int SR = p.sh.S + p.sh.R;
   if (p.whole) {
     s.W = s.x0 = s.x1 = s.ub = 0;
     s.C = p.C;
@@ -217,18 +269,17 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
     return s;
   }
   if (!p.seq_lens) {
-    const int64_t tr = tiles_ret(p.n) + 1, ts = tiles_str(p.n, SR) + 1, Wr = tr * p.U_r;
-    s.W = Wr + ts * p.U_s;
+    s.W = p.line_r + p.line_s;
     cut(s, p.C);
-    if (s.x0 < Wr) {
-      s.u = (int)(s.x0 / tr);
-      s.ub = s.u * tr;
-    } else {
-      s.u = p.U_r + (int)((s.x0 - Wr) / ts);
-      s.ub = Wr + (s.u - p.U_r) * ts;
-    }
+    const bool in_r = s.x0 < p.line_r;
+    const int64_t at = in_r ? s.x0 : s.x0 - p.line_r;
+    const int64_t per = (in_r ? p.tiles_r : p.tiles_s) + 1;
+    const int64_t k = mul_div(at, 1, per);
+    s.u = (int)k + (in_r ? 0 : p.U_r);
+    s.ub = s.x0 - at + k * per;
     return s;
   }
+  const int SR = p.sh.S + p.sh.R;
   // lengths on the device: thread t sums the places of sequences [t per, (t + 1) per), then
   // the thread whose sums hold x0 finds the unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -236,9 +287,9 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   const int b0 = min(tid * per, p.sh.B), b1 = min(b0 + per, p.sh.B);
   int64_t r = 0, q = 0;
   for (int b = b0; b < b1; ++b) {
-    const int64_t n = seq_len(p, b);
-    r += p.sh.n_ret * (tiles_ret(n) + 1);
-    q += p.sh.n_str * (tiles_str(n, SR) + 1);
+    const int n = seq_len(p, b);
+    r += (int64_t)p.sh.n_ret * (tiles_ret(n) + 1);
+    q += (int64_t)p.sh.n_str * (tiles_str(n, SR) + 1);
   }
   const int64_t r_own = r, q_own = q;
 #pragma unroll
@@ -266,10 +317,10 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
     const int heads = in_r ? p.sh.n_ret : p.sh.n_str;
     int64_t base = in_r ? r - r_own : Wr + q - q_own;
     for (int b = b0; b < b1; ++b) {
-      const int64_t n = seq_len(p, b);
+      const int n = seq_len(p, b);
       const int64_t T = (in_r ? tiles_ret(n) : tiles_str(n, SR)) + 1;
       if (s.x0 < base + heads * T) {
-        const int64_t k = (s.x0 - base) / T;
+        const int64_t k = mul_div(s.x0 - base, 1, T);
         scratch[2 * kWarps] = (in_r ? 0 : p.U_r) + (int64_t)b * heads + k;
         scratch[2 * kWarps + 1] = base + k * T;
         break;
@@ -289,11 +340,13 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
 struct Cursor {
   Unit x;
   int64_t ub, x0, x1;
-  int64_t lt, lt1;  // next tile of the unit, and the end of the share's tiles in it
+  int lt, lt1;      // next tile of the unit, and the end of the share's tiles in it
   int row, rows;    // first row of the slice in its codes (32 rows), or in its bf16 rows (1 to 16)
-  bool live, codes;
-  int blk;  // paged codes: the id of the page the slice lies in
+  int code_rows;    // rows of codes of the unit
+  const int32_t* pages;  // paged codes: the unit's row of the block table,
+  int blk;               // and the id of the page the slice lies in
   int warp;
+  bool live, codes;
 
   __device__ __forceinline__ void init(const Kv8DecodeParams& p, const Share& s, int w) {
     warp = w;
@@ -310,26 +363,26 @@ struct Cursor {
   // from tile lt on, the first with a slice for this warp
   __device__ __forceinline__ void settle(const Kv8DecodeParams& p) {
     for (;;) {
-      if (lt < lt1) {
-        const int64_t tc = x.streaming ? 0 : tiles_codes(x.n);
-        if (lt < tc) {
-          const int64_t r = lt * kKv8TK + warp * kRows;
-          if (r < x.n / kKv8Block * kKv8Block) {
-            row = (int)r;
-            codes = true;
-            if (p.pg.table)
-              blk = __ldg(p.pg.table + ((int64_t)x.b * p.sh.n_ret + x.idx) * p.pg.max_blocks +
-                          (uint32_t)row / (uint32_t)p.pg.block_size);
-            return;
+      if (lt < x.tc && lt < lt1) {
+        code_rows = code_rows_of(x.n);
+        const int64_t r = (int64_t)lt * kKv8TK + warp * kRows;
+        if (r < code_rows) {
+          row = (int)r;
+          codes = true;
+          if (p.pg.table) {
+            pages = p.pg.table + ((int64_t)x.b * p.sh.n_ret + x.idx) * p.pg.max_blocks;
+            blk = __ldg(pages + (uint32_t)row / (uint32_t)p.pg.block_size);
           }
-          lt = tc;  // none in the last, partial tile of codes: on to the tail
-          continue;
+          return;
         }
-        const int r = (int)(lt - tc) * kKv8TKBf16 + warp * 16;
+        lt = x.tc;  // none in the last, partial tile of codes: on to the tail
+      }
+      if (lt < lt1) {
+        const int64_t r = (int64_t)(lt - x.tc) * kKv8TKBf16 + warp * 16;
         const int have = bf16_rows(p, x);
         if (r < have) {
-          row = r;
-          rows = min(16, have - r);
+          row = (int)r;
+          rows = min(16, have - row);
           codes = false;
           return;
         }
@@ -347,25 +400,20 @@ struct Cursor {
   }
   __device__ __forceinline__ void advance(const Kv8DecodeParams& p) {
     ++lt;
+    if (codes && lt < lt1 && (int64_t)row + kKv8TK < code_rows) {  // (the most frequent case, kept short)
+      row += kKv8TK;
+      if (p.pg.table) blk = __ldg(pages + (uint32_t)row / (uint32_t)p.pg.block_size);
+      return;
+    }
     settle(p);
   }
 };
 
-// Copies the cursor's slice into a stage (lane 0). False: its page does not exist.
+// Copies the cursor's slice of codes into a stage (lane 0). False: its page does not exist.
 template <int D, int G>
-__device__ __forceinline__ bool issue(const Kv8DecodeParams& p, const Cursor& cur, uint8_t* stage, float* scales,
-                                      uint64_t* bar, uint64_t pol) {
+__device__ __forceinline__ bool issue_codes(const Kv8DecodeParams& p, const Cursor& cur, uint8_t* stage, float* scales,
+                                            uint64_t* bar, uint64_t pol) {
   using C = Cfg<D, G>;
-  if (!cur.codes) {
-    const int64_t first = cur.x.streaming ? ((int64_t)cur.x.b * p.sh.n_str + cur.x.idx) * (p.sh.S + p.sh.R) + cur.row
-                                          : ((int64_t)cur.x.b * p.sh.n_ret + cur.x.idx) * kKv8Block + cur.row;
-    const uint32_t bytes = (uint32_t)cur.rows * D * 2;
-    mbar_arrive_expect_tx(bar, 2 * bytes);
-    bulk_g2s(stage, (cur.x.streaming ? p.k_sr : p.k_tail) + first * D, bytes, bar);
-    bulk_g2s(stage + C::SLICE, (cur.x.streaming ? p.v_sr : p.v_tail) + first * D, bytes, bar);
-    mbar_arrive(bar);
-    return true;
-  }
   int64_t row;
   if (p.pg.table) {
     if (cur.blk < 0 || cur.blk >= p.pg.num_blocks) {
@@ -387,13 +435,32 @@ __device__ __forceinline__ bool issue(const Kv8DecodeParams& p, const Cursor& cu
   return true;
 }
 
+// Copies the cursor's bf16 rows into a stage (every lane; every lane arrives).
+template <int D, int G>
+__device__ __forceinline__ void issue_rows(const Kv8DecodeParams& p, const Cursor& cur, uint8_t* stage, uint64_t* bar,
+                                           int lane) {
+  constexpr int CPR = D / 8;  // 16-byte chunks per row
+  const int64_t first = cur.x.streaming ? ((int64_t)cur.x.b * p.sh.n_str + cur.x.idx) * (p.sh.S + p.sh.R) + cur.row
+                                        : ((int64_t)cur.x.b * p.sh.n_ret + cur.x.idx) * kKv8Block + cur.row;
+  const uint16_t* k = (cur.x.streaming ? p.k_sr : p.k_tail) + first * D;
+  const uint16_t* v = (cur.x.streaming ? p.v_sr : p.v_tail) + first * D;
+#pragma unroll
+  for (int e = 0; e < 16 * CPR / 32; ++e) {
+    const int i = lane + 32 * e, row = i / CPR, c = i % CPR;
+    if (row < cur.rows) {
+      copy16_async(stage + chunk16_at<D>(row, c), k + i * 8);
+      copy16_async(stage + Cfg<D, G>::SLICE + chunk16_at<D>(row, c), v + i * 8);
+    }
+  }
+  arrive_after_copies(bar);
+}
+
 // A warp's running softmax over the keys it has seen. Lane (gid, tig) = (lane / 4, lane % 4)
 // holds, of heads 2 tig and 2 tig + 1, the maximum and its own part of the sum, and of O^T
-// m-tile i the dims DT gid + 2 i (+ 1).
+// m-tile i the dims 16 i + gid (+ 8).
 template <int D, int G>
 struct State {
   static constexpr int MT = D / 16;  // m-tiles of O^T
-  static constexpr int DT = D / 8;   // dims of a lane
   float o[MT][4];
   float m[2], l[2];
 
@@ -443,12 +510,14 @@ struct State {
     }
   }
 
-  // One 32-key slice of codes, every key visible. qb: q in B fragments; kf: K's scale times
-  // the heads' factors.
+  // One 32-key slice of codes, every key visible (addresses in shared memory). qb: q in B
+  // fragments; kf: K's scale times the heads' factors.
   template <int CODE>
-  __device__ __forceinline__ void codes(const uint8_t* sk, const uint8_t* sv, const uint32_t (&qb)[D / 16][2],
-                                        float kf0, float kf1, float vs, int gid, int tig) {
+  __device__ __forceinline__ void codes(uint32_t sk, uint32_t sv, const uint32_t (&qb)[D / 16][2], float kf0, float kf1,
+                                        float vs, int lane) {
     float x[8];
+    // K: a fragment's words are the bytes 4 tig ... of rows gid and gid + 8, one 16-dim chunk each
+    const int krow = lane & 15, kch = lane >> 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // keys 16 h + gid and 16 h + gid + 8
       float sc[2][4];
@@ -456,18 +525,16 @@ struct State {
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k) sc[c][k] = 0.f;
-      const int ra = 16 * h + gid, rb = ra + 8;
 #pragma unroll
-      for (int u = 0; u < D / 64; ++u) {
-        const uint4 va = *reinterpret_cast<const uint4*>(sk + chunk_at<D>(ra, tig + 4 * u));
-        const uint4 vb = *reinterpret_cast<const uint4*>(sk + chunk_at<D>(rb, tig + 4 * u));
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+      for (int j = 0; j < D / 16; j += 2) {
+        uint32_t w[4];
+        ldm4(sk + chunk_at<D>(16 * h + krow, j + kch), w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t a0, a1, a2, a3;
-          decode4<CODE>(wa[i], a0, a2);
-          decode4<CODE>(wb[i], a1, a3);
-          mma<true>(sc[i & 1], a0, a1, a2, a3, qb[4 * u + i][0], qb[4 * u + i][1]);
+          decode4<CODE>(w[2 * c], a0, a2);
+          decode4<CODE>(w[2 * c + 1], a1, a3);
+          mma<true>(sc[c], a0, a1, a2, a3, qb[j + c][0], qb[j + c][1]);
         }
       }
 #pragma unroll
@@ -477,68 +544,55 @@ struct State {
     uint32_t pb[4];  // P^T: keys 16 h + 2 tig (+ 1) and + 8 (+ 9) of head gid
 #pragma unroll
     for (int k = 0; k < 4; ++k) pb[k] = transpose8x8(pack_half2(x[2 * k], x[2 * k + 1]));
-    float acc[MT][4];
+    // V: matrix row 4 t + e is the key whose byte lands in byte e of the words of lanes tig = t,
+    // which is to be key 2 t (+ 1) in the first pair and 2 t + 8 (+ 9) in the second
+    const int e = lane & 3, t = (lane >> 2) & 3;
+    const int pair = CODE == kKv8E4m3 ? e >> 1 : e & 1, place = CODE == kKv8E4m3 ? e & 1 : e >> 1;
+    const int vrow = 2 * t + place + 8 * pair, vch = lane >> 4;
+    constexpr int HALF = MT / 2;  // m-tiles at a time: a slice's own accumulators stay few
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i0 = 0; i0 < MT; i0 += HALF) {
+      float acc[HALF][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+      for (int i = 0; i < HALF; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[4][DT / 4];  // the lane's dims of keys 2 tig, + 1, + 8, + 9
+        for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = 16 * h + 2 * tig + (k & 1) + 8 * (k >> 1);
-        if constexpr (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(sv + chunk_at<D>(row, gid));
-          w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(sv + chunk_at<D>(row, gid >> 1) + (gid & 1) * 8);
-          w[k][0] = v.x, w[k][1] = v.y;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < HALF; i += 2) {
+          uint32_t w[4];
+          ldm2_trans8(sv + chunk_at<D>(16 * h + vrow, i0 + i + vch), w);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t a0, a1, a2, a3;
+            decode4<CODE>(w[2 * c], a0, a2);
+            decode4<CODE>(w[2 * c + 1], a1, a3);
+            mma<true>(acc[i + c], a0, a1, a2, a3, pb[2 * h], pb[2 * h + 1]);
+          }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < DT / 4; ++j) {
-        // bytes of one dim of two neighbouring keys side by side: (dim, dim + 1) per word
-        uint32_t a[2], b[2], c[2], d[2];
-        decode4<CODE>(__byte_perm(w[0][j], w[1][j], 0x5140), a[0], b[0]);
-        decode4<CODE>(__byte_perm(w[0][j], w[1][j], 0x7362), a[1], b[1]);
-        decode4<CODE>(__byte_perm(w[2][j], w[3][j], 0x5140), c[0], d[0]);
-        decode4<CODE>(__byte_perm(w[2][j], w[3][j], 0x7362), c[1], d[1]);
+      for (int i = 0; i < HALF; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mma<true>(acc[2 * j + e], a[e], b[e], c[e], d[e], pb[2 * h], pb[2 * h + 1]);
-      }
+        for (int k = 0; k < 4; ++k) o[i0 + i][k] = fmaf(acc[i][k], vs, o[i0 + i][k]);
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = fmaf(acc[i][k], vs, o[i][k]);
   }
 
   // A slice of up to 16 bf16 rows. vis: bit k set where value k's key is visible (keys gid and
   // gid + 8, heads 2 tig and + 1); what lies in the other rows is not used.
-  __device__ __forceinline__ void rows16(const uint8_t* sk, const uint8_t* sv, uint32_t vis,
-                                         const uint32_t (&qa)[D / 16][2], float qf, int gid, int tig) {
+  __device__ __forceinline__ void rows16(uint32_t sk, uint32_t sv, uint32_t vis, const uint32_t (&qa)[D / 16][2],
+                                         float qf, int lane) {
+    const int tig = lane & 3;
     float sc[2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k) sc[c][k] = 0.f;
 #pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      const uint4 ka = *reinterpret_cast<const uint4*>(sk + gid * D * 2 + (tig + 4 * u) * 16);
-      const uint4 kb = *reinterpret_cast<const uint4*>(sk + (gid + 8) * D * 2 + (tig + 4 * u) * 16);
-      mma<false>(sc[0], ka.x, kb.x, ka.y, kb.y, qa[2 * u][0], qa[2 * u][1]);
-      mma<false>(sc[1], ka.z, kb.z, ka.w, kb.w, qa[2 * u + 1][0], qa[2 * u + 1][1]);
-    }
-    uint32_t w[4][MT];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = 2 * tig + (k & 1) + 8 * (k >> 1);
-#pragma unroll
-      for (int c = 0; c < MT / 4; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(sv + row * D * 2 + DT * 2 * gid + 16 * c);
-        w[k][4 * c] = v.x, w[k][4 * c + 1] = v.y, w[k][4 * c + 2] = v.z, w[k][4 * c + 3] = v.w;
-      }
+    for (int j = 0; j < D / 16; ++j) {
+      uint32_t w[4];
+      ldm4(sk + chunk16_at<D>(lane & 15, 2 * j + (lane >> 4)), w);
+      mma<false>(sc[j & 1], w[0], w[1], w[2], w[3], qa[j][0], qa[j][1]);
     }
     float x[4];
 #pragma unroll
@@ -547,37 +601,39 @@ struct State {
     const uint32_t pb0 = transpose8x8(pack_bf16x2(x[0], x[1]));
     const uint32_t pb1 = transpose8x8(pack_bf16x2(x[2], x[3]));
     // a value row nobody sees (an empty or evicted slot) may hold anything: out of the product.
-    // Value k's key is held by lane (gid, tig); the V fragments want it by row.
-    const uint32_t seen = __ballot_sync(0xffffffffu, vis & 1u);         // bit 4 g: key g
-    const uint32_t seen8 = __ballot_sync(0xffffffffu, (vis >> 2) & 1u); // bit 4 g: key g + 8
+    // Lane (g, .) knows of keys g and g + 8; the V fragments hold keys 2 tig, 2 tig + 1 (+ 8).
+    const uint32_t seen = __ballot_sync(0xffffffffu, vis & 1u);          // bit 4 g: key g
+    const uint32_t seen8 = __ballot_sync(0xffffffffu, (vis >> 2) & 1u);  // bit 4 g: key g + 8
+    const uint32_t m0 = ((seen >> (8 * tig)) & 1u) * 0xFFFFu | ((seen >> (8 * tig + 4)) & 1u) * 0xFFFF0000u;
+    const uint32_t m8 = ((seen8 >> (8 * tig)) & 1u) * 0xFFFFu | ((seen8 >> (8 * tig + 4)) & 1u) * 0xFFFF0000u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int g = 2 * tig + (k & 1);
-      if (!(((k >> 1) ? seen8 : seen) >> (4 * g) & 1u)) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) w[k][i] = 0u;
-      }
+    for (int i = 0; i < MT; ++i) {
+      uint32_t w[4];  // dims 16 i + gid and + 8, keys below 8; the same, keys from 8
+      ldm4_trans(sv + chunk16_at<D>((lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)), w);
+      mma<false>(o[i], w[0] & m0, w[1] & m0, w[2] & m8, w[3] & m8, pb0, pb1);
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      mma<false>(o[i], __byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
-                 __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632), pb0, pb1);
   }
 
-  // (o, max, sum) per head into the CTA's merge buffer: red[(warp G + h) (D + 2) + d]
-  __device__ __forceinline__ void write(float* red, int warp, int gid, int tig) {
+  // the sums of the warp's lanes
+  __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int s = 4; s < 32; s <<= 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) l[e] += __shfl_xor_sync(0xffffffffu, l[e], s);
+  }
+  // (o, max, sum) of heads [h0, h0 + HR) into the CTA's merge buffer: red[(warp HR + h - h0) (D + 2) + d]
+  __device__ __forceinline__ void write(float* red, int h0, int warp, int gid, int tig) {
+    constexpr int HR = Cfg<D, G>::HR;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int h = 2 * tig + e;
-      if (h >= G) continue;
-      float* r = red + (warp * G + h) * (D + 2);
+      const int h = 2 * tig + e - h0;
+      if (h < 0 || h >= HR) continue;
+      float* r = red + (warp * HR + h) * (D + 2);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<float2*>(r + DT * gid + 2 * i) = make_float2(o[i][e], o[i][2 + e]);
+      for (int i = 0; i < MT; ++i) {
+        r[16 * i + gid] = o[i][e];
+        r[16 * i + gid + 8] = o[i][2 + e];
+      }
       if (gid == 0) *reinterpret_cast<float2*>(r + D) = make_float2(m[e], l[e]);
     }
   }
@@ -586,19 +642,14 @@ struct State {
 // q of head gid (nullptr past the last) as bf16 B fragments for rows16, and as fp16 ones for
 // codes: scaled by 2^(8 - e), e the exponent of the head's largest |q|, so that every bf16
 // value down to 2^-22 of the largest stays exact. Returns 2^(e - 8).
-template <int D>
+template <int D, int CODE>
 __device__ __forceinline__ float load_q16(const uint16_t* qh, uint32_t (&qb)[D / 16][2], int tig) {
-  uint32_t w[D / 64][8];  // dims 16 (tig + 4 u) ... + 15
+  uint2 w[D / 16];  // dims 16 j + 4 tig ... + 3
   uint32_t m = 0;
 #pragma unroll
-  for (int u = 0; u < D / 64; ++u) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint4 v = qh ? __ldg(reinterpret_cast<const uint4*>(qh + (tig + 4 * u) * 16 + 8 * c)) : make_uint4(0, 0, 0, 0);
-      w[u][4 * c] = v.x, w[u][4 * c + 1] = v.y, w[u][4 * c + 2] = v.z, w[u][4 * c + 3] = v.w;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = __vmaxu2(m, w[u][k] & 0x7FFF7FFFu);
+  for (int j = 0; j < D / 16; ++j) {
+    w[j] = qh ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * j + 4 * tig)) : make_uint2(0, 0);
+    m = __vmaxu2(m, __vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu));
   }
   m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -606,22 +657,21 @@ __device__ __forceinline__ float load_q16(const uint16_t* qh, uint32_t (&qb)[D /
   e = e < 9 ? 9 : (e > 254 ? 254 : e);
   const float f = __uint_as_float((uint32_t)(262 - e) << 23);
 #pragma unroll
-  for (int u = 0; u < D / 64; ++u)
+  for (int j = 0; j < D / 16; ++j) {
+    const float v[4] = {bf16lo(w[j].x) * f, bf16hi(w[j].x) * f, bf16lo(w[j].y) * f, bf16hi(w[j].y) * f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // word i of a chunk of codes: dims 4 i ... 4 i + 3
-      qb[4 * u + i][0] = pack_half2(bf16lo(w[u][2 * i]) * f, bf16hi(w[u][2 * i]) * f);
-      qb[4 * u + i][1] = pack_half2(bf16lo(w[u][2 * i + 1]) * f, bf16hi(w[u][2 * i + 1]) * f);
-    }
+    for (int k = 0; k < 2; ++k) qb[j][k] = pack_half2(v[byte_of<CODE>(k, 0)], v[byte_of<CODE>(k, 1)]);
+  }
   return __uint_as_float((uint32_t)(e - 8) << 23);
 }
 
 template <int D>
 __device__ __forceinline__ void load_qbf16(const uint16_t* qh, uint32_t (&qa)[D / 16][2], int tig) {
 #pragma unroll
-  for (int u = 0; u < D / 32; ++u) {
-    const uint4 v = qh ? __ldg(reinterpret_cast<const uint4*>(qh + (tig + 4 * u) * 8)) : make_uint4(0, 0, 0, 0);
-    qa[2 * u][0] = v.x, qa[2 * u][1] = v.y, qa[2 * u + 1][0] = v.z, qa[2 * u + 1][1] = v.w;
-  }
+  for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      qa[j][k] = qh ? __ldg(reinterpret_cast<const uint32_t*>(qh + 16 * j + 8 * k + 2 * tig)) : 0u;
 }
 
 template <int D, int G, int CODE>
@@ -634,11 +684,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   uint8_t* ring = smem + warp * kStages * C::STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * kStages;
+  // per stage one barrier for codes (the bulk copies' bytes, and the two scales' arrival) and
+  // one for bf16 rows (every lane's arrival)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * kStages * 2;
   float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE) + warp * kStages * 2;
   if (lane == 0) {
-    // a stage is full after the bulk copies' bytes and the two scales' arrival
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 2);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars[2 * s], 2);
+      mbar_init(&bars[2 * s + 1], 32);
+    }
     fence_mbarrier_init();
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
@@ -653,15 +707,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
 
   Cursor cur;
   cur.init(p, sh, warp);
-  uint32_t issued = 0, used = 0, landed = 0;  // slices; landed: waited for
-  uint32_t bad = 0;                           // lane 0: bit s set if stage s was not copied
+  int fill = 0, use = 0;             // stages to fill and to use next
+  uint32_t pending = 0, phases = 0;  // bit of a barrier: copies under way; the phase to wait for
+  uint32_t bad = 0;                  // lane 0: bit s set if stage s was not copied
+  bool rows_seen = false;
   auto refill = [&]() {
-    const int s = (int)(issued % kStages);
-    if (lane == 0) {
-      const bool ok = issue<D, G>(p, cur, ring + s * C::STAGE, scales + 2 * s, &bars[s], pol);
-      bad = ok ? bad & ~(1u << s) : bad | (1u << s);
+    uint8_t* stage = ring + fill * C::STAGE;
+    if (cur.codes) {
+      if (lane == 0) {
+        if (rows_seen) fence_proxy_async_shared();  // a stage may have held rows written by cp.async
+        const bool there = issue_codes<D, G>(p, cur, stage, scales + 2 * fill, &bars[2 * fill], pol);
+        bad = there ? bad & ~(1u << fill) : bad | (1u << fill);
+      }
+      pending |= 1u << (2 * fill);
+    } else {
+      issue_rows<D, G>(p, cur, stage, &bars[2 * fill + 1], lane);
+      pending |= 2u << (2 * fill);
+      rows_seen = true;
     }
-    ++issued;
+    fill = fill + 1 == kStages ? 0 : fill + 1;
     cur.advance(p);
   };
   for (int s = 0; s < kStages - 1 && cur.live; ++s) refill();
@@ -671,156 +735,187 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   bool ok = true;  // of this warp: a wait that ran out stops its copies, not the CTA's barriers
   State<D, G> st;
   int64_t ub = sh.ub;
+  auto wait = [&](int b) {
+    const bool done = mbar_wait(&bars[b], (phases >> b) & 1u, err, kErrDecodeConsumer);
+    phases ^= 1u << b;
+    pending &= ~(1u << b);
+    return done;
+  };
   // next slice: refills the stage of the one before, and waits for its own
-  auto next = [&]() {
+  auto next = [&](int kind) {
     if (cur.live && ok) refill();
-    const int s = (int)(used % kStages);
-    if (ok) ok = mbar_wait(&bars[s], (used / kStages) & 1u, err, kErrDecodeConsumer);
-    if (ok) ++landed;
-    ++used;
+    const int s = use;
+    if (ok) ok = wait(2 * s + kind);
+    use = use + 1 == kStages ? 0 : use + 1;
     return s;
   };
   for (int u = sh.u; p.whole ? u == sh.u : ub < sh.x1; ++u) {
     const Unit x = unit_of(p, u);
-    const int64_t lt0 = p.whole ? 0 : tiles_before(sh.x0 - ub, x.tiles);
-    const int64_t lt1 = p.whole ? x.tiles : tiles_before(sh.x1 - ub, x.tiles);
+    const int lt0 = p.whole ? 0 : tiles_before(sh.x0 - ub, x.tiles);
+    const int lt1 = p.whole ? x.tiles : tiles_before(sh.x1 - ub, x.tiles);
     if (lt0 >= lt1) {  // (the share starts behind its last tile)
       ub += x.tiles + 1;
       continue;
     }
     st.reset();
-    const uint16_t* qh = gid < G ? p.q + ((int64_t)x.b * p.sh.Hq + (int64_t)x.kvh * G + gid) * D : nullptr;
-    const int64_t tc = x.streaming ? 0 : tiles_codes(x.n);
+    const int64_t hrow = head_row<G>(p, x);
+    const uint16_t* qh = gid < G ? p.q + (hrow + gid) * D : nullptr;
+    const int tc = x.tc;
     if (lt0 < tc) {
       uint32_t qb[D / 16][2];
-      const float f = load_q16<D>(qh, qb, tig) * p.scale_log2;
+      const float f = load_q16<D, CODE>(qh, qb, tig) * p.scale_log2;
       const float f0 = __shfl_sync(0xffffffffu, f, 8 * tig), f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
-      const int64_t full = x.n / kKv8Block * kKv8Block;
-      for (int64_t lt = lt0; lt < lt1 && lt < tc; ++lt) {
-        if (lt * kKv8TK + warp * kRows >= full) break;
-        const int s = next();
+      int left = (lt1 < tc ? lt1 : tc) - lt0;  // this warp's slices: none in a tile it lies behind
+      if ((int64_t)(lt0 + left - 1) * kKv8TK + warp * kRows >= code_rows_of(x.n)) --left;
+      for (; left > 0; --left) {
+        const int s = next(0);
         const bool skip = !ok || ((__shfl_sync(0xffffffffu, bad, 0) >> s) & 1u);
         if (!skip) {
-          const uint8_t* sk = ring + s * C::STAGE;
+          const uint32_t sk = smem_u32(ring + s * C::STAGE);
           const float ks = scales[2 * s], vs = scales[2 * s + 1];
-          st.template codes<CODE>(sk, sk + C::SLICE, qb, f0 * ks, f1 * ks, vs, gid, tig);
+          st.template codes<CODE>(sk, sk + C::SLICE, qb, f0 * ks, f1 * ks, vs, lane);
         }
         __syncwarp();
       }
     }
-    const int64_t tb = lt0 > tc ? lt0 : tc;  // bf16 tiles: a streaming unit's, or the tail's one
+    const int tb = lt0 > tc ? lt0 : tc;  // bf16 tiles: a streaming unit's, or the tail's one
     if (tb < lt1) {
       uint32_t qa[D / 16][2];
       load_qbf16<D>(qh, qa, tig);
       const int have = bf16_rows(p, x);
-      for (int64_t lt = tb; lt < lt1; ++lt) {
-        const int r0 = (int)(lt - tc) * kKv8TKBf16 + warp * 16;
+      for (int lt = tb; lt < lt1; ++lt) {
+        const int r0 = (lt - tc) * kKv8TKBf16 + warp * 16;
         if (r0 >= have) break;
-        int64_t at[2];  // positions of keys gid and gid + 8
+        int at[2];  // positions of keys gid and gid + 8
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int key = gid + 8 * k;
           at[k] = r0 + key >= have ? -1 : (x.streaming ? __ldg(p.pos + (int64_t)x.b * SR + r0 + key) : 0);
         }
-        const int s = next();
+        const int s = next(1);
         uint32_t vis = 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const bool v = at[k] >= 0 && (!x.streaming || (at[k] < x.n && (at[k] < p.sh.S || x.n - 1 - at[k] < p.sh.R)));
           vis |= (v ? 3u : 0u) << (2 * k);
         }
-        const uint8_t* sk = ring + s * C::STAGE;
-        if (ok) st.rows16(sk, sk + C::SLICE, vis, qa, p.scale_log2, gid, tig);
+        const uint32_t sk = smem_u32(ring + s * C::STAGE);
+        if (ok) st.rows16(sk, sk + C::SLICE, vis, qa, p.scale_log2, lane);
         __syncwarp();
       }
     }
 
-    // merge of the eight warps
-    st.write(red, warp, gid, tig);
-    __syncthreads();
+    // merge of the warps, HR heads at a time
+    st.finish();
     int c_first = 0, n_parts = 1;
-    if (!p.whole) {
+    if (!p.whole && (lt0 > 0 || lt1 < x.tiles)) {
       c_first = cta_of(sh, ub);
-      n_parts = cta_of(sh, x.tiles > 1 ? ub + x.tiles : ub) - c_first + 1;
+      n_parts = cta_of(sh, ub + x.tiles) - c_first + 1;
     }
     float* part = p.partials + (int64_t)(lt0 == 0 ? u : U + (int)blockIdx.x) * G * C::PS;
-    for (int e = tid; e < G * D; e += kThreads) {
-      const int h = e / D, d = e % D;
-      float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * G + h) * (D + 2) + D]);
-      float num = 0.f, den = 0.f;
+    for (int h0 = 0; h0 < G; h0 += C::HR) {
+      st.write(red, h0, warp, gid, tig);
+      __syncthreads();
+      for (int e = tid; e < C::HR * D; e += kThreads) {
+        const int h = e / D, d = e % D;
+        float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* r = red + (w * G + h) * (D + 2);
-        const float f = r[D] == -INFINITY && !(r[D + 1] != 0.f) ? 0.f : ex2_approx(r[D] - M);
-        num = fmaf(f, r[d], num);
-        den = fmaf(f, r[D + 1], den);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * C::HR + h) * (D + 2) + D]);
+        float num = 0.f, den = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float* r = red + (w * C::HR + h) * (D + 2);
+          const float f = r[D] == -INFINITY && !(r[D + 1] != 0.f) ? 0.f : ex2_approx(r[D] - M);
+          num = fmaf(f, r[d], num);
+          den = fmaf(f, r[D + 1], den);
+        }
+        float* ph = part + (h0 + h) * C::PS;
+        if (n_parts == 1)
+          p.o[(hrow + h0 + h) * D + d] =
+              __bfloat16_as_ushort(__float2bfloat16_rn(den != 0.f ? num / den : 0.f));
+        else
+          ph[d] = num;
+        if (d == 0 && !p.whole && (n_parts > 1 || lt0 == 0)) {
+          ph[D] = M;
+          ph[D + 1] = den;
+          ph[D + 2] = __int_as_float(c_first);
+          ph[D + 3] = __int_as_float(n_parts);
+        }
       }
-      if (n_parts == 1)
-        p.o[((int64_t)x.b * p.sh.Hq + (int64_t)x.kvh * G + h) * D + d] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(den != 0.f ? num / den : 0.f));
-      if (n_parts > 1) part[h * C::PS + d] = num;
-      if (d == 0 && !p.whole && (n_parts > 1 || lt0 == 0)) {
-        part[h * C::PS + D] = M;
-        part[h * C::PS + D + 1] = den;
-        part[h * C::PS + D + 2] = __int_as_float(c_first);
-        part[h * C::PS + D + 3] = __int_as_float(n_parts);
-      }
+      __syncthreads();  // the buffer is free again
     }
-    __syncthreads();  // the buffer is the next unit's
     ub += x.tiles + 1;
   }
   // copies still in flight (after a wait that ran out) land before the CTA ends
-  if (lane == 0)
-    for (uint32_t j = landed; j < issued; ++j) mbar_wait(&bars[j % kStages], (j / kStages) & 1u, err, kErrDecodeConsumer);
+#pragma unroll
+  for (int b = 0; b < 2 * kStages; ++b)
+    if ((pending >> b) & 1u) wait(b);
   __syncthreads();
 }
 
-// Units whose tiles were split over CTAs: one CTA per (unit, head), warp w takes parts w,
-// w + 8, ...; a lane holds D / 32 dims. Launched as the decode's programmatic dependent.
-template <int D, int G>
-__global__ void __launch_bounds__(kThreads) decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p) {
-  constexpr int PS = Cfg<D, G>::PS, V = D / 32;
-  const int h = blockIdx.x % G, u = blockIdx.x / G;
+// Merge of the units whose tiles were split over CTAs, launched as the decode's programmatic
+// dependent. A CTA takes one unit's head, and of its output kDims dims: its warps are groups of
+// 32 dims times parts i, i + groups, ..., up to kMergeNB of which a warp loads at once. Few
+// units have many parts each (up to one per SM): 32 dims a CTA, eight groups of parts, one round
+// of loads. Many units have few parts: all D dims a CTA, fewer CTAs.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeNB = 20;
+template <int D, int G, int kDims>
+__global__ void __launch_bounds__(kMergeWarps * 32) decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p) {
+  constexpr int PS = Cfg<D, G>::PS, DC = D / kDims, WD = kDims / 32, NG = kMergeWarps / WD;
+  const int dc = blockIdx.x % DC, h = blockIdx.x / DC % G, u = blockIdx.x / (DC * G);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float s_o[kWarps][D], s_m[kWarps], s_l[kWarps];
+  const int grp = warp / WD, wd = warp % WD;
+  __shared__ float s_o[kMergeWarps][32], s_m[kMergeWarps], s_l[kMergeWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* head = p.partials + ((int64_t)u * G + h) * PS;
   const int n_parts = __float_as_int(__ldcg(head + D + 3));
   if (n_parts <= 1) return;
   const int c_first = __float_as_int(__ldcg(head + D + 2));
-  const int U = p.U_r + p.U_s;
-  float acc[V], M = -INFINITY, den = 0.f;
+  const float* cont = p.partials + ((int64_t)(p.U_r + p.U_s + c_first) * G + h) * PS;  // part i >= 1: i G PS further
+  const int d = dc * kDims + wd * 32 + lane;
+  float acc = 0.f, M = -INFINITY, den = 0.f;
+  for (int i0 = grp; i0 < n_parts; i0 += NG * kMergeNB) {
+    float mb[kMergeNB], lb[kMergeNB], ob[kMergeNB];
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n_parts; i += kWarps) {
-    const float* r = i == 0 ? head : p.partials + ((int64_t)(U + c_first + i) * G + h) * PS;
-    const float m = __ldcg(r + D), l = __ldcg(r + D + 1);
-    float ov[V];
+    for (int i = 0; i < kMergeNB; ++i) {
+      const int k = i0 + i * NG;
+      const float* r = k == 0 ? head : cont + (int64_t)k * G * PS;
+      mb[i] = -INFINITY;
+      lb[i] = ob[i] = 0.f;
+      if (k < n_parts) {
+        mb[i] = __ldcg(r + D);
+        lb[i] = __ldcg(r + D + 1);
+        ob[i] = __ldcg(r + d);
+      }
+    }
+    float mn = M;
 #pragma unroll
-    for (int v = 0; v < V; ++v) ov[v] = __ldcg(r + lane * V + v);
-    const float mn = fmaxf(M, m);
+    for (int i = 0; i < kMergeNB; ++i) mn = fmaxf(mn, mb[i]);
     const float fo = M == -INFINITY && !(den != 0.f) ? 0.f : ex2_approx(M - mn);
-    const float fi = m == -INFINITY && !(l != 0.f) ? 0.f : ex2_approx(m - mn);
-    den = den * fo + l * fi;
+    den *= fo;
+    acc *= fo;
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = acc[v] * fo + ov[v] * fi;
+    for (int i = 0; i < kMergeNB; ++i) {
+      const float f = mb[i] == -INFINITY && !(lb[i] != 0.f) ? 0.f : ex2_approx(mb[i] - mn);
+      den = fmaf(f, lb[i], den);
+      acc = fmaf(f, ob[i], acc);
+    }
     M = mn;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
+  s_o[warp][lane] = acc;
   if (lane == 0) s_m[warp] = M, s_l[warp] = den;
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += kThreads) {
+  if (grp == 0) {
     float T = -INFINITY, num = 0.f, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) T = fmaxf(T, s_m[w]);
+    for (int g = 0; g < NG; ++g) T = fmaxf(T, s_m[g * WD + wd]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int g = 0; g < NG; ++g) {
+      const int w = g * WD + wd;
       const float f = s_m[w] == -INFINITY && !(s_l[w] != 0.f) ? 0.f : ex2_approx(s_m[w] - T);
-      num = fmaf(f, s_o[w][d], num);
+      num = fmaf(f, s_o[w][lane], num);
       sum = fmaf(f, s_l[w], sum);
     }
     const bool streaming = u >= p.U_r;
@@ -859,9 +954,13 @@ cudaError_t launch_t(const Kv8DecodeParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, decode_kv8_kernel<D, G, CODE>, p);
   if (e != cudaSuccess || p.whole) return e;
-  cfg.gridDim = dim3((unsigned)((p.U_r + p.U_s) * G));
+  const int64_t U = (int64_t)p.U_r + p.U_s;
+  const bool wide = p.C > 16 * U;  // more parts a unit than a CTA of all dims loads at once
+  cfg.gridDim = dim3((unsigned)(U * G * (wide ? D / 32 : 1)));
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G>, p);
+  return wide ? cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G, 32>, p)
+              : cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G, D>, p);
 }
 
 template <int D, int CODE>
@@ -878,12 +977,14 @@ cudaError_t launch_g(const Kv8DecodeParams& p, cudaStream_t stream) {
 }  // namespace
 
 void plan_decode_kv8(Kv8DecodeParams* p, int num_sms) {
-  const int SR = p->sh.S + p->sh.R;
-  const int64_t tr = p->U_r ? tiles_ret(p->n) : 0, ts = p->U_s ? tiles_str(p->n, SR) : 0;
   const int64_t U = (int64_t)p->U_r + p->U_s;
-  p->whole = U <= num_sms && tr <= kShortTiles && ts <= kShortTiles;
-  const int64_t W = tr * p->U_r + ts * p->U_s;  // (a CTA's share is at least one tile)
-  p->C = (int)(p->whole ? U : (W < num_sms ? W : num_sms));
+  p->tiles_r = tiles_ret((int)p->n);
+  p->tiles_s = tiles_str((int)p->n, p->sh.S + p->sh.R);
+  p->line_r = (int64_t)p->U_r * (p->tiles_r + 1);
+  p->line_s = (int64_t)p->U_s * (p->tiles_s + 1);
+  p->whole = U <= num_sms && (p->U_r == 0 || p->tiles_r <= kShortTiles) && (p->U_s == 0 || p->tiles_s <= kShortTiles);
+  const int64_t most = (p->line_r + p->line_s) / 2;  // two places each at least
+  p->C = (int)(p->whole ? U : (most < num_sms ? most : num_sms));
 }
 
 cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, cudaStream_t stream) {

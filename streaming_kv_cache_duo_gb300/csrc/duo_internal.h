@@ -263,8 +263,14 @@ struct Kv8AppendParams {
 cudaError_t launch_append_kv8(const Kv8AppendParams& p, cudaStream_t stream);
 cudaError_t append_kv8_read_clear_error(uint32_t* code);
 
-constexpr int kKv8TK = 256;       // keys of a decode tile over codes (32 per warp)
-constexpr int kKv8TKBf16 = 128;   // keys of a tile over bf16 rows (ring or tail; 16 per warp)
+#ifndef KV8W
+#define KV8W 8
+#define KV8S 3
+#endif
+constexpr int kKv8Warps = KV8W, kKv8Stages = KV8S;
+constexpr int kKv8Rows = 32;                      // rows of codes a warp takes of a tile
+constexpr int kKv8TK = kKv8Warps * kKv8Rows;      // keys of a decode tile over codes
+constexpr int kKv8TKBf16 = kKv8Warps * 16;        // and over bf16 rows (ring or tail)
 
 struct Kv8DecodeParams {
   CUtensorMap tm_k;  // 2-D over the codes [rows, D], box 32 x D, swizzled by the row width
@@ -283,6 +289,8 @@ struct Kv8DecodeParams {
   int U_r, U_s;             // units (one per (sequence, KV head)) of each kind
   int C;                    // CTAs
   int whole;                // 1: CTA c takes unit c, no unit is split
+  int tiles_r, tiles_s;     // tiles of a unit of each kind at n tokens
+  int64_t line_r, line_s;   // places that all units of each kind take on the line of tiles
   int code_type;
   int64_t cap64;
   float scale_log2;  // log2(e) / sqrt(D)
