@@ -59,11 +59,11 @@ struct Cfg {
   static constexpr int SLICE = kRows * D;  // bytes of a warp's K (or V) codes
   static constexpr int STAGE = 2 * SLICE;
   static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int HR = G < 4 ? G : 4;  // heads merged at a time
+  static constexpr int HR = G < (kWarps > 8 ? 2 : 4) ? G : (kWarps > 8 ? 2 : 4);  // heads merged at a time
   static constexpr int RED = kWarps * HR * (D + 2);
   static constexpr int PS = D + 4;  // floats per head of a part
   static constexpr int OFF_RED = RING;
-  static constexpr int OFF_BAR = OFF_RED + RED * 4;
+  static constexpr int OFF_BAR = OFF_RED + 2 * RED * 4;  // (two merge buffers)
   static constexpr int OFF_SCALE = OFF_BAR + kWarps * kStages * 16;
   static constexpr size_t SMEM = (size_t)OFF_SCALE + kWarps * kStages * 8 + 1024;  // + alignment
 };
@@ -643,14 +643,10 @@ struct State {
 // codes: scaled by 2^(8 - e), e the exponent of the head's largest |q|, so that every bf16
 // value down to 2^-22 of the largest stays exact. Returns 2^(e - 8).
 template <int D, int CODE>
-__device__ __forceinline__ float load_q16(const uint16_t* qh, uint32_t (&qb)[D / 16][2], int tig) {
-  uint2 w[D / 16];  // dims 16 j + 4 tig ... + 3
+__device__ __forceinline__ float convert_q(uint32_t (&qb)[D / 16][2]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    w[j] = qh ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * j + 4 * tig)) : make_uint2(0, 0);
-    m = __vmaxu2(m, __vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu));
-  }
+  for (int j = 0; j < D / 16; ++j) m = __vmaxu2(m, __vmaxu2(qb[j][0] & 0x7FFF7FFFu, qb[j][1] & 0x7FFF7FFFu));
   m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
   int e = (int)(max(m & 0xFFFFu, m >> 16) >> 7);  // biased exponent
@@ -658,20 +654,55 @@ __device__ __forceinline__ float load_q16(const uint16_t* qh, uint32_t (&qb)[D /
   const float f = __uint_as_float((uint32_t)(262 - e) << 23);
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
-    const float v[4] = {bf16lo(w[j].x) * f, bf16hi(w[j].x) * f, bf16lo(w[j].y) * f, bf16hi(w[j].y) * f};
+    const float v[4] = {bf16lo(qb[j][0]) * f, bf16hi(qb[j][0]) * f, bf16lo(qb[j][1]) * f, bf16hi(qb[j][1]) * f};
 #pragma unroll
     for (int k = 0; k < 2; ++k) qb[j][k] = pack_half2(v[byte_of<CODE>(k, 0)], v[byte_of<CODE>(k, 1)]);
   }
   return __uint_as_float((uint32_t)(e - 8) << 23);
 }
 
+// What a lane needs of q's row of head gid (nullptr past the last): for codes dims 16 j + 4 tig
+// ... + 3 (convert_q makes the fragments), for bf16 rows the fragments themselves.
 template <int D>
-__device__ __forceinline__ void load_qbf16(const uint16_t* qh, uint32_t (&qa)[D / 16][2], int tig) {
+__device__ __forceinline__ void fetch_q(const uint16_t* qh, bool codes, uint32_t (&q)[D / 16][2], int tig) {
+  const uint16_t* a = qh ? qh + (codes ? 4 * tig : 2 * tig) : nullptr;
+  const int second = codes ? 2 : 8;
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j)
+  for (int j = 0; j < D / 16; ++j) {
+    q[j][0] = a ? __ldg(reinterpret_cast<const uint32_t*>(a + 16 * j)) : 0u;
+    q[j][1] = a ? __ldg(reinterpret_cast<const uint32_t*>(a + 16 * j + second)) : 0u;
+  }
+}
+
+// A unit and this CTA's tiles of it.
+struct Segment {
+  Unit x;
+  int64_t ub;
+  int lt0, lt1;
+  bool live;
+  // from the unit (u, ub) on, the first of which the share has tiles
+  __device__ __forceinline__ void find(const Kv8DecodeParams& p, const Share& s, int u, int64_t at) {
+    ub = at;
+    for (;; ++u) {
+      live = p.whole ? u == s.u : ub < s.x1;
+      if (!live) return;
+      x = unit_of(p, u);
+      lt0 = p.whole ? 0 : tiles_before(s.x0 - ub, x.tiles);
+      lt1 = p.whole ? x.tiles : tiles_before(s.x1 - ub, x.tiles);
+      if (lt0 < lt1) return;
+      ub += x.tiles + 1;  // (the share starts behind its last tile)
+    }
+  }
+};
+
+// Positions held by ring slots gid and gid + 8 of a warp's slice, which starts at slot r0 (-1
+// past the last; any position does for a tail's rows).
+__device__ __forceinline__ void fetch_pos(const Kv8DecodeParams& p, const Unit& x, int r0, int have, int gid, int (&at)[2]) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      qa[j][k] = qh ? __ldg(reinterpret_cast<const uint32_t*>(qh + 16 * j + 8 * k + 2 * tig)) : 0u;
+  for (int k = 0; k < 2; ++k) {
+    const int row = r0 + gid + 8 * k;
+    at[k] = row >= have ? -1 : (x.streaming ? __ldg(p.pos + (int64_t)x.b * (p.sh.S + p.sh.R) + row) : 0);
+  }
 }
 
 template <int D, int G, int CODE>
@@ -731,10 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   for (int s = 0; s < kStages - 1 && cur.live; ++s) refill();
 
   const int U = p.U_r + p.U_s;
-  const int SR = p.sh.S + p.sh.R;
   bool ok = true;  // of this warp: a wait that ran out stops its copies, not the CTA's barriers
   State<D, G> st;
-  int64_t ub = sh.ub;
   auto wait = [&](int b) {
     const bool done = mbar_wait(&bars[b], (phases >> b) & 1u, err, kErrDecodeConsumer);
     phases ^= 1u << b;
@@ -749,21 +778,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     use = use + 1 == kStages ? 0 : use + 1;
     return s;
   };
-  for (int u = sh.u; p.whole ? u == sh.u : ub < sh.x1; ++u) {
-    const Unit x = unit_of(p, u);
-    const int lt0 = p.whole ? 0 : tiles_before(sh.x0 - ub, x.tiles);
-    const int lt1 = p.whole ? x.tiles : tiles_before(sh.x1 - ub, x.tiles);
-    if (lt0 >= lt1) {  // (the share starts behind its last tile)
-      ub += x.tiles + 1;
-      continue;
-    }
+  Segment sg;
+  sg.find(p, sh, sh.u, sh.ub);
+  // fetched ahead for the unit that comes next, while the warps of this one are merged
+  uint32_t q[D / 16][2];
+  int at[2];
+  int64_t hrow = 0;
+  auto fetch = [&]() {
+    hrow = head_row<G>(p, sg.x);
+    const bool codes = sg.lt0 < sg.x.tc;
+    fetch_q<D>(gid < G ? p.q + (hrow + gid) * D : nullptr, codes, q, tig);
+    if (!codes) fetch_pos(p, sg.x, (sg.lt0 - sg.x.tc) * kKv8TKBf16 + warp * 16, bf16_rows(p, sg.x), gid, at);
+  };
+  if (sg.live) fetch();
+  int buf = 0;
+  while (sg.live) {
+    const Unit x = sg.x;
+    const int lt0 = sg.lt0, lt1 = sg.lt1, tc = x.tc;
+    const int64_t ub = sg.ub, orow = hrow;
     st.reset();
-    const int64_t hrow = head_row<G>(p, x);
-    const uint16_t* qh = gid < G ? p.q + (hrow + gid) * D : nullptr;
-    const int tc = x.tc;
     if (lt0 < tc) {
-      uint32_t qb[D / 16][2];
-      const float f = load_q16<D, CODE>(qh, qb, tig) * p.scale_log2;
+      const float f = convert_q<D, CODE>(q) * p.scale_log2;
       const float f0 = __shfl_sync(0xffffffffu, f, 8 * tig), f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
       int left = (lt1 < tc ? lt1 : tc) - lt0;  // this warp's slices: none in a tile it lies behind
       if ((int64_t)(lt0 + left - 1) * kKv8TK + warp * kRows >= code_rows_of(x.n)) --left;
@@ -773,67 +808,65 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
         if (!skip) {
           const uint32_t sk = smem_u32(ring + s * C::STAGE);
           const float ks = scales[2 * s], vs = scales[2 * s + 1];
-          st.template codes<CODE>(sk, sk + C::SLICE, qb, f0 * ks, f1 * ks, vs, lane);
+          st.template codes<CODE>(sk, sk + C::SLICE, q, f0 * ks, f1 * ks, vs, lane);
         }
         __syncwarp();
       }
-    }
-    const int tb = lt0 > tc ? lt0 : tc;  // bf16 tiles: a streaming unit's, or the tail's one
-    if (tb < lt1) {
-      uint32_t qa[D / 16][2];
-      load_qbf16<D>(qh, qa, tig);
-      const int have = bf16_rows(p, x);
-      for (int lt = tb; lt < lt1; ++lt) {
-        const int r0 = (lt - tc) * kKv8TKBf16 + warp * 16;
-        if (r0 >= have) break;
-        int at[2];  // positions of keys gid and gid + 8
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int key = gid + 8 * k;
-          at[k] = r0 + key >= have ? -1 : (x.streaming ? __ldg(p.pos + (int64_t)x.b * SR + r0 + key) : 0);
-        }
-        const int s = next(1);
-        uint32_t vis = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const bool v = at[k] >= 0 && (!x.streaming || (at[k] < x.n && (at[k] < p.sh.S || x.n - 1 - at[k] < p.sh.R)));
-          vis |= (v ? 3u : 0u) << (2 * k);
-        }
-        const uint32_t sk = smem_u32(ring + s * C::STAGE);
-        if (ok) st.rows16(sk, sk + C::SLICE, vis, qa, p.scale_log2, lane);
-        __syncwarp();
+      if (lt1 > tc) {  // the tail's tile follows
+        fetch_q<D>(gid < G ? p.q + (orow + gid) * D : nullptr, false, q, tig);
+        fetch_pos(p, x, warp * 16, bf16_rows(p, x), gid, at);
       }
     }
+    const int have = bf16_rows(p, x);
+    for (int lt = lt0 > tc ? lt0 : tc; lt < lt1; ++lt) {  // a streaming unit's tiles, or the tail's one
+      const int r0 = (lt - tc) * kKv8TKBf16 + warp * 16;
+      if (r0 >= have) break;
+      uint32_t vis = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool v = at[k] >= 0 && (!x.streaming || (at[k] < x.n && (at[k] < p.sh.S || x.n - 1 - at[k] < p.sh.R)));
+        vis |= (v ? 3u : 0u) << (2 * k);
+      }
+      if (lt + 1 < lt1) fetch_pos(p, x, r0 + kKv8TKBf16, have, gid, at);
+      const int s = next(1);
+      const uint32_t sk = smem_u32(ring + s * C::STAGE);
+      if (ok) st.rows16(sk, sk + C::SLICE, vis, q, p.scale_log2, lane);
+      __syncwarp();
+    }
+    sg.find(p, sh, x.u + 1, ub + x.tiles + 1);
+    if (sg.live) fetch();
 
-    // merge of the warps, HR heads at a time
+    // merge of the warps, HR heads at a time, in two buffers in turn: a warp may write the next
+    // one while another still reads this one, and is past the barrier between before its turn
     st.finish();
     int c_first = 0, n_parts = 1;
     if (!p.whole && (lt0 > 0 || lt1 < x.tiles)) {
       c_first = cta_of(sh, ub);
       n_parts = cta_of(sh, ub + x.tiles) - c_first + 1;
     }
-    float* part = p.partials + (int64_t)(lt0 == 0 ? u : U + (int)blockIdx.x) * G * C::PS;
+    float* part = p.partials + (int64_t)(lt0 == 0 ? x.u : U + (int)blockIdx.x) * G * C::PS;
 #pragma unroll
     for (int h0 = 0; h0 < G; h0 += C::HR) {
-      st.write(red, h0, warp, gid, tig);
+      float* rb = red + buf * C::RED;
+      buf ^= 1;
+      st.write(rb, h0, warp, gid, tig);
       __syncthreads();
       for (int e = tid; e < C::HR * D; e += kThreads) {
         const int h = e / D, d = e % D;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * C::HR + h) * (D + 2) + D]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, rb[(w * C::HR + h) * (D + 2) + D]);
         float num = 0.f, den = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float* r = red + (w * C::HR + h) * (D + 2);
+          const float* r = rb + (w * C::HR + h) * (D + 2);
           const float f = r[D] == -INFINITY && !(r[D + 1] != 0.f) ? 0.f : ex2_approx(r[D] - M);
           num = fmaf(f, r[d], num);
           den = fmaf(f, r[D + 1], den);
         }
         float* ph = part + (h0 + h) * C::PS;
         if (n_parts == 1)
-          p.o[(hrow + h0 + h) * D + d] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(den != 0.f ? num / den : 0.f));
+          p.o[(orow + h0 + h) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(den != 0.f ? num / den : 0.f));
         else
           ph[d] = num;
         if (d == 0 && !p.whole && (n_parts > 1 || lt0 == 0)) {
@@ -843,9 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
           ph[D + 3] = __int_as_float(n_parts);
         }
       }
-      __syncthreads();  // the buffer is free again
     }
-    ub += x.tiles + 1;
   }
   // copies still in flight (after a wait that ran out) land before the CTA ends
 #pragma unroll
