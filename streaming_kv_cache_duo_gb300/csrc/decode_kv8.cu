@@ -31,8 +31,9 @@
 //
 // Merge: as the bf16 decode. The warps of a CTA merge in shared memory; a unit split over
 // CTAs leaves (o, max, sum) parts for a second kernel, launched as a programmatic dependent.
-// A part that starts a unit sits at the unit's index, a continuation at its CTA's (a CTA has
-// one at most), and the first part names the CTAs of the others.
+// A CTA has at most one part that goes on with a unit begun by another (its first) and one that
+// begins a unit it does not end (its last): two places each. So there is one job for the second
+// kernel at most per CTA of the first, however many units there are.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -59,7 +60,7 @@ struct Cfg {
   static constexpr int SLICE = kRows * D;  // bytes of a warp's K (or V) codes
   static constexpr int STAGE = 2 * SLICE;
   static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int HR = G < (kWarps > 8 ? 2 : 4) ? G : (kWarps > 8 ? 2 : 4);  // heads merged at a time
+  static constexpr int HR = G < 4 ? G : 4;  // heads merged at a time
   static constexpr int RED = kWarps * HR * (D + 2);
   static constexpr int PS = D + 4;  // floats per head of a part
   static constexpr int OFF_RED = RING;
@@ -237,10 +238,11 @@ __device__ __forceinline__ int tiles_before(int64_t y, int T) {
 
 // a b / c for a, b, c >= 0; in 32 bits where it fits (64-bit divisions on a CTA's way in and
 // out cost a microsecond).
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
   const int64_t ab = a * b;
   if (((ab | c) >> 32) == 0) return (int64_t)((uint32_t)ab / (uint32_t)c);
-  return ab / c;
+  return div64(ab, c);
 }
 
 // This CTA's share of the line, places [x0, x1) of W, shared by C CTAs (each gets at least two
@@ -661,6 +663,12 @@ __device__ __forceinline__ float convert_q(uint32_t (&qb)[D / 16][2]) {
   return __uint_as_float((uint32_t)(e - 8) << 23);
 }
 
+// Entry of the merge's jobs, behind the parts: by unit (its first CTA, its number of parts) if
+// p.merge_units, else by CTA (a unit it begins and does not end, or -1; its number of parts).
+__device__ __forceinline__ int2* job_of(const Kv8DecodeParams& p, int i) {
+  return reinterpret_cast<int2*>(p.partials + (int64_t)2 * p.C * p.sh.g * (p.sh.D + 4)) + i;
+}
+
 // What a lane needs of q's row of head gid (nullptr past the last): for codes dims 16 j + 4 tig
 // ... + 3 (convert_q makes the fragments), for bf16 rows the fragments themselves.
 template <int D>
@@ -761,7 +769,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   };
   for (int s = 0; s < kStages - 1 && cur.live; ++s) refill();
 
-  const int U = p.U_r + p.U_s;
   bool ok = true;  // of this warp: a wait that ran out stops its copies, not the CTA's barriers
   State<D, G> st;
   auto wait = [&](int b) {
@@ -792,6 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   };
   if (sg.live) fetch();
   int buf = 0;
+  int2 job = make_int2(-1, 0);  // for the merge: a unit this CTA begins and does not end, its parts
   while (sg.live) {
     const Unit x = sg.x;
     const int lt0 = sg.lt0, lt1 = sg.lt1, tc = x.tc;
@@ -839,18 +847,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     // merge of the warps, HR heads at a time, in two buffers in turn: a warp may write the next
     // one while another still reads this one, and is past the barrier between before its turn
     st.finish();
-    int c_first = 0, n_parts = 1;
-    if (!p.whole && (lt0 > 0 || lt1 < x.tiles)) {
-      c_first = cta_of(sh, ub);
-      n_parts = cta_of(sh, ub + x.tiles) - c_first + 1;
+    int n_parts = 1;
+    if (!p.whole && (lt0 > 0 || lt1 < x.tiles)) n_parts = cta_of(sh, ub + x.tiles) - cta_of(sh, ub) + 1;
+    float* part = p.partials + (int64_t)(2 * blockIdx.x + (lt0 == 0)) * G * C::PS;
+    if (lt0 == 0 && p.merge_units) {
+      if (tid == 0) *job_of(p, x.u) = make_int2(blockIdx.x, n_parts);
+    } else if (lt0 == 0 && n_parts > 1) {
+      job = make_int2(x.u, n_parts);
     }
-    float* part = p.partials + (int64_t)(lt0 == 0 ? x.u : U + (int)blockIdx.x) * G * C::PS;
-#pragma unroll
+#pragma unroll 1
     for (int h0 = 0; h0 < G; h0 += C::HR) {
       float* rb = red + buf * C::RED;
       buf ^= 1;
       st.write(rb, h0, warp, gid, tig);
       __syncthreads();
+#pragma unroll 1
       for (int e = tid; e < C::HR * D; e += kThreads) {
         const int h = e / D, d = e % D;
         float M = -INFINITY;
@@ -869,92 +880,103 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
           p.o[(orow + h0 + h) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(den != 0.f ? num / den : 0.f));
         else
           ph[d] = num;
-        if (d == 0 && !p.whole && (n_parts > 1 || lt0 == 0)) {
-          ph[D] = M;
-          ph[D + 1] = den;
-          ph[D + 2] = __int_as_float(c_first);
-          ph[D + 3] = __int_as_float(n_parts);
-        }
+        if (d == 0 && n_parts > 1) *reinterpret_cast<float2*>(ph + D) = make_float2(M, den);
       }
     }
   }
+  if (!p.whole && !p.merge_units && tid == 0) *job_of(p, blockIdx.x) = job;
   // copies still in flight (after a wait that ran out) land before the CTA ends
-#pragma unroll
+#pragma unroll 1
   for (int b = 0; b < 2 * kStages; ++b)
     if ((pending >> b) & 1u) wait(b);
   __syncthreads();
 }
 
 // Merge of the units whose tiles were split over CTAs, launched as the decode's programmatic
-// dependent. A CTA takes one unit's head, and of its output kDims dims: its warps are groups of
-// 32 dims times parts i, i + groups, ..., up to kMergeNB of which a warp loads at once. Few
-// units have many parts each (up to one per SM): 32 dims a CTA, eight groups of parts, one round
-// of loads. Many units have few parts: all D dims a CTA, fewer CTAs.
-constexpr int kMergeWarps = 8;
-constexpr int kMergeNB = 20;
-template <int D, int G, int kDims>
-__global__ void __launch_bounds__(kMergeWarps * 32) decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p) {
-  constexpr int PS = Cfg<D, G>::PS, DC = D / kDims, WD = kDims / 32, NG = kMergeWarps / WD;
-  const int dc = blockIdx.x % DC, h = blockIdx.x / DC % G, u = blockIdx.x / (DC * G);
+// dependent. Two shapes:
+//   kWide: few units, with up to one part per SM each. A CTA takes 32 dims of one unit's head;
+//          four warps take every fourth part, up to 20 of them in flight each.
+//   else:  many units, few parts each. A CTA takes the unit that CTA blockIdx.x of the decode has
+//          begun and not ended, all its heads; the warps of a head take the parts in turn.
+template <int D, int G, bool kWide>
+__global__ void __launch_bounds__(kWide ? 128 : 256) decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p) {
+  constexpr int PS = Cfg<D, G>::PS, V = kWide ? 1 : D / 32;  // dims per lane
+  constexpr int NW = kWide ? 4 : 8, NG = kWide ? 4 : 8 / G;  // warps, and those of one head
+  constexpr int NB = kWide ? 20 : 4;                         // parts in flight per warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int grp = warp / WD, wd = warp % WD;
-  __shared__ float s_o[kMergeWarps][32], s_m[kMergeWarps], s_l[kMergeWarps];
+  const int grp = kWide ? warp : warp / G;
+  const int h = kWide ? blockIdx.x / (D / 32) % G : warp % G;
+  const int d = kWide ? blockIdx.x % (D / 32) * 32 + lane : lane * V;
+  const int key = kWide ? blockIdx.x / (D / 32 * G) : blockIdx.x;
+  __shared__ float s_o[NW][32 * V], s_m[NW], s_l[NW];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float* head = p.partials + ((int64_t)u * G + h) * PS;
-  const int n_parts = __float_as_int(__ldcg(head + D + 3));
+  const int2 job = __ldcg(job_of(p, key));
+  const int u = kWide ? key : job.x, c = kWide ? job.x : key, n_parts = job.y;
   if (n_parts <= 1) return;
-  const int c_first = __float_as_int(__ldcg(head + D + 2));
-  const float* cont = p.partials + ((int64_t)(p.U_r + p.U_s + c_first) * G + h) * PS;  // part i >= 1: i G PS further
-  const int d = dc * kDims + wd * 32 + lane;
-  float acc = 0.f, M = -INFINITY, den = 0.f;
-  for (int i0 = grp; i0 < n_parts; i0 += NG * kMergeNB) {
-    float mb[kMergeNB], lb[kMergeNB], ob[kMergeNB];
+  const float* cont = p.partials + ((int64_t)2 * c * G + h) * PS;  // part i >= 1: 2 i G PS further
+  const float* head = cont + G * PS;
+  float acc[V], M = -INFINITY, den = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMergeNB; ++i) {
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int i0 = grp; i0 < n_parts; i0 += NG * NB) {
+    float mb[NB], lb[NB], ob[NB][V];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
       const int k = i0 + i * NG;
-      const float* r = k == 0 ? head : cont + (int64_t)k * G * PS;
+      const float* r = k == 0 ? head : cont + (int64_t)2 * k * G * PS;
       mb[i] = -INFINITY;
-      lb[i] = ob[i] = 0.f;
+      lb[i] = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) ob[i][v] = 0.f;
       if (k < n_parts) {
         mb[i] = __ldcg(r + D);
         lb[i] = __ldcg(r + D + 1);
-        ob[i] = __ldcg(r + d);
+#pragma unroll
+        for (int v = 0; v < V; ++v) ob[i][v] = __ldcg(r + d + v);
       }
     }
     float mn = M;
 #pragma unroll
-    for (int i = 0; i < kMergeNB; ++i) mn = fmaxf(mn, mb[i]);
+    for (int i = 0; i < NB; ++i) mn = fmaxf(mn, mb[i]);
     const float fo = M == -INFINITY && !(den != 0.f) ? 0.f : ex2_approx(M - mn);
     den *= fo;
-    acc *= fo;
 #pragma unroll
-    for (int i = 0; i < kMergeNB; ++i) {
+    for (int v = 0; v < V; ++v) acc[v] *= fo;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
       const float f = mb[i] == -INFINITY && !(lb[i] != 0.f) ? 0.f : ex2_approx(mb[i] - mn);
       den = fmaf(f, lb[i], den);
-      acc = fmaf(f, ob[i], acc);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, ob[i][v], acc[v]);
     }
     M = mn;
   }
-  s_o[warp][lane] = acc;
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
   if (lane == 0) s_m[warp] = M, s_l[warp] = den;
   __syncthreads();
   if (grp == 0) {
-    float T = -INFINITY, num = 0.f, sum = 0.f;
+    constexpr int STEP = kWide ? 1 : G;  // warps between those of a head
+    float T = -INFINITY, num[V], sum = 0.f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) T = fmaxf(T, s_m[g * WD + wd]);
+    for (int v = 0; v < V; ++v) num[v] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) T = fmaxf(T, s_m[g * STEP + warp]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int w = g * WD + wd;
+      const int w = g * STEP + warp;
       const float f = s_m[w] == -INFINITY && !(s_l[w] != 0.f) ? 0.f : ex2_approx(s_m[w] - T);
-      num = fmaf(f, s_o[w][lane], num);
       sum = fmaf(f, s_l[w], sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v) num[v] = fmaf(f, s_o[w][lane * V + v], num[v]);
     }
     const bool streaming = u >= p.U_r;
     const int us = streaming ? u - p.U_r : u, nk = streaming ? p.sh.n_str : p.sh.n_ret;
     const int b = us / nk;
     const int kvh = streaming ? p.heads.str_head[us - b * nk] : p.heads.ret_head[us - b * nk];
-    p.o[((int64_t)b * p.sh.Hq + (int64_t)kvh * G + h) * D + d] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(sum != 0.f ? num / sum : 0.f));
+    uint16_t* out = p.o + ((int64_t)b * p.sh.Hq + (int64_t)kvh * G + h) * D + d;
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = __bfloat16_as_ushort(__float2bfloat16_rn(sum != 0.f ? num[v] / sum : 0.f));
   }
 }
 
@@ -985,13 +1007,11 @@ cudaError_t launch_t(const Kv8DecodeParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, decode_kv8_kernel<D, G, CODE>, p);
   if (e != cudaSuccess || p.whole) return e;
-  const int64_t U = (int64_t)p.U_r + p.U_s;
-  const bool wide = p.C > 16 * U;  // more parts a unit than a CTA of all dims loads at once
-  cfg.gridDim = dim3((unsigned)(U * G * (wide ? D / 32 : 1)));
-  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return wide ? cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G, 32>, p)
-              : cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G, D>, p);
+  cfg.gridDim = dim3((unsigned)(p.merge_units ? (p.U_r + p.U_s) * G * (D / 32) : p.C));
+  cfg.blockDim = dim3(p.merge_units ? 128 : 256);
+  return p.merge_units ? cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G, true>, p)
+                       : cudaLaunchKernelEx(&cfg, decode_kv8_merge_kernel<D, G, false>, p);
 }
 
 template <int D, int CODE>
@@ -1016,6 +1036,8 @@ void plan_decode_kv8(Kv8DecodeParams* p, int num_sms) {
   p->whole = U <= num_sms && (p->U_r == 0 || p->tiles_r <= kShortTiles) && (p->U_s == 0 || p->tiles_s <= kShortTiles);
   const int64_t most = (p->line_r + p->line_s) / 2;  // two places each at least
   p->C = (int)(p->whole ? U : (most < num_sms ? most : num_sms));
+  // merge by unit, 32 dims a CTA, where that is no more than a CTA per SM
+  p->merge_units = U <= p->C && U * p->sh.g * (p->sh.D / 32) <= num_sms;
 }
 
 cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, cudaStream_t stream) {

@@ -918,7 +918,8 @@ static duo_status decode_kv8_impl(duo_handle* h, const duo_kv_cache* c, const du
   if (reinterpret_cast<uintptr_t>(seq_lens) & 3u) return fail(DUO_ERR_INVALID_ARG, "seq_lens not 4-byte aligned");
   if (!q || !o || !aligned16(q) || !aligned16(o))
     return fail(DUO_ERR_INVALID_ARG, "q / o NULL or not 16-byte aligned");
-  const size_t need = decode_workspace_bytes(sh, h->num_sms);
+  // two parts per CTA and the merge's jobs: within the size every decode entry point asks for
+  const size_t need = decode_workspace_bytes(sh, h->num_sms * kDecodeCtasPerSmKv4);
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(DUO_ERR_INVALID_ARG, "workspace not 256-byte aligned");
   if (!workspace || ws_bytes < need)

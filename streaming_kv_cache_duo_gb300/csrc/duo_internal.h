@@ -289,12 +289,14 @@ struct Kv8DecodeParams {
   int U_r, U_s;             // units (one per (sequence, KV head)) of each kind
   int C;                    // CTAs
   int whole;                // 1: CTA c takes unit c, no unit is split
+  int merge_units;          // merge jobs are by unit, not by CTA
   int tiles_r, tiles_s;     // tiles of a unit of each kind at n tokens
   int64_t line_r, line_s;   // places that all units of each kind take on the line of tiles
   int code_type;
   int64_t cap64;
   float scale_log2;  // log2(e) / sqrt(D)
-  float* partials;   // [U_r + U_s + C][g][D + 4]: first parts by unit, then one continuation per CTA
+  float* partials;   // [C][2][g][D + 4]: per CTA the part that goes on with a unit, and the one that
+                     // begins one; then the merge's jobs, int2 [C]
   Shape sh;
   HeadTable heads;
   PagedLayout pg;
