@@ -7,13 +7,13 @@
 // Until then its rows wait in bf16 in the tail. So the cache does not depend on how the
 // tokens were split into calls, and nothing stored is ever rounded again.
 //
-// Work: grid (chunk of consecutive tokens, retrieval plane x {K, V}, then one row of CTAs
-// for the ring). The CTA that holds the token completing a block does that block: rows of
-// this call from the packed input, earlier ones from the tail. The rows of the block left
-// open are written by the CTA of the sequence's last token, except when an earlier block of
-// this call reads the tail rows they replace: then by the CTA that read them, after it.
-// One pass: the block sits in registers (16 KB over 256 threads) between the maximum and
-// the codes. HBM-bound for prompts: 2 D bytes in, D out per row.
+// Work: grid (chunk of consecutive tokens, one row of CTAs for the ring, then retrieval plane);
+// half of a CTA's threads do K, half V. The CTA that holds the token completing a block does
+// that block: rows of this call from the packed input, earlier ones from the tail. The rows of
+// the block left open are written by the CTA of the sequence's last token, except when an
+// earlier block of this call reads the tail rows they replace: then by the CTA that read them,
+// after it. One pass: the block sits in registers (16 KB over 128 threads) between the maximum
+// and the codes. HBM-bound for prompts: 2 D bytes in, D out per row.
 #include "duo_device.cuh"
 
 namespace duo {
@@ -22,20 +22,73 @@ namespace {
 __device__ unsigned int g_append_kv8_err;
 
 constexpr int kThreads = 256;
+constexpr int kHalf = kThreads / 2;  // threads of K, and of V
 constexpr int kBlk = kKv8Block;
 
-// Two codes of one byte each from two values over the block's scale.
+// Codes of values over their block's scale, rounded from the fp32 quotient x / scale. A division
+// per value costs more than all the rest (a 32K prompt took 93 us with it; HBM's share is 15 us),
+// so each value is rounded from two products instead, with 1 / scale made a little smaller and a
+// little larger: by 2^-21, where u = 2^-24 bounds the relative error of 1 / scale, of each product
+// and of the fp32 quotient itself. The quotient lies between them, and rounding to a code is
+// monotone: where both give the same code it is the quotient's. Where they do not (a border
+// between two codes is that near: about one value in 10^5) the division is done, as it is for
+// scales so small that their reciprocal could overflow.
+constexpr float kTinyScale = 1e-30f;
+struct Inverse {
+  float lo, hi;
+};
+__device__ __forceinline__ Inverse inverse_of(float scale) {
+  const float r = 1.f / scale;
+  return Inverse{r * (1.f - 4.76837158203125e-7f), r * (1.f + 4.76837158203125e-7f)};
+}
+
+// Codes of eight values (two per word of w). The low byte of 1.5 2^23 + v, an fp32 sum rounded to
+// nearest even, is the integer nearest to v (|v| <= 127).
+__device__ __forceinline__ uint32_t pack_bytes(const float (&v)[4]) {
+  const uint32_t a = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040);
+  const uint32_t b = __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 template <int CODE>
-__device__ __forceinline__ uint32_t encode2(float a, float b) {
-  if constexpr (CODE == kKv8E4m3) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
-  } else {
-    const int ia = max(-127, min(127, __float2int_rn(a)));
-    const int ib = max(-127, min(127, __float2int_rn(b)));
-    return (uint32_t)(ia & 0xFF) | ((uint32_t)(ib & 0xFF) << 8);
+__device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], float scale, const Inverse inv, bool tiny) {
+  uint32_t c[2];
+  uint32_t differ = 0;
+  constexpr float kRound = 12582912.f;  // 1.5 2^23
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float x[4] = {bf16lo(w[2 * h]), bf16hi(w[2 * h]), bf16lo(w[2 * h + 1]), bf16hi(w[2 * h + 1])};
+    if constexpr (CODE == kKv8E4m3) {
+      c[h] = e4m3x2(x[0] * inv.lo, x[1] * inv.lo) | (e4m3x2(x[2] * inv.lo, x[3] * inv.lo) << 16);
+      differ |= c[h] ^ (e4m3x2(x[0] * inv.hi, x[1] * inv.hi) | (e4m3x2(x[2] * inv.hi, x[3] * inv.hi) << 16));
+    } else {
+      float a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] = fmaf(x[k], inv.lo, kRound);
+        differ |= __float_as_uint(a[k]) ^ __float_as_uint(fmaf(x[k], inv.hi, kRound));
+      }
+      c[h] = pack_bytes(a);
+    }
   }
+  if (differ || tiny) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t v = w[2 * h + (k >> 1)];
+        q[k] = __fdiv_rn((k & 1) ? bf16hi(v) : bf16lo(v), scale);
+        if (CODE != kKv8E4m3) q[k] = fminf(fmaxf(q[k], -127.f), 127.f) + kRound;
+      }
+      c[h] = CODE == kKv8E4m3 ? e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16) : pack_bytes(q);
+    }
+  }
+  return make_uint2(c[0], c[1]);
 }
 
 // One token of the call: its sequence, position, and the packed index of its sequence's
@@ -87,27 +140,36 @@ __device__ __forceinline__ int64_t block_row(const Kv8AppendParams& p, const Tok
   return row >= 0 && row % kBlk == 0 && row + kBlk <= p.rows ? row : -1;
 }
 
+// tid: of the half. s_max: of the half, one word per warp.
 template <int D, int CODE>
-__device__ void complete_block(const Kv8AppendParams& p, const Token& t, int i, int r, const uint16_t* in,
-                               const uint16_t* tail, uint8_t* codes, float* scales, uint32_t* s_max) {
-  constexpr int VPR = D / 8;                       // 16-byte vectors per row
-  constexpr int NV = kBlk * VPR / kThreads;        // vectors per thread
-  const int64_t row0 = block_row(p, t, i, r);      // (the same for every thread)
+__device__ __forceinline__ void complete_block(const Kv8AppendParams& p, const Token& t, int i, int r, int tid,
+                                               const uint16_t* in, const uint16_t* tail, uint8_t* codes, float* scales,
+                                               uint32_t* s_max) {
+  constexpr int VPR = D / 8;                   // 16-byte vectors per row
+  constexpr int NV = kBlk * VPR / kHalf;       // vectors per thread
+  constexpr int RS = kHalf / VPR;              // rows between a thread's vectors
+  const int64_t row0 = block_row(p, t, i, r);  // (the same for every thread)
   if (row0 < 0) {
-    if (threadIdx.x == 0) atomicOr(&g_append_kv8_err, kErrBadBlock);
+    if (tid == 0) atomicOr(&g_append_kv8_err, kErrBadBlock);
     return;
   }
-  const int head = p.heads.ret_head[r];
+  // row `row` of the block is packed token first + row; before the call's first it is in the tail
+  const int first = i - (kBlk - 1), row_of = tid / VPR, v = tid % VPR;
+  const uint16_t* src = in + ((int64_t)(first + row_of) * p.sh.Hkv + p.heads.ret_head[r]) * D + v * 8;
+  const int64_t step = (int64_t)RS * p.sh.Hkv * D;
   uint4 x[NV];
-  uint32_t m = 0;
+  if (first >= t.first) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int e = threadIdx.x + k * kThreads;
-    const int row = e / VPR, v = e % VPR;
-    const int src = i - (kBlk - 1) + row;  // packed token of the row; before the call's first: in the tail
-    const uint16_t* a = src >= t.first ? in + ((int64_t)src * p.sh.Hkv + head) * D : tail + (int64_t)row * D;
-    x[k] = *reinterpret_cast<const uint4*>(a + v * 8);
+    for (int k = 0; k < NV; ++k) x[k] = __ldg(reinterpret_cast<const uint4*>(src + k * step));
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int row = row_of + k * RS;
+      x[k] = first + row >= t.first ? *reinterpret_cast<const uint4*>(src + k * step)
+                                    : *reinterpret_cast<const uint4*>(tail + row * D + v * 8);
+    }
   }
+  uint32_t m = 0;
   // |x| as 16-bit integers order as the values do; infinities and NaN come out on top
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -118,37 +180,37 @@ __device__ void complete_block(const Kv8AppendParams& p, const Token& t, int i, 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
   __syncthreads();  // the last block's readers are done with s_max
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = __vmaxu2(m, s_max[w]);
+  for (int w = 0; w < kHalf / 32; ++w) m = __vmaxu2(m, s_max[w]);
   m = max(m & 0xFFFFu, m >> 16);
   float scale = __fdiv_rn(__uint_as_float(m << 16), CODE == kKv8E4m3 ? 448.f : 127.f);
   const bool finite = m < 0x7F80u;
   if (!finite) scale = __uint_as_float(0x7FC00000u);
   const bool zero = !finite || scale == 0.f;
-  if (threadIdx.x == 0) scales[row0 / kBlk] = scale;
+  if (tid == 0) scales[row0 / kBlk] = scale;
+  uint8_t* dst = codes + row0 * D + tid * 8;
+  const Inverse inv = inverse_of(scale);
+  const bool tiny = scale < kTinyScale;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int e = threadIdx.x + k * kThreads;
     const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-    uint32_t c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c[j] = zero ? 0u : encode2<CODE>(__fdiv_rn(bf16lo(w[j]), scale), __fdiv_rn(bf16hi(w[j]), scale));
-    *reinterpret_cast<uint2*>(codes + row0 * D + (int64_t)e * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    const uint2 c = zero ? make_uint2(0, 0) : encode8<CODE>(w, scale, inv, tiny);
+    *reinterpret_cast<uint2*>(dst + k * (kHalf * 8)) = c;
   }
 }
 
 // The sequence's new rows of the block it leaves open, into the tail.
 template <int D>
-__device__ void write_tail(const Kv8AppendParams& p, const Token& t, int i, int r, const uint16_t* in, uint16_t* tail) {
+__device__ __forceinline__ void write_tail(const Kv8AppendParams& p, const Token& t, int i, int r, int tid,
+                                           const uint16_t* in, uint16_t* tail) {
   constexpr int VPR = D / 8;
   const int end = t.pos + (t.last - i) + 1;  // length after the call
   const int start = t.pos - (i - t.first);   // and before it
   const int lo = max(end / kBlk * kBlk, start);
   const int head = p.heads.ret_head[r];
-  for (int e = threadIdx.x; e < (end - lo) * VPR; e += kThreads) {
+  for (int e = tid; e < (end - lo) * VPR; e += kHalf) {
     const int pos = lo + e / VPR, v = e % VPR;
     const int64_t src = t.first + (pos - start);
     *reinterpret_cast<uint4*>(tail + (pos % kBlk) * D + v * 8) =
@@ -157,7 +219,7 @@ __device__ void write_tail(const Kv8AppendParams& p, const Token& t, int i, int 
 }
 
 template <int D, int CODE>
-__global__ void __launch_bounds__(kThreads) append_kv8_kernel(const Kv8AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kv8_kernel(const Kv8AppendParams p) {
   // as append_kernel: dependents may be scheduled now, and nothing is touched before the
   // grid before this one (a decode reading the tail or the ring) has ended
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -167,55 +229,75 @@ __global__ void __launch_bounds__(kThreads) append_kv8_kernel(const Kv8AppendPar
   const int n_ret = p.sh.n_ret;
   constexpr int VPR = D / 8;
 
-  if ((int)blockIdx.y == 2 * n_ret) {
-    // ring: the tokens a streaming head still holds after the call, as 16-byte vectors
+  // the ring's CTAs come first: the few with something to copy take longest
+  const bool ring = p.sh.n_str > 0 && blockIdx.y == 0;
+  // what there is to do, token by token: blocks completed and sequences' last tokens, or for
+  // the ring the tokens a streaming head still holds after the call
+  __shared__ Token s_tok[kBlk];
+  __shared__ uint32_t s_todo[kBlk / 32];
+  __shared__ uint32_t s_max[kThreads / 32];
+  __shared__ uint8_t s_list[kBlk];  // ring: the tokens in s_todo, one after the other
+  bool todo = false;
+  if (threadIdx.x < kBlk) {
+    const int i = i0 + (int)threadIdx.x;
+    if (i < i1) {
+      const Token t = token_at(p, i);
+      s_tok[threadIdx.x] = t;
+      const int left = t.last - i;  // tokens of the sequence behind this one
+      todo = t.ok && (ring ? t.pos < p.sh.S || left < p.sh.R : t.pos % kBlk == kBlk - 1 || left == 0);
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, todo);
+    if ((threadIdx.x & 31) == 0) s_todo[threadIdx.x >> 5] = m;
+  }
+  __syncthreads();
+  const uint64_t all = s_todo[0] | ((uint64_t)s_todo[1] << 32);
+  if (ring) {
+    if (todo) s_list[__popcll(all & (((uint64_t)1 << threadIdx.x) - 1))] = (uint8_t)threadIdx.x;
+    __syncthreads();
     const int n_str = p.sh.n_str;
     const int SR = p.sh.S + p.sh.R;
     const int per = n_str * VPR;
-    for (int e = threadIdx.x; e < (i1 - i0) * per; e += kThreads) {
-      const int i = i0 + e / per;
-      const Token t = token_at(p, i);
-      if (!t.ok) continue;
-      const int end = t.pos + (t.last - i) + 1;
-      if (t.pos >= p.sh.S && t.pos < end - p.sh.R) continue;
+    const int count = __popcll(all);
+    // (all vectors of the chunk side by side: token after token would wait for memory each time)
+#pragma unroll 4
+    for (int e = threadIdx.x; e < count * per; e += kThreads) {
+      const int k = s_list[e / per], f = e % per;
+      const Token t = s_tok[k];
       const int slot = t.pos < p.sh.S ? t.pos : p.sh.S + (t.pos - p.sh.S) % p.sh.R;
-      const int si = e % per / VPR, v = e % VPR;
-      const int64_t src = ((int64_t)i * p.sh.Hkv + p.heads.str_head[si]) * VPR + v;
+      const int si = f / VPR, v = f % VPR;
+      const int64_t src = ((int64_t)(i0 + k) * p.sh.Hkv + p.heads.str_head[si]) * VPR + v;
       const int64_t dst = (((int64_t)t.b * n_str + si) * SR + slot) * VPR + v;
       reinterpret_cast<uint4*>(p.k_sr)[dst] = __ldg(reinterpret_cast<const uint4*>(p.k_new) + src);
       reinterpret_cast<uint4*>(p.v_sr)[dst] = __ldg(reinterpret_cast<const uint4*>(p.v_new) + src);
-      if (si == 0 && v == 0) p.pos[(int64_t)t.b * SR + slot] = t.pos;
+      if (f == 0) p.pos[(int64_t)t.b * SR + slot] = t.pos;
     }
     return;
   }
 
-  const int r = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+  const int r = (int)blockIdx.y - (p.sh.n_str > 0);
+  const bool is_v = threadIdx.x >= kHalf;
+  const int tid = threadIdx.x % kHalf;
   const uint16_t* in = is_v ? p.v_new : p.k_new;
   uint16_t* tails = is_v ? p.v_tail : p.k_tail;
   uint8_t* codes = is_v ? p.v_codes : p.k_codes;
   float* scales = is_v ? p.v_scale : p.k_scale;
-  __shared__ Token s_tok[kBlk];
-  __shared__ uint32_t s_max[kThreads / 32];
-  if ((int)threadIdx.x < i1 - i0) s_tok[threadIdx.x] = token_at(p, i0 + threadIdx.x);
-  __syncthreads();
-  for (int i = i0; i < i1; ++i) {
+  for (uint64_t todo = all; todo; todo &= todo - 1) {
+    const int i = i0 + __ffsll((long long)todo) - 1;
     const Token t = s_tok[i - i0];
-    if (!t.ok) continue;
     const int row = t.pos % kBlk;
     const int end_row = (t.pos + (t.last - i)) % kBlk;  // row of the sequence's last token
     const int start = t.pos - (i - t.first);
     uint16_t* tail = tails + ((int64_t)t.b * n_ret + r) * kBlk * D;
     if (row == kBlk - 1) {
-      complete_block<D, CODE>(p, t, i, r, in, tail, codes, scales, s_max);
+      complete_block<D, CODE>(p, t, i, r, tid, in, tail, codes, scales, s_max + (is_v ? kHalf / 32 : 0));
       // the block took rows from the tail: the new open block's rows go there after it
       if (t.pos - (kBlk - 1) < start && end_row != kBlk - 1) {
         __syncthreads();
-        write_tail<D>(p, t, i, r, in, tail);
+        write_tail<D>(p, t, i, r, tid, in, tail);
       }
     } else if (i == t.last) {
       const int open = t.pos / kBlk * kBlk;  // first position of the open block
-      if (start % kBlk == 0 || start >= open) write_tail<D>(p, t, i, r, in, tail);
+      if (start % kBlk == 0 || start >= open) write_tail<D>(p, t, i, r, tid, in, tail);
     }
   }
 }
@@ -226,7 +308,7 @@ cudaError_t launch_t(const Kv8AppendParams& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.tokens + p.chunk - 1) / p.chunk), (unsigned)(2 * p.sh.n_ret + (p.sh.n_str > 0)));
+  cfg.gridDim = dim3((unsigned)((p.tokens + p.chunk - 1) / p.chunk), (unsigned)(p.sh.n_ret + (p.sh.n_str > 0)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;

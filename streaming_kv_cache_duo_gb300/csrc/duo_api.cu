@@ -834,7 +834,7 @@ static duo_status append_kv8_impl(duo_handle* h, duo_kv_cache* c, const duo_page
   p.tokens = (int)tokens;
   // Tokens per CTA and plane: a block's 64 when there are enough for several CTAs per SM,
   // down to one token (64 sequences of one token on a CTA would take them in turn).
-  const int64_t per = tokens * (2 * sh.n_ret + (sh.n_str > 0)) / ((int64_t)h->num_sms * 8);
+  const int64_t per = tokens * (sh.n_ret + (sh.n_str > 0)) / ((int64_t)h->num_sms * 8);
   p.chunk = 1;
   while (p.chunk < kKv8Block && p.chunk * 2 <= per) p.chunk *= 2;
   p.code_type = kv->code_type;
