@@ -359,11 +359,12 @@ class DuoKv8Layer(DuoLayer):
                                       ptr(self.k_tail), ptr(self.v_tail),
                                       _lib.DUO_KV8_INT8 if code == "int8" else _lib.DUO_KV8_E4M3)
         self.paged = None
+        self.index = self.pos.get_device()
 
     def append(self, k_new, v_new, stream=None) -> None:
         T = k_new.shape[1]
-        _on(self.device, "k_new", k_new, (self.B, T, self.Hkv, self.D))
-        _on(self.device, "v_new", v_new, (self.B, T, self.Hkv, self.D))
+        _on(self, "k_new", k_new, (self.B, T, self.Hkv, self.D))
+        _on(self, "v_new", v_new, (self.B, T, self.Hkv, self.D))
         if self.paged is None:
             _lib.duo_kv_append_kv8(self.handle, self.cache, self.kv8, k_new, v_new, T, stream)
         else:
@@ -383,16 +384,18 @@ class DuoKv8Layer(DuoLayer):
         [B], <= max_len); a sequence of length 0 gets zeros."""
         out = self._out(q, (self.B, self.Hq, self.D), out)
         _check_lens(seq_lens, self.B)
+        if seq_lens.get_device() != self.index:
+            raise ValueError(f"seq_lens: on {seq_lens.device}, the layer is on CUDA device {self.index}")
         _lib.duo_attn_decode_kv8_varlen(self.handle, self.cache, self.paged, self.kv8, seq_lens, max_len, q, out,
                                         self.workspace, stream)
         return out
 
     def _out(self, q, shape, out):
         import torch
-        _on(self.device, "q", q, shape)
+        _on(self, "q", q, shape)
         if out is None:
             return torch.empty_like(q)
-        _on(self.device, "o", out, shape)
+        _on(self, "o", out, shape)
         return out
 
     def append_varlen(self, *args, **kwargs):
@@ -404,8 +407,8 @@ class DuoKv8Layer(DuoLayer):
             raise NotImplementedError("8-bit caches: prefill takes the heads of both kinds")
         T = q.shape[1]
         out = self._out(q, (self.B, T, self.Hq, self.D), out)
-        _on(self.device, "k", k, (self.B, T, self.Hkv, self.D))
-        _on(self.device, "v", v, (self.B, T, self.Hkv, self.D))
+        _on(self, "k", k, (self.B, T, self.Hkv, self.D))
+        _on(self, "v", v, (self.B, T, self.Hkv, self.D))
         if self.paged is None:
             _lib.duo_attn_prefill_kv8(self.handle, self.cache, self.kv8, q, k, v, T, out, stream)
         else:
@@ -446,8 +449,10 @@ class DuoKv8PagedLayer(DuoKv8Layer):
     def append_ragged(self, k_new, v_new, slot_map, stream=None) -> None:
         """A packed batch of tokens [num_tokens, Hkv, D], each at its own place (a DuoSlotMap)."""
         N = k_new.shape[0]
-        _on(self.device, "k_new", k_new, (N, self.Hkv, self.D))
-        _on(self.device, "v_new", v_new, (N, self.Hkv, self.D))
+        _on(self, "k_new", k_new, (N, self.Hkv, self.D))
+        _on(self, "v_new", v_new, (N, self.Hkv, self.D))
+        if slot_map.cu_new.get_device() != self.index:
+            raise ValueError(f"slot_map: on {slot_map.cu_new.device}, the layer is on CUDA device {self.index}")
         if slot_map.batch != self.B or slot_map.num_tokens != N or (self.n_ret and slot_map.planes != self.n_ret):
             raise ValueError(f"slot_map: of {slot_map.batch} sequences, {slot_map.num_tokens} tokens and "
                              f"{slot_map.planes} planes; need {self.B}, {N} and {self.n_ret}")
@@ -464,8 +469,8 @@ class DuoSlotMap:
         N = token_seq.shape[0]
         for name, t, dtype, dims in (("cu_new", cu_new, torch.int32, 1), ("token_seq", token_seq, torch.int32, 1),
                                      ("token_pos", token_pos, torch.int32, 1), ("slots", slots, torch.int64, 2)):
-            if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
-                raise ValueError(f"{name}: need a contiguous CUDA {dtype} tensor of {dims} dimension(s)")
+            if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != dims or t.device != cu_new.device:
+                raise ValueError(f"{name}: need a contiguous CUDA {dtype} tensor of {dims} dimension(s), all on one device")
         if token_pos.shape[0] != N or slots.shape[0] != N:
             raise ValueError("token_seq, token_pos and slots: different numbers of tokens")
         self.cu_new, self.token_seq, self.token_pos, self.slots = cu_new, token_seq, token_pos, slots
@@ -487,7 +492,8 @@ class DuoBlockPool:
         self.free_list = torch.arange(num_blocks, **i32)
         self.free_count = torch.full((1,), num_blocks, **i32)
         self.seq_lens = torch.zeros(batch, **i32)
-        self.max_tokens = max_tokens
+        self.batch, self.max_tokens = batch, max_tokens
+        self.index = self.seq_lens.get_device()
         self.slot_map = DuoSlotMap(torch.zeros(batch + 1, **i32), torch.full((max_tokens,), -1, **i32),
                                    torch.full((max_tokens,), -1, **i32),
                                    torch.full((max_tokens, planes), -1, dtype=torch.int64, device=self.device))
@@ -501,23 +507,25 @@ class DuoBlockPool:
         """Sequence b takes new_lens[b] more tokens (-1: it has finished; device int32 [B]).
         Updates tables, free list and lengths (into the *_out tensors if given) and returns
         the slot map of the packed tokens, whose arrays the next update overwrites."""
-        B = self.seq_lens.shape[0]
+        import torch
         lens = self.seq_lens if seq_lens_out is None else seq_lens_out
         count = self.free_count if free_count_out is None else free_count_out
-        for name, t, n in (("new_lens", new_lens, B), ("seq_lens_out", lens, B), ("free_count_out", count, 1)):
-            if str(t.dtype) != "torch.int32" or t.device != self.seq_lens.device or not t.is_contiguous() \
-                    or t.numel() != n:
-                raise ValueError(f"{name}: need a contiguous int32 tensor of {n} element(s) on {self.seq_lens.device}")
+        for name, t, n in (("new_lens", new_lens, self.batch), ("seq_lens_out", lens, self.batch),
+                           ("free_count_out", count, 1)):
+            if t.dtype != torch.int32 or t.get_device() != self.index or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{name}: need a contiguous int32 tensor of {n} element(s) on CUDA device {self.index}")
+        if torch.cuda.current_device() != self.index:
+            raise ValueError(f"the current device is not the pool's (CUDA device {self.index})")
         _lib.duo_block_tables_update(self.c, new_lens, self.max_tokens, lens, count, self.slot_map.c, self.workspace,
                                      stream)
         return self.slot_map
 
 
-def _on(device, name, t, shape):
+def _on(layer, name, t, shape):
     """_lib._bf16, and on the layer's own device."""
     _lib._bf16(t, shape, name)
-    if device.index is not None and t.device.index != device.index:
-        raise ValueError(f"{name}: on {t.device}, the layer is on {device}")
+    if t.get_device() != layer.index:
+        raise ValueError(f"{name}: on {t.device}, the layer is on CUDA device {layer.index}")
 
 
 def _check_mscale(mscale, shape):

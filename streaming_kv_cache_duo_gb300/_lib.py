@@ -189,20 +189,27 @@ def _check(status: int) -> None:
         raise DuoError(status, library().duo_last_error().decode())
 
 
-def _stream_ptr(stream) -> c_void_p:
+_raw_stream = None  # (device index) -> the current stream's handle, without a Stream object around it
+
+
+def _stream_ptr(stream) -> int:
+    global _raw_stream
     if stream is None:
         import torch
-        stream = torch.cuda.current_stream()
-    return c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        if _raw_stream is None:
+            torch.cuda.current_stream()  # initialises CUDA
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        return _raw_stream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ptr(t) -> c_void_p:
-    return c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _bf16(t, shape, name):
     import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.shape != tuple(shape):
         raise ValueError(f"{name}: need a contiguous CUDA bfloat16 tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 

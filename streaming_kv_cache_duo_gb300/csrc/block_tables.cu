@@ -9,11 +9,12 @@
 // avail - 1 - k of the free list, so every table entry and slot follows from the sums
 // without an atomic and the result does not depend on the order of threads.
 //
-// Latency-bound: a few KB of lengths in, 8 + 8 planes bytes a token out. One CTA of 1024
-// threads does the sums (each thread one sequence, warp shuffles, a carry between rounds
-// of 1024). A small step (kFuseWork outputs) is finished by the same CTA in the same
-// launch; larger ones by a second grid, launched as the first one's programmatic
-// dependent, in which each thread finds its sequence by bisecting the sums.
+// Latency-bound: a few KB of lengths in, 8 + 8 planes bytes a token out. One CTA does the sums
+// (each thread one sequence, warp shuffles, a carry between rounds), in shared memory for up
+// to kSmall sequences: the sums are bisected to find the sequence of an entry or a token, and
+// each step of that is a round trip to wherever they are. A small step (kFuseWork outputs) is
+// finished by the same CTA in the same launch; larger ones by a second grid, launched as the
+// first one's programmatic dependent.
 #include "duo_device.cuh"
 
 namespace duo {
@@ -21,7 +22,8 @@ namespace {
 
 __device__ unsigned int g_tables_err;
 
-constexpr int kScanThreads = 1024;
+constexpr int kScanThreads = 1024;  // at most
+constexpr int kSmall = 1024;        // sequences whose sums fit in shared memory
 // outputs (table entries and slots) up to which the scanning CTA writes them itself
 constexpr int64_t kFuseWork = 8192;
 
@@ -33,17 +35,20 @@ struct Scratch {
   int32_t* old_len;
   int32_t* need_base;
   int32_t* rel_base;
+  const int32_t* cu_new;  // (an output as well)
 };
-__device__ __forceinline__ Scratch scratch_of(const BlockTablesParams& p) {
+__device__ __forceinline__ Scratch scratch_at(int32_t* at, int B, const int32_t* cu_new) {
   Scratch s;
-  s.head = p.scratch;
-  s.old_len = p.scratch + 4;
-  s.need_base = s.old_len + p.B;
-  s.rel_base = s.need_base + p.B + 1;
+  s.head = at;
+  s.old_len = at + 4;
+  s.need_base = s.old_len + B;
+  s.rel_base = s.need_base + B + 1;
+  s.cu_new = cu_new;
   return s;
 }
 
-__device__ __forceinline__ int blocks_of(int64_t len, int bs) { return (int)((len + bs - 1) / bs); }
+// (len and bs are below 2^31)
+__device__ __forceinline__ int blocks_of(int64_t len, int bs) { return (int)(((uint32_t)len + bs - 1) / (uint32_t)bs); }
 
 // Largest i in [0, n) with base[i] <= v (base non-decreasing, base[0] = 0 <= v).
 __device__ __forceinline__ int bisect(const int32_t* base, int n, int v) {
@@ -58,12 +63,12 @@ __device__ __forceinline__ int bisect(const int32_t* base, int n, int v) {
   return lo;
 }
 
-// Inclusive sums of three values over the CTA's threads (tok saturates in 64 bits only).
+// Inclusive sums of three values over the CTA's threads; total: those of all of them.
 struct Sums {
   int64_t tok;
   int32_t need, rel;
 };
-__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums) {
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -75,8 +80,9 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums) {
   __syncthreads();  // the last round's readers are done with warp_sums
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
+  const int warps = blockDim.x >> 5;
   if (warp == 0) {
-    Sums w = warp_sums[lane];
+    Sums w = lane < warps ? warp_sums[lane] : Sums{0, 0, 0};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t t = __shfl_up_sync(0xffffffffu, w.tok, o);
@@ -91,6 +97,7 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums) {
     const Sums w = warp_sums[warp - 1];
     v.tok += w.tok, v.need += w.need, v.rel += w.rel;
   }
+  total = warp_sums[warps - 1];
   return v;
 }
 
@@ -109,15 +116,15 @@ __device__ void fill(const BlockTablesParams& p, const Scratch& s, int64_t first
   }
   const int64_t items = (int64_t)p.max_tokens * p.planes;
   for (int64_t it = first; it < items; it += step) {
-    const int i = (int)(it / p.planes);
+    const int i = (int)((it >> 32) ? it / p.planes : (uint32_t)it / (uint32_t)p.planes);
     const int pl = (int)(it - (int64_t)i * p.planes);
     int seq = -1, pos = -1;
     int64_t slot = -1;
     if (i < tokens) {
-      seq = bisect(p.cu_new, p.B, i);
+      seq = bisect(s.cu_new, p.B, i);
       const int old = s.old_len[seq];
       if (old >= 0) {
-        pos = old + (i - p.cu_new[seq]);
+        pos = old + (i - s.cu_new[seq]);
         const int have = blocks_of(old, p.bs);
         const int j = pos / p.bs;
         int id;
@@ -146,15 +153,18 @@ __global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const B
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Sums warp_sums[32];
   __shared__ int s_handed;
-  const Scratch s = scratch_of(p);
-  const int tid = threadIdx.x;
+  __shared__ int32_t s_sums[4 + 3 * kSmall + 2], s_cu[kSmall + 1];
+  const bool small = p.B <= kSmall;
+  const Scratch s = scratch_at(small ? s_sums : p.scratch, p.B, small ? s_cu : p.cu_new);
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int64_t cap = (int64_t)p.max_blocks * p.bs;
   uint32_t err = 0;
+  int count = *p.free_count;
 
   // the sums: tokens, blocks needed, blocks given back
   int64_t c_tok = 0;
   int32_t c_need = 0, c_rel = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += threads) {
     const int b = b0 + tid;
     Sums v{0, 0, 0};
     int len = 0, nw = 0, kind = 2;  // 0 takes tokens, 1 finished, 2 turned down
@@ -173,33 +183,39 @@ __global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const B
       if (kind == 0) v.need = p.planes * (blocks_of(len + (int64_t)nw, p.bs) - blocks_of(len, p.bs));
       if (kind == 1) v.rel = p.planes * blocks_of(len, p.bs);
     }
+    Sums total;
+    Sums u = block_scan(v, warp_sums, total);
     // a sequence whose tokens pass the packed batch is turned down before it asks for blocks
-    Sums t = block_scan(Sums{v.tok, 0, 0}, warp_sums);
-    const int64_t tok_end = c_tok + t.tok, tok_begin = tok_end - v.tok;
-    if (kind == 0 && nw > 0 && tok_end > p.max_tokens) {
-      kind = 2;
-      v.need = 0;
-      err |= kErrPoolFull;
+    const bool past = kind == 0 && nw > 0 && c_tok + u.tok > p.max_tokens;
+    if (__syncthreads_or(past)) {
+      if (past) {
+        kind = 2;
+        v.need = 0;
+        err |= kErrPoolFull;
+      }
+      u = block_scan(v, warp_sums, total);
     }
-    const Sums u = block_scan(Sums{v.tok, v.need, v.rel}, warp_sums);
     if (b < p.B) {
-      p.cu_new[b] = (int)(tok_begin < 0x7fffffff ? tok_begin : 0x7fffffff);
+      const int64_t begin = c_tok + u.tok - v.tok;
+      const int cu = (int)(begin < 0x7fffffff ? begin : 0x7fffffff);
+      p.cu_new[b] = cu;
+      if (small) s_cu[b] = cu;
       s.need_base[b] = c_need + u.need - v.need;
       s.rel_base[b] = c_rel + u.rel - v.rel;
       s.old_len[b] = kind == 0 ? len : (kind == 1 ? -2 - len : -1);
     }
-    const Sums last = warp_sums[31];
-    c_tok += last.tok;
-    c_need += last.need;
-    c_rel += last.rel;
+    c_tok += total.tok;
+    c_need += total.need;
+    c_rel += total.rel;
   }
   if (tid == 0) {
-    p.cu_new[p.B] = (int)(c_tok < 0x7fffffff ? c_tok : 0x7fffffff);
+    const int cu = (int)(c_tok < 0x7fffffff ? c_tok : 0x7fffffff);
+    p.cu_new[p.B] = cu;
+    if (small) s_cu[p.B] = cu;
     s.need_base[p.B] = c_need;
     s.rel_base[p.B] = c_rel;
     s_handed = 0;
   }
-  int count = *p.free_count;
   if (count < 0 || count > p.num_blocks) {
     err |= kErrBadLength;
     count = count < 0 ? 0 : (int)p.num_blocks;
@@ -208,7 +224,7 @@ __global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const B
 
   // returned blocks, in order, dropping ids that are none
   int avail = count;
-  for (int e0 = 0; e0 < c_rel; e0 += kScanThreads) {
+  for (int e0 = 0; e0 < c_rel; e0 += threads) {
     const int e = e0 + tid;
     int id = -1;
     if (e < c_rel) {
@@ -221,16 +237,17 @@ __global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const B
         id = -1;
       }
     }
-    const Sums u = block_scan(Sums{0, id >= 0, 0}, warp_sums);
+    Sums total;
+    const Sums u = block_scan(Sums{0, id >= 0, 0}, warp_sums, total);
     const int64_t at = (int64_t)avail + u.need - 1;
     if (id >= 0 && at < p.num_blocks) p.free_list[at] = id;
-    const int64_t next = (int64_t)avail + warp_sums[31].need;
+    const int64_t next = (int64_t)avail + total.need;
     if (next > p.num_blocks) err |= kErrBadBlock;  // more blocks than the pool has: one came back twice
     avail = (int)(next < p.num_blocks ? next : p.num_blocks);
   }
 
   // who is served
-  for (int b = tid; b < p.B; b += kScanThreads) {
+  for (int b = tid; b < p.B; b += threads) {
     const int old = s.old_len[b];
     const int end = s.need_base[b + 1];
     const bool asks = end > s.need_base[b];
@@ -258,13 +275,16 @@ __global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const B
   if (err) atomicOr(&g_tables_err, err);
   if (fuse) {
     __syncthreads();
-    fill(p, s, tid, kScanThreads);
+    fill(p, s, tid, threads);
+  } else if (small) {  // for the second grid
+    __syncthreads();
+    for (int i = tid; i < 4 + 2 * p.B + 1; i += threads) p.scratch[i] = s_sums[i];
   }
 }
 
 __global__ void __launch_bounds__(256) block_tables_fill_kernel(const BlockTablesParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  fill(p, scratch_of(p), (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+  fill(p, scratch_at(p.scratch, p.B, p.cu_new), (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 }  // namespace
@@ -276,7 +296,10 @@ cudaError_t launch_block_tables(const BlockTablesParams& p, int num_sms, cudaStr
   // beside the full ones
   const int64_t work = (int64_t)p.max_tokens * p.planes + (int64_t)p.B * p.planes;
   const bool fuse = work <= kFuseWork;
-  block_tables_scan_kernel<<<1, kScanThreads, 0, stream>>>(p, fuse ? 1 : 0);
+  // threads: one per sequence, and in a fused step one per output, as far as they go
+  const int64_t want = fuse && work > p.B ? work : p.B;
+  const int threads = want >= kScanThreads ? kScanThreads : (want <= 128 ? 128 : (int)((want + 31) / 32 * 32));
+  block_tables_scan_kernel<<<1, threads, 0, stream>>>(p, fuse ? 1 : 0);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || fuse) return e;
   int64_t blocks = (work + 255) / 256;
