@@ -411,14 +411,22 @@ duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* ca
                                       const duo_kv8_cache* kv8, const int32_t* seq_lens, int64_t max_len,
                                       const void* q, void* o, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Prefill of T new tokens against 8-bit caches, as duo_attn_prefill: cache rows are
+/* Prefill of T new tokens against 8-bit caches, as duo_attn_prefill: the cache's rows are
  * code * scale in fp32 rounded to bf16 (tail and ring rows are bf16 already), the T new
- * tokens' k and v the bf16 inputs. Append the chunk afterwards. */
+ * tokens' k and v the bf16 inputs. Append the chunk afterwards. The rows are written as bf16
+ * to `workspace` once and read from there by every query block; retrieval heads with few
+ * query blocks are split over their keys, their parts merged by log-sum-exp. workspace:
+ * device memory of duo_prefill_kv8_workspace_size(handle, cache->n, T) bytes, 256-byte
+ * aligned (may be NULL if that is 0: nothing cached, or no retrieval head): 4 D bytes per
+ * cached token and retrieval head of the layer, plus the parts. Nothing in it survives the
+ * call; calls sharing one must be ordered on the GPU. */
+size_t duo_prefill_kv8_workspace_size(const duo_handle* handle, int64_t n, int32_t T);
 duo_status duo_attn_prefill_kv8(duo_handle* handle, const duo_kv_cache* cache, const duo_kv8_cache* kv8,
-                                const void* q, const void* k, const void* v, int32_t T, void* o, void* stream);
+                                const void* q, const void* k, const void* v, int32_t T, void* o, void* workspace,
+                                size_t workspace_bytes, void* stream);
 duo_status duo_attn_prefill_kv8_paged(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
                                       const duo_kv8_cache* kv8, const void* q, const void* k, const void* v,
-                                      int32_t T, void* o, void* stream);
+                                      int32_t T, void* o, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Block tables kept on the device. A pool of num_blocks blocks of block_size tokens serves
  * B sequences with `planes` tables each (planes = n_ret: one per retrieval head).

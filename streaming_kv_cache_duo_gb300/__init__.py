@@ -402,17 +402,27 @@ class DuoKv8Layer(DuoLayer):
         raise NotImplementedError("8-bit caches: append_ragged (a paged layer) takes lengths from the device")
 
     def prefill(self, q, k, v, out=None, kind_mask=3, stream=None):
-        """A chunk of T new tokens against the 8-bit caches (dequantized in the kernel)."""
+        """A chunk of T new tokens against the 8-bit caches. Their rows are written as bf16 to a
+        workspace first (4 D bytes per cached token and retrieval head), taken from torch's
+        allocator on the stream the call runs on."""
+        import torch
         if kind_mask != 3:
             raise NotImplementedError("8-bit caches: prefill takes the heads of both kinds")
         T = q.shape[1]
         out = self._out(q, (self.B, T, self.Hq, self.D), out)
         _on(self, "k", k, (self.B, T, self.Hkv, self.D))
         _on(self, "v", v, (self.B, T, self.Hkv, self.D))
+        need = _lib.duo_prefill_kv8_workspace_size(self.handle, self.n, T)
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:  # its memory may be given out again as soon as this returns: in that stream's order
+            handle = _lib._stream_ptr(stream)
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=q.device)):
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         if self.paged is None:
-            _lib.duo_attn_prefill_kv8(self.handle, self.cache, self.kv8, q, k, v, T, out, stream)
+            _lib.duo_attn_prefill_kv8(self.handle, self.cache, self.kv8, q, k, v, T, out, ws, stream)
         else:
-            _lib.duo_attn_prefill_kv8_paged(self.handle, self.cache, self.paged, self.kv8, q, k, v, T, out, stream)
+            _lib.duo_attn_prefill_kv8_paged(self.handle, self.cache, self.paged, self.kv8, q, k, v, T, out, ws, stream)
         return out
 
     def dca_prefill(self, *args, **kwargs):

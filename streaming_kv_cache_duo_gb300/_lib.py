@@ -39,7 +39,7 @@ EXPORTS = (
     "duo_attn_decode_kv4", "duo_kv_append_kv4_paged", "duo_attn_decode_kv4_paged", "duo_attn_prefill_kv4",
     "duo_kv_append_kv8", "duo_kv_append_kv8_paged", "duo_kv_append_kv8_ragged", "duo_attn_decode_kv8",
     "duo_attn_decode_kv8_paged", "duo_attn_decode_kv8_varlen", "duo_attn_prefill_kv8",
-    "duo_attn_prefill_kv8_paged", "duo_block_tables_workspace_size",
+    "duo_attn_prefill_kv8_paged", "duo_prefill_kv8_workspace_size", "duo_block_tables_workspace_size",
     "duo_block_tables_update", "duo_kv_append_varlen", "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait",
     "duo_last_error", "duo_status_string",
 )
@@ -152,11 +152,12 @@ def library() -> ctypes.CDLL:
         "duo_attn_decode_kv8_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
                                                  POINTER(duo_kv8_cache), c_void_p, c_int64, c_void_p, c_void_p,
                                                  c_void_p, c_size_t, c_void_p]),
+        "duo_prefill_kv8_workspace_size": (c_size_t, [c_void_p, c_int64, c_int32]),
         "duo_attn_prefill_kv8": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_kv8_cache), c_void_p,
-                                           c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
+                                           c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
         "duo_attn_prefill_kv8_paged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged),
                                                  POINTER(duo_kv8_cache), c_void_p, c_void_p, c_void_p, c_int32,
-                                                 c_void_p, c_void_p]),
+                                                 c_void_p, c_void_p, c_size_t, c_void_p]),
         "duo_block_tables_workspace_size": (c_size_t, [c_int32]),
         "duo_block_tables_update": (c_int32, [POINTER(duo_block_pool), c_void_p, c_int32, c_void_p, c_void_p,
                                               POINTER(duo_slot_map), c_void_p, c_size_t, c_void_p]),
@@ -372,16 +373,20 @@ def duo_attn_decode_kv8_varlen(handle, cache: "duo_kv_cache", paged, kv8: "duo_k
                                                 _stream_ptr(stream)))
 
 
-def duo_attn_prefill_kv8(handle, cache: "duo_kv_cache", kv8: "duo_kv8_cache", q, k, v, T: int, o,
+def duo_prefill_kv8_workspace_size(handle, n: int, T: int) -> int:
+    return int(library().duo_prefill_kv8_workspace_size(handle, n, T))
+
+
+def duo_attn_prefill_kv8(handle, cache: "duo_kv_cache", kv8: "duo_kv8_cache", q, k, v, T: int, o, workspace,
                          stream=None) -> None:
     _check(library().duo_attn_prefill_kv8(handle, _ref(cache), _ref(kv8), _ptr(q), _ptr(k), _ptr(v), T, _ptr(o),
-                                          _stream_ptr(stream)))
+                                          _ptr(workspace), _nbytes(workspace), _stream_ptr(stream)))
 
 
 def duo_attn_prefill_kv8_paged(handle, cache: "duo_kv_cache", paged: "duo_paged", kv8: "duo_kv8_cache", q, k, v,
-                               T: int, o, stream=None) -> None:
+                               T: int, o, workspace, stream=None) -> None:
     _check(library().duo_attn_prefill_kv8_paged(handle, _ref(cache), _ref(paged), _ref(kv8), _ptr(q), _ptr(k), _ptr(v),
-                                                T, _ptr(o), _stream_ptr(stream)))
+                                                T, _ptr(o), _ptr(workspace), _nbytes(workspace), _stream_ptr(stream)))
 
 
 def duo_block_tables_workspace_size(batch: int) -> int:

@@ -417,9 +417,44 @@ static duo_status check_kv8(const duo_handle* h, const duo_kv_cache* c, const du
   return check_cache(h, c, false, true);
 }
 
+// Prefill over an 8-bit cache of n tokens: its rows as bf16 (K planes, V planes), and the parts of
+// retrieval items split over their key tiles.
+struct Kv8Prefill {
+  int64_t plane_rows;
+  int splits;
+  int64_t parts;   // items x splits, if splits > 1
+  size_t part_at;  // byte offset of the parts in the workspace
+  size_t bytes;    // 0: no cached rows to read
+};
+static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
+  const Shape& sh = h->sh;
+  Kv8Prefill w{pitch64(n), 1, 0, 0, 0};
+  if (n < 1 || T < 1 || sh.n_ret == 0) return w;
+  w.part_at = ((size_t)2 * sh.B * sh.n_ret * w.plane_rows * sh.D * 2 + 255) / 256 * 256;
+  // A CTA per item leaves SMs idle when there are few (a short turn after a long conversation:
+  // 333 tokens after 9001 for two sequences and four heads are 64 items of 73 tiles, 158 us; in
+  // two splits 98 us). Splits that shorten the longest SM's row of tiles by a tenth at least, each
+  // item counted with three tiles' worth of start and merge.
+  const int64_t num_qt = (T + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta;
+  const int64_t items = (int64_t)sh.B * sh.n_ret * sh.g * num_qt;
+  const int64_t cached = (n + kPrefillBN - 1) / kPrefillBN, tiles = cached + num_qt + 1;
+  int64_t best = (items + h->num_sms - 1) / h->num_sms * (tiles + 3);
+  for (int s = 2; s <= kPrefillMaxSplits && s <= cached && items * s <= 8 * h->num_sms; ++s) {
+    const int64_t cost = (items * s + h->num_sms - 1) / h->num_sms * ((tiles + s - 1) / s + 3);
+    if (cost * 10 <= best * 9) {
+      best = cost;
+      w.splits = s;
+    }
+  }
+  if (w.splits > 1) w.parts = items * w.splits;
+  w.bytes = w.part_at + (size_t)w.parts * kPrefillRowsPerCta * (sh.D * sizeof(float) + sizeof(float2));
+  return w;
+}
+
 static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, const void* q,
                                const void* k, const void* v, int32_t T, void* o, int32_t kind_mask, void* stream,
-                               const duo_kv4_cache* kv4 = nullptr, const duo_kv8_cache* kv8 = nullptr) {
+                               const duo_kv4_cache* kv4 = nullptr, const duo_kv8_cache* kv8 = nullptr,
+                               void* workspace = nullptr, size_t ws_bytes = 0) {
   duo_status st = check_handle(h);
   if (st != DUO_OK) return st;
   if (!c) return fail(DUO_ERR_INVALID_ARG, "cache is NULL");
@@ -448,6 +483,8 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
   if ((st = encode_tokens(h, &p.tm_v, v, sh.B, T, sh.Hkv, sh.D)) != DUO_OK) return st;
   const int64_t SR = (int64_t)sh.S + sh.R;
   const int nvalid = (int)(c->n < SR ? c->n : SR);
+  Kv8ExpandParams expand;
+  expand.planes = 0;
   if (kv4) {  // cache tiles are dequantized in the kernel; no tensor maps over the caches
     if ((st = check_capacity(h, pg, c->n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
     p.k4 = static_cast<const uint8_t*>(kv4->k_codes);
@@ -461,17 +498,40 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
     p.cap16 = pitch16(sh.cap);
     p.sr16 = (int)pitch16(SR);
     p.kv4 = 1;
-  } else if (kv8) {  // likewise, but for the bf16 rings (below)
+  } else if (kv8) {  // the retrieval rows as bf16 in the workspace, then as a contiguous cache of them
     if (sh.n_ret > 0 && (st = check_capacity(h, pg, c->n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
-    p.k8 = static_cast<const uint8_t*>(kv8->k_codes);
-    p.v8 = static_cast<const uint8_t*>(kv8->v_codes);
-    p.k8_scale = kv8->k_scale;
-    p.v8_scale = kv8->v_scale;
-    p.k8_tail = static_cast<const uint16_t*>(kv8->k_tail);
-    p.v8_tail = static_cast<const uint16_t*>(kv8->v_tail);
-    p.cap64 = pitch64(sh.cap);
-    p.code_type = kv8->code_type;
-    p.kv8 = 1;
+    const Kv8Prefill plan = plan_prefill_kv8(h, c->n, T);
+    if (plan.bytes > 0) {
+      if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(DUO_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+      if (!workspace || ws_bytes < plan.bytes)
+        return fail(DUO_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.bytes, workspace ? ws_bytes : 0);
+      Kv8ExpandParams e;
+      e.k_codes = static_cast<const uint8_t*>(kv8->k_codes);
+      e.v_codes = static_cast<const uint8_t*>(kv8->v_codes);
+      e.k_scale = kv8->k_scale;
+      e.v_scale = kv8->v_scale;
+      e.k_tail = static_cast<const uint16_t*>(kv8->k_tail);
+      e.v_tail = static_cast<const uint16_t*>(kv8->v_tail);
+      e.k_out = static_cast<uint16_t*>(workspace);
+      e.v_out = e.k_out + plan.plane_rows * sh.B * sh.n_ret * sh.D;
+      e.n = (int)c->n;
+      e.planes = sh.B * sh.n_ret;
+      e.D = sh.D;
+      e.code_type = kv8->code_type;
+      e.cap64 = pitch64(sh.cap);
+      e.pg = pg;
+      const int64_t planes = e.planes;
+      if (planes * plan.plane_rows > 0x7fffffffLL)
+        return fail(DUO_ERR_UNSUPPORTED, "the cached rows of all sequences and retrieval heads reach 2^31");
+      if ((st = encode_cache(h, &p.tm_kfull, e.k_out, planes, plan.plane_rows, c->n, sh.D)) != DUO_OK) return st;
+      if ((st = encode_cache(h, &p.tm_vfull, e.v_out, planes, plan.plane_rows, c->n, sh.D)) != DUO_OK) return st;
+      p.splits = plan.splits;
+      p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_at);
+      p.part_ml = reinterpret_cast<float2*>(p.part_o + plan.parts * kPrefillRowsPerCta * sh.D);
+      expand = e;
+    }
+    pg = PagedLayout{nullptr, 0, 0, 0, nullptr};
   } else if (use_cache && (sh.n_ret > 0 || pg.stream_table)) {
     if ((st = check_capacity(h, pg, c->n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
     if (!is_paged(pg)) {
@@ -505,7 +565,7 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
   const int64_t ir = (kind_mask & 2) ? per_kind * sh.n_ret : 0;
   const int64_t is = (kind_mask & 1) ? per_kind * sh.n_str : 0;
   if (ir + is > 0x7fffffffLL) return fail(DUO_ERR_UNSUPPORTED, "too many query tiles for one launch");
-  p.items_r = (int)ir;
+  p.items_r = (int)ir * std::max(1, p.splits);  // (splits > 1 only with few items)
   p.items_s = (int)is;
   // about one wave of CTAs per KV head; at most num_qt, so qp_group x (items per block)
   // stays within the item count (an int)
@@ -513,7 +573,10 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)sh.D));
   p.sh = sh;
   p.heads = h->heads;
-  cudaError_t ce = launch_prefill(p, (cudaStream_t)stream);
+  cudaError_t ce = cudaSuccess;
+  if (expand.planes > 0 && (ce = launch_expand_kv8(expand, (cudaStream_t)stream)) != cudaSuccess)
+    return cuda_fail(ce, "8-bit cache expansion launch");
+  ce = launch_prefill(p, (cudaStream_t)stream);
   if (ce != cudaSuccess) return cuda_fail(ce, "prefill launch");
   return ok();
 }
@@ -874,18 +937,23 @@ duo_status duo_kv_append_kv8_ragged(duo_handle* h, duo_kv_cache* c, const duo_pa
   return append_kv8_impl(h, c, paged, kv8, map, k_new, v_new, num_tokens, stream);
 }
 
+size_t duo_prefill_kv8_workspace_size(const duo_handle* h, int64_t n, int32_t T) {
+  return h ? plan_prefill_kv8(h, n, T).bytes : 0;
+}
+
 duo_status duo_attn_prefill_kv8(duo_handle* h, const duo_kv_cache* c, const duo_kv8_cache* kv8, const void* q,
-                                const void* k, const void* v, int32_t T, void* o, void* stream) {
+                                const void* k, const void* v, int32_t T, void* o, void* workspace,
+                                size_t workspace_bytes, void* stream) {
   if (!kv8) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
-  return prefill_impl(h, c, nullptr, q, k, v, T, o, 3, stream, nullptr, kv8);
+  return prefill_impl(h, c, nullptr, q, k, v, T, o, 3, stream, nullptr, kv8, workspace, workspace_bytes);
 }
 
 duo_status duo_attn_prefill_kv8_paged(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged,
                                       const duo_kv8_cache* kv8, const void* q, const void* k, const void* v,
-                                      int32_t T, void* o, void* stream) {
+                                      int32_t T, void* o, void* workspace, size_t workspace_bytes, void* stream) {
   if (!paged) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
   if (!kv8) return fail(DUO_ERR_INVALID_ARG, "kv8 is NULL");
-  return prefill_impl(h, c, paged, q, k, v, T, o, 3, stream, nullptr, kv8);
+  return prefill_impl(h, c, paged, q, k, v, T, o, 3, stream, nullptr, kv8, workspace, workspace_bytes);
 }
 
 // 2-D map over codes [rows, D]: boxes of 32 rows, the swizzle of the row's width.
@@ -1103,7 +1171,7 @@ duo_status duo_device_error(uint32_t* code) {
   if (!code) return fail(DUO_ERR_INVALID_ARG, "code is NULL");
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, bt = 0;
+  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, e8 = 0, bt = 0;
   if ((e = prefill_read_clear_error(&a)) != cudaSuccess) return cuda_fail(e, "read prefill error word");
   if ((e = decode_read_clear_error(&b)) != cudaSuccess) return cuda_fail(e, "read decode error word");
   if ((e = selftest_read_clear_error(&t)) != cudaSuccess) return cuda_fail(e, "read self-test error word");
@@ -1111,7 +1179,8 @@ duo_status duo_device_error(uint32_t* code) {
   if ((e = decode_kv8_read_clear_error(&d8)) != cudaSuccess) return cuda_fail(e, "read 8-bit decode error word");
   if ((e = append_kv8_read_clear_error(&a8)) != cudaSuccess) return cuda_fail(e, "read 8-bit append error word");
   if ((e = block_tables_read_clear_error(&bt)) != cudaSuccess) return cuda_fail(e, "read block tables error word");
-  b |= d8;
+  if ((e = expand_kv8_read_clear_error(&e8)) != cudaSuccess) return cuda_fail(e, "read 8-bit expansion error word");
+  b |= d8 | e8;
   ap |= a8;
   *code = a | b | t | ap | bt;
   constexpr uint32_t kFull = kErrAppendCapacity | kErrPoolFull, kBad = kErrBadBlock | kErrBadLength;

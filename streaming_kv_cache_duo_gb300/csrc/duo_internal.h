@@ -170,6 +170,7 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 constexpr int kPrefillBM = 128;        // query rows per query tile
 constexpr int kPrefillBN = 128;        // keys per KV tile
 constexpr int kPrefillRowsPerCta = 256;  // two query tiles per CTA
+constexpr int kPrefillMaxSplits = 16;
 
 struct PrefillParams {
   CUtensorMap tm_q;      // 4-D over q [B, T, Hq, D], box 64 x 1 x 128 x 1, 128B swizzle
@@ -214,17 +215,11 @@ struct PrefillParams {
   int64_t cap16;
   int sr16;
   int kv4;
-  // 8-bit caches (kv8 != 0): the retrieval heads' cache tiles are dequantized the same way,
-  // their last rows copied from the bf16 tail; laid out as in Kv8DecodeParams
-  const uint8_t* k8;
-  const uint8_t* v8;
-  const float* k8_scale;
-  const float* v8_scale;
-  const uint16_t* k8_tail;
-  const uint16_t* v8_tail;
-  int64_t cap64;
-  int kv8;
-  int code_type;
+  // retrieval items split over their key tiles (splits > 1; contiguous caches): split s of item i
+  // leaves its unnormalised output (fp32 [256, D]) and (max, sum) rows at place i splits + s
+  int splits;
+  float* part_o;
+  float2* part_ml;
 };
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);
 
@@ -271,6 +266,23 @@ constexpr int kKv8Warps = KV8W, kKv8Stages = KV8S;
 constexpr int kKv8Rows = 32;                      // rows of codes a warp takes of a tile
 constexpr int kKv8TK = kKv8Warps * kKv8Rows;      // keys of a decode tile over codes
 constexpr int kKv8TKBf16 = kKv8Warps * 16;        // and over bf16 rows (ring or tail)
+
+struct Kv8ExpandParams {
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scale;
+  const float* v_scale;
+  const uint16_t* k_tail;
+  const uint16_t* v_tail;
+  uint16_t* k_out;  // bf16 [planes, n rounded up to 64, D]
+  uint16_t* v_out;
+  int n, planes, D;
+  int code_type;
+  int64_t cap64;
+  PagedLayout pg;
+};
+cudaError_t launch_expand_kv8(const Kv8ExpandParams& p, cudaStream_t stream);
+cudaError_t expand_kv8_read_clear_error(uint32_t* code);
 
 struct Kv8DecodeParams {
   CUtensorMap tm_k;  // 2-D over the codes [rows, D], box 32 x D, swizzled by the row width

@@ -65,18 +65,16 @@ constexpr int kModePaged = 1;  // retrieval caches in a paged pool (block table)
 constexpr int kModePool = 2;   // both head kinds in the paged pool
 constexpr int kModeDca = 3;    // Dual Chunk Attention: one of three query vectors per key tile
 constexpr int kModeKv4 = 4;    // 4-bit caches: cache tiles dequantized into shared memory by warps 10, 11
-constexpr int kModeKv8 = 5;    // 8-bit caches, contiguous or paged: likewise, and the bf16 tail's rows copied
-constexpr int kWarpDeq = 10;   // first of the dequantizing warps (4-bit and 8-bit caches): 10 ... 15
-// cache tiles of retrieval heads (4-bit: of both kinds) are dequantized by warps of the CTA
-__host__ __device__ constexpr bool is_deq_mode(int mode) { return mode == kModeKv4 || mode == kModeKv8; }
+constexpr int kModeSplit = 5;  // plain, each retrieval item's key tiles shared by several CTAs and merged after
+constexpr int kWarpDeq = 10;   // first of the dequantizing warps (4-bit caches): 10 ... 15
 template <int kMode>
 struct Roles {
-  static constexpr bool kDeq = is_deq_mode(kMode);
-  static constexpr int kThreads = kDeq ? 512 : 384;
-  static constexpr int kLaunchRegs = kDeq ? 128 : 168;
-  static constexpr int kRegsSoftmax = kDeq ? 184 : 200;
-  static constexpr int kRegsCtl = kDeq ? 72 : 104;
-  static constexpr int kDeqThreads = kThreads - kWarpDeq * 32;  // dequantizing instances: 192
+  static constexpr bool kKv4 = kMode == kModeKv4;
+  static constexpr int kThreads = kKv4 ? 512 : 384;
+  static constexpr int kLaunchRegs = kKv4 ? 128 : 168;
+  static constexpr int kRegsSoftmax = kKv4 ? 184 : 200;
+  static constexpr int kRegsCtl = kKv4 ? 72 : 104;
+  static constexpr int kDeqThreads = kThreads - kWarpDeq * 32;  // 4-bit instance: 192
   static_assert(2 * 128 * kRegsSoftmax + (kThreads - 256) * kRegsCtl <= kThreads * kLaunchRegs, "register split");
 };
 constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
@@ -101,10 +99,6 @@ struct PCfg {
   static constexpr int RAW_HALF = RAW_CODES + BN * 4;
   static constexpr int OFF_RAW = OFF_BAR + 256;
   static constexpr size_t SMEM_KV4 = (size_t)OFF_RAW + 2 * RAW_HALF + 1024;
-  // 8-bit caches: the tile's codes alone (its scales are read where they are used)
-  static constexpr int RAW8_HALF = BN * D;
-  static constexpr size_t SMEM_KV8 = (size_t)OFF_RAW + 2 * RAW8_HALF + 1024;
-  static_assert(SMEM_KV8 <= 232448, "shared memory");
 };
 
 struct Bars {
@@ -117,7 +111,6 @@ struct Bars {
   uint64_t q_free;  // DCA: the MMAs reading the current query vectors have completed
   uint64_t raw_full[2], raw_empty[2];  // 4-bit caches: the staged raw K (0) and V (1) rows of a cache tile
   uint64_t deq_sync;                   // 4-bit caches: both dequantizing warps are done with K or V
-  int64_t raw_row[2];  // 8-bit caches: first row of the staged codes in the cache, -1: their page does not exist
 };
 static_assert(sizeof(Bars) <= 256, "barrier area");
 
@@ -389,63 +382,6 @@ __device__ __forceinline__ void dequant_row(uint8_t* tile, const uint8_t* codes,
   }
 }
 
-// Four 8-bit codes times their scale, rounded to bf16, as two pairs.
-template <int CODE>
-__device__ __forceinline__ uint2 dequant4(uint32_t w, float2 sc) {
-  float2 a, b;
-  if constexpr (CODE == kKv8E4m3) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-    a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  } else {
-    // a code with its sign bit flipped under the float exponent of 2^23 reads as 2^23 + 128 + code
-    const uint32_t u = w ^ 0x80808080u;
-    const float2 bias = make_float2(-8388736.f, -8388736.f);
-    a = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u)),
-                               __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541u))), bias);
-    b = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542u)),
-                               __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543u))), bias);
-  }
-  a = __fmul2_rn(a, sc);
-  b = __fmul2_rn(b, sc);
-  return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
-}
-
-// One staged tile of 8-bit codes into a K or V tile of a stage, laid out as TMA writes the
-// bf16 rows: `left` rows of codes (scales sc[0] and sc[1] of its two blocks), then the open
-// block's rows from the tail, zeros past the n tokens. A thread takes 16 dims of a row at a
-// time, so that a warp reads 512 staged bytes in a row.
-template <int D, int CODE>
-__device__ __forceinline__ void dequant_tile8(uint8_t* tile, const uint8_t* raw, int left, const float (&sc)[2],
-                                              const uint16_t* tail, int64_t r0, int64_t full, int64_t n, int tid,
-                                              int threads) {
-  constexpr int CPR = D / 16;  // 16-dim chunks per row
-  for (int e = tid; e < BN * CPR; e += threads) {
-    const int r = e / CPR, c = e % CPR;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (r < left) {
-      const uint4 w = *reinterpret_cast<const uint4*>(raw + e * 16);
-      const float s = r < kKv8Block ? sc[0] : sc[1];
-      const float2 s2 = make_float2(s, s);
-      const uint2 a = dequant4<CODE>(w.x, s2), b = dequant4<CODE>(w.y, s2);
-      const uint2 d = dequant4<CODE>(w.z, s2), f = dequant4<CODE>(w.w, s2);
-      lo = make_uint4(a.x, a.y, b.x, b.y);
-      hi = make_uint4(d.x, d.y, f.x, f.y);
-    } else if (r0 + r >= full && r0 + r < n) {
-      const uint4* src = reinterpret_cast<const uint4*>(tail + (r0 + r - full) * D + c * 16);
-      lo = __ldg(src);
-      hi = __ldg(src + 1);
-    }
-    uint8_t* row = tile + (c >> 2) * kBox + r * 128;
-    const int cc = (c & 3) * 2;
-    *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = lo;
-    *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = hi;
-  }
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -468,11 +404,16 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   const DevError err{&g_prefill_err};
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const Item it = item_of(p, blockIdx.x);
+  // kModeSplit: tiles [j0, j0 + ntiles) of the item; else all of them
+  const bool split = kMode == kModeSplit && (int)blockIdx.x < p.items_r;
+  const Item it = item_of(p, split ? blockIdx.x / p.splits : blockIdx.x);
   const TilePlan pl = plan_of<kMode>(p, it);
+  const int s_no = split ? blockIdx.x % p.splits : 0;
+  const int j0 = split ? (int)((int64_t)s_no * pl.total / p.splits) : 0;
+  const int share = split ? (int)((int64_t)(s_no + 1) * pl.total / p.splits) - j0 : pl.total;
   // After any CTA of this kernel gave up a wait, later CTAs do no work, so a
   // failure ends in about one wait limit instead of one per CTA.
-  const int ntiles = (*(volatile unsigned int*)err.word != 0u) ? 0 : pl.total;
+  const int ntiles = (*(volatile unsigned int*)err.word != 0u) ? 0 : share;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
@@ -489,7 +430,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     }
     mbar_init(&bars->drain, 1);
     if (kMode == kModeDca) mbar_init(&bars->q_free, 1);
-    if (is_deq_mode(kMode)) {
+    if (kMode == kModeKv4) {
       for (int h = 0; h < 2; ++h) {
         mbar_init(&bars->raw_full[h], 1);
         mbar_init(&bars->raw_empty[h], 1);
@@ -546,7 +487,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         int j = 0;
         int rc = 0;  // 4-bit caches: raw tiles staged so far
         for (; j < ntiles && ok; ++j) {
-          const Tile t = tile_at<kMode>(pl, j);
+          const Tile t = tile_at<kMode>(pl, kMode == kModeSplit ? j0 + j : j);
           if (kMode == kModeDca) {
             const int v = dt.var(j);
             if (v != qvar) {
@@ -589,38 +530,6 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
               mbar_arrive_expect_tx(&bars->raw_full[h], rows16 * (uint32_t)(D / 2 + 4));
               bulk_g2s(raw, codes + row * (D / 2), rows16 * (D / 2), &bars->raw_full[h]);
               bulk_g2s(raw + C::RAW_CODES, pairs + row, rows16 * 4, &bars->raw_full[h]);
-            }
-            if (!ok) break;
-            ++rc;
-            continue;
-          }
-          if (kMode == kModeKv8 && t.phase == 0 && !it.streaming) {
-            // a retrieval head's cache tile: its rows of codes (whole blocks of 64) into the
-            // staging buffers; warps 10 ... 15 do the rest, the tail's rows included
-            const int64_t r0 = (int64_t)t.k * BN;
-            const int64_t left = p.n / kKv8Block * kKv8Block - r0;
-            const uint32_t bytes = left <= 0 ? 0u : (uint32_t)((left < BN ? left : BN) * D);
-            const int64_t plane = (int64_t)it.b * p.sh.n_ret + it.cidx;
-            int64_t row = plane * p.cap64 + r0;
-            if (p.pg.table && bytes) {
-              const uint32_t bi = (uint32_t)r0 / (uint32_t)p.pg.block_size;
-              const int64_t id = __ldg(p.pg.table + plane * p.pg.max_blocks + bi);
-              row = id * p.pg.block_size + (r0 - (int64_t)bi * p.pg.block_size);
-              if (id < 0 || id >= p.pg.num_blocks) {
-                atomicOr(&g_prefill_err, kErrBadBlock);
-                row = -1;
-              }
-            }
-            for (int h = 0; h < 2 && ok; ++h) {  // K, then V
-              if (!mbar_wait(&bars->raw_empty[h], (uint32_t)((rc & 1) ^ 1), err, kErrPrefillProducer)) {
-                ok = false;
-                break;
-              }
-              bars->raw_row[h] = row;
-              const uint32_t copy = row < 0 ? 0u : bytes;
-              mbar_arrive_expect_tx(&bars->raw_full[h], copy);
-              if (copy)
-                bulk_g2s(smem + C::OFF_RAW + h * C::RAW8_HALF, (h == 0 ? p.k8 : p.v8) + row * D, copy, &bars->raw_full[h]);
             }
             if (!ok) break;
             ++rc;
@@ -691,12 +600,11 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
           // after an early exit, let the copies already issued land before the CTA ends
           mbar_wait(&bars->q_full, kMode == kModeDca ? (uint32_t)((q_loads - 1) & 1) : 0u, err, kErrPrefillProducer);
           for (int jj = (j > kNS ? j - kNS : 0); jj < j; ++jj) {
-            // filled by the dequantizing warps
-            if (jj < pl.n_cache && (kMode == kModeKv4 || (kMode == kModeKv8 && !it.streaming))) continue;
+            if (kMode == kModeKv4 && jj < pl.n_cache) continue;  // filled by the dequantizing warps
             mbar_wait(&bars->k_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
             mbar_wait(&bars->v_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
           }
-          if (is_deq_mode(kMode) && rc > 0)  // the last staging copies
+          if (kMode == kModeKv4 && rc > 0)  // the last staging copies
             for (int h = 0; h < 2; ++h) mbar_wait(&bars->raw_full[h], (uint32_t)((rc - 1) & 1), err, kErrPrefillProducer);
         }
       }
@@ -730,53 +638,6 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
             else
               dequant_row<D, true>(tile, raw, pairs, tid, tid < rows);
           }
-          fence_proxy_async_shared();  // these generic-proxy writes are read by the tensor cores
-          mbar_arrive(&bars->deq_sync);
-          if (!mbar_wait(&bars->deq_sync, (uint32_t)(h & 1), err, kErrPrefillProducer)) {  // two phases a tile
-            ok = false;
-            break;
-          }
-          if (tid == 0) {
-            mbar_arrive(h == 0 ? &bars->k_full[s] : &bars->v_full[s]);
-            mbar_arrive(&bars->raw_empty[h]);  // the staging buffer may take the next tile's rows
-          }
-        }
-      }
-    } else if (kMode == kModeKv8 && warp >= kWarpDeq) {
-      // ------------------------------------------------------------ 8-bit dequantization
-      // As above, for a retrieval head's cache tiles: codes times their block's scale in fp32,
-      // rounded to bf16; rows of the open block as they stand in the tail; zeros past the tokens.
-      const int tid = threadIdx.x - kWarpDeq * 32;
-      const int64_t full = p.n / kKv8Block * kKv8Block;
-      const int64_t plane = (int64_t)it.b * p.sh.n_ret + it.cidx;
-      bool ok = !it.streaming;
-      for (int j = 0; j < ntiles && j < pl.n_cache && ok; ++j) {
-        const int s = j % kNS;
-        const uint32_t ph = (uint32_t)((j / kNS) & 1);
-        const int64_t r0 = (int64_t)j * BN;
-        for (int h = 0; h < 2 && ok; ++h) {  // K into sK[s], then V into sV[s]
-          if (!mbar_wait(&bars->raw_full[h], (uint32_t)(j & 1), err, kErrPrefillProducer) ||
-              !mbar_wait(h == 0 ? &bars->k_empty[s] : &bars->v_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
-            ok = false;
-            break;
-          }
-          const int64_t row = bars->raw_row[h];
-          const int left = (int)(full - r0 < BN ? full - r0 : BN);  // rows of codes
-          float sc[2] = {0.f, 0.f};
-          if (row >= 0) {
-            const float* scale = (h == 0 ? p.k8_scale : p.v8_scale) + row / kKv8Block;
-            if (left > 0) sc[0] = __ldg(scale);
-            if (left > kKv8Block) sc[1] = __ldg(scale + 1);
-          }
-          uint8_t* tile = (h == 0 ? sK : sV) + s * C::KV_BYTES;
-          const uint8_t* raw = smem + C::OFF_RAW + h * C::RAW8_HALF;
-          const uint16_t* tail = (h == 0 ? p.k8_tail : p.v8_tail) + plane * kKv8Block * D;
-          if (p.code_type == kKv8E4m3)
-            dequant_tile8<D, kKv8E4m3>(tile, raw, row >= 0 ? left : 0, sc, tail, r0, full, p.n, tid,
-                                       Roles<kMode>::kDeqThreads);
-          else
-            dequant_tile8<D, kKv8Int8>(tile, raw, row >= 0 ? left : 0, sc, tail, r0, full, p.n, tid,
-                                       Roles<kMode>::kDeqThreads);
           fence_proxy_async_shared();  // these generic-proxy writes are read by the tensor cores
           mbar_arrive(&bars->deq_sync);
           if (!mbar_wait(&bars->deq_sync, (uint32_t)(h & 1), err, kErrPrefillProducer)) {  // two phases a tile
@@ -906,7 +767,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     float l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < ntiles && ok; ++j) {
-      const Tile t = tile_at<kMode>(pl, j);
+      const Tile t = tile_at<kMode>(pl, kMode == kModeSplit ? j0 + j : j);
       const bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
       if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) {
         ok = false;
@@ -979,21 +840,38 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     if (ok && ntiles > 0 && mbar_wait(&bars->o_final[x], 0, err, kErrPrefillSoftmax)) {
       tc_fence_after();
       const bool store = row_local < p.T;
-      const float inv = 1.f / l_run;
-      uint16_t* orow = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq) * D;
+      if (split) {  // this split's part, as it stands
+        const int64_t at = ((int64_t)blockIdx.x * kRows + x * BM + r);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
 #pragma unroll 1
-      for (int q4 = 0; q4 < D / 32; ++q4) {
-        uint32_t ov[32];
-        tmem_ld32_sync(obase + q4 * 32, ov);
-        if (store) {
-          uint32_t pk[16];
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t ov[32];
+          tmem_ld32_sync(obase + q4 * 32, ov);
+          if (store) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
-          uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
+            for (int e = 0; e < 8; ++e)
+              dst[q4 * 8 + e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                            __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+          }
+        }
+        if (store) p.part_ml[at] = make_float2(m_run, l_run);
+      } else {
+        const float inv = 1.f / l_run;
+        uint16_t* orow = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq) * D;
+#pragma unroll 1
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t ov[32];
+          tmem_ld32_sync(obase + q4 * 32, ov);
+          if (store) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            for (int e = 0; e < 16; ++e)
+              pk[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
+            uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          }
         }
       }
     }
@@ -1006,10 +884,52 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   }
 }
 
+// The splits' parts of every row: O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s. A warp takes a row
+// of an item, a lane D / 32 of its dims; all splits are loaded together. Some splits of a row may
+// have seen no key (m = -inf, l = 0), never all of them.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr int V = D / 32;
+  const int item = blockIdx.x / (kRows / 8), row = blockIdx.x % (kRows / 8) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const Item it = item_of(p, item);
+  const int row_local = it.qp * kRows + row;
+  if (row_local >= p.T) return;
+  float2 ml[kPrefillMaxSplits];
+  float o[kPrefillMaxSplits][V];
+  float M = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < kPrefillMaxSplits; ++s)
+    if (s < p.splits) {
+      const int64_t at = ((int64_t)item * p.splits + s) * kRows + row;
+      ml[s] = __ldcg(p.part_ml + at);
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[s][v] = __ldcg(p.part_o + at * D + lane * V + v);
+    }
+#pragma unroll
+  for (int s = 0; s < kPrefillMaxSplits; ++s)
+    if (s < p.splits) M = fmaxf(M, ml[s].x);
+  float acc[V], l = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+  for (int s = 0; s < kPrefillMaxSplits; ++s)
+    if (s < p.splits) {
+      const float f = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - M);
+      l = fmaf(f, ml[s].y, l);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, o[s][v], acc[v]);
+    }
+  uint16_t* out = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq) * D + lane * V;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int v = 0; v < V; ++v) out[v] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[v] * inv));
+}
+
 template <int D, int kMode>
 cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
   using C = PCfg<D>;
-  constexpr size_t smem = kMode == kModeKv4 ? C::SMEM_KV4 : (kMode == kModeKv8 ? C::SMEM_KV8 : C::SMEM);
+  constexpr size_t smem = kMode == kModeKv4 ? C::SMEM_KV4 : C::SMEM;
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e =
@@ -1029,6 +949,11 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
   const int grid = p.items_r + p.items_s;
   if (grid == 0) return cudaSuccess;
   prefill_kernel<D, kMode><<<grid, Roles<kMode>::kThreads, smem, stream>>>(p);
+  if (kMode == kModeSplit) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    prefill_merge_kernel<D><<<p.items_r / p.splits * (kRows / 8), 256, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -1043,8 +968,8 @@ cudaError_t launch_mode(const PrefillParams& p, cudaStream_t stream) {
 
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
   if (p.kv4) return launch_mode<kModeKv4>(p, stream);
-  if (p.kv8) return launch_mode<kModeKv8>(p, stream);
   if (p.chunk_len > 0) return launch_mode<kModeDca>(p, stream);
+  if (p.splits > 1) return launch_mode<kModeSplit>(p, stream);
   if (p.pg.stream_table) return launch_mode<kModePool>(p, stream);
   return p.pg.table ? launch_mode<kModePaged>(p, stream) : launch_mode<kModePlain>(p, stream);
 }

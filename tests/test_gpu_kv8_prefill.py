@@ -107,20 +107,55 @@ def test_a_chunked_prompt_then_decode(code):
 
 
 def test_equals_the_bf16_prefill_over_the_dequantized_rows():
+    """Bit for bit where no item is split over its keys (here: more items than SMs)."""
     from streaming_kv_cache_duo_gb300 import DuoLayer
-    n, T = 777, 400
-    c = Batch(52, [n + T], 8, 2, 128, 64, 256, [1, 0], "int8")
+    n, T, kinds = 777, 300, [1, 1, 1, 0]
+    c = Batch(52, [n + T] * 2, 32, 4, 64, 64, 256, kinds, "int8")
     layer = _layer(c, n + T)
     _fill(c, layer, n)
-    plain = DuoLayer(1, 8, 2, 128, 64, 256, n + T, [1, 0])
+    plain = DuoLayer(2, 32, 4, 64, 64, 256, n + T, kinds)
     kt, vt = c.kt.clone(), c.vt.clone()
     for x, name in ((kt, "k"), (vt, "v")):
-        rows = c.heads_rows(0, 0, n, getattr(c, name))[1]
-        x[0, :n, 0] = torch.from_numpy(rows.astype(np.float32)).to(torch.bfloat16)
+        for b in range(2):
+            for h in range(3):
+                rows = c.heads_rows(b, h, n, getattr(c, name))[1]
+                x[b, :n, h] = torch.from_numpy(rows.astype(np.float32)).to(torch.bfloat16)
     plain.append(kt[:, :n].contiguous().cuda(), vt[:, :n].contiguous().cuda())
     pick = lambda x: x[:, n:n + T].contiguous().cuda()
     want = plain.prefill(pick(c.qt), pick(c.kt), pick(c.vt))
     assert torch.equal(_run(c, layer, n, T), want)
+
+
+def test_workspace():
+    """The size covers the call, anything may be in it, a smaller one is refused; none is needed
+    where no cached row is read."""
+    from streaming_kv_cache_duo_gb300 import DuoError, _lib
+    n, T = 1300, 20
+    c = Batch(55, [n + T], 4, 2, 64, 4, 32, [1, 0], "int8")
+    layer = _layer(c, n + T)
+    assert _lib.duo_prefill_kv8_workspace_size(layer.handle, 0, T) == 0
+    q, k, v = (x[:, :T].contiguous().cuda() for x in (c.qt, c.kt, c.vt))
+    first = torch.empty_like(q)
+    _lib.duo_attn_prefill_kv8(layer.handle, layer.cache, layer.kv8, q, k, v, T, first, None)
+    _fill(c, layer, n)
+    need = _lib.duo_prefill_kv8_workspace_size(layer.handle, n, T)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    q, k, v = (x[:, n:].contiguous().cuda() for x in (c.qt, c.kt, c.vt))
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    _lib.duo_attn_prefill_kv8(layer.handle, layer.cache, layer.kv8, q, k, v, T, a, ws[:need])
+    assert bool((ws[need:] == 0xFF).all())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    layer.prefill(q, k, v, out=b, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    _check_chunk(c, n, T, a)
+    call = lambda w: _lib.duo_attn_prefill_kv8(layer.handle, layer.cache, layer.kv8, q, k, v, T, a, w)
+    for bad in (None, ws[:need - 1]):
+        with pytest.raises(DuoError, match="DUO_ERR_WORKSPACE"):
+            call(bad)
+    with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
+        call(ws[16:])
 
 
 def test_bad_pages_read_as_nothing_and_are_reported():
@@ -150,7 +185,7 @@ def test_refusals():
     for bad in ((q.float(), k, v), (q, k[:, :9].contiguous(), v), (q, k, v.cpu())):
         with pytest.raises(ValueError):
             layer.prefill(*bad)
-    call = lambda kv8, T=10, qq=q: _lib.duo_attn_prefill_kv8(layer.handle, layer.cache, kv8, qq, k, v, T, q)
+    call = lambda kv8, T=10, qq=q: _lib.duo_attn_prefill_kv8(layer.handle, layer.cache, kv8, qq, k, v, T, q, None)
     for args in ((None,), (layer.kv8, 0), (layer.kv8, -1), (layer.kv8, 10, None)):
         with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
             call(*args)
