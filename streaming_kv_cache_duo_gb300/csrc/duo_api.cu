@@ -61,11 +61,12 @@ struct duo_handle {
 
 namespace {
 
-// 4-D map over a token-major bf16 tensor [B, T, H, D]; box 64 x 1 x 128 x 1.
-duo_status encode_tokens(const duo_handle* h, CUtensorMap* map, const void* base, int B, int T, int H, int D) {
+// 4-D map over a token-major bf16 tensor [B, T, H, D]; box 64 x g x 128 / g x 1.
+duo_status encode_tokens(const duo_handle* h, CUtensorMap* map, const void* base, int B, int T, int H, int D,
+                         int g = 1) {
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)T * H * D * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)kPrefillBM, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)g, (cuuint32_t)(kPrefillBM / g), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -417,10 +418,12 @@ static duo_status check_kv8(const duo_handle* h, const duo_kv_cache* c, const du
   return check_cache(h, c, false, true);
 }
 
-// Prefill over an 8-bit cache of n tokens: its rows as bf16 (K planes, V planes), and the parts of
-// retrieval items split over their key tiles.
+// Prefill over an 8-bit cache of n tokens: its rows as bf16 (K planes, V planes), whether the query
+// heads of a KV head share query blocks, and the parts of retrieval items split over their keys.
 struct Kv8Prefill {
   int64_t plane_rows;
+  int64_t num_qt;  // query blocks per head (packed: per KV head)
+  bool packed;
   int splits;
   int64_t parts;   // items x splits, if splits > 1
   size_t part_at;  // byte offset of the parts in the workspace
@@ -428,24 +431,27 @@ struct Kv8Prefill {
 };
 static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
   const Shape& sh = h->sh;
-  Kv8Prefill w{pitch64(n), 1, 0, 0, 0};
+  Kv8Prefill w{pitch64(n), (T + (int64_t)kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, false, 1, 0, 0, 0};
   if (n < 1 || T < 1 || sh.n_ret == 0) return w;
   w.part_at = ((size_t)2 * sh.B * sh.n_ret * w.plane_rows * sh.D * 2 + 255) / 256 * 256;
-  // A CTA per item leaves SMs idle when there are few (a short turn after a long conversation:
-  // 333 tokens after 9001 for two sequences and four heads are 64 items of 73 tiles, 158 us; in
-  // two splits 98 us). Splits that shorten the longest SM's row of tiles by a tenth at least, each
-  // item counted with three tiles' worth of start and merge.
-  const int64_t num_qt = (T + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta;
-  const int64_t items = (int64_t)sh.B * sh.n_ret * sh.g * num_qt;
-  const int64_t cached = (n + kPrefillBN - 1) / kPrefillBN, tiles = cached + num_qt + 1;
-  int64_t best = (items + h->num_sms - 1) / h->num_sms * (tiles + 3);
-  for (int s = 2; s <= kPrefillMaxSplits && s <= cached && items * s <= 8 * h->num_sms; ++s) {
-    const int64_t cost = (items * s + h->num_sms - 1) / h->num_sms * ((tiles + s - 1) / s + 3);
-    if (cost * 10 <= best * 9) {
+  // A CTA per item leaves SMs idle when items are few, and rows of the last query block idle when
+  // tokens are: a short turn after a long conversation (333 tokens after 9001, two sequences, four
+  // retrieval heads, g = 4) is 64 items of 75 tiles, half of them with 77 rows of 256. Packed it is
+  // 48, and each split over several CTAs. Cost: the tiles that the busiest SM works through, each
+  // item counted with three tiles' worth of start and merge; packed where that is a tenth less.
+  const int64_t heads = (int64_t)sh.B * sh.n_ret, sms = h->num_sms;
+  const int64_t cached = (n + kPrefillBN - 1) / kPrefillBN, tiles = cached + (T + kPrefillBN - 1) / kPrefillBN;
+  int64_t best = (heads * sh.g * w.num_qt + sms - 1) / sms * (tiles + 3) * 9 / 10;
+  const int64_t qt = ((int64_t)T * sh.g + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, items = heads * qt;
+  for (int s = 1; s <= kPrefillMaxSplits && s <= cached && (s == 1 || items * s <= 8 * sms); ++s) {
+    const int64_t cost = (items * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
+    if (cost < best) {
       best = cost;
+      w.packed = true;
       w.splits = s;
     }
   }
+  if (w.packed) w.num_qt = qt;
   if (w.splits > 1) w.parts = items * w.splits;
   w.bytes = w.part_at + (size_t)w.parts * kPrefillRowsPerCta * (sh.D * sizeof(float) + sizeof(float2));
   return w;
@@ -478,7 +484,8 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
 
   PrefillParams p;
   memset(&p, 0, sizeof(p));
-  if ((st = encode_tokens(h, &p.tm_q, q, sh.B, T, sh.Hq, sh.D)) != DUO_OK) return st;
+  const Kv8Prefill plan = kv8 ? plan_prefill_kv8(h, c->n, T) : Kv8Prefill{};
+  if ((st = encode_tokens(h, &p.tm_q, q, sh.B, T, sh.Hq, sh.D, plan.packed ? sh.g : 1)) != DUO_OK) return st;
   if ((st = encode_tokens(h, &p.tm_k, k, sh.B, T, sh.Hkv, sh.D)) != DUO_OK) return st;
   if ((st = encode_tokens(h, &p.tm_v, v, sh.B, T, sh.Hkv, sh.D)) != DUO_OK) return st;
   const int64_t SR = (int64_t)sh.S + sh.R;
@@ -500,7 +507,6 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
     p.kv4 = 1;
   } else if (kv8) {  // the retrieval rows as bf16 in the workspace, then as a contiguous cache of them
     if (sh.n_ret > 0 && (st = check_capacity(h, pg, c->n, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
-    const Kv8Prefill plan = plan_prefill_kv8(h, c->n, T);
     if (plan.bytes > 0) {
       if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return fail(DUO_ERR_INVALID_ARG, "workspace not 256-byte aligned");
@@ -526,6 +532,8 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
         return fail(DUO_ERR_UNSUPPORTED, "the cached rows of all sequences and retrieval heads reach 2^31");
       if ((st = encode_cache(h, &p.tm_kfull, e.k_out, planes, plan.plane_rows, c->n, sh.D)) != DUO_OK) return st;
       if ((st = encode_cache(h, &p.tm_vfull, e.v_out, planes, plan.plane_rows, c->n, sh.D)) != DUO_OK) return st;
+      p.packed = plan.packed;
+      while ((1 << p.log2_g) < sh.g) ++p.log2_g;
       p.splits = plan.splits;
       p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_at);
       p.part_ml = reinterpret_cast<float2*>(p.part_o + plan.parts * kPrefillRowsPerCta * sh.D);
@@ -560,8 +568,8 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
   p.n = c->n;
   p.T = T;
   p.nvalid = nvalid;
-  p.num_qt = (T + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta;
-  const int64_t per_kind = (int64_t)sh.B * sh.g * p.num_qt;
+  p.num_qt = plan.packed ? (int)plan.num_qt : (T + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta;
+  const int64_t per_kind = (int64_t)sh.B * (plan.packed ? 1 : sh.g) * p.num_qt;
   const int64_t ir = (kind_mask & 2) ? per_kind * sh.n_ret : 0;
   const int64_t is = (kind_mask & 1) ? per_kind * sh.n_str : 0;
   if (ir + is > 0x7fffffffLL) return fail(DUO_ERR_UNSUPPORTED, "too many query tiles for one launch");
@@ -569,7 +577,7 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
   p.items_s = (int)is;
   // about one wave of CTAs per KV head; at most num_qt, so qp_group x (items per block)
   // stays within the item count (an int)
-  p.qp_group = std::max(1, std::min(h->num_sms / sh.g, p.num_qt));
+  p.qp_group = std::max(1, std::min(plan.packed ? h->num_sms : h->num_sms / sh.g, p.num_qt));
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)sh.D));
   p.sh = sh;
   p.heads = h->heads;

@@ -215,8 +215,12 @@ struct PrefillParams {
   int64_t cap16;
   int sr16;
   int kv4;
-  // retrieval items split over their key tiles (splits > 1; contiguous caches): split s of item i
-  // leaves its unnormalised output (fp32 [256, D]) and (max, sum) rows at place i splits + s
+  // contiguous caches, few tokens: query rows are tokens x heads of a KV head (tm_q's box is 64 x g x
+  // 128 / g x 1, num_qt = ceil(T g / 256)), and retrieval items may be split over their key tiles
+  // (splits > 1): split s of item i leaves its unnormalised output (fp32 [256, D]) and (max, sum)
+  // rows at place i splits + s
+  int packed;
+  int log2_g;
   int splits;
   float* part_o;
   float2* part_ml;

@@ -65,7 +65,10 @@ constexpr int kModePaged = 1;  // retrieval caches in a paged pool (block table)
 constexpr int kModePool = 2;   // both head kinds in the paged pool
 constexpr int kModeDca = 3;    // Dual Chunk Attention: one of three query vectors per key tile
 constexpr int kModeKv4 = 4;    // 4-bit caches: cache tiles dequantized into shared memory by warps 10, 11
-constexpr int kModeSplit = 5;  // plain, each retrieval item's key tiles shared by several CTAs and merged after
+// plain, for few tokens: the query heads of a KV head share query blocks (row = token x g + head, so a
+// block holds 256 / g tokens and a short chunk fills it), and each retrieval item's key tiles may be
+// shared by several CTAs, their parts merged after
+constexpr int kModePacked = 5;
 constexpr int kWarpDeq = 10;   // first of the dequantizing warps (4-bit caches): 10 ... 15
 template <int kMode>
 struct Roles {
@@ -119,9 +122,10 @@ struct Item {
   int b, hq, kvh, cidx, qp;  // qp: index of the 256-row block of query rows
 };
 
+template <int kMode>
 __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
   Item it;
-  const int g = p.sh.g;
+  const int g = kMode == kModePacked ? 1 : p.sh.g;  // items per KV head and query block
   int nk;
   if (idx < p.items_r) {
     it.streaming = false;
@@ -147,7 +151,7 @@ __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
     it.b = bc / nk;
     it.cidx = bc % nk;
     it.kvh = p.heads.ret_head[it.cidx];
-    it.hq = it.kvh * g + (r % g);
+    it.hq = kMode == kModePacked ? it.kvh * p.sh.g : it.kvh * g + (r % g);
     return it;
   }
   const int qp_rev = idx / per_qp;  // longest query blocks first
@@ -157,8 +161,14 @@ __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
   r %= nk * g;
   it.cidx = r / g;
   it.kvh = it.streaming ? p.heads.str_head[it.cidx] : p.heads.ret_head[it.cidx];
-  it.hq = it.kvh * g + (r % g);
+  it.hq = kMode == kModePacked ? it.kvh * p.sh.g : it.kvh * g + (r % g);
   return it;
+}
+
+// Chunk-local token of query row `row` (counted over the item's query blocks).
+template <int kMode>
+__device__ __forceinline__ int token_of(const PrefillParams& p, int row) {
+  return kMode == kModePacked ? row >> p.log2_g : row;
 }
 
 // The KV tiles a CTA visits: first tiles of the cache (phase 0), then tiles of
@@ -184,8 +194,8 @@ struct Tile {
 template <int kMode>
 __device__ __forceinline__ TilePlan plan_of(const PrefillParams& p, const Item& it) {
   TilePlan t;
-  const int q0 = it.qp * kRows;  // first query row (chunk-local) of the CTA
-  const int last_row = min(p.T, q0 + kRows) - 1;
+  const int q0 = token_of<kMode>(p, it.qp * kRows);  // first token (chunk-local) of the CTA
+  const int last_row = min(p.T, token_of<kMode>(p, (it.qp + 1) * kRows)) - 1;
   t.k_hi = last_row / BN;
   if (!it.streaming) {
     t.n_cache = (int)((p.n + BN - 1) / BN);
@@ -404,9 +414,9 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   const DevError err{&g_prefill_err};
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // kModeSplit: tiles [j0, j0 + ntiles) of the item; else all of them
-  const bool split = kMode == kModeSplit && (int)blockIdx.x < p.items_r;
-  const Item it = item_of(p, split ? blockIdx.x / p.splits : blockIdx.x);
+  // kModePacked: tiles [j0, j0 + ntiles) of the item; else all of them
+  const bool split = kMode == kModePacked && p.splits > 1 && (int)blockIdx.x < p.items_r;
+  const Item it = item_of<kMode>(p, split ? blockIdx.x / p.splits : blockIdx.x);
   const TilePlan pl = plan_of<kMode>(p, it);
   const int s_no = split ? blockIdx.x % p.splits : 0;
   const int j0 = split ? (int)((int64_t)s_no * pl.total / p.splits) : 0;
@@ -471,8 +481,8 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         for (int x = 0; x < kQT; ++x)
   #pragma unroll
           for (int bx = 0; bx < C::NBOX; ++bx)
-            tma_load_4d(sQ + x * C::Q_BYTES + bx * kBox, qmap, bx * 64, it.hq, it.qp * kRows + x * BM, it.b,
-                        &bars->q_full);
+            tma_load_4d(sQ + x * C::Q_BYTES + bx * kBox, qmap, bx * 64, it.hq, token_of<kMode>(p, it.qp * kRows + x * BM),
+                        it.b, &bars->q_full);
         bool ok = true;
         // paged: the block id of the next cache tile is read one tile ahead, so its
         // latency overlaps the wait for a free stage
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         int j = 0;
         int rc = 0;  // 4-bit caches: raw tiles staged so far
         for (; j < ntiles && ok; ++j) {
-          const Tile t = tile_at<kMode>(pl, kMode == kModeSplit ? j0 + j : j);
+          const Tile t = tile_at<kMode>(pl, kMode == kModePacked ? j0 + j : j);
           if (kMode == kModeDca) {
             const int v = dt.var(j);
             if (v != qvar) {
@@ -756,18 +766,20 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t sbase = lane_base + col_s(x);
     const uint32_t obase = lane_base + col_o(x);
-    const int row_local = it.qp * kRows + x * BM + r;  // chunk-local query row
+    const int row_local = token_of<kMode>(p, it.qp * kRows + x * BM + r);  // chunk-local token of the query row
     const int i_abs = (int)p.n + row_local;            // absolute position (< 2^31, checked on the host)
     // DCA: the fp32 per-position scale joins softmax_scale on the fp32 product
     const float sl2 = (kMode == kModeDca && p.mscale && row_local < p.T)
                           ? p.scale_log2 * __ldg(p.mscale + (int64_t)it.b * p.T + row_local)
                           : p.scale_log2;
-    const int q_last = x == 0 ? it.qp * kQT : it.qp * kQT + 1;  // diagonal tile of this query tile
+    // diagonal tile of this query tile (packed: the first it has)
+    const int q_last = kMode == kModePacked ? token_of<kMode>(p, it.qp * kRows + x * BM) / BN
+                                            : (x == 0 ? it.qp * kQT : it.qp * kQT + 1);
     float m_run = -INFINITY;  // running max of scaled scores (log2 units)
     float l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < ntiles && ok; ++j) {
-      const Tile t = tile_at<kMode>(pl, kMode == kModeSplit ? j0 + j : j);
+      const Tile t = tile_at<kMode>(pl, kMode == kModePacked ? j0 + j : j);
       const bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
       if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) {
         ok = false;
@@ -857,7 +869,8 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         if (store) p.part_ml[at] = make_float2(m_run, l_run);
       } else {
         const float inv = 1.f / l_run;
-        uint16_t* orow = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq) * D;
+        const int head = kMode == kModePacked ? it.hq + (r & (p.sh.g - 1)) : it.hq;
+        uint16_t* orow = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + head) * D;
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t ov[32];
@@ -892,8 +905,8 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
   constexpr int V = D / 32;
   const int item = blockIdx.x / (kRows / 8), row = blockIdx.x % (kRows / 8) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const Item it = item_of(p, item);
-  const int row_local = it.qp * kRows + row;
+  const Item it = item_of<kModePacked>(p, item);
+  const int row_local = token_of<kModePacked>(p, it.qp * kRows + row);
   if (row_local >= p.T) return;
   float2 ml[kPrefillMaxSplits];
   float o[kPrefillMaxSplits][V];
@@ -920,7 +933,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = fmaf(f, o[s][v], acc[v]);
     }
-  uint16_t* out = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq) * D + lane * V;
+  uint16_t* out = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq + (row & (p.sh.g - 1))) * D + lane * V;
   const float inv = 1.f / l;
 #pragma unroll
   for (int v = 0; v < V; ++v) out[v] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[v] * inv));
@@ -949,7 +962,7 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
   const int grid = p.items_r + p.items_s;
   if (grid == 0) return cudaSuccess;
   prefill_kernel<D, kMode><<<grid, Roles<kMode>::kThreads, smem, stream>>>(p);
-  if (kMode == kModeSplit) {
+  if (kMode == kModePacked && p.splits > 1) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     prefill_merge_kernel<D><<<p.items_r / p.splits * (kRows / 8), 256, 0, stream>>>(p);
@@ -969,7 +982,7 @@ cudaError_t launch_mode(const PrefillParams& p, cudaStream_t stream) {
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
   if (p.kv4) return launch_mode<kModeKv4>(p, stream);
   if (p.chunk_len > 0) return launch_mode<kModeDca>(p, stream);
-  if (p.splits > 1) return launch_mode<kModeSplit>(p, stream);
+  if (p.packed) return launch_mode<kModePacked>(p, stream);
   if (p.pg.stream_table) return launch_mode<kModePool>(p, stream);
   return p.pg.table ? launch_mode<kModePaged>(p, stream) : launch_mode<kModePlain>(p, stream);
 }

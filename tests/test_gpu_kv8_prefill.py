@@ -107,17 +107,18 @@ def test_a_chunked_prompt_then_decode(code):
 
 
 def test_equals_the_bf16_prefill_over_the_dequantized_rows():
-    """Bit for bit where no item is split over its keys (here: more items than SMs)."""
+    """Bit for bit where query heads do not share query blocks and no item is split over its keys (here:
+    full query blocks, and more of them than SMs)."""
     from streaming_kv_cache_duo_gb300 import DuoLayer
-    n, T, kinds = 777, 300, [1, 1, 1, 0]
-    c = Batch(52, [n + T] * 2, 32, 4, 64, 64, 256, kinds, "int8")
+    n, T, kinds = 777, 512, [1, 1, 0, 1, 0, 1, 1, 0]
+    c = Batch(52, [n + T] * 2, 64, 8, 64, 64, 256, kinds, "int8")
     layer = _layer(c, n + T)
     _fill(c, layer, n)
-    plain = DuoLayer(2, 32, 4, 64, 64, 256, n + T, kinds)
+    plain = DuoLayer(2, 64, 8, 64, 64, 256, n + T, kinds)
     kt, vt = c.kt.clone(), c.vt.clone()
     for x, name in ((kt, "k"), (vt, "v")):
         for b in range(2):
-            for h in range(3):
+            for h in c.ret:
                 rows = c.heads_rows(b, h, n, getattr(c, name))[1]
                 x[b, :n, h] = torch.from_numpy(rows.astype(np.float32)).to(torch.bfloat16)
     plain.append(kt[:, :n].contiguous().cuda(), vt[:, :n].contiguous().cuda())
