@@ -437,14 +437,24 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
   // A CTA per item leaves SMs idle when items are few, and rows of the last query block idle when
   // tokens are: a short turn after a long conversation (333 tokens after 9001, two sequences, four
   // retrieval heads, g = 4) is 64 items of 75 tiles, half of them with 77 rows of 256. Packed it is
-  // 48, and each split over several CTAs. Cost: the tiles that the busiest SM works through, each
-  // item counted with three tiles' worth of start and merge; packed where that is a tenth less.
-  const int64_t heads = (int64_t)sh.B * sh.n_ret, sms = h->num_sms;
-  const int64_t cached = (n + kPrefillBN - 1) / kPrefillBN, tiles = cached + (T + kPrefillBN - 1) / kPrefillBN;
-  int64_t best = (heads * sh.g * w.num_qt + sms - 1) / sms * (tiles + 3) * 9 / 10;
+  // 48, and each split over several CTAs. Cost: the tiles until the last SM is done, retrieval items
+  // first, then the streaming heads' in the gaps; each item counted with three tiles' worth of start
+  // and merge. Packed and split where that is a tenth less.
+  const int64_t heads = (int64_t)sh.B * sh.n_ret, others = (int64_t)sh.B * sh.n_str, sms = h->num_sms;
+  const auto tiles_of = [](int64_t rows) { return (rows + kPrefillBN - 1) / kPrefillBN; };
+  const auto makespan = [sms](int64_t r, int64_t tr, int64_t t, int64_t ts) {
+    const int64_t rounds = r / sms, rest = r % sms;
+    const int64_t in_gaps = rest ? (sms - rest) * (tr / ts) : 0;
+    const int64_t more = t > in_gaps ? (t - in_gaps + sms - 1) / sms * ts : 0;
+    return (rounds + (rest > 0)) * tr + more;
+  };
+  const int64_t cached = tiles_of(n), tiles = cached + tiles_of(T);
+  const auto stream_tiles = [&](int64_t tokens) { return tiles_of(sh.S) + tiles_of(sh.R + tokens) + 1 + 3; };
+  int64_t best = makespan(heads * sh.g * w.num_qt, tiles + 3, others * sh.g * w.num_qt,
+                          stream_tiles(kPrefillRowsPerCta)) * 9 / 10;
   const int64_t qt = ((int64_t)T * sh.g + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, items = heads * qt;
   for (int s = 1; s <= kPrefillMaxSplits && s <= cached && (s == 1 || items * s <= 8 * sms); ++s) {
-    const int64_t cost = (items * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
+    const int64_t cost = makespan(items * s, (tiles + s - 1) / s + 3, others * qt, stream_tiles(kPrefillRowsPerCta / sh.g));
     if (cost < best) {
       best = cost;
       w.packed = true;

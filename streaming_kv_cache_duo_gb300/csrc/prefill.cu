@@ -909,15 +909,18 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
   const int row_local = token_of<kModePacked>(p, it.qp * kRows + row);
   if (row_local >= p.T) return;
   float2 ml[kPrefillMaxSplits];
-  float o[kPrefillMaxSplits][V];
+  alignas(16) float o[kPrefillMaxSplits][V];
   float M = -INFINITY;
 #pragma unroll
   for (int s = 0; s < kPrefillMaxSplits; ++s)
     if (s < p.splits) {
       const int64_t at = ((int64_t)item * p.splits + s) * kRows + row;
       ml[s] = __ldcg(p.part_ml + at);
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[s][v] = __ldcg(p.part_o + at * D + lane * V + v);
+      const float* src = p.part_o + at * D + lane * V;
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(o[s]) = __ldcg(reinterpret_cast<const float4*>(src));
+      else
+        *reinterpret_cast<float2*>(o[s]) = __ldcg(reinterpret_cast<const float2*>(src));
     }
 #pragma unroll
   for (int s = 0; s < kPrefillMaxSplits; ++s)
@@ -935,8 +938,13 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
     }
   uint16_t* out = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq + (row & (p.sh.g - 1))) * D + lane * V;
   const float inv = 1.f / l;
+  uint32_t w[V / 2];
 #pragma unroll
-  for (int v = 0; v < V; ++v) out[v] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[v] * inv));
+  for (int v = 0; v < V; v += 2) w[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
 template <int D, int kMode>
