@@ -1,16 +1,16 @@
 // duo_attn_decode_kv8: one query token per sequence over 8-bit caches (codes with one scale
 // per 64 rows of a head, the open block in a bf16 tail) and the streaming heads' bf16 rings.
 //
-// A unit is one (sequence, KV head). Its keys are cut into tiles of 64 KB (at D = 128): 256
-// keys of codes, or 128 bf16 rows of a ring or a tail. All tiles of all units, laid end to end
+// A unit is one (sequence, KV head). Its keys are cut into tiles of 64 KB: 256 keys of codes (512
+// at D = 64), or 128 bf16 rows of a ring or a tail (32 KB at D = 64). All tiles of all units, laid end to end
 // in unit order with one tile's worth of room before each unit for what a unit costs apart from
 // its keys (q, the merge of the warps), are shared out evenly over one CTA per SM: CTA c takes
 // those that start in [c W / C, (c + 1) W / C). With lengths on the device every CTA sums the
 // units' tiles itself, so a batch of ragged lengths is as balanced as a uniform one and
 // nothing is planned on the host but the launch shape.
 //
-// Eight warps, each with its own slice of every tile (32 keys of codes or 16 bf16 rows) and
-// its own ring of three stages (K and V, 8 KB together at D = 128) that it refills itself; no
+// Eight warps, each with its own slice of every tile (32 or 64 keys of codes, or 16 bf16 rows) and
+// its own ring of three stages (K and V, 8 KB together) that it refills itself; no
 // warp waits for another. Codes come by TMA through a swizzled map, so that both fragment
 // reads below are free of bank conflicts while the rows in HBM stay plain row-major, their two
 // scales by 4-byte asynchronous copies on the same barrier; bf16 rows by plain bulk copies.
@@ -47,8 +47,7 @@ __device__ unsigned int g_decode_kv8_err;
 
 constexpr int kWarps = kKv8Warps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kKv8Rows;  // keys of a slice of codes
-constexpr int kStages = kKv8Stages;
+constexpr int kStages = 3;
 // units of at most this many tiles are not split (their merge would cost more)
 constexpr int kShortTiles = 4;
 // p is kept times 2^kPShift: fp16 then holds it down to 2^-(24 + kPShift) of the row maximum,
@@ -57,7 +56,9 @@ constexpr float kPShift = 7.f;
 
 template <int D, int G>
 struct Cfg {
-  static constexpr int SLICE = kRows * D;  // bytes of a warp's K (or V) codes
+  static constexpr int ROWS = kv8_slice_rows(D);  // keys of a slice of codes
+  static constexpr int TK = ROWS * kWarps;        // and of a tile of them
+  static constexpr int SLICE = ROWS * D;          // bytes of a warp's K (or V) codes
   static constexpr int STAGE = 2 * SLICE;
   static constexpr int RING = kWarps * kStages * STAGE;
   static constexpr int HR = G < 4 ? G : 4;  // heads merged at a time
@@ -187,11 +188,14 @@ __device__ __forceinline__ int seq_len(const Kv8DecodeParams& p, int b) {
 // Tiles of a retrieval / streaming unit of a sequence of n tokens (at least one, so that
 // every unit's output is written).
 __host__ __device__ __forceinline__ int code_rows_of(int n) { return n & ~(kKv8Block - 1); }
+template <int D>
 __host__ __device__ __forceinline__ int tiles_codes(int n) {
-  return (int)(((uint32_t)code_rows_of(n) + kKv8TK - 1) / kKv8TK);
+  constexpr uint32_t TK = Cfg<D, 1>::TK;
+  return (int)(((uint32_t)code_rows_of(n) + TK - 1) / TK);
 }
+template <int D>
 __host__ __device__ __forceinline__ int tiles_ret(int n) {
-  const int t = tiles_codes(n) + ((n & (kKv8Block - 1)) > 0);
+  const int t = tiles_codes<D>(n) + ((n & (kKv8Block - 1)) > 0);
   return t > 0 ? t : 1;
 }
 __host__ __device__ __forceinline__ int tiles_str(int n, int SR) {
@@ -205,6 +209,7 @@ struct Unit {
   int tiles, tc;  // tiles, and those of codes among them
   bool streaming;
 };
+template <int D>
 __device__ __forceinline__ Unit unit_of(const Kv8DecodeParams& p, int u) {
   Unit x;
   x.u = u;
@@ -213,8 +218,8 @@ __device__ __forceinline__ Unit unit_of(const Kv8DecodeParams& p, int u) {
   x.b = (int)(k / heads);
   x.idx = (int)(k - x.b * heads);
   x.n = seq_len(p, x.b);
-  x.tiles = x.streaming ? tiles_str(x.n, p.sh.S + p.sh.R) : tiles_ret(x.n);
-  x.tc = x.streaming ? 0 : tiles_codes(x.n);
+  x.tiles = x.streaming ? tiles_str(x.n, p.sh.S + p.sh.R) : tiles_ret<D>(x.n);
+  x.tc = x.streaming ? 0 : tiles_codes<D>(x.n);
   return x;
 }
 // Its query heads' first row in q and o.
@@ -262,6 +267,7 @@ __device__ __forceinline__ void cut(Share& s, int ctas) {
   s.x1 = c < s.C ? mul_div(c + 1, s.W, s.C) : s.W;
 }
 
+template <int D>
 __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   Share s;
   if (p.whole) {
@@ -290,7 +296,7 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   int64_t r = 0, q = 0;
   for (int b = b0; b < b1; ++b) {
     const int n = seq_len(p, b);
-    r += (int64_t)p.sh.n_ret * (tiles_ret(n) + 1);
+    r += (int64_t)p.sh.n_ret * (tiles_ret<D>(n) + 1);
     q += (int64_t)p.sh.n_str * (tiles_str(n, SR) + 1);
   }
   const int64_t r_own = r, q_own = q;
@@ -320,7 +326,7 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
     int64_t base = in_r ? r - r_own : Wr + q - q_own;
     for (int b = b0; b < b1; ++b) {
       const int n = seq_len(p, b);
-      const int64_t T = (in_r ? tiles_ret(n) : tiles_str(n, SR)) + 1;
+      const int64_t T = (in_r ? tiles_ret<D>(n) : tiles_str(n, SR)) + 1;
       if (s.x0 < base + heads * T) {
         const int64_t k = mul_div(s.x0 - base, 1, T);
         scratch[2 * kWarps] = (in_r ? 0 : p.U_r) + (int64_t)b * heads + k;
@@ -337,11 +343,35 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   return s;
 }
 
+// A unit and this CTA's tiles of it.
+template <int D>
+struct Segment {
+  Unit x;
+  int64_t ub;
+  int lt0, lt1;
+  bool live;
+  // from the unit (u, ub) on, the first of which the share has tiles
+  __device__ __forceinline__ void find(const Kv8DecodeParams& p, const Share& s, int u, int64_t at) {
+    ub = at;
+    for (;; ++u) {
+      live = p.whole ? u == s.u : ub < s.x1;
+      if (!live) return;
+      x = unit_of<D>(p, u);
+      lt0 = p.whole ? 0 : tiles_before(s.x0 - ub, x.tiles);
+      lt1 = p.whole ? x.tiles : tiles_before(s.x1 - ub, x.tiles);
+      if (lt0 < lt1) return;
+      ub += x.tiles + 1;  // (the share starts behind its last tile)
+    }
+  }
+};
+
 // The slices this warp takes, in order, over the CTA's share: one tile further each time, across
 // units.
+template <int D>
 struct Cursor {
+  static constexpr int TK = Cfg<D, 1>::TK;
   Unit x;
-  int64_t ub, x0, x1;
+  int64_t ub, x1;
   int lt, lt1;      // next tile of the unit, and the end of the share's tiles in it
   int row, rows;    // first row of the slice in its codes (32 rows), or in its bf16 rows (1 to 16)
   int code_rows;    // rows of codes of the unit
@@ -350,16 +380,16 @@ struct Cursor {
   int warp;
   bool live, codes;
 
-  __device__ __forceinline__ void init(const Kv8DecodeParams& p, const Share& s, int w) {
+  // from this CTA's first segment on
+  __device__ __forceinline__ void init(const Kv8DecodeParams& p, const Share& s, const Segment<D>& first, int w) {
     warp = w;
-    live = p.whole || s.x0 < s.x1;
+    live = first.live;
     if (!live) return;
-    x = unit_of(p, s.u);
-    x0 = s.x0;
+    x = first.x;
+    ub = first.ub;
     x1 = s.x1;
-    ub = s.ub;
-    lt = p.whole ? 0 : tiles_before(x0 - ub, x.tiles);
-    lt1 = p.whole ? x.tiles : tiles_before(x1 - ub, x.tiles);
+    lt = first.lt0;
+    lt1 = first.lt1;
     settle(p);
   }
   // from tile lt on, the first with a slice for this warp
@@ -367,7 +397,7 @@ struct Cursor {
     for (;;) {
       if (lt < x.tc && lt < lt1) {
         code_rows = code_rows_of(x.n);
-        const int64_t r = (int64_t)lt * kKv8TK + warp * kRows;
+        const int64_t r = (int64_t)lt * TK + warp * Cfg<D, 1>::ROWS;
         if (r < code_rows) {
           row = (int)r;
           codes = true;
@@ -395,15 +425,15 @@ struct Cursor {
         live = false;
         return;
       }
-      x = unit_of(p, x.u + 1);
+      x = unit_of<D>(p, x.u + 1);
       lt = 0;
       lt1 = tiles_before(x1 - ub, x.tiles);
     }
   }
   __device__ __forceinline__ void advance(const Kv8DecodeParams& p) {
     ++lt;
-    if (codes && lt < lt1 && (int64_t)row + kKv8TK < code_rows) {  // (the most frequent case, kept short)
-      row += kKv8TK;
+    if (codes && lt < lt1 && (int64_t)row + TK < code_rows) {  // (the most frequent case, kept short)
+      row += TK;
       if (p.pg.table) blk = __ldg(pages + (uint32_t)row / (uint32_t)p.pg.block_size);
       return;
     }
@@ -413,7 +443,7 @@ struct Cursor {
 
 // Copies the cursor's slice of codes into a stage (lane 0). False: its page does not exist.
 template <int D, int G>
-__device__ __forceinline__ bool issue_codes(const Kv8DecodeParams& p, const Cursor& cur, uint8_t* stage, float* scales,
+__device__ __forceinline__ bool issue_codes(const Kv8DecodeParams& p, const Cursor<D>& cur, uint8_t* stage, float* scales,
                                             uint64_t* bar, uint64_t pol) {
   using C = Cfg<D, G>;
   int64_t row;
@@ -439,7 +469,7 @@ __device__ __forceinline__ bool issue_codes(const Kv8DecodeParams& p, const Curs
 
 // Copies the cursor's bf16 rows into a stage (every lane; every lane arrives).
 template <int D, int G>
-__device__ __forceinline__ void issue_rows(const Kv8DecodeParams& p, const Cursor& cur, uint8_t* stage, uint64_t* bar,
+__device__ __forceinline__ void issue_rows(const Kv8DecodeParams& p, const Cursor<D>& cur, uint8_t* stage, uint64_t* bar,
                                            int lane) {
   constexpr int CPR = D / 8;  // 16-byte chunks per row
   const int64_t first = cur.x.streaming ? ((int64_t)cur.x.b * p.sh.n_str + cur.x.idx) * (p.sh.S + p.sh.R) + cur.row
@@ -512,16 +542,17 @@ struct State {
     }
   }
 
-  // One 32-key slice of codes, every key visible (addresses in shared memory). qb: q in B
+  // One slice of codes, every key visible (addresses in shared memory). qb: q in B
   // fragments; kf: K's scale times the heads' factors.
   template <int CODE>
   __device__ __forceinline__ void codes(uint32_t sk, uint32_t sv, const uint32_t (&qb)[D / 16][2], float kf0, float kf1,
                                         float vs, int lane) {
-    float x[8];
+    constexpr int NG = Cfg<D, G>::ROWS / 16;  // 16-key groups
+    float x[4 * NG];
     // K: a fragment's words are the bytes 4 tig ... of rows gid and gid + 8, one 16-dim chunk each
     const int krow = lane & 15, kch = lane >> 4;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // keys 16 h + gid and 16 h + gid + 8
+    for (int h = 0; h < NG; ++h) {  // keys 16 h + gid and 16 h + gid + 8
       float sc[2][4];
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -542,10 +573,10 @@ struct State {
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[4 * h + k] = (sc[0][k] + sc[1][k]) * ((k & 1) ? kf1 : kf0);
     }
-    softmax<8, false>(x, 0u);
-    uint32_t pb[4];  // P^T: keys 16 h + 2 tig (+ 1) and + 8 (+ 9) of head gid
+    softmax<4 * NG, false>(x, 0u);
+    uint32_t pb[2 * NG];  // P^T: keys 16 h + 2 tig (+ 1) and + 8 (+ 9) of head gid
 #pragma unroll
-    for (int k = 0; k < 4; ++k) pb[k] = transpose8x8(pack_half2(x[2 * k], x[2 * k + 1]));
+    for (int k = 0; k < 2 * NG; ++k) pb[k] = transpose8x8(pack_half2(x[2 * k], x[2 * k + 1]));
     // V: matrix row 4 t + e is the key whose byte lands in byte e of the words of lanes tig = t,
     // which is to be key 2 t (+ 1) in the first pair and 2 t + 8 (+ 9) in the second
     const int e = lane & 3, t = (lane >> 2) & 3;
@@ -560,7 +591,7 @@ struct State {
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < NG; ++h)
 #pragma unroll
         for (int i = 0; i < HALF; i += 2) {
           uint32_t w[4];
@@ -682,27 +713,6 @@ __device__ __forceinline__ void fetch_q(const uint16_t* qh, bool codes, uint32_t
   }
 }
 
-// A unit and this CTA's tiles of it.
-struct Segment {
-  Unit x;
-  int64_t ub;
-  int lt0, lt1;
-  bool live;
-  // from the unit (u, ub) on, the first of which the share has tiles
-  __device__ __forceinline__ void find(const Kv8DecodeParams& p, const Share& s, int u, int64_t at) {
-    ub = at;
-    for (;; ++u) {
-      live = p.whole ? u == s.u : ub < s.x1;
-      if (!live) return;
-      x = unit_of(p, u);
-      lt0 = p.whole ? 0 : tiles_before(s.x0 - ub, x.tiles);
-      lt1 = p.whole ? x.tiles : tiles_before(s.x1 - ub, x.tiles);
-      if (lt0 < lt1) return;
-      ub += x.tiles + 1;  // (the share starts behind its last tile)
-    }
-  }
-};
-
 // Positions held by ring slots gid and gid + 8 of a warp's slice, which starts at slot r0 (-1
 // past the last; any position does for a tail's rows).
 __device__ __forceinline__ void fetch_pos(const Kv8DecodeParams& p, const Unit& x, int r0, int have, int gid, int (&at)[2]) {
@@ -740,12 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   // Launched as a programmatic dependent: nothing the grid before it writes is read earlier.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Share sh = share_of(p, reinterpret_cast<int64_t*>(red));
+  const Share sh = share_of<D>(p, reinterpret_cast<int64_t*>(red));
   __syncthreads();  // (share_of's scratch is the merge buffer)
   const uint64_t pol = l2_policy_evict_first();  // codes are read once
 
-  Cursor cur;
-  cur.init(p, sh, warp);
+  Cursor<D> cur;
+  Segment<D> sg;
+  sg.find(p, sh, sh.u, sh.ub);
+  cur.init(p, sh, sg, warp);
   int fill = 0, use = 0;             // stages to fill and to use next
   uint32_t pending = 0, phases = 0;  // bit of a barrier: copies under way; the phase to wait for
   uint32_t bad = 0;                  // lane 0: bit s set if stage s was not copied
@@ -785,8 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     use = use + 1 == kStages ? 0 : use + 1;
     return s;
   };
-  Segment sg;
-  sg.find(p, sh, sh.u, sh.ub);
   // fetched ahead for the unit that comes next, while the warps of this one are merged
   uint32_t q[D / 16][2];
   int at[2];
@@ -809,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
       const float f = convert_q<D, CODE>(q) * p.scale_log2;
       const float f0 = __shfl_sync(0xffffffffu, f, 8 * tig), f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
       int left = (lt1 < tc ? lt1 : tc) - lt0;  // this warp's slices: none in a tile it lies behind
-      if ((int64_t)(lt0 + left - 1) * kKv8TK + warp * kRows >= code_rows_of(x.n)) --left;
+      if ((int64_t)(lt0 + left - 1) * C::TK + warp * C::ROWS >= code_rows_of(x.n)) --left;
       for (; left > 0; --left) {
         const int s = next(0);
         const bool skip = !ok || ((__shfl_sync(0xffffffffu, bad, 0) >> s) & 1u);
@@ -861,26 +871,35 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
       buf ^= 1;
       st.write(rb, h0, warp, gid, tig);
       __syncthreads();
-#pragma unroll 1
-      for (int e = tid; e < C::HR * D; e += kThreads) {
-        const int h = e / D, d = e % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, rb[(w * C::HR + h) * (D + 2) + D]);
-        float num = 0.f, den = 0.f;
+      // a thread two dims of a head, everything it needs in flight together
+      for (int e = tid; e < C::HR * D / 2; e += kThreads) {
+        const int h = e / (D / 2), d = 2 * (e % (D / 2));
+        float2 ml[kWarps], ov[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float* r = rb + (w * C::HR + h) * (D + 2);
-          const float f = r[D] == -INFINITY && !(r[D + 1] != 0.f) ? 0.f : ex2_approx(r[D] - M);
-          num = fmaf(f, r[d], num);
-          den = fmaf(f, r[D + 1], den);
+          ml[w] = *reinterpret_cast<const float2*>(r + D);
+          ov[w] = *reinterpret_cast<const float2*>(r + d);
+        }
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w].x);
+        float n0 = 0.f, n1 = 0.f, den = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ml[w].x == -INFINITY && !(ml[w].y != 0.f) ? 0.f : ex2_approx(ml[w].x - M);
+          n0 = fmaf(f, ov[w].x, n0);
+          n1 = fmaf(f, ov[w].y, n1);
+          den = fmaf(f, ml[w].y, den);
         }
         float* ph = part + (h0 + h) * C::PS;
-        if (n_parts == 1)
-          p.o[(orow + h0 + h) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(den != 0.f ? num / den : 0.f));
-        else
-          ph[d] = num;
-        if (d == 0 && n_parts > 1) *reinterpret_cast<float2*>(ph + D) = make_float2(M, den);
+        if (n_parts == 1) {
+          const float inv = den != 0.f ? 1.f / den : 0.f;
+          *reinterpret_cast<uint32_t*>(p.o + (orow + h0 + h) * D + d) = pack_bf16x2(n0 * inv, n1 * inv);
+        } else {
+          *reinterpret_cast<float2*>(ph + d) = make_float2(n0, n1);
+          if (d == 0) *reinterpret_cast<float2*>(ph + D) = make_float2(M, den);
+        }
       }
     }
   }
@@ -1029,7 +1048,7 @@ cudaError_t launch_g(const Kv8DecodeParams& p, cudaStream_t stream) {
 
 void plan_decode_kv8(Kv8DecodeParams* p, int num_sms) {
   const int64_t U = (int64_t)p->U_r + p->U_s;
-  p->tiles_r = tiles_ret((int)p->n);
+  p->tiles_r = p->sh.D == 128 ? tiles_ret<128>((int)p->n) : tiles_ret<64>((int)p->n);
   p->tiles_s = tiles_str((int)p->n, p->sh.S + p->sh.R);
   p->line_r = (int64_t)p->U_r * (p->tiles_r + 1);
   p->line_s = (int64_t)p->U_s * (p->tiles_s + 1);

@@ -974,11 +974,11 @@ duo_status duo_attn_prefill_kv8_paged(duo_handle* h, const duo_kv_cache* c, cons
   return prefill_impl(h, c, paged, q, k, v, T, o, 3, stream, nullptr, kv8, workspace, workspace_bytes);
 }
 
-// 2-D map over codes [rows, D]: boxes of 32 rows, the swizzle of the row's width.
+// 2-D map over codes [rows, D]: boxes of a warp's rows, the swizzle of the row's width.
 static duo_status encode_codes(const duo_handle* h, CUtensorMap* map, const void* base, int64_t rows, int D) {
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)D};
-  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)kKv8Rows};
+  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)kv8_slice_rows(D)};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,

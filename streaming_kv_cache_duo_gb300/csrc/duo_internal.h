@@ -262,14 +262,10 @@ struct Kv8AppendParams {
 cudaError_t launch_append_kv8(const Kv8AppendParams& p, cudaStream_t stream);
 cudaError_t append_kv8_read_clear_error(uint32_t* code);
 
-#ifndef KV8W
-#define KV8W 8
-#define KV8S 3
-#endif
-constexpr int kKv8Warps = KV8W, kKv8Stages = KV8S;
-constexpr int kKv8Rows = 32;                      // rows of codes a warp takes of a tile
-constexpr int kKv8TK = kKv8Warps * kKv8Rows;      // keys of a decode tile over codes
-constexpr int kKv8TKBf16 = kKv8Warps * 16;        // and over bf16 rows (ring or tail)
+constexpr int kKv8Warps = 8;                    // of a decode CTA
+constexpr int kKv8TKBf16 = kKv8Warps * 16;      // keys of a decode tile over bf16 rows (ring or tail)
+// Rows of codes a warp takes of a tile: 4 KB of K and 4 KB of V either way.
+__host__ __device__ constexpr int kv8_slice_rows(int D) { return D == 128 ? 32 : 64; }
 
 struct Kv8ExpandParams {
   const uint8_t* k_codes;
