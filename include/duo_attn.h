@@ -398,7 +398,8 @@ duo_status duo_kv_append_kv8_ragged(duo_handle* handle, duo_kv_cache* cache, con
  * calls): scores and outputs are accumulated in fp32 from the codes (fp16 tensor-core
  * operands, exact for both code types; q scaled to fp16 by a power of two of its own per
  * head, so any finite bf16 q is taken) and the tail and ring rows (bf16 operands); p is
- * rounded to fp16 over codes and to bf16 over bf16 rows. Workspace as for duo_attn_decode.
+ * rounded to fp16 over codes and to bf16 over bf16 rows. Workspace as for duo_attn_decode; o
+ * must not overlap q.
  * duo_attn_decode_kv8_varlen reads the lengths on the device (seq_lens int32 [B], clamped
  * to [0, max_len], the new token included; a sequence of length 0 gets zeros) and splits the
  * work by them; `paged` may be NULL (contiguous caches). */
@@ -419,7 +420,7 @@ duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* ca
  * device memory of duo_prefill_kv8_workspace_size(handle, cache->n, T) bytes, 256-byte
  * aligned (may be NULL if that is 0: nothing cached, or no retrieval head): 4 D bytes per
  * cached token and retrieval head of the layer, plus the parts. Nothing in it survives the
- * call; calls sharing one must be ordered on the GPU. */
+ * call; calls sharing one must be ordered on the GPU. o must not overlap q, k or v. */
 size_t duo_prefill_kv8_workspace_size(const duo_handle* handle, int64_t n, int32_t T);
 duo_status duo_attn_prefill_kv8(duo_handle* handle, const duo_kv_cache* cache, const duo_kv8_cache* kv8,
                                 const void* q, const void* k, const void* v, int32_t T, void* o, void* workspace,

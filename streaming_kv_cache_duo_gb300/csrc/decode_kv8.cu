@@ -2,18 +2,22 @@
 // per 64 rows of a head, the open block in a bf16 tail) and the streaming heads' bf16 rings.
 //
 // A unit is one (sequence, KV head). Its keys are cut into tiles of 64 KB: 256 keys of codes (512
-// at D = 64), or 128 bf16 rows of a ring or a tail (32 KB at D = 64). All tiles of all units, laid end to end
-// in unit order with one tile's worth of room before each unit for what a unit costs apart from
-// its keys (q, the merge of the warps), are shared out evenly over one CTA per SM: CTA c takes
-// those that start in [c W / C, (c + 1) W / C). With lengths on the device every CTA sums the
-// units' tiles itself, so a batch of ragged lengths is as balanced as a uniform one and
-// nothing is planned on the host but the launch shape.
+// at D = 64), or 128 bf16 rows of a ring or a tail (32 KB at D = 64). All tiles of all units, laid
+// end to end in unit order with one tile's worth of room before each unit for what a unit costs
+// apart from its keys (q, the merge of the warps), are shared out evenly over one CTA per SM:
+// CTA c takes those that start in [c W / C, (c + 1) W / C). With lengths on the device every CTA
+// sums the units' tiles itself, so a batch of ragged lengths is as balanced as a uniform one and
+// nothing is planned on the host but the launch shape. (With the streaming units laid end to end
+// without that room, the last CTAs had most of them: 119 us for a million tokens, 100 us with it.)
 //
 // Eight warps, each with its own slice of every tile (32 or 64 keys of codes, or 16 bf16 rows) and
-// its own ring of three stages (K and V, 8 KB together) that it refills itself; no
-// warp waits for another. Codes come by TMA through a swizzled map, so that both fragment
-// reads below are free of bank conflicts while the rows in HBM stay plain row-major, their two
-// scales by 4-byte asynchronous copies on the same barrier; bf16 rows by plain bulk copies.
+// its own ring of three stages (K and V, 8 KB together) that it refills itself; no warp waits for
+// another. Codes come by TMA through a swizzled map, so that the matrix loads below are free of
+// bank conflicts while the rows in HBM stay plain row-major, their two scales by 4-byte
+// asynchronous copies on the same barrier; bf16 rows by 16-byte ones, swizzled by their addresses.
+// (Twelve warps of 168 registers with two stages each were no faster: 93 us against 88 us for a
+// million tokens. D = 64 with 32-key slices paid every slice's fixed cost twice: 59 us against 35 us
+// for 11 x 110556 tokens.)
 //
 // Per slice, on warp-level tensor-core products (a decode has one to eight query heads per
 // KV head: 8 columns, far too few rows to fill a 128-row tcgen05 tile, and the time is
@@ -27,7 +31,15 @@
 // as fp16 after a scaling by a power of two of its own (exact), p as fp16 with 7 bits of
 // headroom taken from above (p <= 2^15, flushed below 2^-31 of the maximum).
 //
+// K's fragments come by ldmatrix, V's by its transposing form for bytes, whose rows are named in
+// the order that makes each lane's four bytes the keys of its P fragment: no byte is shuffled.
+//
 // bf16 rows (at most 63 of a tail, S + R of a ring) take bf16 products. Only these need masks.
+//
+// Bound by HBM: one million tokens with two retrieval heads, int8, 88 us = 6.1 TB/s of the 538 MB
+// stored (0.90 of the measured copy rate; a CTA works through a tile in 1.34 us, 7.4 TB/s in all).
+// What is left is fixed: 2.8 us until a CTA's first tiles are under way, a merge of 0.8 us, the
+// second kernel and two launches, 8 us.
 //
 // Merge: as the bf16 decode. The warps of a CTA merge in shared memory; a unit split over
 // CTAs leaves (o, max, sum) parts for a second kernel, launched as a programmatic dependent.
@@ -743,8 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
       mbar_init(&bars[2 * s + 1], 32);
     }
     fence_mbarrier_init();
-    prefetch_tmap(&p.tm_k);
-    prefetch_tmap(&p.tm_v);
+    if (p.U_r > 0) {
+      prefetch_tmap(&p.tm_k);
+      prefetch_tmap(&p.tm_v);
+    }
   }
   __syncthreads();
   // Launched as a programmatic dependent: nothing the grid before it writes is read earlier.
