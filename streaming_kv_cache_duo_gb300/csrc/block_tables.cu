@@ -26,6 +26,7 @@ constexpr int kScanThreads = 1024;  // at most
 constexpr int kSmall = 1024;        // sequences whose sums fit in shared memory
 // outputs (table entries and slots) up to which the scanning CTA writes them itself
 constexpr int64_t kFuseWork = 8192;
+constexpr int kPlanes = 4;  // planes whose slots a thread writes
 
 // Scratch, int32: [0] free blocks after the returns, [1] blocks handed out, [2] tokens in
 // the packed batch (at most max_tokens), then per sequence the old length (-1: turned down
@@ -101,8 +102,7 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total)
   return v;
 }
 
-// Writes the new blocks' table entries and the tokens' maps (items = tokens x planes), both
-// shared out among `step` threads, of which this is number `first`.
+// Writes the new blocks' table entries and the tokens' maps, both shared out among `step` threads, of which this is number `first`.
 __device__ void fill(const BlockTablesParams& p, const Scratch& s, int64_t first, int64_t step) {
   const int avail = s.head[0], handed = s.head[1], tokens = s.head[2];
   for (int64_t e = first; e < handed; e += step) {
@@ -114,38 +114,47 @@ __device__ void fill(const BlockTablesParams& p, const Scratch& s, int64_t first
     if (id < 0 || id >= p.num_blocks) atomicOr(&g_tables_err, kErrBadBlock);
     p.table[((int64_t)b * p.planes + k / per) * p.max_blocks + have + k % per] = id;
   }
-  const int64_t items = (int64_t)p.max_tokens * p.planes;
+  // a thread takes a token's slots for kPlanes planes: its sequence is found once, and 32 bytes a
+  // thread fill whole lines
+  const int groups = (p.planes + kPlanes - 1) / kPlanes;
+  const int64_t items = (int64_t)p.max_tokens * groups;
   for (int64_t it = first; it < items; it += step) {
-    const int i = (int)((it >> 32) ? it / p.planes : (uint32_t)it / (uint32_t)p.planes);
-    const int pl = (int)(it - (int64_t)i * p.planes);
+    const int i = (int)((it >> 32) ? it / groups : (uint32_t)it / (uint32_t)groups);
+    const int p0 = (int)(it - (int64_t)i * groups) * kPlanes;
     int seq = -1, pos = -1;
-    int64_t slot = -1;
+    int64_t slot[kPlanes] = {-1, -1, -1, -1};
     if (i < tokens) {
       seq = bisect(s.cu_new, p.B, i);
       const int old = s.old_len[seq];
       if (old >= 0) {
         pos = old + (i - s.cu_new[seq]);
         const int have = blocks_of(old, p.bs);
-        const int j = pos / p.bs;
-        int id;
-        if (j < have) {
-          id = p.table[((int64_t)seq * p.planes + pl) * p.max_blocks + j];
-        } else {
-          const int nb = s.need_base[seq];
-          const int per = (s.need_base[seq + 1] - nb) / p.planes;
-          id = p.free_list[avail - 1 - (nb + pl * per + (j - have))];
-        }
-        if (id < 0 || id >= p.num_blocks)
-          atomicOr(&g_tables_err, kErrBadBlock);
-        else
-          slot = (int64_t)id * p.bs + (pos - j * p.bs);
+        const int j = (int)((uint32_t)pos / (uint32_t)p.bs);
+        const int nb = s.need_base[seq];
+        const int per = (int)((uint32_t)(s.need_base[seq + 1] - nb) / (uint32_t)p.planes);
+        int id[kPlanes];
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k)
+          if (p0 + k < p.planes)
+            id[k] = j < have ? p.table[((int64_t)seq * p.planes + p0 + k) * p.max_blocks + j]
+                             : p.free_list[avail - 1 - (nb + (p0 + k) * per + (j - have))];
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k)
+          if (p0 + k < p.planes) {
+            if (id[k] < 0 || id[k] >= p.num_blocks)
+              atomicOr(&g_tables_err, kErrBadBlock);
+            else
+              slot[k] = (int64_t)id[k] * p.bs + (pos - j * p.bs);
+          }
       }
     }
-    if (pl == 0) {
+    if (p0 == 0) {
       p.token_seq[i] = seq;
       p.token_pos[i] = pos;
     }
-    p.slots[it] = slot;
+#pragma unroll
+    for (int k = 0; k < kPlanes; ++k)
+      if (p0 + k < p.planes) p.slots[(int64_t)i * p.planes + p0 + k] = slot[k];
   }
 }
 
@@ -302,7 +311,8 @@ cudaError_t launch_block_tables(const BlockTablesParams& p, int num_sms, cudaStr
   block_tables_scan_kernel<<<1, threads, 0, stream>>>(p, fuse ? 1 : 0);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || fuse) return e;
-  int64_t blocks = (work + 255) / 256;
+  const int64_t items = (int64_t)p.max_tokens * ((p.planes + kPlanes - 1) / kPlanes) + (int64_t)p.B * p.planes;
+  int64_t blocks = (items + 255) / 256;
   if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -898,44 +898,52 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
 }
 
 // The splits' parts of every row: O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s. A warp takes a row
-// of an item, a lane D / 32 of its dims; all splits are loaded together. Some splits of a row may
-// have seen no key (m = -inf, l = 0), never all of them.
+// of an item, a lane D / 32 of its dims; four splits are loaded at a time (all sixteen at once took
+// 119 registers, two CTAs per SM, and three times as long). Some splits of a row may have seen no key
+// (m = -inf, l = 0), never all of them.
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
-  constexpr int V = D / 32;
+  constexpr int V = D / 32, NB = 4;
   const int item = blockIdx.x / (kRows / 8), row = blockIdx.x % (kRows / 8) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const Item it = item_of<kModePacked>(p, item);
   const int row_local = token_of<kModePacked>(p, it.qp * kRows + row);
   if (row_local >= p.T) return;
-  float2 ml[kPrefillMaxSplits];
-  alignas(16) float o[kPrefillMaxSplits][V];
-  float M = -INFINITY;
+  const int64_t at0 = (int64_t)item * p.splits * kRows + row;
+  const float2* ml_at = p.part_ml + at0;
+  const float* o_at = p.part_o + at0 * D + lane * V;
+  float acc[V], l = 0.f, M = -INFINITY;
 #pragma unroll
-  for (int s = 0; s < kPrefillMaxSplits; ++s)
-    if (s < p.splits) {
-      const int64_t at = ((int64_t)item * p.splits + s) * kRows + row;
-      ml[s] = __ldcg(p.part_ml + at);
-      const float* src = p.part_o + at * D + lane * V;
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int s0 = 0; s0 < p.splits; s0 += NB) {
+    float2 ml[NB];
+    alignas(16) float o[NB][V];
+    float mn = M;
+#pragma unroll
+    for (int s = 0; s < NB; ++s) {
+      const bool there = s0 + s < p.splits;
+      ml[s] = there ? __ldcg(ml_at + (s0 + s) * kRows) : make_float2(-INFINITY, 0.f);
+      const float* src = o_at + (int64_t)(there ? s0 + s : 0) * kRows * D;
       if constexpr (V == 4)
         *reinterpret_cast<float4*>(o[s]) = __ldcg(reinterpret_cast<const float4*>(src));
       else
         *reinterpret_cast<float2*>(o[s]) = __ldcg(reinterpret_cast<const float2*>(src));
     }
 #pragma unroll
-  for (int s = 0; s < kPrefillMaxSplits; ++s)
-    if (s < p.splits) M = fmaxf(M, ml[s].x);
-  float acc[V], l = 0.f;
+    for (int s = 0; s < NB; ++s) mn = fmaxf(mn, ml[s].x);
+    const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mn);
+    l *= keep;
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int v = 0; v < V; ++v) acc[v] *= keep;
 #pragma unroll
-  for (int s = 0; s < kPrefillMaxSplits; ++s)
-    if (s < p.splits) {
-      const float f = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - M);
+    for (int s = 0; s < NB; ++s) {
+      const float f = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - mn);
       l = fmaf(f, ml[s].y, l);
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = fmaf(f, o[s][v], acc[v]);
     }
+    M = mn;
+  }
   uint16_t* out = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq + (row & (p.sh.g - 1))) * D + lane * V;
   const float inv = 1.f / l;
   uint32_t w[V / 2];
