@@ -32,12 +32,12 @@
  *     aligned.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Every kernel runs on it, asynchronously to the host. The append and decode
- *     kernels use programmatic dependent launch among themselves (an append lets the
- *     decode after it start early, each waits for the grid before it before touching
- *     its data); stream order holds as usual for any kernel launched without the
- *     cudaLaunchAttributeProgrammaticStreamSerialization attribute. A caller kernel
- *     launched with that attribute right after an append or a decode must call
- *     cudaGridDependencySynchronize() before it reads what they wrote.
+ *     kernels, those of the 8-bit caches and of the block tables use programmatic dependent
+ *     launch among themselves (an append lets the decode after it start early, each waits
+ *     for the grid before it before touching its data); stream order holds as usual for any
+ *     kernel launched without the cudaLaunchAttributeProgrammaticStreamSerialization
+ *     attribute. A caller kernel launched with that attribute right after one of them must
+ *     call cudaGridDependencySynchronize() before it reads what they wrote.
  *   - Arguments are checked on the host before any launch. On an error nothing is
  *     written, the cache length is unchanged, the status is returned and
  *     duo_last_error() describes it.

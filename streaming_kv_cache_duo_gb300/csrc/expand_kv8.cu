@@ -47,6 +47,8 @@ __device__ __forceinline__ uint2 expand4(uint32_t w, float scale) {
 
 template <int D, int CODE>
 __global__ void __launch_bounds__(kThreads) expand_kv8_kernel(const Kv8ExpandParams p) {
+  // (a prefill launched as a programmatic dependent waits for this grid before it reads a row)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const bool is_v = threadIdx.x >= kHalf;
   const int tid = threadIdx.x % kHalf;
   const uint32_t blocks = ((uint32_t)p.n + kKv8Block - 1) / kKv8Block;  // of a plane

@@ -457,6 +457,12 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  if (kMode == kModePacked) {
+    // launched as a programmatic dependent of the kernel that writes the cached rows as bf16; the merge
+    // of the splits may be scheduled once every CTA is here
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   if (warp >= 8) {
     // ================================================ warpgroup 2: TMA, MMA, idle
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<kMode>::kRegsCtl));
@@ -906,6 +912,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
   constexpr int V = D / 32, NB = 4;
   const int item = blockIdx.x / (kRows / 8), row = blockIdx.x % (kRows / 8) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Item it = item_of<kModePacked>(p, item);
   const int row_local = token_of<kModePacked>(p, it.qp * kRows + row);
   if (row_local >= p.T) return;
@@ -977,13 +984,27 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
   if (regs != Roles<kMode>::kLaunchRegs) return cudaErrorInvalidConfiguration;
   const int grid = p.items_r + p.items_s;
   if (grid == 0) return cudaSuccess;
-  prefill_kernel<D, kMode><<<grid, Roles<kMode>::kThreads, smem, stream>>>(p);
-  if (kMode == kModePacked && p.splits > 1) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    prefill_merge_kernel<D><<<p.items_r / p.splits * (kRows / 8), 256, 0, stream>>>(p);
+  if constexpr (kMode != kModePacked) {
+    prefill_kernel<D, kMode><<<grid, Roles<kMode>::kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+  } else {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(Roles<kMode>::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, kMode>, p);
+    if (e != cudaSuccess || p.splits <= 1) return e;
+    cfg.gridDim = dim3((unsigned)(p.items_r / p.splits * (kRows / 8)));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p);
   }
-  return cudaGetLastError();
 }
 
 template <int kMode>
