@@ -419,8 +419,9 @@ duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* ca
  * query blocks are split over their keys, their parts merged by log-sum-exp. workspace:
  * device memory of duo_prefill_kv8_workspace_size(handle, cache->n, T) bytes, 256-byte
  * aligned (may be NULL if that is 0: nothing cached, or no retrieval head): 4 D bytes per
- * cached token and retrieval head of the layer, plus the parts. Nothing in it survives the
- * call; calls sharing one must be ordered on the GPU. o must not overlap q, k or v. */
+ * cached token and retrieval head of the layer, plus the parts (at most 8 per SM, and none when
+ * the split would not pay, so a longer cache can need less: ask for each n and T). Nothing in it
+ * survives the call; calls sharing one must be ordered on the GPU. o must not overlap q, k or v. */
 size_t duo_prefill_kv8_workspace_size(const duo_handle* handle, int64_t n, int32_t T);
 duo_status duo_attn_prefill_kv8(duo_handle* handle, const duo_kv_cache* cache, const duo_kv8_cache* kv8,
                                 const void* q, const void* k, const void* v, int32_t T, void* o, void* workspace,

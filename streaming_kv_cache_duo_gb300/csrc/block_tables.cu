@@ -102,7 +102,8 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total)
   return v;
 }
 
-// Writes the new blocks' table entries and the tokens' maps, both shared out among `step` threads, of which this is number `first`.
+// Writes the new blocks' table entries and the tokens' maps, both shared out among `step`
+// threads, of which this is number `first`.
 __device__ void fill(const BlockTablesParams& p, const Scratch& s, int64_t first, int64_t step) {
   const int avail = s.head[0], handed = s.head[1], tokens = s.head[2];
   for (int64_t e = first; e < handed; e += step) {

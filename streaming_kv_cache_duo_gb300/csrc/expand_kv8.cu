@@ -8,8 +8,8 @@
 // cached tokens (8 of 32 heads), 2.9 us a tile against 1.6 us from a bf16 cache. Done once, it
 // is a copy, HBM-bound: 3 bytes moved per value.
 //
-// A CTA per block of 64 rows, plane after plane; half of a CTA's threads do K, half V. A thread turns 8 codes
-// into 16 bytes at a time, all its loads in flight together.
+// A CTA per block of 64 rows, plane after plane; half of a CTA's threads do K, half V. A thread
+// turns 8 codes into 16 bytes at a time, all its loads in flight together.
 #include <cuda_fp16.h>
 
 #include "duo_device.cuh"

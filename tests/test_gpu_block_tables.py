@@ -184,3 +184,29 @@ def test_refusals():
     small = pool.workspace[:16]
     with pytest.raises(DuoError, match="DUO_ERR_WORKSPACE"):
         _lib.duo_block_tables_update(pool.c, new, 32, pool.seq_lens, pool.free_count, pool.slot_map.c, small)
+
+
+def test_tables_serve_the_bf16_paged_caches():
+    """The pool's table behind a bf16 paged layer, sequences of one length: the same rows as a
+    contiguous layer's, so a prefill, appends and a decode give the same bits."""
+    from streaming_kv_cache_duo_gb300 import DuoLayer, DuoPagedLayer
+    B, Hq, Hkv, D, S, R, page, mb = 2, 4, 2, 64, 4, 32, 128, 3
+    kinds, g = [1, 0], torch.Generator().manual_seed(3)
+    pool = _pool(B, 1, page, mb, B * mb, B * 300)
+    paged = DuoPagedLayer(B, Hq, Hkv, D, S, R, page, mb, B * mb, pool.block_table, kinds)
+    plain = DuoLayer(B, Hq, Hkv, D, S, R, page * mb, kinds)
+    paged.k_full.zero_(), paged.v_full.zero_()
+    for T in (1, 127, 130, 1):
+        q, k, v = (torch.randn(B, T, h, D, generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv))
+        pool.update(torch.full((B,), T, dtype=torch.int32, device="cuda"))
+        assert torch.equal(paged.prefill(q, k, v), plain.prefill(q, k, v))
+        paged.append(k, v)
+        plain.append(k, v)
+        last = q[:, -1].contiguous()
+        a, b = paged.decode(last), plain.decode(last)
+        assert torch.equal(a, b)
+        n = paged.n
+        for s in range(B):
+            rows = paged.k_full[pool.block_table[s, 0, :-(-n // page)].long()].reshape(-1, D)[:n]
+            assert torch.equal(rows, plain.k_full[s, 0, :n])
+    assert int(pool.free_count) == 0 and pool.seq_lens.tolist() == [259, 259]

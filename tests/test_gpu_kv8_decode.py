@@ -196,6 +196,21 @@ def test_non_finite_blocks_show_and_stay_with_their_head():
     check(got[0, 2:], ref[2:], tol[2:])
 
 
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_non_finite_block_among_many_ctas(which):
+    """The same where the head is shared by many CTAs, of which one has the block."""
+    n = 70000
+    c = Batch(42, [n], 4, 2, 64, 4, 32, [1, 1], "e4m3")
+    bad = {"k": c.kt.clone(), "v": c.vt.clone()}
+    bad[which][0, 40000, 0] = float("nan")
+    layer, clean = _layer(c, n), _layer(c, n)
+    layer.append(bad["k"].cuda(), bad["v"].cuda())
+    c.fill(clean)
+    got, want = f64(layer.decode(c.query([n]))), f64(clean.decode(c.query([n])))
+    assert np.isnan(got[0, :2]).all()
+    assert np.array_equal(got[0, 2:], want[0, 2:])
+
+
 def test_bad_blocks_are_reported_and_skipped():
     from streaming_kv_cache_duo_gb300 import duo_device_error
     n, page = 600, 128

@@ -193,3 +193,56 @@ def test_refusals():
     layer.cache.n = 101
     with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
         call(layer.kv8)
+
+
+@pytest.mark.parametrize("B,T", [(1, 9), (2, 300)], ids=["split", "whole_blocks"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_non_finite_blocks_show_and_stay_with_their_head(B, T, which):
+    """An infinity in one cached token of one head: every output of that head's queries is NaN, also
+    where its block falls to one of several CTAs; the other heads and sequences are as ever."""
+    n = 1500
+    c = Batch(57, [n + T] * B, 4, 2, 128, 4, 32, [1, 1], "e4m3")
+    layer = _layer(c, n + T)
+    bad = {"k": c.kt.clone(), "v": c.vt.clone()}
+    bad[which][0, 70, 0] = float("inf")
+    layer.append(bad["k"][:, :n].contiguous().cuda(), bad["v"][:, :n].contiguous().cuda())
+    got = f64(_run(c, layer, n, T))
+    assert np.isnan(got[0, :, :2]).all()
+    assert np.isfinite(got[0, :, 2:]).all() and np.isfinite(got[1:]).all()
+    clean = _layer(c, n + T)
+    clean.append(c.kt[:, :n].contiguous().cuda(), c.vt[:, :n].contiguous().cuda())
+    want = f64(_run(c, clean, n, T))
+    assert np.array_equal(got[0, :, 2:], want[0, :, 2:]) and np.array_equal(got[1:], want[1:])
+
+
+def test_captured_chunk_append_and_decode():
+    """A chunk's prefill, its append and a decode as one graph, with the workspace that the capture was
+    given, replayed on other values than it was captured with: the same bits as the calls one by one."""
+    n, T = 900, 70
+    c = Batch(58, [n + T] * 2, 8, 2, 128, 4, 64, [1, 0], "int8")
+    eager, layer = _layer(c, n + T), _layer(c, n + T)
+    cut = lambda x: x[:, n:n + T].contiguous().cuda()
+    for x in (eager, layer):
+        x.append(c.kt[:, :n].contiguous().cuda(), c.vt[:, :n].contiguous().cuda())
+    q, k, v, last = cut(c.qt), cut(c.kt), cut(c.vt), c.query([n + T] * 2)
+    qs, ks, vs, ls = (torch.zeros_like(x) for x in (q, k, v, last))
+    warm = _layer(c, n + T)  # kernels loaded before the capture
+    warm.append(c.kt[:, :n].contiguous().cuda(), c.vt[:, :n].contiguous().cuda())
+    warm.prefill(q, k, v)
+    warm.append(k, v)
+    warm.decode(last)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer.prefill(qs, ks, vs)
+        layer.append(ks, vs)
+        dec = layer.decode(ls)
+    for dst, src in ((qs, q), (ks, k), (vs, v), (ls, last)):
+        dst.copy_(src)
+    graph.replay()
+    want = eager.prefill(q, k, v)
+    eager.append(k, v)
+    want_dec = eager.decode(last)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(dec, want_dec)
+    _check_chunk(c, n, T, out, [0, T - 1])
