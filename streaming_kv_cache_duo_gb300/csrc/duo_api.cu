@@ -425,13 +425,14 @@ struct Kv8Prefill {
   int64_t num_qt;  // query blocks per head (packed: per KV head)
   bool packed;
   int splits;
+  int short_by;    // tiles that an item's last part has fewer than its others
   int64_t parts;   // items x splits, if splits > 1
   size_t part_at;  // byte offset of the parts in the workspace
   size_t bytes;    // 0: no cached rows to read
 };
 static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
   const Shape& sh = h->sh;
-  Kv8Prefill w{pitch64(n), (T + (int64_t)kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, false, 1, 0, 0, 0};
+  Kv8Prefill w{pitch64(n), (T + (int64_t)kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, false, 1, 0, 0, 0, 0};
   if (n < 1 || T < 1 || sh.n_ret == 0) return w;
   w.part_at = ((size_t)2 * sh.B * sh.n_ret * w.plane_rows * sh.D * 2 + 255) / 256 * 256;
   // A CTA per item leaves SMs idle when items are few, and rows of the last query block idle when
@@ -454,11 +455,25 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
                           stream_tiles(kPrefillRowsPerCta)) * 9 / 10;
   const int64_t qt = ((int64_t)T * sh.g + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, items = heads * qt;
   for (int s = 1; s <= kPrefillMaxSplits && s <= cached && (s == 1 || items * s <= 8 * sms); ++s) {
-    const int64_t cost = makespan(items * s, (tiles + s - 1) / s + 3, others * qt, stream_tiles(kPrefillRowsPerCta / sh.g));
+    const int64_t ts = stream_tiles(kPrefillRowsPerCta / sh.g);
+    int64_t cost = makespan(items * s, (tiles + s - 1) / s + 3, others * qt, ts), short_by = 0;
+    // Or, with all parts in one round: the parts but the last ones on SMs of their own, the streaming
+    // items on the rest, and after them the last parts, shorter by what those SMs did before.
+    const int64_t left = sms - items * (s - 1);
+    if (s > 1 && others > 0 && items <= left) {
+      const int64_t rounds = (others * qt + left - 1) / left;  // streaming items of the busiest of them
+      const int64_t before = (items <= rounds * left - others * qt ? rounds - 1 : rounds) * ts;
+      const int64_t c = std::max((tiles + before + s - 1) / s + 3, rounds * ts);
+      if (before > 0 && c < cost && (s - 1) * before + s <= cached) {
+        cost = c;
+        short_by = before;
+      }
+    }
     if (cost < best) {
       best = cost;
       w.packed = true;
       w.splits = s;
+      w.short_by = (int)short_by;
     }
   }
   if (w.packed) w.num_qt = qt;
@@ -545,6 +560,7 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
       p.packed = plan.packed;
       while ((1 << p.log2_g) < sh.g) ++p.log2_g;
       p.splits = plan.splits;
+      p.short_by = plan.short_by;
       p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_at);
       p.part_ml = reinterpret_cast<float2*>(p.part_o + plan.parts * kPrefillRowsPerCta * sh.D);
       expand = e;
@@ -583,7 +599,7 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
   const int64_t ir = (kind_mask & 2) ? per_kind * sh.n_ret : 0;
   const int64_t is = (kind_mask & 1) ? per_kind * sh.n_str : 0;
   if (ir + is > 0x7fffffffLL) return fail(DUO_ERR_UNSUPPORTED, "too many query tiles for one launch");
-  p.items_r = (int)ir * std::max(1, p.splits);  // (splits > 1 only with few items)
+  p.items_r = (int)ir;
   p.items_s = (int)is;
   // about one wave of CTAs per KV head; at most num_qt, so qp_group x (items per block)
   // stays within the item count (an int)

@@ -165,6 +165,26 @@ __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
   return it;
 }
 
+// What a CTA does: an item (its index as item_of counts them) and its part of it (-1: all).
+// Retrieval items in splits come part by part; with shorter last parts those come behind the
+// streaming items, so that the SMs that took one of these take them.
+struct Part {
+  int idx, no;
+};
+template <int kMode>
+__device__ __forceinline__ Part part_of(const PrefillParams& p, int cta) {
+  if (kMode != kModePacked || p.splits == 1) return Part{cta, -1};
+  const int s = p.splits, long_parts = s - (p.short_by > 0), items = p.items_r;
+  if (cta < items * long_parts) return Part{cta / long_parts, cta % long_parts};
+  cta -= items * long_parts;
+  if (cta < p.items_s) return Part{items + cta, -1};
+  return Part{cta - p.items_s, s - 1};
+}
+// First tile of part `no` of an item of `total`: equal parts, the last one short_by shorter.
+__device__ __forceinline__ int part_start(const PrefillParams& p, int total, int no) {
+  return no == p.splits ? total : (int)((int64_t)no * (total + p.short_by) / p.splits);
+}
+
 // Chunk-local token of query row `row` (counted over the item's query blocks).
 template <int kMode>
 __device__ __forceinline__ int token_of(const PrefillParams& p, int row) {
@@ -415,12 +435,12 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // kModePacked: tiles [j0, j0 + ntiles) of the item; else all of them
-  const bool split = kMode == kModePacked && p.splits > 1 && (int)blockIdx.x < p.items_r;
-  const Item it = item_of<kMode>(p, split ? blockIdx.x / p.splits : blockIdx.x);
+  const Part part = part_of<kMode>(p, blockIdx.x);
+  const bool split = part.no >= 0;
+  const Item it = item_of<kMode>(p, part.idx);
   const TilePlan pl = plan_of<kMode>(p, it);
-  const int s_no = split ? blockIdx.x % p.splits : 0;
-  const int j0 = split ? (int)((int64_t)s_no * pl.total / p.splits) : 0;
-  const int share = split ? (int)((int64_t)(s_no + 1) * pl.total / p.splits) - j0 : pl.total;
+  const int j0 = split ? part_start(p, pl.total, part.no) : 0;
+  const int share = split ? part_start(p, pl.total, part.no + 1) - j0 : pl.total;
   // After any CTA of this kernel gave up a wait, later CTAs do no work, so a
   // failure ends in about one wait limit instead of one per CTA.
   const int ntiles = (*(volatile unsigned int*)err.word != 0u) ? 0 : share;
@@ -859,7 +879,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       tc_fence_after();
       const bool store = row_local < p.T;
       if (split) {  // this split's part, as it stands
-        const int64_t at = ((int64_t)blockIdx.x * kRows + x * BM + r);
+        const int64_t at = ((int64_t)part.idx * p.splits + part.no) * kRows + x * BM + r;
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -982,7 +1002,7 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
   }
   // the setmaxnreg split is sized for exactly this launch allocation
   if (regs != Roles<kMode>::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const int grid = p.items_r + p.items_s;
+  const int grid = p.items_r * (kMode == kModePacked ? p.splits : 1) + p.items_s;
   if (grid == 0) return cudaSuccess;
   if constexpr (kMode != kModePacked) {
     prefill_kernel<D, kMode><<<grid, Roles<kMode>::kThreads, smem, stream>>>(p);
@@ -1000,7 +1020,7 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, kMode>, p);
     if (e != cudaSuccess || p.splits <= 1) return e;
-    cfg.gridDim = dim3((unsigned)(p.items_r / p.splits * (kRows / 8)));
+    cfg.gridDim = dim3((unsigned)(p.items_r * (kRows / 8)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p);
