@@ -349,13 +349,18 @@ __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, con
   } else if (!it.streaming) {
     vis = bits_below((int)p.n - t.k * BN - c0);  // rows >= n hold no token
   } else {
-    const int32_t* prow = p.pos + (int64_t)it.b * (S + R);
-    vis = 0u;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int slot = t.k * BN + c0 + e;
-      const int jp = slot < p.nvalid ? __ldg(prow + slot) : -1;
-      vis |= (uint32_t)(jp >= 0 && jp <= i_abs && (jp < S || i_abs - jp < R)) << e;
+    // a lane reads one slot's position; most slots are seen by all of the warp's rows or by none
+    // (rows' positions rise with the lane), the few others are compared row by row
+    const int slot = t.k * BN + c0 + (int)(threadIdx.x & 31u);
+    const int jp = slot < p.nvalid ? __ldg(p.pos + (int64_t)it.b * (S + R) + slot) : -1;
+    const int i0 = __shfl_sync(0xffffffffu, i_abs, 0), i1 = __shfl_sync(0xffffffffu, i_abs, 31);
+    const bool all = jp >= 0 && jp <= i0 && (jp < S || i1 - jp < R);
+    const bool none = jp < 0 || jp > i1 || (jp >= S && i0 - jp >= R);
+    vis = __ballot_sync(0xffffffffu, all);
+    for (uint32_t some = __ballot_sync(0xffffffffu, !all && !none); some; some &= some - 1) {
+      const int e = __ffs((int)some) - 1;
+      const int j = __shfl_sync(0xffffffffu, jp, e);
+      vis |= (uint32_t)(j <= i_abs && (j < S || i_abs - j < R)) << e;
     }
   }
 #pragma unroll
