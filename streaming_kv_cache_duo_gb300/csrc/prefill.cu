@@ -336,7 +336,7 @@ __device__ __forceinline__ uint32_t bits_below(int hi) {
 // score; ring-cache slots are looked up one by one.
 template <int kMode>
 __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, const Item& it, const Tile& t, int c0,
-                                           int i_abs) {
+                                           int i_abs, int jp) {
   const int S = p.sh.S, R = p.sh.R;
   uint32_t vis;
   if (t.phase == 1 || (kMode == kModePool && it.streaming)) {
@@ -349,10 +349,8 @@ __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, con
   } else if (!it.streaming) {
     vis = bits_below((int)p.n - t.k * BN - c0);  // rows >= n hold no token
   } else {
-    // a lane reads one slot's position; most slots are seen by all of the warp's rows or by none
+    // a lane has one slot's position; most slots are seen by all of the warp's rows or by none
     // (rows' positions rise with the lane), the few others are compared row by row
-    const int slot = t.k * BN + c0 + (int)(threadIdx.x & 31u);
-    const int jp = slot < p.nvalid ? __ldg(p.pos + (int64_t)it.b * (S + R) + slot) : -1;
     const int i0 = __shfl_sync(0xffffffffu, i_abs, 0), i1 = __shfl_sync(0xffffffffu, i_abs, 31);
     const bool all = jp >= 0 && jp <= i0 && (jp < S || i1 - jp < R);
     const bool none = jp < 0 || jp > i1 || (jp >= S && i0 - jp >= R);
@@ -363,6 +361,8 @@ __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, con
       vis |= (uint32_t)(j <= i_abs && (j < S || i_abs - j < R)) << e;
     }
   }
+  // (a window's or the diagonal's edge crosses few of a warp's chunks)
+  if (__all_sync(0xffffffffu, vis == 0xffffffffu)) return;
 #pragma unroll
   for (int e = 0; e < 32; ++e)
     if (!((vis >> e) & 1u)) v[e] = -INFINITY;
@@ -812,6 +812,16 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     for (int j = 0; j < ntiles && ok; ++j) {
       const Tile t = tile_at<kMode>(pl, kMode == kModePacked ? j0 + j : j);
       const bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
+      // a ring tile: the positions its slots hold, -1 past the last (slot 32 q4 + lane)
+      int ring_pos[BN / 32];
+      if (kMode != kModePool && it.streaming && t.phase == 0) {
+        const int32_t* prow = p.pos + (int64_t)it.b * (p.sh.S + p.sh.R);
+#pragma unroll
+        for (int q4 = 0; q4 < BN / 32; ++q4) {
+          const int slot = t.k * BN + q4 * 32 + lane;
+          ring_pos[q4] = slot < p.nvalid ? __ldg(prow + slot) : -1;
+        }
+      }
       if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) {
         ok = false;
         break;
@@ -827,7 +837,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       }
       if (masked) {
 #pragma unroll
-        for (int q4 = 0; q4 < BN / 32; ++q4) mask_chunk<kMode>(v + q4 * 32, p, it, t, q4 * 32, i_abs);
+        for (int q4 = 0; q4 < BN / 32; ++q4) mask_chunk<kMode>(v + q4 * 32, p, it, t, q4 * 32, i_abs, ring_pos[q4]);
       }
       float mxa = v[0], mxb = v[1];
 #pragma unroll
