@@ -217,8 +217,9 @@ struct PrefillParams {
   int kv4;
   // contiguous caches, few tokens: query rows are tokens x heads of a KV head (tm_q's box is 64 x g x
   // 128 / g x 1, num_qt = ceil(T g / 256)), and retrieval items may be split over their key tiles
-  // (splits > 1): split s of item i leaves its unnormalised output (fp32 [256, D]) and (max, sum)
-  // rows at place i splits + s. The last split has short_by tiles fewer than the others.
+  // (splits > 1): split s of item i leaves its unnormalised output (fp32 [D / 4, 256 rows, 4]) and
+  // its rows' (max, sum) at place i splits + s. The last split has short_by tiles fewer than the
+  // others.
   int packed;
   int log2_g;
   int splits;

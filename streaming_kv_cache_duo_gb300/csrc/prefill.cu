@@ -894,8 +894,9 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       tc_fence_after();
       const bool store = row_local < p.T;
       if (split) {  // this split's part, as it stands
-        const int64_t at = ((int64_t)part.idx * p.splits + part.no) * kRows + x * BM + r;
-        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
+        // (four dims of a thread's row beside those of the next thread's: whole lines)
+        const int64_t at = (int64_t)part.idx * p.splits + part.no;
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * kRows * D) + x * BM + r;
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t ov[32];
@@ -903,11 +904,11 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
           if (store) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[q4 * 8 + e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
-                                            __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+              dst[(q4 * 8 + e) * kRows] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                                      __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
           }
         }
-        if (store) p.part_ml[at] = make_float2(m_run, l_run);
+        if (store) p.part_ml[at * kRows + x * BM + r] = make_float2(m_run, l_run);
       } else {
         const float inv = 1.f / l_run;
         const int head = kMode == kModePacked ? it.hq + (r & (p.sh.g - 1)) : it.hq;
@@ -938,63 +939,76 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   }
 }
 
-// The splits' parts of every row: O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s. A warp takes a row
-// of an item, a lane D / 32 of its dims; four splits are loaded at a time (all sixteen at once took
-// 119 registers, two CTAs per SM, and three times as long). Some splits of a row may have seen no key
-// (m = -inf, l = 0), never all of them.
+// The splits' parts of every row: O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s. A CTA takes 32
+// rows of an item, a lane a row and a warp D / 8 of the dims, in the parts' order; the outputs
+// pass through shared memory, so that they too are written in whole lines. Four splits are loaded
+// at a time. Some splits of a row may have seen no key (m = -inf, l = 0), never all of them.
+constexpr int kMergeRows = 32;
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
-  constexpr int V = D / 32, NB = 4;
-  const int item = blockIdx.x / (kRows / 8), row = blockIdx.x % (kRows / 8) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  constexpr int NB = 4, NV = D / 32;  // float4 per thread and split
+  __shared__ uint2 s_out[kMergeRows][D / 4 + 1];
+  const int item = blockIdx.x / (kRows / kMergeRows), row0 = blockIdx.x % (kRows / kMergeRows) * kMergeRows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Item it = item_of<kModePacked>(p, item);
-  const int row_local = token_of<kModePacked>(p, it.qp * kRows + row);
-  if (row_local >= p.T) return;
-  const int64_t at0 = (int64_t)item * p.splits * kRows + row;
-  const float2* ml_at = p.part_ml + at0;
-  const float* o_at = p.part_o + at0 * D + lane * V;
-  float acc[V], l = 0.f, M = -INFINITY;
+  const int first = it.qp * kRows + row0;  // query rows of the item
+  const int rows = min(kMergeRows, p.T * p.sh.g - first);
+  if (rows <= 0) return;
+  if (lane < rows) {
+    const int64_t at0 = (int64_t)item * p.splits;
+    const float2* ml_at = p.part_ml + at0 * kRows + row0 + lane;
+    const float4* o_at = reinterpret_cast<const float4*>(p.part_o + at0 * kRows * D) + row0 + lane;
+    float4 acc[NV];
+    float l = 0.f, M = -INFINITY;
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int s0 = 0; s0 < p.splits; s0 += NB) {
-    float2 ml[NB];
-    alignas(16) float o[NB][V];
-    float mn = M;
+    for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < p.splits; s0 += NB) {
+      float2 ml[NB];
+      float4 o[NB][NV];
+      float mn = M;
 #pragma unroll
-    for (int s = 0; s < NB; ++s) {
-      const bool there = s0 + s < p.splits;
-      ml[s] = there ? __ldcg(ml_at + (s0 + s) * kRows) : make_float2(-INFINITY, 0.f);
-      const float* src = o_at + (int64_t)(there ? s0 + s : 0) * kRows * D;
-      if constexpr (V == 4)
-        *reinterpret_cast<float4*>(o[s]) = __ldcg(reinterpret_cast<const float4*>(src));
-      else
-        *reinterpret_cast<float2*>(o[s]) = __ldcg(reinterpret_cast<const float2*>(src));
+      for (int s = 0; s < NB; ++s) {
+        const int k = s0 + s;
+        const bool there = k < p.splits;
+        ml[s] = there ? __ldcg(ml_at + k * kRows) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          o[s][v] = there ? __ldcg(o_at + ((int64_t)k * (D / 4) + warp * NV + v) * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int s = 0; s < NB; ++s) mn = fmaxf(mn, ml[s].x);
+      const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mn);
+      l *= keep;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) acc[v].x *= keep, acc[v].y *= keep, acc[v].z *= keep, acc[v].w *= keep;
+#pragma unroll
+      for (int s = 0; s < NB; ++s) {
+        const float f = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - mn);
+        l = fmaf(f, ml[s].y, l);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          acc[v].x = fmaf(f, o[s][v].x, acc[v].x);
+          acc[v].y = fmaf(f, o[s][v].y, acc[v].y);
+          acc[v].z = fmaf(f, o[s][v].z, acc[v].z);
+          acc[v].w = fmaf(f, o[s][v].w, acc[v].w);
+        }
+      }
+      M = mn;
     }
+    const float inv = 1.f / l;
 #pragma unroll
-    for (int s = 0; s < NB; ++s) mn = fmaxf(mn, ml[s].x);
-    const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mn);
-    l *= keep;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] *= keep;
-#pragma unroll
-    for (int s = 0; s < NB; ++s) {
-      const float f = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - mn);
-      l = fmaf(f, ml[s].y, l);
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, o[s][v], acc[v]);
-    }
-    M = mn;
+    for (int v = 0; v < NV; ++v)
+      s_out[lane][warp * NV + v] =
+          make_uint2(pack_bf16x2(acc[v].x * inv, acc[v].y * inv), pack_bf16x2(acc[v].z * inv, acc[v].w * inv));
   }
-  uint16_t* out = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + it.hq + (row & (p.sh.g - 1))) * D + lane * V;
-  const float inv = 1.f / l;
-  uint32_t w[V / 2];
-#pragma unroll
-  for (int v = 0; v < V; v += 2) w[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(out) = w[0];
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
+    const int r = e / (D / 4), c = e % (D / 4);
+    const int row = first + r;
+    const int64_t at = ((int64_t)it.b * p.T + token_of<kModePacked>(p, row)) * p.sh.Hq + it.hq + (row & (p.sh.g - 1));
+    reinterpret_cast<uint2*>(p.o + at * D)[c] = s_out[r][c];
+  }
 }
 
 template <int D, int kMode>
@@ -1035,7 +1049,7 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, kMode>, p);
     if (e != cudaSuccess || p.splits <= 1) return e;
-    cfg.gridDim = dim3((unsigned)(p.items_r * (kRows / 8)));
+    cfg.gridDim = dim3((unsigned)(p.items_r * (kRows / kMergeRows)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p);
