@@ -450,7 +450,8 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
     return (rounds + (rest > 0)) * tr + more;
   };
   const int64_t cached = tiles_of(n), tiles = cached + tiles_of(T);
-  const auto stream_tiles = [&](int64_t tokens) { return tiles_of(sh.S) + tiles_of(sh.R + tokens) + 1 + 3; };
+  // (every tile of a streaming item is masked: half as much again)
+  const auto stream_tiles = [&](int64_t tokens) { return (tiles_of(sh.S) + tiles_of(sh.R + tokens) + 1) * 3 / 2 + 3; };
   int64_t best = makespan(heads * sh.g * w.num_qt, tiles + 3, others * sh.g * w.num_qt,
                           stream_tiles(kPrefillRowsPerCta)) * 9 / 10;
   const int64_t qt = ((int64_t)T * sh.g + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, items = heads * qt;
