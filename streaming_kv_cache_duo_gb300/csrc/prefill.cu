@@ -449,6 +449,8 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   // After any CTA of this kernel gave up a wait, later CTAs do no work, so a
   // failure ends in about one wait limit instead of one per CTA.
   const int ntiles = (*(volatile unsigned int*)err.word != 0u) ? 0 : share;
+  // query tiles with rows: packed, the second one of the last block may have none
+  const int nq = kMode == kModePacked && p.T * p.sh.g - it.qp * kRows <= BM ? 1 : kQT;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
@@ -507,13 +509,15 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         prefetch_tmap(qmap);
         // each query tile is read by this CTA alone; K/V tiles by every CTA of the KV head
         const uint64_t pol_kv = l2_policy_evict_last();
-        mbar_arrive_expect_tx(&bars->q_full, kQT * C::Q_BYTES);
+        mbar_arrive_expect_tx(&bars->q_full, nq * C::Q_BYTES);
   #pragma unroll
-        for (int x = 0; x < kQT; ++x)
+        for (int x = 0; x < kQT; ++x) {
+          if (x >= nq) break;
   #pragma unroll
           for (int bx = 0; bx < C::NBOX; ++bx)
             tma_load_4d(sQ + x * C::Q_BYTES + bx * kBox, qmap, bx * 64, it.hq, token_of<kMode>(p, it.qp * kRows + x * BM),
                         it.b, &bars->q_full);
+        }
         bool ok = true;
         // paged: the block id of the next cache tile is read one tile ahead, so its
         // latency overlaps the wait for a free stage
@@ -726,7 +730,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
           if (ok) {
             tc_fence_after();
             issue_s(0, 0);
-            issue_s(1, 0);
+            if (nq > 1) issue_s(1, 0);
             tc_commit(&bars->k_empty[0]);
           }
         }
@@ -760,7 +764,9 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
             ok = false;
             break;
           }
-          for (int x = 0; x < kQT && ok; ++x) {
+#pragma unroll
+          for (int x = 0; x < kQT; ++x) {
+            if (x > 0 && (!ok || x >= nq)) break;
             if (!mbar_wait(&bars->p_full[x], (uint32_t)(j & 1), err, kErrPrefillMma)) {
               ok = false;
               break;
@@ -798,7 +804,8 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     const uint32_t sbase = lane_base + col_s(x);
     const uint32_t obase = lane_base + col_o(x);
     const int row_local = token_of<kMode>(p, it.qp * kRows + x * BM + r);  // chunk-local token of the query row
-    const int i_abs = (int)p.n + row_local;            // absolute position (< 2^31, checked on the host)
+    // absolute position (< 2^31, checked on the host); a row past the chunk takes the last one's
+    const int i_abs = (int)p.n + (kMode == kModePacked ? min(row_local, p.T - 1) : row_local);
     // DCA: the fp32 per-position scale joins softmax_scale on the fp32 product
     const float sl2 = (kMode == kModeDca && p.mscale && row_local < p.T)
                           ? p.scale_log2 * __ldg(p.mscale + (int64_t)it.b * p.T + row_local)
@@ -809,7 +816,18 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     float m_run = -INFINITY;  // running max of scaled scores (log2 units)
     float l_run = 0.f;
     bool ok = true;
-    for (int j = 0; j < ntiles && ok; ++j) {
+    // packed: a warp without a row of the chunk does no softmax (what its rows of S hold goes for P,
+    // and their O is not stored). In a loop of its own: a branch in the other one cost 1 %.
+    int my_tiles = x < nq ? ntiles : 0;
+    if (kMode == kModePacked && __shfl_sync(0xffffffffu, row_local, 0) >= p.T) {
+      for (int j = 0; j < my_tiles; ++j) {
+        if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[x]);
+      }
+      my_tiles = 0;
+    }
+    for (int j = 0; j < my_tiles && ok; ++j) {
       const Tile t = tile_at<kMode>(pl, kMode == kModePacked ? j0 + j : j);
       const bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
       // a ring tile: the positions its slots hold, -1 past the last (slot 32 q4 + lane)
@@ -890,7 +908,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       if (lane == 0) mbar_arrive(&bars->p_full[x]);
     }
     // ---------------------------------------------------------------- epilogue
-    if (ok && ntiles > 0 && mbar_wait(&bars->o_final[x], 0, err, kErrPrefillSoftmax)) {
+    if (ok && my_tiles > 0 && mbar_wait(&bars->o_final[x], 0, err, kErrPrefillSoftmax)) {
       tc_fence_after();
       const bool store = row_local < p.T;
       if (split) {  // this split's part, as it stands
