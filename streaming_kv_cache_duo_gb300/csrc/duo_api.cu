@@ -470,6 +470,7 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
         short_by = before;
       }
     }
+    if (s > 1) cost += s / 8;  // the merge reads them four at a time
     if (cost < best) {
       best = cost;
       w.packed = true;

@@ -170,7 +170,7 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 constexpr int kPrefillBM = 128;        // query rows per query tile
 constexpr int kPrefillBN = 128;        // keys per KV tile
 constexpr int kPrefillRowsPerCta = 256;  // two query tiles per CTA
-constexpr int kPrefillMaxSplits = 16;
+constexpr int kPrefillMaxSplits = 64;
 
 struct PrefillParams {
   CUtensorMap tm_q;      // 4-D over q [B, T, Hq, D], box 64 x 1 x 128 x 1, 128B swizzle
