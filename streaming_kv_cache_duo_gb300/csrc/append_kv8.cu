@@ -7,13 +7,17 @@
 // Until then its rows wait in bf16 in the tail. So the cache does not depend on how the
 // tokens were split into calls, and nothing stored is ever rounded again.
 //
-// Work: grid (chunk of consecutive tokens, one row of CTAs for the ring, then retrieval plane);
-// half of a CTA's threads do K, half V. The CTA that holds the token completing a block does
+// Work: grid (chunk of consecutive tokens, one row of CTAs for the ring, then K and V of each
+// retrieval plane). The CTA that holds the token completing a block does
 // that block: rows of this call from the packed input, earlier ones from the tail. The rows of
 // the block left open are written by the CTA of the sequence's last token, except when an
 // earlier block of this call reads the tail rows they replace: then by the CTA that read them,
 // after it. One pass: the block sits in registers (16 KB over 128 threads) between the maximum
-// and the codes. HBM-bound for prompts: 2 D bytes in, D out per row.
+// and the codes. HBM-bound for prompts: 2 D bytes in, D out per row. A prompt of 32K tokens with four
+// retrieval heads, D = 128: 26.6 us (e4m3), 25.2 (int8); HBM's share is 15. As many CTAs per SM as
+// registers allow without spills: seven (72 registers) at D = 128, ten at 64. K and V in one CTA of
+// 256 threads took 27.1 / 25.4 us, and 20.2 instead of 17.4 for 2 x 8192 tokens, eight heads, D = 64;
+// CTAs that fetch the next block's rows while they round the ones they have 32 / 28.
 #include "duo_device.cuh"
 
 namespace duo {
@@ -21,8 +25,7 @@ namespace {
 
 __device__ unsigned int g_append_kv8_err;
 
-constexpr int kThreads = 256;
-constexpr int kHalf = kThreads / 2;  // threads of K, and of V
+constexpr int kThreads = 128;
 constexpr int kBlk = kKv8Block;
 
 // Codes of values over their block's scale, rounded from the fp32 quotient x / scale. A division
@@ -140,14 +143,14 @@ __device__ __forceinline__ int64_t block_row(const Kv8AppendParams& p, const Tok
   return row >= 0 && row % kBlk == 0 && row + kBlk <= p.rows ? row : -1;
 }
 
-// tid: of the half. s_max: of the half, one word per warp.
+// s_max: one word per warp.
 template <int D, int CODE>
 __device__ __forceinline__ void complete_block(const Kv8AppendParams& p, const Token& t, int i, int r, int tid,
                                                const uint16_t* in, const uint16_t* tail, uint8_t* codes, float* scales,
                                                uint32_t* s_max) {
   constexpr int VPR = D / 8;                   // 16-byte vectors per row
-  constexpr int NV = kBlk * VPR / kHalf;       // vectors per thread
-  constexpr int RS = kHalf / VPR;              // rows between a thread's vectors
+  constexpr int NV = kBlk * VPR / kThreads;       // vectors per thread
+  constexpr int RS = kThreads / VPR;              // rows between a thread's vectors
   const int64_t row0 = block_row(p, t, i, r);  // (the same for every thread)
   if (row0 < 0) {
     if (tid == 0) atomicOr(&g_append_kv8_err, kErrBadBlock);
@@ -183,7 +186,7 @@ __device__ __forceinline__ void complete_block(const Kv8AppendParams& p, const T
   if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kHalf / 32; ++w) m = __vmaxu2(m, s_max[w]);
+  for (int w = 0; w < kThreads / 32; ++w) m = __vmaxu2(m, s_max[w]);
   m = max(m & 0xFFFFu, m >> 16);
   float scale = __fdiv_rn(__uint_as_float(m << 16), CODE == kKv8E4m3 ? 448.f : 127.f);
   const bool finite = m < 0x7F80u;
@@ -197,7 +200,7 @@ __device__ __forceinline__ void complete_block(const Kv8AppendParams& p, const T
   for (int k = 0; k < NV; ++k) {
     const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
     const uint2 c = zero ? make_uint2(0, 0) : encode8<CODE>(w, scale, inv, tiny);
-    *reinterpret_cast<uint2*>(dst + k * (kHalf * 8)) = c;
+    *reinterpret_cast<uint2*>(dst + k * (kThreads * 8)) = c;
   }
 }
 
@@ -210,7 +213,7 @@ __device__ __forceinline__ void write_tail(const Kv8AppendParams& p, const Token
   const int start = t.pos - (i - t.first);   // and before it
   const int lo = max(end / kBlk * kBlk, start);
   const int head = p.heads.ret_head[r];
-  for (int e = tid; e < (end - lo) * VPR; e += kHalf) {
+  for (int e = tid; e < (end - lo) * VPR; e += kThreads) {
     const int pos = lo + e / VPR, v = e % VPR;
     const int64_t src = t.first + (pos - start);
     *reinterpret_cast<uint4*>(tail + (pos % kBlk) * D + v * 8) =
@@ -219,7 +222,7 @@ __device__ __forceinline__ void write_tail(const Kv8AppendParams& p, const Token
 }
 
 template <int D, int CODE>
-__global__ void __launch_bounds__(kThreads, 4) append_kv8_kernel(const Kv8AppendParams p) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 10 : 7) append_kv8_kernel(const Kv8AppendParams p) {
   // as append_kernel: dependents may be scheduled now, and nothing is touched before the
   // grid before this one (a decode reading the tail or the ring) has ended
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -274,9 +277,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_kv8_kernel(const Kv8Append
     return;
   }
 
-  const int r = (int)blockIdx.y - (p.sh.n_str > 0);
-  const bool is_v = threadIdx.x >= kHalf;
-  const int tid = threadIdx.x % kHalf;
+  const int y = (int)blockIdx.y - (p.sh.n_str > 0);
+  const int r = y >> 1;
+  const bool is_v = y & 1;
+  const int tid = threadIdx.x;
   const uint16_t* in = is_v ? p.v_new : p.k_new;
   uint16_t* tails = is_v ? p.v_tail : p.k_tail;
   uint8_t* codes = is_v ? p.v_codes : p.k_codes;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kv8_kernel(const Kv8Append
     const int start = t.pos - (i - t.first);
     uint16_t* tail = tails + ((int64_t)t.b * n_ret + r) * kBlk * D;
     if (row == kBlk - 1) {
-      complete_block<D, CODE>(p, t, i, r, tid, in, tail, codes, scales, s_max + (is_v ? kHalf / 32 : 0));
+      complete_block<D, CODE>(p, t, i, r, tid, in, tail, codes, scales, s_max);
       // the block took rows from the tail: the new open block's rows go there after it
       if (t.pos - (kBlk - 1) < start && end_row != kBlk - 1) {
         __syncthreads();
@@ -308,7 +312,7 @@ cudaError_t launch_t(const Kv8AppendParams& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.tokens + p.chunk - 1) / p.chunk), (unsigned)(p.sh.n_ret + (p.sh.n_str > 0)));
+  cfg.gridDim = dim3((unsigned)((p.tokens + p.chunk - 1) / p.chunk), (unsigned)(2 * p.sh.n_ret + (p.sh.n_str > 0)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -123,6 +123,76 @@ def test_single_tokens_leave_the_same_cache_as_one_call(code):
         assert torch.equal(a, b), name
 
 
+@pytest.mark.parametrize("D,code,lead", [(64, "int8", 0), (128, "e4m3", 64), (64, "e4m3", 37), (128, "int8", 101)])
+def test_long_calls_leave_the_same_cache_as_short_ones(D, code, lead):
+    """Calls with more chunks than fit on the GPU at once, from a block's start and from inside one."""
+    B, Hkv, S, R, n = 2, 9, 70, 300, 9000 + 17
+    kinds = [1, 1, 0, 1, 1, 1, 1, 1, 1]
+    rng = np.random.default_rng(60)
+    kt, vt = (normal(rng, B, lead + n, Hkv, D)[0].cuda() for _ in range(2))
+    cut = lambda x, a, b: x[:, a:b].contiguous()
+    one, many = (_layer(B, Hkv, D, S, R, kinds, lead + n, code) for _ in range(2))
+    for layer in (one, many):
+        _mark(layer)
+        if lead:
+            layer.append(cut(kt, 0, lead), cut(vt, 0, lead))
+    one.append(cut(kt, lead, lead + n), cut(vt, lead, lead + n))
+    for t in range(lead, lead + n, 1000):
+        many.append(cut(kt, t, min(t + 1000, lead + n)), cut(vt, t, min(t + 1000, lead + n)))
+    open_rows = (lead + n) % BLOCK
+    for name in BUFFERS:
+        a, b = getattr(one, name).view(torch.uint8), getattr(many, name).view(torch.uint8)
+        if "tail" in name:
+            a, b = a[:, :, :open_rows], b[:, :, :open_rows]
+        assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_long_ragged_calls_leave_the_same_cache_as_short_ones(code):
+    """A packed batch of many sequences (none, one or thousands of new tokens, from anywhere in a
+    block, skipped ones between) in one call, and sequence by sequence."""
+    from streaming_kv_cache_duo_gb300 import duo_device_error
+    B, Hkv, D, S, R, page = 40, 9, 64, 4, 32, 128
+    kinds = [1, 1, 1, 1, 0, 1, 1, 1, 1]
+    rng = np.random.default_rng(61)
+    start = [int(x) for x in rng.integers(0, 200, B)]
+    new = [int(x) for x in rng.choice([0, 1, 5, 63, 64, 65, 300, 700], B)]
+    new[3], new[20] = 3000, 2049
+    skip = (5, 21)
+    cap = max(s + t for s, t in zip(start, new))
+    mb = -(-cap // page)
+    table, _ = scattered_table(rng, B, 8, mb)
+    from streaming_kv_cache_duo_gb300 import DuoKv8PagedLayer
+    nb = int(table.max()) + 1
+    layers = [DuoKv8PagedLayer(B, Hkv, Hkv, D, S, R, page, mb, nb, table, kinds, code=code) for _ in range(2)]
+    total = sum(new)
+    assert total > 8700
+    kt, vt = (torch.from_numpy(rng.standard_normal((sum(start) + total, Hkv, D)).astype(np.float32)).bfloat16().cuda()
+              for _ in range(2))
+    first = sum(start)
+    for layer in layers:
+        _mark(layer)
+        layer.append_ragged(kt[:first].contiguous(), vt[:first].contiguous(), _maps(table, page, [0] * B, start))
+    layers[0].append_ragged(kt[first:].contiguous(), vt[first:].contiguous(), _maps(table, page, start, new, skip=skip))
+    at = first
+    for b in range(B):
+        if new[b] and b not in skip:
+            alone = [new[b] if i == b else 0 for i in range(B)]
+            layers[1].append_ragged(kt[at:at + new[b]].contiguous(), vt[at:at + new[b]].contiguous(),
+                                    _maps(table, page, start, alone))
+        at += new[b]
+    torch.cuda.synchronize()
+    assert duo_device_error() == 0
+    held = [s + (0 if b in skip else t) for b, (s, t) in enumerate(zip(start, new))]
+    for name in BUFFERS:
+        a, b = (getattr(x, name).view(torch.uint8) for x in layers)
+        if "tail" in name:
+            for i, n in enumerate(held):
+                assert torch.equal(a[i, :, :n % BLOCK], b[i, :, :n % BLOCK]), (name, i)
+        else:
+            assert torch.equal(a, b), name
+
+
 def _edge_block(kind, D, rng):
     """64 rows [64, D] of bf16 values where the rounding can go wrong."""
     x = rng.standard_normal((BLOCK, D))
