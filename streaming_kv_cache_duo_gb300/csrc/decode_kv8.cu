@@ -11,12 +11,15 @@
 // without that room, the last CTAs had most of them: 119 us for a million tokens, 100 us with it.)
 //
 // Eight warps, each with its own slice of every tile (32 or 64 keys of codes, or 16 bf16 rows) and
-// its own ring of three stages (K and V, 8 KB together) that it refills itself; no warp waits for
-// another. Codes come by TMA through a swizzled map, so that the matrix loads below are free of
-// bank conflicts while the rows in HBM stay plain row-major, their two scales by 4-byte
-// asynchronous copies on the same barrier; bf16 rows by 16-byte ones, swizzled by their addresses.
+// its own ring of two stages (K and V, 8 KB together) that it refills itself; no warp waits for
+// another. Two, for fairness: with three, 128 KB or more on their way into every SM, some SMs got
+// their bytes a fifth slower than others and the last one ended late (eight sequences of 131072
+// tokens, e4m3: 75 us on average, 85 at most; 93 us against 86 in all).
+// Codes come by TMA through a swizzled map, so that the matrix loads below are free of bank
+// conflicts while the rows in HBM stay plain row-major, their two scales by 4-byte asynchronous
+// copies on the same barrier; bf16 rows by 16-byte ones, swizzled by their addresses.
 // (Twelve warps of 168 registers with two stages each were no faster: 93 us against 88 us for a
-// million tokens. D = 64 with 32-key slices paid every slice's fixed cost twice: 59 us against 35 us
+// million tokens then. D = 64 with 32-key slices paid every slice's fixed cost twice: 59 us against 35 us
 // for 11 x 110556 tokens.)
 //
 // Per slice, on warp-level tensor-core products (a decode has one to eight query heads per
@@ -36,8 +39,8 @@
 //
 // bf16 rows (at most 63 of a tail, S + R of a ring) take bf16 products. Only these need masks.
 //
-// Bound by HBM: one million tokens with two retrieval heads, int8, 88 us = 6.1 TB/s of the 538 MB
-// stored (0.90 of the measured copy rate; a CTA works through a tile in 1.34 us, 7.4 TB/s in all).
+// Bound by HBM: one million tokens with two retrieval heads, int8, 86 us = 6.3 TB/s of the 538 MB
+// stored (0.92 of the measured copy rate; a CTA works through a tile in 1.3 us, 7.5 TB/s in all).
 // What is left is fixed: 2.8 us until a CTA's first tiles are under way, a merge of 0.8 us, the
 // second kernel and two launches, 8 us.
 //
@@ -59,7 +62,7 @@ __device__ unsigned int g_decode_kv8_err;
 
 constexpr int kWarps = kKv8Warps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 // units of at most this many tiles are not split (their merge would cost more)
 constexpr int kShortTiles = 4;
 // p is kept times 2^kPShift: fp16 then holds it down to 2^-(24 + kPShift) of the row maximum,
