@@ -51,6 +51,7 @@
 // kernel at most per CTA of the first, however many units there are.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "duo_device.cuh"
@@ -65,6 +66,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
 // units of at most this many tiles are not split (their merge would cost more)
 constexpr int kShortTiles = 4;
+// weight of a place of a retrieval unit on the line of tiles, and the least that a CTA's share
+// weighs: 2.5 places, so two of them whole wherever it begins
+constexpr int kPlace = 8;
+constexpr int kLeast = 20;
 // p is kept times 2^kPShift: fp16 then holds it down to 2^-(24 + kPShift) of the row maximum,
 // and up to 2^8 (lazy rescale) x 2^kPShift = 2^15
 constexpr float kPShift = 7.f;
@@ -265,35 +270,47 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
   return div64(ab, c);
 }
 
-// This CTA's share of the line, places [x0, x1) of W, shared by C CTAs (each gets at least two
-// places, so none inside a unit's span is left without a tile of it), starting in unit u at ub.
+// This CTA's share of the line of Wr places of retrieval units and W - Wr of streaming ones, places
+// [x0, x1), starting in unit u at ub. The line is cut by weight: a retrieval place weighs kPlace, a
+// streaming one p.str_place, WW in all. Each of the C CTAs that share
+// it gets at least two places, so none inside a unit's span is left without a tile of it.
 struct Share {
-  int64_t W, x0, x1, ub;
+  int64_t W, Wr, WW, x0, x1, ub;
   int C, u;
 };
-__device__ __forceinline__ int cta_of(const Share& s, int64_t x) {
-  const int64_t a = (x + 1) * s.C - 1;
-  return (int)mul_div(a, 1, s.W);
+// The CTA with place x.
+__device__ __forceinline__ int cta_of(const Kv8DecodeParams& p, const Share& s, int64_t x) {
+  const int64_t str = x + 1 - s.Wr;
+  const int64_t end = str > 0 ? s.Wr * kPlace + str * p.str_place : (x + 1) * kPlace;  // weight up to its end
+  return (int)mul_div(end * s.C - 1, 1, s.WW);
 }
-__device__ __forceinline__ void cut(Share& s, int ctas) {
+// The place in which weight w lies.
+__device__ __forceinline__ int64_t place_at(const Kv8DecodeParams& p, const Share& s, int64_t w) {
+  const int64_t str = w - s.Wr * kPlace;
+  return str >= 0 ? s.Wr + mul_div(str, 1, p.str_place) : w / kPlace;
+}
+__device__ __forceinline__ void cut(const Kv8DecodeParams& p, Share& s, int64_t Wr, int64_t Ws) {
   const int c = blockIdx.x;
-  s.C = (int)(ctas < s.W / 2 ? ctas : s.W / 2);
-  s.x0 = c < s.C ? mul_div(c, s.W, s.C) : s.W;
-  s.x1 = c < s.C ? mul_div(c + 1, s.W, s.C) : s.W;
+  s.Wr = Wr;
+  s.W = Wr + Ws;
+  s.WW = Wr * kPlace + Ws * p.str_place;
+  const int64_t most = s.WW / kLeast;
+  s.C = (int)(p.C < most ? p.C : (most > 1 ? most : 1));
+  s.x0 = c < s.C ? place_at(p, s, mul_div(c, s.WW, s.C)) : s.W;
+  s.x1 = c < s.C ? place_at(p, s, mul_div(c + 1, s.WW, s.C)) : s.W;
 }
 
 template <int D>
 __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
   Share s;
   if (p.whole) {
-    s.W = s.x0 = s.x1 = s.ub = 0;
+    s.W = s.Wr = s.WW = s.x0 = s.x1 = s.ub = 0;
     s.C = p.C;
     s.u = blockIdx.x;
     return s;
   }
   if (!p.seq_lens) {
-    s.W = p.line_r + p.line_s;
-    cut(s, p.C);
+    cut(p, s, p.line_r, p.line_s);
     const bool in_r = s.x0 < p.line_r;
     const int64_t at = in_r ? s.x0 : s.x0 - p.line_r;
     const int64_t per = (in_r ? p.tiles_r : p.tiles_s) + 1;
@@ -332,8 +349,7 @@ __device__ Share share_of(const Kv8DecodeParams& p, int64_t* scratch) {
     Wr += scratch[w];
     Wq += scratch[kWarps + w];
   }
-  s.W = Wr + Wq;
-  cut(s, p.C);
+  cut(p, s, Wr, Wq);
   const bool in_r = s.x0 < Wr && s.x0 >= r - r_own && s.x0 < r;
   const bool in_q = s.x0 >= Wr && s.x0 - Wr >= q - q_own && s.x0 - Wr < q;
   if (in_r || in_q) {
@@ -875,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     // one while another still reads this one, and is past the barrier between before its turn
     st.finish();
     int n_parts = 1;
-    if (!p.whole && (lt0 > 0 || lt1 < x.tiles)) n_parts = cta_of(sh, ub + x.tiles) - cta_of(sh, ub) + 1;
+    if (!p.whole && (lt0 > 0 || lt1 < x.tiles)) n_parts = cta_of(p, sh, ub + x.tiles) - cta_of(p, sh, ub) + 1;
     float* part = p.partials + (int64_t)(2 * blockIdx.x + (lt0 == 0)) * G * C::PS;
     if (lt0 == 0 && p.merge_units) {
       if (tid == 0) *job_of(p, x.u) = make_int2(blockIdx.x, n_parts);
@@ -1070,7 +1086,11 @@ void plan_decode_kv8(Kv8DecodeParams* p, int num_sms) {
   p->line_r = (int64_t)p->U_r * (p->tiles_r + 1);
   p->line_s = (int64_t)p->U_s * (p->tiles_s + 1);
   p->whole = U <= num_sms && (p->U_r == 0 || p->tiles_r <= kShortTiles) && (p->U_s == 0 || p->tiles_s <= kShortTiles);
-  const int64_t most = (p->line_r + p->line_s) / 2;  // two places each at least
+  // int8 codes take a fifth longer per tile than e4m3's or a ring's rows (a streaming unit of one
+  // tile costs its two places all the same): 128 ragged sequences of up to 700 tokens 49.2 us with
+  // even places, 46.5 so; 48 of up to 32000 84.3, 83.1; e4m3 so 79.3 instead of 75.6
+  p->str_place = p->code_type == kKv8Int8 && p->sh.S + p->sh.R > kKv8TKBf16 ? kPlace - 1 : kPlace;
+  const int64_t most = std::max<int64_t>(1, (p->line_r * kPlace + p->line_s * p->str_place) / kLeast);
   p->C = (int)(p->whole ? U : (most < num_sms ? most : num_sms));
   // merge by unit, 32 dims a CTA, where that is no more than a CTA per SM
   p->merge_units = U <= p->C && U * p->sh.g * (p->sh.D / 32) <= num_sms;

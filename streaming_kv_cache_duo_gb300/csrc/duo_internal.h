@@ -306,6 +306,7 @@ struct Kv8DecodeParams {
   int merge_units;          // merge jobs are by unit, not by CTA
   int tiles_r, tiles_s;     // tiles of a unit of each kind at n tokens
   int64_t line_r, line_s;   // places that all units of each kind take on the line of tiles
+  int str_place;            // weight of a streaming unit's place (a retrieval one weighs 8)
   int code_type;
   int64_t cap64;
   float scale_log2;  // log2(e) / sqrt(D)
