@@ -413,13 +413,14 @@ duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* ca
                                       const void* q, void* o, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Prefill of T new tokens against 8-bit caches, as duo_attn_prefill: the cache's rows are
- * code * scale in fp32 rounded to bf16 (tail and ring rows are bf16 already), the T new
- * tokens' k and v the bf16 inputs. Append the chunk afterwards. The rows are written as bf16
- * to `workspace` once and read from there by every query block; retrieval heads with few
+ * code * scale (tail and ring rows are bf16), the T new tokens' k and v the bf16 inputs.
+ * Append the chunk afterwards. The codes are written to `workspace` once, as bf16 times the
+ * power of two in their scale (exact; the rest of the scale is applied in fp32, V's to p before
+ * p is rounded to bf16), and read from there by every query block; retrieval heads with few
  * query blocks are split over their keys, their parts merged by log-sum-exp. workspace:
  * device memory of duo_prefill_kv8_workspace_size(handle, cache->n, T) bytes, 256-byte
  * aligned (may be NULL if that is 0: nothing cached, or no retrieval head): 4 D bytes per
- * cached token and retrieval head of the layer, plus the parts (at most 8 per SM, and none when
+ * cached token and retrieval head of the layer, 8 per 64 of them, plus the parts (at most 8 per SM, and none when
  * the split would not pay, so a longer cache can need less: ask for each n and T). Nothing in it
  * survives the call; calls sharing one must be ordered on the GPU. o must not overlap q, k or v. */
 size_t duo_prefill_kv8_workspace_size(const duo_handle* handle, int64_t n, int32_t T);

@@ -427,14 +427,17 @@ struct Kv8Prefill {
   int splits;
   int short_by;    // tiles that an item's last part has fewer than its others
   int64_t parts;   // items x splits, if splits > 1
-  size_t part_at;  // byte offset of the parts in the workspace
+  size_t fac_at;   // byte offsets in the workspace: of the factors,
+  size_t part_at;  // and of the parts
   size_t bytes;    // 0: no cached rows to read
 };
 static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
   const Shape& sh = h->sh;
-  Kv8Prefill w{pitch64(n), (T + (int64_t)kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, false, 1, 0, 0, 0, 0};
+  Kv8Prefill w{pitch64(n), (T + (int64_t)kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, false, 1, 0, 0, 0, 0, 0};
   if (n < 1 || T < 1 || sh.n_ret == 0) return w;
-  w.part_at = ((size_t)2 * sh.B * sh.n_ret * w.plane_rows * sh.D * 2 + 255) / 256 * 256;
+  const size_t rows = (size_t)2 * sh.B * sh.n_ret * w.plane_rows;  // of K and V
+  w.fac_at = rows * sh.D * 2;
+  w.part_at = (w.fac_at + rows / kKv8Block * sizeof(float) + 255) / 256 * 256;
   // A CTA per item leaves SMs idle when items are few, and rows of the last query block idle when
   // tokens are: a short turn after a long conversation (333 tokens after 9001, two sequences, four
   // retrieval heads, g = 4) is 64 items of 75 tiles, half of them with 77 rows of 256. Packed it is
@@ -548,6 +551,8 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
       e.v_tail = static_cast<const uint16_t*>(kv8->v_tail);
       e.k_out = static_cast<uint16_t*>(workspace);
       e.v_out = e.k_out + plan.plane_rows * sh.B * sh.n_ret * sh.D;
+      e.k_fac = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.fac_at);
+      e.v_fac = e.k_fac + plan.plane_rows / kKv8Block * sh.B * sh.n_ret;
       e.n = (int)c->n;
       e.planes = sh.B * sh.n_ret;
       e.D = sh.D;
@@ -559,8 +564,10 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
         return fail(DUO_ERR_UNSUPPORTED, "the cached rows of all sequences and retrieval heads reach 2^31");
       if ((st = encode_cache(h, &p.tm_kfull, e.k_out, planes, plan.plane_rows, c->n, sh.D)) != DUO_OK) return st;
       if ((st = encode_cache(h, &p.tm_vfull, e.v_out, planes, plan.plane_rows, c->n, sh.D)) != DUO_OK) return st;
-      p.packed = plan.packed;
-      while ((1 << p.log2_g) < sh.g) ++p.log2_g;
+      p.k_fac = e.k_fac;
+      p.v_fac = e.v_fac;
+      p.fac_blocks = (int)(plan.plane_rows / kKv8Block);
+      while (plan.packed && (1 << p.log2_g) < sh.g) ++p.log2_g;
       p.splits = plan.splits;
       p.short_by = plan.short_by;
       p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_at);

@@ -215,13 +215,16 @@ struct PrefillParams {
   int64_t cap16;
   int sr16;
   int kv4;
-  // contiguous caches, few tokens: query rows are tokens x heads of a KV head (tm_q's box is 64 x g x
+  // 8-bit caches (k_fac != nullptr): factors per 64 cached rows, [B n_ret, fac_blocks] (V's as log2).
+  // For few tokens query rows are tokens x heads of a KV head (log2_g > 0: tm_q's box is 64 x g x
   // 128 / g x 1, num_qt = ceil(T g / 256)), and retrieval items may be split over their key tiles
   // (splits > 1): split s of item i leaves its unnormalised output (fp32 [D / 4, 256 rows, 4]) and
   // its rows' (max, sum) at place i splits + s. The last split has short_by tiles fewer than the
   // others.
-  int packed;
-  int log2_g;
+  const float* k_fac;
+  const float* v_fac;
+  int fac_blocks;
+  int log2_g;  // of the query heads that share query rows: g, or 1
   int splits;
   int short_by;
   float* part_o;
@@ -276,8 +279,10 @@ struct Kv8ExpandParams {
   const float* v_scale;
   const uint16_t* k_tail;
   const uint16_t* v_tail;
-  uint16_t* k_out;  // bf16 [planes, n rounded up to 64, D]
+  uint16_t* k_out;  // bf16 [planes, n rounded up to 64, D]: code times the power of two in the scale
   uint16_t* v_out;
+  float* k_fac;     // [planes, blocks]: what is left of K's scales,
+  float* v_fac;     // and the logarithm (base 2) of what is left of V's
   int n, planes, D;
   int code_type;
   int64_t cap64;

@@ -65,10 +65,11 @@ constexpr int kModePaged = 1;  // retrieval caches in a paged pool (block table)
 constexpr int kModePool = 2;   // both head kinds in the paged pool
 constexpr int kModeDca = 3;    // Dual Chunk Attention: one of three query vectors per key tile
 constexpr int kModeKv4 = 4;    // 4-bit caches: cache tiles dequantized into shared memory by warps 10, 11
-// plain, for few tokens: the query heads of a KV head share query blocks (row = token x g + head, so a
-// block holds 256 / g tokens and a short chunk fills it), and each retrieval item's key tiles may be
-// shared by several CTAs, their parts merged after
-constexpr int kModePacked = 5;
+// 8-bit caches: the cached rows are bf16 codes times a power of two (exact), with a factor for K and one
+// for V per 64 of them; K's multiplies the scores, V's goes into P. For few tokens the query heads of a
+// KV head share query blocks (row = token x g + head, so a block holds 256 / g tokens and a short chunk
+// fills it), and each retrieval item's key tiles may be shared by several CTAs, their parts merged after
+constexpr int kModeKv8 = 5;
 constexpr int kWarpDeq = 10;   // first of the dequantizing warps (4-bit caches): 10 ... 15
 template <int kMode>
 struct Roles {
@@ -125,7 +126,7 @@ struct Item {
 template <int kMode>
 __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
   Item it;
-  const int g = kMode == kModePacked ? 1 : p.sh.g;  // items per KV head and query block
+  const int g = kMode == kModeKv8 ? p.sh.g >> p.log2_g : p.sh.g;  // items per KV head and query block
   int nk;
   if (idx < p.items_r) {
     it.streaming = false;
@@ -151,7 +152,7 @@ __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
     it.b = bc / nk;
     it.cidx = bc % nk;
     it.kvh = p.heads.ret_head[it.cidx];
-    it.hq = kMode == kModePacked ? it.kvh * p.sh.g : it.kvh * g + (r % g);
+    it.hq = it.kvh * p.sh.g + (r % g);
     return it;
   }
   const int qp_rev = idx / per_qp;  // longest query blocks first
@@ -161,7 +162,7 @@ __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
   r %= nk * g;
   it.cidx = r / g;
   it.kvh = it.streaming ? p.heads.str_head[it.cidx] : p.heads.ret_head[it.cidx];
-  it.hq = kMode == kModePacked ? it.kvh * p.sh.g : it.kvh * g + (r % g);
+  it.hq = it.kvh * p.sh.g + (r % g);
   return it;
 }
 
@@ -173,7 +174,7 @@ struct Part {
 };
 template <int kMode>
 __device__ __forceinline__ Part part_of(const PrefillParams& p, int cta) {
-  if (kMode != kModePacked || p.splits == 1) return Part{cta, -1};
+  if (kMode != kModeKv8 || p.splits == 1) return Part{cta, -1};
   const int s = p.splits, long_parts = s - (p.short_by > 0), items = p.items_r;
   if (cta < items * long_parts) return Part{cta / long_parts, cta % long_parts};
   cta -= items * long_parts;
@@ -188,7 +189,7 @@ __device__ __forceinline__ int part_start(const PrefillParams& p, int total, int
 // Chunk-local token of query row `row` (counted over the item's query blocks).
 template <int kMode>
 __device__ __forceinline__ int token_of(const PrefillParams& p, int row) {
-  return kMode == kModePacked ? row >> p.log2_g : row;
+  return kMode == kModeKv8 ? row >> p.log2_g : row;
 }
 
 // The KV tiles a CTA visits: first tiles of the cache (phase 0), then tiles of
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   const DevError err{&g_prefill_err};
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // kModePacked: tiles [j0, j0 + ntiles) of the item; else all of them
+  // kModeKv8: tiles [j0, j0 + ntiles) of the item; else all of them
   const Part part = part_of<kMode>(p, blockIdx.x);
   const bool split = part.no >= 0;
   const Item it = item_of<kMode>(p, part.idx);
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   // failure ends in about one wait limit instead of one per CTA.
   const int ntiles = (*(volatile unsigned int*)err.word != 0u) ? 0 : share;
   // query tiles with rows: packed, the second one of the last block may have none
-  const int nq = kMode == kModePacked && p.T * p.sh.g - it.qp * kRows <= BM ? 1 : kQT;
+  const int nq = kMode == kModeKv8 && (p.T << p.log2_g) - it.qp * kRows <= BM ? 1 : kQT;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  if (kMode == kModePacked) {
+  if (kMode == kModeKv8) {
     // launched as a programmatic dependent of the kernel that writes the cached rows as bf16; the merge
     // of the splits may be scheduled once every CTA is here
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         int j = 0;
         int rc = 0;  // 4-bit caches: raw tiles staged so far
         for (; j < ntiles && ok; ++j) {
-          const Tile t = tile_at<kMode>(pl, kMode == kModePacked ? j0 + j : j);
+          const Tile t = tile_at<kMode>(pl, kMode == kModeKv8 ? j0 + j : j);
           if (kMode == kModeDca) {
             const int v = dt.var(j);
             if (v != qvar) {
@@ -805,21 +806,23 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     const uint32_t obase = lane_base + col_o(x);
     const int row_local = token_of<kMode>(p, it.qp * kRows + x * BM + r);  // chunk-local token of the query row
     // absolute position (< 2^31, checked on the host); a row past the chunk takes the last one's
-    const int i_abs = (int)p.n + (kMode == kModePacked ? min(row_local, p.T - 1) : row_local);
+    const int i_abs = (int)p.n + (kMode == kModeKv8 ? min(row_local, p.T - 1) : row_local);
     // DCA: the fp32 per-position scale joins softmax_scale on the fp32 product
     const float sl2 = (kMode == kModeDca && p.mscale && row_local < p.T)
                           ? p.scale_log2 * __ldg(p.mscale + (int64_t)it.b * p.T + row_local)
                           : p.scale_log2;
     // diagonal tile of this query tile (packed: the first it has)
-    const int q_last = kMode == kModePacked ? token_of<kMode>(p, it.qp * kRows + x * BM) / BN
+    const int q_last = kMode == kModeKv8 ? token_of<kMode>(p, it.qp * kRows + x * BM) / BN
                                             : (x == 0 ? it.qp * kQT : it.qp * kQT + 1);
     float m_run = -INFINITY;  // running max of scaled scores (log2 units)
     float l_run = 0.f;
     bool ok = true;
+    // factors of 32 blocks (16 tiles) of an 8-bit cache, one per lane: K's, and the logarithm of V's
+    float fk = 1.f, lf = 0.f;
     // packed: a warp without a row of the chunk does no softmax (what its rows of S hold goes for P,
     // and their O is not stored). In a loop of its own: a branch in the other one cost 1 %.
     int my_tiles = x < nq ? ntiles : 0;
-    if (kMode == kModePacked && __shfl_sync(0xffffffffu, row_local, 0) >= p.T) {
+    if (kMode == kModeKv8 && __shfl_sync(0xffffffffu, row_local, 0) >= p.T) {
       for (int j = 0; j < my_tiles; ++j) {
         if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) break;
         __syncwarp();
@@ -828,8 +831,23 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       my_tiles = 0;
     }
     for (int j = 0; j < my_tiles && ok; ++j) {
-      const Tile t = tile_at<kMode>(pl, kMode == kModePacked ? j0 + j : j);
+      const Tile t = tile_at<kMode>(pl, kMode == kModeKv8 ? j0 + j : j);
       const bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
+      // log2 units per unit of score in the tile's halves, and what V's factors add to P's exponent
+      float sl2h[2] = {sl2, sl2}, lfh[2] = {0.f, 0.f};
+      if (kMode == kModeKv8 && !it.streaming && t.phase == 0) {
+        if (j == 0 || (t.k & 15) == 0) {
+          const int blk = (t.k & ~15) * 2 + lane;
+          const int64_t at = ((int64_t)it.b * p.sh.n_ret + it.cidx) * p.fac_blocks + blk;
+          fk = blk < p.fac_blocks ? __ldg(p.k_fac + at) : 1.f;
+          lf = blk < p.fac_blocks ? __ldg(p.v_fac + at) : 0.f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sl2h[h] *= __shfl_sync(0xffffffffu, fk, (t.k & 15) * 2 + h);
+          lfh[h] = __shfl_sync(0xffffffffu, lf, (t.k & 15) * 2 + h);
+        }
+      }
       // a ring tile: the positions its slots hold, -1 past the last (slot 32 q4 + lane)
       int ring_pos[BN / 32];
       if (kMode != kModePool && it.streaming && t.phase == 0) {
@@ -857,15 +875,32 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
 #pragma unroll
         for (int q4 = 0; q4 < BN / 32; ++q4) mask_chunk<kMode>(v + q4 * 32, p, it, t, q4 * 32, i_abs, ring_pos[q4]);
       }
-      float mxa = v[0], mxb = v[1];
+      float mx_s;
+      if constexpr (kMode == kModeKv8) {
+        float mxh[2];
 #pragma unroll
-      for (int e = 2; e < BN; e += 4) {
-        mxa = max3(mxa, v[e], v[e + 1]);
-        if (e + 3 < BN) mxb = max3(mxb, v[e + 2], v[e + 3]);
-        else mxb = fmaxf(mxb, v[e + 2]);
+        for (int h = 0; h < 2; ++h) {
+          const float* w = v + h * (BN / 2);
+          float mxa = w[0], mxb = w[1];
+#pragma unroll
+          for (int e = 2; e + 3 < BN / 2; e += 4) {
+            mxa = max3(mxa, w[e], w[e + 1]);
+            mxb = max3(mxb, w[e + 2], w[e + 3]);
+          }
+          mxh[h] = max3(fmaxf(mxa, mxb), w[BN / 2 - 2], w[BN / 2 - 1]) * sl2h[h];
+        }
+        mx_s = fmaxf(mxh[0], mxh[1]);
+      } else {
+        float mxa = v[0], mxb = v[1];
+#pragma unroll
+        for (int e = 2; e < BN; e += 4) {
+          mxa = max3(mxa, v[e], v[e + 1]);
+          if (e + 3 < BN) mxb = max3(mxb, v[e + 2], v[e + 3]);
+          else mxb = fmaxf(mxb, v[e + 2]);
+        }
+        const float mx = fmaxf(mxa, mxb);
+        mx_s = mx * sl2;
       }
-      const float mx = fmaxf(mxa, mxb);
-      const float mx_s = mx * sl2;
       float f = 1.f;
       if (mx_s > m_run + 8.f) {
         f = ex2_approx(m_run - mx_s);  // 0 while nothing was visible
@@ -886,9 +921,20 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       // P = exp2(s * scale - m), written over the first 64 columns of S
       const float m_use = m_run == -INFINITY ? 0.f : m_run;
       float2 ls = make_float2(0.f, 0.f);
-      const float2 sl2x2 = make_float2(sl2, sl2), negm2 = make_float2(-m_use, -m_use);
+      float2 sl2x2 = make_float2(sl2, sl2), negm2 = make_float2(-m_use, -m_use);
 #pragma unroll
       for (int q4 = 0; q4 < BN / 32; ++q4) {
+        if constexpr (kMode == kModeKv8) {
+          // P times V's factor; the sum so far goes on in the second half's units
+          const int h = q4 / 2;
+          sl2x2 = make_float2(sl2h[h], sl2h[h]);
+          negm2 = make_float2(lfh[h] - m_use, lfh[h] - m_use);
+          if (q4 == 2) {
+            const float to = ex2_approx(lfh[1] - lfh[0]);
+            ls.x *= to;
+            ls.y *= to;
+          }
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -901,7 +947,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         }
         tmem_st16(sbase + q4 * 16, pk);
       }
-      l_run += ls.x + ls.y;
+      l_run += kMode == kModeKv8 ? (ls.x + ls.y) * ex2_approx(-lfh[1]) : ls.x + ls.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -929,7 +975,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
         if (store) p.part_ml[at * kRows + x * BM + r] = make_float2(m_run, l_run);
       } else {
         const float inv = 1.f / l_run;
-        const int head = kMode == kModePacked ? it.hq + (r & (p.sh.g - 1)) : it.hq;
+        const int head = kMode == kModeKv8 ? it.hq + (r & ((1 << p.log2_g) - 1)) : it.hq;
         uint16_t* orow = p.o + (((int64_t)it.b * p.T + row_local) * p.sh.Hq + head) * D;
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -969,9 +1015,9 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
   const int item = blockIdx.x / (kRows / kMergeRows), row0 = blockIdx.x % (kRows / kMergeRows) * kMergeRows;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Item it = item_of<kModePacked>(p, item);
+  const Item it = item_of<kModeKv8>(p, item);
   const int first = it.qp * kRows + row0;  // query rows of the item
-  const int rows = min(kMergeRows, p.T * p.sh.g - first);
+  const int rows = min(kMergeRows, (p.T << p.log2_g) - first);
   if (rows <= 0) return;
   if (lane < rows) {
     const int64_t at0 = (int64_t)item * p.splits;
@@ -1024,7 +1070,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
   for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
     const int r = e / (D / 4), c = e % (D / 4);
     const int row = first + r;
-    const int64_t at = ((int64_t)it.b * p.T + token_of<kModePacked>(p, row)) * p.sh.Hq + it.hq + (row & (p.sh.g - 1));
+    const int64_t at = ((int64_t)it.b * p.T + token_of<kModeKv8>(p, row)) * p.sh.Hq + it.hq + (row & ((1 << p.log2_g) - 1));
     reinterpret_cast<uint2*>(p.o + at * D)[c] = s_out[r][c];
   }
 }
@@ -1049,9 +1095,9 @@ cudaError_t launch_t(const PrefillParams& p, cudaStream_t stream) {
   }
   // the setmaxnreg split is sized for exactly this launch allocation
   if (regs != Roles<kMode>::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const int grid = p.items_r * (kMode == kModePacked ? p.splits : 1) + p.items_s;
+  const int grid = p.items_r * (kMode == kModeKv8 ? p.splits : 1) + p.items_s;
   if (grid == 0) return cudaSuccess;
-  if constexpr (kMode != kModePacked) {
+  if constexpr (kMode != kModeKv8) {
     prefill_kernel<D, kMode><<<grid, Roles<kMode>::kThreads, smem, stream>>>(p);
     return cudaGetLastError();
   } else {
@@ -1086,7 +1132,7 @@ cudaError_t launch_mode(const PrefillParams& p, cudaStream_t stream) {
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
   if (p.kv4) return launch_mode<kModeKv4>(p, stream);
   if (p.chunk_len > 0) return launch_mode<kModeDca>(p, stream);
-  if (p.packed) return launch_mode<kModePacked>(p, stream);
+  if (p.k_fac) return launch_mode<kModeKv8>(p, stream);
   if (p.pg.stream_table) return launch_mode<kModePool>(p, stream);
   return p.pg.table ? launch_mode<kModePaged>(p, stream) : launch_mode<kModePlain>(p, stream);
 }

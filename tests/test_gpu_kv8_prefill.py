@@ -1,6 +1,6 @@
 """Prefill of a chunk against 8-bit caches: every head of sampled rows against attention in 64 bits
-over the cache's rows (code * scale rounded to bf16, as documented; the open block's as they were)
-and the chunk's own keys, within the bound of kv8_util.attend."""
+over the cache's rows (code * scale; the open block's as they were) and the chunk's own keys, within
+the bound of kv8_util.attend."""
 
 import numpy as np
 import pytest
@@ -20,18 +20,13 @@ def _layer(c, cap, page=0, seed=1):
     return DuoKv8Layer(c.B, c.Hq, c.Hkv, c.D, c.S, c.R, cap, c.kinds, code=c.code)
 
 
-def _bf16(x):
-    return torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16).double().numpy()
-
-
 def _check_chunk(c, n, T, out, rows=None):
     got = f64(out)
     for b in range(c.B):
         for h in range(c.Hkv):
             keep = {}
             for name, x in (("k", c.k), ("v", c.v)):
-                _, cached, full = c.heads_rows(b, h, n, x)
-                cached = np.concatenate([_bf16(np.float32(cached[:full])), cached[full:]]) if c.kinds[h] else cached
+                cached = c.heads_rows(b, h, n, x)[1]
                 keep[name] = np.concatenate([cached, x[b, n:n + T, h]])
             at = np.arange(n + T)
             for t in rows if rows is not None else range(T):
@@ -107,11 +102,17 @@ def test_a_chunked_prompt_then_decode(code):
 
 
 def test_equals_the_bf16_prefill_over_the_dequantized_rows():
-    """Bit for bit where query heads do not share query blocks and no item is split over its keys (here:
-    full query blocks, and more of them than SMs)."""
+    """Bit for bit where the scales are powers of two (so the rows are bf16 values), query heads do not
+    share query blocks and no item is split over its keys (here: full query blocks, and more of them
+    than SMs)."""
     from streaming_kv_cache_duo_gb300 import DuoLayer
     n, T, kinds = 777, 512, [1, 1, 0, 1, 0, 1, 1, 0]
     c = Batch(52, [n + T] * 2, 64, 8, 64, 64, 256, kinds, "int8")
+    for name in ("k", "v"):  # the largest of every block is 127 / 64
+        t = getattr(c, name + "t").clamp(-127 / 64, 127 / 64)
+        t[:, ::BLOCK, :, 0] = 127 / 64
+        setattr(c, name + "t", t)
+        setattr(c, name, t.double().numpy())
     layer = _layer(c, n + T)
     _fill(c, layer, n)
     plain = DuoLayer(2, 64, 8, 64, 64, 256, n + T, kinds)
@@ -246,3 +247,24 @@ def test_captured_chunk_append_and_decode():
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(dec, want_dec)
     _check_chunk(c, n, T, out, [0, T - 1])
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("T", [9, 300])
+def test_blocks_of_scales_far_apart(T, code):
+    """Blocks of zeros, of values near the smallest and far above the others, and of one that is all
+    that counts: each block's scale is its own."""
+    n = 64 * 20 + 17
+    c = Batch(59, [n + T] * 2, 4, 2, 128, 4, 32, [1, 1], code)
+    kt, vt = c.kt.clone(), c.vt.clone()
+    for j in range(20):
+        rows = slice(64 * j, 64 * j + 64)
+        kt[:, rows] *= [1, 0, 2.0 ** -40, 1.5, 0.3][j % 5]
+        vt[:, rows] *= [1, 2.0 ** 3, 0, 2.0 ** -12, 2.0 ** -131, 0.7, 2.0 ** -60][j % 7]
+    vt[1, 64 * 3:64 * 4] *= 2.0 ** 60
+    for name, t in (("k", kt), ("v", vt)):
+        setattr(c, name + "t", t)
+        setattr(c, name, t.double().numpy())
+    layer = _layer(c, n + T, 128)
+    _fill(c, layer, n)
+    _check_chunk(c, n, T, _run(c, layer, n, T), [0, T // 2, T - 1])
