@@ -818,7 +818,13 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     float l_run = 0.f;
     bool ok = true;
     // factors of 32 blocks (16 tiles) of an 8-bit cache, one per lane: K's, and the logarithm of V's
-    float fk = 1.f, lf = 0.f;
+    float fk = 1.f, lf = 0.f, fk_next = 1.f, lf_next = 0.f;
+    auto factors = [&](int k, float& f, float& l) {  // of the 16 tiles around tile k
+      const int blk = (k & ~15) * 2 + lane;
+      const int64_t at = ((int64_t)it.b * p.sh.n_ret + it.cidx) * p.fac_blocks + blk;
+      f = blk < p.fac_blocks ? __ldg(p.k_fac + at) : 1.f;
+      l = blk < p.fac_blocks ? __ldg(p.v_fac + at) : 0.f;
+    };
     // packed: a warp without a row of the chunk does no softmax (what its rows of S hold goes for P,
     // and their O is not stored). In a loop of its own: a branch in the other one cost 1 %.
     int my_tiles = x < nq ? ntiles : 0;
@@ -836,11 +842,13 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       // log2 units per unit of score in the tile's halves, and what V's factors add to P's exponent
       float sl2h[2] = {sl2, sl2}, lfh[2] = {0.f, 0.f};
       if (kMode == kModeKv8 && !it.streaming && t.phase == 0) {
-        if (j == 0 || (t.k & 15) == 0) {
-          const int blk = (t.k & ~15) * 2 + lane;
-          const int64_t at = ((int64_t)it.b * p.sh.n_ret + it.cidx) * p.fac_blocks + blk;
-          fk = blk < p.fac_blocks ? __ldg(p.k_fac + at) : 1.f;
-          lf = blk < p.fac_blocks ? __ldg(p.v_fac + at) : 0.f;
+        if (j == 0) {
+          factors(t.k, fk, lf);
+          factors(t.k + 16, fk_next, lf_next);
+        } else if ((t.k & 15) == 0) {
+          fk = fk_next;
+          lf = lf_next;
+          factors(t.k + 16, fk_next, lf_next);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
