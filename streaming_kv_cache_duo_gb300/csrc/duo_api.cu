@@ -443,7 +443,7 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
   // retrieval heads, g = 4) is 64 items of 75 tiles, half of them with 77 rows of 256. Packed it is
   // 48, and each split over several CTAs. Cost: the tiles until the last SM is done, retrieval items
   // first, then the streaming heads' in the gaps; each item counted with three tiles' worth of start
-  // and merge. Packed and split where that is a tenth less.
+  // and merge. Packed and split where that is a tenth less. (That turn: 221 us unsplit, 70 so.)
   const int64_t heads = (int64_t)sh.B * sh.n_ret, others = (int64_t)sh.B * sh.n_str, sms = h->num_sms;
   const auto tiles_of = [](int64_t rows) { return (rows + kPrefillBN - 1) / kPrefillBN; };
   const auto makespan = [sms](int64_t r, int64_t tr, int64_t t, int64_t ts) {
