@@ -425,7 +425,7 @@ struct Kv8Prefill {
   int64_t num_qt;  // query blocks per head (packed: per KV head)
   bool packed;
   int splits;
-  int short_by;    // tiles that an item's last part has fewer than its others
+  int part_tiles;  // tiles of an item's parts but the last, which has what is left (0: all the same)
   int64_t parts;   // items x splits, if splits > 1
   size_t fac_at;   // byte offsets in the workspace: of the factors,
   size_t part_at;  // and of the parts
@@ -441,9 +441,10 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
   // A CTA per item leaves SMs idle when items are few, and rows of the last query block idle when
   // tokens are: a short turn after a long conversation (333 tokens after 9001, two sequences, four
   // retrieval heads, g = 4) is 64 items of 75 tiles, half of them with 77 rows of 256. Packed it is
-  // 48, and each split over several CTAs. Cost: the tiles until the last SM is done, retrieval items
-  // first, then the streaming heads' in the gaps; each item counted with three tiles' worth of start
-  // and merge. Packed and split where that is a tenth less. (That turn: 221 us unsplit, 70 so.)
+  // 48, and each split over several CTAs: 70 us in place of 221. Cost: the tiles until the last SM is
+  // done, retrieval items first, then the streaming heads' in the gaps; each item counted with three
+  // tiles' worth of start and end, and a merge's reads. Long chunks gain too, by last parts for the SMs
+  // that are without an item of their own (4096 tokens over 28672, 128 items: 411 -> 400 us).
   const int64_t heads = (int64_t)sh.B * sh.n_ret, others = (int64_t)sh.B * sh.n_str, sms = h->num_sms;
   const auto tiles_of = [](int64_t rows) { return (rows + kPrefillBN - 1) / kPrefillBN; };
   const auto makespan = [sms](int64_t r, int64_t tr, int64_t t, int64_t ts) {
@@ -452,33 +453,44 @@ static Kv8Prefill plan_prefill_kv8(const duo_handle* h, int64_t n, int32_t T) {
     const int64_t more = t > in_gaps ? (t - in_gaps + sms - 1) / sms * ts : 0;
     return (rounds + (rest > 0)) * tr + more;
   };
+  // tiles of a retrieval item: of the last query block, and of all of them on average
   const int64_t cached = tiles_of(n), tiles = cached + tiles_of(T);
+  const int64_t mean = cached + (tiles_of(T) + tiles_of(kPrefillRowsPerCta / sh.g)) / 2;
   // (every tile of a streaming item is masked: half as much again)
   const auto stream_tiles = [&](int64_t tokens) { return (tiles_of(sh.S) + tiles_of(sh.R + tokens) + 1) * 3 / 2 + 3; };
   int64_t best = makespan(heads * sh.g * w.num_qt, tiles + 3, others * sh.g * w.num_qt,
-                          stream_tiles(kPrefillRowsPerCta)) * 9 / 10;
+                          stream_tiles(kPrefillRowsPerCta));
   const int64_t qt = ((int64_t)T * sh.g + kPrefillRowsPerCta - 1) / kPrefillRowsPerCta, items = heads * qt;
   for (int s = 1; s <= kPrefillMaxSplits && s <= cached && (s == 1 || items * s <= 8 * sms); ++s) {
     const int64_t ts = stream_tiles(kPrefillRowsPerCta / sh.g);
-    int64_t cost = makespan(items * s, (tiles + s - 1) / s + 3, others * qt, ts), short_by = 0;
-    // Or, with all parts in one round: the parts but the last ones on SMs of their own, the streaming
-    // items on the rest, and after them the last parts, shorter by what those SMs did before.
+    int64_t cost = makespan(items * s, (tiles + s - 1) / s + 3, others * qt, ts), part_tiles = 0;
+    // Or all parts but the last ones (of `len` tiles) on SMs of their own, on the rest the streaming items
+    // and then the last parts, of what is left: one an SM, or several, which end a part apart.
     const int64_t left = sms - items * (s - 1);
-    if (s > 1 && others > 0 && items <= left) {
-      const int64_t rounds = (others * qt + left - 1) / left;  // streaming items of the busiest of them
+    if (s > 1 && left > 0) {
+      const int64_t rounds = (others * qt + left - 1) / left, lasts = (items + left - 1) / left;
       const int64_t before = (items <= rounds * left - others * qt ? rounds - 1 : rounds) * ts;
-      const int64_t c = std::max((tiles + before + s - 1) / s + 3, rounds * ts);
-      if (before > 0 && c < cost && (s - 1) * before + s <= cached) {
-        cost = c;
-        short_by = before;
+      const int64_t even = lasts == 1 ? (tiles + before + s - 1) / s
+                                      : (items * (mean + 3 * s) + others * qt * ts + sms - 1) / sms - 3;
+      for (int64_t len = even, k = 0; k < 5; ++k, len += even / 20 + 1) {
+        const int64_t last = tiles - (s - 1) * len, part = std::max<int64_t>(mean - (s - 1) * len, 0) + 3;
+        if (last < 1) break;
+        const int64_t end = lasts == 1 ? before + last + 3
+                                       : std::max(lasts * (last + 3), (others * qt * ts + items * part) / left + part);
+        const int64_t c = std::max({len + 3, end, rounds * ts});
+        if (c < cost) {
+          cost = c;
+          part_tiles = len;
+        }
+        if (lasts == 1) break;
       }
     }
-    if (s > 1) cost += s / 8;  // the merge reads them four at a time
+    if (s > 1) cost += items * s / 40 + s / 8;  // the merge's reads, and its steps
     if (cost < best) {
       best = cost;
       w.packed = true;
       w.splits = s;
-      w.short_by = (int)short_by;
+      w.part_tiles = (int)part_tiles;
     }
   }
   if (w.packed) w.num_qt = qt;
@@ -569,7 +581,7 @@ static duo_status prefill_impl(duo_handle* h, const duo_kv_cache* c, const duo_p
       p.fac_blocks = (int)(plan.plane_rows / kKv8Block);
       while (plan.packed && (1 << p.log2_g) < sh.g) ++p.log2_g;
       p.splits = plan.splits;
-      p.short_by = plan.short_by;
+      p.part_tiles = plan.part_tiles;
       p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_at);
       p.part_ml = reinterpret_cast<float2*>(p.part_o + plan.parts * kPrefillRowsPerCta * sh.D);
       expand = e;

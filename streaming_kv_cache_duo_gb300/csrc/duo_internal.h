@@ -219,14 +219,14 @@ struct PrefillParams {
   // For few tokens query rows are tokens x heads of a KV head (log2_g > 0: tm_q's box is 64 x g x
   // 128 / g x 1, num_qt = ceil(T g / 256)), and retrieval items may be split over their key tiles
   // (splits > 1): split s of item i leaves its unnormalised output (fp32 [D / 4, 256 rows, 4]) and
-  // its rows' (max, sum) at place i splits + s. The last split has short_by tiles fewer than the
-  // others.
+  // its rows' (max, sum) at place i splits + s. Splits have part_tiles tiles, the last one
+  // what is left (one at least); part_tiles = 0: all the same.
   const float* k_fac;
   const float* v_fac;
   int fac_blocks;
   int log2_g;  // of the query heads that share query rows: g, or 1
   int splits;
-  int short_by;
+  int part_tiles;
   float* part_o;
   float2* part_ml;
 };

@@ -167,23 +167,25 @@ __device__ __forceinline__ Item item_of(const PrefillParams& p, int idx) {
 }
 
 // What a CTA does: an item (its index as item_of counts them) and its part of it (-1: all).
-// Retrieval items in splits come part by part; with shorter last parts those come behind the
-// streaming items, so that the SMs that took one of these take them.
+// Retrieval items in splits come part by part; with last parts of their own length those come behind
+// the streaming items, for the SMs that took these.
 struct Part {
   int idx, no;
 };
 template <int kMode>
 __device__ __forceinline__ Part part_of(const PrefillParams& p, int cta) {
   if (kMode != kModeKv8 || p.splits == 1) return Part{cta, -1};
-  const int s = p.splits, long_parts = s - (p.short_by > 0), items = p.items_r;
+  const int s = p.splits, long_parts = s - (p.part_tiles > 0), items = p.items_r;
   if (cta < items * long_parts) return Part{cta / long_parts, cta % long_parts};
   cta -= items * long_parts;
   if (cta < p.items_s) return Part{items + cta, -1};
   return Part{cta - p.items_s, s - 1};
 }
-// First tile of part `no` of an item of `total`: equal parts, the last one short_by shorter.
+// First tile of part `no` of an item of `total`: parts of part_tiles and what is left, or equal ones.
+// (Every item has at least as many tiles as there are splits, and every part one: the merge reads all.)
 __device__ __forceinline__ int part_start(const PrefillParams& p, int total, int no) {
-  return no == p.splits ? total : (int)((int64_t)no * (total + p.short_by) / p.splits);
+  return p.part_tiles > 0 && no < p.splits ? min(no * p.part_tiles, total - (p.splits - no))
+                                           : (int)((int64_t)no * total / p.splits);
 }
 
 // Chunk-local token of query row `row` (counted over the item's query blocks).

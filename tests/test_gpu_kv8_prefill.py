@@ -268,3 +268,17 @@ def test_blocks_of_scales_far_apart(T, code):
     layer = _layer(c, n + T, 128)
     _fill(c, layer, n)
     _check_chunk(c, n, T, _run(c, layer, n, T), [0, T // 2, T - 1])
+
+
+@pytest.mark.parametrize("Hq,Hkv,kinds", [(8, 8, [1] * 8), (8, 5, None), (8, 4, [1, 0, 1, 1])], ids=["mha", "mixed", "gqa"])
+def test_long_chunks_whose_last_parts_differ(Hq, Hkv, kinds):
+    """Chunks with about an item per SM, whose keys go on over the SMs without one: parts of one length,
+    the last of what is left, from one tile (the first query block) up."""
+    n, T = 9000 - 37, 4096 - 5
+    if kinds is None:
+        Hq, kinds = 10, [1, 1, 1, 1, 0]
+    c = Batch(63, [n + T], Hq, Hkv, 64, 64, 256, kinds, "e4m3")
+    layer = _layer(c, n + T)
+    _fill(c, layer, n)
+    out = _run(c, layer, n, T)
+    _check_chunk(c, n, T, out, [0, 127, 128, 255, 256, 2000, T - 1])
