@@ -160,7 +160,10 @@ __device__ void fill(const BlockTablesParams& p, const Scratch& s, int64_t first
 }
 
 __global__ void __launch_bounds__(kScanThreads) block_tables_scan_kernel(const BlockTablesParams p, int fuse) {
+  // as the appends: dependents may be scheduled now, nothing is touched before the grid before this
+  // one has ended
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ Sums warp_sums[32];
   __shared__ int s_handed;
   __shared__ int32_t s_sums[4 + 3 * kSmall + 2], s_cu[kSmall + 1];
@@ -309,21 +312,22 @@ cudaError_t launch_block_tables(const BlockTablesParams& p, int num_sms, cudaStr
   // threads: one per sequence, and in a fused step one per output, as far as they go
   const int64_t want = fuse && work > p.B ? work : p.B;
   const int threads = want >= kScanThreads ? kScanThreads : (want <= 128 ? 128 : (int)((want + 31) / 32 * 32));
-  block_tables_scan_kernel<<<1, threads, 0, stream>>>(p, fuse ? 1 : 0);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || fuse) return e;
-  const int64_t items = (int64_t)p.max_tokens * ((p.planes + kPlanes - 1) / kPlanes) + (int64_t)p.B * p.planes;
-  int64_t blocks = (items + 255) / 256;
-  if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, block_tables_scan_kernel, p, fuse ? 1 : 0);
+  if (e != cudaSuccess || fuse) return e;
+  const int64_t items = (int64_t)p.max_tokens * ((p.planes + kPlanes - 1) / kPlanes) + (int64_t)p.B * p.planes;
+  int64_t blocks = (items + 255) / 256;
+  if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, block_tables_fill_kernel, p);
 }
 
