@@ -359,7 +359,9 @@ class DuoKv8Layer(DuoLayer):
                                       ptr(self.k_tail), ptr(self.v_tail),
                                       _lib.DUO_KV8_INT8 if code == "int8" else _lib.DUO_KV8_E4M3)
         self.paged = None
-        self.index = self.pos.get_device()
+        # (looked up here: a small call's time is the host's)
+        self.index, self.bf16, self.empty_like = self.pos.get_device(), torch.bfloat16, torch.empty_like
+        self.row = (self.B, self.Hq, self.D)
 
     def append(self, k_new, v_new, stream=None) -> None:
         T = k_new.shape[1]
@@ -371,7 +373,7 @@ class DuoKv8Layer(DuoLayer):
             _lib.duo_kv_append_kv8_paged(self.handle, self.cache, self.paged, self.kv8, k_new, v_new, T, stream)
 
     def decode(self, q, out=None, stream=None):
-        out = self._out(q, (self.B, self.Hq, self.D), out)
+        out = self._out(q, self.row, out)
         if self.paged is None:
             _lib.duo_attn_decode_kv8(self.handle, self.cache, self.kv8, q, out, self.workspace, stream)
         else:
@@ -382,7 +384,7 @@ class DuoKv8Layer(DuoLayer):
     def decode_varlen(self, q, seq_lens, max_len, out=None, stream=None):
         """Decode where sequence b holds seq_lens[b] tokens, the new one included (device int32
         [B], <= max_len); a sequence of length 0 gets zeros."""
-        out = self._out(q, (self.B, self.Hq, self.D), out)
+        out = self._out(q, self.row, out)
         _check_lens(seq_lens, self.B)
         if seq_lens.get_device() != self.index:
             raise ValueError(f"seq_lens: on {seq_lens.device}, the layer is on CUDA device {self.index}")
@@ -391,10 +393,9 @@ class DuoKv8Layer(DuoLayer):
         return out
 
     def _out(self, q, shape, out):
-        import torch
         _on(self, "q", q, shape)
         if out is None:
-            return torch.empty_like(q)
+            return self.empty_like(q)
         _on(self, "o", out, shape)
         return out
 
@@ -503,7 +504,7 @@ class DuoBlockPool:
         self.free_count = torch.full((1,), num_blocks, **i32)
         self.seq_lens = torch.zeros(batch, **i32)
         self.batch, self.max_tokens = batch, max_tokens
-        self.index = self.seq_lens.get_device()
+        self.index, self.int32 = self.seq_lens.get_device(), torch.int32
         self.slot_map = DuoSlotMap(torch.zeros(batch + 1, **i32), torch.full((max_tokens,), -1, **i32),
                                    torch.full((max_tokens,), -1, **i32),
                                    torch.full((max_tokens, planes), -1, dtype=torch.int64, device=self.device))
@@ -517,14 +518,13 @@ class DuoBlockPool:
         """Sequence b takes new_lens[b] more tokens (-1: it has finished; device int32 [B]).
         Updates tables, free list and lengths (into the *_out tensors if given) and returns
         the slot map of the packed tokens, whose arrays the next update overwrites."""
-        import torch
         lens = self.seq_lens if seq_lens_out is None else seq_lens_out
         count = self.free_count if free_count_out is None else free_count_out
         for name, t, n in (("new_lens", new_lens, self.batch), ("seq_lens_out", lens, self.batch),
                            ("free_count_out", count, 1)):
-            if t.dtype != torch.int32 or t.get_device() != self.index or not t.is_contiguous() or t.numel() != n:
+            if t.dtype is not self.int32 or t.get_device() != self.index or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{name}: need a contiguous int32 tensor of {n} element(s) on CUDA device {self.index}")
-        if torch.cuda.current_device() != self.index:
+        if _lib._current_device() != self.index:
             raise ValueError(f"the current device is not the pool's (CUDA device {self.index})")
         _lib.duo_block_tables_update(self.c, new_lens, self.max_tokens, lens, count, self.slot_map.c, self.workspace,
                                      stream)
@@ -533,8 +533,8 @@ class DuoBlockPool:
 
 def _on(layer, name, t, shape):
     """_lib._bf16, and on the layer's own device."""
-    _lib._bf16(t, shape, name)
-    if t.get_device() != layer.index:
+    if (t.dtype is not layer.bf16 or t.get_device() != layer.index or t.shape != shape or not t.is_contiguous()):
+        _lib._bf16(t, shape, name)
         raise ValueError(f"{name}: on {t.device}, the layer is on CUDA device {layer.index}")
 
 

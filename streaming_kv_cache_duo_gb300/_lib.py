@@ -193,15 +193,27 @@ def _check(status: int) -> None:
 _raw_stream = None  # (device index) -> the current stream's handle, without a Stream object around it
 
 
-def _stream_ptr(stream) -> int:
-    global _raw_stream
-    if stream is None:
+_device = None  # () -> index of the current device
+
+
+def _current_device() -> int:
+    global _raw_stream, _device
+    if _device is None:
         import torch
-        if _raw_stream is None:
-            torch.cuda.current_stream()  # initialises CUDA
-            _raw_stream = torch._C._cuda_getCurrentRawStream
-        return _raw_stream(torch._C._cuda_getDevice())
+        torch.cuda.current_stream()  # initialises CUDA
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _device()
+
+
+def _stream_ptr(stream) -> int:
+    if stream is None:
+        return _raw_stream(_device()) if _raw_stream is not None else _stream_ptr_first()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_ptr_first() -> int:
+    index = _current_device()
+    return _raw_stream(index)
 
 
 def _ptr(t):
