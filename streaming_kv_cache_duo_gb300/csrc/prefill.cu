@@ -807,8 +807,9 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     const uint32_t sbase = lane_base + col_s(x);
     const uint32_t obase = lane_base + col_o(x);
     const int row_local = token_of<kMode>(p, it.qp * kRows + x * BM + r);  // chunk-local token of the query row
-    // absolute position (< 2^31, checked on the host); a row past the chunk takes the last one's
-    const int i_abs = (int)p.n + (kMode == kModeKv8 ? min(row_local, p.T - 1) : row_local);
+    // absolute position (< 2^31, checked on the host); a row past the chunk takes the last one's, so
+    // that a warp's positions rise with the lane up to the last position there is
+    const int i_abs = (int)p.n + min(row_local, p.T - 1);
     // DCA: the fp32 per-position scale joins softmax_scale on the fp32 product
     const float sl2 = (kMode == kModeDca && p.mscale && row_local < p.T)
                           ? p.scale_log2 * __ldg(p.mscale + (int64_t)it.b * p.T + row_local)

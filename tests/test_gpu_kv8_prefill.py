@@ -282,3 +282,21 @@ def test_long_chunks_whose_last_parts_differ(Hq, Hkv, kinds):
     _fill(c, layer, n)
     out = _run(c, layer, n, T)
     _check_chunk(c, n, T, out, [0, 127, 128, 255, 256, 2000, T - 1])
+
+
+@pytest.mark.parametrize("layer", ["DuoLayer", "DuoKv8Layer"])
+def test_ring_positions_at_the_last_ones_there_are(layer):
+    """Streaming heads up to position 2^31 - 5, a chunk whose query block goes on past 2^31: as at small
+    positions with the same slots."""
+    import streaming_kv_cache_duo_gb300 as duo
+    S, R, T, n = 0, 256, 105, (1 << 31) - 110
+    rng = np.random.default_rng(64)
+    far, near = (getattr(duo, layer)(1, 4, 2, 64, S, R, 1, [0, 0]) for _ in range(2))
+    draw = lambda t, h: torch.from_numpy(rng.standard_normal((1, t, h, 64)).astype(np.float32)).bfloat16().cuda()
+    k, v = draw(R, 2), draw(R, 2)
+    for x, at in ((far, n - R), (near, n % R)):
+        x.cache.n = at
+        x.append(k, v)
+    q, k, v = draw(T, 4), draw(T, 2), draw(T, 2)
+    assert far.n == n
+    assert torch.equal(far.prefill(q, k, v), near.prefill(q, k, v))
