@@ -857,7 +857,7 @@ struct WarpSync {
   __device__ __forceinline__ bool sync(DevError err) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    const bool ok = mbar_wait(bar, phase, err, kErrDecodeConsumer);
+    const bool ok = mbar_wait_warp(bar, phase, err, kErrDecodeConsumer);
     phase ^= 1u;
     __syncwarp();
     return ok;
@@ -1003,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, is_kv4_mode(kMode) ? kDecodeCtasPerS
         cur.advance(p, c, t1, live);
         ++issued;
       }
-      if (!mbar_wait(&wfull[s], (uint32_t)((j / C::NSW) & 1), err, kErrDecodeConsumer)) {
+      if (!mbar_wait_warp(&wfull[s], (uint32_t)((j / C::NSW) & 1), err, kErrDecodeConsumer)) {
         ok = false;
         break;
       }

@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
   bool ok = true;  // of this warp: a wait that ran out stops its copies, not the CTA's barriers
   State<D, G> st;
   auto wait = [&](int b) {
-    const bool done = mbar_wait(&bars[b], (phases >> b) & 1u, err, kErrDecodeConsumer);
+    const bool done = mbar_wait_warp(&bars[b], (phases >> b) & 1u, err, kErrDecodeConsumer);
     phases ^= 1u << b;
     pending &= ~(1u << b);
     return done;

@@ -80,6 +80,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, DevErr
   }
 }
 
+// The same for a whole warp, all 32 lanes of which call it together: they get one answer. With a
+// wait per lane the phase may complete between one lane's last try and another's, and the lanes then
+// part ways in front of the warp-wide instructions that the wait guards (shuffles, matrix loads and
+// products, TMEM accesses). The warp goes on once every lane has seen the phase (each needs its own
+// acquire), and gives up once any lane's time is over (limit_ns may differ from lane to lane).
+__device__ __forceinline__ bool mbar_wait_warp_for(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 255u) == 255u && __any_sync(0xffffffffu, global_timer_ns() - t0 > limit_ns)) return false;
+  }
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, DevError err, uint32_t code) {
+  if (mbar_wait_warp_for(bar, parity, kWaitLimitNs)) return true;
+  if ((threadIdx.x & 31) == 0) atomicOr(err.word, code);
+  return false;
+}
+
 // ---------------------------------------------------------------- bulk copies
 __device__ __forceinline__ void bulk_g2s(void* dst_smem, const void* src_gmem, uint32_t bytes, uint64_t* bar) {
   asm volatile(

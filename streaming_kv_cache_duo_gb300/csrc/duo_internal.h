@@ -22,6 +22,7 @@ enum : uint32_t {
   kErrDecodeProducer = 1u << 8,
   kErrDecodeConsumer = 1u << 9,
   kErrSelftest = 1u << 16,
+  kErrSelftestSplit = 1u << 17,  // the lanes of a waiting warp came out with different answers
   kErrAppendCapacity = 1u << 20,
   kErrBadBlock = 1u << 21,
   kErrPoolFull = 1u << 22,   // block tables: a sequence was turned down

@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     int my_tiles = x < nq ? ntiles : 0;
     if (kMode == kModeKv8 && __shfl_sync(0xffffffffu, row_local, 0) >= p.T) {
       for (int j = 0; j < my_tiles; ++j) {
-        if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) break;
+        if (!mbar_wait_warp(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[x]);
       }
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
           ring_pos[q4] = slot < p.nvalid ? __ldg(prow + slot) : -1;
         }
       }
-      if (!mbar_wait(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) {
+      if (!mbar_wait_warp(&bars->s_full[x], (uint32_t)(j & 1), err, kErrPrefillSoftmax)) {
         ok = false;
         break;
       }
@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       if (lane == 0) mbar_arrive(&bars->p_full[x]);
     }
     // ---------------------------------------------------------------- epilogue
-    if (ok && my_tiles > 0 && mbar_wait(&bars->o_final[x], 0, err, kErrPrefillSoftmax)) {
+    if (ok && my_tiles > 0 && mbar_wait_warp(&bars->o_final[x], 0, err, kErrPrefillSoftmax)) {
       tc_fence_after();
       const bool store = row_local < p.T;
       if (split) {  // this split's part, as it stands
