@@ -389,7 +389,8 @@ typedef struct {
  * `map` alone (cache->n is neither read nor changed, no table is read), so a step captured
  * in a CUDA graph replays with other lengths. Tokens at position -1 are skipped and nothing
  * of their sequence changes. A slot or sequence out of range is not dereferenced: its rows
- * are skipped and duo_device_error() reports DUO_ERR_INVALID_ARG. */
+ * are skipped and duo_device_error() reports DUO_ERR_INVALID_ARG; so it is with the tokens of a
+ * sequence whose last position would reach 2^31 - 1. */
 duo_status duo_kv_append_kv8_ragged(duo_handle* handle, duo_kv_cache* cache, const duo_paged* paged,
                                     const duo_kv8_cache* kv8, const duo_slot_map* map, int32_t num_tokens,
                                     const void* k_new, const void* v_new, void* stream);

@@ -115,11 +115,13 @@ __device__ __forceinline__ Token token_at(const Kv8AppendParams& p, int i) {
   t.ok = t.pos >= 0;
   t.first = t.last = i;
   if (!t.ok) return t;
-  bool good = t.b >= 0 && t.b < p.sh.B && t.pos < 0x7fffffff;
+  bool good = t.b >= 0 && t.b < p.sh.B;
   if (good) {
     t.first = p.cu_new[t.b];
     t.last = p.cu_new[t.b + 1] - 1;
-    good = t.first >= 0 && t.first <= i && t.last >= i && t.last < p.tokens && t.pos >= i - t.first;
+    // (the sequence's length before and after the call follow from these, in 32 bits)
+    good = t.first >= 0 && t.first <= i && t.last >= i && t.last < p.tokens && t.pos >= i - t.first &&
+           t.last - i < 0x7fffffff - t.pos;
   }
   if (!good) {
     atomicOr(&g_append_kv8_err, kErrBadBlock);
