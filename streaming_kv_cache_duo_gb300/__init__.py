@@ -442,14 +442,10 @@ class DuoKv8PagedLayer(DuoKv8Layer):
 
     def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, block_size,
                  max_blocks, num_blocks, block_table, is_retrieval, code="int8", device="cuda"):
-        import torch
         super().__init__(batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, 1, is_retrieval,
                          code=code, device=device)
         if block_table is not None:
-            if (block_table.dtype != torch.int32 or not block_table.is_cuda or not block_table.is_contiguous()
-                    or tuple(block_table.shape) != (batch, self.n_ret, max_blocks)):
-                raise ValueError(f"block_table: need a contiguous CUDA int32 tensor of shape "
-                                 f"{(batch, self.n_ret, max_blocks)}")
+            _check_table(block_table, (batch, self.n_ret, max_blocks), self.index)
         blocks = num_blocks if self.n_ret else 0
         self._codes(code, (blocks, block_size), (blocks, block_size // _lib.DUO_KV8_BLOCK))
         self.block_size = block_size
@@ -536,6 +532,15 @@ def _on(layer, name, t, shape):
     if (t.dtype is not layer.bf16 or t.get_device() != layer.index or t.shape != shape or not t.is_contiguous()):
         _lib._bf16(t, shape, name)
         raise ValueError(f"{name}: on {t.device}, the layer is on CUDA device {layer.index}")
+
+
+def _check_table(t, shape, index):
+    """A block table of a layer on CUDA device `index`."""
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"block_table: need a contiguous CUDA int32 tensor of shape {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"block_table: on {t.device}, the layer is on CUDA device {index}")
 
 
 def _check_mscale(mscale, shape):
