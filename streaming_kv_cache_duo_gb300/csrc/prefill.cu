@@ -450,8 +450,9 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
   const int j0 = split ? part_start(p, pl.total, part.no) : 0;
   const int share = split ? part_start(p, pl.total, part.no + 1) - j0 : pl.total;
   // After any CTA of this kernel gave up a wait, later CTAs do no work, so a
-  // failure ends in about one wait limit instead of one per CTA.
-  const int ntiles = (*(volatile unsigned int*)err.word != 0u) ? 0 : share;
+  // failure ends in about one wait limit instead of one per CTA. (A block id outside
+  // the pool, recorded in the same word, concerns its rows alone.)
+  const int ntiles = (*(volatile unsigned int*)err.word & ~kErrBadBlock) != 0u ? 0 : share;
   // query tiles with rows: packed, the second one of the last block may have none
   const int nq = kMode == kModeKv8 && (p.T << p.log2_g) - it.qp * kRows <= BM ? 1 : kQT;
 
