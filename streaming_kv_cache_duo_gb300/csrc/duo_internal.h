@@ -283,7 +283,7 @@ struct Kv8ExpandParams {
   uint16_t* k_out;  // bf16 [planes, n rounded up to 64, D]: code times the power of two in the scale
   uint16_t* v_out;
   float* k_fac;     // [planes, blocks]: what is left of K's scales,
-  float* v_fac;     // and the logarithm (base 2) of what is left of V's
+  float* v_fac;     // and the logarithm (base 2) of what is left of V's (-inf: no such page)
   int n, planes, D;
   int code_type;
   int64_t cap64;

@@ -71,10 +71,10 @@ __global__ void __launch_bounds__(kThreads) expand_kv8_kernel(const Kv8ExpandPar
     const int bi = (int)((uint32_t)r0 / (uint32_t)p.pg.block_size);
     const int64_t id = __ldg(p.pg.table + plane * p.pg.max_blocks + bi);
     row = id * p.pg.block_size + (r0 - bi * p.pg.block_size);
-    if (id < 0 || id >= p.pg.num_blocks) {  // no such block: its rows read as zeros
+    if (id < 0 || id >= p.pg.num_blocks) {  // no such block: the prefill leaves its rows out
       if (tid == 0) {
         atomicOr(&g_expand_kv8_err, kErrBadBlock);
-        *fac = is_v ? 0.f : 1.f;
+        *fac = is_v ? -INFINITY : 1.f;
       }
 #pragma unroll
       for (int k = 0; k < N; ++k) reinterpret_cast<uint4*>(out)[tid + k * kHalf] = make_uint4(0, 0, 0, 0);

@@ -351,6 +351,7 @@ __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, con
     if (t.phase == 0) vis &= bits_below((int)p.n - j0);                        // rows >= n hold no token
   } else if (!it.streaming) {
     vis = bits_below((int)p.n - t.k * BN - c0);  // rows >= n hold no token
+    if (kMode == kModeKv8 && jp < 0) vis = 0u;   // nor do the rows of a page that does not exist
   } else {
     // a lane has one slot's position; most slots are seen by all of the warp's rows or by none
     // (rows' positions rise with the lane), the few others are compared row by row
@@ -842,7 +843,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     }
     for (int j = 0; j < my_tiles && ok; ++j) {
       const Tile t = tile_at<kMode>(pl, kMode == kModeKv8 ? j0 + j : j);
-      const bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
+      bool masked = it.streaming || (t.phase == 0 ? (int64_t)(t.k + 1) * BN > p.n : t.k >= q_last);
       // log2 units per unit of score in the tile's halves, and what V's factors add to P's exponent
       float sl2h[2] = {sl2, sl2}, lfh[2] = {0.f, 0.f};
       if (kMode == kModeKv8 && !it.streaming && t.phase == 0) {
@@ -862,6 +863,15 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       }
       // a ring tile: the positions its slots hold, -1 past the last (slot 32 q4 + lane)
       int ring_pos[BN / 32];
+      if (kMode == kModeKv8 && !it.streaming && t.phase == 0) {  // -1: a half whose page does not exist
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool gone = lfh[h] == -INFINITY;
+          ring_pos[2 * h] = ring_pos[2 * h + 1] = gone ? -1 : 0;
+          lfh[h] = gone ? 0.f : lfh[h];
+          masked |= gone;
+        }
+      }
       if (kMode != kModePool && it.streaming && t.phase == 0) {
         const int32_t* prow = p.pos + (int64_t)it.b * (p.sh.S + p.sh.R);
 #pragma unroll
