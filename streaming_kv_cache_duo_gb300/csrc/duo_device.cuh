@@ -95,7 +95,7 @@ __device__ __forceinline__ bool mbar_wait_warp_for(uint64_t* bar, uint32_t parit
 }
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, DevError err, uint32_t code) {
   if (mbar_wait_warp_for(bar, parity, kWaitLimitNs)) return true;
-  if ((threadIdx.x & 31) == 0) atomicOr(err.word, code);
+  atomicOr(err.word, code);  // (by every lane: a condition here made the 4-bit decode spill)
   return false;
 }
 
