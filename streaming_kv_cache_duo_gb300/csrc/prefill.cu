@@ -336,8 +336,9 @@ __device__ __forceinline__ uint32_t bits_below(int hi) {
 // Where the chunk's keys are consecutive positions j0 ... j0+31, the keys row i_abs
 // sees form at most two runs (the sinks j < S, and j in (i - R, i]), so the chunk's
 // visibility is a 32-bit mask built from a few shifts, applied with one bit test per
-// score; ring-cache slots are looked up one by one.
-template <int kMode>
+// score. Ring-cache slots: jp is the position that slot 32 q4 + lane holds, fetched before
+// the scores arrive; with kFetch it is fetched here.
+template <int kMode, bool kFetch>
 __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, const Item& it, const Tile& t, int c0,
                                            int i_abs, int jp) {
   const int S = p.sh.S, R = p.sh.R;
@@ -353,6 +354,10 @@ __device__ __forceinline__ void mask_chunk(float* v, const PrefillParams& p, con
     vis = bits_below((int)p.n - t.k * BN - c0);  // rows >= n hold no token
     if (kMode == kModeKv8 && jp < 0) vis = 0u;   // nor do the rows of a page that does not exist
   } else {
+    if constexpr (kFetch) {
+      const int slot = t.k * BN + c0 + (int)(threadIdx.x & 31);
+      jp = slot < p.nvalid ? __ldg(p.pos + (int64_t)it.b * (S + R) + slot) : -1;
+    }
     // a lane has one slot's position; most slots are seen by all of the warp's rows or by none
     // (rows' positions rise with the lane), the few others are compared row by row
     const int i0 = __shfl_sync(0xffffffffu, i_abs, 0), i1 = __shfl_sync(0xffffffffu, i_abs, 31);
@@ -861,7 +866,11 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
           lfh[h] = __shfl_sync(0xffffffffu, lf, (t.k & 15) * 2 + h);
         }
       }
-      // a ring tile: the positions its slots hold, -1 past the last (slot 32 q4 + lane)
+      // a ring tile: the positions its slots hold, -1 past the last (slot 32 q4 + lane). The 4-bit
+      // instance for D = 128 has no registers left for them: fetched early they cost its retrieval
+      // heads more than its streaming ones gained (2048 tokens over 16384, half of the heads each:
+      // 419.0 us early, 416.8 late; streaming heads alone 88.9 and 91.9)
+      constexpr bool kFetchLate = kMode == kModeKv4 && D == 128;
       int ring_pos[BN / 32];
       if (kMode == kModeKv8 && !it.streaming && t.phase == 0) {  // -1: a half whose page does not exist
 #pragma unroll
@@ -872,7 +881,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
           masked |= gone;
         }
       }
-      if (kMode != kModePool && it.streaming && t.phase == 0) {
+      if (!kFetchLate && kMode != kModePool && it.streaming && t.phase == 0) {
         const int32_t* prow = p.pos + (int64_t)it.b * (p.sh.S + p.sh.R);
 #pragma unroll
         for (int q4 = 0; q4 < BN / 32; ++q4) {
@@ -895,7 +904,7 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
       }
       if (masked) {
 #pragma unroll
-        for (int q4 = 0; q4 < BN / 32; ++q4) mask_chunk<kMode>(v + q4 * 32, p, it, t, q4 * 32, i_abs, ring_pos[q4]);
+        for (int q4 = 0; q4 < BN / 32; ++q4) mask_chunk<kMode, kFetchLate>(v + q4 * 32, p, it, t, q4 * 32, i_abs, ring_pos[q4]);
       }
       float mx_s;
       if constexpr (kMode == kModeKv8) {
