@@ -404,7 +404,7 @@ struct Cursor {
   Unit x;
   int64_t ub, x1;
   int lt, lt1;      // next tile of the unit, and the end of the share's tiles in it
-  int row, rows;    // first row of the slice in its codes (32 rows), or in its bf16 rows (1 to 16)
+  int row, rows;    // first row of the slice in its codes (kv8_slice_rows(D) of them), or in its bf16 rows (1 to 16)
   int code_rows;    // rows of codes of the unit
   const int32_t* pages;  // paged codes: the unit's row of the block table,
   int blk;               // and the id of the page the slice lies in
@@ -1094,6 +1094,12 @@ void plan_decode_kv8(Kv8DecodeParams* p, int num_sms) {
   p->C = (int)(p->whole ? U : (most < num_sms ? most : num_sms));
   // merge by unit, 32 dims a CTA, where that is no more than a CTA per SM
   p->merge_units = U <= p->C && U * p->sh.g * (p->sh.D / 32) <= num_sms;
+}
+
+size_t decode_kv8_workspace_bytes(const Kv8DecodeParams& p) {
+  if (p.whole) return 0;
+  const size_t part = (size_t)p.sh.g * (p.sh.D + 4) * sizeof(float);
+  return 2 * (size_t)p.C * part + (p.merge_units ? (size_t)p.U_r + p.U_s : (size_t)p.C) * sizeof(int2);
 }
 
 cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, cudaStream_t stream) {

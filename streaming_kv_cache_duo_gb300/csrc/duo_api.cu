@@ -1041,7 +1041,7 @@ static duo_status decode_kv8_impl(duo_handle* h, const duo_kv_cache* c, const du
   if (reinterpret_cast<uintptr_t>(seq_lens) & 3u) return fail(DUO_ERR_INVALID_ARG, "seq_lens not 4-byte aligned");
   if (!q || !o || !aligned16(q) || !aligned16(o))
     return fail(DUO_ERR_INVALID_ARG, "q / o NULL or not 16-byte aligned");
-  // two parts per CTA and the merge's jobs: within the size every decode entry point asks for
+  // the size every decode entry point asks for
   const size_t need = decode_workspace_bytes(sh, h->num_sms * kDecodeCtasPerSmKv4);
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(DUO_ERR_INVALID_ARG, "workspace not 256-byte aligned");
@@ -1075,6 +1075,10 @@ static duo_status decode_kv8_impl(duo_handle* h, const duo_kv_cache* c, const du
   p.heads = h->heads;
   p.pg = pg;
   plan_decode_kv8(&p, h->num_sms);
+  // (two parts per CTA and the merge's jobs: within that size for every shape; refused if it were not)
+  if (decode_kv8_workspace_bytes(p) > need)
+    return fail(DUO_ERR_WORKSPACE, "the plan's %zu bytes of workspace pass the %zu of a decode",
+                decode_kv8_workspace_bytes(p), need);
   cudaError_t ce = launch_decode_kv8(p, (cudaStream_t)stream);
   if (ce != cudaSuccess) return cuda_fail(ce, "decode launch (8-bit)");
   return ok();

@@ -293,7 +293,7 @@ cudaError_t launch_expand_kv8(const Kv8ExpandParams& p, cudaStream_t stream);
 cudaError_t expand_kv8_read_clear_error(uint32_t* code);
 
 struct Kv8DecodeParams {
-  CUtensorMap tm_k;  // 2-D over the codes [rows, D], box 32 x D, swizzled by the row width
+  CUtensorMap tm_k;  // 2-D over the codes [rows, D], box kv8_slice_rows(D) x D, swizzled by the row width
   CUtensorMap tm_v;
   const uint16_t* q;  // bf16 [B, Hq, D]
   uint16_t* o;
@@ -317,13 +317,15 @@ struct Kv8DecodeParams {
   int64_t cap64;
   float scale_log2;  // log2(e) / sqrt(D)
   float* partials;   // [C][2][g][D + 4]: per CTA the part that goes on with a unit, and the one that
-                     // begins one; then the merge's jobs, int2 [C]
+                     // begins one; then the merge's jobs, int2 [C], or [U_r + U_s] if merge_units
   Shape sh;
   HeadTable heads;
   PagedLayout pg;
 };
-// Chooses C and whole from the other fields.
+// Sets C, whole, merge_units, tiles_r, tiles_s, line_r, line_s and str_place from sh, U_r, U_s, n and
+// code_type.
 void plan_decode_kv8(Kv8DecodeParams* p, int num_sms);
+size_t decode_kv8_workspace_bytes(const Kv8DecodeParams& p);  // that a planned decode writes
 cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, cudaStream_t stream);
 cudaError_t decode_kv8_read_clear_error(uint32_t* code);
 
