@@ -77,8 +77,9 @@ def block_tables_update(table, free, count, lens, new, block_size, max_tokens):
         if new[b] == -1:
             for p in range(planes):
                 for j in range(held[b]):
-                    free[count] = int(table[b, p, j])
-                    count += 1
+                    if 0 <= table[b, p, j] < len(free):  # an id that is none is dropped
+                        free[count] = int(table[b, p, j])
+                        count += 1
             lens[b] = 0
     cu = np.zeros(B + 1, np.int64)
     for b in range(B):

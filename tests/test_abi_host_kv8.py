@@ -59,3 +59,13 @@ def test_kv8_entry_points_refuse_a_null_handle(lib):
     for call in calls:
         with pytest.raises(lib.DuoError, match="DUO_ERR_INVALID_ARG"):
             call()
+
+
+def test_kv8_prefill_entry_points_refuse_a_null_handle(lib):
+    cache, kv8, paged = lib.duo_kv_cache(), lib.duo_kv8_cache(), lib.duo_paged()
+    calls = [lambda: lib.duo_attn_prefill_kv8(None, cache, kv8, None, None, None, 1, None, None, stream=0),
+             lambda: lib.duo_attn_prefill_kv8_paged(None, cache, paged, kv8, None, None, None, 1, None, None, stream=0)]
+    for call in calls:
+        with pytest.raises(lib.DuoError, match="DUO_ERR_INVALID_ARG"):
+            call()
+    assert lib.duo_prefill_kv8_workspace_size(None, 1000, 16) == 0
