@@ -127,7 +127,7 @@ __device__ __forceinline__ int cta_of(const DecodeParams& p, int64_t t) {
 // array clamped to the planned maximum n (so no tile beyond the plan is read).
 __device__ __forceinline__ int64_t seq_len(const DecodeParams& p, int b) {
   if (!p.seq_lens) return p.n;
-  const int64_t v = __ldg(p.seq_lens + b);
+  const int64_t v = p.seq_lens[b];
   return v < 0 ? 0 : (v > p.n ? p.n : v);
 }
 
@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, is_kv4_mode(kMode) ? kDecodeCtasPerS
             bool valid = key < rows;
             if (x.streaming && valid) {
               const int64_t slot = kt * C::TK + (int64_t)warp * C::KPW + key;
-              const int jp = str_pool ? (int)slot : __ldg(p.pos + (int64_t)x.b * SR + slot);
+              const int jp = str_pool ? (int)slot : p.pos[(int64_t)x.b * SR + slot];
               valid = jp >= 0 && jp <= x.pq && (jp < p.sh.S || x.pq - jp < p.sh.R);
             }
             kvalid |= (uint32_t)valid << k;
@@ -1050,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, is_kv4_mode(kMode) ? kDecodeCtasPerS
             valid = key < rows;
             if (x.streaming && valid) {
               const int64_t slot = kt * C::TK + (int64_t)warp * C::KPW + key;
-              const int jp = str_pool ? (int)slot : __ldg(p.pos + (int64_t)x.b * SR + slot);
+              const int jp = str_pool ? (int)slot : p.pos[(int64_t)x.b * SR + slot];
               valid = jp >= 0 && jp <= x.pq && (jp < p.sh.S || x.pq - jp < p.sh.R);
             }
           }

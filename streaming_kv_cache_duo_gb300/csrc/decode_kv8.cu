@@ -201,7 +201,7 @@ __device__ __forceinline__ int chunk16_at(int row, int c) {
 
 __device__ __forceinline__ int seq_len(const Kv8DecodeParams& p, int b) {
   if (!p.seq_lens) return (int)p.n;
-  const int v = __ldg(p.seq_lens + b);
+  const int v = p.seq_lens[b];
   return v < 0 ? 0 : (v > p.n ? (int)p.n : v);
 }
 
@@ -434,7 +434,7 @@ struct Cursor {
           codes = true;
           if (p.pg.table) {
             pages = p.pg.table + ((int64_t)x.b * p.sh.n_ret + x.idx) * p.pg.max_blocks;
-            blk = __ldg(pages + (uint32_t)row / (uint32_t)p.pg.block_size);
+            blk = pages[(uint32_t)row / (uint32_t)p.pg.block_size];
           }
           return;
         }
@@ -465,7 +465,7 @@ struct Cursor {
     ++lt;
     if (codes && lt < lt1 && (int64_t)row + TK < code_rows) {  // (the most frequent case, kept short)
       row += TK;
-      if (p.pg.table) blk = __ldg(pages + (uint32_t)row / (uint32_t)p.pg.block_size);
+      if (p.pg.table) blk = pages[(uint32_t)row / (uint32_t)p.pg.block_size];
       return;
     }
     settle(p);
@@ -750,7 +750,7 @@ __device__ __forceinline__ void fetch_pos(const Kv8DecodeParams& p, const Unit& 
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int row = r0 + gid + 8 * k;
-    at[k] = row >= have ? -1 : (x.streaming ? __ldg(p.pos + (int64_t)x.b * (p.sh.S + p.sh.R) + row) : 0);
+    at[k] = row >= have ? -1 : (x.streaming ? p.pos[(int64_t)x.b * (p.sh.S + p.sh.R) + row] : 0);
   }
 }
 
@@ -780,7 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv8_kernel(const __grid_co
     }
   }
   __syncthreads();
-  // Launched as a programmatic dependent: nothing the grid before it writes is read earlier.
+  // Launched as a programmatic dependent: nothing the grid before it writes is read earlier, and none of
+  // it (lengths, tables, ring positions) through the read-only path, which may assume that it does not
+  // change while this kernel lives.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Share sh = share_of<D>(p, reinterpret_cast<int64_t*>(red));

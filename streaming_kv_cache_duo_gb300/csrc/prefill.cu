@@ -829,11 +829,12 @@ __global__ void __launch_bounds__(Roles<kMode>::kThreads, 1) prefill_kernel(cons
     bool ok = true;
     // factors of 32 blocks (16 tiles) of an 8-bit cache, one per lane: K's, and the logarithm of V's
     float fk = 1.f, lf = 0.f, fk_next = 1.f, lf_next = 0.f;
+    // (plain loads: the grid that writes them may still run when this one is launched)
     auto factors = [&](int k, float& f, float& l) {  // of the 16 tiles around tile k
       const int blk = (k & ~15) * 2 + lane;
       const int64_t at = ((int64_t)it.b * p.sh.n_ret + it.cidx) * p.fac_blocks + blk;
-      f = blk < p.fac_blocks ? __ldg(p.k_fac + at) : 1.f;
-      l = blk < p.fac_blocks ? __ldg(p.v_fac + at) : 0.f;
+      f = blk < p.fac_blocks ? p.k_fac[at] : 1.f;
+      l = blk < p.fac_blocks ? p.v_fac[at] : 0.f;
     };
     // packed: a warp without a row of the chunk does no softmax (what its rows of S hold goes for P,
     // and their O is not stored). In a loop of its own: a branch in the other one cost 1 %.
