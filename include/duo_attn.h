@@ -399,8 +399,8 @@ duo_status duo_kv_append_kv8_ragged(duo_handle* handle, duo_kv_cache* cache, con
  * calls): scores and outputs are accumulated in fp32 from the codes (fp16 tensor-core
  * operands, exact for both code types; q scaled to fp16 by a power of two of its own per
  * head, so any finite bf16 q is taken) and the tail and ring rows (bf16 operands); p is
- * rounded to fp16 over codes and to bf16 over bf16 rows. Workspace as for duo_attn_decode; o
- * must not overlap q.
+ * rounded to fp16 over codes and to two bf16 terms (2^-17) over bf16 rows. Workspace as for
+ * duo_attn_decode; o must not overlap q.
  * duo_attn_decode_kv8_varlen reads the lengths on the device (seq_lens int32 [B], clamped
  * to [0, max_len], the new token included; a sequence of length 0 gets zeros) and splits the
  * work by them; `paged` may be NULL (contiguous caches). */

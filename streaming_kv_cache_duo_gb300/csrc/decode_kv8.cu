@@ -37,7 +37,8 @@
 // K's fragments come by ldmatrix, V's by its transposing form for bytes, whose rows are named in
 // the order that makes each lane's four bytes the keys of its P fragment: no byte is shuffled.
 //
-// bf16 rows (at most 63 of a tail, S + R of a ring) take bf16 products. Only these need masks.
+// bf16 rows (at most 63 of a tail, S + R of a ring) take bf16 products, p as two terms. Only these need
+// masks.
 //
 // Bound by HBM: one million tokens with two retrieval heads, int8, 86 us = 6.3 TB/s of the 538 MB
 // stored (0.92 of the measured copy rate; a CTA works through a tile in 1.3 us, 7.5 TB/s in all).
@@ -662,8 +663,12 @@ struct State {
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = (sc[0][k] + sc[1][k]) * qf;
     softmax<4, true>(x, vis);
-    const uint32_t pb0 = transpose8x8(pack_bf16x2(x[0], x[1]));
-    const uint32_t pb1 = transpose8x8(pack_bf16x2(x[2], x[3]));
+    // p in two bf16 terms, 2^-17 of it left out: one alone, 2^-9, was most of the decode's error (outputs
+    // 0.0022 of their norm off, the streaming heads' above all, where the output's rounding is 0.0017)
+    const uint32_t p01 = pack_bf16x2(x[0], x[1]), p23 = pack_bf16x2(x[2], x[3]);
+    const uint32_t pb0 = transpose8x8(p01), pb1 = transpose8x8(p23);
+    const uint32_t pl0 = transpose8x8(pack_bf16x2(x[0] - bf16lo(p01), x[1] - bf16hi(p01)));
+    const uint32_t pl1 = transpose8x8(pack_bf16x2(x[2] - bf16lo(p23), x[3] - bf16hi(p23)));
     // a value row nobody sees (an empty or evicted slot) may hold anything: out of the product.
     // Lane (g, .) knows of keys g and g + 8; the V fragments hold keys 2 tig, 2 tig + 1 (+ 8).
     const uint32_t seen = __ballot_sync(0xffffffffu, vis & 1u);          // bit 4 g: key g
@@ -674,7 +679,9 @@ struct State {
     for (int i = 0; i < MT; ++i) {
       uint32_t w[4];  // dims 16 i + gid and + 8, keys below 8; the same, keys from 8
       ldm4_trans(sv + chunk16_at<D>((lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)), w);
-      mma<false>(o[i], w[0] & m0, w[1] & m0, w[2] & m8, w[3] & m8, pb0, pb1);
+      const uint32_t v0 = w[0] & m0, v1 = w[1] & m0, v2 = w[2] & m8, v3 = w[3] & m8;
+      mma<false>(o[i], v0, v1, v2, v3, pl0, pl1);
+      mma<false>(o[i], v0, v1, v2, v3, pb0, pb1);
     }
   }
 
