@@ -214,7 +214,9 @@ duo_status duo_attn_decode_static(duo_handle* handle, const duo_kv_cache* cache,
  * The capacity of a head is block_size * max_blocks tokens (max_seq_len is not used).
  * A block id outside [0, num_blocks) that would be read or written is never
  * dereferenced: its rows are skipped and duo_device_error() reports
- * DUO_ERR_INVALID_ARG. Retrieval results equal the contiguous layout's, bit for bit. */
+ * DUO_ERR_INVALID_ARG (a prefill over bf16 pools reads them as zeros, which take part in its
+ * softmax; decodes and the 8-bit prefill leave them out). Other rows, and later calls, are
+ * not affected. Retrieval results equal the contiguous layout's, bit for bit. */
 typedef struct {
   const int32_t* block_table;  /* int32 [B, n_ret, max_blocks], device memory (NULL if n_ret = 0) */
   int32_t block_size;          /* rows per block, a positive multiple of 128 */
@@ -415,7 +417,9 @@ duo_status duo_attn_decode_kv8_varlen(duo_handle* handle, const duo_kv_cache* ca
 
 /* Prefill of T new tokens against 8-bit caches, as duo_attn_prefill: the cache's rows are
  * code * scale (tail and ring rows are bf16), the T new tokens' k and v the bf16 inputs.
- * Append the chunk afterwards. The codes are written to `workspace` once, as bf16 times the
+ * Append the chunk afterwards. Every sequence holds cache->n tokens and takes T: there is no form
+ * with lengths on the device, so ragged prompts are prefilled a sequence (or a group of one length)
+ * at a time, through a handle of that batch. The codes are written to `workspace` once, as bf16 times the
  * power of two in their scale (exact; the rest of the scale is applied in fp32, V's to p before
  * p is rounded to bf16), and read from there by every query block; retrieval heads with few
  * query blocks are split over their keys, their parts merged by log-sum-exp. workspace:

@@ -14,10 +14,11 @@
 // earlier block of this call reads the tail rows they replace: then by the CTA that read them,
 // after it. One pass: the block sits in registers (16 KB over 128 threads) between the maximum
 // and the codes. HBM-bound for prompts: 2 D bytes in, D out per row. A prompt of 32K tokens with four
-// retrieval heads, D = 128: 26.6 us (e4m3), 25.2 (int8); HBM's share is 15. As many CTAs per SM as
-// registers allow without spills: seven (72 registers) at D = 128, ten at 64. K and V in one CTA of
-// 256 threads took 27.1 / 25.4 us, and 20.2 instead of 17.4 for 2 x 8192 tokens, eight heads, D = 64;
-// CTAs that fetch the next block's rows while they round the ones they have 32 / 28.
+// retrieval heads, D = 128, e4m3: 25.4 us (replayed graphs, one after the other; 22.7 among other calls,
+// whose starts and ends overlap); HBM's share is 15. As many CTAs per SM as registers allow without
+// spills in the loops: seven (72 registers) at D = 128, ten at 64 (48, 4 bytes spilled). K and V in one
+// CTA of 256 threads took 27.1 us, and 20.2 instead of 17.4 for 2 x 8192 tokens, eight heads, D = 64;
+// CTAs that fetch the next block's rows while they round the ones they have 32 / 28 (graphs as well).
 #include "duo_device.cuh"
 
 namespace duo {

@@ -40,10 +40,11 @@
 // bf16 rows (at most 63 of a tail, S + R of a ring) take bf16 products, p as two terms. Only these need
 // masks.
 //
-// Bound by HBM: one million tokens with two retrieval heads, int8, 86 us = 6.3 TB/s of the 538 MB
-// stored (0.92 of the measured copy rate; a CTA works through a tile in 1.3 us, 7.5 TB/s in all).
-// What is left is fixed: 2.8 us until a CTA's first tiles are under way, a merge of 0.8 us, the
-// second kernel and two launches, 8 us.
+// Bound by HBM: one million tokens with two retrieval heads, int8: 86 us in replayed graphs, one after the
+// other = 6.25 TB/s of the 538 MB stored (0.92 of the measured copy rate), 83 us (0.95) among other calls,
+// whose starts and merges overlap; a CTA works through a tile in 1.3 us, 7.5 TB/s in all. What is left is
+// fixed: 2.8 us until a CTA's first tiles are under way, a merge of 0.8 us, the second kernel and two
+// launches, 8 us. (The figures above and below are of replayed graphs.)
 //
 // Merge: as the bf16 decode. The warps of a CTA merge in shared memory; a unit split over
 // CTAs leaves (o, max, sum) parts for a second kernel, launched as a programmatic dependent.
