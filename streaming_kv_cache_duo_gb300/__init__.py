@@ -454,7 +454,9 @@ class DuoKv8PagedLayer(DuoKv8Layer):
                                     max_blocks, num_blocks, None)
 
     def append_ragged(self, k_new, v_new, slot_map, stream=None) -> None:
-        """A packed batch of tokens [num_tokens, Hkv, D], each at its own place (a DuoSlotMap)."""
+        """A packed batch of tokens [num_tokens, Hkv, D], each at its own place (a DuoSlotMap). The lengths
+        stay on the device: ``n`` does not change, so ``decode`` and ``prefill``, which go by it, need
+        ``cache.n`` set by the caller (and sequences of one length)."""
         N = k_new.shape[0]
         _on(self, "k_new", k_new, (N, self.Hkv, self.D))
         _on(self, "v_new", v_new, (N, self.Hkv, self.D))
