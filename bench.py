@@ -42,27 +42,26 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 
 
 # DRAM traffic per launch (dram__bytes_read.sum + dram__bytes_write.sum) from the ncu
-# captures summarised in profiles/, valid only for the kernel sources they were taken on
-# (the decode records were re-keyed after a comment-only edit to the 4-bit consumer).
+# captures summarised in profiles/, valid only for the kernel sources they were taken on.
 L2_BYTES = 129e6  # GB300 L2 capacity
 
 MEASURED_TRAFFIC = {
-    "prefill": {"src": ("prefill.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "7a550e89e096f3fb",
-                "bytes": 471.982e6 + 233.347e6},
+    "prefill": {"src": ("prefill.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "aab557001cd88135",
+                "bytes": 472.376e6 + 233.057e6},
     # the 8 prefill launches of one chunked-prefill step (Llama-2-7B shape, 8 x 4096 tokens)
-    "prefill_chunked": {"src": ("prefill.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "7a550e89e096f3fb",
-                        "bytes": 1305.004e6 + 96.197e6},
+    "prefill_chunked": {"src": ("prefill.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "aab557001cd88135",
+                        "bytes": 1304.527e6 + 102.780e6},
     # the same against 4-bit caches (codes + pairs read and dequantized in the kernel)
-    "prefill_chunked_kv4": {"src": ("prefill.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "7a550e89e096f3fb",
-                            "bytes": 940.968e6 + 84.545e6},
+    "prefill_chunked_kv4": {"src": ("prefill.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "aab557001cd88135",
+                            "bytes": 940.606e6 + 86.176e6},
     # one decode launch of the batched 8 x 128K workload (device lengths, graph replay)
-    "decode_batched": {"src": ("decode.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "2a2b52e1174c6bc6",
-                       "bytes": 1.081919e9 + 1.479e6},
-    "decode": {"src": ("decode.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "2a2b52e1174c6bc6",
-               "bytes": 1.074810e9 + 1.485e6},
+    "decode_batched": {"src": ("decode.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "0ac0eec9e9eb318e",
+                       "bytes": 1.081921e9 + 1.831e6},
+    "decode": {"src": ("decode.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "0ac0eec9e9eb318e",
+               "bytes": 1.074808e9 + 1.527e6},
     # one decode launch of the million-token decode over 4-bit caches (stored bytes read)
-    "decode_kv4": {"src": ("decode.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "2a2b52e1174c6bc6",
-                   "bytes": 285.598976e6 + 3.443456e6},
+    "decode_kv4": {"src": ("decode.cu", "duo_device.cuh", "duo_internal.h"), "sha1": "0ac0eec9e9eb318e",
+                   "bytes": 285.558e6 + 1.547e6},
 }
 
 
