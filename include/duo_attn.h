@@ -485,6 +485,63 @@ duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* ne
                                    int32_t* seq_lens_out, int32_t* free_count_out, const duo_slot_map* map,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* A packed ragged step over bf16 paged caches: the tokens of all sequences lie one behind the
+ * other, a duo_slot_map says whose they are and where they go, and every length is read on the
+ * device, so the calls of a step can be captured in a CUDA graph. In this order:
+ *   a step with chunks:  duo_rope_rotate (q, k), duo_attn_prefill_ragged, duo_kv_append_ragged
+ *                        (without a rotation: k is rotated already)
+ *   one token each:      duo_kv_append_ragged (with the rotation, q beside k),
+ *                        duo_attn_decode_paged_varlen
+ * Rows are bf16 [num_tokens, heads, D] whose tokens may lie apart, as slices of a fused
+ * projection's output do: token t begins `stride` elements after token t - 1 (a multiple of 8,
+ * at least heads x D; data 16-byte aligned). */
+typedef struct {
+  void* data;
+  int64_t stride;
+} duo_rows;
+
+/* Rotary positions. Pair i (0 <= i < rotary_dim / 2) of a row, (a, b), at position p becomes
+ *     (scale (a cos t - b sin t), scale (b cos t + a sin t)),  t = p f_i,
+ * computed in fp32 from bf16 values and rounded once. The pairs are dims (i, i + rotary_dim / 2)
+ * (DUO_ROPE_HALF) or (2 i, 2 i + 1) (DUO_ROPE_INTERLEAVED) of the head; dims from rotary_dim on
+ * pass through unchanged. Any frequencies will do (scaled ones for long contexts are made on the
+ * host); `scale` is the factor that some of these schemes apply to rotated pairs, else 1.
+ *   turns: device memory, [rotary_dim / 2], from duo_rope_turns: the angle per position of each
+ *          pair as a fraction of a full turn, in units of 2^-64. A position times it wraps as
+ *          angles do, so the angle is exact at every position up to 2^31 - 1. */
+#define DUO_ROPE_HALF 0
+#define DUO_ROPE_INTERLEAVED 1
+
+typedef struct {
+  const uint64_t* turns;
+  int32_t rotary_dim; /* a multiple of 16, 16 ... head_dim */
+  int32_t layout;     /* DUO_ROPE_HALF or DUO_ROPE_INTERLEAVED */
+  float scale;
+} duo_rope;
+
+/* turns[i] of angles per position inv_freq[i] (radians, finite). Host arrays; host only. */
+duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns);
+
+/* Rotates the rows of q and, unless k is NULL, of k (head_dim 64 or 128) by positions [num_tokens]
+ * (int32, device memory); a token at a position below 0 is skipped, its rows of q_out and k_out are
+ * left as they were. q_out may be q (with its stride) and k_out k; other overlaps are not allowed. */
+duo_status duo_rope_rotate(const duo_rope* rope, int32_t head_dim, const int32_t* positions, int32_t num_tokens,
+                           const duo_rows* q, const duo_rows* q_out, int32_t num_q_heads, const duo_rows* k,
+                           const duo_rows* k_out, int32_t num_kv_heads, void* stream);
+
+/* Append of a packed batch into bf16 paged caches, each sequence with its own length and number of
+ * new tokens: k_new, v_new [num_tokens, Hkv, D]. Positions and rows come from `map` alone, as for
+ * duo_kv_append_kv8_ragged: retrieval rows to the pool's rows map->slots, streaming heads' rows to
+ * their sink + ring slots (of the tokens of one call only those still held when it ends); tokens at
+ * position -1 are skipped; a slot or sequence out of range is not dereferenced, its rows are skipped
+ * and duo_device_error() reports DUO_ERR_INVALID_ARG. paged->stream_table must be NULL. cache->n is
+ * neither read nor changed. With `rope` (or NULL: none) K is rotated by map->token_pos on the way,
+ * and with q and q_out [num_tokens, Hq, D] (or both NULL) q is rotated beside it (q_out may be q). */
+duo_status duo_kv_append_ragged(duo_handle* handle, duo_kv_cache* cache, const duo_paged* paged,
+                                const duo_slot_map* map, int32_t num_tokens, const duo_rope* rope,
+                                const duo_rows* k_new, const duo_rows* v_new, const duo_rows* q,
+                                const duo_rows* q_out, void* stream);
+
 /* Dual Chunk Attention (vLLM pull request "[Model] Implement DualChunkAttention for
  * Qwen2 Models"): the sequence is cut into chunks of chunk_len positions from the start
  * (the last one may be shorter) and every position carries three query vectors made by

@@ -158,6 +158,7 @@ class DuoPagedLayer(DuoLayer):
                          device=device)
         bf = dict(dtype=torch.bfloat16, device=self.device)
         self.block_size = block_size
+        self.index, self.bf16 = self.pos.get_device(), torch.bfloat16
         self.k_full = torch.empty((num_blocks, block_size, head_dim), **bf)
         self.v_full = torch.empty_like(self.k_full)
         self.cache.k_full = self.k_full.data_ptr()
@@ -199,6 +200,146 @@ class DuoPagedLayer(DuoLayer):
             out = torch.empty_like(q)
         _lib.duo_attn_decode_paged(self.handle, self.cache, self.paged, q, out, self.workspace, stream)
         return out
+
+
+    def append_ragged(self, k_new, v_new, slot_map, rope=None, q=None, q_out=None, stream=None):
+        """A packed batch of tokens [num_tokens, Hkv, D], each at its own place (a DuoSlotMap); with
+        ``rope`` (a DuoRope) K is rotated on the way, and q [num_tokens, Hq, D] beside it into q_out
+        (allocated if not given; it may be q), which is returned. Tokens may lie apart (slices of a
+        fused projection). The lengths stay on the device: ``n`` does not change."""
+        N = k_new.shape[0]
+        self._check_packed(slot_map, N, planes=True)
+        _packed_rows(self, "k_new", k_new, (N, self.Hkv, self.D))
+        _packed_rows(self, "v_new", v_new, (N, self.Hkv, self.D))
+        if q is not None:
+            _packed_rows(self, "q", q, (N, self.Hq, self.D))
+            if q_out is None:
+                import torch
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            else:
+                _packed_rows(self, "q_out", q_out, (N, self.Hq, self.D))
+        if rope is not None and (rope.head_dim != self.D or rope.index != self.index):
+            raise ValueError(f"rope: for head_dim {rope.head_dim} on CUDA device {rope.index}, the layer has {self.D} on {self.index}")
+        _lib.duo_kv_append_ragged(self.handle, self.cache, self.paged, slot_map.c, N, None if rope is None else rope.c,
+                                  k_new, v_new, q, q_out, stream)
+        return q_out
+
+    def _check_packed(self, slot_map, N, planes):
+        if slot_map.cu_new.get_device() != self.index:
+            raise ValueError(f"slot_map: on {slot_map.cu_new.device}, the layer is on CUDA device {self.index}")
+        if slot_map.batch != self.B or slot_map.num_tokens != N or (planes and self.n_ret and slot_map.planes != self.n_ret):
+            raise ValueError(f"slot_map: of {slot_map.batch} sequences, {slot_map.num_tokens} tokens and "
+                             f"{slot_map.planes} planes; need {self.B}, {N} and {self.n_ret}")
+
+
+class DuoRope:
+    """Frequencies of rotary positions (duo_rope): the first ``rotary_dim`` dims (a multiple of 16; all by
+    default) of a head are rotated, in pairs half of them apart (layout "half") or of neighbours
+    ("interleaved"). Pair i turns theta^(-2 i / rotary_dim) radians a position; ``scaling`` changes that
+    for contexts past the trained length:
+
+      dict(kind="linear", factor)     every frequency divided by factor
+      dict(kind="ntk", factor)        theta multiplied by factor^(rotary_dim / (rotary_dim - 2))
+      dict(kind="yarn", factor, original[, beta_fast=32, beta_slow=1])
+                                      pairs that turn more than beta_fast times over the original length
+                                      keep their frequency, those that turn less than beta_slow times get
+                                      it divided by factor, a ramp over the pairs between; rotated pairs
+                                      are multiplied by 0.1 ln(factor) + 1
+      dict(kind="wavelength", factor, low, high, original)
+                                      as yarn, the ramp over the number of turns, between low and high;
+                                      no factor on the pairs
+
+    ``inv_freq`` (radians per position, rotary_dim / 2 of them) gives any other frequencies, ``scale`` any
+    other factor of the rotated pairs. Angles are exact at every position up to 2^31 - 1."""
+
+    def __init__(self, head_dim, theta=10000.0, rotary_dim=None, layout="half", scaling=None, inv_freq=None,
+                 scale=None, device="cuda"):
+        import torch
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f'layout: "half" or "interleaved", got {layout!r}')
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if head_dim not in (64, 128) or rotary_dim % 16 or not 16 <= rotary_dim <= head_dim:
+            raise ValueError(f"head_dim {head_dim}, rotary_dim {rotary_dim}: need 64 or 128, and a multiple of 16 up to it")
+        if inv_freq is None:
+            inv_freq, factor = rope_frequencies(rotary_dim, theta, scaling)
+        elif scaling is not None:
+            raise ValueError("inv_freq: given frequencies are not scaled")
+        else:
+            inv_freq, factor = [float(f) for f in inv_freq], 1.0
+        if len(inv_freq) != rotary_dim // 2:
+            raise ValueError(f"inv_freq: {len(inv_freq)} frequencies for {rotary_dim // 2} pairs")
+        self.head_dim, self.rotary_dim, self.layout, self.inv_freq = head_dim, rotary_dim, layout, inv_freq
+        self.scale = float(factor if scale is None else scale)
+        self.device = torch.device(device)
+        turns = [t - (1 << 64) if t >> 63 else t for t in _lib.duo_rope_turns(inv_freq)]
+        self.turns = torch.tensor(turns, dtype=torch.int64).to(self.device)
+        self.index, self.bf16, self.int32 = self.turns.get_device(), torch.bfloat16, torch.int32
+        self.empty = torch.empty
+        self.c = _lib.duo_rope(self.turns.data_ptr(), rotary_dim,
+                               _lib.DUO_ROPE_HALF if layout == "half" else _lib.DUO_ROPE_INTERLEAVED, self.scale)
+
+    def rotate(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """q [num_tokens, Hq, head_dim] and k [num_tokens, Hkv, head_dim] (or None) rotated by positions
+        (int32 [num_tokens]); returns (q_out, k_out), new tensors unless given (they may be q and k).
+        Rows of tokens at positions below 0 are not written."""
+        N = positions.shape[0]
+        if (positions.dtype is not self.int32 or positions.get_device() != self.index or positions.dim() != 1
+                or not positions.is_contiguous()):
+            raise ValueError(f"positions: need a contiguous int32 tensor of one dimension on CUDA device {self.index}")
+        if _lib._current_device() != self.index:
+            raise ValueError(f"the current device is not the frequencies' (CUDA device {self.index})")
+        _packed_rows(self, "q", q, (N, q.shape[1], self.head_dim))
+        if q_out is None:
+            q_out = self.empty(q.shape, dtype=self.bf16, device=q.device)
+        else:
+            _packed_rows(self, "q_out", q_out, q.shape)
+        if k is not None:
+            _packed_rows(self, "k", k, (N, k.shape[1], self.head_dim))
+            if k_out is None:
+                k_out = self.empty(k.shape, dtype=self.bf16, device=k.device)
+            else:
+                _packed_rows(self, "k_out", k_out, k.shape)
+        _lib.duo_rope_rotate(self.c, self.head_dim, positions, N, q, q_out, k, None if k is None else k_out, stream)
+        return q_out, k_out
+
+
+def rope_frequencies(rotary_dim, theta=10000.0, scaling=None):
+    """(radians per position of each pair, factor of the rotated pairs), as DuoRope describes them."""
+    import math
+    if not theta > 1:
+        raise ValueError(f"theta = {theta} is not above 1")
+    freq = [float(theta) ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if scaling is None:
+        return freq, 1.0
+    need = {"linear": ("factor",), "ntk": ("factor",), "yarn": ("factor", "original"),
+            "wavelength": ("factor", "low", "high", "original")}
+    kind = scaling.get("kind")
+    if kind not in need:
+        raise ValueError(f"scaling: kind {kind!r} is none of {sorted(need)}")
+    allowed = ("kind",) + need[kind] + (("beta_fast", "beta_slow") if kind == "yarn" else ())
+    if any(key not in scaling for key in need[kind]) or any(key not in allowed for key in scaling):
+        raise ValueError(f"scaling: {kind} takes {', '.join(allowed[1:])}; got {sorted(scaling)}")
+    if any(not (isinstance(scaling[key], (int, float)) and scaling[key] > 0) for key in scaling if key != "kind"):
+        raise ValueError("scaling: every value has to be a number above 0")
+    s = float(scaling["factor"])
+    if kind == "linear":
+        return [f / s for f in freq], 1.0
+    if kind == "ntk":
+        base = theta * s ** (rotary_dim / (rotary_dim - 2.0))
+        return [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)], 1.0
+    over = scaling["original"] / (2.0 * math.pi)  # turns over the original length: over x frequency
+    if kind == "wavelength":
+        low, high = scaling["low"], scaling["high"]
+        if not low < high:
+            raise ValueError(f"scaling: low = {low} is not below high = {high}")
+        keep = [min(1.0, max(0.0, (over * f - low) / (high - low))) for f in freq]
+        return [f * w + f / s * (1.0 - w) for f, w in zip(freq, keep)], 1.0
+    # the pair (a real number) that turns n times over the original length
+    pair = lambda n: rotary_dim * math.log(over / n) / (2.0 * math.log(theta))
+    first = max(0, math.floor(pair(scaling.get("beta_fast", 32.0))))
+    last = min(rotary_dim - 1, math.ceil(pair(scaling.get("beta_slow", 1.0))))
+    past = [min(1.0, max(0.0, (i - first) / max(last - first, 0.001))) for i in range(rotary_dim // 2)]
+    return [f * (1.0 - w) + f / s * w for f, w in zip(freq, past)], 0.1 * math.log(s) + 1.0
 
 
 class DuoKv4Layer(DuoLayer):
@@ -534,6 +675,14 @@ def _on(layer, name, t, shape):
     if (t.dtype is not layer.bf16 or t.get_device() != layer.index or t.shape != shape or not t.is_contiguous()):
         _lib._bf16(t, shape, name)
         raise ValueError(f"{name}: on {t.device}, the layer is on CUDA device {layer.index}")
+
+
+def _packed_rows(owner, name, t, shape):
+    """Rows of a packed batch on the owner's device: bf16 [tokens, heads, D], a token's rows in one piece."""
+    if (t.dtype is not owner.bf16 or t.get_device() != owner.index or t.shape != tuple(shape)
+            or (t.numel() and (t.stride(2) != 1 or t.stride(1) != shape[2] or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2])))):
+        raise ValueError(f"{name}: need a bfloat16 tensor of shape {tuple(shape)} on CUDA device {owner.index} with each token's "
+                         f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
 def _check_table(t, shape, index):

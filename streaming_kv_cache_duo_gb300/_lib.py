@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int32, c_int64, c_size_t, c_uint8, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint8, c_uint32, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libduo_attn.so")
 
@@ -30,6 +30,9 @@ DUO_KV8_BLOCK = 64  # tokens that share a scale in an 8-bit cache
 DUO_KV8_INT8 = 0
 DUO_KV8_E4M3 = 1
 
+DUO_ROPE_HALF = 0
+DUO_ROPE_INTERLEAVED = 1
+
 # exported names of include/duo_attn.h (checked against the library by the tests)
 EXPORTS = (
     "duo_classify_heads", "duo_create", "duo_destroy", "duo_set_head_mask", "duo_cache_reset", "duo_kv_append",
@@ -40,8 +43,9 @@ EXPORTS = (
     "duo_kv_append_kv8", "duo_kv_append_kv8_paged", "duo_kv_append_kv8_ragged", "duo_attn_decode_kv8",
     "duo_attn_decode_kv8_paged", "duo_attn_decode_kv8_varlen", "duo_attn_prefill_kv8",
     "duo_attn_prefill_kv8_paged", "duo_prefill_kv8_workspace_size", "duo_block_tables_workspace_size",
-    "duo_block_tables_update", "duo_kv_append_varlen", "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait",
-    "duo_last_error", "duo_status_string",
+    "duo_block_tables_update", "duo_rope_turns", "duo_rope_rotate", "duo_kv_append_ragged", "duo_kv_append_varlen",
+    "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait", "duo_last_error",
+    "duo_status_string",
 )
 
 
@@ -80,6 +84,14 @@ class duo_block_pool(ctypes.Structure):
     _fields_ = [(name, c_void_p) for name in ("block_table", "free_list", "free_count", "seq_lens")] + \
         [("batch", c_int32), ("planes", c_int32), ("block_size", c_int32), ("max_blocks", c_int32),
          ("num_blocks", c_int64)]
+
+
+class duo_rows(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride", c_int64)]
+
+
+class duo_rope(ctypes.Structure):
+    _fields_ = [("turns", c_void_p), ("rotary_dim", c_int32), ("layout", c_int32), ("scale", c_float)]
 
 
 class duo_kv_cache(ctypes.Structure):
@@ -161,6 +173,12 @@ def library() -> ctypes.CDLL:
         "duo_block_tables_workspace_size": (c_size_t, [c_int32]),
         "duo_block_tables_update": (c_int32, [POINTER(duo_block_pool), c_void_p, c_int32, c_void_p, c_void_p,
                                               POINTER(duo_slot_map), c_void_p, c_size_t, c_void_p]),
+        "duo_rope_turns": (c_int32, [POINTER(c_double), c_int32, POINTER(c_uint64)]),
+        "duo_rope_rotate": (c_int32, [POINTER(duo_rope), c_int32, c_void_p, c_int32, POINTER(duo_rows), POINTER(duo_rows),
+                                      c_int32, POINTER(duo_rows), POINTER(duo_rows), c_int32, c_void_p]),
+        "duo_kv_append_ragged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), POINTER(duo_slot_map),
+                                           c_int32, POINTER(duo_rope), POINTER(duo_rows), POINTER(duo_rows),
+                                           POINTER(duo_rows), POINTER(duo_rows), c_void_p]),
         "duo_kv_append_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_void_p, c_void_p,
                                            c_void_p]),
         "duo_attn_decode_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_int64, c_void_p, c_void_p,
@@ -433,6 +451,35 @@ def duo_paged_stream_dead_blocks(sink_size: int, recent_size: int, block_size: i
     _check(library().duo_paged_stream_dead_blocks(sink_size, recent_size, block_size, n, ctypes.byref(lo),
                                                   ctypes.byref(hi)))
     return int(lo.value), int(hi.value)
+
+
+def _rows(t):
+    """duo_rows of a tensor [num_tokens, heads, D] whose tokens may lie apart (or None)."""
+    if t is None:
+        return None
+    return ctypes.byref(duo_rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]))
+
+
+def duo_rope_turns(inv_freq) -> list:
+    """Angles per position (radians) -> fractions of a full turn in units of 2^-64."""
+    n = len(inv_freq)
+    turns = (c_uint64 * n)()
+    _check(library().duo_rope_turns((c_double * n)(*inv_freq), n, turns))
+    return list(turns)
+
+
+def duo_rope_rotate(rope: "duo_rope", head_dim: int, positions, num_tokens: int, q, q_out, k, k_out,
+                    stream=None) -> None:
+    """q and k (or None) [num_tokens, heads, head_dim] rotated by their tokens' positions."""
+    _check(library().duo_rope_rotate(_ref(rope), head_dim, _ptr(positions), num_tokens, _rows(q), _rows(q_out), q.shape[1],
+                                     _rows(k), _rows(k_out), 0 if k is None else k.shape[1], _stream_ptr(stream)))
+
+
+def duo_kv_append_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot_map: "duo_slot_map", num_tokens: int,
+                         rope, k_new, v_new, q=None, q_out=None, stream=None) -> None:
+    """A packed batch into bf16 paged caches, K (and q into q_out) rotated on the way with rope."""
+    _check(library().duo_kv_append_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, _ref(rope),
+                                          _rows(k_new), _rows(v_new), _rows(q), _rows(q_out), _stream_ptr(stream)))
 
 
 def duo_kv_append_varlen(handle, cache: "duo_kv_cache", seq_lens, k_new, v_new, stream=None) -> None:

@@ -15,6 +15,7 @@
 
 #include "../../include/duo_attn.h"
 #include "duo_internal.h"
+#include "ragged_internal.h"
 
 using namespace duo;
 
@@ -1166,6 +1167,160 @@ duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* ne
   return ok();
 }
 
+// ---------------------------------------------------------------------- packed ragged steps
+// Rows [num_tokens, heads, D] of a packed batch; `what` names them in messages.
+static duo_status check_rows(const duo_rows* r, int heads, int D, const char* what) {
+  if (!r || !r->data || !aligned16(r->data))
+    return fail(DUO_ERR_INVALID_ARG, "%s: NULL or not 16-byte aligned", what);
+  if (r->stride < (int64_t)heads * D || r->stride % 8 != 0)
+    return fail(DUO_ERR_INVALID_ARG, "%s: stride = %lld is not a multiple of 8, or below %d heads x %d", what,
+                (long long)r->stride, heads, D);
+  return DUO_OK;
+}
+
+// Rows that are rotated: out may be in itself.
+static duo_status check_rotated(const duo_rows* in, const duo_rows* out, int heads, int D, const char* what,
+                                RaggedRows* rows) {
+  duo_status st = check_rows(in, heads, D, what);
+  if (st != DUO_OK || (st = check_rows(out, heads, D, what)) != DUO_OK) return st;
+  if (in->data == out->data && in->stride != out->stride)
+    return fail(DUO_ERR_INVALID_ARG, "%s: rotated in place with another stride", what);
+  *rows = RaggedRows{static_cast<const uint16_t*>(in->data), static_cast<uint16_t*>(out->data), in->stride, out->stride,
+                     heads};
+  return DUO_OK;
+}
+
+static duo_status check_rope(const duo_rope* rope, int D, RopeParams* out) {
+  if (!rope->turns || (reinterpret_cast<uintptr_t>(rope->turns) & 7u))
+    return fail(DUO_ERR_INVALID_ARG, "rope: turns NULL or not 8-byte aligned");
+  if (rope->layout != DUO_ROPE_HALF && rope->layout != DUO_ROPE_INTERLEAVED)
+    return fail(DUO_ERR_INVALID_ARG, "rope: layout = %d is neither DUO_ROPE_HALF nor DUO_ROPE_INTERLEAVED", rope->layout);
+  if (rope->rotary_dim < 2 || rope->rotary_dim > D)
+    return fail(DUO_ERR_INVALID_ARG, "rope: rotary_dim = %d outside [2, %d]", rope->rotary_dim, D);
+  if (rope->rotary_dim % 16 != 0)
+    return fail(DUO_ERR_UNSUPPORTED, "rope: rotary_dim = %d is not a multiple of 16", rope->rotary_dim);
+  if (!std::isfinite(rope->scale)) return fail(DUO_ERR_INVALID_ARG, "rope: scale is not finite");
+  *out = RopeParams{rope->turns, rope->rotary_dim, rope->layout, rope->scale};
+  return DUO_OK;
+}
+
+// Tokens per CTA: one, so that a step of few tokens spreads over the SMs, up to kRopeChunk when there are
+// enough for eight CTAs an SM.
+static int rope_chunk(int tokens, int sms) { return std::max(1, std::min(tokens / (sms * 8), kRopeChunk)); }
+
+duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns) {
+  if (!inv_freq || !turns || count < 0) return fail(DUO_ERR_INVALID_ARG, "rope: NULL array or count < 0");
+  // f / 2 pi as a sum of two doubles (1 / 2 pi in two), its whole turns left out, then times 2^64
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57, kWord = 4294967296.0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (!std::isfinite(inv_freq[i])) return fail(DUO_ERR_INVALID_ARG, "rope: frequency %d is not finite", i);
+  }
+  for (int32_t i = 0; i < count; ++i) {
+    const double f = inv_freq[i], t = f * kHi;
+    const double rest = std::fma(f, kHi, -t) + f * kLo;
+    const double x = (t - std::floor(t)) * kWord, whole = std::floor(x);
+    const double low = std::rint((x - whole) * kWord + rest * kWord * kWord);  // |.| < 2^54
+    turns[i] = ((uint64_t)whole << 32) + (uint64_t)(int64_t)low;
+  }
+  return ok();
+}
+
+duo_status duo_rope_rotate(const duo_rope* rope, int32_t head_dim, const int32_t* positions, int32_t num_tokens,
+                           const duo_rows* q, const duo_rows* q_out, int32_t num_q_heads, const duo_rows* k,
+                           const duo_rows* k_out, int32_t num_kv_heads, void* stream) {
+  if (!rope) return fail(DUO_ERR_INVALID_ARG, "rope is NULL");
+  if (head_dim != 64 && head_dim != 128) return fail(DUO_ERR_UNSUPPORTED, "head_dim = %d not in {64, 128}", head_dim);
+  if (num_tokens < 0) return fail(DUO_ERR_INVALID_ARG, "num_tokens = %d < 0", num_tokens);
+  if (num_q_heads < 1 || num_q_heads > 65535 || (k && (num_kv_heads < 1 || num_kv_heads > 65535)))
+    return fail(DUO_ERR_INVALID_ARG, "number of heads outside [1, 65535]");
+  RopeAppendParams p;
+  memset(&p, 0, sizeof(p));
+  duo_status st = check_rope(rope, head_dim, &p.rope);
+  if (st != DUO_OK) return st;
+  if (num_tokens == 0) return ok();
+  if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(DUO_ERR_INVALID_ARG, "positions NULL or not 4-byte aligned");
+  if ((st = check_rotated(q, q_out, num_q_heads, head_dim, "q", &p.q)) != DUO_OK) return st;
+  if (k && (st = check_rotated(k, k_out, num_kv_heads, head_dim, "k", &p.k)) != DUO_OK) return st;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  p.positions = positions;
+  p.tokens = num_tokens;
+  p.chunk = rope_chunk(num_tokens, sms);
+  p.sh.D = head_dim;
+  e = launch_rope(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rotation launch");
+  return ok();
+}
+
+// What the calls of a packed step have in common: caches, pool and slot map of bf16 paged caches.
+static duo_status check_ragged(const duo_handle* h, const duo_kv_cache* c, const duo_paged* pgd, PagedLayout* pg) {
+  if (!pgd) return fail(DUO_ERR_INVALID_ARG, "paged is NULL");
+  if (pgd->stream_table)
+    return fail(DUO_ERR_UNSUPPORTED, "packed steps keep streaming heads in their ring caches");
+  *pg = PagedLayout{nullptr, 0, 0, 0, nullptr};
+  duo_status st;
+  if (h->sh.n_ret > 0 && (st = check_paged(h, pgd, pg)) != DUO_OK) return st;
+  if (!c) return fail(DUO_ERR_INVALID_ARG, "cache is NULL");
+  if (h->sh.n_ret > 0 && (!c->k_full || !c->v_full || !aligned16(c->k_full) || !aligned16(c->v_full)))
+    return fail(DUO_ERR_INVALID_ARG, "k_full / v_full NULL or not 16-byte aligned");
+  if (h->sh.n_str > 0 && (!c->k_sr || !c->v_sr || !c->pos || !aligned16(c->k_sr) || !aligned16(c->v_sr) || !aligned16(c->pos)))
+    return fail(DUO_ERR_INVALID_ARG, "k_sr / v_sr / pos NULL or not 16-byte aligned");
+  return DUO_OK;
+}
+
+static duo_status check_slot_map(const duo_slot_map* map, bool seq, bool slots) {
+  if (!map->cu_new || !map->token_pos || (seq && !map->token_seq) || (slots && !map->slots))
+    return fail(DUO_ERR_INVALID_ARG, "slot map: NULL array");
+  if ((reinterpret_cast<uintptr_t>(map->cu_new) | reinterpret_cast<uintptr_t>(map->token_seq) |
+       reinterpret_cast<uintptr_t>(map->token_pos)) & 3u || reinterpret_cast<uintptr_t>(map->slots) & 7u)
+    return fail(DUO_ERR_INVALID_ARG, "slot map: misaligned array");
+  return DUO_OK;
+}
+
+duo_status duo_kv_append_ragged(duo_handle* h, duo_kv_cache* c, const duo_paged* paged, const duo_slot_map* map,
+                                int32_t num_tokens, const duo_rope* rope, const duo_rows* k_new, const duo_rows* v_new,
+                                const duo_rows* q, const duo_rows* q_out, void* stream) {
+  duo_status st = check_handle(h);
+  if (st != DUO_OK) return st;
+  if (!map) return fail(DUO_ERR_INVALID_ARG, "map is NULL");
+  if (num_tokens < 0) return fail(DUO_ERR_INVALID_ARG, "num_tokens = %d < 0", num_tokens);
+  const Shape& sh = h->sh;
+  RopeAppendParams p;
+  memset(&p, 0, sizeof(p));
+  PagedLayout pg;
+  if ((st = check_ragged(h, c, paged, &pg)) != DUO_OK) return st;
+  if (rope && (st = check_rope(rope, sh.D, &p.rope)) != DUO_OK) return st;
+  if (!rope && (q || q_out)) return fail(DUO_ERR_INVALID_ARG, "q is rotated on the way: it needs rope");
+  if (!q != !q_out) return fail(DUO_ERR_INVALID_ARG, "q and q_out: one of them is NULL");
+  if (num_tokens == 0) return ok();
+  if ((st = check_slot_map(map, true, sh.n_ret > 0)) != DUO_OK) return st;
+  if ((st = check_rows(k_new, sh.Hkv, sh.D, "k_new")) != DUO_OK) return st;
+  if ((st = check_rows(v_new, sh.Hkv, sh.D, "v_new")) != DUO_OK) return st;
+  if (q && (st = check_rotated(q, q_out, sh.Hq, sh.D, "q", &p.q)) != DUO_OK) return st;
+  p.k = RaggedRows{static_cast<const uint16_t*>(k_new->data), nullptr, k_new->stride, 0, sh.Hkv};
+  p.v = RaggedRows{static_cast<const uint16_t*>(v_new->data), nullptr, v_new->stride, 0, sh.Hkv};
+  p.positions = map->token_pos;
+  p.tokens = num_tokens;
+  p.chunk = rope_chunk(num_tokens, h->num_sms);
+  p.cu_new = map->cu_new;
+  p.token_seq = map->token_seq;
+  p.slots = map->slots;
+  p.k_pool = static_cast<uint16_t*>(c->k_full);
+  p.v_pool = static_cast<uint16_t*>(c->v_full);
+  p.k_sr = static_cast<uint16_t*>(c->k_sr);
+  p.v_sr = static_cast<uint16_t*>(c->v_sr);
+  p.pos = c->pos;
+  p.rows = pg.num_blocks * pg.block_size;
+  p.sh = sh;
+  p.heads = h->heads;
+  const cudaError_t e = launch_append_ragged(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append launch (packed)");
+  return ok();
+}
+
 duo_status duo_kv_append_varlen(duo_handle* h, duo_kv_cache* c, int32_t* seq_lens, const void* k_new,
                                 const void* v_new, void* stream) {
   duo_status st = check_handle(h);
@@ -1230,7 +1385,7 @@ duo_status duo_device_error(uint32_t* code) {
   if (!code) return fail(DUO_ERR_INVALID_ARG, "code is NULL");
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, e8 = 0, bt = 0;
+  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, e8 = 0, bt = 0, ar = 0;
   if ((e = prefill_read_clear_error(&a)) != cudaSuccess) return cuda_fail(e, "read prefill error word");
   if ((e = decode_read_clear_error(&b)) != cudaSuccess) return cuda_fail(e, "read decode error word");
   if ((e = selftest_read_clear_error(&t)) != cudaSuccess) return cuda_fail(e, "read self-test error word");
@@ -1239,8 +1394,9 @@ duo_status duo_device_error(uint32_t* code) {
   if ((e = append_kv8_read_clear_error(&a8)) != cudaSuccess) return cuda_fail(e, "read 8-bit append error word");
   if ((e = block_tables_read_clear_error(&bt)) != cudaSuccess) return cuda_fail(e, "read block tables error word");
   if ((e = expand_kv8_read_clear_error(&e8)) != cudaSuccess) return cuda_fail(e, "read 8-bit expansion error word");
+  if ((e = append_ragged_read_clear_error(&ar)) != cudaSuccess) return cuda_fail(e, "read packed append error word");
   b |= d8 | e8;
-  ap |= a8;
+  ap |= a8 | ar;
   *code = a | b | t | ap | bt;
   constexpr uint32_t kFull = kErrAppendCapacity | kErrPoolFull, kBad = kErrBadBlock | kErrBadLength;
   if ((*code & kErrBadLength) && !(*code & ~(kFull | kBad)))
