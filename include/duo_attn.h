@@ -542,6 +542,36 @@ duo_status duo_kv_append_ragged(duo_handle* handle, duo_kv_cache* cache, const d
                                 const duo_rows* k_new, const duo_rows* v_new, const duo_rows* q,
                                 const duo_rows* q_out, void* stream);
 
+/* Attention of a packed batch of chunks over bf16 paged caches: sequence b's tokens are map->cu_new[b]
+ * ... map->cu_new[b + 1] - 1, at the positions from map->token_pos of the first one on, which is also how
+ * many tokens its caches hold (before these are appended). q, k, v [num_tokens, Hq or Hkv, D], rotated
+ * already; o bf16 [num_tokens, Hq, D], dense. What a query sees is as for duo_attn_prefill: its cached
+ * rows (retrieval heads through paged->block_table, streaming heads in cache->k_sr, v_sr, pos) and its
+ * own sequence's new tokens; any mixture of single tokens and long chunks may come in one call. A sequence
+ * whose first token is at position -1 is skipped, its rows of o and those of padding are left as they
+ * were. Scores, softmax and outputs are accumulated in fp32, p is rounded to bf16 before its product
+ * with v. Nothing behind a sequence's last row takes part, whatever it holds (other sequences, padding, rows
+ * of a block not written yet); within a sequence, an infinity or NaN in v reaches the 127 tokens before
+ * it as well. Rows of a block id outside [0, num_blocks) are left out and duo_device_error() reports
+ * DUO_ERR_INVALID_ARG; so it does where cu_new falls or passes num_tokens, or a position passes the tables'
+ * capacity: that sequence is skipped. paged->stream_table must be NULL.
+ * workspace: duo_prefill_ragged_workspace_size(handle, num_tokens) bytes of device memory, 256-byte aligned
+ * (parts of items that several CTAs share); nothing in it survives the call, and calls sharing it must be
+ * ordered on the GPU. o must not overlap q, k or v. */
+size_t duo_prefill_ragged_workspace_size(const duo_handle* handle, int32_t num_tokens);
+duo_status duo_attn_prefill_ragged(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
+                                   const duo_slot_map* map, int32_t num_tokens, const duo_rows* q, const duo_rows* k,
+                                   const duo_rows* v, void* o, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its form for one token a sequence, appended before (as duo_attn_decode): sequence b holds seq_lens[b]
+ * tokens (device int32 [B], clamped to [0, max_len], the new one included), its query is at position
+ * seq_lens[b] - 1, and a sequence of length 0 gets zeros. q, o: bf16 [B, Hq, D]. Bad block ids as above;
+ * a query all of whose blocks are bad gets zeros. workspace as for duo_attn_decode
+ * (duo_decode_workspace_size); o must not overlap q. */
+duo_status duo_attn_decode_paged_varlen(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
+                                        const int32_t* seq_lens, int64_t max_len, const void* q, void* o,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Dual Chunk Attention (vLLM pull request "[Model] Implement DualChunkAttention for
  * Qwen2 Models"): the sequence is cut into chunks of chunk_len positions from the start
  * (the last one may be shorter) and every position carries three query vectors made by

@@ -224,6 +224,42 @@ class DuoPagedLayer(DuoLayer):
                                   k_new, v_new, q, q_out, stream)
         return q_out
 
+    def prefill_ragged(self, q, k, v, slot_map, out=None, stream=None):
+        """Attention of a packed batch of chunks [num_tokens, heads, D]: each sequence's new tokens (a
+        DuoSlotMap) over its caches, as they were before, and over each other. Append the tokens
+        afterwards. q, k and v are rotated already, and may lie apart (slices of a fused projection).
+        Rows of ``out`` of tokens that the map turns down, and of padding, are not written."""
+        import torch
+        N = q.shape[0]
+        self._check_packed(slot_map, N, planes=False)
+        _packed_rows(self, "q", q, (N, self.Hq, self.D))
+        _packed_rows(self, "k", k, (N, self.Hkv, self.D))
+        _packed_rows(self, "v", v, (N, self.Hkv, self.D))
+        if out is None:
+            out = torch.empty((N, self.Hq, self.D), dtype=torch.bfloat16, device=q.device)
+        _on(self, "o", out, (N, self.Hq, self.D))
+        ws = _stream_workspace(_lib.duo_prefill_ragged_workspace_size(self.handle, N), q.device, stream)
+        _lib.duo_attn_prefill_ragged(self.handle, self.cache, self.paged, slot_map.c, N, q, k, v, out, ws, stream)
+        return out
+
+    def decode_varlen(self, q, seq_lens, max_len, out=None, stream=None):
+        """Decode where sequence b holds seq_lens[b] tokens, the new one included (device int32 [B], <=
+        max_len); a sequence of length 0 gets zeros."""
+        _on(self, "q", q, (self.B, self.Hq, self.D))
+        if out is None:
+            import torch
+            out = torch.empty_like(q)
+        _on(self, "o", out, (self.B, self.Hq, self.D))
+        _check_lens(seq_lens, self.B)
+        if seq_lens.get_device() != self.index:
+            raise ValueError(f"seq_lens: on {seq_lens.device}, the layer is on CUDA device {self.index}")
+        _lib.duo_attn_decode_paged_varlen(self.handle, self.cache, self.paged, seq_lens, max_len, q, out, self.workspace,
+                                          stream)
+        return out
+
+    def append_varlen(self, *args, **kwargs):
+        raise NotImplementedError("paged caches: append_ragged takes lengths from the device")
+
     def _check_packed(self, slot_map, N, planes):
         if slot_map.cu_new.get_device() != self.index:
             raise ValueError(f"slot_map: on {slot_map.cu_new.device}, the layer is on CUDA device {self.index}")
@@ -683,6 +719,16 @@ def _packed_rows(owner, name, t, shape):
             or (t.numel() and (t.stride(2) != 1 or t.stride(1) != shape[2] or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2])))):
         raise ValueError(f"{name}: need a bfloat16 tensor of shape {tuple(shape)} on CUDA device {owner.index} with each token's "
                          f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+
+
+def _stream_workspace(nbytes, device, stream):
+    """Workspace of one call on `stream` (None: the current one), from torch's allocator in that stream's
+    order: its memory may be given out again as soon as the call has returned."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_lib._stream_ptr(stream), device=device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _check_table(t, shape, index):

@@ -43,7 +43,8 @@ EXPORTS = (
     "duo_kv_append_kv8", "duo_kv_append_kv8_paged", "duo_kv_append_kv8_ragged", "duo_attn_decode_kv8",
     "duo_attn_decode_kv8_paged", "duo_attn_decode_kv8_varlen", "duo_attn_prefill_kv8",
     "duo_attn_prefill_kv8_paged", "duo_prefill_kv8_workspace_size", "duo_block_tables_workspace_size",
-    "duo_block_tables_update", "duo_rope_turns", "duo_rope_rotate", "duo_kv_append_ragged", "duo_kv_append_varlen",
+    "duo_block_tables_update", "duo_rope_turns", "duo_rope_rotate", "duo_kv_append_ragged",
+    "duo_prefill_ragged_workspace_size", "duo_attn_prefill_ragged", "duo_attn_decode_paged_varlen", "duo_kv_append_varlen",
     "duo_attn_decode_varlen", "duo_device_error", "duo_selftest_bounded_wait", "duo_last_error",
     "duo_status_string",
 )
@@ -179,6 +180,12 @@ def library() -> ctypes.CDLL:
         "duo_kv_append_ragged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), POINTER(duo_slot_map),
                                            c_int32, POINTER(duo_rope), POINTER(duo_rows), POINTER(duo_rows),
                                            POINTER(duo_rows), POINTER(duo_rows), c_void_p]),
+        "duo_prefill_ragged_workspace_size": (c_size_t, [c_void_p, c_int32]),
+        "duo_attn_prefill_ragged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), POINTER(duo_slot_map),
+                                              c_int32, POINTER(duo_rows), POINTER(duo_rows), POINTER(duo_rows), c_void_p,
+                                              c_void_p, c_size_t, c_void_p]),
+        "duo_attn_decode_paged_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), c_void_p, c_int64,
+                                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         "duo_kv_append_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_void_p, c_void_p,
                                            c_void_p]),
         "duo_attn_decode_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_int64, c_void_p, c_void_p,
@@ -480,6 +487,25 @@ def duo_kv_append_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot
     """A packed batch into bf16 paged caches, K (and q into q_out) rotated on the way with rope."""
     _check(library().duo_kv_append_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, _ref(rope),
                                           _rows(k_new), _rows(v_new), _rows(q), _rows(q_out), _stream_ptr(stream)))
+
+
+def duo_prefill_ragged_workspace_size(handle, num_tokens: int) -> int:
+    return int(library().duo_prefill_ragged_workspace_size(handle, num_tokens))
+
+
+def duo_attn_prefill_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot_map: "duo_slot_map",
+                            num_tokens: int, q, k, v, o, workspace, stream=None) -> None:
+    """Chunks of a packed batch over bf16 paged caches and their own tokens."""
+    _check(library().duo_attn_prefill_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, _rows(q),
+                                             _rows(k), _rows(v), _ptr(o), _ptr(workspace), _nbytes(workspace),
+                                             _stream_ptr(stream)))
+
+
+def duo_attn_decode_paged_varlen(handle, cache: "duo_kv_cache", paged: "duo_paged", seq_lens, max_len: int, q, o,
+                                 workspace, stream=None) -> None:
+    """Decode over bf16 paged caches with per-sequence lengths read on the device."""
+    _check(library().duo_attn_decode_paged_varlen(handle, _ref(cache), _ref(paged), _ptr(seq_lens), max_len, _ptr(q),
+                                                  _ptr(o), _ptr(workspace), _nbytes(workspace), _stream_ptr(stream)))
 
 
 def duo_kv_append_varlen(handle, cache: "duo_kv_cache", seq_lens, k_new, v_new, stream=None) -> None:

@@ -26,7 +26,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 LIBS = {
     os.path.join(PKG, "libduo_attn.so"): [os.path.join(CSRC, f) for f in
                                           ("duo_api.cu", "append.cu", "decode.cu", "prefill.cu", "selftest.cu", "append_kv8.cu",
-                                           "decode_kv8.cu", "expand_kv8.cu", "block_tables.cu", "append_ragged.cu")],
+                                           "decode_kv8.cu", "expand_kv8.cu", "block_tables.cu", "append_ragged.cu",
+                                           "attn_ragged.cu")],
     os.path.join(ROOT, "duo_synth", "libduo_synth.so"): [os.path.join(ROOT, "duo_synth", "csrc", "synth.cu")],
 }
 

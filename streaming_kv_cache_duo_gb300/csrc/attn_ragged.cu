@@ -1,0 +1,1125 @@
+// duo_attn_prefill_ragged and duo_attn_decode_paged_varlen: attention of a packed batch over bf16 paged
+// caches, every length read on the device.
+//
+// What it computes: sequence b's query at position i attends to the keys its caches hold and to the new
+// tokens of its own sequence, by the visibility rule of the library (retrieval j <= i; streaming also
+// j < S or i - j < R). Chunks: the caches as they were before the call, then the new tokens. Single
+// tokens: the caches alone, the query's token appended before.
+//
+// Items. Query rows are packed, row = token x g + head of a KV head, so that one token's g heads share
+// every K and V tile and a short chunk fills the rows of a tile. An item is up to 256 rows of one
+// (sequence, KV head), and what it reads is a list of 128-key tiles: of the cache, then of the new
+// tokens. All items' tiles are laid end to end on a line, retrieval items before streaming ones, with
+// room before each item for what it costs apart from its tiles, and CTA c of C (one an SM) takes the
+// tiles that begin in [c W / C, (c + 1) W / C). So a batch of one long and many short sequences is as
+// balanced as a uniform one, however long a context is. Nothing is planned on the host or by a kernel
+// before: where a sequence, a head and a block of queries begin on the line follows from the lengths in
+// closed form, so each CTA sums the sequences' lengths and finds its own first item. An item that
+// several CTAs share leaves parts (output, maximum, sum) that a second kernel merges; a CTA has at most
+// two: one that goes on with an item, one that begins one.
+//
+// One CTA, 12 warps (setmaxnreg moves registers from the third warpgroup to the two softmax ones):
+//   warp 11     walks the CTA's share of the line, and hands descriptors of its segments (an item's tiles
+//               or some of them) to the others through a ring of two
+//   warp 8      TMA producer: Q, then K and V tiles (128-byte swizzle) into rings of kNS stages, running
+//               ahead over segments' ends
+//   warp 9      one thread issues tcgen05.mma
+//   warp 10     zeroes rows of a V tile that no token of the sequence owns (below)
+//   warps 0-3, 4-7  softmax: thread r has query row r (TMEM lane r), with its running maximum and sum
+// Segments of more than 128 rows have two query tiles, one a softmax warpgroup, and every K/V tile serves
+// both: S0(j), S1(j), PV0(j), S0(j+1), PV1(j), S1(j+1), ... Shorter ones (decodes, short chunks) have
+// one query tile and the two warpgroups take the even and the odd key tiles, each with its own
+// output accumulator, so that one's softmax runs beside the other's products all the same; at the end the
+// warpgroups read both accumulators (same TMEM lanes), half of the dims each, and merge them. A decode
+// uses few of the 128 rows: a tile's products take 0.7 us of the tensor core, its 64 KB 1.5 us of an SM's
+// share of HBM, so wasted rows cost nothing that bounds it, and warps without rows do no softmax.
+//
+// What lies behind a sequence's last row in a tile (another sequence's tokens, padding, rows of a block
+// never written) may be anything. Scores there are masked by selection; for V, zero times an infinity or
+// NaN would not do, so the product stops after the 16 rows that hold the last one, and warp 10
+// writes zeros over what is left of those. A block id outside the pool: its rows are left out.
+#include "duo_device.cuh"
+#include "ragged_internal.h"
+
+namespace duo {
+namespace {
+
+__device__ unsigned int g_attn_ragged_err;
+
+constexpr int BM = 128;  // rows per query tile
+constexpr int BN = 128;  // keys per tile
+constexpr int kThreads = 384;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10, kWarpLine = 11;
+// 2 x 128 x 200 + 128 x 104 = 384 x 168 = 64512, the launch's registers
+constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
+constexpr int kSegs = 2;         // descriptors in flight
+constexpr int kSegUsers = 11;    // producer, MMA, tail, eight softmax warps
+
+// Places on the line: a retrieval tile's, a streaming one's (all of its tiles are masked), and an item's
+// own. A CTA's share has kLeast at least; an item of up to kShort tiles is not shared.
+constexpr int kPlaceR = 2, kPlaceS = 3, kPlaceItem = 6, kLeast = 6, kShort = 3;
+
+__host__ __device__ constexpr uint32_t col_s(int x) { return (uint32_t)x * 256u; }
+__host__ __device__ constexpr uint32_t col_o(int x) { return (uint32_t)x * 256u + 128u; }
+
+template <int D>
+struct Cfg {
+  static constexpr int NBOX = D / 64;
+  static constexpr int kNS = D == 64 ? 4 : 2;  // K/V stages
+  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int KV_BYTES = BN * D * 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + kNS * KV_BYTES;
+  static constexpr int OFF_ML = OFF_V + kNS * KV_BYTES;  // float2 [2][BM]
+  static constexpr int OFF_BAR = OFF_ML + 2 * BM * 8;
+  static constexpr size_t SMEM = (size_t)OFF_BAR + 1024 + 1024;  // + alignment slack
+};
+
+// What a segment is. Cache rows are [0, held) of the pool's plane or of the ring.
+struct Seg {
+  int last;       // no more segments
+  int b, tok0, T, n;  // sequence: its first token of the packed batch, new tokens, cached ones
+  int q0, rows;   // first token (of the sequence) and packed rows of the item
+  int kvh, cidx, streaming;
+  int j0, j1;     // tiles of the item
+  int held, n_cache, sink_eff, w_lo;
+  int part;       // place of its part, -1: the whole item
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t v_ask, v_fixed;  // a V tile with rows to zero has arrived; they are zero
+  uint64_t pair_ml[4], pair_done[4];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int stop;  // an earlier CTA gave up a wait
+  // the line: places of all items, and where this CTA's share begins
+  long long sums[2][kThreads / 32];
+  long long start_at;
+  int start_b;
+  Seg seg[kSegs];
+};
+static_assert(sizeof(Bars) <= 1024, "barrier area");
+
+// ---------------------------------------------------------------- the line
+struct Sequence {
+  int tok0, T, n;
+};
+
+// Sequence b; T = 0 where it has nothing to compute. report: note what cannot be.
+__device__ __forceinline__ Sequence sequence_at(const RaggedAttnParams& p, int b, bool report) {
+  Sequence s{0, 0, 0};
+  if (!p.cu_new) {
+    const int64_t len = p.seq_lens[b];
+    s.tok0 = b;
+    s.n = (int)(len < 0 ? 0 : (len > p.max_len ? p.max_len : len));
+    s.T = s.n > 0;
+    return s;
+  }
+  const int first = p.cu_new[b], end = p.cu_new[b + 1];
+  bool good = first >= 0 && end >= first;
+  if (good && (end == first || first >= p.tokens)) return s;  // (behind the batch: turned down)
+  if (good) {
+    const int pos = p.token_pos[first];
+    if (pos < 0) return s;  // turned down
+    const int64_t cap = (int64_t)p.pg.block_size * p.pg.max_blocks;
+    good = end <= p.tokens && end - first <= 0x7fffffff - pos && (p.sh.n_ret == 0 || pos <= cap);
+    if (good) s = Sequence{first, end - first, pos};
+  }
+  if (!good && report) atomicOr(&g_attn_ragged_err, kErrBadLength);
+  return s;
+}
+
+// Places of a head's items on the line, in the order of their tokens.
+struct HeadLine {
+  int blocks;  // items: blocks of `tb` tokens
+  int exact;   // the first of them, whose tiles are counted; the others are given `late` each
+  int cached;  // cache tiles of those
+  int late;
+  int place;
+  int T, log2_g;
+  bool chunks;
+  // sum over the first m blocks of the new-token tiles that block k sees, ceil(min(T, (k + 1) tb) / 128)
+  __device__ __forceinline__ int64_t new_tiles(int m) const {
+    if (!chunks || m == 0) return 0;
+    const int64_t f = m == blocks ? m - 1 : m;
+    int64_t sum;
+    if (log2_g == 0) {  // tb = 256
+      sum = f * (f + 1);
+    } else {  // 2^l blocks a tile
+      const int l = log2_g - 1;
+      const int64_t q = f >> l, rest = f & ((1 << l) - 1);
+      sum = ((q * (q + 1) / 2) << l) + rest * (q + 1);
+    }
+    return m == blocks ? sum + (T + BN - 1) / BN : sum;
+  }
+  __device__ __forceinline__ int64_t upto(int m) const {
+    const int e = min(m, exact);
+    return (int64_t)e * (kPlaceItem + (int64_t)place * cached) + place * new_tiles(e) +
+           (int64_t)(m - e) * (kPlaceItem + place * late);
+  }
+};
+
+__device__ __forceinline__ int tiles_of(int64_t rows) { return (int)((rows + BN - 1) / BN); }
+
+__device__ __forceinline__ HeadLine head_line(const RaggedAttnParams& p, const Sequence& s, bool streaming) {
+  HeadLine h;
+  const int tb = kRaggedRows >> p.log2_g;
+  h.chunks = p.cu_new != nullptr;
+  h.blocks = (int)(((int64_t)s.T + tb - 1) / tb);
+  h.T = s.T;
+  h.log2_g = p.log2_g;
+  h.exact = h.blocks;
+  h.late = 0;
+  if (!streaming) {
+    h.cached = tiles_of(s.n);
+    h.place = kPlaceR;
+  } else {
+    const int held = min(s.n, p.sh.S + p.sh.R);
+    h.cached = tiles_of(held);
+    h.place = kPlaceS;
+    if (h.chunks) {
+      // blocks whose first query sees more of the ring than the sinks
+      h.exact = min(h.blocks, (p.sh.R - 1 + tb - 1) / tb);
+      h.late = tiles_of(min(held, p.sh.S)) + (s.n < p.sh.S ? tiles_of(p.sh.S - s.n) : 0) + (p.sh.R + tb) / BN + 2;
+    }
+  }
+  return h;
+}
+
+// The tiles of block `blk` of a sequence and kind: cache tiles 0 ... n_cache - 1, then of the new tokens
+// [0, sink_eff) and [w_lo, ...].
+__device__ __forceinline__ int plan_item(const RaggedAttnParams& p, const Sequence& s, bool streaming, int blk, Seg* g) {
+  const int tb = kRaggedRows >> p.log2_g;
+  const int q0 = blk * tb;
+  const int tokens = min(tb, s.T - q0);
+  g->q0 = q0;
+  g->rows = tokens << p.log2_g;
+  g->held = streaming ? min(s.n, p.sh.S + p.sh.R) : s.n;
+  g->n_cache = tiles_of(g->held);
+  g->sink_eff = 0;
+  g->w_lo = 0;
+  if (!p.cu_new) return g->n_cache;
+  if (streaming) {
+    if (q0 + 1 >= p.sh.R) g->n_cache = tiles_of(min(p.sh.S, g->held));  // only sinks are still seen
+    const int first = q0 - p.sh.R + 1;
+    g->w_lo = first > 0 ? first / BN : 0;
+    const int sinks = p.sh.S > s.n ? tiles_of(p.sh.S - s.n) : 0;  // new tokens that are sinks
+    g->sink_eff = min(sinks, g->w_lo);
+  }
+  return g->n_cache + g->sink_eff + (q0 + tokens - 1) / BN - g->w_lo + 1;
+}
+
+// First place of CTA c of `ctas` on a line of W, and the CTA that place x belongs to.
+__device__ __forceinline__ int64_t bound(int64_t W, int ctas, int c) { return c * W / ctas; }
+__device__ __forceinline__ int owner(int64_t W, int ctas, int64_t x) { return (int)(((x + 1) * ctas + W - 1) / W) - 1; }
+
+struct Tile {
+  bool cache;
+  int k;      // tile of its source
+  int valid;  // rows of it that hold a token of the sequence
+};
+__device__ __forceinline__ Tile tile_at(const Seg& g, int j) {
+  Tile t;
+  t.cache = j < g.n_cache;
+  if (t.cache) {
+    t.k = j;
+    t.valid = min(BN, g.held - j * BN);
+  } else {
+    j -= g.n_cache;
+    t.k = j < g.sink_eff ? j : g.w_lo + (j - g.sink_eff);
+    t.valid = min(BN, g.T - t.k * BN);
+  }
+  return t;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bits_below(int hi) {
+  return hi <= 0 ? 0u : (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Which of the 32 keys of a chunk (columns c0 ... of tile t) row i_abs sees. Where they are consecutive
+// positions, the visible ones are at most two runs (sinks, and (i - R, i]): a 32-bit mask from a few
+// shifts. Ring slots: jp is the position slot c0 + lane holds, -1 if none; most are seen by all of the
+// warp's rows or by none (rows' positions rise with the lane), the few others are compared row by row.
+__device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg& g, const Tile& t, int c0, int i_abs,
+                                            int jp) {
+  const int S = p.sh.S, R = p.sh.R;
+  if (!t.cache) {
+    const int first = g.n + t.k * BN + c0;
+    const int d0 = i_abs - first;  // column e is the key d0 - e positions back
+    const uint32_t vis = bits_below(d0 + 1);
+    return g.streaming ? vis & (bits_below(S - first) | ~bits_below(d0 - R + 1)) : vis;
+  }
+  if (!g.streaming) return bits_below(t.valid - c0);
+  const int i0 = __shfl_sync(0xffffffffu, i_abs, 0), i1 = __shfl_sync(0xffffffffu, i_abs, 31);
+  const bool all = jp >= 0 && jp <= i0 && (jp < S || i1 - jp < R);
+  const bool none = jp < 0 || jp > i1 || (jp >= S && i0 - jp >= R);
+  uint32_t vis = __ballot_sync(0xffffffffu, all);
+  for (uint32_t some = __ballot_sync(0xffffffffu, !all && !none); some; some &= some - 1) {
+    const int e = __ffs((int)some) - 1;
+    const int j = __shfl_sync(0xffffffffu, jp, e);
+    vis |= (uint32_t)(j <= i_abs && (j < S || i_abs - j < R)) << e;
+  }
+  return vis;
+}
+
+// Reads the descriptors in order: next() waits for one, done() gives it back.
+struct SegReader {
+  Bars* bars;
+  int count = 0;
+  __device__ __forceinline__ explicit SegReader(Bars* b) : bars(b) {}
+  __device__ __forceinline__ const Seg& seg() const { return bars->seg[count % kSegs]; }
+  __device__ __forceinline__ uint64_t* full() const { return &bars->seg_full[count % kSegs]; }
+  __device__ __forceinline__ uint32_t parity() const { return (uint32_t)((count / kSegs) & 1); }
+  __device__ __forceinline__ void done() {  // by one lane
+    mbar_arrive(&bars->seg_empty[count % kSegs]);
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_constant__ RaggedAttnParams p) {
+  using C = Cfg<D>;
+  constexpr int kNS = C::kNS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  float2* sML = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+
+  const DevError err{&g_attn_ragged_err};
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 1);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 4);
+      mbar_init(&bars->o_final[s], 1);
+    }
+    for (int s = 0; s < kNS; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&bars->seg_full[s], 1);
+      mbar_init(&bars->seg_empty[s], kSegUsers);
+    }
+    for (int w = 0; w < 4; ++w) {
+      mbar_init(&bars->pair_ml[w], 2);
+      mbar_init(&bars->pair_done[w], 2);
+    }
+    mbar_init(&bars->v_ask, 1);
+    mbar_init(&bars->v_fixed, 1);
+    mbar_init(&bars->drain, 1);
+    fence_mbarrier_init();
+    // After any CTA gave up a wait, later ones do no work, so that a failure ends in about one wait limit.
+    // (Bad lengths and block ids, recorded in the same word, concern their sequences alone.)
+    bars->stop = (*(volatile unsigned int*)err.word & ~(kErrBadBlock | kErrBadLength)) != 0u;
+    bars->start_b = -1;
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  // the merge may be scheduled now; nothing that earlier grids write is read before they have ended
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---------------------------------------------------------------- this CTA's share of the line
+  const int B = p.sh.B;
+  long long mine[2] = {0, 0};  // places of this thread's sequences: retrieval, streaming
+  for (int b = threadIdx.x; b < B; b += kThreads) {
+    const Sequence s = sequence_at(p, b, blockIdx.x == 0);
+    if (s.T > 0) {
+      if (p.sh.n_ret > 0) mine[0] += p.sh.n_ret * head_line(p, s, false).upto(head_line(p, s, false).blocks);
+      if (p.sh.n_str > 0) mine[1] += p.sh.n_str * head_line(p, s, true).upto(head_line(p, s, true).blocks);
+    } else if (!p.cu_new && (int)(b % gridDim.x) == (int)blockIdx.x) {
+      // a sequence without a token: zeros
+      uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)b * p.sh.Hq * D);
+      for (int e = 0; e < p.sh.Hq * D / 8; ++e) o[e] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    long long v = mine[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) bars->sums[k][warp] = v;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  int64_t W_r = 0, W = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) W_r += bars->sums[0][w], W += bars->sums[1][w];
+  W += W_r;
+  const int ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, W / kLeast));
+  const int64_t lo = (int)blockIdx.x < ctas ? bound(W, ctas, blockIdx.x) : W;
+  const int64_t hi = (int)blockIdx.x < ctas ? bound(W, ctas, blockIdx.x + 1) : W;
+  const bool any = lo < hi && !bars->stop;
+  const int kind0 = lo < W_r ? 0 : 1;
+  if (any) {  // (the same for all threads) the sequence whose items of that kind hold place lo
+    const int64_t x = kind0 == 0 ? lo : lo - W_r;
+    long long before = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+      const int b = b0 + (int)threadIdx.x;
+      long long v = 0;
+      if (B <= kThreads) {
+        v = mine[kind0];
+      } else if (b < B) {
+        const Sequence s = sequence_at(p, b, false);
+        if (s.T > 0) {
+          const HeadLine h = head_line(p, s, kind0 == 1);
+          v = (kind0 == 0 ? p.sh.n_ret : p.sh.n_str) * h.upto(h.blocks);
+        }
+      }
+      long long upto = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      __syncthreads();  // sums have been read
+      if (lane == 31) bars->sums[0][warp] = upto;
+      __syncthreads();
+      long long all = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) upto += bars->sums[0][w];
+        all += bars->sums[0][w];
+      }
+      if (before + upto - v <= x && x < before + upto) {
+        bars->start_b = b;
+        bars->start_at = before + upto - v;
+      }
+      before += all;
+      if (before > x) break;  // (the same for all threads)
+    }
+  }
+  __syncthreads();
+
+  if (warp >= 8) {
+    // ================================================ warpgroup 2: TMA, MMA, tails, the line
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (warp == kWarpLine) {
+      // ------------------------------------------------------------ segments
+      int count = 0;
+      RaggedJob job{-1, 0, 0, 0};
+      bool ok = true;
+      if (any && bars->start_b >= 0) {
+        int kind = kind0, base = bars->start_b;
+        int64_t at = bars->start_at + (kind ? W_r : 0);  // where sequence base begins
+        int64_t cur = lo;
+        while (ok && cur < hi) {
+          // 32 sequences from base on
+          Sequence s{0, 0, 0};
+          long long v = 0;
+          if (base + lane < B) s = sequence_at(p, base + lane, false);
+          const int heads = kind ? p.sh.n_str : p.sh.n_ret;
+          if (s.T > 0 && heads > 0) {
+            const HeadLine h = head_line(p, s, kind == 1);
+            v = heads * h.upto(h.blocks);
+          }
+          for (int w = 0; w < 32 && ok && cur < hi; ++w) {
+            const Sequence q{__shfl_sync(0xffffffffu, s.tok0, w), __shfl_sync(0xffffffffu, s.T, w),
+                             __shfl_sync(0xffffffffu, s.n, w)};
+            const int64_t places = __shfl_sync(0xffffffffu, v, w);
+            if (places == 0) continue;
+            const HeadLine hl = head_line(p, q, kind == 1);
+            const int64_t per_head = hl.upto(hl.blocks);
+            while (cur < hi && cur < at + places) {
+              const int h = (int)((cur - at) / per_head);
+              const int64_t head_at = at + h * per_head, y = cur - head_at;
+              int blk = 0;  // the last one that begins at or before y
+              for (int top = hl.blocks; top - blk > 1;) {
+                const int mid = blk + (top - blk) / 2;
+                if (hl.upto(mid) <= y) blk = mid;
+                else top = mid;
+              }
+              const int64_t begin = head_at + hl.upto(blk), end = head_at + hl.upto(blk + 1);
+              Seg g;
+              g.last = 0;
+              g.b = base + w;
+              g.tok0 = q.tok0;
+              g.T = q.T;
+              g.n = q.n;
+              g.cidx = h;
+              g.streaming = kind;
+              g.kvh = kind ? p.heads.str_head[h] : p.heads.ret_head[h];
+              const int total = plan_item(p, q, kind == 1, blk, &g);
+              // tile j's place is begin + kPlaceItem + j place
+              const int64_t first = begin + kPlaceItem;
+              g.j0 = 0;
+              g.j1 = total;
+              if (total <= kShort) {
+                if (begin < lo) g.j1 = 0;  // the CTA's where it begins
+              } else {
+                const int64_t a = cur - first, e = min(hi, end) - first;
+                if (a > 0) g.j0 = (int)min((int64_t)total, (a + hl.place - 1) / hl.place);
+                if (hi < end) g.j1 = e > 0 ? (int)min((int64_t)total, (e + hl.place - 1) / hl.place) : 0;
+              }
+              cur = end;
+              if (g.j0 >= g.j1) continue;
+              g.part = -1;
+              if (g.j0 > 0) {
+                g.part = 2 * blockIdx.x;
+              } else if (g.j1 < total) {
+                g.part = 2 * blockIdx.x + 1;
+                job = RaggedJob{owner(W, ctas, first + (int64_t)(total - 1) * hl.place), g.tok0 + g.q0, g.rows,
+                                g.kvh << p.log2_g};
+              }
+              const int slot = count % kSegs;
+              if (!mbar_wait_warp(&bars->seg_empty[slot], (uint32_t)(((count / kSegs) & 1) ^ 1), err, kErrPrefillProducer)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                bars->seg[slot] = g;
+                mbar_arrive(&bars->seg_full[slot]);
+              }
+              ++count;
+            }
+            at += places;
+          }
+          base += 32;
+          if (base >= B) {  // on to the streaming items (they begin at W_r), or the end
+            if (kind == 1) break;
+            kind = 1;
+            base = 0;
+            at = W_r;
+          }
+        }
+      }
+      const int slot = count % kSegs;
+      if (ok && mbar_wait_warp(&bars->seg_empty[slot], (uint32_t)(((count / kSegs) & 1) ^ 1), err, kErrPrefillProducer) &&
+          lane == 0) {
+        bars->seg[slot].last = 1;
+        mbar_arrive(&bars->seg_full[slot]);
+      }
+      if (lane == 0) p.jobs[blockIdx.x] = job;
+    } else if (warp == kWarpTma) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        const uint64_t pol_again = l2_policy_evict_last(), pol_once = l2_policy_evict_first();
+        SegReader in(bars);
+        bool ok = true;
+        int jt = 0;                // tiles so far
+        int q_uses[2] = {0, 0};    // of each query tile's place
+        int slot = 0;              // the place of the next single query tile
+        while (ok) {
+          if (!mbar_wait(in.full(), in.parity(), err, kErrPrefillProducer)) {
+            ok = false;
+            break;
+          }
+          const Seg g = in.seg();
+          if (g.last) break;
+          const bool two = g.rows > BM;
+          // a sequence's other blocks of queries read the tiles again
+          const uint64_t pol_kv = (int64_t)g.T << p.log2_g > kRaggedRows ? pol_again : pol_once;
+          for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
+            const int s = two ? x : slot;
+            if (!mbar_wait(&bars->q_empty[s], (uint32_t)((q_uses[s] & 1) ^ 1), err, kErrPrefillProducer)) {
+              ok = false;
+              break;
+            }
+            ++q_uses[s];
+            const bool few = g.rows <= 8;
+            mbar_arrive_expect_tx(&bars->q_full[s], few ? C::NBOX * 1024 : C::Q_BYTES);
+#pragma unroll
+            for (int bx = 0; bx < C::NBOX; ++bx)
+              tma_load_3d(sQ + s * C::Q_BYTES + bx * kBox, few ? &p.tm_q8 : &p.tm_q, bx * 64, g.kvh << p.log2_g,
+                          g.tok0 + g.q0 + x * (BM >> p.log2_g), &bars->q_full[s]);
+          }
+          if (!two) slot ^= 1;
+          const int32_t* row = p.pg.table + ((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks;
+          const unsigned tpb = (unsigned)p.pg.block_size / BN;
+          const bool paged = !g.streaming;
+          int blk_next = paged && g.j0 < g.n_cache ? row[(unsigned)g.j0 / tpb] : 0;
+          for (int j = g.j0; j < g.j1 && ok; ++j, ++jt) {
+            const Tile t = tile_at(g, j);
+            int blk = blk_next, prow = 0;
+            if (paged && t.cache) {
+              prow = (int)((unsigned)t.k % tpb) * BN;
+              if (blk < 0 || blk >= p.pg.num_blocks) {
+                atomicOr(&g_attn_ragged_err, kErrBadBlock);
+                blk = (int)p.pg.num_blocks;  // out of range: zeros
+              }
+              if (j + 1 < g.n_cache && j + 1 < g.j1) blk_next = row[(unsigned)(t.k + 1) / tpb];
+            }
+            const int s = jt % kNS;
+            const uint32_t ph = (uint32_t)((jt / kNS) & 1);
+            auto load = [&](uint8_t* dst, uint64_t* bar, const CUtensorMap* fresh, const CUtensorMap* pool,
+                            const CUtensorMap* ring) {
+              mbar_arrive_expect_tx(bar, C::KV_BYTES);
+#pragma unroll
+              for (int bx = 0; bx < C::NBOX; ++bx) {
+                if (!t.cache)
+                  tma_load_3d_hint(dst + bx * kBox, fresh, bx * 64, g.kvh, g.tok0 + t.k * BN, bar, pol_kv);
+                else if (paged)
+                  tma_load_3d_hint(dst + bx * kBox, pool, bx * 64, prow, blk, bar, pol_kv);
+                else
+                  tma_load_3d_hint(dst + bx * kBox, ring, bx * 64, t.k * BN, g.b * p.sh.n_str + g.cidx, bar, pol_kv);
+              }
+            };
+            if (!mbar_wait(&bars->k_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
+              ok = false;
+              break;
+            }
+            load(sK + s * C::KV_BYTES, &bars->k_full[s], &p.tm_k, &p.tm_kpool, &p.tm_ksr);
+            if (!mbar_wait(&bars->v_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
+              ok = false;
+              mbar_wait(&bars->k_full[s], ph, err, kErrPrefillProducer);  // in flight
+              break;
+            }
+            load(sV + s * C::KV_BYTES, &bars->v_full[s], &p.tm_v, &p.tm_vpool, &p.tm_vsr);
+          }
+          in.done();
+          ++in.count;
+        }
+        if (!ok) {
+          // after an early exit, let the copies already issued land before the CTA ends
+          for (int s = 0; s < 2; ++s)
+            if (q_uses[s] > 0) mbar_wait(&bars->q_full[s], (uint32_t)((q_uses[s] - 1) & 1), err, kErrPrefillProducer);
+          for (int jj = (jt > kNS ? jt - kNS : 0); jj < jt; ++jj) {
+            mbar_wait(&bars->k_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
+            mbar_wait(&bars->v_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
+          }
+        }
+      }
+    } else if (warp == kWarpTail) {
+      // ------------------------------------------------------------ rows of V that no token owns
+      // (told of by the MMA thread, tile by tile: this warp does not follow the stages' phases itself)
+      SegReader in(bars);
+      int jt = 0, asked = 0;
+      bool ok = true;
+      while (ok) {
+        if (!mbar_wait_warp(in.full(), in.parity(), err, kErrPrefillProducer)) break;
+        const Seg g = in.seg();
+        if (g.last) break;
+        for (int j = g.j0; j < g.j1 && ok; ++j) {
+          const Tile t = tile_at(g, j);
+          const int odd = t.valid & 15;
+          if (odd == 0) continue;
+          const int jj = jt + (j - g.j0), s = jj % kNS;
+          if (!mbar_wait_warp(&bars->v_ask, (uint32_t)(asked++ & 1), err, kErrPrefillProducer)) {
+            ok = false;
+            break;
+          }
+          // (whole 128-byte rows of the boxes, so the swizzle does not matter)
+          uint8_t* v = sV + s * C::KV_BYTES + t.valid * 128;
+          for (int e = lane; e < (16 - odd) * 8 * C::NBOX; e += 32)
+            *reinterpret_cast<uint4*>(v + (e / ((16 - odd) * 8)) * kBox + e % ((16 - odd) * 8) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_shared();  // read by the tensor core next
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->v_fixed);
+        }
+        jt += g.j1 - g.j0;
+        __syncwarp();
+        if (lane == 0) in.done();
+        ++in.count;
+      }
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+        // (a k-step only moves the start address, in the descriptors' low bits)
+        const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), kBox, 1024);
+        // S_x = Q K(jt)^T, Q in place qs
+        auto issue_s = [&](int x, int qs, int jt) {
+          const uint64_t dq = dq0 + (uint64_t)((qs * C::Q_BYTES) >> 4);
+          const uint64_t dk = dk0 + (uint64_t)(((jt % kNS) * C::KV_BYTES) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t koff = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + col_s(x), dq + koff, dk + koff, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&bars->s_full[x]);
+        };
+        // O_x (+)= P_x V(jt) over the first `steps` groups of 16 keys
+        auto issue_pv = [&](int x, int jt, bool first, int steps) {
+          const uint64_t dv = dv0 + (uint64_t)(((jt % kNS) * C::KV_BYTES) >> 4);
+          if (steps == BN / 16) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                     (!first || kk > 0) ? 1u : 0u);
+          } else {
+            for (int kk = 0; kk < steps; ++kk)
+              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                     (!first || kk > 0) ? 1u : 0u);
+          }
+        };
+        SegReader in(bars);
+        int jt = 0, fixed = 0, slot = 0;
+        int q_uses[2] = {0, 0}, s_uses[2] = {0, 0};  // s_uses: p_full phases awaited
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, int uses) {
+          ok = ok && mbar_wait(bar, (uint32_t)(uses & 1), err, kErrPrefillMma);
+          return ok;
+        };
+        while (ok) {
+          if (!mbar_wait(in.full(), in.parity(), err, kErrPrefillMma)) break;
+          const Seg g = in.seg();
+          if (g.last) break;
+          const int nt = g.j1 - g.j0;
+          // V(t) is there, its rows without a token zeroed; the 16-key groups to multiply
+          auto v_ready = [&](int t) {
+            const int valid = tile_at(g, g.j0 + t).valid;
+            const int s = (jt + t) % kNS;
+            wait(&bars->v_full[s], (jt + t) / kNS);
+            if (valid & 15) {
+              if (ok) mbar_arrive(&bars->v_ask);
+              wait(&bars->v_fixed, fixed++);
+            }
+            return (valid + 15) >> 4;
+          };
+          if (g.rows > BM) {
+            // two query tiles, each K/V tile for both
+            wait(&bars->q_full[0], q_uses[0]++);
+            wait(&bars->q_full[1], q_uses[1]++);
+            if (!wait(&bars->k_full[jt % kNS], jt / kNS)) break;
+            tc_fence_after();
+            issue_s(0, 0, jt);
+            issue_s(1, 1, jt);
+            tc_commit(&bars->k_empty[jt % kNS]);
+            for (int t = 0; t < nt; ++t) {
+              const bool more = t + 1 < nt;
+              if (!more) {  // the scores are the last of Q
+                tc_commit(&bars->q_empty[0]);
+                tc_commit(&bars->q_empty[1]);
+              }
+              const int steps = v_ready(t);
+              if (more) wait(&bars->k_full[(jt + t + 1) % kNS], (jt + t + 1) / kNS);
+              if (!ok) break;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                if (!wait(&bars->p_full[x], s_uses[x]++)) break;
+                tc_fence_after();
+                issue_pv(x, jt + t, t == 0, steps);
+                if (more) issue_s(x, x, jt + t + 1);
+                else tc_commit(&bars->o_final[x]);
+              }
+              if (!ok) break;
+              tc_commit(&bars->v_empty[(jt + t) % kNS]);
+              if (more) tc_commit(&bars->k_empty[(jt + t + 1) % kNS]);
+            }
+            if (!ok) break;
+          } else {
+            // one query tile, even key tiles with S_0 and O_0, odd ones with S_1 and O_1
+            const int qs = slot;
+            slot ^= 1;
+            wait(&bars->q_full[qs], q_uses[qs]++);
+            for (int t = 0; t < 2 && t < nt; ++t) {
+              if (!wait(&bars->k_full[(jt + t) % kNS], (jt + t) / kNS)) break;
+              tc_fence_after();
+              issue_s(t, qs, jt + t);
+              tc_commit(&bars->k_empty[(jt + t) % kNS]);
+            }
+            if (nt <= 2) tc_commit(&bars->q_empty[qs]);
+            for (int t = 0; t < nt && ok; ++t) {
+              const int x = t & 1;
+              const int steps = v_ready(t);
+              if (!wait(&bars->p_full[x], s_uses[x]++)) break;
+              tc_fence_after();
+              issue_pv(x, jt + t, t < 2, steps);
+              tc_commit(&bars->v_empty[(jt + t) % kNS]);
+              if (t + 2 < nt) {
+                if (!wait(&bars->k_full[(jt + t + 2) % kNS], (jt + t + 2) / kNS)) break;
+                tc_fence_after();
+                issue_s(x, qs, jt + t + 2);
+                tc_commit(&bars->k_empty[(jt + t + 2) % kNS]);
+                if (t + 3 == nt) tc_commit(&bars->q_empty[qs]);
+              } else {
+                tc_commit(&bars->o_final[x]);
+              }
+            }
+            if (!ok) break;
+          }
+          jt += nt;
+          in.done();
+          ++in.count;
+        }
+        // every MMA this thread issued has finished before TMEM is released
+        tc_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, err, kErrPrefillMma);
+      }
+    }
+  } else {
+    // ================================================ warpgroups 0, 1: softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int x = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row within the query tile == TMEM lane
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t sbase = lane_base + col_s(x);
+    const uint32_t obase = lane_base + col_o(x);
+    const float sl2 = p.scale_log2;
+    SegReader in(bars);
+    // phases of the barriers waited for, a bit each (o_final[0] has one a segment)
+    uint32_t phase = 0;
+    constexpr uint32_t kPhS = 1, kPhO0 = 2, kPhO1 = 4, kPhPair = 8;
+    bool ok = true;
+    while (ok) {
+      if (!mbar_wait_warp(in.full(), in.parity(), err, kErrPrefillSoftmax)) break;
+      const Seg& g = in.seg();
+      if (g.last) break;
+      const bool two = g.rows > BM;
+      const int nt = g.j1 - g.j0;
+      const int step = two ? 1 : 2, t0 = two ? 0 : x;  // its tiles: t0, t0 + step, ...
+      const int row = two ? x * BM + r : r;            // of the item
+      const bool mine_any = row - lane < g.rows;       // (the same for the warp)
+      // token of the sequence, and absolute position; a row past the item takes the last one's
+      const int tok = g.q0 + (min(row, g.rows - 1) >> p.log2_g);
+      const int i_abs = p.cu_new ? g.n + tok : g.n - 1;
+      // first tile of the new tokens that some row of this query tile does not see whole
+      const int diag = (g.q0 + ((two ? x * BM : 0) >> p.log2_g)) / BN;
+      float m_run = -INFINITY, l_run = 0.f;
+      if (!mine_any) {
+        // no rows: what its rows of S hold goes for P, and their O is not read
+        for (int t = t0; t < nt && ok; t += step) {
+          ok = mbar_wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax);
+          phase ^= kPhS;
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&bars->p_full[x]);
+        }
+      } else {
+        for (int t = t0; t < nt; t += step) {
+          // masks first, while the scores are on their way
+          uint32_t vis[BN / 32] = {~0u, ~0u, ~0u, ~0u};
+          bool masked;
+          {
+            const Tile tl = tile_at(g, g.j0 + t);
+            masked = g.streaming || (tl.cache ? tl.valid < BN : tl.k >= diag);
+            if (tl.cache && !g.streaming) {
+              const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks +
+                                        (unsigned)tl.k / ((unsigned)p.pg.block_size / BN)];
+              if (masked) {
+#pragma unroll
+                for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = visible(p, g, tl, q4 * 32, i_abs, 0);
+              }
+              if (id < 0 || id >= p.pg.num_blocks) {  // a block that does not exist
+                masked = true;
+#pragma unroll
+                for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = 0u;
+              }
+            } else if (masked) {
+              const int32_t* held = p.pos + (int64_t)g.b * (p.sh.S + p.sh.R);
+              int jp[BN / 32];
+#pragma unroll
+              for (int q4 = 0; q4 < BN / 32; ++q4) {
+                const int s = tl.k * BN + q4 * 32 + lane;
+                jp[q4] = tl.cache && s < g.held ? held[s] : -1;
+              }
+#pragma unroll
+              for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = visible(p, g, tl, q4 * 32, i_abs, jp[q4]);
+            }
+            masked = __any_sync(0xffffffffu, (vis[0] & vis[1] & vis[2] & vis[3]) != ~0u);
+          }
+          if (!mbar_wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
+            ok = false;
+            break;
+          }
+          phase ^= kPhS;
+          tc_fence_after();
+          float v[BN];
+          {
+            uint32_t raw[BN];
+            tmem_ld128_sync(sbase, raw);
+#pragma unroll
+            for (int e = 0; e < BN; ++e) v[e] = __uint_as_float(raw[e]);
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < BN; ++e)
+              if (!((vis[e / 32] >> (e % 32)) & 1u)) v[e] = -INFINITY;
+          }
+          float mxa = v[0], mxb = v[1];
+#pragma unroll
+          for (int e = 2; e < BN; e += 4) {
+            mxa = max3(mxa, v[e], v[e + 1]);
+            if (e + 3 < BN) mxb = max3(mxb, v[e + 2], v[e + 3]);
+          }
+          const float mx_s = fmaxf(mxa, mxb) * sl2;
+          float f = 1.f;
+          if (mx_s > m_run + 8.f) {
+            f = ex2_approx(m_run - mx_s);  // 0 while nothing was visible
+            l_run *= f;
+            m_run = mx_s;
+          }
+          // O rescale (rare); the last P V of this accumulator is complete since this S is
+          if (__any_sync(0xffffffffu, f != 1.f && t > t0)) {
+#pragma unroll 1
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              uint32_t ov[32];
+              tmem_ld32_sync(obase + q4 * 32, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+              tmem_st32(obase + q4 * 32, ov);
+            }
+          }
+          // P = exp2(s scale - m), written over the first 64 columns of S
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          float2 ls = make_float2(0.f, 0.f);
+          const float2 sl2x2 = make_float2(sl2, sl2), negm2 = make_float2(-m_use, -m_use);
+#pragma unroll
+          for (int q4 = 0; q4 < BN / 32; ++q4) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = __ffma2_rn(make_float2(v[q4 * 32 + 2 * e], v[q4 * 32 + 2 * e + 1]), sl2x2, negm2);
+              const float p0 = ex2_approx(y.x);
+              const float p1 = ex2_approx(y.y);
+              ls = __fadd2_rn(ls, make_float2(p0, p1));
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(sbase + q4 * 16, pk);
+          }
+          l_run += ls.x + ls.y;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[x]);
+        }
+      }
+      // ---------------------------------------------------------------- the segment's end
+      const bool both = !two && nt > 1;  // two accumulators of the same rows
+      const int part = g.part;
+      if (ok && mine_any && (two || both || x == 0)) {
+        // weights of the accumulators, and the dims this warp reads: all of its own, or half of both
+        float f0 = 1.f, f1 = 0.f, m = m_run, l = l_run;
+        if (both) {
+          sML[x * BM + r] = make_float2(m_run, l_run);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->pair_ml[warp & 3]);
+          ok = mbar_wait_warp(&bars->pair_ml[warp & 3], (phase & kPhPair) != 0, err, kErrPrefillSoftmax) &&
+               mbar_wait_warp(&bars->o_final[0], (phase & kPhO0) != 0, err, kErrPrefillSoftmax) &&
+               mbar_wait_warp(&bars->o_final[1], (phase & kPhO1) != 0, err, kErrPrefillSoftmax);
+          if (ok) {
+            const float2 a = sML[r], b = sML[BM + r];
+            m = fmaxf(a.x, b.x);
+            f0 = a.x == -INFINITY ? 0.f : ex2_approx(a.x - m);
+            f1 = b.x == -INFINITY ? 0.f : ex2_approx(b.x - m);
+            l = f0 * a.y + f1 * b.y;
+          }
+        } else {
+          ok = mbar_wait_warp(&bars->o_final[x], (phase & (x ? kPhO1 : kPhO0)) != 0, err, kErrPrefillSoftmax);
+        }
+        if (ok) {
+          tc_fence_after();
+          const bool store = row < g.rows;
+          if (part < 0) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // (no key at all: zeros)
+            f0 *= inv;
+            f1 *= inv;
+          }
+          const int q_first = both ? x * (D / 64) : 0, q_end = both ? q_first + D / 64 : D / 32;
+          const int head = (g.kvh << p.log2_g) + (row & ((1 << p.log2_g) - 1));
+          uint16_t* orow = p.o + ((int64_t)(g.tok0 + tok) * p.sh.Hq + head) * D;
+          float4* prow = reinterpret_cast<float4*>(p.part_o + (int64_t)part * p.part_rows * D) + row;
+#pragma unroll 1
+          for (int q4 = q_first; q4 < q_end; ++q4) {
+            float ov[32];
+            {
+              uint32_t raw[32];
+              tmem_ld32_sync((both ? lane_base + col_o(0) : obase) + q4 * 32, raw);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __uint_as_float(raw[e]) * f0;
+              if (both) {
+                tmem_ld32_sync(lane_base + col_o(1) + q4 * 32, raw);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = fmaf(__uint_as_float(raw[e]), f1, ov[e]);
+              }
+            }
+            if (store && part >= 0) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                prow[(int64_t)(q4 * 8 + e) * p.part_rows] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+            } else if (store) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint4*>(orow + q4 * 32)[e] =
+                    make_uint4(pack_bf16x2(ov[8 * e], ov[8 * e + 1]), pack_bf16x2(ov[8 * e + 2], ov[8 * e + 3]),
+                               pack_bf16x2(ov[8 * e + 4], ov[8 * e + 5]), pack_bf16x2(ov[8 * e + 6], ov[8 * e + 7]));
+            }
+          }
+          if (store && part >= 0 && (!both || x == 0)) p.part_ml[(int64_t)part * p.part_rows + row] = make_float2(m, l);
+          if (both) {
+            // neither accumulator is written again before both warps have read it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->pair_done[warp & 3]);
+            ok = mbar_wait_warp(&bars->pair_done[warp & 3], (phase & kPhPair) != 0, err, kErrPrefillSoftmax);
+            phase ^= kPhPair;
+          }
+        }
+      }
+      phase ^= kPhO0;
+      if (two || both) phase ^= kPhO1;
+      __syncwarp();
+      if (lane == 0) in.done();
+      ++in.count;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// The parts of an item: O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s. A CTA takes 32 rows and 32 dims of
+// an item: a lane a row, a warp four dims; with fewer rows the lanes left over share the parts. Eight
+// parts are on their way at a time.
+template <int D>
+__global__ void __launch_bounds__(256) merge_ragged_kernel(const __grid_constant__ RaggedAttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int NB = 8;
+  const RaggedJob job = p.jobs[blockIdx.x];
+  const int r0 = (int)blockIdx.y / (D / 32) * 32;
+  if (job.last < 0 || r0 >= job.rows) return;
+  const int lane = threadIdx.x & 31, vec = (int)blockIdx.y % (D / 32) * 8 + (threadIdx.x >> 5);
+  int share = 1;  // lanes per row
+  while (share < 32 && job.rows * share * 2 <= 32) share *= 2;
+  const int width = 32 / share;
+  const int row = r0 + lane % width, first = lane / width;
+  const int parts = job.last - (int)blockIdx.x + 1;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, l = 0.f;
+  if (row < job.rows) {
+    for (int s0 = first; s0 < parts; s0 += NB * share) {
+      float2 ml[NB];
+      float4 o[NB];
+      float mn = M;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int s = s0 + k * share;
+        const int64_t at = s == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * (int64_t)(blockIdx.x + s);
+        ml[k] = make_float2(-INFINITY, 0.f);
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < parts) {
+          ml[k] = __ldcg(p.part_ml + at * p.part_rows + row);
+          o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * p.part_rows * D) + (int64_t)vec * p.part_rows + row);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) mn = fmaxf(mn, ml[k].x);
+      const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mn);
+      l *= keep;
+      acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const float f = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - mn);
+        l = fmaf(f, ml[k].y, l);
+        acc.x = fmaf(f, o[k].x, acc.x);
+        acc.y = fmaf(f, o[k].y, acc.y);
+        acc.z = fmaf(f, o[k].z, acc.z);
+        acc.w = fmaf(f, o[k].w, acc.w);
+      }
+      M = mn;
+    }
+  }
+  for (int o = width; o < 32; o *= 2) {
+    const float M2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+    const float x2 = __shfl_xor_sync(0xffffffffu, acc.x, o), y2 = __shfl_xor_sync(0xffffffffu, acc.y, o);
+    const float z2 = __shfl_xor_sync(0xffffffffu, acc.z, o), w2 = __shfl_xor_sync(0xffffffffu, acc.w, o);
+    const float mn = fmaxf(M, M2);
+    const float a = M == -INFINITY ? 0.f : ex2_approx(M - mn), b = M2 == -INFINITY ? 0.f : ex2_approx(M2 - mn);
+    M = mn;
+    l = a * l + b * l2;
+    acc = make_float4(a * acc.x + b * x2, a * acc.y + b * y2, a * acc.z + b * z2, a * acc.w + b * w2);
+  }
+  if (row < job.rows && first == 0) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = ((int64_t)(job.tok + (row >> p.log2_g)) * p.sh.Hq + job.head + (row & ((1 << p.log2_g) - 1))) * D;
+    reinterpret_cast<uint2*>(p.o + at)[vec] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const RaggedAttnParams& p, cudaStream_t stream) {
+  using C = Cfg<D>;
+  static_assert(C::SMEM <= 227 * 1024, "shared memory");
+  // (per device and thread-safe enough: setting it twice does no harm)
+  cudaError_t e = cudaFuncSetAttribute(attn_ragged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, attn_ragged_kernel<D>)) != cudaSuccess) return e;
+    regs = fa.numRegs;
+  }
+  // the setmaxnreg split is sized for exactly this launch allocation
+  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, attn_ragged_kernel<D>, p)) != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.part_rows + 31) / 32 * (D / 32)));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, merge_ragged_kernel<D>, p);
+}
+
+}  // namespace
+
+size_t ragged_workspace_bytes(int ctas, int rows, int D) {
+  return (size_t)2 * ctas * rows * (D * sizeof(float) + sizeof(float2)) + (size_t)ctas * sizeof(RaggedJob);
+}
+
+cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t stream) {
+  if (p.sh.D == 128) return launch_t<128>(p, stream);
+  if (p.sh.D == 64) return launch_t<64>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t attn_ragged_read_clear_error(uint32_t* code) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_ragged_err, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *code = v;
+  if (v) {
+    v = 0;
+    e = cudaMemcpyToSymbol(g_attn_ragged_err, &v, sizeof(v));
+  }
+  return e;
+}
+
+}  // namespace duo

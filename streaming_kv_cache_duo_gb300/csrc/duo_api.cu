@@ -1321,6 +1321,129 @@ duo_status duo_kv_append_ragged(duo_handle* h, duo_kv_cache* c, const duo_paged*
   return ok();
 }
 
+// 3-D map over rows [N, H, D] of a packed batch; box 64 x heads x tokens.
+static duo_status encode_rows(const duo_handle* h, CUtensorMap* map, const void* base, int64_t stride, int N, int H, int D,
+                              int heads, int tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)N};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DUO_ERR_CUDA, "cuTensorMapEncodeTiled (packed rows) failed: %d", (int)r);
+  return DUO_OK;
+}
+
+// Packed query rows of an item at most, of a batch of num_tokens.
+static int ragged_rows(const duo_handle* h, int32_t num_tokens) {
+  return (int)std::min<int64_t>(kRaggedRows, (int64_t)num_tokens * h->sh.g);
+}
+
+size_t duo_prefill_ragged_workspace_size(const duo_handle* h, int32_t num_tokens) {
+  return h && num_tokens > 0 ? ragged_workspace_bytes(h->num_sms, ragged_rows(h, num_tokens), h->sh.D) : 0;
+}
+
+// q, o: N tokens; map (chunks) or seq_lens (single tokens).
+static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const PagedLayout& pg, const duo_slot_map* map,
+                              const int32_t* seq_lens, int64_t max_len, int N, int rows, const duo_rows& q,
+                              const duo_rows* k, const duo_rows* v, void* o, void* workspace, void* stream) {
+  const Shape& sh = h->sh;
+  RaggedAttnParams p;
+  memset(&p, 0, sizeof(p));
+  duo_status st;
+  if ((st = encode_rows(h, &p.tm_q, q.data, q.stride, N, sh.Hq, sh.D, sh.g, kPrefillBM / sh.g)) != DUO_OK) return st;
+  if ((st = encode_rows(h, &p.tm_q8, q.data, q.stride, N, sh.Hq, sh.D, sh.g, 8 / sh.g)) != DUO_OK) return st;
+  if (map) {
+    if ((st = encode_rows(h, &p.tm_k, k->data, k->stride, N, sh.Hkv, sh.D, 1, kPrefillBN)) != DUO_OK) return st;
+    if ((st = encode_rows(h, &p.tm_v, v->data, v->stride, N, sh.Hkv, sh.D, 1, kPrefillBN)) != DUO_OK) return st;
+    p.cu_new = map->cu_new;
+    p.token_pos = map->token_pos;
+  }
+  if (sh.n_ret > 0) {
+    const int64_t bs = pg.block_size;
+    if ((st = encode_cache(h, &p.tm_kpool, c->k_full, pg.num_blocks, bs, bs, sh.D)) != DUO_OK) return st;
+    if ((st = encode_cache(h, &p.tm_vpool, c->v_full, pg.num_blocks, bs, bs, sh.D)) != DUO_OK) return st;
+  }
+  if (sh.n_str > 0) {
+    const int64_t SR = (int64_t)sh.S + sh.R, planes = (int64_t)sh.B * sh.n_str;
+    if ((st = encode_cache(h, &p.tm_ksr, c->k_sr, planes, SR, SR, sh.D)) != DUO_OK) return st;
+    if ((st = encode_cache(h, &p.tm_vsr, c->v_sr, planes, SR, SR, sh.D)) != DUO_OK) return st;
+  }
+  p.o = static_cast<uint16_t*>(o);
+  p.seq_lens = seq_lens;
+  p.max_len = max_len;
+  p.pos = c->pos;
+  p.tokens = N;
+  while ((1 << p.log2_g) < sh.g) ++p.log2_g;
+  p.ctas = h->num_sms;
+  p.part_rows = rows;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)sh.D));
+  const size_t parts = (size_t)2 * p.ctas * rows;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + parts * sh.D);
+  p.jobs = reinterpret_cast<RaggedJob*>(p.part_ml + parts);
+  p.sh = sh;
+  p.heads = h->heads;
+  p.pg = pg;
+  const cudaError_t e = launch_attn_ragged(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch (packed)");
+  return ok();
+}
+
+static duo_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(DUO_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  if (!workspace || bytes < need)
+    return fail(DUO_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? bytes : 0);
+  return DUO_OK;
+}
+
+duo_status duo_attn_prefill_ragged(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged, const duo_slot_map* map,
+                                   int32_t num_tokens, const duo_rows* q, const duo_rows* k, const duo_rows* v, void* o,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  duo_status st = check_handle(h);
+  if (st != DUO_OK) return st;
+  if (!map) return fail(DUO_ERR_INVALID_ARG, "map is NULL");
+  if (num_tokens < 0) return fail(DUO_ERR_INVALID_ARG, "num_tokens = %d < 0", num_tokens);
+  PagedLayout pg;
+  if ((st = check_ragged(h, c, paged, &pg)) != DUO_OK) return st;
+  if (num_tokens == 0) return ok();
+  const Shape& sh = h->sh;
+  if ((st = check_slot_map(map, false, false)) != DUO_OK) return st;
+  if ((st = check_rows(q, sh.Hq, sh.D, "q")) != DUO_OK) return st;
+  if ((st = check_rows(k, sh.Hkv, sh.D, "k")) != DUO_OK) return st;
+  if ((st = check_rows(v, sh.Hkv, sh.D, "v")) != DUO_OK) return st;
+  if (!o || !aligned16(o)) return fail(DUO_ERR_INVALID_ARG, "o NULL or not 16-byte aligned");
+  if ((st = check_workspace(workspace, ws_bytes, duo_prefill_ragged_workspace_size(h, num_tokens))) != DUO_OK) return st;
+  return attn_ragged(h, c, pg, map, nullptr, 0, num_tokens, ragged_rows(h, num_tokens), *q, k, v, o, workspace, stream);
+}
+
+duo_status duo_attn_decode_paged_varlen(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged,
+                                        const int32_t* seq_lens, int64_t max_len, const void* q, void* o, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  duo_status st = check_handle(h);
+  if (st != DUO_OK) return st;
+  if (!seq_lens || (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
+    return fail(DUO_ERR_INVALID_ARG, "seq_lens NULL or not 4-byte aligned");
+  if (max_len < 1 || max_len > 0x7fffffffLL)
+    return fail(DUO_ERR_INVALID_ARG, "max_len = %lld outside [1, 2^31)", (long long)max_len);
+  PagedLayout pg;
+  if ((st = check_ragged(h, c, paged, &pg)) != DUO_OK) return st;
+  const Shape& sh = h->sh;
+  if (sh.n_ret > 0 && (st = check_capacity(h, pg, max_len, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
+  if (!q || !o || !aligned16(q) || !aligned16(o))
+    return fail(DUO_ERR_INVALID_ARG, "q / o NULL or not 16-byte aligned");
+  // the size every decode entry point asks for; two parts per CTA and the jobs fit in it for every shape
+  const size_t need = decode_workspace_bytes(sh, h->num_sms * kDecodeCtasPerSmKv4);
+  if ((st = check_workspace(workspace, ws_bytes, need)) != DUO_OK) return st;
+  if (ragged_workspace_bytes(h->num_sms, sh.g, sh.D) > need)
+    return fail(DUO_ERR_WORKSPACE, "%zu bytes of workspace needed pass the %zu of a decode",
+                ragged_workspace_bytes(h->num_sms, sh.g, sh.D), need);
+  const duo_rows rows{const_cast<void*>(q), (int64_t)sh.Hq * sh.D};
+  return attn_ragged(h, c, pg, nullptr, seq_lens, max_len, sh.B, sh.g, rows, nullptr, nullptr, o, workspace, stream);
+}
+
 duo_status duo_kv_append_varlen(duo_handle* h, duo_kv_cache* c, int32_t* seq_lens, const void* k_new,
                                 const void* v_new, void* stream) {
   duo_status st = check_handle(h);
@@ -1385,7 +1508,7 @@ duo_status duo_device_error(uint32_t* code) {
   if (!code) return fail(DUO_ERR_INVALID_ARG, "code is NULL");
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, e8 = 0, bt = 0, ar = 0;
+  uint32_t a = 0, b = 0, t = 0, ap = 0, d8 = 0, a8 = 0, e8 = 0, bt = 0, ar = 0, at = 0;
   if ((e = prefill_read_clear_error(&a)) != cudaSuccess) return cuda_fail(e, "read prefill error word");
   if ((e = decode_read_clear_error(&b)) != cudaSuccess) return cuda_fail(e, "read decode error word");
   if ((e = selftest_read_clear_error(&t)) != cudaSuccess) return cuda_fail(e, "read self-test error word");
@@ -1395,7 +1518,9 @@ duo_status duo_device_error(uint32_t* code) {
   if ((e = block_tables_read_clear_error(&bt)) != cudaSuccess) return cuda_fail(e, "read block tables error word");
   if ((e = expand_kv8_read_clear_error(&e8)) != cudaSuccess) return cuda_fail(e, "read 8-bit expansion error word");
   if ((e = append_ragged_read_clear_error(&ar)) != cudaSuccess) return cuda_fail(e, "read packed append error word");
+  if ((e = attn_ragged_read_clear_error(&at)) != cudaSuccess) return cuda_fail(e, "read packed attention error word");
   b |= d8 | e8;
+  a |= at;
   ap |= a8 | ar;
   *code = a | b | t | ap | bt;
   constexpr uint32_t kFull = kErrAppendCapacity | kErrPoolFull, kBad = kErrBadBlock | kErrBadLength;

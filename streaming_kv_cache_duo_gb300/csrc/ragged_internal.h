@@ -51,4 +51,51 @@ cudaError_t launch_rope(const RopeAppendParams& p, cudaStream_t stream);
 cudaError_t launch_append_ragged(const RopeAppendParams& p, cudaStream_t stream);
 cudaError_t append_ragged_read_clear_error(uint32_t* code);
 
+// ------------------------------------------------------------------ attention
+constexpr int kRaggedRows = 256;  // packed query rows (token x head of a KV head) of an item at most
+
+// An item whose key tiles several CTAs share, noted by the CTA that begins it (last < 0: it begins none):
+// CTA `at` has the first part in its place 2 at + 1, CTAs at + 1 ... last the others in place 2 c.
+struct RaggedJob {
+  int last;
+  int tok;   // first token of the packed batch
+  int rows;  // packed query rows
+  int head;  // first query head
+};
+
+struct RaggedAttnParams {
+  CUtensorMap tm_q;      // 3-D over q [N, Hq, D], box 64 x g x 128 / g, 128B swizzle
+  CUtensorMap tm_q8;     // the same, box 64 x g x 8 / g: the tokens of up to 8 rows
+  CUtensorMap tm_k;      // 3-D over k [N, Hkv, D], box 64 x 1 x 128 (chunks only)
+  CUtensorMap tm_v;
+  CUtensorMap tm_kpool;  // 3-D over the pools [num_blocks, block_size, D], box 64 x 128 x 1
+  CUtensorMap tm_vpool;
+  CUtensorMap tm_ksr;    // 3-D over the rings [B n_str, S + R, D]
+  CUtensorMap tm_vsr;
+  uint16_t* o;           // bf16 [N, Hq, D]
+  // chunks: sequence b has tokens cu_new[b] ... cu_new[b + 1] - 1, the first one at position
+  // token_pos[cu_new[b]], which is also what its caches hold; single tokens (cu_new = nullptr): token b is
+  // the last of the seq_lens[b] (clamped to [0, max_len]) that its caches hold
+  const int32_t* cu_new;
+  const int32_t* token_pos;
+  const int32_t* seq_lens;
+  int64_t max_len;
+  const int32_t* pos;    // int32 [B, S+R]
+  int tokens;            // N
+  int log2_g;
+  int ctas;
+  int part_rows;         // rows a part has room for
+  float scale_log2;      // log2(e) / sqrt(D)
+  float* part_o;         // [2 ctas][D / 4][part_rows][4], unnormalised
+  float2* part_ml;       // [2 ctas][part_rows] (max, sum)
+  RaggedJob* jobs;       // [ctas]
+  Shape sh;
+  HeadTable heads;
+  PagedLayout pg;
+};
+// Bytes of parts and jobs for items of up to `rows` rows on `ctas` CTAs.
+size_t ragged_workspace_bytes(int ctas, int rows, int D);
+cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t stream);
+cudaError_t attn_ragged_read_clear_error(uint32_t* code);
+
 }  // namespace duo
