@@ -54,7 +54,7 @@ constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10, kWarpLine = 11;
 constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
-constexpr int kSegs = 2;         // descriptors in flight
+constexpr int kSegs = 4;         // descriptors in flight
 constexpr int kSegUsers = 11;    // producer, MMA, tail, eight softmax warps
 
 // Places on the line: a retrieval tile's, a streaming one's (all of its tiles are masked), and an item's
@@ -74,7 +74,8 @@ struct Cfg {
   static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_V = OFF_K + kNS * KV_BYTES;
   static constexpr int OFF_ML = OFF_V + kNS * KV_BYTES;  // float2 [2][BM]
-  static constexpr int OFF_BAR = OFF_ML + 2 * BM * 8;
+  static constexpr int OFF_VIS = OFF_ML + 2 * BM * 8;  // uint4 per softmax thread
+  static constexpr int OFF_BAR = OFF_VIS + 2 * BM * 16;
   static constexpr size_t SMEM = (size_t)OFF_BAR + 1024 + 1024;  // + alignment slack
 };
 
@@ -85,8 +86,12 @@ struct Seg {
   int q0, rows;   // first token (of the sequence) and packed rows of the item
   int kvh, cidx, streaming;
   int j0, j1;     // tiles of the item
-  int held, n_cache, sink_eff, w_lo;
+  int n_cache, sink_eff, w_lo;
+  // the tiles not all of whose rows hold a token of the sequence (-1: none): the last one of the cache and
+  // the last one of the new tokens, and the rows that do
+  int cut_cache, rows_cache, cut_new, rows_new;
   int part;       // place of its part, -1: the whole item
+  int bad;        // a block of its tiles does not exist (written later than the rest: seg_known)
 };
 
 struct Bars {
@@ -95,7 +100,7 @@ struct Bars {
   uint64_t s_full[2], p_full[2], o_final[2];
   uint64_t v_ask, v_fixed;  // a V tile with rows to zero has arrived; they are zero
   uint64_t pair_ml[4], pair_done[4];
-  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t seg_full[kSegs], seg_empty[kSegs], seg_known[kSegs];
   uint64_t drain;
   uint32_t tmem_base;
   int stop;  // an earlier CTA gave up a wait
@@ -159,6 +164,14 @@ struct HeadLine {
     }
     return m == blocks ? sum + (T + BN - 1) / BN : sum;
   }
+  // places of block m
+  __device__ __forceinline__ int64_t item(int m) const {
+    if (m >= exact) return kPlaceItem + place * late;
+    const int tb = kRaggedRows >> log2_g;
+    const int fresh = chunks ? (int)((min((int64_t)T, (int64_t)(m + 1) * tb) + BN - 1) / BN) : 0;
+    return kPlaceItem + (int64_t)place * (cached + fresh);
+  }
+  // and of the first m blocks
   __device__ __forceinline__ int64_t upto(int m) const {
     const int e = min(m, exact);
     return (int64_t)e * (kPlaceItem + (int64_t)place * cached) + place * new_tiles(e) +
@@ -201,42 +214,50 @@ __device__ __forceinline__ int plan_item(const RaggedAttnParams& p, const Sequen
   const int tokens = min(tb, s.T - q0);
   g->q0 = q0;
   g->rows = tokens << p.log2_g;
-  g->held = streaming ? min(s.n, p.sh.S + p.sh.R) : s.n;
-  g->n_cache = tiles_of(g->held);
+  const int held = streaming ? min(s.n, p.sh.S + p.sh.R) : s.n;
+  g->n_cache = tiles_of(held);
   g->sink_eff = 0;
   g->w_lo = 0;
+  g->cut_new = -1;
+  g->rows_new = BN;
+  if (p.cu_new && streaming && q0 + 1 >= p.sh.R) g->n_cache = tiles_of(min(p.sh.S, held));  // only sinks are still seen
+  g->rows_cache = min(BN, held - (g->n_cache - 1) * BN);
+  g->cut_cache = g->n_cache > 0 && g->rows_cache < BN ? g->n_cache - 1 : -1;
   if (!p.cu_new) return g->n_cache;
   if (streaming) {
-    if (q0 + 1 >= p.sh.R) g->n_cache = tiles_of(min(p.sh.S, g->held));  // only sinks are still seen
     const int first = q0 - p.sh.R + 1;
     g->w_lo = first > 0 ? first / BN : 0;
     const int sinks = p.sh.S > s.n ? tiles_of(p.sh.S - s.n) : 0;  // new tokens that are sinks
     g->sink_eff = min(sinks, g->w_lo);
   }
-  return g->n_cache + g->sink_eff + (q0 + tokens - 1) / BN - g->w_lo + 1;
+  const int last = (q0 + tokens - 1) / BN;
+  const int total = g->n_cache + g->sink_eff + last - g->w_lo + 1;
+  if ((int64_t)(last + 1) * BN > s.T) {
+    g->cut_new = total - 1;
+    g->rows_new = s.T - last * BN;
+  }
+  return total;
 }
 
 // First place of CTA c of `ctas` on a line of W, and the CTA that place x belongs to.
 __device__ __forceinline__ int64_t bound(int64_t W, int ctas, int c) { return c * W / ctas; }
 __device__ __forceinline__ int owner(int64_t W, int ctas, int64_t x) { return (int)(((x + 1) * ctas + W - 1) / W) - 1; }
 
+// Tile j of an item: of the cache or of the new tokens, and which one of these.
 struct Tile {
   bool cache;
-  int k;      // tile of its source
-  int valid;  // rows of it that hold a token of the sequence
+  int k;
 };
 __device__ __forceinline__ Tile tile_at(const Seg& g, int j) {
   Tile t;
   t.cache = j < g.n_cache;
-  if (t.cache) {
-    t.k = j;
-    t.valid = min(BN, g.held - j * BN);
-  } else {
-    j -= g.n_cache;
-    t.k = j < g.sink_eff ? j : g.w_lo + (j - g.sink_eff);
-    t.valid = min(BN, g.T - t.k * BN);
-  }
+  j -= t.cache ? 0 : g.n_cache;
+  t.k = t.cache || j < g.sink_eff ? j : g.w_lo + (j - g.sink_eff);
   return t;
+}
+// Rows of it that hold a token of the sequence.
+__device__ __forceinline__ int rows_of(const Seg& g, int j) {
+  return j == g.cut_cache ? g.rows_cache : (j == g.cut_new ? g.rows_new : BN);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -260,8 +281,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 // positions, the visible ones are at most two runs (sinks, and (i - R, i]): a 32-bit mask from a few
 // shifts. Ring slots: jp is the position slot c0 + lane holds, -1 if none; most are seen by all of the
 // warp's rows or by none (rows' positions rise with the lane), the few others are compared row by row.
-__device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg& g, const Tile& t, int c0, int i_abs,
-                                            int jp) {
+__device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg& g, const Tile& t, int rows, int c0,
+                                            int i_abs, int jp) {
   const int S = p.sh.S, R = p.sh.R;
   if (!t.cache) {
     const int first = g.n + t.k * BN + c0;
@@ -269,7 +290,7 @@ __device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg
     const uint32_t vis = bits_below(d0 + 1);
     return g.streaming ? vis & (bits_below(S - first) | ~bits_below(d0 - R + 1)) : vis;
   }
-  if (!g.streaming) return bits_below(t.valid - c0);
+  if (!g.streaming) return bits_below(rows - c0);
   const int i0 = __shfl_sync(0xffffffffu, i_abs, 0), i1 = __shfl_sync(0xffffffffu, i_abs, 31);
   const bool all = jp >= 0 && jp <= i0 && (jp < S || i1 - jp < R);
   const bool none = jp < 0 || jp > i1 || (jp >= S && i0 - jp >= R);
@@ -282,6 +303,11 @@ __device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg
   return vis;
 }
 
+// Position of packed row `row` of a segment's item; a row past the item takes the last one's.
+__device__ __forceinline__ int position(const RaggedAttnParams& p, const Seg& g, int row) {
+  return p.cu_new ? g.n + g.q0 + (min(row, g.rows - 1) >> p.log2_g) : g.n - 1;
+}
+
 // Reads the descriptors in order: next() waits for one, done() gives it back.
 struct SegReader {
   Bars* bars;
@@ -289,6 +315,7 @@ struct SegReader {
   __device__ __forceinline__ explicit SegReader(Bars* b) : bars(b) {}
   __device__ __forceinline__ const Seg& seg() const { return bars->seg[count % kSegs]; }
   __device__ __forceinline__ uint64_t* full() const { return &bars->seg_full[count % kSegs]; }
+  __device__ __forceinline__ uint64_t* known() const { return &bars->seg_known[count % kSegs]; }
   __device__ __forceinline__ uint32_t parity() const { return (uint32_t)((count / kSegs) & 1); }
   __device__ __forceinline__ void done() {  // by one lane
     mbar_arrive(&bars->seg_empty[count % kSegs]);
@@ -305,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   uint8_t* sK = smem + C::OFF_K;
   uint8_t* sV = smem + C::OFF_V;
   float2* sML = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  uint4* sVis = reinterpret_cast<uint4*>(smem + C::OFF_VIS);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
 
   const DevError err{&g_attn_ragged_err};
@@ -328,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&bars->seg_full[s], 1);
       mbar_init(&bars->seg_empty[s], kSegUsers);
+      mbar_init(&bars->seg_known[s], 1);
     }
     for (int w = 0; w < 4; ++w) {
       mbar_init(&bars->pair_ml[w], 2);
@@ -374,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
   int64_t W_r = 0, W = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) W_r += bars->sums[0][w], W += bars->sums[1][w];
@@ -453,16 +481,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             if (places == 0) continue;
             const HeadLine hl = head_line(p, q, kind == 1);
             const int64_t per_head = hl.upto(hl.blocks);
-            while (cur < hi && cur < at + places) {
-              const int h = (int)((cur - at) / per_head);
-              const int64_t head_at = at + h * per_head, y = cur - head_at;
-              int blk = 0;  // the last one that begins at or before y
+            if (cur >= at + places) {
+              at += places;
+              continue;
+            }
+            // its first item that ends behind cur (the first one of all, but where the share begins)
+            int h = 0, blk = 0;
+            int64_t begin = at;
+            if (cur > at) {
+              h = (int)((cur - at) / per_head);
+              begin += h * per_head;
+              const int64_t y = cur - begin;
               for (int top = hl.blocks; top - blk > 1;) {
                 const int mid = blk + (top - blk) / 2;
                 if (hl.upto(mid) <= y) blk = mid;
                 else top = mid;
               }
-              const int64_t begin = head_at + hl.upto(blk), end = head_at + hl.upto(blk + 1);
+              begin += hl.upto(blk);
+            }
+            for (; h < heads && cur < hi; blk = blk + 1 < hl.blocks ? blk + 1 : 0, h += blk == 0) {
+              const int64_t end = begin + hl.item(blk);
               Seg g;
               g.last = 0;
               g.b = base + w;
@@ -474,17 +512,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               g.kvh = kind ? p.heads.str_head[h] : p.heads.ret_head[h];
               const int total = plan_item(p, q, kind == 1, blk, &g);
               // tile j's place is begin + kPlaceItem + j place
-              const int64_t first = begin + kPlaceItem;
+              const int64_t first = begin + kPlaceItem, from = begin;
               g.j0 = 0;
               g.j1 = total;
               if (total <= kShort) {
-                if (begin < lo) g.j1 = 0;  // the CTA's where it begins
+                if (from < lo) g.j1 = 0;  // the CTA's where it begins
               } else {
                 const int64_t a = cur - first, e = min(hi, end) - first;
                 if (a > 0) g.j0 = (int)min((int64_t)total, (a + hl.place - 1) / hl.place);
                 if (hi < end) g.j1 = e > 0 ? (int)min((int64_t)total, (e + hl.place - 1) / hl.place) : 0;
               }
-              cur = end;
+              cur = begin = end;
               if (g.j0 >= g.j1) continue;
               g.part = -1;
               if (g.j0 > 0) {
@@ -502,6 +540,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               if (lane == 0) {
                 bars->seg[slot] = g;
                 mbar_arrive(&bars->seg_full[slot]);
+              }
+              // while Q and the first tiles are on their way: do all of its blocks exist?
+              bool bad = false;
+              if (kind == 0 && g.j0 < g.n_cache) {
+                const int32_t* row = p.pg.table + ((int64_t)g.b * p.sh.n_ret + h) * p.pg.max_blocks;
+                const int tpb = p.pg.block_size / BN, end_blk = (min(g.j1, g.n_cache) - 1) / tpb;
+                for (int i = g.j0 / tpb + lane; i <= end_blk; i += 32) {
+                  const int id = row[i];
+                  bad |= id < 0 || id >= p.pg.num_blocks;
+                }
+              }
+              bad = __any_sync(0xffffffffu, bad);
+              if (lane == 0) {
+                if (bad) atomicOr(&g_attn_ragged_err, kErrBadBlock);
+                bars->seg[slot].bad = bad;
+                mbar_arrive(&bars->seg_known[slot]);
               }
               ++count;
             }
@@ -530,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         SegReader in(bars);
         bool ok = true;
         int jt = 0;                // tiles so far
-        int q_uses[2] = {0, 0};    // of each query tile's place
-        int slot = 0;              // the place of the next single query tile
+        uint32_t used = 0, qp = 3;  // places of query tiles: used at all, and the phases of q_empty (a bit each)
+        int slot = 0;               // the place of the next single query tile
         while (ok) {
           if (!mbar_wait(in.full(), in.parity(), err, kErrPrefillProducer)) {
             ok = false;
@@ -544,11 +598,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           const uint64_t pol_kv = (int64_t)g.T << p.log2_g > kRaggedRows ? pol_again : pol_once;
           for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
             const int s = two ? x : slot;
-            if (!mbar_wait(&bars->q_empty[s], (uint32_t)((q_uses[s] & 1) ^ 1), err, kErrPrefillProducer)) {
+            if (!mbar_wait(&bars->q_empty[s], (qp >> s) & 1u, err, kErrPrefillProducer)) {
               ok = false;
               break;
             }
-            ++q_uses[s];
+            qp ^= 1u << s;
+            used |= 1u << s;
             const bool few = g.rows <= 8;
             mbar_arrive_expect_tx(&bars->q_full[s], few ? C::NBOX * 1024 : C::Q_BYTES);
 #pragma unroll
@@ -566,10 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             int blk = blk_next, prow = 0;
             if (paged && t.cache) {
               prow = (int)((unsigned)t.k % tpb) * BN;
-              if (blk < 0 || blk >= p.pg.num_blocks) {
-                atomicOr(&g_attn_ragged_err, kErrBadBlock);
-                blk = (int)p.pg.num_blocks;  // out of range: zeros
-              }
+              if (blk < 0 || blk >= p.pg.num_blocks) blk = (int)p.pg.num_blocks;  // out of range: zeros
               if (j + 1 < g.n_cache && j + 1 < g.j1) blk_next = row[(unsigned)(t.k + 1) / tpb];
             }
             const int s = jt % kNS;
@@ -605,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         if (!ok) {
           // after an early exit, let the copies already issued land before the CTA ends
           for (int s = 0; s < 2; ++s)
-            if (q_uses[s] > 0) mbar_wait(&bars->q_full[s], (uint32_t)((q_uses[s] - 1) & 1), err, kErrPrefillProducer);
+            if ((used >> s) & 1u) mbar_wait(&bars->q_full[s], (qp >> s) & 1u, err, kErrPrefillProducer);
           for (int jj = (jt > kNS ? jt - kNS : 0); jj < jt; ++jj) {
             mbar_wait(&bars->k_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
             mbar_wait(&bars->v_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
@@ -623,8 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         const Seg g = in.seg();
         if (g.last) break;
         for (int j = g.j0; j < g.j1 && ok; ++j) {
-          const Tile t = tile_at(g, j);
-          const int odd = t.valid & 15;
+          const int rows = rows_of(g, j), odd = rows & 15;
           if (odd == 0) continue;
           const int jj = jt + (j - g.j0), s = jj % kNS;
           if (!mbar_wait_warp(&bars->v_ask, (uint32_t)(asked++ & 1), err, kErrPrefillProducer)) {
@@ -632,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             break;
           }
           // (whole 128-byte rows of the boxes, so the swizzle does not matter)
-          uint8_t* v = sV + s * C::KV_BYTES + t.valid * 128;
+          uint8_t* v = sV + s * C::KV_BYTES + rows * 128;
           for (int e = lane; e < (16 - odd) * 8 * C::NBOX; e += 32)
             *reinterpret_cast<uint4*>(v + (e / ((16 - odd) * 8)) * kBox + e % ((16 - odd) * 8) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_shared();  // read by the tensor core next
@@ -649,14 +700,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       if (lane == 0) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-        // (a k-step only moves the start address, in the descriptors' low bits)
+        // (a k-step only moves the start address, in the descriptors' low bits. Each role reads the TMEM
+        // address for itself: kept since the start it was spilled, and loaded again for every product)
+        const uint32_t tmem = *(volatile uint32_t*)&bars->tmem_base;
         const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), kBox, 1024);
-        // S_x = Q K(jt)^T, Q in place qs
-        auto issue_s = [&](int x, int qs, int jt) {
+        // S_x = Q K^T, Q in place qs, K in stage s
+        auto issue_s = [&](int x, int qs, int s) {
           const uint64_t dq = dq0 + (uint64_t)((qs * C::Q_BYTES) >> 4);
-          const uint64_t dk = dk0 + (uint64_t)(((jt % kNS) * C::KV_BYTES) >> 4);
+          const uint64_t dk = dk0 + (uint64_t)((s * C::KV_BYTES) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t koff = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
@@ -664,109 +717,122 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           }
           tc_commit(&bars->s_full[x]);
         };
-        // O_x (+)= P_x V(jt) over the first `steps` groups of 16 keys
-        auto issue_pv = [&](int x, int jt, bool first, int steps) {
-          const uint64_t dv = dv0 + (uint64_t)(((jt % kNS) * C::KV_BYTES) >> 4);
-          if (steps == BN / 16) {
+        // O_x (+)= P_x V, V in stage s, over the first `rows` keys (in groups of 16)
+        auto issue_pv = [&](int x, int s, bool first, int rows) {
+          const uint64_t dv = dv0 + (uint64_t)((s * C::KV_BYTES) >> 4);
+          if (rows == BN) {
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
               mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
                      (!first || kk > 0) ? 1u : 0u);
           } else {
-            for (int kk = 0; kk < steps; ++kk)
+#pragma unroll 1
+            for (int kk = 0; kk < (rows + 15) >> 4; ++kk)
               mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
                      (!first || kk > 0) ? 1u : 0u);
           }
         };
         SegReader in(bars);
-        int jt = 0, fixed = 0, slot = 0;
-        int q_uses[2] = {0, 0}, s_uses[2] = {0, 0};  // s_uses: p_full phases awaited
+        int jt = 0;                        // tiles so far: tile jt is in stage jt % kNS
+        uint32_t pp = 0, qp = 0, fp = 0;   // phases: of p_full and q_full (a bit each), of v_fixed
+        int slot = 0;
         bool ok = true;
-        auto wait = [&](uint64_t* bar, int uses) {
-          ok = ok && mbar_wait(bar, (uint32_t)(uses & 1), err, kErrPrefillMma);
-          return ok;
-        };
         while (ok) {
-          if (!mbar_wait(in.full(), in.parity(), err, kErrPrefillMma)) break;
-          const Seg g = in.seg();
-          if (g.last) break;
-          const int nt = g.j1 - g.j0;
-          // V(t) is there, its rows without a token zeroed; the 16-key groups to multiply
-          auto v_ready = [&](int t) {
-            const int valid = tile_at(g, g.j0 + t).valid;
-            const int s = (jt + t) % kNS;
-            wait(&bars->v_full[s], (jt + t) / kNS);
-            if (valid & 15) {
-              if (ok) mbar_arrive(&bars->v_ask);
-              wait(&bars->v_fixed, fixed++);
-            }
-            return (valid + 15) >> 4;
+          if (!(ok = mbar_wait(in.full(), in.parity(), err, kErrPrefillMma))) break;
+          int nt, rows, cut_c, cut_n, rows_c, rows_n;
+          {
+            const Seg& g = in.seg();
+            if (g.last) break;
+            nt = g.j1 - g.j0;
+            rows = g.rows;
+            cut_c = g.cut_cache - g.j0;
+            cut_n = g.cut_new - g.j0;
+            rows_c = g.rows_cache;
+            rows_n = g.rows_new;
+          }
+          in.done();
+          ++in.count;
+          auto k_ready = [&](int j) {
+            return mbar_wait(&bars->k_full[j % kNS], (uint32_t)((j / kNS) & 1), err, kErrPrefillMma);
           };
-          if (g.rows > BM) {
+          // the tile's V has arrived, and those of its rows without a token that would be multiplied are
+          // zero; the rows to multiply (0: a wait ran out)
+          auto v_ready = [&](int t, int j) {
+            if (!mbar_wait(&bars->v_full[j % kNS], (uint32_t)((j / kNS) & 1), err, kErrPrefillMma)) return 0;
+            if (t != cut_c && t != cut_n) return BN;
+            const int r = t == cut_c ? rows_c : rows_n;
+            if ((r & 15) == 0) return r;
+            mbar_arrive(&bars->v_ask);
+            fp ^= 1u;
+            return mbar_wait(&bars->v_fixed, fp ^ 1u, err, kErrPrefillMma) ? r : 0;
+          };
+          if (rows > BM) {
             // two query tiles, each K/V tile for both
-            wait(&bars->q_full[0], q_uses[0]++);
-            wait(&bars->q_full[1], q_uses[1]++);
-            if (!wait(&bars->k_full[jt % kNS], jt / kNS)) break;
+            ok = mbar_wait(&bars->q_full[0], qp & 1u, err, kErrPrefillMma) &&
+                 mbar_wait(&bars->q_full[1], (qp >> 1) & 1u, err, kErrPrefillMma) && k_ready(jt);
+            qp ^= 3u;
+            if (!ok) break;
             tc_fence_after();
-            issue_s(0, 0, jt);
-            issue_s(1, 1, jt);
+            issue_s(0, 0, jt % kNS);
+            issue_s(1, 1, jt % kNS);
             tc_commit(&bars->k_empty[jt % kNS]);
-            for (int t = 0; t < nt; ++t) {
+            for (int t = 0; t < nt; ++t, ++jt) {
               const bool more = t + 1 < nt;
               if (!more) {  // the scores are the last of Q
                 tc_commit(&bars->q_empty[0]);
                 tc_commit(&bars->q_empty[1]);
               }
-              const int steps = v_ready(t);
-              if (more) wait(&bars->k_full[(jt + t + 1) % kNS], (jt + t + 1) / kNS);
-              if (!ok) break;
+              const int v_rows = v_ready(t, jt);
+              if (v_rows == 0 || (more && !k_ready(jt + 1))) {
+                ok = false;
+                break;
+              }
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                if (!wait(&bars->p_full[x], s_uses[x]++)) break;
+                if (!ok || !(ok = mbar_wait(&bars->p_full[x], (pp >> x) & 1u, err, kErrPrefillMma))) break;
                 tc_fence_after();
-                issue_pv(x, jt + t, t == 0, steps);
-                if (more) issue_s(x, x, jt + t + 1);
+                issue_pv(x, jt % kNS, t == 0, v_rows);
+                if (more) issue_s(x, x, (jt + 1) % kNS);
                 else tc_commit(&bars->o_final[x]);
               }
               if (!ok) break;
-              tc_commit(&bars->v_empty[(jt + t) % kNS]);
-              if (more) tc_commit(&bars->k_empty[(jt + t + 1) % kNS]);
+              pp ^= 3u;
+              tc_commit(&bars->v_empty[jt % kNS]);
+              if (more) tc_commit(&bars->k_empty[(jt + 1) % kNS]);
             }
-            if (!ok) break;
           } else {
             // one query tile, even key tiles with S_0 and O_0, odd ones with S_1 and O_1
             const int qs = slot;
             slot ^= 1;
-            wait(&bars->q_full[qs], q_uses[qs]++);
-            for (int t = 0; t < 2 && t < nt; ++t) {
-              if (!wait(&bars->k_full[(jt + t) % kNS], (jt + t) / kNS)) break;
+            ok = mbar_wait(&bars->q_full[qs], (qp >> qs) & 1u, err, kErrPrefillMma);
+            qp ^= 1u << qs;
+            for (int t = 0; t < 2 && t < nt && ok; ++t) {
+              if (!(ok = k_ready(jt + t))) break;
               tc_fence_after();
-              issue_s(t, qs, jt + t);
+              issue_s(t, qs, (jt + t) % kNS);
               tc_commit(&bars->k_empty[(jt + t) % kNS]);
             }
+            if (!ok) break;
             if (nt <= 2) tc_commit(&bars->q_empty[qs]);
-            for (int t = 0; t < nt && ok; ++t) {
+            for (int t = 0; t < nt; ++t, ++jt) {
               const int x = t & 1;
-              const int steps = v_ready(t);
-              if (!wait(&bars->p_full[x], s_uses[x]++)) break;
+              const int v_rows = v_ready(t, jt);
+              if (!(ok = v_rows > 0 && mbar_wait(&bars->p_full[x], (pp >> x) & 1u, err, kErrPrefillMma))) break;
+              pp ^= 1u << x;
               tc_fence_after();
-              issue_pv(x, jt + t, t < 2, steps);
-              tc_commit(&bars->v_empty[(jt + t) % kNS]);
+              issue_pv(x, jt % kNS, t < 2, v_rows);
+              tc_commit(&bars->v_empty[jt % kNS]);
               if (t + 2 < nt) {
-                if (!wait(&bars->k_full[(jt + t + 2) % kNS], (jt + t + 2) / kNS)) break;
+                if (!(ok = k_ready(jt + 2))) break;
                 tc_fence_after();
-                issue_s(x, qs, jt + t + 2);
-                tc_commit(&bars->k_empty[(jt + t + 2) % kNS]);
+                issue_s(x, qs, (jt + 2) % kNS);
+                tc_commit(&bars->k_empty[(jt + 2) % kNS]);
                 if (t + 3 == nt) tc_commit(&bars->q_empty[qs]);
               } else {
                 tc_commit(&bars->o_final[x]);
               }
             }
-            if (!ok) break;
           }
-          jt += nt;
-          in.done();
-          ++in.count;
         }
         // every MMA this thread issued has finished before TMEM is released
         tc_commit(&bars->drain);
@@ -778,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row within the query tile == TMEM lane
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t lane_base = *(volatile uint32_t*)&bars->tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t sbase = lane_base + col_s(x);
     const uint32_t obase = lane_base + col_o(x);
     const float sl2 = p.scale_log2;
@@ -791,16 +857,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       if (!mbar_wait_warp(in.full(), in.parity(), err, kErrPrefillSoftmax)) break;
       const Seg& g = in.seg();
       if (g.last) break;
+      if (!mbar_wait_warp(in.known(), in.parity(), err, kErrPrefillSoftmax)) break;
       const bool two = g.rows > BM;
       const int nt = g.j1 - g.j0;
       const int step = two ? 1 : 2, t0 = two ? 0 : x;  // its tiles: t0, t0 + step, ...
       const int row = two ? x * BM + r : r;            // of the item
       const bool mine_any = row - lane < g.rows;       // (the same for the warp)
-      // token of the sequence, and absolute position; a row past the item takes the last one's
-      const int tok = g.q0 + (min(row, g.rows - 1) >> p.log2_g);
-      const int i_abs = p.cu_new ? g.n + tok : g.n - 1;
-      // first tile of the new tokens that some row of this query tile does not see whole
-      const int diag = (g.q0 + ((two ? x * BM : 0) >> p.log2_g)) / BN;
+      // tiles below plain are seen whole by every row, and so are those from n_cache on below diag, the first
+      // one of the new tokens that some row of this query tile does not see whole; a streaming head's are
+      // all masked, and so are those of a segment with a block that does not exist
+      const int n_cache = g.n_cache;
+      const int plain = g.streaming || g.bad ? 0 : (g.cut_cache >= 0 ? n_cache - 1 : n_cache);
+      const int diag = g.streaming ? 0 : n_cache + (g.q0 + ((two ? x * BM : 0) >> p.log2_g)) / BN;
       float m_run = -INFINITY, l_run = 0.f;
       if (!mine_any) {
         // no rows: what its rows of S hold goes for P, and their O is not read
@@ -812,36 +880,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         }
       } else {
         for (int t = t0; t < nt; t += step) {
-          // masks first, while the scores are on their way
-          uint32_t vis[BN / 32] = {~0u, ~0u, ~0u, ~0u};
-          bool masked;
-          {
-            const Tile tl = tile_at(g, g.j0 + t);
-            masked = g.streaming || (tl.cache ? tl.valid < BN : tl.k >= diag);
-            if (tl.cache && !g.streaming) {
-              const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks +
-                                        (unsigned)tl.k / ((unsigned)p.pg.block_size / BN)];
-              if (masked) {
-#pragma unroll
-                for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = visible(p, g, tl, q4 * 32, i_abs, 0);
-              }
-              if (id < 0 || id >= p.pg.num_blocks) {  // a block that does not exist
-                masked = true;
-#pragma unroll
-                for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = 0u;
-              }
-            } else if (masked) {
+          const int j = g.j0 + t;
+          uint32_t masked = 0;  // 32-key chunks in which some row of the warp does not see some key
+          if (j >= plain && (j < n_cache || j >= diag)) {
+            // the masks first, while the scores are on their way; they wait in shared memory
+            const Tile tl = tile_at(g, j);
+            const int i_abs = position(p, g, row);
+            int jp[BN / 32];
+            if (g.streaming && tl.cache) {
               const int32_t* held = p.pos + (int64_t)g.b * (p.sh.S + p.sh.R);
-              int jp[BN / 32];
+              const int slots = min(g.n, p.sh.S + p.sh.R);
 #pragma unroll
               for (int q4 = 0; q4 < BN / 32; ++q4) {
                 const int s = tl.k * BN + q4 * 32 + lane;
-                jp[q4] = tl.cache && s < g.held ? held[s] : -1;
+                jp[q4] = s < slots ? held[s] : -1;
               }
-#pragma unroll
-              for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = visible(p, g, tl, q4 * 32, i_abs, jp[q4]);
             }
-            masked = __any_sync(0xffffffffu, (vis[0] & vis[1] & vis[2] & vis[3]) != ~0u);
+            uint32_t vis[BN / 32];
+#pragma unroll
+            for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = visible(p, g, tl, rows_of(g, j), q4 * 32, i_abs, jp[q4]);
+            if (g.bad && tl.cache) {
+              const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks + tl.k / (p.pg.block_size / BN)];
+              if (id < 0 || id >= p.pg.num_blocks) vis[0] = vis[1] = vis[2] = vis[3] = 0u;
+            }
+#pragma unroll
+            for (int q4 = 0; q4 < BN / 32; ++q4) masked |= (uint32_t)__any_sync(0xffffffffu, vis[q4] != ~0u) << q4;
+            sVis[threadIdx.x] = make_uint4(vis[0], vis[1], vis[2], vis[3]);
           }
           if (!mbar_wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
             ok = false;
@@ -858,8 +922,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           }
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < BN; ++e)
-              if (!((vis[e / 32] >> (e % 32)) & 1u)) v[e] = -INFINITY;
+            for (int q4 = 0; q4 < BN / 32; ++q4) {
+              if (!((masked >> q4) & 1u)) continue;
+              const uint32_t vis = reinterpret_cast<const uint32_t*>(&sVis[threadIdx.x])[q4];
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((vis >> e) & 1u)) v[q4 * 32 + e] = -INFINITY;
+            }
           }
           float mxa = v[0], mxb = v[1];
 #pragma unroll
@@ -941,8 +1010,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             f1 *= inv;
           }
           const int q_first = both ? x * (D / 64) : 0, q_end = both ? q_first + D / 64 : D / 32;
-          const int head = (g.kvh << p.log2_g) + (row & ((1 << p.log2_g) - 1));
-          uint16_t* orow = p.o + ((int64_t)(g.tok0 + tok) * p.sh.Hq + head) * D;
           float4* prow = reinterpret_cast<float4*>(p.part_o + (int64_t)part * p.part_rows * D) + row;
 #pragma unroll 1
           for (int q4 = q_first; q4 < q_end; ++q4) {
@@ -962,12 +1029,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 prow[(int64_t)(q4 * 8 + e) * p.part_rows] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-            } else if (store) {
+            } else if (part < 0) {
+              // four lanes exchange their rows' 64 bytes, so that each store has these of a row side by side
+              // (32 rows of 16 bytes a store took 32 wavefronts)
+              uint32_t w[4][4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                reinterpret_cast<uint4*>(orow + q4 * 32)[e] =
-                    make_uint4(pack_bf16x2(ov[8 * e], ov[8 * e + 1]), pack_bf16x2(ov[8 * e + 2], ov[8 * e + 3]),
-                               pack_bf16x2(ov[8 * e + 4], ov[8 * e + 5]), pack_bf16x2(ov[8 * e + 6], ov[8 * e + 7]));
+              for (int e = 0; e < 16; ++e) w[e / 4][e % 4] = pack_bf16x2(ov[2 * e], ov[2 * e + 1]);
+#pragma unroll
+              for (int k = 1; k < 4; k *= 2) {
+                const bool up = lane & k;
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                  if (a & k) continue;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[a][e] : w[a + k][e], k);
+                    w[a][e] = up ? got : w[a][e];
+                    w[a + k][e] = up ? w[a + k][e] : got;
+                  }
+                }
+              }
+#pragma unroll
+              for (int a = 0; a < 4; ++a) {  // chunk lane % 4 of row `to`
+                const int to = row - (lane & 3) + a;
+                if (to < g.rows) {
+                  const int64_t at = (int64_t)(g.tok0 + g.q0 + (to >> p.log2_g)) * p.sh.Hq + (g.kvh << p.log2_g) +
+                                     (to & ((1 << p.log2_g) - 1));
+                  reinterpret_cast<uint4*>(p.o + at * D + q4 * 32)[lane & 3] = make_uint4(w[a][0], w[a][1], w[a][2], w[a][3]);
+                }
+              }
             }
           }
           if (store && part >= 0 && (!both || x == 0)) p.part_ml[(int64_t)part * p.part_rows + row] = make_float2(m, l);
@@ -992,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   __syncthreads();
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(bars->tmem_base, kTmemCols);
   }
 }
 
