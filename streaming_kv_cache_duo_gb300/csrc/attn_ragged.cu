@@ -49,13 +49,13 @@ __device__ unsigned int g_attn_ragged_err;
 constexpr int BM = 128;  // rows per query tile
 constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10, kWarpLine = 11;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpLine = 11;  // (warp 10 is idle)
 // 2 x 128 x 200 + 128 x 104 = 384 x 168 = 64512, the launch's registers
 constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
 constexpr int kSegs = 4;         // descriptors in flight
-constexpr int kSegUsers = 11;    // producer, MMA, tail, eight softmax warps
+constexpr int kSegUsers = 10;    // producer, MMA, eight softmax warps
 
 // Places on the line: a retrieval tile's, a streaming one's (all of its tiles are masked), and an item's
 // own. A CTA's share has kLeast at least; an item of up to kShort tiles is not shared.
@@ -98,7 +98,6 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2], o_final[2];
-  uint64_t v_ask, v_fixed;  // a V tile with rows to zero has arrived; they are zero
   uint64_t pair_ml[4], pair_done[4];
   uint64_t seg_full[kSegs], seg_empty[kSegs], seg_known[kSegs];
   uint64_t drain;
@@ -308,7 +307,13 @@ __device__ __forceinline__ int position(const RaggedAttnParams& p, const Seg& g,
   return p.cu_new ? g.n + g.q0 + (min(row, g.rows - 1) >> p.log2_g) : g.n - 1;
 }
 
-// Reads the descriptors in order: next() waits for one, done() gives it back.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// Reads the descriptors in order: done() gives one back.
 struct SegReader {
   Bars* bars;
   int count = 0;
@@ -362,8 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       mbar_init(&bars->pair_ml[w], 2);
       mbar_init(&bars->pair_done[w], 2);
     }
-    mbar_init(&bars->v_ask, 1);
-    mbar_init(&bars->v_fixed, 1);
     mbar_init(&bars->drain, 1);
     fence_mbarrier_init();
     // After any CTA gave up a wait, later ones do no work, so that a failure ends in about one wait limit.
@@ -664,177 +667,151 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           }
         }
       }
-    } else if (warp == kWarpTail) {
-      // ------------------------------------------------------------ rows of V that no token owns
-      // (told of by the MMA thread, tile by tile: this warp does not follow the stages' phases itself)
-      SegReader in(bars);
-      int jt = 0, asked = 0;
-      bool ok = true;
-      while (ok) {
-        if (!mbar_wait_warp(in.full(), in.parity(), err, kErrPrefillProducer)) break;
-        const Seg g = in.seg();
-        if (g.last) break;
-        for (int j = g.j0; j < g.j1 && ok; ++j) {
-          const int rows = rows_of(g, j), odd = rows & 15;
-          if (odd == 0) continue;
-          const int jj = jt + (j - g.j0), s = jj % kNS;
-          if (!mbar_wait_warp(&bars->v_ask, (uint32_t)(asked++ & 1), err, kErrPrefillProducer)) {
-            ok = false;
-            break;
-          }
-          // (whole 128-byte rows of the boxes, so the swizzle does not matter)
-          uint8_t* v = sV + s * C::KV_BYTES + rows * 128;
-          for (int e = lane; e < (16 - odd) * 8 * C::NBOX; e += 32)
-            *reinterpret_cast<uint4*>(v + (e / ((16 - odd) * 8)) * kBox + e % ((16 - odd) * 8) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_shared();  // read by the tensor core next
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->v_fixed);
-        }
-        jt += g.j1 - g.j0;
-        __syncwarp();
-        if (lane == 0) in.done();
-        ++in.count;
-      }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-        // (a k-step only moves the start address, in the descriptors' low bits. Each role reads the TMEM
-        // address for itself: kept since the start it was spilled, and loaded again for every product)
-        const uint32_t tmem = *(volatile uint32_t*)&bars->tmem_base;
-        const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), kBox, 1024);
-        // S_x = Q K^T, Q in place qs, K in stage s
-        auto issue_s = [&](int x, int qs, int s) {
-          const uint64_t dq = dq0 + (uint64_t)((qs * C::Q_BYTES) >> 4);
-          const uint64_t dk = dk0 + (uint64_t)((s * C::KV_BYTES) >> 4);
+      // The whole warp follows the tiles and one lane issues. What decides where it goes is read through
+      // shuffles, so that the compiler knows it to be the same for all lanes and keeps counters, barrier
+      // addresses and descriptors in uniform registers, where the products need them: with one lane
+      // following alone, they went there one by one, and a tile took 500 cycles more.
+      constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+      auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+      const uint32_t tmem = uniform(*(volatile uint32_t*)&bars->tmem_base);
+      // (a k-step only moves the start address, in the descriptors' low bits)
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), kBox, 1024);
+      // S_x = Q K^T, Q in place qs, K in stage s
+      auto issue_s = [&](int x, int qs, int s) {
+        const uint64_t dq = dq0 + (uint64_t)((qs * C::Q_BYTES) >> 4);
+        const uint64_t dk = dk0 + (uint64_t)((s * C::KV_BYTES) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t koff = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + col_s(x), dq + koff, dk + koff, idesc_s, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&bars->s_full[x]);
-        };
-        // O_x (+)= P_x V, V in stage s, over the first `rows` keys (in groups of 16)
-        auto issue_pv = [&](int x, int s, bool first, int rows) {
-          const uint64_t dv = dv0 + (uint64_t)((s * C::KV_BYTES) >> 4);
-          if (rows == BN) {
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t koff = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + col_s(x), dq + koff, dk + koff, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars->s_full[x]);
+      };
+      // O_x (+)= P_x V, V in stage s, over the first `rows` keys (in groups of 16)
+      auto issue_pv = [&](int x, int s, bool first, int rows) {
+        const uint64_t dv = dv0 + (uint64_t)((s * C::KV_BYTES) >> 4);
+        if (rows == BN) {
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                     (!first || kk > 0) ? 1u : 0u);
-          } else {
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                   (!first || kk > 0) ? 1u : 0u);
+        } else {
 #pragma unroll 1
-            for (int kk = 0; kk < (rows + 15) >> 4; ++kk)
-              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                     (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < (rows + 15) >> 4; ++kk)
+            mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                   (!first || kk > 0) ? 1u : 0u);
+        }
+      };
+      auto ready = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, err, kErrPrefillMma); };
+      SegReader in(bars);
+      int jt = 0;                // tiles so far: tile jt is in stage jt % kNS
+      uint32_t pp = 0, qp = 0;   // phases of p_full and q_full, a bit each
+      int slot = 0;
+      bool ok = true;
+      while (ok) {
+        if (!(ok = ready(in.full(), in.parity()))) break;
+        const Seg& g = in.seg();
+        if (uniform(g.last)) break;
+        const int nt = uniform(g.j1 - g.j0), rows = uniform(g.rows);
+        const int cut_c = uniform(g.cut_cache - g.j0), cut_n = uniform(g.cut_new - g.j0);
+        const int rows_c = uniform(g.rows_cache), rows_n = uniform(g.rows_new);
+        if (elect_one()) in.done();
+        ++in.count;
+        auto k_ready = [&](int j) { return ready(&bars->k_full[j % kNS], (uint32_t)((j / kNS) & 1)); };
+        auto v_ready = [&](int j) { return ready(&bars->v_full[j % kNS], (uint32_t)((j / kNS) & 1)); };
+        // rows of tile t's V to multiply; what no token owns of their last 16 is set to zero first
+        // (whole 128-byte rows of the boxes, so the swizzle does not matter)
+        auto rows_to_use = [&](int t, int s) {
+          if (t != cut_c && t != cut_n) return BN;
+          const int r = t == cut_c ? rows_c : rows_n, pad = 16 - (r & 15);
+          if (pad < 16) {
+            uint8_t* v = sV + s * C::KV_BYTES + r * 128;
+            for (int e = lane; e < pad * 8 * C::NBOX; e += 32)
+              *reinterpret_cast<uint4*>(v + (e / (pad * 8)) * kBox + e % (pad * 8) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_shared();  // read by the tensor core next
+            __syncwarp();
           }
+          return r;
         };
-        SegReader in(bars);
-        int jt = 0;                        // tiles so far: tile jt is in stage jt % kNS
-        uint32_t pp = 0, qp = 0, fp = 0;   // phases: of p_full and q_full (a bit each), of v_fixed
-        int slot = 0;
-        bool ok = true;
-        while (ok) {
-          if (!(ok = mbar_wait(in.full(), in.parity(), err, kErrPrefillMma))) break;
-          int nt, rows, cut_c, cut_n, rows_c, rows_n;
-          {
-            const Seg& g = in.seg();
-            if (g.last) break;
-            nt = g.j1 - g.j0;
-            rows = g.rows;
-            cut_c = g.cut_cache - g.j0;
-            cut_n = g.cut_new - g.j0;
-            rows_c = g.rows_cache;
-            rows_n = g.rows_new;
-          }
-          in.done();
-          ++in.count;
-          auto k_ready = [&](int j) {
-            return mbar_wait(&bars->k_full[j % kNS], (uint32_t)((j / kNS) & 1), err, kErrPrefillMma);
-          };
-          // the tile's V has arrived, and those of its rows without a token that would be multiplied are
-          // zero; the rows to multiply (0: a wait ran out)
-          auto v_ready = [&](int t, int j) {
-            if (!mbar_wait(&bars->v_full[j % kNS], (uint32_t)((j / kNS) & 1), err, kErrPrefillMma)) return 0;
-            if (t != cut_c && t != cut_n) return BN;
-            const int r = t == cut_c ? rows_c : rows_n;
-            if ((r & 15) == 0) return r;
-            mbar_arrive(&bars->v_ask);
-            fp ^= 1u;
-            return mbar_wait(&bars->v_fixed, fp ^ 1u, err, kErrPrefillMma) ? r : 0;
-          };
-          if (rows > BM) {
-            // two query tiles, each K/V tile for both
-            ok = mbar_wait(&bars->q_full[0], qp & 1u, err, kErrPrefillMma) &&
-                 mbar_wait(&bars->q_full[1], (qp >> 1) & 1u, err, kErrPrefillMma) && k_ready(jt);
-            qp ^= 3u;
-            if (!ok) break;
+        if (rows > BM) {
+          // two query tiles, each K/V tile for both
+          ok = ready(&bars->q_full[0], qp & 1u) && ready(&bars->q_full[1], (qp >> 1) & 1u) && k_ready(jt);
+          qp ^= 3u;
+          if (!ok) break;
+          if (elect_one()) {
             tc_fence_after();
             issue_s(0, 0, jt % kNS);
             issue_s(1, 1, jt % kNS);
             tc_commit(&bars->k_empty[jt % kNS]);
-            for (int t = 0; t < nt; ++t, ++jt) {
-              const bool more = t + 1 < nt;
-              if (!more) {  // the scores are the last of Q
-                tc_commit(&bars->q_empty[0]);
-                tc_commit(&bars->q_empty[1]);
-              }
-              const int v_rows = v_ready(t, jt);
-              if (v_rows == 0 || (more && !k_ready(jt + 1))) {
-                ok = false;
-                break;
-              }
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                if (!ok || !(ok = mbar_wait(&bars->p_full[x], (pp >> x) & 1u, err, kErrPrefillMma))) break;
-                tc_fence_after();
-                issue_pv(x, jt % kNS, t == 0, v_rows);
-                if (more) issue_s(x, x, (jt + 1) % kNS);
-                else tc_commit(&bars->o_final[x]);
-              }
-              if (!ok) break;
-              pp ^= 3u;
-              tc_commit(&bars->v_empty[jt % kNS]);
-              if (more) tc_commit(&bars->k_empty[(jt + 1) % kNS]);
+            if (nt == 1) {
+              tc_commit(&bars->q_empty[0]);
+              tc_commit(&bars->q_empty[1]);
             }
-          } else {
-            // one query tile, even key tiles with S_0 and O_0, odd ones with S_1 and O_1
-            const int qs = slot;
-            slot ^= 1;
-            ok = mbar_wait(&bars->q_full[qs], (qp >> qs) & 1u, err, kErrPrefillMma);
-            qp ^= 1u << qs;
-            for (int t = 0; t < 2 && t < nt && ok; ++t) {
-              if (!(ok = k_ready(jt + t))) break;
-              tc_fence_after();
-              issue_s(t, qs, (jt + t) % kNS);
-              tc_commit(&bars->k_empty[(jt + t) % kNS]);
+          }
+          for (int t = 0; t < nt; ++t, ++jt) {
+            const bool more = t + 1 < nt;
+            const int s = jt % kNS, sn = (jt + 1) % kNS;
+            if (!(ok = v_ready(jt) && (!more || k_ready(jt + 1)))) break;
+            const int v_rows = rows_to_use(t, s);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!ok || !(ok = ready(&bars->p_full[x], (pp >> x) & 1u))) break;
+              if (elect_one()) {
+                tc_fence_after();
+                issue_pv(x, s, t == 0, v_rows);
+                if (more) issue_s(x, x, sn);
+                else tc_commit(&bars->o_final[x]);
+                if (x == 1) {
+                  tc_commit(&bars->v_empty[s]);
+                  if (more) tc_commit(&bars->k_empty[sn]);
+                }
+                if (t + 2 == nt) tc_commit(&bars->q_empty[x]);  // the last scores of Q
+              }
             }
             if (!ok) break;
-            if (nt <= 2) tc_commit(&bars->q_empty[qs]);
-            for (int t = 0; t < nt; ++t, ++jt) {
-              const int x = t & 1;
-              const int v_rows = v_ready(t, jt);
-              if (!(ok = v_rows > 0 && mbar_wait(&bars->p_full[x], (pp >> x) & 1u, err, kErrPrefillMma))) break;
+            pp ^= 3u;
+          }
+        } else {
+          // one query tile, even key tiles with S_0 and O_0, odd ones with S_1 and O_1
+          const int qs = slot;
+          slot ^= 1;
+          ok = ready(&bars->q_full[qs], (qp >> qs) & 1u);
+          qp ^= 1u << qs;
+          for (int t = -2; t < nt && ok; ++t) {
+            // P_x V of tile t (from 0 on), then the scores of tile t + 2
+            const int x = t & 1, j = jt + t;
+            int v_rows = 0;
+            if (t >= 0) {
+              if (!(ok = v_ready(j))) break;
+              v_rows = rows_to_use(t, j % kNS);
+              if (!(ok = ready(&bars->p_full[x], (pp >> x) & 1u))) break;
               pp ^= 1u << x;
+            }
+            if (t + 2 < nt && !(ok = k_ready(j + 2))) break;
+            if (elect_one()) {
               tc_fence_after();
-              issue_pv(x, jt % kNS, t < 2, v_rows);
-              tc_commit(&bars->v_empty[jt % kNS]);
+              if (t >= 0) {
+                issue_pv(x, j % kNS, t < 2, v_rows);
+                tc_commit(&bars->v_empty[j % kNS]);
+                if (t + 2 >= nt) tc_commit(&bars->o_final[x]);
+              }
               if (t + 2 < nt) {
-                if (!(ok = k_ready(jt + 2))) break;
-                tc_fence_after();
-                issue_s(x, qs, (jt + 2) % kNS);
-                tc_commit(&bars->k_empty[(jt + 2) % kNS]);
+                issue_s(x, qs, (j + 2) % kNS);
+                tc_commit(&bars->k_empty[(j + 2) % kNS]);
                 if (t + 3 == nt) tc_commit(&bars->q_empty[qs]);
-              } else {
-                tc_commit(&bars->o_final[x]);
               }
             }
           }
+          jt += nt;
         }
-        // every MMA this thread issued has finished before TMEM is released
+      }
+      // every MMA issued here has finished before TMEM is released
+      if (elect_one()) {
         tc_commit(&bars->drain);
         mbar_wait(&bars->drain, 0, err, kErrPrefillMma);
       }
