@@ -785,22 +785,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           for (int t = -2; t < nt && ok; ++t) {
             // P_x V of tile t (from 0 on), then the scores of tile t + 2
             const int x = t & 1, j = jt + t;
-            int v_rows = 0;
             if (t >= 0) {
               if (!(ok = v_ready(j))) break;
-              v_rows = rows_to_use(t, j % kNS);
+              const int v_rows = rows_to_use(t, j % kNS);
               if (!(ok = ready(&bars->p_full[x], (pp >> x) & 1u))) break;
               pp ^= 1u << x;
-            }
-            if (t + 2 < nt && !(ok = k_ready(j + 2))) break;
-            if (elect_one()) {
-              tc_fence_after();
-              if (t >= 0) {
+              if (elect_one()) {
+                tc_fence_after();
                 issue_pv(x, j % kNS, t < 2, v_rows);
                 tc_commit(&bars->v_empty[j % kNS]);
                 if (t + 2 >= nt) tc_commit(&bars->o_final[x]);
               }
-              if (t + 2 < nt) {
+            }
+            if (t + 2 < nt) {  // (K is waited for behind the product that gives V's stage back)
+              if (!(ok = k_ready(j + 2))) break;
+              if (elect_one()) {
+                tc_fence_after();
                 issue_s(x, qs, (j + 2) % kNS);
                 tc_commit(&bars->k_empty[(j + 2) % kNS]);
                 if (t + 3 == nt) tc_commit(&bars->q_empty[qs]);
