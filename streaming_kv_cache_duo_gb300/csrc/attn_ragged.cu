@@ -49,17 +49,18 @@ __device__ unsigned int g_attn_ragged_err;
 constexpr int BM = 128;  // rows per query tile
 constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpLine = 11;  // (warp 10 is idle)
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpZero = 10, kWarpLine = 11;
 // 2 x 128 x 200 + 128 x 104 = 384 x 168 = 64512, the launch's registers
 constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
 constexpr int kSegs = 4;         // descriptors in flight
+constexpr int kWarpBatch = 64;   // sequences that the line's warp sums alone
 constexpr int kSegUsers = 10;    // producer, MMA, eight softmax warps
 
 // Places on the line: a retrieval tile's, a streaming one's (all of its tiles are masked), and an item's
 // own. A CTA's share has kLeast at least; an item of up to kShort tiles is not shared.
-constexpr int kPlaceR = 2, kPlaceS = 3, kPlaceItem = 6, kLeast = 6, kShort = 3;
+constexpr int kPlaceR = 2, kPlaceS = 3, kPlaceItem = 6, kLeast = kRaggedLeast, kShort = kRaggedShort;
 
 __host__ __device__ constexpr uint32_t col_s(int x) { return (uint32_t)x * 256u; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return (uint32_t)x * 256u + 128u; }
@@ -105,7 +106,7 @@ struct Bars {
   int stop;  // an earlier CTA gave up a wait
   // the line: places of all items, and where this CTA's share begins
   long long sums[2][kThreads / 32];
-  long long start_at;
+  long long places, places_r, start_at;
   int start_b;
   Seg seg[kSegs];
 };
@@ -238,9 +239,36 @@ __device__ __forceinline__ int plan_item(const RaggedAttnParams& p, const Sequen
   return total;
 }
 
-// First place of CTA c of `ctas` on a line of W, and the CTA that place x belongs to.
-__device__ __forceinline__ int64_t bound(int64_t W, int ctas, int c) { return c * W / ctas; }
-__device__ __forceinline__ int owner(int64_t W, int ctas, int64_t x) { return (int)(((x + 1) * ctas + W - 1) / W) - 1; }
+// a / b for a >= 0, b > 0 (64-bit divisions take several times as long)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// CTAs that share a line of W places, the first place of CTA c of them, and the CTA of place x.
+__device__ __forceinline__ int sharers(int64_t W) {
+  return (int)min((int64_t)gridDim.x, max((int64_t)1, divide(W, kLeast)));
+}
+__device__ __forceinline__ int64_t bound(int64_t W, int ctas, int c) { return divide(c * W, ctas); }
+__device__ __forceinline__ int owner(int64_t W, int ctas, int64_t x) { return (int)divide((x + 1) * ctas + W - 1, W) - 1; }
+struct Share {
+  int ctas;
+  int64_t lo, hi;  // of this CTA
+};
+__device__ __forceinline__ Share share_of(int64_t W) {
+  const int ctas = sharers(W), c = blockIdx.x;
+  return Share{ctas, c < ctas ? bound(W, ctas, c) : W, c < ctas ? bound(W, ctas, c + 1) : W};
+}
+// Places of all items of a sequence's heads of one kind.
+__device__ __forceinline__ int64_t places_of(const RaggedAttnParams& p, const Sequence& s, bool streaming) {
+  const int heads = streaming ? p.sh.n_str : p.sh.n_ret;
+  if (s.T == 0 || heads == 0) return 0;
+  const HeadLine h = head_line(p, s, streaming);
+  return heads * h.upto(h.blocks);
+}
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
 // Tile j of an item: of the cache or of the new tokens, and which one of these.
 struct Tile {
@@ -306,6 +334,9 @@ __device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg
 __device__ __forceinline__ int position(const RaggedAttnParams& p, const Seg& g, int row) {
   return p.cu_new ? g.n + g.q0 + (min(row, g.rows - 1) >> p.log2_g) : g.n - 1;
 }
+
+// A value that is the same in all lanes, known to be so by the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -383,77 +414,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---------------------------------------------------------------- this CTA's share of the line
+  // A batch of few sequences is summed by the line's warp alone (two barriers of the whole CTA and
+  // their way through memory cost a small decode 2 us); of many, by all threads: the places of either
+  // kind, and the sequence where the CTA's share begins.
   const int B = p.sh.B;
-  long long mine[2] = {0, 0};  // places of this thread's sequences: retrieval, streaming
-  for (int b = threadIdx.x; b < B; b += kThreads) {
-    const Sequence s = sequence_at(p, b, blockIdx.x == 0);
-    if (s.T > 0) {
-      if (p.sh.n_ret > 0) mine[0] += p.sh.n_ret * head_line(p, s, false).upto(head_line(p, s, false).blocks);
-      if (p.sh.n_str > 0) mine[1] += p.sh.n_str * head_line(p, s, true).upto(head_line(p, s, true).blocks);
-    } else if (!p.cu_new && (int)(b % gridDim.x) == (int)blockIdx.x) {
-      // a sequence without a token: zeros
-      uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)b * p.sh.Hq * D);
-      for (int e = 0; e < p.sh.Hq * D / 8; ++e) o[e] = make_uint4(0, 0, 0, 0);
+  if (B > kWarpBatch) {
+    long long mine[2] = {0, 0};  // places of this thread's sequences: retrieval, streaming
+    for (int b = threadIdx.x; b < B; b += kThreads) {
+      const Sequence s = sequence_at(p, b, blockIdx.x == 0);
+      mine[0] += places_of(p, s, false);
+      mine[1] += places_of(p, s, true);
     }
-  }
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    long long v = mine[k];
+    for (int k = 0; k < 2; ++k) {
+      const long long v = warp_sum(mine[k]);
+      if (lane == 0) bars->sums[k][warp] = v;
+    }
+    __syncthreads();
+    int64_t W_r = 0, W = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) bars->sums[k][warp] = v;
+    for (int w = 0; w < kThreads / 32; ++w) W_r += bars->sums[0][w], W += bars->sums[1][w];
+    W += W_r;
+    const Share sh = share_of(W);
+    const bool streaming = sh.lo >= W_r;
+    if (sh.lo < sh.hi) {  // (the same for all threads) the sequence whose items of that kind hold place lo
+      const int64_t x = streaming ? sh.lo - W_r : sh.lo;
+      long long before = 0;
+      for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int b = b0 + (int)threadIdx.x;
+        long long v = 0;
+        if (B <= kThreads) v = streaming ? mine[1] : mine[0];
+        else if (b < B) v = places_of(p, sequence_at(p, b, false), streaming);
+        long long upto = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += u;
+        }
+        __syncthreads();  // sums have been read
+        if (lane == 31) bars->sums[0][warp] = upto;
+        __syncthreads();
+        long long all = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < warp) upto += bars->sums[0][w];
+          all += bars->sums[0][w];
+        }
+        if (before + upto - v <= x && x < before + upto) {
+          bars->start_b = b;
+          bars->start_at = before + upto - v;
+        }
+        before += all;
+        if (before > x) break;  // (the same for all threads)
+      }
+    }
+    if (threadIdx.x == 0) {
+      bars->places = W;
+      bars->places_r = W_r;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t W_r = 0, W = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) W_r += bars->sums[0][w], W += bars->sums[1][w];
-  W += W_r;
-  const int ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, W / kLeast));
-  const int64_t lo = (int)blockIdx.x < ctas ? bound(W, ctas, blockIdx.x) : W;
-  const int64_t hi = (int)blockIdx.x < ctas ? bound(W, ctas, blockIdx.x + 1) : W;
-  const bool any = lo < hi && !bars->stop;
-  const int kind0 = lo < W_r ? 0 : 1;
-  if (any) {  // (the same for all threads) the sequence whose items of that kind hold place lo
-    const int64_t x = kind0 == 0 ? lo : lo - W_r;
-    long long before = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-      const int b = b0 + (int)threadIdx.x;
-      long long v = 0;
-      if (B <= kThreads) {
-        v = mine[kind0];
-      } else if (b < B) {
-        const Sequence s = sequence_at(p, b, false);
-        if (s.T > 0) {
-          const HeadLine h = head_line(p, s, kind0 == 1);
-          v = (kind0 == 0 ? p.sh.n_ret : p.sh.n_str) * h.upto(h.blocks);
-        }
-      }
-      long long upto = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += u;
-      }
-      __syncthreads();  // sums have been read
-      if (lane == 31) bars->sums[0][warp] = upto;
-      __syncthreads();
-      long long all = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) upto += bars->sums[0][w];
-        all += bars->sums[0][w];
-      }
-      if (before + upto - v <= x && x < before + upto) {
-        bars->start_b = b;
-        bars->start_at = before + upto - v;
-      }
-      before += all;
-      if (before > x) break;  // (the same for all threads)
-    }
-  }
-  __syncthreads();
 
   if (warp >= 8) {
     // ================================================ warpgroup 2: TMA, MMA, tails, the line
@@ -463,20 +485,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       int count = 0;
       RaggedJob job{-1, 0, 0, 0};
       bool ok = true;
-      if (any && bars->start_b >= 0) {
-        int kind = kind0, base = bars->start_b;
-        int64_t at = bars->start_at + (kind ? W_r : 0);  // where sequence base begins
+      int64_t W_r = bars->places_r, W = bars->places;
+      if (B <= kWarpBatch) {
+        long long r = 0, all = 0;
+        for (int b = lane; b < B; b += 32) {
+          const Sequence s = sequence_at(p, b, blockIdx.x == 0);
+          r += places_of(p, s, false);
+          all += places_of(p, s, true);
+        }
+        W_r = warp_sum(r);
+        W = W_r + warp_sum(all);
+      }
+      const Share sh = share_of(W);
+      const int ctas = sh.ctas;
+      const int64_t lo = sh.lo, hi = sh.hi;
+      if (lo < hi && !bars->stop && (B <= kWarpBatch || bars->start_b >= 0)) {
+        int kind = lo < W_r ? 0 : 1, base = 0;
+        int64_t at = kind ? W_r : 0;  // where sequence base begins
+        if (B > kWarpBatch) {
+          base = bars->start_b;
+          at += bars->start_at;
+        }
         int64_t cur = lo;
         while (ok && cur < hi) {
           // 32 sequences from base on
           Sequence s{0, 0, 0};
-          long long v = 0;
           if (base + lane < B) s = sequence_at(p, base + lane, false);
+          const long long v = places_of(p, s, kind == 1);
           const int heads = kind ? p.sh.n_str : p.sh.n_ret;
-          if (s.T > 0 && heads > 0) {
-            const HeadLine h = head_line(p, s, kind == 1);
-            v = heads * h.upto(h.blocks);
-          }
           for (int w = 0; w < 32 && ok && cur < hi; ++w) {
             const Sequence q{__shfl_sync(0xffffffffu, s.tok0, w), __shfl_sync(0xffffffffu, s.T, w),
                              __shfl_sync(0xffffffffu, s.n, w)};
@@ -492,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             int h = 0, blk = 0;
             int64_t begin = at;
             if (cur > at) {
-              h = (int)((cur - at) / per_head);
+              h = (int)divide(cur - at, per_head);
               begin += h * per_head;
               const int64_t y = cur - begin;
               for (int top = hl.blocks; top - blk > 1;) {
@@ -579,7 +615,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         bars->seg[slot].last = 1;
         mbar_arrive(&bars->seg_full[slot]);
       }
-      if (lane == 0) p.jobs[blockIdx.x] = job;
+      if (lane == 0 && p.jobs) p.jobs[blockIdx.x] = job;
+    } else if (warp == kWarpZero) {
+      // ------------------------------------------------------------ sequences without a token: zeros
+      if (!p.cu_new) {
+        for (int b = blockIdx.x; b < B; b += gridDim.x) {
+          if (p.seq_lens[b] > 0) continue;
+          uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)b * p.sh.Hq * D);
+          for (int e = lane; e < p.sh.Hq * D / 8; e += 32) o[e] = make_uint4(0, 0, 0, 0);
+        }
+      }
     } else if (warp == kWarpTma) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0) {
@@ -675,7 +720,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       // following alone, they went there one by one, and a tile took 500 cycles more.
       constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-      auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
       const uint32_t tmem = uniform(*(volatile uint32_t*)&bars->tmem_base);
       // (a k-step only moves the start address, in the descriptors' low bits)
       const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
@@ -819,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   } else {
     // ================================================ warpgroups 0, 1: softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int x = warp >> 2;
+    const int x = uniform(warp >> 2);
     const int r = (warp & 3) * 32 + lane;  // row within the query tile == TMEM lane
     const uint32_t lane_base = *(volatile uint32_t*)&bars->tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t sbase = lane_base + col_s(x);
@@ -835,17 +879,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       const Seg& g = in.seg();
       if (g.last) break;
       if (!mbar_wait_warp(in.known(), in.parity(), err, kErrPrefillSoftmax)) break;
-      const bool two = g.rows > BM;
-      const int nt = g.j1 - g.j0;
+      const bool two = uniform(g.rows) > BM;
+      const int j0 = uniform(g.j0), nt = uniform(g.j1) - j0;
       const int step = two ? 1 : 2, t0 = two ? 0 : x;  // its tiles: t0, t0 + step, ...
       const int row = two ? x * BM + r : r;            // of the item
       const bool mine_any = row - lane < g.rows;       // (the same for the warp)
       // tiles below plain are seen whole by every row, and so are those from n_cache on below diag, the first
       // one of the new tokens that some row of this query tile does not see whole; a streaming head's are
       // all masked, and so are those of a segment with a block that does not exist
-      const int n_cache = g.n_cache;
-      const int plain = g.streaming || g.bad ? 0 : (g.cut_cache >= 0 ? n_cache - 1 : n_cache);
-      const int diag = g.streaming ? 0 : n_cache + (g.q0 + ((two ? x * BM : 0) >> p.log2_g)) / BN;
+      const int n_cache = uniform(g.n_cache);
+      const int plain = uniform(g.streaming || g.bad ? 0 : (g.cut_cache >= 0 ? n_cache - 1 : n_cache));
+      const int diag = uniform(g.streaming ? 0 : n_cache + (g.q0 + ((two ? x * BM : 0) >> p.log2_g)) / BN);
       float m_run = -INFINITY, l_run = 0.f;
       if (!mine_any) {
         // no rows: what its rows of S hold goes for P, and their O is not read
@@ -857,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         }
       } else {
         for (int t = t0; t < nt; t += step) {
-          const int j = g.j0 + t;
+          const int j = j0 + t;
           uint32_t masked = 0;  // 32-key chunks in which some row of the warp does not see some key
           if (j >= plain && (j < n_cache || j >= diag)) {
             // the masks first, while the scores are on their way; they wait in shared memory
@@ -1158,7 +1202,7 @@ cudaError_t launch_t(const RaggedAttnParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, attn_ragged_kernel<D>, p)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, attn_ragged_kernel<D>, p)) != cudaSuccess || !p.jobs) return e;
   cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.part_rows + 31) / 32 * (D / 32)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

@@ -1383,6 +1383,14 @@ static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const 
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + parts * sh.D);
   p.jobs = reinterpret_cast<RaggedJob*>(p.part_ml + parts);
+  if (!map) {  // single tokens: no more than their longest item's tiles, and no more CTAs than places
+    const int64_t tiles_r = sh.n_ret > 0 ? (max_len + kPrefillBN - 1) / kPrefillBN : 0;
+    const int64_t tiles_s = sh.n_str > 0 ? ((int64_t)std::min<int64_t>(max_len, (int64_t)sh.S + sh.R) + kPrefillBN - 1) / kPrefillBN : 0;
+    if (std::max(tiles_r, tiles_s) <= kRaggedShort) {
+      p.jobs = nullptr;
+      p.ctas = (int)std::min<int64_t>(p.ctas, (int64_t)sh.B * sh.Hkv);
+    }
+  }
   p.sh = sh;
   p.heads = h->heads;
   p.pg = pg;

@@ -53,6 +53,8 @@ cudaError_t append_ragged_read_clear_error(uint32_t* code);
 
 // ------------------------------------------------------------------ attention
 constexpr int kRaggedRows = 256;  // packed query rows (token x head of a KV head) of an item at most
+constexpr int kRaggedLeast = 6;   // places of a CTA's share at least
+constexpr int kRaggedShort = 4;   // tiles of an item that is not shared at most
 
 // An item whose key tiles several CTAs share, noted by the CTA that begins it (last < 0: it begins none):
 // CTA `at` has the first part in its place 2 at + 1, CTAs at + 1 ... last the others in place 2 c.
@@ -88,7 +90,7 @@ struct RaggedAttnParams {
   float scale_log2;      // log2(e) / sqrt(D)
   float* part_o;         // [2 ctas][D / 4][part_rows][4], unnormalised
   float2* part_ml;       // [2 ctas][part_rows] (max, sum)
-  RaggedJob* jobs;       // [ctas]
+  RaggedJob* jobs;       // [ctas], or nullptr: no item is long enough to be shared
   Shape sh;
   HeadTable heads;
   PagedLayout pg;
