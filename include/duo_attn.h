@@ -493,13 +493,8 @@ duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* ne
  *   one token each:      duo_kv_append_ragged (with the rotation, q beside k),
  *                        duo_attn_decode_paged_varlen
  * Rows are bf16 [num_tokens, heads, D] whose tokens may lie apart, as slices of a fused
- * projection's output do: token t begins `stride` elements after token t - 1 (a multiple of 8,
- * at least heads x D; data 16-byte aligned). */
-typedef struct {
-  void* data;
-  int64_t stride;
-} duo_rows;
-
+ * projection's output do: token t begins x_stride elements after token t - 1 (a multiple of 8,
+ * at least heads x D; addresses 16-byte aligned). */
 /* Rotary positions. Pair i (0 <= i < rotary_dim / 2) of a row, (a, b), at position p becomes
  *     (scale (a cos t - b sin t), scale (b cos t + a sin t)),  t = p f_i,
  * computed in fp32 from bf16 values and rounded once. The pairs are dims (i, i + rotary_dim / 2)
@@ -526,8 +521,9 @@ duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns
  * (int32, device memory); a token at a position below 0 is skipped, its rows of q_out and k_out are
  * left as they were. q_out may be q (with its stride) and k_out k; other overlaps are not allowed. */
 duo_status duo_rope_rotate(const duo_rope* rope, int32_t head_dim, const int32_t* positions, int32_t num_tokens,
-                           const duo_rows* q, const duo_rows* q_out, int32_t num_q_heads, const duo_rows* k,
-                           const duo_rows* k_out, int32_t num_kv_heads, void* stream);
+                           const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                           const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, int32_t num_kv_heads,
+                           void* stream);
 
 /* Append of a packed batch into bf16 paged caches, each sequence with its own length and number of
  * new tokens: k_new, v_new [num_tokens, Hkv, D]. Positions and rows come from `map` alone, as for
@@ -539,8 +535,8 @@ duo_status duo_rope_rotate(const duo_rope* rope, int32_t head_dim, const int32_t
  * and with q and q_out [num_tokens, Hq, D] (or both NULL) q is rotated beside it (q_out may be q). */
 duo_status duo_kv_append_ragged(duo_handle* handle, duo_kv_cache* cache, const duo_paged* paged,
                                 const duo_slot_map* map, int32_t num_tokens, const duo_rope* rope,
-                                const duo_rows* k_new, const duo_rows* v_new, const duo_rows* q,
-                                const duo_rows* q_out, void* stream);
+                                const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                                const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, void* stream);
 
 /* Attention of a packed batch of chunks over bf16 paged caches: sequence b's tokens are map->cu_new[b]
  * ... map->cu_new[b + 1] - 1, at the positions from map->token_pos of the first one on, which is also how
@@ -560,8 +556,9 @@ duo_status duo_kv_append_ragged(duo_handle* handle, duo_kv_cache* cache, const d
  * ordered on the GPU. o must not overlap q, k or v. */
 size_t duo_prefill_ragged_workspace_size(const duo_handle* handle, int32_t num_tokens);
 duo_status duo_attn_prefill_ragged(duo_handle* handle, const duo_kv_cache* cache, const duo_paged* paged,
-                                   const duo_slot_map* map, int32_t num_tokens, const duo_rows* q, const duo_rows* k,
-                                   const duo_rows* v, void* o, void* workspace, size_t workspace_bytes, void* stream);
+                                   const duo_slot_map* map, int32_t num_tokens, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* o,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Its form for one token a sequence, appended before (as duo_attn_decode): sequence b holds seq_lens[b]
  * tokens (device int32 [B], clamped to [0, max_len], the new one included), its query is at position

@@ -158,7 +158,9 @@ class DuoPagedLayer(DuoLayer):
                          device=device)
         bf = dict(dtype=torch.bfloat16, device=self.device)
         self.block_size = block_size
+        # (looked up here: a small call's time is the host's)
         self.index, self.bf16 = self.pos.get_device(), torch.bfloat16
+        self.empty_like, self.dense = torch.empty_like, torch.contiguous_format
         self.k_full = torch.empty((num_blocks, block_size, head_dim), **bf)
         self.v_full = torch.empty_like(self.k_full)
         self.cache.k_full = self.k_full.data_ptr()
@@ -214,8 +216,7 @@ class DuoPagedLayer(DuoLayer):
         if q is not None:
             _packed_rows(self, "q", q, (N, self.Hq, self.D))
             if q_out is None:
-                import torch
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = self.empty_like(q, memory_format=self.dense)
             else:
                 _packed_rows(self, "q_out", q_out, (N, self.Hq, self.D))
         if rope is not None and (rope.head_dim != self.D or rope.index != self.index):
@@ -229,15 +230,15 @@ class DuoPagedLayer(DuoLayer):
         DuoSlotMap) over its caches, as they were before, and over each other. Append the tokens
         afterwards. q, k and v are rotated already, and may lie apart (slices of a fused projection).
         Rows of ``out`` of tokens that the map turns down, and of padding, are not written."""
-        import torch
         N = q.shape[0]
         self._check_packed(slot_map, N, planes=False)
         _packed_rows(self, "q", q, (N, self.Hq, self.D))
         _packed_rows(self, "k", k, (N, self.Hkv, self.D))
         _packed_rows(self, "v", v, (N, self.Hkv, self.D))
         if out is None:
-            out = torch.empty((N, self.Hq, self.D), dtype=torch.bfloat16, device=q.device)
-        _on(self, "o", out, (N, self.Hq, self.D))
+            out = self.empty_like(q, memory_format=self.dense)
+        else:
+            _on(self, "o", out, (N, self.Hq, self.D))
         ws = _stream_workspace(_lib.duo_prefill_ragged_workspace_size(self.handle, N), q.device, stream)
         _lib.duo_attn_prefill_ragged(self.handle, self.cache, self.paged, slot_map.c, N, q, k, v, out, ws, stream)
         return out
@@ -247,9 +248,9 @@ class DuoPagedLayer(DuoLayer):
         max_len); a sequence of length 0 gets zeros."""
         _on(self, "q", q, (self.B, self.Hq, self.D))
         if out is None:
-            import torch
-            out = torch.empty_like(q)
-        _on(self, "o", out, (self.B, self.Hq, self.D))
+            out = self.empty_like(q)
+        else:
+            _on(self, "o", out, (self.B, self.Hq, self.D))
         _check_lens(seq_lens, self.B)
         if seq_lens.get_device() != self.index:
             raise ValueError(f"seq_lens: on {seq_lens.device}, the layer is on CUDA device {self.index}")
@@ -261,7 +262,7 @@ class DuoPagedLayer(DuoLayer):
         raise NotImplementedError("paged caches: append_ragged takes lengths from the device")
 
     def _check_packed(self, slot_map, N, planes):
-        if slot_map.cu_new.get_device() != self.index:
+        if slot_map.index != self.index:
             raise ValueError(f"slot_map: on {slot_map.cu_new.device}, the layer is on CUDA device {self.index}")
         if slot_map.batch != self.B or slot_map.num_tokens != N or (planes and self.n_ret and slot_map.planes != self.n_ret):
             raise ValueError(f"slot_map: of {slot_map.batch} sequences, {slot_map.num_tokens} tokens and "
@@ -310,7 +311,7 @@ class DuoRope:
         turns = [t - (1 << 64) if t >> 63 else t for t in _lib.duo_rope_turns(inv_freq)]
         self.turns = torch.tensor(turns, dtype=torch.int64).to(self.device)
         self.index, self.bf16, self.int32 = self.turns.get_device(), torch.bfloat16, torch.int32
-        self.empty = torch.empty
+        self.empty_like, self.dense = torch.empty_like, torch.contiguous_format
         self.c = _lib.duo_rope(self.turns.data_ptr(), rotary_dim,
                                _lib.DUO_ROPE_HALF if layout == "half" else _lib.DUO_ROPE_INTERLEAVED, self.scale)
 
@@ -326,13 +327,13 @@ class DuoRope:
             raise ValueError(f"the current device is not the frequencies' (CUDA device {self.index})")
         _packed_rows(self, "q", q, (N, q.shape[1], self.head_dim))
         if q_out is None:
-            q_out = self.empty(q.shape, dtype=self.bf16, device=q.device)
+            q_out = self.empty_like(q, memory_format=self.dense)
         else:
             _packed_rows(self, "q_out", q_out, q.shape)
         if k is not None:
             _packed_rows(self, "k", k, (N, k.shape[1], self.head_dim))
             if k_out is None:
-                k_out = self.empty(k.shape, dtype=self.bf16, device=k.device)
+                k_out = self.empty_like(k, memory_format=self.dense)
             else:
                 _packed_rows(self, "k_out", k_out, k.shape)
         _lib.duo_rope_rotate(self.c, self.head_dim, positions, N, q, q_out, k, None if k is None else k_out, stream)
@@ -661,6 +662,7 @@ class DuoSlotMap:
             raise ValueError("token_seq, token_pos and slots: different numbers of tokens")
         self.cu_new, self.token_seq, self.token_pos, self.slots = cu_new, token_seq, token_pos, slots
         self.batch, self.num_tokens, self.planes = cu_new.shape[0] - 1, N, slots.shape[1]
+        self.index = cu_new.get_device()
         self.c = _lib.duo_slot_map(cu_new.data_ptr(), token_seq.data_ptr(), token_pos.data_ptr(), slots.data_ptr())
 
 
@@ -715,10 +717,14 @@ def _on(layer, name, t, shape):
 
 def _packed_rows(owner, name, t, shape):
     """Rows of a packed batch on the owner's device: bf16 [tokens, heads, D], a token's rows in one piece."""
-    if (t.dtype is not owner.bf16 or t.get_device() != owner.index or t.shape != tuple(shape)
-            or (t.numel() and (t.stride(2) != 1 or t.stride(1) != shape[2] or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2])))):
-        raise ValueError(f"{name}: need a bfloat16 tensor of shape {tuple(shape)} on CUDA device {owner.index} with each token's "
-                         f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+    if t.dtype is owner.bf16 and t.get_device() == owner.index and t.shape == shape:
+        if t.is_contiguous():
+            return
+        s = t.stride()
+        if s[2] == 1 and s[1] == shape[2] and (s[0] >= shape[1] * shape[2] or shape[0] < 2):
+            return
+    raise ValueError(f"{name}: need a bfloat16 tensor of shape {tuple(shape)} on CUDA device {owner.index} with each token's "
+                     f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
 def _stream_workspace(nbytes, device, stream):

@@ -87,10 +87,6 @@ class duo_block_pool(ctypes.Structure):
          ("num_blocks", c_int64)]
 
 
-class duo_rows(ctypes.Structure):
-    _fields_ = [("data", c_void_p), ("stride", c_int64)]
-
-
 class duo_rope(ctypes.Structure):
     _fields_ = [("turns", c_void_p), ("rotary_dim", c_int32), ("layout", c_int32), ("scale", c_float)]
 
@@ -175,15 +171,15 @@ def library() -> ctypes.CDLL:
         "duo_block_tables_update": (c_int32, [POINTER(duo_block_pool), c_void_p, c_int32, c_void_p, c_void_p,
                                               POINTER(duo_slot_map), c_void_p, c_size_t, c_void_p]),
         "duo_rope_turns": (c_int32, [POINTER(c_double), c_int32, POINTER(c_uint64)]),
-        "duo_rope_rotate": (c_int32, [POINTER(duo_rope), c_int32, c_void_p, c_int32, POINTER(duo_rows), POINTER(duo_rows),
-                                      c_int32, POINTER(duo_rows), POINTER(duo_rows), c_int32, c_void_p]),
+        "duo_rope_rotate": (c_int32, [POINTER(duo_rope), c_int32, c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64,
+                                      c_int32, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p]),
         "duo_kv_append_ragged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), POINTER(duo_slot_map),
-                                           c_int32, POINTER(duo_rope), POINTER(duo_rows), POINTER(duo_rows),
-                                           POINTER(duo_rows), POINTER(duo_rows), c_void_p]),
+                                           c_int32, POINTER(duo_rope), c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                           c_int64, c_void_p, c_int64, c_void_p]),
         "duo_prefill_ragged_workspace_size": (c_size_t, [c_void_p, c_int32]),
         "duo_attn_prefill_ragged": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), POINTER(duo_slot_map),
-                                              c_int32, POINTER(duo_rows), POINTER(duo_rows), POINTER(duo_rows), c_void_p,
-                                              c_void_p, c_size_t, c_void_p]),
+                                              c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                              c_void_p, c_void_p, c_size_t, c_void_p]),
         "duo_attn_decode_paged_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), POINTER(duo_paged), c_void_p, c_int64,
                                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         "duo_kv_append_varlen": (c_int32, [c_void_p, POINTER(duo_kv_cache), c_void_p, c_void_p, c_void_p,
@@ -461,10 +457,9 @@ def duo_paged_stream_dead_blocks(sink_size: int, recent_size: int, block_size: i
 
 
 def _rows(t):
-    """duo_rows of a tensor [num_tokens, heads, D] whose tokens may lie apart (or None)."""
-    if t is None:
-        return None
-    return ctypes.byref(duo_rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]))
+    """Address of rows [num_tokens, heads, D] whose tokens may lie apart (or None), and elements from one
+    token to the next."""
+    return (None, 0) if t is None else (t.data_ptr(), t.stride(0))
 
 
 def duo_rope_turns(inv_freq) -> list:
@@ -478,15 +473,16 @@ def duo_rope_turns(inv_freq) -> list:
 def duo_rope_rotate(rope: "duo_rope", head_dim: int, positions, num_tokens: int, q, q_out, k, k_out,
                     stream=None) -> None:
     """q and k (or None) [num_tokens, heads, head_dim] rotated by their tokens' positions."""
-    _check(library().duo_rope_rotate(_ref(rope), head_dim, _ptr(positions), num_tokens, _rows(q), _rows(q_out), q.shape[1],
-                                     _rows(k), _rows(k_out), 0 if k is None else k.shape[1], _stream_ptr(stream)))
+    _check(library().duo_rope_rotate(_ref(rope), head_dim, _ptr(positions), num_tokens, *_rows(q), *_rows(q_out),
+                                     q.shape[1], *_rows(k), *_rows(k_out), 0 if k is None else k.shape[1],
+                                     _stream_ptr(stream)))
 
 
 def duo_kv_append_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot_map: "duo_slot_map", num_tokens: int,
                          rope, k_new, v_new, q=None, q_out=None, stream=None) -> None:
     """A packed batch into bf16 paged caches, K (and q into q_out) rotated on the way with rope."""
     _check(library().duo_kv_append_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, _ref(rope),
-                                          _rows(k_new), _rows(v_new), _rows(q), _rows(q_out), _stream_ptr(stream)))
+                                          *_rows(k_new), *_rows(v_new), *_rows(q), *_rows(q_out), _stream_ptr(stream)))
 
 
 def duo_prefill_ragged_workspace_size(handle, num_tokens: int) -> int:
@@ -496,8 +492,8 @@ def duo_prefill_ragged_workspace_size(handle, num_tokens: int) -> int:
 def duo_attn_prefill_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot_map: "duo_slot_map",
                             num_tokens: int, q, k, v, o, workspace, stream=None) -> None:
     """Chunks of a packed batch over bf16 paged caches and their own tokens."""
-    _check(library().duo_attn_prefill_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, _rows(q),
-                                             _rows(k), _rows(v), _ptr(o), _ptr(workspace), _nbytes(workspace),
+    _check(library().duo_attn_prefill_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, *_rows(q),
+                                             *_rows(k), *_rows(v), _ptr(o), _ptr(workspace), _nbytes(workspace),
                                              _stream_ptr(stream)))
 
 

@@ -38,6 +38,8 @@
 // never written) may be anything. Scores there are masked by selection; for V, zero times an infinity or
 // NaN would not do, so the product stops after the 16 rows that hold the last one, and warp 10
 // writes zeros over what is left of those. A block id outside the pool: its rows are left out.
+#include <atomic>
+
 #include "duo_device.cuh"
 #include "ragged_internal.h"
 
@@ -1177,21 +1179,29 @@ __global__ void __launch_bounds__(256) merge_ragged_kernel(const __grid_constant
   }
 }
 
+// The kernel's attributes on a device: set, and looked at, the first time.
 template <int D>
-cudaError_t launch_t(const RaggedAttnParams& p, cudaStream_t stream) {
+cudaError_t prepare_t(int device) {
+  static std::atomic<uint64_t> done{0};  // a bit per device (those past the last bit are prepared every time)
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaError_t e =
+      cudaFuncSetAttribute(attn_ragged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, attn_ragged_kernel<D>)) != cudaSuccess) return e;
+  // the setmaxnreg split is sized for exactly this launch allocation
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  done.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch_t(const RaggedAttnParams& p, int device, cudaStream_t stream) {
   using C = Cfg<D>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
-  // (per device and thread-safe enough: setting it twice does no harm)
-  cudaError_t e = cudaFuncSetAttribute(attn_ragged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  cudaError_t e = prepare_t<D>(device);
   if (e != cudaSuccess) return e;
-  static int regs = -1;
-  if (regs < 0) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, attn_ragged_kernel<D>)) != cudaSuccess) return e;
-    regs = fa.numRegs;
-  }
-  // the setmaxnreg split is sized for exactly this launch allocation
-  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1215,9 +1225,9 @@ size_t ragged_workspace_bytes(int ctas, int rows, int D) {
   return (size_t)2 * ctas * rows * (D * sizeof(float) + sizeof(float2)) + (size_t)ctas * sizeof(RaggedJob);
 }
 
-cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t stream) {
-  if (p.sh.D == 128) return launch_t<128>(p, stream);
-  if (p.sh.D == 64) return launch_t<64>(p, stream);
+cudaError_t launch_attn_ragged(const RaggedAttnParams& p, int device, cudaStream_t stream) {
+  if (p.sh.D == 128) return launch_t<128>(p, device, stream);
+  if (p.sh.D == 64) return launch_t<64>(p, device, stream);
   return cudaErrorInvalidValue;
 }
 

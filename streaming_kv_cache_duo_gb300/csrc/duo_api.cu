@@ -1169,24 +1169,24 @@ duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* ne
 
 // ---------------------------------------------------------------------- packed ragged steps
 // Rows [num_tokens, heads, D] of a packed batch; `what` names them in messages.
-static duo_status check_rows(const duo_rows* r, int heads, int D, const char* what) {
-  if (!r || !r->data || !aligned16(r->data))
-    return fail(DUO_ERR_INVALID_ARG, "%s: NULL or not 16-byte aligned", what);
-  if (r->stride < (int64_t)heads * D || r->stride % 8 != 0)
+// A single token's stride is not used.
+static duo_status check_rows(const void* x, int64_t* stride, int num_tokens, int heads, int D, const char* what) {
+  if (!x || !aligned16(x)) return fail(DUO_ERR_INVALID_ARG, "%s: NULL or not 16-byte aligned", what);
+  if (num_tokens == 1) *stride = (int64_t)heads * D;
+  if (*stride < (int64_t)heads * D || *stride % 8 != 0 || *stride >= (int64_t)1 << 38)
     return fail(DUO_ERR_INVALID_ARG, "%s: stride = %lld is not a multiple of 8, or below %d heads x %d", what,
-                (long long)r->stride, heads, D);
+                (long long)*stride, heads, D);
   return DUO_OK;
 }
 
 // Rows that are rotated: out may be in itself.
-static duo_status check_rotated(const duo_rows* in, const duo_rows* out, int heads, int D, const char* what,
-                                RaggedRows* rows) {
-  duo_status st = check_rows(in, heads, D, what);
-  if (st != DUO_OK || (st = check_rows(out, heads, D, what)) != DUO_OK) return st;
-  if (in->data == out->data && in->stride != out->stride)
+static duo_status check_rotated(const void* in, int64_t in_stride, void* out, int64_t out_stride, int num_tokens,
+                                int heads, int D, const char* what, RaggedRows* rows) {
+  duo_status st = check_rows(in, &in_stride, num_tokens, heads, D, what);
+  if (st != DUO_OK || (st = check_rows(out, &out_stride, num_tokens, heads, D, what)) != DUO_OK) return st;
+  if (in == out && in_stride != out_stride)
     return fail(DUO_ERR_INVALID_ARG, "%s: rotated in place with another stride", what);
-  *rows = RaggedRows{static_cast<const uint16_t*>(in->data), static_cast<uint16_t*>(out->data), in->stride, out->stride,
-                     heads};
+  *rows = RaggedRows{static_cast<const uint16_t*>(in), static_cast<uint16_t*>(out), in_stride, out_stride, heads};
   return DUO_OK;
 }
 
@@ -1226,8 +1226,9 @@ duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns
 }
 
 duo_status duo_rope_rotate(const duo_rope* rope, int32_t head_dim, const int32_t* positions, int32_t num_tokens,
-                           const duo_rows* q, const duo_rows* q_out, int32_t num_q_heads, const duo_rows* k,
-                           const duo_rows* k_out, int32_t num_kv_heads, void* stream) {
+                           const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                           const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, int32_t num_kv_heads,
+                           void* stream) {
   if (!rope) return fail(DUO_ERR_INVALID_ARG, "rope is NULL");
   if (head_dim != 64 && head_dim != 128) return fail(DUO_ERR_UNSUPPORTED, "head_dim = %d not in {64, 128}", head_dim);
   if (num_tokens < 0) return fail(DUO_ERR_INVALID_ARG, "num_tokens = %d < 0", num_tokens);
@@ -1240,8 +1241,10 @@ duo_status duo_rope_rotate(const duo_rope* rope, int32_t head_dim, const int32_t
   if (num_tokens == 0) return ok();
   if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u))
     return fail(DUO_ERR_INVALID_ARG, "positions NULL or not 4-byte aligned");
-  if ((st = check_rotated(q, q_out, num_q_heads, head_dim, "q", &p.q)) != DUO_OK) return st;
-  if (k && (st = check_rotated(k, k_out, num_kv_heads, head_dim, "k", &p.k)) != DUO_OK) return st;
+  if ((st = check_rotated(q, q_stride, q_out, q_out_stride, num_tokens, num_q_heads, head_dim, "q", &p.q)) != DUO_OK) return st;
+  if (k && (st = check_rotated(k, k_stride, k_out, k_out_stride, num_tokens, num_kv_heads, head_dim, "k",
+                               &p.k)) != DUO_OK)
+    return st;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1281,8 +1284,9 @@ static duo_status check_slot_map(const duo_slot_map* map, bool seq, bool slots) 
 }
 
 duo_status duo_kv_append_ragged(duo_handle* h, duo_kv_cache* c, const duo_paged* paged, const duo_slot_map* map,
-                                int32_t num_tokens, const duo_rope* rope, const duo_rows* k_new, const duo_rows* v_new,
-                                const duo_rows* q, const duo_rows* q_out, void* stream) {
+                                int32_t num_tokens, const duo_rope* rope, const void* k_new, int64_t k_stride,
+                                const void* v_new, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                                int64_t q_out_stride, void* stream) {
   duo_status st = check_handle(h);
   if (st != DUO_OK) return st;
   if (!map) return fail(DUO_ERR_INVALID_ARG, "map is NULL");
@@ -1297,11 +1301,11 @@ duo_status duo_kv_append_ragged(duo_handle* h, duo_kv_cache* c, const duo_paged*
   if (!q != !q_out) return fail(DUO_ERR_INVALID_ARG, "q and q_out: one of them is NULL");
   if (num_tokens == 0) return ok();
   if ((st = check_slot_map(map, true, sh.n_ret > 0)) != DUO_OK) return st;
-  if ((st = check_rows(k_new, sh.Hkv, sh.D, "k_new")) != DUO_OK) return st;
-  if ((st = check_rows(v_new, sh.Hkv, sh.D, "v_new")) != DUO_OK) return st;
-  if (q && (st = check_rotated(q, q_out, sh.Hq, sh.D, "q", &p.q)) != DUO_OK) return st;
-  p.k = RaggedRows{static_cast<const uint16_t*>(k_new->data), nullptr, k_new->stride, 0, sh.Hkv};
-  p.v = RaggedRows{static_cast<const uint16_t*>(v_new->data), nullptr, v_new->stride, 0, sh.Hkv};
+  if ((st = check_rows(k_new, &k_stride, num_tokens, sh.Hkv, sh.D, "k_new")) != DUO_OK) return st;
+  if ((st = check_rows(v_new, &v_stride, num_tokens, sh.Hkv, sh.D, "v_new")) != DUO_OK) return st;
+  if (q && (st = check_rotated(q, q_stride, q_out, q_out_stride, num_tokens, sh.Hq, sh.D, "q", &p.q)) != DUO_OK) return st;
+  p.k = RaggedRows{static_cast<const uint16_t*>(k_new), nullptr, k_stride, 0, sh.Hkv};
+  p.v = RaggedRows{static_cast<const uint16_t*>(v_new), nullptr, v_stride, 0, sh.Hkv};
   p.positions = map->token_pos;
   p.tokens = num_tokens;
   p.chunk = rope_chunk(num_tokens, h->num_sms);
@@ -1346,17 +1350,18 @@ size_t duo_prefill_ragged_workspace_size(const duo_handle* h, int32_t num_tokens
 
 // q, o: N tokens; map (chunks) or seq_lens (single tokens).
 static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const PagedLayout& pg, const duo_slot_map* map,
-                              const int32_t* seq_lens, int64_t max_len, int N, int rows, const duo_rows& q,
-                              const duo_rows* k, const duo_rows* v, void* o, void* workspace, void* stream) {
+                              const int32_t* seq_lens, int64_t max_len, int N, int rows, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* o, void* workspace,
+                              void* stream) {
   const Shape& sh = h->sh;
   RaggedAttnParams p;
   memset(&p, 0, sizeof(p));
   duo_status st;
-  if ((st = encode_rows(h, &p.tm_q, q.data, q.stride, N, sh.Hq, sh.D, sh.g, kPrefillBM / sh.g)) != DUO_OK) return st;
-  if ((st = encode_rows(h, &p.tm_q8, q.data, q.stride, N, sh.Hq, sh.D, sh.g, 8 / sh.g)) != DUO_OK) return st;
+  if ((st = encode_rows(h, &p.tm_q, q, q_stride, N, sh.Hq, sh.D, sh.g, kPrefillBM / sh.g)) != DUO_OK) return st;
+  if ((st = encode_rows(h, &p.tm_q8, q, q_stride, N, sh.Hq, sh.D, sh.g, 8 / sh.g)) != DUO_OK) return st;
   if (map) {
-    if ((st = encode_rows(h, &p.tm_k, k->data, k->stride, N, sh.Hkv, sh.D, 1, kPrefillBN)) != DUO_OK) return st;
-    if ((st = encode_rows(h, &p.tm_v, v->data, v->stride, N, sh.Hkv, sh.D, 1, kPrefillBN)) != DUO_OK) return st;
+    if ((st = encode_rows(h, &p.tm_k, k, k_stride, N, sh.Hkv, sh.D, 1, kPrefillBN)) != DUO_OK) return st;
+    if ((st = encode_rows(h, &p.tm_v, v, v_stride, N, sh.Hkv, sh.D, 1, kPrefillBN)) != DUO_OK) return st;
     p.cu_new = map->cu_new;
     p.token_pos = map->token_pos;
   }
@@ -1394,7 +1399,7 @@ static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const 
   p.sh = sh;
   p.heads = h->heads;
   p.pg = pg;
-  const cudaError_t e = launch_attn_ragged(p, (cudaStream_t)stream);
+  const cudaError_t e = launch_attn_ragged(p, h->device, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch (packed)");
   return ok();
 }
@@ -1408,8 +1413,9 @@ static duo_status check_workspace(const void* workspace, size_t bytes, size_t ne
 }
 
 duo_status duo_attn_prefill_ragged(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged, const duo_slot_map* map,
-                                   int32_t num_tokens, const duo_rows* q, const duo_rows* k, const duo_rows* v, void* o,
-                                   void* workspace, size_t ws_bytes, void* stream) {
+                                   int32_t num_tokens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, void* o, void* workspace, size_t ws_bytes,
+                                   void* stream) {
   duo_status st = check_handle(h);
   if (st != DUO_OK) return st;
   if (!map) return fail(DUO_ERR_INVALID_ARG, "map is NULL");
@@ -1419,12 +1425,13 @@ duo_status duo_attn_prefill_ragged(duo_handle* h, const duo_kv_cache* c, const d
   if (num_tokens == 0) return ok();
   const Shape& sh = h->sh;
   if ((st = check_slot_map(map, false, false)) != DUO_OK) return st;
-  if ((st = check_rows(q, sh.Hq, sh.D, "q")) != DUO_OK) return st;
-  if ((st = check_rows(k, sh.Hkv, sh.D, "k")) != DUO_OK) return st;
-  if ((st = check_rows(v, sh.Hkv, sh.D, "v")) != DUO_OK) return st;
+  if ((st = check_rows(q, &q_stride, num_tokens, sh.Hq, sh.D, "q")) != DUO_OK) return st;
+  if ((st = check_rows(k, &k_stride, num_tokens, sh.Hkv, sh.D, "k")) != DUO_OK) return st;
+  if ((st = check_rows(v, &v_stride, num_tokens, sh.Hkv, sh.D, "v")) != DUO_OK) return st;
   if (!o || !aligned16(o)) return fail(DUO_ERR_INVALID_ARG, "o NULL or not 16-byte aligned");
   if ((st = check_workspace(workspace, ws_bytes, duo_prefill_ragged_workspace_size(h, num_tokens))) != DUO_OK) return st;
-  return attn_ragged(h, c, pg, map, nullptr, 0, num_tokens, ragged_rows(h, num_tokens), *q, k, v, o, workspace, stream);
+  return attn_ragged(h, c, pg, map, nullptr, 0, num_tokens, ragged_rows(h, num_tokens), q, q_stride, k, k_stride, v, v_stride, o,
+                     workspace, stream);
 }
 
 duo_status duo_attn_decode_paged_varlen(duo_handle* h, const duo_kv_cache* c, const duo_paged* paged,
@@ -1448,8 +1455,8 @@ duo_status duo_attn_decode_paged_varlen(duo_handle* h, const duo_kv_cache* c, co
   if (ragged_workspace_bytes(h->num_sms, sh.g, sh.D) > need)
     return fail(DUO_ERR_WORKSPACE, "%zu bytes of workspace needed pass the %zu of a decode",
                 ragged_workspace_bytes(h->num_sms, sh.g, sh.D), need);
-  const duo_rows rows{const_cast<void*>(q), (int64_t)sh.Hq * sh.D};
-  return attn_ragged(h, c, pg, nullptr, seq_lens, max_len, sh.B, sh.g, rows, nullptr, nullptr, o, workspace, stream);
+  return attn_ragged(h, c, pg, nullptr, seq_lens, max_len, sh.B, sh.g, q, (int64_t)sh.Hq * sh.D, nullptr, 0, nullptr, 0, o,
+                     workspace, stream);
 }
 
 duo_status duo_kv_append_varlen(duo_handle* h, duo_kv_cache* c, int32_t* seq_lens, const void* k_new,

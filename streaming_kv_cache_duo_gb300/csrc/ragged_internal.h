@@ -97,7 +97,7 @@ struct RaggedAttnParams {
 };
 // Bytes of parts and jobs for items of up to `rows` rows on `ctas` CTAs.
 size_t ragged_workspace_bytes(int ctas, int rows, int D);
-cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_attn_ragged(const RaggedAttnParams& p, int device, cudaStream_t stream);
 cudaError_t attn_ragged_read_clear_error(uint32_t* code);
 
 }  // namespace duo
