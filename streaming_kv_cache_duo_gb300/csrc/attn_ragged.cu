@@ -57,12 +57,14 @@ constexpr int kLaunchRegs = 168, kRegsSoftmax = 200, kRegsCtl = 104;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
 constexpr int kSegs = 4;         // descriptors in flight
-constexpr int kWarpBatch = 64;   // sequences that the line's warp sums alone
+constexpr int kWarpBatch = 32;   // sequences that the line's warp sums alone
 constexpr int kSegUsers = 10;    // producer, MMA, eight softmax warps
 
 // Places on the line: a retrieval tile's, a streaming one's (all of its tiles are masked), and an item's
 // own. A CTA's share has kLeast at least; an item of up to kShort tiles is not shared.
-constexpr int kPlaceR = 2, kPlaceS = 3, kPlaceItem = 6, kLeast = kRaggedLeast, kShort = kRaggedShort;
+// (Measured, in units of 0.7 us: two query tiles, 2.0 to 2.1 a retrieval tile, 21.5 a streaming item of five
+// tiles; one, 1.9 a retrieval tile from HBM, 10.5 a streaming item of three.)
+constexpr int kPlaceR = 2, kPlaceS = 3, kPlaceSOne = 2, kPlaceItem = 5, kLeast = kRaggedLeast, kShort = kRaggedShort;
 
 __host__ __device__ constexpr uint32_t col_s(int x) { return (uint32_t)x * 256u; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return (uint32_t)x * 256u + 128u; }
@@ -143,69 +145,50 @@ __device__ __forceinline__ Sequence sequence_at(const RaggedAttnParams& p, int b
   return s;
 }
 
-// Places of a head's items on the line, in the order of their tokens.
-struct HeadLine {
-  int blocks;  // items: blocks of `tb` tokens
-  int exact;   // the first of them, whose tiles are counted; the others are given `late` each
-  int cached;  // cache tiles of those
-  int late;
-  int place;
-  int T, log2_g;
-  bool chunks;
-  // sum over the first m blocks of the new-token tiles that block k sees, ceil(min(T, (k + 1) tb) / 128)
-  __device__ __forceinline__ int64_t new_tiles(int m) const {
-    if (!chunks || m == 0) return 0;
-    const int64_t f = m == blocks ? m - 1 : m;
-    int64_t sum;
-    if (log2_g == 0) {  // tb = 256
-      sum = f * (f + 1);
-    } else {  // 2^l blocks a tile
-      const int l = log2_g - 1;
-      const int64_t q = f >> l, rest = f & ((1 << l) - 1);
-      sum = ((q * (q + 1) / 2) << l) + rest * (q + 1);
-    }
-    return m == blocks ? sum + (T + BN - 1) / BN : sum;
-  }
-  // places of block m
-  __device__ __forceinline__ int64_t item(int m) const {
-    if (m >= exact) return kPlaceItem + place * late;
-    const int tb = kRaggedRows >> log2_g;
-    const int fresh = chunks ? (int)((min((int64_t)T, (int64_t)(m + 1) * tb) + BN - 1) / BN) : 0;
-    return kPlaceItem + (int64_t)place * (cached + fresh);
-  }
-  // and of the first m blocks
-  __device__ __forceinline__ int64_t upto(int m) const {
-    const int e = min(m, exact);
-    return (int64_t)e * (kPlaceItem + (int64_t)place * cached) + place * new_tiles(e) +
-           (int64_t)(m - e) * (kPlaceItem + place * late);
-  }
-};
-
 __device__ __forceinline__ int tiles_of(int64_t rows) { return (int)((rows + BN - 1) / BN); }
 
-__device__ __forceinline__ HeadLine head_line(const RaggedAttnParams& p, const Sequence& s, bool streaming) {
-  HeadLine h;
-  const int tb = kRaggedRows >> p.log2_g;
-  h.chunks = p.cu_new != nullptr;
-  h.blocks = (int)(((int64_t)s.T + tb - 1) / tb);
-  h.T = s.T;
-  h.log2_g = p.log2_g;
-  h.exact = h.blocks;
-  h.late = 0;
-  if (!streaming) {
-    h.cached = tiles_of(s.n);
-    h.place = kPlaceR;
-  } else {
-    const int held = min(s.n, p.sh.S + p.sh.R);
-    h.cached = tiles_of(held);
-    h.place = kPlaceS;
-    if (h.chunks) {
-      // blocks whose first query sees more of the ring than the sinks
-      h.exact = min(h.blocks, (p.sh.R - 1 + tb - 1) / tb);
-      h.late = tiles_of(min(held, p.sh.S)) + (s.n < p.sh.S ? tiles_of(p.sh.S - s.n) : 0) + (p.sh.R + tb) / BN + 2;
-    }
+// Places on the line of a head's first m items (all, if it has no more), in the order of their tokens. An
+// item reads cache tiles and the new tokens' tiles up to its last token, ceil(min(T, (k + 1) tb) / 128)
+// for block k of tb tokens; a streaming head's, from the first block on whose every query is past the
+// ring but for the sinks, tiles of sinks and of a window (p.window). Out of line, and with few instructions:
+// when a CTA begins, none of them is in its SM's cache, and each costs some 30 cycles the first time.
+__device__ __noinline__ long long line_upto(int T, int n, bool streaming, int m, int log2_g, bool chunks, int S, int R,
+                                            int window) {
+  const int shift = 8 - log2_g;  // tb = 2^shift
+  const int blocks = (int)(((unsigned)T + (1u << shift) - 1u) >> shift);
+  m = min(m, blocks);
+  int place = kPlaceR, held = n, whole = blocks;  // blocks that see the cache whole
+  if (streaming) {
+    place = T > (BM >> log2_g) ? kPlaceS : kPlaceSOne;
+    held = min(n, S + R);
+    if (chunks) whole = min(blocks, (R - 1 + (1 << shift) - 1) >> shift);
   }
-  return h;
+  const int e = min(m, whole);
+  long long tiles = (long long)e * tiles_of(held);
+  if (chunks && e > 0) {
+    const unsigned f = e == blocks ? e - 1 : e;
+    const int l = max(0, log2_g - 1);  // 2^l blocks a tile, or (tb = 256) a block two tiles
+    const unsigned q = f >> l, rest = f & ((1u << l) - 1u);
+    const long long half = (long long)q * (q + 1) / 2;
+    tiles += log2_g == 0 ? 2 * half : (half << l) + (long long)rest * (q + 1);
+    if (e == blocks) tiles += tiles_of(T);
+  }
+  if (m > e) {
+    const int sinks = tiles_of(min(held, S)) + (n < S ? tiles_of(S - n) : 0);
+    const int l = max(0, log2_g - 1);
+    const unsigned longer = window & 15, in = (1u << l) - 1u;
+    const auto ones = [&](unsigned k) { return (int)((k >> l) * __popc(longer) + __popc(longer & ((1u << (k & in)) - 1u))); };
+    tiles += (long long)(m - e) * (sinks + (window >> 4)) + ones(m) - ones(e);
+  }
+  return (long long)m * kPlaceItem + place * tiles;
+}
+__device__ __forceinline__ long long line_upto(const RaggedAttnParams& p, const Sequence& s, bool streaming, int m) {
+  return line_upto(s.T, s.n, streaming, m, p.log2_g, p.cu_new != nullptr, p.sh.S, p.sh.R, p.window);
+}
+constexpr int kAllItems = 0x7fffffff;
+// Places of all items of a sequence's heads of one kind.
+__device__ __forceinline__ long long places_of(const RaggedAttnParams& p, const Sequence& s, bool streaming) {
+  return (streaming ? p.sh.n_str : p.sh.n_ret) * line_upto(p, s, streaming, kAllItems);
 }
 
 // The tiles of block `blk` of a sequence and kind: cache tiles 0 ... n_cache - 1, then of the new tokens
@@ -258,13 +241,6 @@ struct Share {
 __device__ __forceinline__ Share share_of(int64_t W) {
   const int ctas = sharers(W), c = blockIdx.x;
   return Share{ctas, c < ctas ? bound(W, ctas, c) : W, c < ctas ? bound(W, ctas, c + 1) : W};
-}
-// Places of all items of a sequence's heads of one kind.
-__device__ __forceinline__ int64_t places_of(const RaggedAttnParams& p, const Sequence& s, bool streaming) {
-  const int heads = streaming ? p.sh.n_str : p.sh.n_ret;
-  if (s.T == 0 || heads == 0) return 0;
-  const HeadLine h = head_line(p, s, streaming);
-  return heads * h.upto(h.blocks);
 }
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
@@ -488,60 +464,75 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       RaggedJob job{-1, 0, 0, 0};
       bool ok = true;
       int64_t W_r = bars->places_r, W = bars->places;
-      if (B <= kWarpBatch) {
-        long long r = 0, all = 0;
-        for (int b = lane; b < B; b += 32) {
-          const Sequence s = sequence_at(p, b, blockIdx.x == 0);
-          r += places_of(p, s, false);
-          all += places_of(p, s, true);
+      // a window of 32 sequences, one a lane, from `base` on; with few sequences it is all of them, and
+      // says itself where the share begins
+      int base = 0, w = 0, kind = 0;
+      int64_t at = 0;  // where sequence base + w begins
+      Sequence s{0, 0, 0};
+      long long v[2] = {0, 0};
+      auto window = [&]() {
+        s = Sequence{0, 0, 0};
+        if (base + lane < B) s = sequence_at(p, base + lane, B <= kWarpBatch && blockIdx.x == 0);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const long long x = places_of(p, s, k == 1);
+          if (k == 0) v[0] = x;
+          else v[1] = x;
         }
-        W_r = warp_sum(r);
-        W = W_r + warp_sum(all);
+      };
+      if (B <= kWarpBatch) {
+        window();
+        long long upto[2] = {v[0], v[1]};
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long a = __shfl_up_sync(0xffffffffu, upto[0], o), b = __shfl_up_sync(0xffffffffu, upto[1], o);
+          upto[0] += lane >= o ? a : 0;
+          upto[1] += lane >= o ? b : 0;
+        }
+        W_r = __shfl_sync(0xffffffffu, upto[0], 31);
+        W = W_r + __shfl_sync(0xffffffffu, upto[1], 31);
+        const Share sh = share_of(W);
+        kind = sh.lo >= W_r;
+        const long long end = kind ? W_r + upto[1] : upto[0], from = end - (kind ? v[1] : v[0]);
+        w = max(0, __ffs((int)__ballot_sync(0xffffffffu, from <= sh.lo && sh.lo < end)) - 1);
+        at = __shfl_sync(0xffffffffu, from, w);
+      } else {
+        kind = share_of(W).lo >= W_r;
+        base = bars->start_b;
+        at = bars->start_at + (kind ? W_r : 0);
+        if (base >= 0) window();
       }
       const Share sh = share_of(W);
       const int ctas = sh.ctas;
       const int64_t lo = sh.lo, hi = sh.hi;
-      if (lo < hi && !bars->stop && (B <= kWarpBatch || bars->start_b >= 0)) {
-        int kind = lo < W_r ? 0 : 1, base = 0;
-        int64_t at = kind ? W_r : 0;  // where sequence base begins
-        if (B > kWarpBatch) {
-          base = bars->start_b;
-          at += bars->start_at;
-        }
+      if (lo < hi && !bars->stop && base >= 0) {
         int64_t cur = lo;
         while (ok && cur < hi) {
-          // 32 sequences from base on
-          Sequence s{0, 0, 0};
-          if (base + lane < B) s = sequence_at(p, base + lane, false);
-          const long long v = places_of(p, s, kind == 1);
-          const int heads = kind ? p.sh.n_str : p.sh.n_ret;
-          for (int w = 0; w < 32 && ok && cur < hi; ++w) {
-            const Sequence q{__shfl_sync(0xffffffffu, s.tok0, w), __shfl_sync(0xffffffffu, s.T, w),
-                             __shfl_sync(0xffffffffu, s.n, w)};
-            const int64_t places = __shfl_sync(0xffffffffu, v, w);
-            if (places == 0) continue;
-            const HeadLine hl = head_line(p, q, kind == 1);
-            const int64_t per_head = hl.upto(hl.blocks);
-            if (cur >= at + places) {
-              at += places;
-              continue;
-            }
+          const Sequence q{__shfl_sync(0xffffffffu, s.tok0, w), __shfl_sync(0xffffffffu, s.T, w),
+                           __shfl_sync(0xffffffffu, s.n, w)};
+          const int64_t places = __shfl_sync(0xffffffffu, kind ? v[1] : v[0], w);
+          if (places > 0) {
+            const int place = kind == 0 ? kPlaceR : (q.T > (BM >> p.log2_g) ? kPlaceS : kPlaceSOne);
+            const int heads = kind ? p.sh.n_str : p.sh.n_ret;
+            const int blocks = (int)(((unsigned)q.T + (kRaggedRows >> p.log2_g) - 1u) >> (8 - p.log2_g));
+            const int64_t per_head = line_upto(p, q, kind == 1, kAllItems);
             // its first item that ends behind cur (the first one of all, but where the share begins)
             int h = 0, blk = 0;
-            int64_t begin = at;
+            int64_t head_at = at, begin = at;
             if (cur > at) {
               h = (int)divide(cur - at, per_head);
-              begin += h * per_head;
-              const int64_t y = cur - begin;
-              for (int top = hl.blocks; top - blk > 1;) {
+              head_at += h * per_head;
+#pragma unroll 1
+              for (int top = blocks; top - blk > 1;) {
                 const int mid = blk + (top - blk) / 2;
-                if (hl.upto(mid) <= y) blk = mid;
+                if (head_at + line_upto(p, q, kind == 1, mid) <= cur) blk = mid;
                 else top = mid;
               }
-              begin += hl.upto(blk);
+              begin = head_at + line_upto(p, q, kind == 1, blk);
             }
-            for (; h < heads && cur < hi; blk = blk + 1 < hl.blocks ? blk + 1 : 0, h += blk == 0) {
-              const int64_t end = begin + hl.item(blk);
+#pragma unroll 1
+            while (h < heads && cur < hi) {
+              const int64_t end = head_at + line_upto(p, q, kind == 1, blk + 1);
               Seg g;
               g.last = 0;
               g.b = base + w;
@@ -553,24 +544,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               g.kvh = kind ? p.heads.str_head[h] : p.heads.ret_head[h];
               const int total = plan_item(p, q, kind == 1, blk, &g);
               // tile j's place is begin + kPlaceItem + j place
-              const int64_t first = begin + kPlaceItem, from = begin;
+              const int64_t first = begin + kPlaceItem;
               g.j0 = 0;
               g.j1 = total;
               if (total <= kShort) {
-                if (from < lo) g.j1 = 0;  // the CTA's where it begins
+                if (begin < lo) g.j1 = 0;  // the CTA's where it begins
               } else {
                 const int64_t a = cur - first, e = min(hi, end) - first;
-                if (a > 0) g.j0 = (int)min((int64_t)total, (a + hl.place - 1) / hl.place);
-                if (hi < end) g.j1 = e > 0 ? (int)min((int64_t)total, (e + hl.place - 1) / hl.place) : 0;
+                if (a > 0) g.j0 = (int)min((int64_t)total, divide(a + place - 1, place));
+                if (hi < end) g.j1 = e > 0 ? (int)min((int64_t)total, divide(e + place - 1, place)) : 0;
               }
               cur = begin = end;
+              if (++blk == blocks) {
+                blk = 0;
+                ++h;
+                head_at = end;
+              }
               if (g.j0 >= g.j1) continue;
               g.part = -1;
               if (g.j0 > 0) {
                 g.part = 2 * blockIdx.x;
               } else if (g.j1 < total) {
                 g.part = 2 * blockIdx.x + 1;
-                job = RaggedJob{owner(W, ctas, first + (int64_t)(total - 1) * hl.place), g.tok0 + g.q0, g.rows,
+                job = RaggedJob{owner(W, ctas, first + (int64_t)(total - 1) * place), g.tok0 + g.q0, g.rows,
                                 g.kvh << p.log2_g};
               }
               const int slot = count % kSegs;
@@ -585,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               // while Q and the first tiles are on their way: do all of its blocks exist?
               bool bad = false;
               if (kind == 0 && g.j0 < g.n_cache) {
-                const int32_t* row = p.pg.table + ((int64_t)g.b * p.sh.n_ret + h) * p.pg.max_blocks;
+                const int32_t* row = p.pg.table + ((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks;
                 const int tpb = p.pg.block_size / BN, end_blk = (min(g.j1, g.n_cache) - 1) / tpb;
                 for (int i = g.j0 / tpb + lane; i <= end_blk; i += 32) {
                   const int id = row[i];
@@ -602,12 +598,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             }
             at += places;
           }
-          base += 32;
-          if (base >= B) {  // on to the streaming items (they begin at W_r), or the end
-            if (kind == 1) break;
-            kind = 1;
-            base = 0;
-            at = W_r;
+          if (++w == 32 || base + w >= B) {  // on to the next sequences, or to the streaming items (from W_r on)
+            if (base + w >= B) {
+              if (kind == 1) break;
+              kind = 1;
+              at = W_r;
+              w = 0;
+              if (base == 0) continue;
+              base = 0;
+            } else {
+              base += 32;
+              w = 0;
+            }
+            window();
           }
         }
       }

@@ -1348,6 +1348,17 @@ size_t duo_prefill_ragged_workspace_size(const duo_handle* h, int32_t num_tokens
   return h && num_tokens > 0 ? ragged_workspace_bytes(h->num_sms, ragged_rows(h, num_tokens), h->sh.D) : 0;
 }
 
+// RaggedAttnParams::window: tiles that positions i0 - R + 1 ... i0 + tb - 1 touch, by i0 modulo 128.
+static int ragged_window(int R, int tb) {
+  const int bn = kPrefillBN, shift = (R / bn + 1) * bn;  // (whole tiles, so that nothing is below 0)
+  const auto tiles = [&](int f) { return (f * tb + tb - 1 + shift) / bn - (f * tb - R + 1 + shift) / bn + 1; };
+  const int places = std::max(1, bn / tb);
+  int least = tiles(0), longer = 0;
+  for (int f = 1; f < places; ++f) least = std::min(least, tiles(f));
+  for (int f = 0; f < places; ++f) longer |= (tiles(f) - least) << f;
+  return least * 16 + longer;
+}
+
 // q, o: N tokens; map (chunks) or seq_lens (single tokens).
 static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const PagedLayout& pg, const duo_slot_map* map,
                               const int32_t* seq_lens, int64_t max_len, int N, int rows, const void* q, int64_t q_stride,
@@ -1381,6 +1392,7 @@ static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const 
   p.pos = c->pos;
   p.tokens = N;
   while ((1 << p.log2_g) < sh.g) ++p.log2_g;
+  p.window = ragged_window(sh.R, kRaggedRows / sh.g);
   p.ctas = h->num_sms;
   p.part_rows = rows;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)sh.D));

@@ -85,6 +85,10 @@ struct RaggedAttnParams {
   const int32_t* pos;    // int32 [B, S+R]
   int tokens;            // N
   int log2_g;
+  // a streaming head's window of tb + R - 1 positions, seen from a block of tb = 256 / g tokens: 16 x the
+  // tiles it touches at least, + a bit for each of the 128 / tb places in a tile a block may begin at (place
+  // 0 alone where tb is 128 or 256): one tile more
+  int window;
   int ctas;
   int part_rows;         // rows a part has room for
   float scale_log2;      // log2(e) / sqrt(D)
