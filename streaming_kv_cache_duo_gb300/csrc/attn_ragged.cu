@@ -225,7 +225,7 @@ __device__ __forceinline__ int plan_item(const RaggedAttnParams& p, const Sequen
 }
 
 // a / b for a >= 0, b > 0 (64-bit divisions take several times as long)
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+__device__ __noinline__ int64_t divide(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 // CTAs that share a line of W places, the first place of CTA c of them, and the CTA of place x.
@@ -238,7 +238,7 @@ struct Share {
   int ctas;
   int64_t lo, hi;  // of this CTA
 };
-__device__ __forceinline__ Share share_of(int64_t W) {
+__device__ __noinline__ Share share_of(int64_t W) {
   const int ctas = sharers(W), c = blockIdx.x;
   return Share{ctas, c < ctas ? bound(W, ctas, c) : W, c < ctas ? bound(W, ctas, c + 1) : W};
 }
@@ -313,6 +313,39 @@ __device__ __forceinline__ int position(const RaggedAttnParams& p, const Seg& g,
   return p.cu_new ? g.n + g.q0 + (min(row, g.rows - 1) >> p.log2_g) : g.n - 1;
 }
 
+// Bounded waits as mbar_wait and mbar_wait_warp, in fewer instructions (they are written out some forty
+// times: with those the kernel was 164 KB of code, more than an SM's instruction caches hold, and what
+// runs now and then, a segment's beginning and end, took several times as long as it should).
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, DevError err, uint32_t code) {
+  uint64_t since = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i & 255u) continue;  // (the clock is slow to read)
+    const uint64_t now = global_timer_ns();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitNs) {
+      atomicOr(err.word, code);
+      return false;
+    }
+  }
+  return true;
+}
+// By all 32 lanes together, which get one answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, DevError err, uint32_t code) {
+  uint64_t since = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i) {
+    if (i & 255u) continue;
+    const uint64_t now = global_timer_ns();
+    if (since == 0) since = now;
+    if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
+      atomicOr(err.word, code);
+      return false;
+    }
+  }
+  return true;
+}
+
 // A value that is the same in all lanes, known to be so by the compiler.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -354,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 1);
@@ -398,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   const int B = p.sh.B;
   if (B > kWarpBatch) {
     long long mine[2] = {0, 0};  // places of this thread's sequences: retrieval, streaming
+#pragma unroll 1
     for (int b = threadIdx.x; b < B; b += kThreads) {
       const Sequence s = sequence_at(p, b, blockIdx.x == 0);
       mine[0] += places_of(p, s, false);
@@ -418,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     if (sh.lo < sh.hi) {  // (the same for all threads) the sequence whose items of that kind hold place lo
       const int64_t x = streaming ? sh.lo - W_r : sh.lo;
       long long before = 0;
+#pragma unroll 1
       for (int b0 = 0; b0 < B; b0 += kThreads) {
         const int b = b0 + (int)threadIdx.x;
         long long v = 0;
@@ -570,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
                                 g.kvh << p.log2_g};
               }
               const int slot = count % kSegs;
-              if (!mbar_wait_warp(&bars->seg_empty[slot], (uint32_t)(((count / kSegs) & 1) ^ 1), err, kErrPrefillProducer)) {
+              if (!wait_warp(&bars->seg_empty[slot], (uint32_t)(((count / kSegs) & 1) ^ 1), err, kErrPrefillProducer)) {
                 ok = false;
                 break;
               }
@@ -583,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               if (kind == 0 && g.j0 < g.n_cache) {
                 const int32_t* row = p.pg.table + ((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks;
                 const int tpb = p.pg.block_size / BN, end_blk = (min(g.j1, g.n_cache) - 1) / tpb;
+#pragma unroll 1
                 for (int i = g.j0 / tpb + lane; i <= end_blk; i += 32) {
                   const int id = row[i];
                   bad |= id < 0 || id >= p.pg.num_blocks;
@@ -615,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         }
       }
       const int slot = count % kSegs;
-      if (ok && mbar_wait_warp(&bars->seg_empty[slot], (uint32_t)(((count / kSegs) & 1) ^ 1), err, kErrPrefillProducer) &&
+      if (ok && wait_warp(&bars->seg_empty[slot], (uint32_t)(((count / kSegs) & 1) ^ 1), err, kErrPrefillProducer) &&
           lane == 0) {
         bars->seg[slot].last = 1;
         mbar_arrive(&bars->seg_full[slot]);
@@ -624,9 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     } else if (warp == kWarpZero) {
       // ------------------------------------------------------------ sequences without a token: zeros
       if (!p.cu_new) {
+#pragma unroll 1
         for (int b = blockIdx.x; b < B; b += gridDim.x) {
           if (p.seq_lens[b] > 0) continue;
           uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)b * p.sh.Hq * D);
+#pragma unroll 1
           for (int e = lane; e < p.sh.Hq * D / 8; e += 32) o[e] = make_uint4(0, 0, 0, 0);
         }
       }
@@ -640,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         uint32_t used = 0, qp = 3;  // places of query tiles: used at all, and the phases of q_empty (a bit each)
         int slot = 0;               // the place of the next single query tile
         while (ok) {
-          if (!mbar_wait(in.full(), in.parity(), err, kErrPrefillProducer)) {
+          if (!wait_for(in.full(), in.parity(), err, kErrPrefillProducer)) {
             ok = false;
             break;
           }
@@ -649,9 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           const bool two = g.rows > BM;
           // a sequence's other blocks of queries read the tiles again
           const uint64_t pol_kv = (int64_t)g.T << p.log2_g > kRaggedRows ? pol_again : pol_once;
+#pragma unroll 1
           for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
             const int s = two ? x : slot;
-            if (!mbar_wait(&bars->q_empty[s], (qp >> s) & 1u, err, kErrPrefillProducer)) {
+            if (!wait_for(&bars->q_empty[s], (qp >> s) & 1u, err, kErrPrefillProducer)) {
               ok = false;
               break;
             }
@@ -669,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           const unsigned tpb = (unsigned)p.pg.block_size / BN;
           const bool paged = !g.streaming;
           int blk_next = paged && g.j0 < g.n_cache ? row[(unsigned)g.j0 / tpb] : 0;
+#pragma unroll 1
           for (int j = g.j0; j < g.j1 && ok; ++j, ++jt) {
             const Tile t = tile_at(g, j);
             int blk = blk_next, prow = 0;
@@ -692,14 +733,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
                   tma_load_3d_hint(dst + bx * kBox, ring, bx * 64, t.k * BN, g.b * p.sh.n_str + g.cidx, bar, pol_kv);
               }
             };
-            if (!mbar_wait(&bars->k_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
+            if (!wait_for(&bars->k_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
               ok = false;
               break;
             }
             load(sK + s * C::KV_BYTES, &bars->k_full[s], &p.tm_k, &p.tm_kpool, &p.tm_ksr);
-            if (!mbar_wait(&bars->v_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
+            if (!wait_for(&bars->v_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
               ok = false;
-              mbar_wait(&bars->k_full[s], ph, err, kErrPrefillProducer);  // in flight
+              wait_for(&bars->k_full[s], ph, err, kErrPrefillProducer);  // in flight
               break;
             }
             load(sV + s * C::KV_BYTES, &bars->v_full[s], &p.tm_v, &p.tm_vpool, &p.tm_vsr);
@@ -709,11 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         }
         if (!ok) {
           // after an early exit, let the copies already issued land before the CTA ends
+#pragma unroll 1
           for (int s = 0; s < 2; ++s)
-            if ((used >> s) & 1u) mbar_wait(&bars->q_full[s], (qp >> s) & 1u, err, kErrPrefillProducer);
+            if ((used >> s) & 1u) wait_for(&bars->q_full[s], (qp >> s) & 1u, err, kErrPrefillProducer);
+#pragma unroll 1
           for (int jj = (jt > kNS ? jt - kNS : 0); jj < jt; ++jj) {
-            mbar_wait(&bars->k_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
-            mbar_wait(&bars->v_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
+            wait_for(&bars->k_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
+            wait_for(&bars->v_full[jj % kNS], (uint32_t)((jj / kNS) & 1), err, kErrPrefillProducer);
           }
         }
       }
@@ -756,11 +799,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
                    (!first || kk > 0) ? 1u : 0u);
         }
       };
-      auto ready = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, err, kErrPrefillMma); };
+      auto ready = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, err, kErrPrefillMma); };
       SegReader in(bars);
       int jt = 0;                // tiles so far: tile jt is in stage jt % kNS
       uint32_t pp = 0, qp = 0;   // phases of p_full and q_full, a bit each
-      int slot = 0;
+      int slot = 0, turn = 0;    // of segments with one query tile: Q's place, and x of the next tile
       bool ok = true;
       while (ok) {
         if (!(ok = ready(in.full(), in.parity()))) break;
@@ -780,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           const int r = t == cut_c ? rows_c : rows_n, pad = 16 - (r & 15);
           if (pad < 16) {
             uint8_t* v = sV + s * C::KV_BYTES + r * 128;
+#pragma unroll 1
             for (int e = lane; e < pad * 8 * C::NBOX; e += 32)
               *reinterpret_cast<uint4*>(v + (e / (pad * 8)) * kBox + e % (pad * 8) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_shared();  // read by the tensor core next
@@ -802,6 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               tc_commit(&bars->q_empty[1]);
             }
           }
+#pragma unroll 1
           for (int t = 0; t < nt; ++t, ++jt) {
             const bool more = t + 1 < nt;
             const int s = jt % kNS, sn = (jt + 1) % kNS;
@@ -826,14 +871,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             pp ^= 3u;
           }
         } else {
-          // one query tile, even key tiles with S_0 and O_0, odd ones with S_1 and O_1
+          // one query tile; the key tiles by turns with S_0 and O_0, and with S_1 and O_1 (across segments, so
+          // that the end of one with a single tile runs beside the next one's softmax)
           const int qs = slot;
           slot ^= 1;
           ok = ready(&bars->q_full[qs], (qp >> qs) & 1u);
           qp ^= 1u << qs;
+#pragma unroll 1
           for (int t = -2; t < nt && ok; ++t) {
             // P_x V of tile t (from 0 on), then the scores of tile t + 2
-            const int x = t & 1, j = jt + t;
+            const int x = (t ^ turn) & 1, j = jt + t;
             if (t >= 0) {
               if (!(ok = v_ready(j))) break;
               const int v_rows = rows_to_use(t, j % kNS);
@@ -856,13 +903,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               }
             }
           }
+          turn ^= nt & 1;
           jt += nt;
         }
       }
       // every MMA issued here has finished before TMEM is released
       if (elect_one()) {
         tc_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0, err, kErrPrefillMma);
+        wait_for(&bars->drain, 0, err, kErrPrefillMma);
       }
     }
   } else {
@@ -875,18 +923,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     const uint32_t obase = lane_base + col_o(x);
     const float sl2 = p.scale_log2;
     SegReader in(bars);
-    // phases of the barriers waited for, a bit each (o_final[0] has one a segment)
+    // phases of the barriers waited for, a bit each
     uint32_t phase = 0;
     constexpr uint32_t kPhS = 1, kPhO0 = 2, kPhO1 = 4, kPhPair = 8;
+    int turn = 0;  // of segments with one query tile: x of the next tile
     bool ok = true;
     while (ok) {
-      if (!mbar_wait_warp(in.full(), in.parity(), err, kErrPrefillSoftmax)) break;
+      if (!wait_warp(in.full(), in.parity(), err, kErrPrefillSoftmax)) break;
       const Seg& g = in.seg();
       if (g.last) break;
-      if (!mbar_wait_warp(in.known(), in.parity(), err, kErrPrefillSoftmax)) break;
+      if (!wait_warp(in.known(), in.parity(), err, kErrPrefillSoftmax)) break;
       const bool two = uniform(g.rows) > BM;
       const int j0 = uniform(g.j0), nt = uniform(g.j1) - j0;
-      const int step = two ? 1 : 2, t0 = two ? 0 : x;  // its tiles: t0, t0 + step, ...
+      const int step = two ? 1 : 2, t0 = two ? 0 : x ^ turn;  // its tiles: t0, t0 + step, ...
       const int row = two ? x * BM + r : r;            // of the item
       const bool mine_any = row - lane < g.rows;       // (the same for the warp)
       // tiles below plain are seen whole by every row, and so are those from n_cache on below diag, the first
@@ -898,13 +947,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       float m_run = -INFINITY, l_run = 0.f;
       if (!mine_any) {
         // no rows: what its rows of S hold goes for P, and their O is not read
+#pragma unroll 1
         for (int t = t0; t < nt && ok; t += step) {
-          ok = mbar_wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax);
+          ok = wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax);
           phase ^= kPhS;
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(&bars->p_full[x]);
         }
       } else {
+#pragma unroll 1
         for (int t = t0; t < nt; t += step) {
           const int j = j0 + t;
           uint32_t masked = 0;  // 32-key chunks in which some row of the warp does not see some key
@@ -912,28 +963,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             // the masks first, while the scores are on their way; they wait in shared memory
             const Tile tl = tile_at(g, j);
             const int i_abs = position(p, g, row);
-            int jp[BN / 32];
-            if (g.streaming && tl.cache) {
-              const int32_t* held = p.pos + (int64_t)g.b * (p.sh.S + p.sh.R);
-              const int slots = min(g.n, p.sh.S + p.sh.R);
-#pragma unroll
-              for (int q4 = 0; q4 < BN / 32; ++q4) {
-                const int s = tl.k * BN + q4 * 32 + lane;
-                jp[q4] = s < slots ? held[s] : -1;
-              }
-            }
-            uint32_t vis[BN / 32];
-#pragma unroll
-            for (int q4 = 0; q4 < BN / 32; ++q4) vis[q4] = visible(p, g, tl, rows_of(g, j), q4 * 32, i_abs, jp[q4]);
+            const int32_t* held = p.pos + (int64_t)g.b * (p.sh.S + p.sh.R);
+            const int slots = min(g.n, p.sh.S + p.sh.R), keys = rows_of(g, j);
+            bool gone = false;
             if (g.bad && tl.cache) {
               const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks + tl.k / (p.pg.block_size / BN)];
-              if (id < 0 || id >= p.pg.num_blocks) vis[0] = vis[1] = vis[2] = vis[3] = 0u;
+              gone = id < 0 || id >= p.pg.num_blocks;
             }
-#pragma unroll
-            for (int q4 = 0; q4 < BN / 32; ++q4) masked |= (uint32_t)__any_sync(0xffffffffu, vis[q4] != ~0u) << q4;
-            sVis[threadIdx.x] = make_uint4(vis[0], vis[1], vis[2], vis[3]);
+            int jp = 0, jp_next = 0;
+            const auto slot_pos = [&](int q4) {
+              const int c = tl.k * BN + q4 * 32 + lane;
+              return g.streaming && tl.cache && c < slots ? held[c] : -1;
+            };
+            jp_next = slot_pos(0);
+#pragma unroll 1
+            for (int q4 = 0; q4 < BN / 32; ++q4) {
+              jp = jp_next;
+              if (q4 < 3) jp_next = slot_pos(q4 + 1);
+              const uint32_t vis = gone ? 0u : visible(p, g, tl, keys, q4 * 32, i_abs, jp);
+              masked |= (uint32_t)__any_sync(0xffffffffu, vis != ~0u) << q4;
+              reinterpret_cast<uint32_t*>(&sVis[threadIdx.x])[q4] = vis;
+            }
           }
-          if (!mbar_wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
+          if (!wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
             ok = false;
             break;
           }
@@ -1007,16 +1059,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       // ---------------------------------------------------------------- the segment's end
       const bool both = !two && nt > 1;  // two accumulators of the same rows
       const int part = g.part;
-      if (ok && mine_any && (two || both || x == 0)) {
+      if (ok && mine_any && (two || both || x == turn)) {
         // weights of the accumulators, and the dims this warp reads: all of its own, or half of both
         float f0 = 1.f, f1 = 0.f, m = m_run, l = l_run;
         if (both) {
           sML[x * BM + r] = make_float2(m_run, l_run);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->pair_ml[warp & 3]);
-          ok = mbar_wait_warp(&bars->pair_ml[warp & 3], (phase & kPhPair) != 0, err, kErrPrefillSoftmax) &&
-               mbar_wait_warp(&bars->o_final[0], (phase & kPhO0) != 0, err, kErrPrefillSoftmax) &&
-               mbar_wait_warp(&bars->o_final[1], (phase & kPhO1) != 0, err, kErrPrefillSoftmax);
+          ok = wait_warp(&bars->pair_ml[warp & 3], (phase & kPhPair) != 0, err, kErrPrefillSoftmax) &&
+               wait_warp(&bars->o_final[0], (phase & kPhO0) != 0, err, kErrPrefillSoftmax) &&
+               wait_warp(&bars->o_final[1], (phase & kPhO1) != 0, err, kErrPrefillSoftmax);
           if (ok) {
             const float2 a = sML[r], b = sML[BM + r];
             m = fmaxf(a.x, b.x);
@@ -1025,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             l = f0 * a.y + f1 * b.y;
           }
         } else {
-          ok = mbar_wait_warp(&bars->o_final[x], (phase & (x ? kPhO1 : kPhO0)) != 0, err, kErrPrefillSoftmax);
+          ok = wait_warp(&bars->o_final[x], (phase & (x ? kPhO1 : kPhO0)) != 0, err, kErrPrefillSoftmax);
         }
         if (ok) {
           tc_fence_after();
@@ -1092,13 +1144,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->pair_done[warp & 3]);
-            ok = mbar_wait_warp(&bars->pair_done[warp & 3], (phase & kPhPair) != 0, err, kErrPrefillSoftmax);
+            ok = wait_warp(&bars->pair_done[warp & 3], (phase & kPhPair) != 0, err, kErrPrefillSoftmax);
             phase ^= kPhPair;
           }
         }
       }
-      phase ^= kPhO0;
-      if (two || both) phase ^= kPhO1;
+      phase ^= two || both ? kPhO0 | kPhO1 : (turn ? kPhO1 : kPhO0);
+      if (!two) turn ^= nt & 1;
       __syncwarp();
       if (lane == 0) in.done();
       ++in.count;
