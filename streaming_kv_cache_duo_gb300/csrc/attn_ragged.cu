@@ -60,12 +60,6 @@ constexpr int kSegs = 4;         // descriptors in flight
 constexpr int kWarpBatch = 32;   // sequences that the line's warp sums alone
 constexpr int kSegUsers = 10;    // producer, MMA, eight softmax warps
 
-// Places on the line: a retrieval tile's, a streaming one's (all of its tiles are masked), and an item's
-// own. A CTA's share has kLeast at least; an item of up to kShort tiles is not shared.
-// (Measured, in units of 0.7 us: two query tiles, 2.0 to 2.1 a retrieval tile, 21.5 a streaming item of five
-// tiles; one, 1.9 a retrieval tile from HBM, 10.5 a streaming item of three.)
-constexpr int kPlaceR = 2, kPlaceS = 3, kPlaceSOne = 2, kPlaceItem = 5, kLeast = kRaggedLeast, kShort = kRaggedShort;
-
 __host__ __device__ constexpr uint32_t col_s(int x) { return (uint32_t)x * 256u; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return (uint32_t)x * 256u + 128u; }
 
@@ -152,14 +146,13 @@ __device__ __forceinline__ int tiles_of(int64_t rows) { return (int)((rows + BN 
 // for block k of tb tokens; a streaming head's, from the first block on whose every query is past the
 // ring but for the sinks, tiles of sinks and of a window (p.window). Out of line, and with few instructions:
 // when a CTA begins, none of them is in its SM's cache, and each costs some 30 cycles the first time.
-__device__ __noinline__ long long line_upto(int T, int n, bool streaming, int m, int log2_g, bool chunks, int S, int R,
-                                            int window) {
+__device__ __noinline__ long long line_upto(int T, int n, bool streaming, int m, int place, int item, int log2_g,
+                                            bool chunks, int S, int R, int window) {
   const int shift = 8 - log2_g;  // tb = 2^shift
   const int blocks = (int)(((unsigned)T + (1u << shift) - 1u) >> shift);
   m = min(m, blocks);
-  int place = kPlaceR, held = n, whole = blocks;  // blocks that see the cache whole
+  int held = n, whole = blocks;  // blocks that see the cache whole
   if (streaming) {
-    place = T > (BM >> log2_g) ? kPlaceS : kPlaceSOne;
     held = min(n, S + R);
     if (chunks) whole = min(blocks, (R - 1 + (1 << shift) - 1) >> shift);
   }
@@ -180,10 +173,16 @@ __device__ __noinline__ long long line_upto(int T, int n, bool streaming, int m,
     const auto ones = [&](unsigned k) { return (int)((k >> l) * __popc(longer) + __popc(longer & ((1u << (k & in)) - 1u))); };
     tiles += (long long)(m - e) * (sinks + (window >> 4)) + ones(m) - ones(e);
   }
-  return (long long)m * kPlaceItem + place * tiles;
+  return (long long)m * item + place * tiles;
+}
+// Places of a tile.
+__device__ __forceinline__ int place_of(const RaggedAttnParams& p, int T, bool streaming) {
+  const bool two = T > (BM >> p.log2_g);
+  return streaming ? (two ? p.places.stream_two : p.places.stream_one) : (two ? p.places.two : p.places.one);
 }
 __device__ __forceinline__ long long line_upto(const RaggedAttnParams& p, const Sequence& s, bool streaming, int m) {
-  return line_upto(s.T, s.n, streaming, m, p.log2_g, p.cu_new != nullptr, p.sh.S, p.sh.R, p.window);
+  return line_upto(s.T, s.n, streaming, m, place_of(p, s.T, streaming), p.places.item, p.log2_g, p.cu_new != nullptr,
+                   p.sh.S, p.sh.R, p.window);
 }
 constexpr int kAllItems = 0x7fffffff;
 // Places of all items of a sequence's heads of one kind.
@@ -230,7 +229,7 @@ __device__ __noinline__ int64_t divide(int64_t a, int64_t b) {
 }
 // CTAs that share a line of W places, the first place of CTA c of them, and the CTA of place x.
 __device__ __forceinline__ int sharers(int64_t W) {
-  return (int)min((int64_t)gridDim.x, max((int64_t)1, divide(W, kLeast)));
+  return (int)min((int64_t)gridDim.x, max((int64_t)1, divide(W, kRaggedLeast)));
 }
 __device__ __forceinline__ int64_t bound(int64_t W, int ctas, int c) { return divide(c * W, ctas); }
 __device__ __forceinline__ int owner(int64_t W, int ctas, int64_t x) { return (int)divide((x + 1) * ctas + W - 1, W) - 1; }
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
                            __shfl_sync(0xffffffffu, s.n, w)};
           const int64_t places = __shfl_sync(0xffffffffu, kind ? v[1] : v[0], w);
           if (places > 0) {
-            const int place = kind == 0 ? kPlaceR : (q.T > (BM >> p.log2_g) ? kPlaceS : kPlaceSOne);
+            const int place = place_of(p, q.T, kind == 1);
             const int heads = kind ? p.sh.n_str : p.sh.n_ret;
             const int blocks = (int)(((unsigned)q.T + (kRaggedRows >> p.log2_g) - 1u) >> (8 - p.log2_g));
             const int64_t per_head = line_upto(p, q, kind == 1, kAllItems);
@@ -579,11 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               g.streaming = kind;
               g.kvh = kind ? p.heads.str_head[h] : p.heads.ret_head[h];
               const int total = plan_item(p, q, kind == 1, blk, &g);
-              // tile j's place is begin + kPlaceItem + j place
-              const int64_t first = begin + kPlaceItem;
+              // tile j's place is begin + item + j place
+              const int64_t first = begin + p.places.item;
               g.j0 = 0;
               g.j1 = total;
-              if (total <= kShort) {
+              if (total <= kRaggedShort) {
                 if (begin < lo) g.j1 = 0;  // the CTA's where it begins
               } else {
                 const int64_t a = cur - first, e = min(hi, end) - first;

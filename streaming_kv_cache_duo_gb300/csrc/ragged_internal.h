@@ -53,7 +53,12 @@ cudaError_t append_ragged_read_clear_error(uint32_t* code);
 
 // ------------------------------------------------------------------ attention
 constexpr int kRaggedRows = 256;  // packed query rows (token x head of a KV head) of an item at most
-constexpr int kRaggedLeast = 6;   // places of a CTA's share at least
+// Places on the line of work (attn_ragged.cu), of some 0.2 us each: a retrieval tile's with two query tiles and
+// with one, a streaming tile's (all of them are masked) likewise, and an item's own.
+struct RaggedPlaces {
+  int two, one, stream_two, stream_one, item;
+};
+constexpr int kRaggedLeast = 24;  // places of a CTA's share at least
 constexpr int kRaggedShort = 4;   // tiles of an item that is not shared at most
 
 // An item whose key tiles several CTAs share, noted by the CTA that begins it (last < 0: it begins none):
@@ -89,6 +94,7 @@ struct RaggedAttnParams {
   // tiles it touches at least, + a bit for each of the 128 / tb places in a tile a block may begin at (place
   // 0 alone where tb is 128 or 256): one tile more
   int window;
+  RaggedPlaces places;
   int ctas;
   int part_rows;         // rows a part has room for
   float scale_log2;      // log2(e) / sqrt(D)
