@@ -258,8 +258,10 @@ class DuoPagedLayer(DuoLayer):
                                           stream)
         return out
 
-    def append_varlen(self, *args, **kwargs):
-        raise NotImplementedError("paged caches: append_ragged takes lengths from the device")
+    def append_varlen(self, k_new, v_new, seq_lens, stream=None) -> None:
+        if self.n_ret or self.stream_table is not None:
+            raise NotImplementedError("paged caches: append_ragged takes lengths from the device")
+        super().append_varlen(k_new, v_new, seq_lens, stream)  # rings alone
 
     def _check_packed(self, slot_map, N, planes):
         if slot_map.index != self.index:

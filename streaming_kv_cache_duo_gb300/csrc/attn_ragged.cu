@@ -20,24 +20,43 @@
 //
 // One CTA, 12 warps (setmaxnreg moves registers from the third warpgroup to the two softmax ones):
 //   warp 11     walks the CTA's share of the line, and hands descriptors of its segments (an item's tiles
-//               or some of them) to the others through a ring of two
+//               or some of them) to the others through a ring of four
 //   warp 8      TMA producer: Q, then K and V tiles (128-byte swizzle) into rings of kNS stages, running
 //               ahead over segments' ends
-//   warp 9      one thread issues tcgen05.mma
-//   warp 10     zeroes rows of a V tile that no token of the sequence owns (below)
+//   warp 9      MMA: the whole warp follows the tiles, one elected lane issues tcgen05.mma
+//   warp 10     writes zeros for single-token sequences that hold nothing
 //   warps 0-3, 4-7  softmax: thread r has query row r (TMEM lane r), with its running maximum and sum
 // Segments of more than 128 rows have two query tiles, one a softmax warpgroup, and every K/V tile serves
 // both: S0(j), S1(j), PV0(j), S0(j+1), PV1(j), S1(j+1), ... Shorter ones (decodes, short chunks) have
-// one query tile and the two warpgroups take the even and the odd key tiles, each with its own
-// output accumulator, so that one's softmax runs beside the other's products all the same; at the end the
+// one query tile and the two warpgroups take the key tiles by turns, each with its own output
+// accumulator, so that one's softmax runs beside the other's products all the same; at the end the
 // warpgroups read both accumulators (same TMEM lanes), half of the dims each, and merge them. A decode
 // uses few of the 128 rows: a tile's products take 0.7 us of the tensor core, its 64 KB 1.5 us of an SM's
 // share of HBM, so wasted rows cost nothing that bounds it, and warps without rows do no softmax.
 //
 // What lies behind a sequence's last row in a tile (another sequence's tokens, padding, rows of a block
 // never written) may be anything. Scores there are masked by selection; for V, zero times an infinity or
-// NaN would not do, so the product stops after the 16 rows that hold the last one, and warp 10
+// NaN would not do, so the product stops after the 16 rows that hold the last one, and the MMA warp
 // writes zeros over what is left of those. A block id outside the pool: its rows are left out.
+//
+// P is rounded to bf16 (its sum is of the unrounded values, in fp32), as the matrix unit takes operands of
+// one type and V is bf16: that is what parts the outputs (0.0021 to 0.0023 of their norm from 64 bits) from
+// those of a product in fp32, rounded once (0.0017). Scores, maxima, sums and outputs are fp32.
+//
+// Measured (graphs replayed one by one, MEASURED peaks 6.77 TB/s and 1904 TFLOP/s):
+//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1320 us, 1650 TFLOP/s (the uniform prefill 1380);
+//     D = 64: 1026 us (the uniform prefill 1166), where the exponentials bind. All streaming: 185 us.
+//   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 390 us
+//   one sequence of 1048576 tokens, one token: 167 us, 6.4 TB/s; 48 of up to 32000: 122 us, the floor of
+//     their bytes
+//   128 short ones, D = 64: 79 us where their bytes take 30: each item is Q, a few tiles and an end, one
+//     after the other. Two sequences of a few blocks: 10 us, of which 5 go by before the first segment is
+//     known and 3 at its end, most of it first reads of the instructions.
+// Of the ways tried: one thread that issues, with counters and descriptors of its own, 1712 us for the
+// first case (they were carried to uniform registers one by one); two issuing warps, one a query tile, 1828
+// (the softmaxes fall into phase); chunks of scores masked and summed in a rolled loop, and dead chunks
+// skipped, 1415 (spills); streaming items shared out over all CTAs beside the retrieval ones 80 -> 65 us for
+// the 128 short decodes, but 121 -> 125 for the 48 long ones, as every CTA then begins twice.
 #include <atomic>
 
 #include "duo_device.cuh"
@@ -491,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   tc_fence_after();
 
   if (warp >= 8) {
-    // ================================================ warpgroup 2: TMA, MMA, tails, the line
+    // ================================================ warpgroup 2: TMA, MMA, zeros, the line
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
     if (warp == kWarpLine) {
       // ------------------------------------------------------------ segments

@@ -1210,17 +1210,19 @@ static int rope_chunk(int tokens, int sms) { return std::max(1, std::min(tokens 
 
 duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns) {
   if (!inv_freq || !turns || count < 0) return fail(DUO_ERR_INVALID_ARG, "rope: NULL array or count < 0");
-  // f / 2 pi as a sum of two doubles (1 / 2 pi in two), its whole turns left out, then times 2^64
+  // |f| / 2 pi as a sum of two doubles (1 / 2 pi in two), its whole turns left out (exact for a number that is
+  // not negative), then times 2^64; of a negative f the opposite
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57, kWord = 4294967296.0;
   for (int32_t i = 0; i < count; ++i) {
     if (!std::isfinite(inv_freq[i])) return fail(DUO_ERR_INVALID_ARG, "rope: frequency %d is not finite", i);
   }
   for (int32_t i = 0; i < count; ++i) {
-    const double f = inv_freq[i], t = f * kHi;
+    const double f = std::fabs(inv_freq[i]), t = f * kHi;
     const double rest = std::fma(f, kHi, -t) + f * kLo;
     const double x = (t - std::floor(t)) * kWord, whole = std::floor(x);
     const double low = std::rint((x - whole) * kWord + rest * kWord * kWord);  // |.| < 2^54
-    turns[i] = ((uint64_t)whole << 32) + (uint64_t)(int64_t)low;
+    const uint64_t word = ((uint64_t)whole << 32) + (uint64_t)(int64_t)low;
+    turns[i] = inv_freq[i] < 0 ? 0 - word : word;
   }
   return ok();
 }
@@ -1553,7 +1555,7 @@ duo_status duo_device_error(uint32_t* code) {
   *code = a | b | t | ap | bt;
   constexpr uint32_t kFull = kErrAppendCapacity | kErrPoolFull, kBad = kErrBadBlock | kErrBadLength;
   if ((*code & kErrBadLength) && !(*code & ~(kFull | kBad)))
-    return fail(DUO_ERR_INVALID_ARG, "block tables: a length or count is out of range (code 0x%x)", *code);
+    return fail(DUO_ERR_INVALID_ARG, "block tables or a packed batch: a length or count is out of range (code 0x%x)", *code);
   if ((*code & kErrBadBlock) && !(*code & ~(kFull | kBad)))
     return fail(DUO_ERR_INVALID_ARG, "a block table held an id outside [0, num_blocks) (code 0x%x)", *code);
   if (bt && !(a | b | t | ap))
