@@ -32,7 +32,9 @@
 // accumulator, so that one's softmax runs beside the other's products all the same; at the end the
 // warpgroups read both accumulators (same TMEM lanes), half of the dims each, and merge them. A decode
 // uses few of the 128 rows: a tile's products take 0.7 us of the tensor core, its 64 KB 1.5 us of an SM's
-// share of HBM, so wasted rows cost nothing that bounds it, and warps without rows do no softmax.
+// share of HBM, so wasted rows cost nothing that bounds it. What does is the way from a tile's scores to
+// its P, as V's stage waits for it: up to eight rows are loaded once for each warp, which takes 32 of a tile's
+// 128 keys (a million tokens 167.3 -> 164.4 us, 128 short sequences of 64-dim heads 78 -> 64).
 //
 // What lies behind a sequence's last row in a tile (another sequence's tokens, padding, rows of a block
 // never written) may be anything. Scores there are masked by selection; for V, zero times an infinity or
@@ -40,18 +42,20 @@
 // writes zeros over what is left of those. A block id outside the pool: its rows are left out.
 //
 // P is rounded to bf16 (its sum is of the unrounded values, in fp32), as the matrix unit takes operands of
-// one type and V is bf16: that is what parts the outputs (0.0021 to 0.0023 of their norm from 64 bits) from
-// those of a product in fp32, rounded once (0.0017). Scores, maxima, sums and outputs are fp32.
+// one type and V is bf16: that is what parts the outputs of chunks (0.0021 to 0.0023 of their norm from
+// 64 bits) from those of a product in fp32, rounded once (0.0017). A second term would make the products
+// 1.5 times as many. With up to eight rows it costs nothing, being other rows of the same product, and single
+// tokens are as exact as a product in fp32. Scores, maxima, sums and outputs are fp32.
 //
-// Measured (graphs replayed one by one, MEASURED peaks 6.77 TB/s and 1904 TFLOP/s):
-//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1320 us, 1650 TFLOP/s (the uniform prefill 1380);
-//     D = 64: 1026 us (the uniform prefill 1166), where the exponentials bind. All streaming: 185 us.
-//   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 390 us
-//   one sequence of 1048576 tokens, one token: 167 us, 6.4 TB/s; 48 of up to 32000: 122 us, the floor of
+// Measured (graphs replayed one by one; measured peaks 6.77 TB/s and 1904 TFLOP/s):
+//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1315 us, 1660 TFLOP/s (the uniform prefill 1380);
+//     D = 64: 1020 us (the uniform prefill 1166), where the exponentials bind. All streaming: 184 us.
+//   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 382 us
+//   one sequence of 1048576 tokens, one token: 164 us, 6.5 TB/s; 48 of up to 32000: 118 us, the floor of
 //     their bytes
-//   128 short ones, D = 64: 79 us where their bytes take 30: each item is Q, a few tiles and an end, one
-//     after the other. Two sequences of a few blocks: 10 us, of which 5 go by before the first segment is
-//     known and 3 at its end, most of it first reads of the instructions.
+//   128 short ones, D = 64: 64 us where their bytes take 30: each item is Q, a few tiles and an end, one
+//     after the other. Two sequences of a few blocks: 9.5 us, of which 5 go by before the first segment is
+//     known, most of it first reads of the instructions.
 // Of the ways tried: one thread that issues, with counters and descriptors of its own, 1712 us for the
 // first case (they were carried to uniform registers one by one); two issuing warps, one a query tile, 1828
 // (the softmaxes fall into phase); chunks of scores masked and summed in a rolled loop, and dead chunks
@@ -77,6 +81,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kBox = 128 * 128;  // bytes of a 128-row x 64-column bf16 box
 constexpr int kSegs = 4;         // descriptors in flight
 constexpr int kWarpBatch = 32;   // sequences that the line's warp sums alone
+constexpr int kFew = 8;          // rows of a segment whose tiles the four warps of a warpgroup share at most
 constexpr int kSegUsers = 10;    // producer, MMA, eight softmax warps
 
 __host__ __device__ constexpr uint32_t col_s(int x) { return (uint32_t)x * 256u; }
@@ -93,7 +98,9 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + kNS * KV_BYTES;
   static constexpr int OFF_ML = OFF_V + kNS * KV_BYTES;  // float2 [2][BM]
   static constexpr int OFF_VIS = OFF_ML + 2 * BM * 8;  // uint4 per softmax thread
-  static constexpr int OFF_BAR = OFF_VIS + 2 * BM * 16;
+  static constexpr int PITCH = D / 2 + 4;  // floats from a row to the next (16 bytes on in the banks)
+  static constexpr int OFF_SUM = OFF_VIS + 2 * BM * 16;  // float [2][4 warps][kFew][PITCH]
+  static constexpr int OFF_BAR = OFF_SUM + 2 * 4 * kFew * PITCH * 4;
   static constexpr size_t SMEM = (size_t)OFF_BAR + 1024 + 1024;  // + alignment slack
 };
 
@@ -117,6 +124,7 @@ struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2], o_final[2];
   uint64_t pair_ml[4], pair_done[4];
+  uint64_t meet_both, meet_one[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs], seg_known[kSegs];
   uint64_t drain;
   uint32_t tmem_base;
@@ -194,13 +202,17 @@ __device__ __noinline__ long long line_upto(int T, int n, bool streaming, int m,
   }
   return (long long)m * item + place * tiles;
 }
-// Places of a tile.
+// Places of a tile, and of an item apart from its tiles.
+__device__ __forceinline__ bool two_query_tiles(const RaggedAttnParams& p, int T) { return T > (BM >> p.log2_g); }
+__device__ __forceinline__ int item_of(const RaggedAttnParams& p, int T) {
+  return two_query_tiles(p, T) ? p.places.item_two : p.places.item_one;
+}
 __device__ __forceinline__ int place_of(const RaggedAttnParams& p, int T, bool streaming) {
-  const bool two = T > (BM >> p.log2_g);
+  const bool two = two_query_tiles(p, T);
   return streaming ? (two ? p.places.stream_two : p.places.stream_one) : (two ? p.places.two : p.places.one);
 }
 __device__ __forceinline__ long long line_upto(const RaggedAttnParams& p, const Sequence& s, bool streaming, int m) {
-  return line_upto(s.T, s.n, streaming, m, place_of(p, s.T, streaming), p.places.item, p.log2_g, p.cu_new != nullptr,
+  return line_upto(s.T, s.n, streaming, m, place_of(p, s.T, streaming), item_of(p, s.T), p.log2_g, p.cu_new != nullptr,
                    p.sh.S, p.sh.R, p.window);
 }
 constexpr int kAllItems = 0x7fffffff;
@@ -398,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   uint8_t* sV = smem + C::OFF_V;
   float2* sML = reinterpret_cast<float2*>(smem + C::OFF_ML);
   uint4* sVis = reinterpret_cast<uint4*>(smem + C::OFF_VIS);
+  float* sSum = reinterpret_cast<float*>(smem + C::OFF_SUM);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
 
   const DevError err{&g_attn_ragged_err};
@@ -412,7 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_final[s], 1);
+      mbar_init(&bars->meet_one[s], 4);
     }
+    mbar_init(&bars->meet_both, 8);
     for (int s = 0; s < kNS; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
               g.kvh = kind ? p.heads.str_head[h] : p.heads.ret_head[h];
               const int total = plan_item(p, q, kind == 1, blk, &g);
               // tile j's place is begin + item + j place
-              const int64_t first = begin + p.places.item;
+              const int64_t first = begin + item_of(p, q.T);
               g.j0 = 0;
               g.j1 = total;
               if (total <= kRaggedShort) {
@@ -715,12 +730,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             }
             qp ^= 1u << s;
             used |= 1u << s;
-            const bool few = g.rows <= 8;
-            mbar_arrive_expect_tx(&bars->q_full[s], few ? C::NBOX * 1024 : C::Q_BYTES);
+            // a few rows: eight times, as rows 0-7 and 8-15 of each warp's 32
+            const bool few = g.rows <= kFew;
+            const int head = g.kvh << p.log2_g, tok = g.tok0 + g.q0 + x * (BM >> p.log2_g);
+            mbar_arrive_expect_tx(&bars->q_full[s], few ? C::NBOX * 8 * 1024 : C::Q_BYTES);
 #pragma unroll
-            for (int bx = 0; bx < C::NBOX; ++bx)
-              tma_load_3d(sQ + s * C::Q_BYTES + bx * kBox, few ? &p.tm_q8 : &p.tm_q, bx * 64, g.kvh << p.log2_g,
-                          g.tok0 + g.q0 + x * (BM >> p.log2_g), &bars->q_full[s]);
+            for (int bx = 0; bx < C::NBOX; ++bx) {
+              uint8_t* dst = sQ + s * C::Q_BYTES + bx * kBox;
+              if (!few) tma_load_3d(dst, &p.tm_q, bx * 64, head, tok, &bars->q_full[s]);
+#pragma unroll 1
+              for (int c = 0; few && c < 8; ++c)
+                tma_load_3d(dst + (c >> 1) * 4096 + (c & 1) * 1024, &p.tm_q8, bx * 64, head, tok, &bars->q_full[s]);
+            }
           }
           if (!two) slot ^= 1;
           const int32_t* row = p.pg.table + ((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks;
@@ -738,18 +759,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             }
             const int s = jt % kNS;
             const uint32_t ph = (uint32_t)((jt / kNS) & 1);
+            // (row and plane of the tile in whichever tensor it is in)
+            const int c1 = !t.cache ? g.kvh : (paged ? prow : t.k * BN);
+            const int c2 = !t.cache ? g.tok0 + t.k * BN : (paged ? blk : g.b * p.sh.n_str + g.cidx);
             auto load = [&](uint8_t* dst, uint64_t* bar, const CUtensorMap* fresh, const CUtensorMap* pool,
                             const CUtensorMap* ring) {
+              const CUtensorMap* map = !t.cache ? fresh : (paged ? pool : ring);
               mbar_arrive_expect_tx(bar, C::KV_BYTES);
 #pragma unroll
-              for (int bx = 0; bx < C::NBOX; ++bx) {
-                if (!t.cache)
-                  tma_load_3d_hint(dst + bx * kBox, fresh, bx * 64, g.kvh, g.tok0 + t.k * BN, bar, pol_kv);
-                else if (paged)
-                  tma_load_3d_hint(dst + bx * kBox, pool, bx * 64, prow, blk, bar, pol_kv);
-                else
-                  tma_load_3d_hint(dst + bx * kBox, ring, bx * 64, t.k * BN, g.b * p.sh.n_str + g.cidx, bar, pol_kv);
-              }
+              for (int bx = 0; bx < C::NBOX; ++bx) tma_load_3d_hint(dst + bx * kBox, map, bx * 64, c1, c2, bar, pol_kv);
             };
             if (!wait_for(&bars->k_empty[s], ph ^ 1u, err, kErrPrefillProducer)) {
               ok = false;
@@ -943,7 +961,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     SegReader in(bars);
     // phases of the barriers waited for, a bit each
     uint32_t phase = 0;
-    constexpr uint32_t kPhS = 1, kPhO0 = 2, kPhO1 = 4, kPhPair = 8;
+    constexpr uint32_t kPhS = 1, kPhO0 = 2, kPhO1 = 4, kPhPair = 8, kPhBoth = 16, kPhOne = 32;
+    // the warps of both warpgroups, or of this one, wait for one another
+    auto meet = [&](bool both) {
+      const uint32_t bit = both ? kPhBoth : kPhOne;
+      uint64_t* bar = both ? &bars->meet_both : &bars->meet_one[x];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      const bool met = wait_warp(bar, (phase & bit) != 0, err, kErrPrefillSoftmax);
+      phase ^= bit;
+      return met;
+    };
     int turn = 0;  // of segments with one query tile: x of the next tile
     bool ok = true;
     while (ok) {
@@ -963,7 +991,96 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       const int plain = uniform(g.streaming || g.bad ? 0 : (g.cut_cache >= 0 ? n_cache - 1 : n_cache));
       const int diag = uniform(g.streaming ? 0 : n_cache + (g.q0 + ((two ? x * BM : 0) >> p.log2_g)) / BN);
       float m_run = -INFINITY, l_run = 0.f;
-      if (!mine_any) {
+      const bool few = uniform(g.rows) <= kFew;
+      if (few) {
+        // A few rows (single tokens): they stand in each warp's lanes 0-7 and again in 8-15. A warp takes 32 of
+        // a tile's keys, with a maximum and a sum of its own, and leaves zeros for the others' keys in its rows
+        // of P; lanes 8-15 write what the bf16 of lanes 0-7 leaves of P. The rows of O are added up at the
+        // segment's end.
+        const int w = warp & 3;
+#pragma unroll 1
+        for (int t = t0; t < nt; t += 2) {
+          const int j = j0 + t;
+          uint32_t vis = ~0u;
+          if (j >= plain && (j < n_cache || j >= diag)) {
+            const Tile tl = tile_at(g, j);
+            bool gone = false;
+            if (g.bad && tl.cache) {
+              const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks + tl.k / (p.pg.block_size / BN)];
+              gone = id < 0 || id >= p.pg.num_blocks;
+            }
+            const int c = tl.k * BN + w * 32 + lane;
+            const bool slot = g.streaming && tl.cache && c < min(g.n, p.sh.S + p.sh.R);
+            const int jp = slot ? p.pos[(int64_t)g.b * (p.sh.S + p.sh.R) + c] : -1;
+            vis = gone ? 0u : visible(p, g, tl, rows_of(g, j), w * 32, position(p, g, lane & 7), jp);
+          }
+          const bool masked = __any_sync(0xffffffffu, vis != ~0u);
+          if (!wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
+            ok = false;
+            break;
+          }
+          phase ^= kPhS;
+          tc_fence_after();
+          float v[32];
+          {
+            uint32_t raw[32];
+            tmem_ld32_sync(sbase + w * 32, raw);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
+            const uint32_t none[16] = {};
+#pragma unroll
+            for (int i = 1; i < 4; ++i) tmem_st16(sbase + ((w + i) & 3) * 16, none);
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((vis >> e) & 1u)) v[e] = -INFINITY;
+          }
+          float mx = v[0], mx2 = v[1];
+#pragma unroll
+          for (int e = 2; e < 32; e += 4) {
+            mx = max3(mx, v[e], v[e + 1]);
+            if (e + 3 < 32) mx2 = max3(mx2, v[e + 2], v[e + 3]);
+          }
+          mx = fmaxf(mx, mx2) * sl2;
+          float f = 1.f;
+          if (mx > m_run + 8.f) {
+            f = ex2_approx(m_run - mx);
+            l_run *= f;
+            m_run = mx;
+          }
+          if (__any_sync(0xffffffffu, lane < kFew && f != 1.f && t > t0)) {
+#pragma unroll 1
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              uint32_t ov[32];
+              tmem_ld32_sync(obase + q4 * 32, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+              tmem_st32(obase + q4 * 32, ov);
+            }
+          }
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          const float2 sl2x2 = make_float2(sl2, sl2), negm2 = make_float2(-m_use, -m_use);
+          const float less = lane & kFew ? -1.f : 0.f;
+          float2 ls = make_float2(0.f, 0.f);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = __ffma2_rn(make_float2(v[2 * e], v[2 * e + 1]), sl2x2, negm2);
+            const float2 pe = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            ls = __fadd2_rn(ls, pe);
+            const uint32_t hi = pack_bf16x2(pe.x, pe.y);
+            const float2 rest = __ffma2_rn(make_float2(bf16lo(hi), bf16hi(hi)), make_float2(less, less), pe);
+            pk[e] = pack_bf16x2(rest.x, rest.y);
+          }
+          l_run += ls.x + ls.y;
+          tmem_st16(sbase + w * 16, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[x]);
+        }
+      } else if (!mine_any) {
         // no rows: what its rows of S hold goes for P, and their O is not read
 #pragma unroll 1
         for (int t = t0; t < nt && ok; t += step) {
@@ -1077,7 +1194,77 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       // ---------------------------------------------------------------- the segment's end
       const bool both = !two && nt > 1;  // two accumulators of the same rows
       const int part = g.part;
-      if (ok && mine_any && (two || both || x == turn)) {
+      if (few && ok && (both || x == turn)) {
+        // row r: the sum over the warps (and the accumulators), half of the dims at a time (two accumulators: a
+        // half by either warpgroup)
+        const int w = warp & 3;
+        if (lane < kFew) sML[x * BM + w * 32 + lane] = make_float2(m_run, l_run);
+        ok = meet(both) && (!(both || x == 0) || wait_warp(&bars->o_final[0], (phase & kPhO0) != 0, err, kErrPrefillSoftmax)) &&
+             (!(both || x == 1) || wait_warp(&bars->o_final[1], (phase & kPhO1) != 0, err, kErrPrefillSoftmax));
+        if (ok) {
+          tc_fence_after();
+          // (lane: the parts of warp lane / 8)
+          const float2 none = make_float2(-INFINITY, 0.f), *mls = sML + (lane & 7) + (lane >> 3) * 32;
+          const float2 a0 = both || x == 0 ? mls[0] : none, a1 = both || x == 1 ? mls[BM] : none;
+          float m = fmaxf(a0.x, a1.x);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          float f0 = a0.x == -INFINITY ? 0.f : ex2_approx(a0.x - m), f1 = a1.x == -INFINITY ? 0.f : ex2_approx(a1.x - m);
+          float l = f0 * a0.y + f1 * a1.y;
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          const float inv = part >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);  // (no key at all: zeros)
+          f0 = __shfl_sync(0xffffffffu, f0, w * 8 + (lane & 7)) * inv;  // of this warp's own parts
+          f1 = __shfl_sync(0xffffffffu, f1, w * 8 + (lane & 7)) * inv;
+          if (part >= 0 && w == 0 && lane < g.rows && (!both || x == 0))
+            p.part_ml[(int64_t)part * p.part_rows + lane] = make_float2(m, l);
+          float* sum = sSum + (x * 4 * kFew) * C::PITCH;
+          const int unit = w * 32 + lane, urow = unit / (D / 8), vec = unit % (D / 8);
+#pragma unroll 1
+          for (int h = both ? x : 0; ok && h < (both ? x + 1 : 2); ++h) {
+#pragma unroll 1
+            for (int u = 0; u < D / 64; ++u) {
+              const uint32_t col = (uint32_t)(h * (D / 2) + u * 32);
+              float ov[32] = {};
+#pragma unroll 1
+              for (int i = both ? 0 : x; i < (both ? 2 : x + 1); ++i) {
+                uint32_t raw[32];
+                tmem_ld32_sync(lane_base + col_o(i) + col, raw);
+                const float fi = i ? f1 : f0;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = fmaf(__uint_as_float(raw[e]), fi, ov[e]);
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] += __shfl_xor_sync(0xffffffffu, ov[e], kFew);
+              if (lane < kFew) {
+                float4* to = reinterpret_cast<float4*>(sum + (w * kFew + lane) * C::PITCH + u * 32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) to[e] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              }
+            }
+            // (the accumulators have been read, too: the next segment's products may write them)
+            tc_fence_before();
+            if (!(ok = meet(both))) break;
+            if (urow < g.rows) {
+              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 a = *reinterpret_cast<const float4*>(sum + (i * kFew + urow) * C::PITCH + vec * 4);
+                o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
+              }
+              const int at4 = h * (D / 8) + vec;
+              if (part >= 0) {
+                reinterpret_cast<float4*>(p.part_o + (int64_t)part * p.part_rows * D)[(int64_t)at4 * p.part_rows + urow] = o;
+              } else {
+                const int64_t at = (int64_t)(g.tok0 + g.q0 + (urow >> p.log2_g)) * p.sh.Hq + (g.kvh << p.log2_g) +
+                                   (urow & ((1 << p.log2_g) - 1));
+                reinterpret_cast<uint2*>(p.o + at * D)[at4] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+              }
+            }
+            ok = meet(both);  // the sums have been read
+          }
+        }
+      } else if (!few && ok && mine_any && (two || both || x == turn)) {
         // weights of the accumulators, and the dims this warp reads: all of its own, or half of both
         float f0 = 1.f, f1 = 0.f, m = m_run, l = l_run;
         if (both) {

@@ -54,9 +54,9 @@ cudaError_t append_ragged_read_clear_error(uint32_t* code);
 // ------------------------------------------------------------------ attention
 constexpr int kRaggedRows = 256;  // packed query rows (token x head of a KV head) of an item at most
 // Places on the line of work (attn_ragged.cu), of some 0.2 us each: a retrieval tile's with two query tiles and
-// with one, a streaming tile's (all of them are masked) likewise, and an item's own.
+// with one, a streaming tile's (all of them are masked) likewise, and an item's own, likewise.
 struct RaggedPlaces {
-  int two, one, stream_two, stream_one, item;
+  int two, one, stream_two, stream_one, item_two, item_one;
 };
 constexpr int kRaggedLeast = 24;  // places of a CTA's share at least
 constexpr int kRaggedShort = 4;   // tiles of an item that is not shared at most

@@ -240,6 +240,31 @@ def test_one_long_sequence():
     _decode(Batch(23, [(40000, 1)], 8, 2, 1, 128, 4, 32, 256, appended=True))
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,scale", [(64, 8, 1, 1.0), (64, 1, 1, 4.0), (128, 2, 1, 4.0)])
+def test_long_sequences_shared_by_many_ctas(D, Hq, Hkv, scale):
+    _decode(Batch(27, [(9000, 1), (0, 0), (20000, 1)], Hq, Hkv, Hkv, D, 4, 32, 128, appended=True, scale=scale))
+
+
+@pytest.mark.parametrize("D,Hq", [(128, 8), (64, 4)])
+def test_single_tokens_are_off_by_their_own_rounding(D, Hq):
+    """P is a sum of two bf16 terms there, which leaves 2^-17 of it, sums are fp32: next to the outputs' rounding
+    (some 2^-9.2 of their norm) that is nothing, and an eighth more is allowed. One term would be off by
+    as much again, and the norm of both by 1.4 of the rounding's."""
+    x = Batch(28, [(3000, 1), (1500, 1)], Hq, 1, 1, D, 4, 32, 128, appended=True)
+    got = f64(_decode(x))
+    ref = np.stack([np.stack([x.expected(b, n, j)[0] for j in range(Hq)]) for b, (n, _) in enumerate(x.seqs)])
+    own = f64(torch.tensor(ref).to(torch.bfloat16)) - ref
+    assert np.linalg.norm(got - ref) < 1.125 * np.linalg.norm(own)
+
+
+@pytest.mark.parametrize("g", [1, 2, 4, 8])
+def test_short_chunks_beside_long_ones(g):
+    """Up to eight packed rows, and one more, in one call with more."""
+    few = 8 // g
+    x = Batch(29, [(700, few), (130, few + 1), (0, 300), (64, max(1, few - 1)), (1000, few)], g, 1, 1, 128, 4, 32, 128)
+    _prefill(x, pad=3)
+
+
 def test_lengths_past_max_len_are_clamped():
     """As if the caches held max_len tokens: the same outputs as those lengths give."""
     x = Batch(24, [(299, 1), (99, 1)], 4, 2, 2, 64, 4, 32, 128, appended=True)
