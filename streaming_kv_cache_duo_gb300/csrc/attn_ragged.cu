@@ -886,11 +886,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
           for (int t = 0; t < nt; ++t, ++jt) {
             const bool more = t + 1 < nt;
             const int s = jt % kNS, sn = (jt + 1) % kNS;
-            if (!(ok = v_ready(jt) && (!more || k_ready(jt + 1)))) break;
+            // A look at a barrier takes the warp 110 to 150 cycles, also when its phase is long over. D = 128, where
+            // the tensor core bounds it: at three in one go (16384 tokens 1323 -> 1287 us). D = 64, where the
+            // softmaxes do: not, as the later products keep the two of them out of phase (1012; 1114 with it).
+            bool there = false;
+            if constexpr (D == 128) {
+              const bool v = mbar_try_wait(&bars->v_full[s], (uint32_t)((jt / kNS) & 1));
+              const bool k = !more || mbar_try_wait(&bars->k_full[sn], (uint32_t)(((jt + 1) / kNS) & 1));
+              const bool p0 = mbar_try_wait(&bars->p_full[0], pp & 1u);
+              there = __all_sync(0xffffffffu, v && k && p0);
+            }
+            if (!there && !(ok = v_ready(jt) && (!more || k_ready(jt + 1)))) break;
             const int v_rows = rows_to_use(t, s);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (!ok || !(ok = ready(&bars->p_full[x], (pp >> x) & 1u))) break;
+              if (!ok || (!(x == 0 && there) && !(ok = ready(&bars->p_full[x], (pp >> x) & 1u)))) break;
               if (elect_one()) {
                 tc_fence_after();
                 issue_pv(x, s, t == 0, v_rows);
