@@ -48,8 +48,9 @@
 // tokens are as exact as a product in fp32. Scores, maxima, sums and outputs are fp32.
 //
 // Measured (graphs replayed one by one; measured peaks 6.77 TB/s and 1904 TFLOP/s):
-//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1315 us, 1660 TFLOP/s (the uniform prefill 1380);
-//     D = 64: 1020 us (the uniform prefill 1166), where the exponentials bind. All streaming: 184 us.
+//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1287 us, 1710 TFLOP/s (the uniform prefill 1380);
+//     D = 64: 1012 us (the uniform prefill 1166), where a tile's way through softmax (1240 cycles) and the
+//     MMA warp's own instructions take the time, not the products (512). All streaming: 183 us.
 //   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 382 us
 //   one sequence of 1048576 tokens, one token: 164 us, 6.5 TB/s; 48 of up to 32000: 118 us, the floor of
 //     their bytes
@@ -57,10 +58,12 @@
 //     after the other. Two sequences of a few blocks: 9.5 us, of which 5 go by before the first segment is
 //     known, most of it first reads of the instructions.
 // Of the ways tried: one thread that issues, with counters and descriptors of its own, 1712 us for the
-// first case (they were carried to uniform registers one by one); two issuing warps, one a query tile, 1828
-// (the softmaxes fall into phase); chunks of scores masked and summed in a rolled loop, and dead chunks
-// skipped, 1415 (spills); streaming items shared out over all CTAs beside the retrieval ones 80 -> 65 us for
-// the 128 short decodes, but 121 -> 125 for the 48 long ones, as every CTA then begins twice.
+// first case where the warp took 1330 (they were carried to uniform registers one by one); two issuing warps,
+// one a query tile, 1828 (the softmaxes fall into phase); chunks of scores masked and summed in a rolled loop,
+// and dead chunks skipped, 1415 (spills); one loop of steps for both kinds of segments 1470; a quarter of the
+// exponentials by a polynomial 1375, and 1130 for D = 64; a third place of scores there, so that a softmax
+// finds its next tile ready, 1071. Streaming items shared out over all CTAs beside the retrieval ones: 80 ->
+// 65 us for the 128 short decodes, but 121 -> 125 for the 48 long ones, as every CTA then begins twice.
 #include <atomic>
 
 #include "duo_device.cuh"
