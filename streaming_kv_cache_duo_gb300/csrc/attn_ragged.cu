@@ -303,8 +303,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t bits_below(int hi) {
-  return hi <= 0 ? 0u : (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u);
+__device__ __forceinline__ uint32_t bits_below(int hi) {  // (shl gives 0 for 32 and more)
+  uint32_t above;
+  asm("shl.b32 %0, %1, %2;" : "=r"(above) : "r"(0xffffffffu), "r"(max(hi, 0)));
+  return ~above;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -315,20 +317,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// Which of the 32 keys of a chunk (columns c0 ... of tile t) row i_abs sees. Where they are consecutive
-// positions, the visible ones are at most two runs (sinks, and (i - R, i]): a 32-bit mask from a few
-// shifts. Ring slots: jp is the position slot c0 + lane holds, -1 if none; most are seen by all of the
-// warp's rows or by none (rows' positions rise with the lane), the few others are compared row by row.
-__device__ __forceinline__ uint32_t visible(const RaggedAttnParams& p, const Seg& g, const Tile& t, int rows, int c0,
-                                            int i_abs, int jp) {
+// Which of the 32 keys from column c0 of a tile on a row sees, as a mask. New tokens, whose positions are
+// consecutive (column 0 is d positions before the row): at most two runs, sinks and (i - R, i], from a few
+// shifts.
+__device__ __forceinline__ uint32_t visible_new(const RaggedAttnParams& p, bool streaming, int i_abs, int d, int c0) {
+  const int sinks = streaming ? p.sh.S - (i_abs - d) : 0, out = streaming ? d - p.sh.R + 1 : 0;
+  return bits_below(d + 1 - c0) & (bits_below(sinks - c0) | ~bits_below(out - c0));
+}
+// Cached ones: of `rows` in the tile all are visible to a retrieval head. Ring slots: jp is the position slot
+// c0 + lane holds, -1 if none; most are seen by all of the warp's rows or by none (rows' positions rise with
+// the lane), the few others are compared row by row.
+__device__ __forceinline__ uint32_t visible_held(const RaggedAttnParams& p, bool streaming, int rows, int c0, int i_abs,
+                                                 int jp) {
+  if (!streaming) return bits_below(rows - c0);
   const int S = p.sh.S, R = p.sh.R;
-  if (!t.cache) {
-    const int first = g.n + t.k * BN + c0;
-    const int d0 = i_abs - first;  // column e is the key d0 - e positions back
-    const uint32_t vis = bits_below(d0 + 1);
-    return g.streaming ? vis & (bits_below(S - first) | ~bits_below(d0 - R + 1)) : vis;
-  }
-  if (!g.streaming) return bits_below(rows - c0);
   const int i0 = __shfl_sync(0xffffffffu, i_abs, 0), i1 = __shfl_sync(0xffffffffu, i_abs, 31);
   const bool all = jp >= 0 && jp <= i0 && (jp < S || i1 - jp < R);
   const bool none = jp < 0 || jp > i1 || (jp >= S && i0 - jp >= R);
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
 
   const DevError err{&g_attn_ragged_err};
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform(threadIdx.x >> 5);  // (with roles that are the warps' own, shuffles need no care: 157 -> 146 KB)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -990,13 +992,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
     while (ok) {
       if (!wait_warp(in.full(), in.parity(), err, kErrPrefillSoftmax)) break;
       const Seg& g = in.seg();
-      if (g.last) break;
+      if (uniform(g.last)) break;
       if (!wait_warp(in.known(), in.parity(), err, kErrPrefillSoftmax)) break;
       const bool two = uniform(g.rows) > BM;
       const int j0 = uniform(g.j0), nt = uniform(g.j1) - j0;
       const int step = two ? 1 : 2, t0 = two ? 0 : x ^ turn;  // its tiles: t0, t0 + step, ...
       const int row = two ? x * BM + r : r;            // of the item
-      const bool mine_any = row - lane < g.rows;       // (the same for the warp)
+      const bool mine_any = uniform(row) < uniform(g.rows);
       // tiles below plain are seen whole by every row, and so are those from n_cache on below diag, the first
       // one of the new tokens that some row of this query tile does not see whole; a streaming head's are
       // all masked, and so are those of a segment with a block that does not exist
@@ -1025,7 +1027,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             const int c = tl.k * BN + w * 32 + lane;
             const bool slot = g.streaming && tl.cache && c < min(g.n, p.sh.S + p.sh.R);
             const int jp = slot ? p.pos[(int64_t)g.b * (p.sh.S + p.sh.R) + c] : -1;
-            vis = gone ? 0u : visible(p, g, tl, rows_of(g, j), w * 32, position(p, g, lane & 7), jp);
+            const int i_abs = position(p, g, lane & 7);
+            if (!tl.cache) vis = visible_new(p, g.streaming, i_abs, i_abs - (g.n + tl.k * BN), w * 32);
+            else vis = gone ? 0u : visible_held(p, g.streaming, rows_of(g, j), w * 32, i_abs, jp);
           }
           const bool masked = __any_sync(0xffffffffu, vis != ~0u);
           if (!wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
@@ -1113,24 +1117,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             const int i_abs = position(p, g, row);
             const int32_t* held = p.pos + (int64_t)g.b * (p.sh.S + p.sh.R);
             const int slots = min(g.n, p.sh.S + p.sh.R), keys = rows_of(g, j);
-            bool gone = false;
-            if (g.bad && tl.cache) {
-              const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks + tl.k / (p.pg.block_size / BN)];
-              gone = id < 0 || id >= p.pg.num_blocks;
-            }
-            int jp = 0, jp_next = 0;
-            const auto slot_pos = [&](int q4) {
-              const int c = tl.k * BN + q4 * 32 + lane;
-              return g.streaming && tl.cache && c < slots ? held[c] : -1;
-            };
-            jp_next = slot_pos(0);
+            if (j >= n_cache) {
+              const int d = i_abs - (g.n + tl.k * BN);
+              uint32_t vis[4];
+#pragma unroll
+              for (int q4 = 0; q4 < BN / 32; ++q4) {
+                vis[q4] = visible_new(p, g.streaming, i_abs, d, q4 * 32);
+                masked |= (uint32_t)__any_sync(0xffffffffu, vis[q4] != ~0u) << q4;
+              }
+              sVis[threadIdx.x] = make_uint4(vis[0], vis[1], vis[2], vis[3]);
+            } else {
+              bool gone = false;
+              if (g.bad) {
+                const int id = p.pg.table[((int64_t)g.b * p.sh.n_ret + g.cidx) * p.pg.max_blocks + tl.k / (p.pg.block_size / BN)];
+                gone = id < 0 || id >= p.pg.num_blocks;
+              }
+              int jp = 0, jp_next = 0;
+              const auto slot_pos = [&](int q4) {
+                const int c = tl.k * BN + q4 * 32 + lane;
+                return g.streaming && c < slots ? held[c] : -1;
+              };
+              jp_next = slot_pos(0);
 #pragma unroll 1
-            for (int q4 = 0; q4 < BN / 32; ++q4) {
-              jp = jp_next;
-              if (q4 < 3) jp_next = slot_pos(q4 + 1);
-              const uint32_t vis = gone ? 0u : visible(p, g, tl, keys, q4 * 32, i_abs, jp);
-              masked |= (uint32_t)__any_sync(0xffffffffu, vis != ~0u) << q4;
-              reinterpret_cast<uint32_t*>(&sVis[threadIdx.x])[q4] = vis;
+              for (int q4 = 0; q4 < BN / 32; ++q4) {
+                jp = jp_next;
+                if (q4 < 3) jp_next = slot_pos(q4 + 1);
+                const uint32_t vis = gone ? 0u : visible_held(p, g.streaming, keys, q4 * 32, i_abs, jp);
+                masked |= (uint32_t)__any_sync(0xffffffffu, vis != ~0u) << q4;
+                reinterpret_cast<uint32_t*>(&sVis[threadIdx.x])[q4] = vis;
+              }
             }
           }
           if (!wait_warp(&bars->s_full[x], phase & kPhS, err, kErrPrefillSoftmax)) {
@@ -1206,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
       }
       // ---------------------------------------------------------------- the segment's end
       const bool both = !two && nt > 1;  // two accumulators of the same rows
-      const int part = g.part;
+      const int part = uniform(g.part);
       if (few && ok && (both || x == turn)) {
         // row r: the sum over the warps (and the accumulators), half of the dims at a time (two accumulators: a
         // half by either warpgroup)
