@@ -48,22 +48,26 @@
 // tokens are as exact as a product in fp32. Scores, maxima, sums and outputs are fp32.
 //
 // Measured (graphs replayed one by one; measured peaks 6.77 TB/s and 1904 TFLOP/s):
-//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1287 us, 1710 TFLOP/s (the uniform prefill 1380);
-//     D = 64: 1012 us (the uniform prefill 1166), where a tile's way through softmax (1240 cycles) and the
-//     MMA warp's own instructions take the time, not the products (512). All streaming: 183 us.
-//   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 382 us
-//   one sequence of 1048576 tokens, one token: 164 us, 6.5 TB/s; 48 of up to 32000: 118 us, the floor of
-//     their bytes
-//   128 short ones, D = 64: 64 us where their bytes take 30: each item is Q, a few tiles and an end, one
+//   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1270 us, 1730 TFLOP/s (the uniform prefill 1380);
+//     D = 64: 990 us (the uniform prefill 1166), where a tile's way through softmax (1240 cycles) and the
+//     MMA warp's own instructions take the time, not the products (512). All streaming: 163 us, an item of
+//     four masked tiles 12, some 3 of them its end.
+//   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 379 us
+//   one sequence of 1048576 tokens, one token: 162 to 164 us, 6.6 TB/s; 48 of up to 32000: 116 to 118 us, the
+//     floor of their bytes
+//   128 short ones, D = 64: 56 us where their bytes take 30: each item is Q, a few tiles and an end, one
 //     after the other. Two sequences of a few blocks: 9.5 us, of which 5 go by before the first segment is
 //     known, most of it first reads of the instructions.
-// Of the ways tried: one thread that issues, with counters and descriptors of its own, 1712 us for the
-// first case where the warp took 1330 (they were carried to uniform registers one by one); two issuing warps,
-// one a query tile, 1828 (the softmaxes fall into phase); chunks of scores masked and summed in a rolled loop,
-// and dead chunks skipped, 1415 (spills); one loop of steps for both kinds of segments 1470; a quarter of the
-// exponentials by a polynomial 1375, and 1130 for D = 64; a third place of scores there, so that a softmax
-// finds its next tile ready, 1071. Streaming items shared out over all CTAs beside the retrieval ones: 80 ->
-// 65 us for the 128 short decodes, but 121 -> 125 for the 48 long ones, as every CTA then begins twice.
+// Of the ways tried, with the times before and after at that point, us, for the first case unless said: one
+// thread that issues, with counters and descriptors of its own, 1330 -> 1712 (they were carried to uniform
+// registers one by one); two issuing warps, one a query tile, 1712 -> 1828 (the softmaxes fall into phase); scores
+// masked and summed in rolled loops of chunks, and dead chunks skipped, 1330 -> 1415 (spills); one loop of
+// steps for both kinds of segments 1324 -> 1470; an eighth of the exponentials by a polynomial 1345 -> 1365,
+// and 1015 -> 1067 for D = 64; four partial sums, or the exponentials in between the sums by hand, 1301 ->
+// 1320 to 1345 (spills); a third place of scores for D = 64, so that a softmax finds its next tile ready,
+// 990 -> 1045; new tokens' tiles classed as seen whole or not at all before they are masked, 183 -> 187 for
+// streaming heads. Streaming items shared out over all CTAs beside the retrieval ones: 80 -> 65 for 128 short
+// decodes, but 121 -> 125 for the 48 long ones, as every CTA then begins twice.
 #include <atomic>
 
 #include "duo_device.cuh"
@@ -893,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
             const int s = jt % kNS, sn = (jt + 1) % kNS;
             // A look at a barrier takes the warp 110 to 150 cycles, also when its phase is long over. D = 128, where
             // the tensor core bounds it: at three in one go (16384 tokens 1323 -> 1287 us). D = 64, where the
-            // softmaxes do: not, as the later products keep the two of them out of phase (1012; 1114 with it).
+            // softmaxes do: not, as the later products keep the two of them out of phase (990; 1048 with it).
             bool there = false;
             if constexpr (D == 128) {
               const bool v = mbar_try_wait(&bars->v_full[s], (uint32_t)((jt / kNS) & 1));

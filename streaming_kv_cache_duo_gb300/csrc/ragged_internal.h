@@ -53,8 +53,10 @@ cudaError_t append_ragged_read_clear_error(uint32_t* code);
 
 // ------------------------------------------------------------------ attention
 constexpr int kRaggedRows = 256;  // packed query rows (token x head of a KV head) of an item at most
-// Places on the line of work (attn_ragged.cu), of some 0.2 us each: a retrieval tile's with two query tiles and
-// with one, a streaming tile's (all of them are masked) likewise, and an item's own, likewise.
+// Places on the line of work (attn_ragged.cu), of some 0.17 us each: a retrieval tile's with two query tiles
+// and with one, a streaming tile's (most are masked) likewise, and an item's own, likewise. They only decide how
+// evenly the CTAs are loaded, and are fitted over chunks, mixed batches and decodes of either head dim. (With one
+// figure for either kind of items 32 mixed sequences took 249 us, with two 239; 4096 tokens over 28672 390 and 382.)
 struct RaggedPlaces {
   int two, one, stream_two, stream_one, item_two, item_one;
 };
