@@ -342,6 +342,34 @@ def _map_of(x, start, new):
     return m
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 1), (64, 2, 2)])
+def test_streaming_heads_at_the_last_positions(D, Hq, Hkv):
+    """Chunks and single tokens up to position 2^31 - 2: what is 32-bit does not pass its range."""
+    from streaming_kv_cache_duo_gb300 import DuoPagedLayer, duo_device_error
+    rng, S, R, before = np.random.default_rng(37), 4, 40, 60
+    for T in (9, 70, 300):
+        first = 2 ** 31 - 1 - T
+        k, v, q = (normal(rng, before + T, h, D) for h in (Hkv, Hkv, Hq))
+        layer = DuoPagedLayer(1, Hq, Hkv, D, S, R, 128, 1, 1, None, [0] * Hkv)
+        m = slot_map(None, 128, [first - before], [before])
+        layer.append_ragged(k[0][:before].cuda(), v[0][:before].cuda(), m)
+        m = slot_map(None, 128, [first], [T])
+        qc, kc, vc = (x[0][before:].cuda() for x in (q, k, v))
+        got = f64(layer.prefill_ragged(qc, kc, vc, m))
+        layer.append_ragged(kc, vc, m)
+        n = torch.tensor([2 ** 31 - 1], dtype=torch.int32, device="cuda")
+        last = f64(layer.decode_varlen(qc[-1:], n, 2 ** 31 - 1))
+        assert duo_device_error() == 0
+        for t in range(T):
+            i = before + t
+            for j in range(Hq):
+                see = slice(i - R + 1, i + 1)
+                ref, tol = attend(q[1][i, j], k[1][see, j * Hkv // Hq], v[1][see, j * Hkv // Hq])
+                check(got[t, j], ref, tol, f"chunk of {T}: {t}")
+                if t == T - 1:
+                    check(last[0, j], ref, tol, f"single token after {T}")
+
+
 def test_calls_repeat_and_streams():
     """Equal results call after call (no order of atomics in them), on another stream, into a slice of rows."""
     x = Batch(30, [(3000, 60), (0, 200), (40, 1)], 8, 2, 1, 128, 4, 32, 128)
