@@ -50,8 +50,8 @@
 // Measured (graphs replayed one by one; measured peaks 6.77 TB/s and 1904 TFLOP/s):
 //   16384 tokens, 32 heads over 8, all retrieval, D = 128: 1270 us, 1730 TFLOP/s (the uniform prefill 1380);
 //     D = 64: 990 us (the uniform prefill 1166), where a tile's way through softmax (1240 cycles) and the
-//     MMA warp's own instructions take the time, not the products (512). All streaming: 163 us, an item of
-//     four masked tiles 12, some 3 of them its end.
+//     MMA warp's own instructions take the time, not the products (512). All streaming: 151 us, an item of
+//     four masked tiles 11, some 2 of them its end.
 //   4096 tokens over 28672, MHA 32 heads, 8 of them retrieval: 379 us
 //   one sequence of 1048576 tokens, one token: 162 to 164 us, 6.6 TB/s; 48 of up to 32000: 116 to 118 us, the
 //     floor of their bytes
@@ -1319,6 +1319,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
         if (ok) {
           tc_fence_after();
           const bool store = row < g.rows;
+          // four rows whose chunks the lane stores: from `left` on behind the item; 4 divides g or g divides 4, so
+          // where they lie apart is the same for all lanes
+          const int four = row - (lane & 3), left = g.rows - four;
+          const int64_t at = (int64_t)(g.tok0 + g.q0 + (four >> p.log2_g)) * p.sh.Hq + (g.kvh << p.log2_g) +
+                             (four & ((1 << p.log2_g) - 1));
+          uint4* orow = reinterpret_cast<uint4*>(p.o + at * D) + (lane & 3);
+          int next_row[4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            next_row[a] = ((a >> p.log2_g) * p.sh.Hq + (a & ((1 << p.log2_g) - 1))) * (D / 8);
           if (part < 0) {
             const float inv = l == 0.f ? 0.f : 1.f / l;  // (no key at all: zeros)
             f0 *= inv;
@@ -1365,14 +1375,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_ragged_kernel(const __grid_c
                 }
               }
 #pragma unroll
-              for (int a = 0; a < 4; ++a) {  // chunk lane % 4 of row `to`
-                const int to = row - (lane & 3) + a;
-                if (to < g.rows) {
-                  const int64_t at = (int64_t)(g.tok0 + g.q0 + (to >> p.log2_g)) * p.sh.Hq + (g.kvh << p.log2_g) +
-                                     (to & ((1 << p.log2_g) - 1));
-                  reinterpret_cast<uint4*>(p.o + at * D + q4 * 32)[lane & 3] = make_uint4(w[a][0], w[a][1], w[a][2], w[a][3]);
-                }
-              }
+              for (int a = 0; a < 4; ++a)  // chunk lane % 4 of row `four` + a
+                if (a < left) orow[next_row[a] + q4 * 4] = make_uint4(w[a][0], w[a][1], w[a][2], w[a][3]);
             }
           }
           if (store && part >= 0 && (!both || x == 0)) p.part_ml[(int64_t)part * p.part_rows + row] = make_float2(m, l);
