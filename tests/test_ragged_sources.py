@@ -22,6 +22,10 @@ def test_nothing_is_read_as_constant(name):
 
 
 def test_softmax_and_mma_warps_wait_together():
-    for line in _text("attn_ragged.cu").splitlines():
-        if re.search(r"wait\w*\(&?bars->(s_full|o_final|p_full|pair_ml|pair_done|v_full)", line):
-            assert "wait_warp(" in line or "ready(" in line or "mbar_wait(&bars->k_full" in line or "wait_for(&bars->v_full" in line, line
+    """Barriers that only whole warps wait for: one answer for all lanes (single looks are voted on)."""
+    text = _text("attn_ragged.cu")
+    waits = [line.strip() for line in text.splitlines()
+             if re.search(r"wait\w*\(&?bars->(s_full|o_final|p_full|pair_ml|pair_done)", line)]
+    looks = [line for line in waits if "mbar_try_wait(" in line]
+    assert waits and all("wait_warp(" in line or line in looks for line in waits), waits
+    assert re.search(r"__all_sync\(0xffffffffu, v && k && p0\)", text) and len(looks) == 1
