@@ -1444,6 +1444,7 @@ duo_status duo_attn_prefill_ragged(duo_handle* h, const duo_kv_cache* c, const d
   if ((st = check_rows(k, &k_stride, num_tokens, sh.Hkv, sh.D, "k")) != DUO_OK) return st;
   if ((st = check_rows(v, &v_stride, num_tokens, sh.Hkv, sh.D, "v")) != DUO_OK) return st;
   if (!o || !aligned16(o)) return fail(DUO_ERR_INVALID_ARG, "o NULL or not 16-byte aligned");
+  if (o == q || o == k || o == v) return fail(DUO_ERR_INVALID_ARG, "o is one of q, k and v");
   if ((st = check_workspace(workspace, ws_bytes, duo_prefill_ragged_workspace_size(h, num_tokens))) != DUO_OK) return st;
   return attn_ragged(h, c, pg, map, nullptr, 0, num_tokens, ragged_rows(h, num_tokens), q, q_stride, k, k_stride, v, v_stride, o,
                      workspace, stream);
@@ -1464,6 +1465,7 @@ duo_status duo_attn_decode_paged_varlen(duo_handle* h, const duo_kv_cache* c, co
   if (sh.n_ret > 0 && (st = check_capacity(h, pg, max_len, DUO_ERR_INVALID_ARG)) != DUO_OK) return st;
   if (!q || !o || !aligned16(q) || !aligned16(o))
     return fail(DUO_ERR_INVALID_ARG, "q / o NULL or not 16-byte aligned");
+  if (o == q) return fail(DUO_ERR_INVALID_ARG, "o is q");
   // the size every decode entry point asks for; two parts per CTA and the jobs fit in it for every shape
   const size_t need = decode_workspace_bytes(sh, h->num_sms * kDecodeCtasPerSmKv4);
   if ((st = check_workspace(workspace, ws_bytes, need)) != DUO_OK) return st;

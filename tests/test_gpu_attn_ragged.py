@@ -481,6 +481,9 @@ def test_refusals():
         L.decode_varlen(q[:2], lens, 0)
     with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
         L.decode_varlen(q[:2], lens, 129)  # past the tables
+    for call in (lambda: L.prefill_ragged(q, k, v, m, out=q), lambda: L.decode_varlen(q[:2], lens, 100, out=q[:2])):
+        with pytest.raises(DuoError, match="DUO_ERR_INVALID_ARG"):
+            call()
     with pytest.raises(NotImplementedError):
         L.append_varlen(k, v, lens)
     o, need = torch.empty_like(q), _lib.duo_prefill_ragged_workspace_size(L.handle, 7)
