@@ -214,9 +214,9 @@ class DuoPagedLayer(DuoLayer):
         _packed_rows(self, "k_new", k_new, (N, self.Hkv, self.D))
         _packed_rows(self, "v_new", v_new, (N, self.Hkv, self.D))
         if q is not None:
-            _packed_rows(self, "q", q, (N, self.Hq, self.D))
+            dense = _packed_rows(self, "q", q, (N, self.Hq, self.D))
             if q_out is None:
-                q_out = self.empty_like(q, memory_format=self.dense)
+                q_out = self.empty_like(q) if dense else self.empty_like(q, memory_format=self.dense)
             else:
                 _packed_rows(self, "q_out", q_out, (N, self.Hq, self.D))
         if rope is not None and (rope.head_dim != self.D or rope.index != self.index):
@@ -232,11 +232,11 @@ class DuoPagedLayer(DuoLayer):
         Rows of ``out`` of tokens that the map turns down, and of padding, are not written."""
         N = q.shape[0]
         self._check_packed(slot_map, N, planes=False)
-        _packed_rows(self, "q", q, (N, self.Hq, self.D))
+        dense = _packed_rows(self, "q", q, (N, self.Hq, self.D))
         _packed_rows(self, "k", k, (N, self.Hkv, self.D))
         _packed_rows(self, "v", v, (N, self.Hkv, self.D))
         if out is None:
-            out = self.empty_like(q, memory_format=self.dense)
+            out = self.empty_like(q) if dense else self.empty_like(q, memory_format=self.dense)
         else:
             _on(self, "o", out, (N, self.Hq, self.D))
         ws = _stream_workspace(_lib.duo_prefill_ragged_workspace_size(self.handle, N), q.device, stream)
@@ -327,15 +327,15 @@ class DuoRope:
             raise ValueError(f"positions: need a contiguous int32 tensor of one dimension on CUDA device {self.index}")
         if _lib._current_device() != self.index:
             raise ValueError(f"the current device is not the frequencies' (CUDA device {self.index})")
-        _packed_rows(self, "q", q, (N, q.shape[1], self.head_dim))
+        dense = _packed_rows(self, "q", q, (N, q.shape[1], self.head_dim))
         if q_out is None:
-            q_out = self.empty_like(q, memory_format=self.dense)
+            q_out = self.empty_like(q) if dense else self.empty_like(q, memory_format=self.dense)
         else:
             _packed_rows(self, "q_out", q_out, q.shape)
         if k is not None:
-            _packed_rows(self, "k", k, (N, k.shape[1], self.head_dim))
+            dense = _packed_rows(self, "k", k, (N, k.shape[1], self.head_dim))
             if k_out is None:
-                k_out = self.empty_like(k, memory_format=self.dense)
+                k_out = self.empty_like(k) if dense else self.empty_like(k, memory_format=self.dense)
             else:
                 _packed_rows(self, "k_out", k_out, k.shape)
         _lib.duo_rope_rotate(self.c, self.head_dim, positions, N, q, q_out, k, None if k is None else k_out, stream)
@@ -718,13 +718,14 @@ def _on(layer, name, t, shape):
 
 
 def _packed_rows(owner, name, t, shape):
-    """Rows of a packed batch on the owner's device: bf16 [tokens, heads, D], a token's rows in one piece."""
+    """Rows of a packed batch on the owner's device: bf16 [tokens, heads, D], a token's rows in one piece.
+    Whether the tokens are so, too."""
     if t.dtype is owner.bf16 and t.get_device() == owner.index and t.shape == shape:
         if t.is_contiguous():
-            return
+            return True
         s = t.stride()
         if s[2] == 1 and s[1] == shape[2] and (s[0] >= shape[1] * shape[2] or shape[0] < 2):
-            return
+            return False
     raise ValueError(f"{name}: need a bfloat16 tensor of shape {tuple(shape)} on CUDA device {owner.index} with each token's "
                      f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 

@@ -473,16 +473,22 @@ def duo_rope_turns(inv_freq) -> list:
 def duo_rope_rotate(rope: "duo_rope", head_dim: int, positions, num_tokens: int, q, q_out, k, k_out,
                     stream=None) -> None:
     """q and k (or None) [num_tokens, heads, head_dim] rotated by their tokens' positions."""
-    _check(library().duo_rope_rotate(_ref(rope), head_dim, _ptr(positions), num_tokens, *_rows(q), *_rows(q_out),
-                                     q.shape[1], *_rows(k), *_rows(k_out), 0 if k is None else k.shape[1],
-                                     _stream_ptr(stream)))
+    kp, ks, kop, kos, kh = (None, 0, None, 0, 0) if k is None else (*_rows(k), *_rows(k_out), k.shape[1])
+    status = (_LIB or library()).duo_rope_rotate(_ref(rope), head_dim, positions.data_ptr(), num_tokens, q.data_ptr(),
+                                                 q.stride(0), q_out.data_ptr(), q_out.stride(0), q.shape[1], kp, ks, kop,
+                                                 kos, kh, _stream_ptr(stream))
+    if status:
+        _check(status)
 
 
 def duo_kv_append_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot_map: "duo_slot_map", num_tokens: int,
                          rope, k_new, v_new, q=None, q_out=None, stream=None) -> None:
     """A packed batch into bf16 paged caches, K (and q into q_out) rotated on the way with rope."""
-    _check(library().duo_kv_append_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, _ref(rope),
-                                          *_rows(k_new), *_rows(v_new), *_rows(q), *_rows(q_out), _stream_ptr(stream)))
+    status = (_LIB or library()).duo_kv_append_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens,
+                                                      _ref(rope), k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(),
+                                                      v_new.stride(0), *_rows(q), *_rows(q_out), _stream_ptr(stream))
+    if status:
+        _check(status)
 
 
 def duo_prefill_ragged_workspace_size(handle, num_tokens: int) -> int:
@@ -492,16 +498,21 @@ def duo_prefill_ragged_workspace_size(handle, num_tokens: int) -> int:
 def duo_attn_prefill_ragged(handle, cache: "duo_kv_cache", paged: "duo_paged", slot_map: "duo_slot_map",
                             num_tokens: int, q, k, v, o, workspace, stream=None) -> None:
     """Chunks of a packed batch over bf16 paged caches and their own tokens."""
-    _check(library().duo_attn_prefill_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens, *_rows(q),
-                                             *_rows(k), *_rows(v), _ptr(o), _ptr(workspace), _nbytes(workspace),
-                                             _stream_ptr(stream)))
+    status = (_LIB or library()).duo_attn_prefill_ragged(handle, _ref(cache), _ref(paged), _ref(slot_map), num_tokens,
+                                                         *_rows(q), *_rows(k), *_rows(v), _ptr(o), _ptr(workspace),
+                                                         _nbytes(workspace), _stream_ptr(stream))
+    if status:
+        _check(status)
 
 
 def duo_attn_decode_paged_varlen(handle, cache: "duo_kv_cache", paged: "duo_paged", seq_lens, max_len: int, q, o,
                                  workspace, stream=None) -> None:
     """Decode over bf16 paged caches with per-sequence lengths read on the device."""
-    _check(library().duo_attn_decode_paged_varlen(handle, _ref(cache), _ref(paged), _ptr(seq_lens), max_len, _ptr(q),
-                                                  _ptr(o), _ptr(workspace), _nbytes(workspace), _stream_ptr(stream)))
+    status = (_LIB or library()).duo_attn_decode_paged_varlen(handle, _ref(cache), _ref(paged), _ptr(seq_lens), max_len,
+                                                              _ptr(q), _ptr(o), _ptr(workspace), _nbytes(workspace),
+                                                              _stream_ptr(stream))
+    if status:
+        _check(status)
 
 
 def duo_kv_append_varlen(handle, cache: "duo_kv_cache", seq_lens, k_new, v_new, stream=None) -> None:
