@@ -21,7 +21,11 @@ class DuoLayer:
 
     k_full/v_full: bf16 [B, n_ret, max_seq_len, D]; k_sr/v_sr: bf16 [B, n_str, S+R, D];
     pos: int32 [B, S+R]; ``n`` tokens appended so far. ``workspace`` is the decode
-    workspace (zero-filled once)."""
+    workspace.
+
+    Every call runs on ``stream`` (a torch stream or a raw handle; None: the current one), behind what was
+    launched there before. An output that is not given is allocated as that stream's: to use it on
+    another one, wait for the call there, and tell torch's allocator (``record_stream``) before it is dropped."""
 
     def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, max_seq_len,
                  is_retrieval, device="cuda"):
@@ -71,7 +75,7 @@ class DuoLayer:
         _lib._bf16(k, (self.B, T, self.Hkv, self.D), "k")
         _lib._bf16(v, (self.B, T, self.Hkv, self.D), "v")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, T, self.Hq, self.D), "o")
         duo_attn_prefill_select(self.handle, self.cache, q, k, v, T, out, kind_mask, stream)
         return out
@@ -80,7 +84,7 @@ class DuoLayer:
         import torch
         _lib._bf16(q, (self.B, self.Hq, self.D), "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, self.Hq, self.D), "o")
         duo_attn_decode(self.handle, self.cache, q, out, self.workspace, stream)
         return out
@@ -97,7 +101,7 @@ class DuoLayer:
         _lib._bf16(v, (self.B, T, self.Hkv, self.D), "v")
         _check_mscale(mscale, (self.B, T))
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, T, self.Hq, self.D), "o")
         _lib.duo_dca_prefill(self.handle, self.cache, q, q_succ, q_inter, k, v, mscale, T, chunk_len, out, stream)
         return out
@@ -109,7 +113,7 @@ class DuoLayer:
             _lib._bf16(t, (self.B, self.Hq, self.D), name)
         _check_mscale(mscale, (self.B,))
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, self.Hq, self.D), "o")
         _lib.duo_dca_decode(self.handle, self.cache, q, q_succ, q_inter, mscale, chunk_len, out, self.workspace, stream)
         return out
@@ -127,7 +131,7 @@ class DuoLayer:
         _lib._bf16(q, (self.B, self.Hq, self.D), "q")
         _check_lens(seq_lens, self.B)
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, self.Hq, self.D), "o")
         duo_attn_decode_varlen(self.handle, self.cache, seq_lens, max_len, q, out, self.workspace, stream)
         return out
@@ -160,7 +164,7 @@ class DuoPagedLayer(DuoLayer):
         self.block_size = block_size
         # (looked up here: a small call's time is the host's)
         self.index, self.bf16 = self.pos.get_device(), torch.bfloat16
-        self.empty_like, self.dense = torch.empty_like, torch.contiguous_format
+        self.empty_like = torch.empty_like
         self.k_full = torch.empty((num_blocks, block_size, head_dim), **bf)
         self.v_full = torch.empty_like(self.k_full)
         self.cache.k_full = self.k_full.data_ptr()
@@ -191,7 +195,7 @@ class DuoPagedLayer(DuoLayer):
         T = q.shape[1]
         _lib._bf16(q, (self.B, T, self.Hq, self.D), "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib.duo_attn_prefill_paged(self.handle, self.cache, self.paged, q, k, v, T, out, stream)
         return out
 
@@ -199,7 +203,7 @@ class DuoPagedLayer(DuoLayer):
         import torch
         _lib._bf16(q, (self.B, self.Hq, self.D), "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib.duo_attn_decode_paged(self.handle, self.cache, self.paged, q, out, self.workspace, stream)
         return out
 
@@ -216,7 +220,7 @@ class DuoPagedLayer(DuoLayer):
         if q is not None:
             dense = _packed_rows(self, "q", q, (N, self.Hq, self.D))
             if q_out is None:
-                q_out = self.empty_like(q) if dense else self.empty_like(q, memory_format=self.dense)
+                q_out = self.empty_like(q) if dense and stream is None else _output(q, stream)
             else:
                 _packed_rows(self, "q_out", q_out, (N, self.Hq, self.D))
         if rope is not None and (rope.head_dim != self.D or rope.index != self.index):
@@ -236,7 +240,7 @@ class DuoPagedLayer(DuoLayer):
         _packed_rows(self, "k", k, (N, self.Hkv, self.D))
         _packed_rows(self, "v", v, (N, self.Hkv, self.D))
         if out is None:
-            out = self.empty_like(q) if dense else self.empty_like(q, memory_format=self.dense)
+            out = self.empty_like(q) if dense and stream is None else _output(q, stream)
         else:
             _on(self, "o", out, (N, self.Hq, self.D))
         ws = _stream_workspace(_lib.duo_prefill_ragged_workspace_size(self.handle, N), q.device, stream)
@@ -248,7 +252,7 @@ class DuoPagedLayer(DuoLayer):
         max_len); a sequence of length 0 gets zeros."""
         _on(self, "q", q, (self.B, self.Hq, self.D))
         if out is None:
-            out = self.empty_like(q)
+            out = self.empty_like(q) if stream is None else _output(q, stream)
         else:
             _on(self, "o", out, (self.B, self.Hq, self.D))
         _check_lens(seq_lens, self.B)
@@ -313,13 +317,14 @@ class DuoRope:
         turns = [t - (1 << 64) if t >> 63 else t for t in _lib.duo_rope_turns(inv_freq)]
         self.turns = torch.tensor(turns, dtype=torch.int64).to(self.device)
         self.index, self.bf16, self.int32 = self.turns.get_device(), torch.bfloat16, torch.int32
-        self.empty_like, self.dense = torch.empty_like, torch.contiguous_format
+        self.empty_like = torch.empty_like
         self.c = _lib.duo_rope(self.turns.data_ptr(), rotary_dim,
                                _lib.DUO_ROPE_HALF if layout == "half" else _lib.DUO_ROPE_INTERLEAVED, self.scale)
 
     def rotate(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """q [num_tokens, Hq, head_dim] and k [num_tokens, Hkv, head_dim] (or None) rotated by positions
-        (int32 [num_tokens]); returns (q_out, k_out), new tensors unless given (they may be q and k).
+        (int32 [num_tokens]); returns (q_out, k_out), new tensors of ``stream`` (as DuoLayer's) unless given
+        (they may be q and k).
         Rows of tokens at positions below 0 are not written."""
         N = positions.shape[0]
         if (positions.dtype is not self.int32 or positions.get_device() != self.index or positions.dim() != 1
@@ -329,13 +334,13 @@ class DuoRope:
             raise ValueError(f"the current device is not the frequencies' (CUDA device {self.index})")
         dense = _packed_rows(self, "q", q, (N, q.shape[1], self.head_dim))
         if q_out is None:
-            q_out = self.empty_like(q) if dense else self.empty_like(q, memory_format=self.dense)
+            q_out = self.empty_like(q) if dense and stream is None else _output(q, stream)
         else:
             _packed_rows(self, "q_out", q_out, q.shape)
         if k is not None:
             dense = _packed_rows(self, "k", k, (N, k.shape[1], self.head_dim))
             if k_out is None:
-                k_out = self.empty_like(k) if dense else self.empty_like(k, memory_format=self.dense)
+                k_out = self.empty_like(k) if dense and stream is None else _output(k, stream)
             else:
                 _packed_rows(self, "k_out", k_out, k.shape)
         _lib.duo_rope_rotate(self.c, self.head_dim, positions, N, q, q_out, k, None if k is None else k_out, stream)
@@ -425,7 +430,7 @@ class DuoKv4Layer(DuoLayer):
         import torch
         _lib._bf16(q, (self.B, self.Hq, self.D), "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, self.Hq, self.D), "o")
         _lib.duo_attn_decode_kv4(self.handle, self.cache, self.kv4, q, out, self.workspace, stream)
         return out
@@ -439,7 +444,7 @@ class DuoKv4Layer(DuoLayer):
         _lib._bf16(k, (self.B, T, self.Hkv, self.D), "k")
         _lib._bf16(v, (self.B, T, self.Hkv, self.D), "v")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, T, self.Hq, self.D), "o")
         _lib.duo_attn_prefill_kv4(self.handle, self.cache, self.kv4, q, k, v, T, out, stream)
         return out
@@ -489,7 +494,7 @@ class DuoKv4PagedLayer(DuoKv4Layer):
         import torch
         _lib._bf16(q, (self.B, self.Hq, self.D), "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _output(q, stream)
         _lib._bf16(out, (self.B, self.Hq, self.D), "o")
         _lib.duo_attn_decode_kv4_paged(self.handle, self.cache, self.paged, self.kv4, q, out, self.workspace, stream)
         return out
@@ -553,7 +558,7 @@ class DuoKv8Layer(DuoLayer):
             _lib.duo_kv_append_kv8_paged(self.handle, self.cache, self.paged, self.kv8, k_new, v_new, T, stream)
 
     def decode(self, q, out=None, stream=None):
-        out = self._out(q, self.row, out)
+        out = self._out(q, self.row, out, stream)
         if self.paged is None:
             _lib.duo_attn_decode_kv8(self.handle, self.cache, self.kv8, q, out, self.workspace, stream)
         else:
@@ -564,7 +569,7 @@ class DuoKv8Layer(DuoLayer):
     def decode_varlen(self, q, seq_lens, max_len, out=None, stream=None):
         """Decode where sequence b holds seq_lens[b] tokens, the new one included (device int32
         [B], <= max_len); a sequence of length 0 gets zeros."""
-        out = self._out(q, self.row, out)
+        out = self._out(q, self.row, out, stream)
         _check_lens(seq_lens, self.B)
         if seq_lens.get_device() != self.index:
             raise ValueError(f"seq_lens: on {seq_lens.device}, the layer is on CUDA device {self.index}")
@@ -572,10 +577,10 @@ class DuoKv8Layer(DuoLayer):
                                         self.workspace, stream)
         return out
 
-    def _out(self, q, shape, out):
+    def _out(self, q, shape, out, stream):
         _on(self, "q", q, shape)
         if out is None:
-            return self.empty_like(q)
+            return self.empty_like(q) if stream is None else _output(q, stream)
         _on(self, "o", out, shape)
         return out
 
@@ -590,16 +595,11 @@ class DuoKv8Layer(DuoLayer):
         if kind_mask != 3:
             raise NotImplementedError("8-bit caches: prefill takes the heads of both kinds")
         T = q.shape[1]
-        out = self._out(q, (self.B, T, self.Hq, self.D), out)
+        out = self._out(q, (self.B, T, self.Hq, self.D), out, stream)
         _on(self, "k", k, (self.B, T, self.Hkv, self.D))
         _on(self, "v", v, (self.B, T, self.Hkv, self.D))
         need = _lib.duo_prefill_kv8_workspace_size(self.handle, self.n, T)
-        if stream is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:  # its memory may be given out again as soon as this returns: in that stream's order
-            handle = _lib._stream_ptr(stream)
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=q.device)):
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _stream_workspace(need, q.device, stream)
         if self.paged is None:
             _lib.duo_attn_prefill_kv8(self.handle, self.cache, self.kv8, q, k, v, T, out, ws, stream)
         else:
@@ -730,13 +730,29 @@ def _packed_rows(owner, name, t, shape):
                      f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
+def _in_order_of(stream, device):
+    """What is allocated within comes from torch's allocator in the order of `stream`."""
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(_lib._stream_ptr(stream), device=device))
+
+
+def _output(q, stream):
+    """A dense tensor like q for a call on `stream` (None: the current one) to write, in that stream's order: in
+    another's, its memory may be in use there still, and may be given out again while `stream` writes it."""
+    import torch
+    if stream is None:
+        return torch.empty_like(q, memory_format=torch.contiguous_format)
+    with _in_order_of(stream, q.device):
+        return torch.empty_like(q, memory_format=torch.contiguous_format)
+
+
 def _stream_workspace(nbytes, device, stream):
-    """Workspace of one call on `stream` (None: the current one), from torch's allocator in that stream's
-    order: its memory may be given out again as soon as the call has returned."""
+    """Workspace of one call on `stream` (None: the current one), in that stream's order: its memory may be
+    given out again as soon as the call has returned."""
     import torch
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_lib._stream_ptr(stream), device=device)):
+    with _in_order_of(stream, device):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
