@@ -499,8 +499,8 @@ duo_status duo_block_tables_update(const duo_block_pool* pool, const int32_t* ne
  *     (scale (a cos t - b sin t), scale (b cos t + a sin t)),  t = p f_i,
  * computed in fp32 from bf16 values and rounded once. The pairs are dims (i, i + rotary_dim / 2)
  * (DUO_ROPE_HALF) or (2 i, 2 i + 1) (DUO_ROPE_INTERLEAVED) of the head; dims from rotary_dim on
- * pass through unchanged. Any frequencies will do (scaled ones for long contexts are made on the
- * host); `scale` is the factor that some of these schemes apply to rotated pairs, else 1.
+ * pass through unchanged. Any frequencies up to 2^40 radians a position will do (scaled ones for long
+ * contexts are made on the host); `scale` is the factor that some of these schemes apply to rotated pairs, else 1.
  *   turns: device memory, [rotary_dim / 2], from duo_rope_turns: the angle per position of each
  *          pair as a fraction of a full turn, in units of 2^-64. A position times it wraps as
  *          angles do, so the angle is exact at every position up to 2^31 - 1. */
@@ -514,7 +514,8 @@ typedef struct {
   float scale;
 } duo_rope;
 
-/* turns[i] of angles per position inv_freq[i] (radians, finite). Host arrays; host only. */
+/* turns[i] of angles per position inv_freq[i] (radians, up to 2^40 in size), each within one unit. Host
+ * arrays; host only. */
 duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns);
 
 /* Rotates the rows of q and, unless k is NULL, of k (head_dim 64 or 128) by positions [num_tokens]

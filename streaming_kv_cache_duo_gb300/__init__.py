@@ -292,8 +292,8 @@ class DuoRope:
                                       as yarn, the ramp over the number of turns, between low and high;
                                       no factor on the pairs
 
-    ``inv_freq`` (radians per position, rotary_dim / 2 of them) gives any other frequencies, ``scale`` any
-    other factor of the rotated pairs. Angles are exact at every position up to 2^31 - 1."""
+    ``inv_freq`` (radians per position, up to 2^40, rotary_dim / 2 of them) gives any other frequencies, ``scale``
+    any other factor of the rotated pairs. Angles are exact at every position up to 2^31 - 1."""
 
     def __init__(self, head_dim, theta=10000.0, rotary_dim=None, layout="half", scaling=None, inv_freq=None,
                  scale=None, device="cuda"):

@@ -1211,16 +1211,20 @@ static int rope_chunk(int tokens, int sms) { return std::max(1, std::min(tokens 
 duo_status duo_rope_turns(const double* inv_freq, int32_t count, uint64_t* turns) {
   if (!inv_freq || !turns || count < 0) return fail(DUO_ERR_INVALID_ARG, "rope: NULL array or count < 0");
   // |f| / 2 pi as a sum of two doubles (1 / 2 pi in two), its whole turns left out (exact for a number that is
-  // not negative), then times 2^64; of a negative f the opposite
+  // not negative), then times 2^64; of a negative f the opposite. Up to |f| = 2^40 the result is within one unit:
+  // kHi + kLo is off by 2^-110, times f 2^-6 units; f kLo is rounded by 2^-6 of one, rest (below 2^-15) by 2^-5,
+  // the last sum (below 2^50) by 2^-4, and rint by a half. Past it rest would run out of bits, and of an int64_t.
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57, kWord = 4294967296.0;
+  constexpr double kMost = 1099511627776.0;  // 2^40
   for (int32_t i = 0; i < count; ++i) {
-    if (!std::isfinite(inv_freq[i])) return fail(DUO_ERR_INVALID_ARG, "rope: frequency %d is not finite", i);
+    if (!(std::fabs(inv_freq[i]) <= kMost))
+      return fail(DUO_ERR_INVALID_ARG, "rope: frequency %d = %g is not a number of up to 2^40 radians", i, inv_freq[i]);
   }
   for (int32_t i = 0; i < count; ++i) {
     const double f = std::fabs(inv_freq[i]), t = f * kHi;
     const double rest = std::fma(f, kHi, -t) + f * kLo;
     const double x = (t - std::floor(t)) * kWord, whole = std::floor(x);
-    const double low = std::rint((x - whole) * kWord + rest * kWord * kWord);  // |.| < 2^54
+    const double low = std::rint((x - whole) * kWord + rest * kWord * kWord);  // |.| < 2^50
     const uint64_t word = ((uint64_t)whole << 32) + (uint64_t)(int64_t)low;
     turns[i] = inv_freq[i] < 0 ? 0 - word : word;
   }
