@@ -287,7 +287,7 @@ class DuoRope:
                                       pairs that turn more than beta_fast times over the original length
                                       keep their frequency, those that turn less than beta_slow times get
                                       it divided by factor, a ramp over the pairs between; rotated pairs
-                                      are multiplied by 0.1 ln(factor) + 1
+                                      are multiplied by 0.1 ln(factor) + 1 (factors up to 1: by 1)
       dict(kind="wavelength", factor, low, high, original)
                                       as yarn, the ramp over the number of turns, between low and high;
                                       no factor on the pairs
@@ -383,7 +383,7 @@ def rope_frequencies(rotary_dim, theta=10000.0, scaling=None):
     first = max(0, math.floor(pair(scaling.get("beta_fast", 32.0))))
     last = min(rotary_dim - 1, math.ceil(pair(scaling.get("beta_slow", 1.0))))
     past = [min(1.0, max(0.0, (i - first) / max(last - first, 0.001))) for i in range(rotary_dim // 2)]
-    return [f * (1.0 - w) + f / s * w for f, w in zip(freq, past)], 0.1 * math.log(s) + 1.0
+    return [f * (1.0 - w) + f / s * w for f, w in zip(freq, past)], 0.1 * math.log(max(s, 1.0)) + 1.0
 
 
 class DuoKv4Layer(DuoLayer):
