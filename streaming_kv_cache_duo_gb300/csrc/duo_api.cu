@@ -1399,7 +1399,7 @@ static duo_status attn_ragged(const duo_handle* h, const duo_kv_cache* c, const 
   p.tokens = N;
   while ((1 << p.log2_g) < sh.g) ++p.log2_g;
   p.window = ragged_window(sh.R, kRaggedRows / sh.g);
-  p.places = sh.D == 128 ? RaggedPlaces{8, 6, 10, 6, 28, 16} : RaggedPlaces{8, 6, 11, 8, 22, 20};
+  p.places = sh.D == 128 ? kRaggedPlaces128 : kRaggedPlaces64;
   p.ctas = h->num_sms;
   p.part_rows = rows;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)sh.D));

@@ -54,13 +54,20 @@ cudaError_t append_ragged_read_clear_error(uint32_t* code);
 // ------------------------------------------------------------------ attention
 constexpr int kRaggedRows = 256;  // packed query rows (token x head of a KV head) of an item at most
 // Places on the line of work (attn_ragged.cu), of some 0.17 us each: a retrieval tile's with two query tiles
-// and with one, a streaming tile's (most are masked) likewise, and an item's own, likewise. They only decide how
-// evenly the CTAs are loaded, and are fitted over chunks, mixed batches and decodes of either head dim. (With one
-// figure for either kind of items 32 mixed sequences took 249 us, with two 239; 4096 tokens over 28672 390 and 382.)
+// and with one, a streaming tile's (most are masked) likewise, and an item's own, likewise. What they are decides
+// how evenly the CTAs are loaded, and they are fitted over chunks, mixed batches and decodes of either head dim.
+// (With one figure for either kind of items 32 mixed sequences took 249 us, with two 239; 4096 tokens over 28672
+// 390 and 382.) One thing is more than balance: a tile takes no more places than a CTA's share has at least, so
+// that every CTA between an item's first and last one begins a tile of it and leaves the part that the merge reads.
 struct RaggedPlaces {
   int two, one, stream_two, stream_one, item_two, item_one;
 };
+constexpr RaggedPlaces kRaggedPlaces128 = {8, 6, 10, 6, 28, 16}, kRaggedPlaces64 = {8, 6, 11, 8, 22, 20};
 constexpr int kRaggedLeast = 24;  // places of a CTA's share at least
+constexpr bool tiles_fit_a_share(RaggedPlaces p) {
+  return p.two <= kRaggedLeast && p.one <= kRaggedLeast && p.stream_two <= kRaggedLeast && p.stream_one <= kRaggedLeast;
+}
+static_assert(tiles_fit_a_share(kRaggedPlaces128) && tiles_fit_a_share(kRaggedPlaces64), "a part would be missing");
 constexpr int kRaggedShort = 4;   // tiles of an item that is not shared at most
 
 // An item whose key tiles several CTAs share, noted by the CTA that begins it (last < 0: it begins none):
