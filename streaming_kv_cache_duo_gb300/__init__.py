@@ -155,6 +155,8 @@ class DuoPagedLayer(DuoLayer):
     given (block-granular eviction: ``dead_blocks()`` names the blocks the caller may
     free), else they keep the sink + ring cache."""
 
+    uniform_rings = False  # decode_varlen by the kernel of contiguous caches: rings alone
+
     def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, sink_size, recent_size, block_size,
                  max_blocks, num_blocks, block_table, is_retrieval, device="cuda", stream_table=None):
         import torch
@@ -175,6 +177,8 @@ class DuoPagedLayer(DuoLayer):
                 assert tuple(t.shape) == (batch, rows, max_blocks), name
         self.block_table = block_table
         self.stream_table = stream_table
+        if not self.n_ret and stream_table is None:
+            self.uniform_rings = _uniform_rings(batch * num_kv_heads, sink_size + recent_size)
         self.paged = _lib.duo_paged(block_table.data_ptr() if block_table is not None else None, block_size,
                                     max_blocks, num_blocks,
                                     stream_table.data_ptr() if stream_table is not None else None)
@@ -258,8 +262,11 @@ class DuoPagedLayer(DuoLayer):
         _check_lens(seq_lens, self.B)
         if seq_lens.get_device() != self.index:
             raise ValueError(f"seq_lens: on {seq_lens.device}, the layer is on CUDA device {self.index}")
-        _lib.duo_attn_decode_paged_varlen(self.handle, self.cache, self.paged, seq_lens, max_len, q, out, self.workspace,
-                                          stream)
+        if self.uniform_rings:
+            duo_attn_decode_varlen(self.handle, self.cache, seq_lens, max_len, q, out, self.workspace, stream)
+        else:
+            _lib.duo_attn_decode_paged_varlen(self.handle, self.cache, self.paged, seq_lens, max_len, q, out, self.workspace,
+                                              stream)
         return out
 
     def append_varlen(self, k_new, v_new, seq_lens, stream=None) -> None:
@@ -728,6 +735,17 @@ def _packed_rows(owner, name, t, shape):
             return False
     raise ValueError(f"{name}: need a bfloat16 tensor of shape {tuple(shape)} on CUDA device {owner.index} with each token's "
                      f"rows in one piece, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+
+
+def _uniform_rings(units, rows):
+    """Whether single tokens over rings alone, `units` of `rows` rows, are for duo_attn_decode_varlen, not for the
+    packed kernel. That one spends 9 to 12 us on its beginning and its items' ends, and the other streams a ring by
+    one or two CTAs. Measured, us, the one / the packed, graphs replayed (64-dim heads ... 128-dim ones, one to eight
+    query heads a KV head): 36 rows, 8 units 4.7 ... 5.6 / 8.9 ... 12.5, 1024 units 18 ... 25 / 27 ... 32; 320 rows,
+    512 units 20 ... 30 / 24 ... 28; 640 rows, 256 units 16 ... 23 / 20 ... 25, 512 units 29 ... 43 / 30 ... 42; 1024
+    rows, 64 units 12 ... 17 / 14 ... 17, 256 units 22 ... 32 / 23 ... 34, but 1024 units 72 ... 105 / 59 ... 93; 2048
+    rows, 8 units 20 ... 29 / 13 ... 15, 512 units 75 ... 112 / 53 ... 93."""
+    return rows <= 640 or (rows <= 1024 and units <= 304)
 
 
 def _in_order_of(stream, device):
