@@ -344,6 +344,8 @@ class DuoRope:
             q_out = self.empty_like(q) if dense and stream is None else _output(q, stream)
         else:
             _packed_rows(self, "q_out", q_out, q.shape)
+        if k is None and k_out is not None:
+            raise ValueError("k_out: given without k")
         if k is not None:
             dense = _packed_rows(self, "k", k, (N, k.shape[1], self.head_dim))
             if k_out is None:
