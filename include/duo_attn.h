@@ -547,9 +547,11 @@ duo_status duo_kv_append_ragged(duo_handle* handle, duo_kv_cache* cache, const d
  * own sequence's new tokens; any mixture of single tokens and long chunks may come in one call. A sequence
  * whose first token is at position -1 is skipped, its rows of o and those of padding are left as they
  * were. Scores, softmax and outputs are accumulated in fp32, p is rounded to bf16 before its product
- * with v (to two bf16 terms for a sequence of up to 8 / g tokens). Nothing behind a sequence's last row takes
- * part, whatever it holds (other sequences, padding, rows of a block not written yet); within a sequence, an
- * infinity or NaN in v also reaches queries that do not see it but read its tile of 128 keys. Rows of a block id outside [0, num_blocks) are left out and duo_device_error() reports
+ * with v (to two bf16 terms for a sequence of up to 8 / g tokens).
+ * Nothing behind a sequence's last row takes part, whatever it holds (other sequences, padding, rows of a
+ * block not written yet); within a sequence, an infinity or NaN in v also reaches queries that do not see
+ * it but read its tile of 128 keys.
+ * Rows of a block id outside [0, num_blocks) are left out and duo_device_error() reports
  * DUO_ERR_INVALID_ARG; so it does where cu_new falls or passes num_tokens, or a position passes the tables'
  * capacity: that sequence is skipped. paged->stream_table must be NULL.
  * workspace: duo_prefill_ragged_workspace_size(handle, num_tokens) bytes of device memory, 256-byte aligned

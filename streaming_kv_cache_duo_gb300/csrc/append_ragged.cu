@@ -17,8 +17,10 @@
 // once for all heads (a thread per pair), then a thread moves 32 bytes of a row, two 16-byte vectors that
 // lie half a (rotated or unrotated) part apart, which for the one layout are the two halves of eight pairs
 // and for the other four whole pairs each. Measured: 24001 tokens of 40 heads of 128 dims 80 us = 6.16 TB/s
-// (0.91 of a copy); 8 tokens a CTA there, fewer where a call has not enough for every SM. 64 tokens: 2.5 us
-// alone, 3.7 with the append, and 14 to 16 among other calls, where the host is what takes the time.
+// (0.91 of a copy); 8 tokens a CTA there, fewer where a call has not enough for every SM. 64 tokens: 2.5 to 2.8 us
+// alone, 3.7 with the append, and 12 to 17 among other calls that make their outputs, where the host is what takes
+// the time. Nothing rotated: 64 tokens 2.7 us (6.4 to 7 among others), four prompts of 20480 tokens, 4 of 8 heads
+// retrieval, 19.5 us where their rows take 13.3.
 #include "duo_device.cuh"
 #include "ragged_internal.h"
 

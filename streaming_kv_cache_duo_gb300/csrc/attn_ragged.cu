@@ -178,8 +178,11 @@ __device__ __forceinline__ int tiles_of(int64_t rows) { return (int)((rows + BN 
 // Places on the line of a head's first m items (all, if it has no more), in the order of their tokens. An
 // item reads cache tiles and the new tokens' tiles up to its last token, ceil(min(T, (k + 1) tb) / 128)
 // for block k of tb tokens; a streaming head's, from the first block on whose every query is past the
-// ring but for the sinks, tiles of sinks and of a window (p.window). Out of line, and with few instructions:
-// when a CTA begins, none of them is in its SM's cache, and each costs some 30 cycles the first time.
+// ring but for the sinks, tiles of sinks and of a window (p.window). Never fewer than its items read, which would
+// lose tiles, but some more: sinks among the new tokens are counted beside a window that still reaches them. And
+// places go by the sequence, though its last block, of 128 rows or fewer, runs with one query tile and not two.
+// Both cost balance alone. Out of line, and with few instructions: when a CTA begins, none of them is in its SM's
+// cache, and each costs some 30 cycles the first time.
 __device__ __noinline__ long long line_upto(int T, int n, bool streaming, int m, int place, int item, int log2_g,
                                             bool chunks, int S, int R, int window) {
   const int shift = 8 - log2_g;  // tb = 2^shift
