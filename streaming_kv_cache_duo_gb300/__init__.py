@@ -743,37 +743,39 @@ def _uniform_rings(units, rows):
     """Whether single tokens over rings alone, `units` of `rows` rows, are for duo_attn_decode_varlen, not for the
     packed kernel. That one spends 9 to 12 us on its beginning and its items' ends, and the other streams a ring by
     one or two CTAs. Measured, us, the one / the packed, graphs replayed (64-dim heads ... 128-dim ones, one to eight
-    query heads a KV head): 36 rows, 8 units 4.7 ... 5.6 / 8.9 ... 12.5, 1024 units 18 ... 25 / 27 ... 32; 320 rows,
-    512 units 20 ... 30 / 24 ... 28; 640 rows, 256 units 16 ... 23 / 20 ... 25, 512 units 29 ... 43 / 30 ... 42; 1024
-    rows, 64 units 12 ... 17 / 14 ... 17, 256 units 22 ... 32 / 23 ... 34, but 1024 units 72 ... 105 / 59 ... 93; 2048
-    rows, 8 units 20 ... 29 / 13 ... 15, 512 units 75 ... 112 / 53 ... 93."""
+    query heads a KV head): 36 rows, 8 units 4.5 ... 5.6 / 8.8 ... 12.4, 1024 units 18 ... 25 / 27 ... 32; 320 rows,
+    512 units 20 ... 30 / 24 ... 28; 640 rows, 256 units 16 ... 23 / 20 ... 25, 512 units 29 ... 43 / 30 ... 42, 1024
+    units 50 ... 74 / 48 ... 68; 1024 rows, 64 units 12 ... 17 / 14 ... 17, 256 units 22 ... 32 / 23 ... 34, but 1024
+    units 72 ... 105 / 59 ... 93; 2048 rows, 8 units 20 ... 29 / 12 ... 15, 512 units 75 ... 112 / 53 ... 93."""
     return rows <= 640 or (rows <= 1024 and units <= 304)
 
 
-def _in_order_of(stream, device):
-    """What is allocated within comes from torch's allocator in the order of `stream`."""
-    import torch
-    return torch.cuda.stream(torch.cuda.ExternalStream(_lib._stream_ptr(stream), device=device))
+def _in_order_of(stream, make):
+    """What make() allocates, from torch's allocator in the order of `stream` (None: the current one)."""
+    if stream is None or _lib._stream_ptr(stream) == _lib._stream_ptr(None):
+        return make()
+    from torch import cuda
+    before = cuda.current_stream()
+    # (13 -> 6 us of host against cuda.stream as a context)
+    cuda.set_stream(stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(_lib._stream_ptr(stream)))
+    try:
+        return make()
+    finally:
+        cuda.set_stream(before)
 
 
 def _output(q, stream):
     """A dense tensor like q for a call on `stream` (None: the current one) to write, in that stream's order: in
     another's, its memory may be in use there still, and may be given out again while `stream` writes it."""
     import torch
-    if stream is None:
-        return torch.empty_like(q, memory_format=torch.contiguous_format)
-    with _in_order_of(stream, q.device):
-        return torch.empty_like(q, memory_format=torch.contiguous_format)
+    return _in_order_of(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
 
 
 def _stream_workspace(nbytes, device, stream):
     """Workspace of one call on `stream` (None: the current one), in that stream's order: its memory may be
     given out again as soon as the call has returned."""
     import torch
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with _in_order_of(stream, device):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _in_order_of(stream, lambda: torch.empty(nbytes, dtype=torch.uint8, device=device))
 
 
 def _check_table(t, shape, index):

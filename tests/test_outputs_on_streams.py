@@ -1,7 +1,6 @@
 """Outputs that a call makes itself come from the allocator in the order of the stream the call runs on (CPU:
-torch's stream context, the allocation and the library are recorded)."""
+torch's current stream, the allocations and the library are recorded)."""
 
-import contextlib
 import inspect
 
 import pytest
@@ -11,7 +10,7 @@ import streaming_kv_cache_duo_gb300 as duo
 from streaming_kv_cache_duo_gb300 import _lib
 
 B, T, Hq, Hkv, D = 2, 3, 4, 2, 64
-STREAM = 0x5eed0
+STREAM, CURRENT = 0x5eed0, 0xc0de0
 
 
 @pytest.fixture
@@ -20,11 +19,8 @@ def record(monkeypatch):
     made, within = [], []
     real_like, real_empty = torch.empty_like, torch.empty
 
-    @contextlib.contextmanager
     def on(stream):
-        within.append(stream)
-        yield
-        within.pop()
+        within[:] = [] if stream == CURRENT else [stream]
 
     def like(*a, **kw):
         t = real_like(*a, **kw)
@@ -38,16 +34,19 @@ def record(monkeypatch):
 
     monkeypatch.setattr(torch, "empty_like", like)
     monkeypatch.setattr(torch, "empty", empty)
-    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "set_stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: CURRENT)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: ptr)
     monkeypatch.setattr(_lib, "_bf16", lambda *a: None)
     monkeypatch.setattr(_lib, "_current_device", lambda: -1)
+    monkeypatch.setattr(_lib, "_stream_ptr", lambda s: CURRENT if s is None else s)
     monkeypatch.setattr(duo, "_check_lens", lambda *a: None)
     for module in (_lib, duo):
         for name in list(vars(module)):
             if name.startswith("duo_") and callable(getattr(module, name)) and not isinstance(getattr(module, name), type):
                 monkeypatch.setattr(module, name, lambda *a, **kw: 1024)
-    return made
+    yield made
+    assert not within  # (the current stream is what it was)
 
 
 def _layer(cls):
@@ -122,9 +121,10 @@ def test_outputs_are_the_streams_own(record, name, dense):
     for o in outs:
         assert [s for s, t in record if t is o] == [STREAM], name
     assert all(s == STREAM for s, _ in record)  # and so is what the call needs besides
-    record.clear()
-    outs = CALLS[name](None, dense)
-    assert record and all(s is None for s, _ in record) and all(o.is_contiguous() for o in outs)
+    for stream in (None, CURRENT):  # the current one: nothing to switch
+        record.clear()
+        outs = CALLS[name](stream, dense)
+        assert record and all(s is None for s, _ in record) and all(o.is_contiguous() for o in outs)
 
 
 def test_every_call_with_a_stream_and_an_output_is_among_them():
